@@ -209,7 +209,18 @@ const char* mo_status_string(mo_status status);
 #define MO_PHASE_SO_SORT    19  /* SOAP: E = I, eigenvalue sort, sorted fp32 eigenvectors */
 #define MO_PHASE_SO_PRODUCTS 20 /* SOAP: the six eigenbasis products, V', N and W written */
 #define MO_PHASE_SO_WARM    21  /* SOAP: a warm start's four products per eigendecomposition */
-#define MO_PHASE_COUNT    22
+#define MO_PHASE_EMB_FWD    22  /* embedding: lookup */
+#define MO_PHASE_EMB_SORT   23  /* embedding gradient: positions sorted by token */
+#define MO_PHASE_EMB_BWD    24  /* embedding gradient: sums of the runs, zeros elsewhere */
+#define MO_PHASE_LN_FWD     25  /* layer norm: forward */
+#define MO_PHASE_LN_BWD     26  /* layer norm: dx, partial and final weight gradients */
+#define MO_PHASE_HD_PREP    27  /* output head: coefficients, operand copies and transposes */
+#define MO_PHASE_HD_TARGET  28  /* output head: target logits, losses, delta at the targets */
+#define MO_PHASE_HD_LSE     29  /* output head: logits product with its log-sum-exp */
+#define MO_PHASE_HD_DELTA   30  /* output head: logits product with delta */
+#define MO_PHASE_HD_DW      31  /* output head: dW = delta^T H */
+#define MO_PHASE_HD_DH      32  /* output head: dH = delta W */
+#define MO_PHASE_COUNT      33
 
 /* Enable (1) or disable (0) per-launch timing on the calling thread.  While
  * enabled, every kernel launch is bracketed by HIP events on its own stream;
@@ -405,6 +416,139 @@ mo_status soap_owner_step(const mo_soap_matrix* mats, int32_t n_mats, const mo_s
 mo_status soap_converged(const mo_soap_matrix* mats, int32_t n_mats, const mo_soap_hparams* hp,
                          const void* workspace, size_t workspace_bytes, int32_t* rotating,
                          void* stream);
+
+/* ---- gradients the owner steps read ---------------------------------------
+ * The steps above take gradients as given.  The entry points below compute the
+ * ones at the two ends of a model, straight into the buffers the steps read:
+ * the embedding's and the output head's matrices (G of a Muon, Shampoo or SOAP
+ * descriptor), and the norm vectors of the packed fp32 tail (g of
+ * adamw_tail_step).  Conventions as above (strides in elements, 0 = the row
+ * length, at most 2^26; any element alignment; host-side checks first;
+ * written tensors disjoint from every other; bit-identical results on equal
+ * inputs).  No call allocates or uploads, so each can be captured in a graph;
+ * a workspace may not be shared by calls that run concurrently.  Elements of
+ * a row behind its length, and rows behind the last, are never touched. */
+
+/* Y[i] = scale * W[tokens[i]] for n tokens; W is vocab x dim, Y n x dim, both of
+ * `dtype`.  A token outside 0 .. vocab - 1 (padding) gives a zero row.
+ * Errors: MO_ERR_INVALID_ARG (null pointer, negative size, bad stride,
+ * non-finite scale), MO_ERR_UNSUPPORTED (dtype, n > 2^30, vocab > 2^27,
+ * dim > 2^20), MO_ERR_ALIAS, MO_ERR_HIP. */
+mo_status embedding_forward(const int64_t* tokens, int64_t n, const void* W, int64_t ld_w,
+                            int64_t vocab, int64_t dim, int32_t dtype, float scale, void* Y,
+                            int64_t ld_y, void* stream);
+
+/* Bytes of device workspace embedding_backward needs (0 for an empty call). */
+mo_status embedding_workspace_bytes(int64_t n, int64_t vocab, int64_t dim, size_t* bytes);
+
+/* The lookup's gradient: G[v] = scale * (sum of dY[i] over tokens[i] == v), or,
+ * with accumulate nonzero, G[v] += that for the rows named by a token (for a
+ * matrix tied to the output head, whose G then already holds the head's
+ * gradient).  Without accumulate every row of G is written, rows no token
+ * names with zeros.  dY (n x dim, dy_dtype) and G (vocab x dim, g_dtype) may
+ * differ in type; sums are fp32 over the positions in increasing order, rounded
+ * once.  dY rows of padded positions are not read.  Errors as
+ * embedding_forward, MO_ERR_WORKSPACE_TOO_SMALL. */
+mo_status embedding_backward(const int64_t* tokens, int64_t n, const void* dY, int64_t ld_dy,
+                             int32_t dy_dtype, void* G, int64_t ld_g, int32_t g_dtype,
+                             int64_t vocab, int64_t dim, float scale, int32_t accumulate,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* Layer norm of each row of X (rows x cols, dtype): with mu the row's mean and
+ * r = (mean((x - mu)^2) + eps)^-1/2, Y = (x - mu) r weight + bias, Y of X's
+ * dtype.  weight and bias are fp32 vectors of cols (slices of the packed tail),
+ * NULL for ones and zeros.  mean and rstd (fp32, rows) receive mu and r for the
+ * backward pass, NULL to drop them.  Errors: MO_ERR_INVALID_ARG (null X or Y,
+ * negative size, bad stride, eps negative or not finite), MO_ERR_UNSUPPORTED
+ * (dtype, cols > 2^24, rows > 2^32), MO_ERR_ALIAS, MO_ERR_HIP. */
+mo_status layer_norm_forward(const void* X, int64_t ld_x, const float* weight, const float* bias,
+                             void* Y, int64_t ld_y, float* mean, float* rstd, int64_t rows,
+                             int64_t cols, int32_t dtype, float eps, void* stream);
+
+/* Bytes of device workspace layer_norm_backward needs for dweight and dbias. */
+mo_status layer_norm_workspace_bytes(int64_t rows, int64_t cols, size_t* bytes);
+
+/* Gradients of layer_norm_forward from dY (dtype), X and the saved mean and rstd:
+ * dX (dtype), dweight and dbias (fp32 vectors of cols, slices of the tail's
+ * gradient g), each optional (NULL).  With rows == 0, dweight and dbias are
+ * zeroed.  Sums are fp32 in a fixed order.  Without dweight and dbias no
+ * workspace is needed.  Errors as layer_norm_forward,
+ * MO_ERR_WORKSPACE_TOO_SMALL. */
+mo_status layer_norm_backward(const void* dY, int64_t ld_dy, const void* X, int64_t ld_x,
+                              const float* weight, const float* mean, const float* rstd, void* dX,
+                              int64_t ld_dx, float* dweight, float* dbias, int64_t rows,
+                              int64_t cols, int32_t dtype, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* An output head: hidden states H (tokens x dim) and the weight W (vocab x dim),
+ * both of `dtype`.  The logits z = H W^T are never stored: both losses walk the
+ * vocabulary in pieces. */
+typedef struct mo_head {
+    const void* H;
+    const void* W;
+    int64_t     tokens, vocab, dim;
+    int64_t     ld_h, ld_w;
+    int32_t     dtype;
+} mo_head;
+
+/* Bytes of device workspace the forward (backward = 0) or the backward call
+ * needs for these tensors.  The pointers' and strides' alignment counts (rows
+ * that are not 16-byte aligned are copied first), their contents do not. */
+mo_status softmax_xent_workspace_bytes(const mo_head* head, int32_t backward, size_t* bytes);
+
+/* Softmax cross entropy: lse_n = log(sum_v exp(z_nv)), loss_n = lse_n - z_n,label,
+ * both fp32 per token.  A label outside 0 .. vocab - 1 marks a position without
+ * a target (padding): its loss and lse are 0 and its H row, which may hold
+ * anything, takes no part in any gradient.  bf16 tensors go through bf16 MFMA
+ * with fp32 accumulation; fp32 ones as three bf16 parts each, to fp32
+ * accuracy (an infinity in a row that counts gives NaN).
+ * Errors: MO_ERR_INVALID_ARG (null pointer with tokens > 0, tokens < 0, vocab or
+ * dim < 1, bad stride), MO_ERR_UNSUPPORTED (dtype, tokens > 2^20, vocab > 2^26,
+ * dim > 2^16), MO_ERR_WORKSPACE_TOO_SMALL, MO_ERR_ALIAS, MO_ERR_HIP. */
+mo_status softmax_xent_forward(const mo_head* head, const int64_t* labels, float* loss, float* lse,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of sum_n dloss_n loss_n: dH (tokens x dim) and dW (vocab x dim), of
+ * the head's dtype, each optional (NULL), every row written.  loss and lse are
+ * the forward call's.  delta_nv = dloss_n (exp(z_nv - lse_n) - [v = label]) is
+ * computed again from H and W, rounded to dtype, dH = delta W, dW = delta^T H
+ * with fp32 sums.  A row with dloss_n == 0 takes no part. */
+mo_status softmax_xent_backward(const mo_head* head, const int64_t* labels, const float* loss,
+                                const float* lse, const float* dloss, void* dH, int64_t ld_dh,
+                                void* dW, int64_t ld_dw, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/* A teacher's top logits per token: ids (tokens x k int64) and logits (tokens x
+ * k, dtype), 1 <= k <= MO_TOPK_MAX, and the temperature T > 0.  An id outside
+ * 0 .. vocab - 1 is an absent entry; its logit is not used. */
+#define MO_TOPK_MAX 1024
+typedef struct mo_topk {
+    const int64_t* ids;
+    const void*    logits;
+    int64_t        ld_ids, ld_logits;
+    int32_t        k, dtype;
+    float          temperature;
+} mo_topk;
+
+mo_status topk_distill_workspace_bytes(const mo_head* head, const mo_topk* top, int32_t backward,
+                                       size_t* bytes);
+
+/* Distillation: p = softmax(logits / T) over a row's present entries, q =
+ * softmax(z / T) over the whole vocabulary, loss_n = T^2 sum_k p_k (log p_k -
+ * log q_k), the divergence of the student from the teacher's renormalised top
+ * entries.  An id named twice counts as two entries.  lse_n = log(sum_v
+ * exp(z_nv / T)), z (tokens x k fp32, contiguous) the student's logits at the ids
+ * (0 where absent), both for the backward call.  A row without present entries,
+ * or whose present logits are all -infinity, has loss and lse 0 and no gradient. */
+mo_status topk_distill_forward(const mo_head* head, const mo_topk* top, float* loss, float* lse,
+                               float* z, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of sum_n dloss_n loss_n with respect to H and W, as
+ * softmax_xent_backward with delta = T dloss_n (q - p). */
+mo_status topk_distill_backward(const mo_head* head, const mo_topk* top, const float* lse,
+                                const float* z, const float* dloss, void* dH, int64_t ld_dh,
+                                void* dW, int64_t ld_dw, void* workspace, size_t workspace_bytes,
+                                void* stream);
 
 /* ---- owner planner (host only) --------------------------------------------
  * The step upstream of a bucket: which data-parallel rank owns each role

@@ -29,7 +29,9 @@ LR_ADJUST = {"original": 0, "match_rms_adamw": 1, "none": 2}
 
 PHASES = ["momentum", "norm", "gram", "poly", "update", "apply", "adamw", "copy", "update_last",
           "sh_layout", "sh_stats", "sh_rootprep", "sh_root", "sh_left", "sh_right",
-          "so_prep", "so_stats", "so_solve", "so_apply", "so_sort", "so_products", "so_warm"]
+          "so_prep", "so_stats", "so_solve", "so_apply", "so_sort", "so_products", "so_warm",
+          "emb_fwd", "emb_sort", "emb_bwd", "ln_fwd", "ln_bwd",
+          "hd_prep", "hd_target", "hd_lse", "hd_delta", "hd_dw", "hd_dh"]
 
 
 class MoError(RuntimeError):
@@ -94,7 +96,11 @@ EXPORTS = ["muon_workspace_bytes", "muon_build_worklist", "muon_owner_step", "ad
            "mo_status_string", "mo_profile_enable", "mo_profile_read", "mo_device_copy",
            "mo_plan_owners", "mo_plan_score", "mo_plan_layout", "shampoo_workspace_bytes",
            "shampoo_owner_step", "soap_workspace_bytes", "soap_owner_step", "soap_converged",
-           "muon_owner_step_noalloc"]
+           "muon_owner_step_noalloc", "embedding_forward", "embedding_workspace_bytes",
+           "embedding_backward", "layer_norm_forward", "layer_norm_workspace_bytes",
+           "layer_norm_backward", "softmax_xent_workspace_bytes", "softmax_xent_forward",
+           "softmax_xent_backward", "topk_distill_workspace_bytes", "topk_distill_forward",
+           "topk_distill_backward"]
 
 ROLE_MATRIX, ROLE_TAIL = 0, 1
 PLAN_POLICIES = {"role_greedy": 0, "scope_greedy": 1, "cost_aware": 2}
@@ -104,6 +110,20 @@ class MoRole(ctypes.Structure):
     """mo_role of include/mo.h."""
     _fields_ = [("block", ctypes.c_int32), ("kind", ctypes.c_int32),
                 ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
+
+
+class MoHead(ctypes.Structure):
+    """mo_head of include/mo.h."""
+    _fields_ = [("H", ctypes.c_void_p), ("W", ctypes.c_void_p), ("tokens", ctypes.c_int64),
+                ("vocab", ctypes.c_int64), ("dim", ctypes.c_int64), ("ld_h", ctypes.c_int64),
+                ("ld_w", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
+class MoTopk(ctypes.Structure):
+    """mo_topk of include/mo.h."""
+    _fields_ = [("ids", ctypes.c_void_p), ("logits", ctypes.c_void_p), ("ld_ids", ctypes.c_int64),
+                ("ld_logits", ctypes.c_int64), ("k", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("temperature", ctypes.c_float)]
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -154,6 +174,27 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                     ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
     lib.soap_converged.argtypes = [P(MoSoapMatrix), ctypes.c_int32, P(MoSoapHParams), ctypes.c_void_p,
                                    ctypes.c_size_t, P(ctypes.c_int32), ctypes.c_void_p]
+    ptr, i64, i32, f32, size = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float,
+                                ctypes.c_size_t)
+    head, topk, out = P(MoHead), P(MoTopk), P(ctypes.c_size_t)
+    operators = {
+        "embedding_forward": [ptr, i64, ptr, i64, i64, i64, i32, f32, ptr, i64, ptr],
+        "embedding_workspace_bytes": [i64, i64, i64, out],
+        "embedding_backward": [ptr, i64, ptr, i64, i32, ptr, i64, i32, i64, i64, f32, i32, ptr, size, ptr],
+        "layer_norm_forward": [ptr, i64, ptr, ptr, ptr, i64, ptr, ptr, i64, i64, i32, f32, ptr],
+        "layer_norm_workspace_bytes": [i64, i64, out],
+        "layer_norm_backward": [ptr, i64, ptr, i64, ptr, ptr, ptr, ptr, i64, ptr, ptr, i64, i64, i32, ptr,
+                                size, ptr],
+        "softmax_xent_workspace_bytes": [head, i32, out],
+        "softmax_xent_forward": [head, ptr, ptr, ptr, ptr, size, ptr],
+        "softmax_xent_backward": [head, ptr, ptr, ptr, ptr, ptr, i64, ptr, i64, ptr, size, ptr],
+        "topk_distill_workspace_bytes": [head, topk, i32, out],
+        "topk_distill_forward": [head, topk, ptr, ptr, ptr, ptr, size, ptr],
+        "topk_distill_backward": [head, topk, ptr, ptr, ptr, ptr, i64, ptr, i64, ptr, size, ptr],
+    }
+    for name, types in operators.items():
+        getattr(lib, name).argtypes = types
+        getattr(lib, name).restype = ctypes.c_int32
     for name in ("muon_workspace_bytes", "muon_build_worklist", "muon_owner_step",
                  "adamw_tail_step", "mo_profile_enable", "mo_profile_read", "mo_device_copy",
                  "mo_plan_owners", "mo_plan_score", "mo_plan_layout", "shampoo_workspace_bytes",

@@ -1,0 +1,711 @@
+// The output head's losses without its logits: softmax cross entropy, and
+// distillation from a teacher's top logits, with the gradients of the hidden
+// states H (tokens x dim) and the head W (vocab x dim).
+//
+//   z = H W^T,  lse_n = log sum_v exp(z_nv / T)
+//   cross entropy (T = 1)  loss_n = lse_n - z_ny
+//   distillation           p = softmax(t / T) over the stored entries,
+//                          loss_n = T^2 sum_k p_k (log p_k - (z_k / T - lse_n))
+//   delta_nv = c_n (exp(z_nv / T - lse_n) - p_nv),  c_n = T dloss_n
+//   dH = delta W,  dW = delta^T H
+//
+// Forward: one product whose epilogue keeps, per tile and token, the maximum
+// and the sum of exponentials over the tile's 256 vocabulary rows; the target
+// logits are gathered dot products.  Backward: pieces of the vocabulary, each
+// computed again from H and W into delta (bf16, or the three planes of fp32),
+// in both orientations, from which dW's rows are finished and dH accumulated
+// in fp32.  8 N V d flops in all, against 6 N V d when the logits are kept.
+//
+// Rounding: the logits are never rounded (fp32 accumulators); delta takes the
+// tensors' own precision (bf16: half a unit in 2^8, the size of the rounding
+// of the results themselves; fp32: exact); sums are fp32.
+#include "head_gemm.h"
+#include "op_common.h"
+#include "operators.h"
+
+namespace {
+
+using namespace mo_head_gemm;
+
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+
+MO_DEV float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// ---- operand copies ---------------------------------------------------------------
+
+// One 8-element chunk of a value's planes (16 bytes each).
+template <int PL> MO_DEV void put_planes(bf16_t* dst, int64_t plane, const f32x8& v) {
+    if constexpr (PL == 1) {
+        st8(dst, v);
+    } else {
+        bf16x8 h, m, l;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            bf16_t a, b, c;
+            split_f32(v.v[e], a, b, c);
+            h[e] = a; m[e] = b; l[e] = c;
+        }
+        *reinterpret_cast<u32x4*>(dst) = __builtin_bit_cast(u32x4, h);
+        *reinterpret_cast<u32x4*>(dst + plane) = __builtin_bit_cast(u32x4, m);
+        *reinterpret_cast<u32x4*>(dst + 2 * plane) = __builtin_bit_cast(u32x4, l);
+    }
+}
+
+// dst[plane][row][kd] <- src rows, zeros from dim to kd.
+template <typename T, int PL>
+__global__ __launch_bounds__(256) void head_pack_kernel(const T* src, int64_t ld, int64_t rows, int dim,
+                                                        bf16_t* dst, int kd, int64_t plane) {
+    const int64_t chunks = int64_t(kd / 8) * rows;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < chunks; i += int64_t(gridDim.x) * 256) {
+        const int64_t r = i / (kd / 8);
+        const int c = int(i - r * (kd / 8)) * 8;
+        put_planes<PL>(dst + r * kd + c, plane, widen(ld8n(src + r * ld + c, dim - c)));
+    }
+}
+
+// dst[plane][c][ldt] <- src[r][c] for the 64 x 64 tile (blockIdx.x over rows,
+// blockIdx.y over columns); rows from `rows` to 64 * gridDim.x are zero, and so
+// are the rows whose coefficient is 0 (they may hold anything).
+template <typename T, int PL>
+__global__ __launch_bounds__(256) void head_transpose_kernel(const T* src, int64_t ld, int64_t rows, int dim,
+                                                             const float* coef, bf16_t* dst, int64_t ldt,
+                                                             int64_t plane) {
+    __shared__ float tile[64][65];
+    const int64_t r0 = int64_t(blockIdx.x) * 64;
+    const int c0 = blockIdx.y * 64;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int q = threadIdx.x + 256 * i, r = q >> 3, c = (q & 7) * 8;
+        const bool on = r0 + r < rows && (!coef || coef[r0 + r] != 0.f);
+        const f32x8 v = widen(ld8n(src + (r0 + r) * ld + c0 + c, on ? dim - c0 - c : 0));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) tile[r][c + e] = v.v[e];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int q = threadIdx.x + 256 * i, c = q >> 3, r = (q & 7) * 8;
+        if (c0 + c >= dim) continue;
+        f32x8 v;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v.v[e] = tile[r + e][c];
+        put_planes<PL>(dst + int64_t(c0 + c) * ldt + r0 + r, plane, v);
+    }
+}
+
+// ---- forward ----------------------------------------------------------------------
+
+// Tile (ti, tj): vocabulary rows 256 ti .. of the piece, tokens TN tj ...  Each
+// lane holds 16 MB vocabulary values of one token per column block, so the
+// maximum and the sum are mostly in registers.
+template <int NB, int PL>
+__global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2, 2))) void head_lse_kernel(
+    Operand W, Operand H, int nk, uint32_t tm, uint32_t tn, float zscale, float2* part, int64_t n_pad) {
+    using L = Layout<NB>;
+    __shared__ __align__(16) uint8_t smem[head_lds(NB)];
+    uint32_t ti, tj;
+    if (!head_tile_of(blockIdx.x, tm, tn, ti, tj)) return;
+    const int64_t v0 = int64_t(ti) * 256, n0 = int64_t(tj) * 64 * NB;
+    f32x16 acc[L::MB][L::NBW];
+    head_tile<NB, PL>(smem, W, H, v0, n0, 0, nk, acc);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int wm = wave / L::WN, wn = wave % L::WN, r32 = lane & 31, kg = lane >> 5;
+    const int left = int(W.rows - v0 < 256 ? W.rows - v0 : 256) - wm * (L::MB * 32) - kg * 4;
+    float2* st = reinterpret_cast<float2*>(smem);   // [WM][TN]
+    const float k2 = zscale * LOG2E;
+#pragma unroll
+    for (int b = 0; b < L::NBW; ++b) {
+        float m = -__builtin_inff(), s = 0.f;
+#pragma unroll
+        for (int a = 0; a < L::MB; ++a)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                const int row = a * 32 + (v >> 2) * 8 + (v & 3);
+                const float z = row < left ? acc[a][b][v] * k2 : -__builtin_inff();
+                acc[a][b][v] = z;
+                m = fmaxf(m, z);
+            }
+        m = fmaxf(m, __shfl_xor(m, 32, 64));
+        const float mm = m == -__builtin_inff() ? 0.f : m;   // nothing but -inf: the sum is 0
+#pragma unroll
+        for (int a = 0; a < L::MB; ++a)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) s += exp2_hw(acc[a][b][v] - mm);
+        s += __shfl_xor(s, 32, 64);
+        if (kg == 0) st[wm * 64 * NB + wn * 64 + b * 32 + r32] = float2{m, s};
+    }
+    __syncthreads();
+    for (int t = threadIdx.x; t < 64 * NB; t += H_THREADS) {
+        float m = -__builtin_inff(), s = 0.f;
+#pragma unroll
+        for (int w = 0; w < L::WM; ++w) m = fmaxf(m, st[w * 64 * NB + t].x);
+        const float mm = m == -__builtin_inff() ? 0.f : m;
+#pragma unroll
+        for (int w = 0; w < L::WM; ++w) s += st[w * 64 * NB + t].y * exp2_hw(st[w * 64 * NB + t].x - mm);
+        part[int64_t(ti) * n_pad + n0 + t] = float2{m, s};
+    }
+}
+
+// z[n][j] = H_n . W_id (not yet divided by T), 0 where the id is outside the
+// vocabulary: one wavefront per pair.
+template <typename T>
+__global__ __launch_bounds__(256) void head_target_kernel(const T* H, int64_t ldh, const T* W, int64_t ldw,
+                                                          const int64_t* ids, int64_t ld_ids, int k,
+                                                          int64_t pairs, int64_t vocab, int dim, float* z) {
+    const int lane = threadIdx.x & 63;
+    for (int64_t i = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6); i < pairs; i += int64_t(gridDim.x) * 4) {
+        const int64_t n = i / k, id = ids[n * ld_ids + (i - n * k)];
+        float s = 0.f;
+        if (uint64_t(id) < uint64_t(vocab)) {
+            const T *h = H + n * ldh, *w = W + id * ldw;
+            for (int c = lane * 8; c < dim; c += 512) {
+                const f32x8 a = widen(ld8n(h + c, dim - c)), b = widen(ld8n(w + c, dim - c));
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s = __builtin_fmaf(a.v[e], b.v[e], s);
+            }
+            s = wave_sum(s);
+        }
+        if (lane == 0) z[i] = s;
+    }
+}
+
+// log2-domain partial sums of 32 tokens -> lse (natural log), 32 strided shares
+// of the vocabulary tiles per token, combined in order.  Cross entropy's loss
+// comes with it; z holds the label's logit.
+__global__ __launch_bounds__(1024) void head_combine_kernel(const float2* part, int64_t n_pad, int64_t v_tiles,
+                                                            int64_t tokens, const int64_t* labels,
+                                                            int64_t vocab, const float* z, float* loss,
+                                                            float* lse) {
+    __shared__ float2 sh[32][33];
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int64_t n = int64_t(blockIdx.x) * 32 + tx;
+    float m = -__builtin_inff(), s = 0.f;
+    if (n < tokens)
+        for (int64_t t = ty; t < v_tiles; t += 32) {
+            const float2 q = part[t * n_pad + n];
+            const float mn = fmaxf(m, q.x), mm = mn == -__builtin_inff() ? 0.f : mn;
+            s = s * exp2_hw(m - mm) + q.y * exp2_hw(q.x - mm);
+            m = mn;
+        }
+    sh[ty][tx] = float2{m, s};
+    __syncthreads();
+    if (ty == 0 && n < tokens) {
+        for (int t = 1; t < 32; ++t) m = fmaxf(m, sh[t][tx].x);
+        const float mm = m == -__builtin_inff() ? 0.f : m;
+        s = 0.f;
+        for (int t = 0; t < 32; ++t) s += sh[t][tx].y * exp2_hw(sh[t][tx].x - mm);
+        float l = m * LN2 + logf(s);
+        if (labels) {
+            const bool in = uint64_t(labels[n]) < uint64_t(vocab);
+            loss[n] = in ? l - z[n] : 0.f;
+            l = in ? l : 0.f;
+        }
+        lse[n] = l;
+    }
+}
+
+// One row of the teacher, by one wavefront: the maximum of t / T over the entries
+// whose id is inside the vocabulary, and the sum of exp(t / T - maximum).  False
+// for a row with no such entry, or only entries of -infinity.
+MO_DEV bool teacher_row(const int64_t* ids, const void* teacher, bool bf16, int k, int64_t vocab, float inv_t,
+                        float& maxt, float& sum) {
+    const int lane = threadIdx.x & 63;
+    float m = -__builtin_inff();
+    for (int j = lane; j < k; j += 64)
+        if (uint64_t(ids[j]) < uint64_t(vocab)) m = fmaxf(m, load_elem(teacher, j, bf16) * inv_t);
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+    float s = 0.f;
+    const float mm = m == -__builtin_inff() ? 0.f : m;
+    for (int j = lane; j < k; j += 64)
+        if (uint64_t(ids[j]) < uint64_t(vocab)) s += expf(load_elem(teacher, j, bf16) * inv_t - mm);
+    sum = wave_sum(s);
+    maxt = mm;
+    return sum != 0.f;   // NaN counts as live and propagates
+}
+
+// loss_n = T^2 sum_j p_j (log p_j - (z_j / T - lse)); rows without entries: loss
+// and lse 0.  One wavefront per row.
+__global__ __launch_bounds__(256) void head_distill_loss_kernel(const int64_t* ids, int64_t ld_ids,
+                                                                const void* teacher, int64_t ld_t, bool t_bf16,
+                                                                int k, int64_t tokens, int64_t vocab,
+                                                                float inv_t, float t, const float* z,
+                                                                float* loss, float* lse) {
+    const int lane = threadIdx.x & 63;
+    for (int64_t n = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6); n < tokens; n += int64_t(gridDim.x) * 4) {
+        const int64_t* id = ids + n * ld_ids;
+        const uint8_t* te = static_cast<const uint8_t*>(teacher) + n * ld_t * (t_bf16 ? 2 : 4);
+        float mt, st;
+        const bool live = teacher_row(id, te, t_bf16, k, vocab, inv_t, mt, st);
+        const float l = lse[n], lst = logf(st);
+        float s = 0.f;
+        if (live)
+            for (int j = lane; j < k; j += 64) {
+                if (uint64_t(id[j]) >= uint64_t(vocab)) continue;
+                const float logp = load_elem(te, j, t_bf16) * inv_t - mt - lst, p = expf(logp);
+                if (p != 0.f) s += p * (logp - (z[n * k + j] * inv_t - l));
+            }
+        s = wave_sum(s);
+        if (lane == 0) {
+            loss[n] = live ? t * t * s : 0.f;
+            if (!live) lse[n] = 0.f;
+        }
+    }
+}
+
+// ---- backward: per-token coefficients ------------------------------------------------
+
+// coef[n] = T dloss_n (0: the row takes no part), nl2[n] = -lse_n log2 e, and
+// delta at the label, c (exp(z_y - lse) - 1) = c expm1(-loss).
+__global__ __launch_bounds__(256) void head_xent_prep_kernel(const int64_t* labels, const float* loss,
+                                                             const float* lse, const float* dloss,
+                                                             int64_t tokens, int64_t n_pad, int64_t vocab,
+                                                             float* coef, float* nl2, float* tval) {
+    const int64_t n = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    if (n >= n_pad) return;
+    float c = 0.f, l = 0.f;
+    if (n < tokens && uint64_t(labels[n]) < uint64_t(vocab)) {
+        c = dloss[n];
+        l = -lse[n] * LOG2E;
+    }
+    coef[n] = c;
+    nl2[n] = l;
+    if (n < tokens) tval[n] = c != 0.f ? c * expm1f(-loss[n]) : 0.f;
+}
+
+// The same for distillation, one wavefront per row; the entries of an id that a
+// row names twice add up, and each of them gets the one value of that id.
+__global__ __launch_bounds__(256) void head_distill_prep_kernel(const int64_t* ids, int64_t ld_ids,
+                                                                const void* teacher, int64_t ld_t, bool t_bf16,
+                                                                int k, int64_t tokens, int64_t n_pad,
+                                                                int64_t vocab, float inv_t, float t,
+                                                                const float* z, const float* lse,
+                                                                const float* dloss, float* coef, float* nl2,
+                                                                float* tval) {
+    const int lane = threadIdx.x & 63;
+    const int64_t n = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
+    if (n >= n_pad) return;
+    float c = 0.f, l = 0.f;
+    if (n < tokens) {
+        const int64_t* id = ids + n * ld_ids;
+        const uint8_t* te = static_cast<const uint8_t*>(teacher) + n * ld_t * (t_bf16 ? 2 : 4);
+        float mt, st;
+        if (teacher_row(id, te, t_bf16, k, vocab, inv_t, mt, st)) {
+            c = t * dloss[n];
+            l = lse[n];
+        }
+        for (int j = lane; j < k; j += 64) {
+            const int64_t v = id[j];
+            float o = 0.f;
+            if (c != 0.f && uint64_t(v) < uint64_t(vocab)) {
+                float p = 0.f;
+                for (int u = 0; u < k; ++u)
+                    if (id[u] == v) p += expf(load_elem(te, u, t_bf16) * inv_t - mt) / st;
+                o = c * (expf(z[n * k + j] * inv_t - l) - p);
+            }
+            tval[n * k + j] = o;
+        }
+    }
+    if (lane == 0) {
+        coef[n] = c;
+        nl2[n] = -l * LOG2E;
+    }
+}
+
+// ---- backward: delta of one piece ----------------------------------------------------
+
+// D[plane][token][piece] and DT[plane][vocabulary row][n_pad].
+template <int NB, int PL>
+__global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2, 2))) void head_delta_kernel(
+    Operand W, Operand H, int nk, uint32_t tm, uint32_t tn, float zscale, const float* coef, const float* nl2,
+    bf16_t* D, int64_t ldd, int64_t plane_d, bf16_t* DT, int64_t ldt, int64_t plane_t) {
+    using L = Layout<NB>;
+    __shared__ __align__(16) uint8_t smem[head_lds(NB)];
+    uint32_t ti, tj;
+    if (!head_tile_of(blockIdx.x, tm, tn, ti, tj)) return;
+    const int64_t v0 = int64_t(ti) * 256, n0 = int64_t(tj) * 64 * NB;
+    f32x16 acc[L::MB][L::NBW];
+    head_tile<NB, PL>(smem, W, H, v0, n0, 0, nk, acc);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int wm = wave / L::WN, wn = wave % L::WN, r32 = lane & 31, kg = lane >> 5;
+    const int left = int(W.rows - v0 < 256 ? W.rows - v0 : 256) - wm * (L::MB * 32) - kg * 4;
+    uint8_t* st = smem + wave * (32 * 64 * 4);
+    float c[2], l[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        c[b] = coef[n0 + wn * 64 + b * 32 + r32];
+        l[b] = nl2[n0 + wn * 64 + b * 32 + r32];
+    }
+    const float k2 = zscale * LOG2E;
+#pragma unroll
+    for (int a = 0; a < L::MB; ++a) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                f32x4 v4;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float d = c[b] * exp2_hw(__builtin_fmaf(acc[a][b][4 * g + e], k2, l[b]));
+                    // rows behind the vocabulary and tokens that take no part
+                    v4[e] = a * 32 + g * 8 + e < left && c[b] != 0.f ? d : 0.f;
+                }
+                *reinterpret_cast<f32x4*>(st + st_off(b * 32 + r32, g * 8 + kg * 4)) = v4;
+            }
+        __builtin_amdgcn_wave_barrier();
+        const int64_t vrow = v0 + wm * (L::MB * 32) + a * 32, tok = n0 + wn * 64;
+        // token j of the block, 8 vocabulary rows
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int j = (lane >> 2) + 16 * t, ic = lane & 3;
+            const f32x4 lo = *reinterpret_cast<const f32x4*>(st + st_off(j, ic * 8));
+            const f32x4 hi = *reinterpret_cast<const f32x4*>(st + st_off(j, ic * 8 + 4));
+            f32x8 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) { v.v[e] = lo[e]; v.v[4 + e] = hi[e]; }
+            put_planes<PL>(D + (tok + j) * ldd + vrow + ic * 8, plane_d, v);
+        }
+        // vocabulary row, 8 tokens
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int cc = lane & 7, row = (lane >> 3) + 8 * t;
+            f32x8 v;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v.v[e] = *reinterpret_cast<const float*>(st + st_off(cc * 8 + e, row));
+            put_planes<PL>(DT + (vrow + row) * ldt + tok + cc * 8, plane_t, v);
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// delta at the targets that fall into the piece, in both orientations.
+template <int PL>
+__global__ __launch_bounds__(256) void head_patch_kernel(const int64_t* ids, int64_t ld_ids, int k,
+                                                         int64_t pairs, const float* tval, const float* coef,
+                                                         int64_t v0, int64_t rows, bf16_t* D, int64_t ldd,
+                                                         int64_t plane_d, bf16_t* DT, int64_t ldt,
+                                                         int64_t plane_t) {
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < pairs; i += int64_t(gridDim.x) * 256) {
+        const int64_t n = i / k, v = ids[n * ld_ids + (i - n * k)] - v0;
+        if (uint64_t(v) >= uint64_t(rows) || coef[n] == 0.f) continue;
+        const float x = tval[i];
+        bf16_t p[3];
+        if constexpr (PL == 1) p[0] = (bf16_t)x;
+        else split_f32(x, p[0], p[1], p[2]);
+#pragma unroll
+        for (int q = 0; q < PL; ++q) {
+            D[q * plane_d + n * ldd + v] = p[q];
+            DT[q * plane_t + v * ldt + n] = p[q];
+        }
+    }
+}
+
+// ---- backward: the two products of a piece --------------------------------------------
+
+// dW rows of the piece = DT HT^T (K over the tokens), rounded to T.
+template <typename T, int NB, int PL>
+__global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2, 2))) void head_dw_kernel(
+    Operand DT, Operand HT, int nk, uint32_t tm, uint32_t tn, T* dW, int64_t ldw, int dim) {
+    using L = Layout<NB>;
+    __shared__ __align__(16) uint8_t smem[head_lds(NB)];
+    uint32_t ti, tj;
+    if (!head_tile_of(blockIdx.x, tm, tn, ti, tj)) return;
+    const int64_t v0 = int64_t(ti) * 256, c0 = int64_t(tj) * 64 * NB;
+    f32x16 acc[L::MB][L::NBW];
+    head_tile<NB, PL>(smem, DT, HT, v0, c0, 0, nk, acc);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int wm = wave / L::WN, wn = wave % L::WN, r32 = lane & 31, kg = lane >> 5;
+    uint8_t* st = smem + wave * (32 * 64 * 4);
+#pragma unroll
+    for (int a = 0; a < L::MB; ++a) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                *reinterpret_cast<f32x4*>(st + st_off(b * 32 + r32, g * 8 + kg * 4)) =
+                    f32x4{acc[a][b][4 * g], acc[a][b][4 * g + 1], acc[a][b][4 * g + 2], acc[a][b][4 * g + 3]};
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int cc = lane & 7, row = (lane >> 3) + 8 * t;
+            f32x8 v;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v.v[e] = *reinterpret_cast<const float*>(st + st_off(cc * 8 + e, row));
+            const int64_t vr = v0 + wm * (L::MB * 32) + a * 32 + row;
+            const int c = int(c0) + wn * 64 + cc * 8;
+            if (vr < DT.rows) st8n(dW + vr * ldw + c, v, dim - c);
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// One split of dH^T += WT D^T over the piece's vocabulary rows: the fp32 tile in
+// accumulator order (lane by lane, 16 bytes each), read and written whole.
+template <int NB, int PL>
+__global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2, 2))) void head_dh_kernel(
+    Operand WT, Operand D, int nk, int stages, uint32_t tm, uint32_t tn, uint32_t splits, int first,
+    f32x4* out) {
+    using L = Layout<NB>;
+    __shared__ __align__(16) uint8_t smem[head_lds(NB)];
+    uint32_t ti, tj;
+    // the splits of a tile are rows of tiles: tile row ti of split s is s tm + ti
+    if (!head_tile_of(blockIdx.x, tm * splits, tn, ti, tj)) return;
+    const uint32_t sp = ti / tm;
+    ti -= sp * tm;
+    const int k0 = int(sp) * stages, n = nk - k0 < stages ? nk - k0 : stages;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    f32x4* o = out + (((int64_t(sp) * tm + ti) * tn + tj) * 8 + wave) * (L::MB * L::NBW * 4 * 64) + lane;
+    if (n <= 0) {
+        // a short last piece may leave a split without stages
+        if (first)
+#pragma unroll
+            for (int i = 0; i < L::MB * L::NBW * 4; ++i) o[i * 64] = f32x4{0.f, 0.f, 0.f, 0.f};
+        return;
+    }
+    f32x16 acc[L::MB][L::NBW];
+    head_tile<NB, PL>(smem, WT, D, int64_t(ti) * 256, int64_t(tj) * 64 * NB, k0, n, acc);
+#pragma unroll
+    for (int a = 0; a < L::MB; ++a)
+#pragma unroll
+        for (int b = 0; b < L::NBW; ++b)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                f32x4 v = {acc[a][b][4 * g], acc[a][b][4 * g + 1], acc[a][b][4 * g + 2], acc[a][b][4 * g + 3]};
+                f32x4* q = o + ((a * L::NBW + b) * 4 + g) * 64;
+                if (!first) {
+                    const f32x4 old = *q;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] += old[e];
+                }
+                *q = v;
+            }
+}
+
+// dH <- the sum of the splits in order, one workgroup per wave block of a tile
+// (32 MB columns of dH x 64 tokens), turned through LDS.  Tokens that take no
+// part get zeros.
+template <typename T, int NB>
+__global__ __launch_bounds__(256) void head_dh_out_kernel(const f32x4* acc, uint32_t tm, uint32_t tn,
+                                                          uint32_t splits, const float* coef, T* dH,
+                                                          int64_t ld, int64_t tokens, int dim) {
+    using L = Layout<NB>;
+    constexpr int BLK = L::MB * L::NBW * 4, COLS = 32 * L::MB;
+    __shared__ float tile[64][COLS + 4];
+    const uint32_t wave = blockIdx.x & 7, tile_id = blockIdx.x >> 3, ti = tile_id / tn, tj = tile_id - ti * tn;
+    for (int i = threadIdx.x; i < BLK * 64; i += 256) {
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+        for (uint32_t s = 0; s < splits; ++s) {
+            const f32x4 x = acc[((int64_t(s) * tm * tn + tile_id) * 8 + wave) * (BLK * 64) + i];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] += x[e];
+        }
+        const int lane = i & 63, q = i >> 6, g = q & 3, b = (q >> 2) % L::NBW, a = (q >> 2) / L::NBW;
+        *reinterpret_cast<f32x4*>(&tile[b * 32 + (lane & 31)][a * 32 + g * 8 + (lane >> 5) * 4]) = v;
+    }
+    __syncthreads();
+    const int64_t n0 = int64_t(tj) * 64 * NB + (wave % L::WN) * 64;
+    const int c0 = int(ti) * 256 + int(wave / L::WN) * COLS;
+    for (int i = threadIdx.x; i < 64 * (COLS / 8); i += 256) {
+        const int j = i / (COLS / 8), c = (i % (COLS / 8)) * 8;
+        if (n0 + j >= tokens || c0 + c >= dim) continue;
+        const bool on = coef[n0 + j] != 0.f;
+        f32x8 v;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v.v[e] = on ? tile[j][c + e] : 0.f;
+        st8n(dH + (n0 + j) * ld + c0 + c, v, dim - c0 - c);
+    }
+}
+
+// ---- operands ---------------------------------------------------------------------
+
+Operand rows_of(const void* p, int64_t ld_elems, int64_t rows, int64_t plane_elems) {
+    return {static_cast<const uint8_t*>(p), ld_elems * 2, rows, plane_elems * 2};
+}
+Operand h_operand(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws) {
+    return p.pack_h ? rows_of(ws + p.off_hp, p.kd, a.tokens, a.tokens * p.kd) : rows_of(a.H, a.ldh, a.tokens, 0);
+}
+Operand w_operand(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int64_t v0, int64_t rows) {
+    return p.pack_w ? rows_of(ws + p.off_wp, p.kd, rows, p.piece * p.kd)
+                    : rows_of(static_cast<const bf16_t*>(a.W) + v0 * a.ldw, a.ldw, rows, 0);
+}
+
+unsigned cap_grid(int64_t want, int64_t cap) { return unsigned(want < 1 ? 1 : want < cap ? want : cap); }
+
+template <typename K, typename... A>
+hipError_t go(K* kernel, dim3 grid, dim3 block, hipStream_t s, A... args) {
+    hipLaunchKernelGGL(kernel, grid, block, 0, s, args...);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+// Calls `f` with the plan's tile width and plane count as template arguments.
+#define MO_HEAD_PICK(NBV, PLV, CALL)                                    \
+    do {                                                                \
+        if ((PLV) == 1) {                                               \
+            if ((NBV) == 4) { CALL(4, 1); }                             \
+            if ((NBV) == 2) { CALL(2, 1); }                             \
+            CALL(1, 1);                                                 \
+        }                                                               \
+        if ((NBV) == 4) { CALL(4, 3); }                                 \
+        if ((NBV) == 2) { CALL(2, 3); }                                 \
+        CALL(1, 3);                                                     \
+    } while (0)
+
+hipError_t mo_launch_head_pack(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, bool h, int64_t v0,
+                               int64_t rows, hipStream_t s) {
+    const int64_t ld = h ? a.ldh : a.ldw;
+    bf16_t* dst = reinterpret_cast<bf16_t*>(ws + (h ? p.off_hp : p.off_wp));
+    const int64_t plane = (h ? a.tokens : p.piece) * p.kd;
+    const dim3 grid(cap_grid((rows * (p.kd / 8) + 255) / 256, 1 << 16)), block(256);
+    if (p.planes == 1)
+        return go(head_pack_kernel<bf16_t, 1>, grid, block, s, static_cast<const bf16_t*>(h ? a.H : a.W) + v0 * ld, ld,
+                  rows, int(a.dim), dst, int(p.kd), plane);
+    return go(head_pack_kernel<float, 3>, grid, block, s, static_cast<const float*>(h ? a.H : a.W) + v0 * ld, ld, rows,
+              int(a.dim), dst, int(p.kd), plane);
+}
+
+hipError_t mo_launch_head_lse(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int64_t v0, int64_t rows,
+                              hipStream_t s) {
+    const Operand H = h_operand(a, p, ws), W = w_operand(a, p, ws, v0, rows);
+    const uint32_t tm = uint32_t((rows + 255) / 256), tn = uint32_t(p.n_pad / (64 * p.nb));
+    float2* part = reinterpret_cast<float2*>(ws + p.off_part) + v0 / 256 * p.n_pad;
+    const dim3 grid(head_grid(uint64_t(tm) * tn)), block(H_THREADS);
+#define MO_CALL(NB, PL) \
+    return go(head_lse_kernel<NB, PL>, grid, block, s, W, H, int(p.kd / 32), tm, tn, a.inv_t, part, p.n_pad)
+    MO_HEAD_PICK(p.nb, p.planes, MO_CALL);
+#undef MO_CALL
+}
+
+hipError_t mo_launch_head_targets(const MoHeadArgs& a, hipStream_t s) {
+    const int64_t pairs = a.tokens * a.k;
+    const dim3 grid(cap_grid((pairs + 3) / 4, 1 << 20)), block(256);
+    if (a.dtype == MO_BF16)
+        return go(head_target_kernel<bf16_t>, grid, block, s, static_cast<const bf16_t*>(a.H), a.ldh,
+                  static_cast<const bf16_t*>(a.W), a.ldw, a.ids, a.ld_ids, a.k, pairs, a.vocab, int(a.dim), a.z);
+    return go(head_target_kernel<float>, grid, block, s, static_cast<const float*>(a.H), a.ldh,
+              static_cast<const float*>(a.W), a.ldw, a.ids, a.ld_ids, a.k, pairs, a.vocab, int(a.dim), a.z);
+}
+
+hipError_t mo_launch_head_loss(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, hipStream_t s) {
+    const float2* part = reinterpret_cast<const float2*>(ws + p.off_part);
+    hipError_t e = go(head_combine_kernel, dim3(unsigned((a.tokens + 31) / 32)), dim3(1024), s, part, p.n_pad,
+                      p.v_tiles, a.tokens, a.teacher ? nullptr : a.ids, a.vocab, a.z, a.loss, a.lse);
+    if (e != hipSuccess || !a.teacher) return e;
+    return go(head_distill_loss_kernel, dim3(cap_grid((a.tokens + 3) / 4, 1 << 20)), dim3(256), s, a.ids, a.ld_ids,
+              a.teacher, a.ld_teacher, a.teacher_dtype == MO_BF16, a.k, a.tokens, a.vocab, a.inv_t, a.t,
+              static_cast<const float*>(a.z), a.loss, a.lse);
+}
+
+hipError_t mo_launch_head_prep(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, hipStream_t s) {
+    float *coef = reinterpret_cast<float*>(ws + p.off_coef), *nl2 = reinterpret_cast<float*>(ws + p.off_nl2);
+    float* tval = reinterpret_cast<float*>(ws + p.off_tval);
+    if (!a.teacher)
+        return go(head_xent_prep_kernel, dim3(unsigned((p.n_pad + 255) / 256)), dim3(256), s, a.ids, a.loss_in,
+                  a.lse_in, a.dloss, a.tokens, p.n_pad, a.vocab, coef, nl2, tval);
+    return go(head_distill_prep_kernel, dim3(unsigned((p.n_pad + 3) / 4)), dim3(256), s, a.ids, a.ld_ids, a.teacher,
+              a.ld_teacher, a.teacher_dtype == MO_BF16, a.k, a.tokens, p.n_pad, a.vocab, a.inv_t, a.t, a.z_in,
+              a.lse_in, a.dloss, coef, nl2, tval);
+}
+
+hipError_t mo_launch_head_ht(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, hipStream_t s) {
+    const float* coef = reinterpret_cast<const float*>(ws + p.off_coef);
+    bf16_t* dst = reinterpret_cast<bf16_t*>(ws + p.off_ht);
+    const dim3 grid(unsigned(p.n_pad / 64), unsigned((a.dim + 63) / 64)), block(256);
+    if (p.planes == 1)
+        return go(head_transpose_kernel<bf16_t, 1>, grid, block, s, static_cast<const bf16_t*>(a.H), a.ldh, a.tokens,
+                  int(a.dim), coef, dst, p.n_pad, a.dim * p.n_pad);
+    return go(head_transpose_kernel<float, 3>, grid, block, s, static_cast<const float*>(a.H), a.ldh, a.tokens,
+              int(a.dim), coef, dst, p.n_pad, a.dim * p.n_pad);
+}
+
+hipError_t mo_launch_head_wt(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int64_t v0, int64_t rows,
+                             hipStream_t s) {
+    bf16_t* dst = reinterpret_cast<bf16_t*>(ws + p.off_wt);
+    const dim3 grid(unsigned((rows + 255) / 256 * 4), unsigned((a.dim + 63) / 64)), block(256);
+    if (p.planes == 1)
+        return go(head_transpose_kernel<bf16_t, 1>, grid, block, s, static_cast<const bf16_t*>(a.W) + v0 * a.ldw, a.ldw,
+                  rows, int(a.dim), static_cast<const float*>(nullptr), dst, p.piece, a.dim * p.piece);
+    return go(head_transpose_kernel<float, 3>, grid, block, s, static_cast<const float*>(a.W) + v0 * a.ldw, a.ldw, rows,
+              int(a.dim), static_cast<const float*>(nullptr), dst, p.piece, a.dim * p.piece);
+}
+
+hipError_t mo_launch_head_delta(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int64_t v0, int64_t rows,
+                                hipStream_t s) {
+    const Operand H = h_operand(a, p, ws), W = w_operand(a, p, ws, v0, rows);
+    const uint32_t tm = uint32_t((rows + 255) / 256), tn = uint32_t(p.n_pad / (64 * p.nb));
+    const dim3 grid(head_grid(uint64_t(tm) * tn)), block(H_THREADS);
+    const float *coef = reinterpret_cast<const float*>(ws + p.off_coef),
+                *nl2 = reinterpret_cast<const float*>(ws + p.off_nl2);
+    bf16_t *D = reinterpret_cast<bf16_t*>(ws + p.off_d), *DT = reinterpret_cast<bf16_t*>(ws + p.off_dt);
+#define MO_CALL(NB, PL)                                                                                      \
+    return go(head_delta_kernel<NB, PL>, grid, block, s, W, H, int(p.kd / 32), tm, tn, a.inv_t, coef, nl2, D, \
+              p.piece, p.n_pad * p.piece, DT, p.n_pad, p.n_pad * p.piece)
+    MO_HEAD_PICK(p.nb, p.planes, MO_CALL);
+#undef MO_CALL
+}
+
+hipError_t mo_launch_head_patch(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int64_t v0, int64_t rows,
+                                hipStream_t s) {
+    const int64_t pairs = a.tokens * a.k;
+    const float *coef = reinterpret_cast<const float*>(ws + p.off_coef),
+                *tval = reinterpret_cast<const float*>(ws + p.off_tval);
+    bf16_t *D = reinterpret_cast<bf16_t*>(ws + p.off_d), *DT = reinterpret_cast<bf16_t*>(ws + p.off_dt);
+    const dim3 grid(cap_grid((pairs + 255) / 256, 1 << 16)), block(256);
+    if (p.planes == 1)
+        return go(head_patch_kernel<1>, grid, block, s, a.ids, a.ld_ids, a.k, pairs, tval, coef, v0, rows, D, p.piece,
+                  p.n_pad * p.piece, DT, p.n_pad, p.n_pad * p.piece);
+    return go(head_patch_kernel<3>, grid, block, s, a.ids, a.ld_ids, a.k, pairs, tval, coef, v0, rows, D, p.piece,
+              p.n_pad * p.piece, DT, p.n_pad, p.n_pad * p.piece);
+}
+
+hipError_t mo_launch_head_dw(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int64_t v0, int64_t rows,
+                             hipStream_t s) {
+    const Operand DT = rows_of(ws + p.off_dt, p.n_pad, rows, p.n_pad * p.piece);
+    const Operand HT = rows_of(ws + p.off_ht, p.n_pad, a.dim, a.dim * p.n_pad);
+    const uint32_t tm = uint32_t((rows + 255) / 256), tn = uint32_t((a.dim + 64 * p.nb_dw - 1) / (64 * p.nb_dw));
+    const dim3 grid(head_grid(uint64_t(tm) * tn)), block(H_THREADS);
+    const int nk = int(p.n_pad / 32);
+    if (p.planes == 1) {
+        bf16_t* dW = static_cast<bf16_t*>(a.dW) + v0 * a.lddw;
+        if (p.nb_dw == 4) return go(head_dw_kernel<bf16_t, 4, 1>, grid, block, s, DT, HT, nk, tm, tn, dW, a.lddw, int(a.dim));
+        if (p.nb_dw == 2) return go(head_dw_kernel<bf16_t, 2, 1>, grid, block, s, DT, HT, nk, tm, tn, dW, a.lddw, int(a.dim));
+        return go(head_dw_kernel<bf16_t, 1, 1>, grid, block, s, DT, HT, nk, tm, tn, dW, a.lddw, int(a.dim));
+    }
+    float* dW = static_cast<float*>(a.dW) + v0 * a.lddw;
+    if (p.nb_dw == 4) return go(head_dw_kernel<float, 4, 3>, grid, block, s, DT, HT, nk, tm, tn, dW, a.lddw, int(a.dim));
+    if (p.nb_dw == 2) return go(head_dw_kernel<float, 2, 3>, grid, block, s, DT, HT, nk, tm, tn, dW, a.lddw, int(a.dim));
+    return go(head_dw_kernel<float, 1, 3>, grid, block, s, DT, HT, nk, tm, tn, dW, a.lddw, int(a.dim));
+}
+
+hipError_t mo_launch_head_dh(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, bool first, int64_t rows,
+                             hipStream_t s) {
+    const Operand WT = rows_of(ws + p.off_wt, p.piece, a.dim, a.dim * p.piece);
+    const Operand D = rows_of(ws + p.off_d, p.piece, p.n_pad, p.n_pad * p.piece);
+    const int nk = int((rows + 255) / 256 * 8);   // the piece's rows, rounded up to whole tiles
+    const dim3 grid(head_grid(uint64_t(p.dh_tm) * p.dh_tn * p.dh_splits)), block(H_THREADS);
+    f32x4* acc = reinterpret_cast<f32x4*>(ws + p.off_acc);
+#define MO_CALL(NB, PL)                                                                                        \
+    return go(head_dh_kernel<NB, PL>, grid, block, s, WT, D, nk, p.dh_stages, p.dh_tm, p.dh_tn,                \
+              uint32_t(p.dh_splits), first ? 1 : 0, acc)
+    MO_HEAD_PICK(p.nb, p.planes, MO_CALL);
+#undef MO_CALL
+}
+
+hipError_t mo_launch_head_dh_out(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, hipStream_t s) {
+    const f32x4* acc = reinterpret_cast<const f32x4*>(ws + p.off_acc);
+    const float* coef = reinterpret_cast<const float*>(ws + p.off_coef);
+    const dim3 grid(p.dh_tm * p.dh_tn * 8), block(256);
+#define MO_OUT(T, NB)                                                                                    \
+    return go(head_dh_out_kernel<T, NB>, grid, block, s, acc, p.dh_tm, p.dh_tn, uint32_t(p.dh_splits), coef, \
+              static_cast<T*>(a.dH), a.lddh, a.tokens, int(a.dim))
+    if (p.planes == 1) {
+        if (p.nb == 4) MO_OUT(bf16_t, 4);
+        if (p.nb == 2) MO_OUT(bf16_t, 2);
+        MO_OUT(bf16_t, 1);
+    }
+    if (p.nb == 4) MO_OUT(float, 4);
+    if (p.nb == 2) MO_OUT(float, 2);
+    MO_OUT(float, 1);
+#undef MO_OUT
+}

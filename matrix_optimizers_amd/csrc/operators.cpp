@@ -1,0 +1,570 @@
+// Host side of the operators that write the gradients the owner steps read: the
+// embedding, the layer norm and the output head's losses.  Argument checks,
+// workspace plans and launches; the kernels are in embedding.hip, layer_norm.hip
+// and head_loss.hip.  Every plan follows from sizes and alignments alone, no host
+// memory is uploaded, and nothing is allocated, so each call can be captured.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <vector>
+
+#include "../../include/mo.h"
+#include "host_common.h"
+#include "mo_worklist.h"
+#include "operators.h"
+
+using namespace mo_host;
+
+namespace {
+
+#define MO_TRY(x)                          \
+    do {                                   \
+        const mo_status st_ = (x);         \
+        if (st_ != MO_OK) return st_;      \
+    } while (0)
+#define MO_RUN(phase, launch)                                                              \
+    do {                                                                                   \
+        if (timed_launch(phase, s, [&] { return launch; }) != hipSuccess) return MO_ERR_HIP; \
+    } while (0)
+
+// Row strides up to 2^26 elements: byte ranges stay far inside 63 bits.
+constexpr int64_t kMaxLd = int64_t(1) << 26;
+
+// The stride in elements (0 means the row length).
+mo_status stride_of(int64_t ld, int64_t cols, int64_t* out) {
+    *out = ld ? ld : cols;
+    if (*out < cols) return MO_ERR_INVALID_ARG;
+    return *out > kMaxLd ? MO_ERR_UNSUPPORTED : MO_OK;
+}
+
+bool dtype_ok(int32_t d) { return d == MO_F32 || d == MO_BF16; }
+
+Range vec_range(const void* p, int64_t n, int64_t es, int writable) { return matrix_range(p, 1, n, n, es, writable); }
+
+// The workspace as a range and its aligned base; false when it is too small.
+bool take_workspace(void* workspace, size_t have, uint64_t need, std::vector<Range>* ranges, uint8_t** base) {
+    if (need == 0) {
+        *base = nullptr;
+        return true;
+    }
+    if (!workspace || have < need + MO_WS_ALIGN) return false;
+    const uintptr_t w = reinterpret_cast<uintptr_t>(workspace);
+    ranges->push_back(Range{w, w + have, 1});
+    *base = reinterpret_cast<uint8_t*>(align_up(w, MO_WS_ALIGN));
+    return true;
+}
+
+// Consecutive 256-byte aligned regions.
+struct Carve {
+    uint64_t at = 0;
+    uint64_t operator()(uint64_t bytes) {
+        const uint64_t o = at;
+        at = align_up(at + bytes, MO_WS_ALIGN);
+        return o;
+    }
+};
+
+// ---- layer norm ------------------------------------------------------------------
+
+constexpr int64_t kMaxRowLen = int64_t(1) << 24, kMaxRows = int64_t(1) << 32;
+
+mo_status ln_shape(int64_t rows, int64_t cols, int32_t dtype) {
+    if (rows < 0 || cols < 0) return MO_ERR_INVALID_ARG;
+    if (!dtype_ok(dtype) || cols > kMaxRowLen || rows > kMaxRows) return MO_ERR_UNSUPPORTED;
+    return MO_OK;
+}
+
+uint64_t ln_bwd_bytes(int64_t rows, int64_t cols) { return uint64_t(mo_ln_bwd_parts(rows, cols)) * 2 * cols * 4; }
+
+// ---- embedding -------------------------------------------------------------------
+
+constexpr int64_t kMaxVocab = int64_t(1) << 27, kMaxTokens = int64_t(1) << 30, kMaxDim = int64_t(1) << 20;
+
+mo_status emb_shape(int64_t n, int64_t vocab, int64_t dim) {
+    if (n < 0 || vocab < 0 || dim < 0) return MO_ERR_INVALID_ARG;
+    if (n > kMaxTokens || vocab > kMaxVocab || dim > kMaxDim) return MO_ERR_UNSUPPORTED;
+    return MO_OK;
+}
+
+MoEmbPlan emb_plan(int64_t n, int64_t vocab, int64_t dim) {
+    MoEmbPlan p = {};
+    if (n == 0 || dim == 0 || vocab == 0) return p;
+    int bits = 1;
+    while ((int64_t(1) << bits) <= vocab) ++bits;     // keys 0 .. vocab (the padded positions)
+    p.passes = (bits + 8) / 9;
+    p.bits = (bits + p.passes - 1) / p.passes;
+    p.tiles = uint32_t((n + MO_EMB_SORT_TILE - 1) / MO_EMB_SORT_TILE);
+    p.C = int(std::max<int64_t>(4, (n + 2047) / 2048));
+    p.chunks = uint32_t((n + p.C - 1) / p.C);
+    Carve take;
+    for (int b = 0; b < 2; ++b) {
+        p.off_keys[b] = take(uint64_t(n) * 4);
+        p.off_idx[b] = take(uint64_t(n) * 4);
+    }
+    p.off_hist = take((uint64_t(p.tiles) << p.bits) * 4);
+    p.off_head = take(uint64_t(p.chunks) * dim * 4);
+    p.off_tail = take(uint64_t(p.chunks) * dim * 4);
+    p.bytes = take.at;
+    return p;
+}
+
+// ---- output head -----------------------------------------------------------------
+
+constexpr int64_t kHeadMaxTokens = int64_t(1) << 20, kHeadMaxVocab = int64_t(1) << 26,
+                  kHeadMaxDim = int64_t(1) << 16;
+constexpr int64_t kHeadPieceBytes = int64_t(768) << 20;
+
+mo_status head_shape(const mo_head* h, int64_t* ldh, int64_t* ldw) {
+    if (!h) return MO_ERR_INVALID_ARG;
+    if (h->tokens < 0 || h->vocab < 1 || h->dim < 1) return MO_ERR_INVALID_ARG;
+    if (!dtype_ok(h->dtype)) return MO_ERR_UNSUPPORTED;
+    if (h->tokens > kHeadMaxTokens || h->vocab > kHeadMaxVocab || h->dim > kHeadMaxDim) return MO_ERR_UNSUPPORTED;
+    MO_TRY(stride_of(h->ld_h, h->dim, ldh));
+    return stride_of(h->ld_w, h->dim, ldw);
+}
+
+// A K extent the GEMM's stages cover: 64, 128 or a multiple of 64 from 256 on.
+int64_t k_extent(int64_t k) { return k <= 64 ? 64 : k <= 128 ? 128 : std::max<int64_t>(256, (k + 63) / 64 * 64); }
+
+// Whether bf16 rows can be loaded in place: 16-byte aligned rows of whole
+// stages, less than 2^24 bytes apart (the GEMM's 32-bit row offsets).
+bool in_place(const void* p, int64_t ld, int64_t dim) {
+    return k_extent(dim) == dim && ((reinterpret_cast<uintptr_t>(p) | uintptr_t(ld * 2)) & 15) == 0 &&
+           ld * 2 < (int64_t(1) << 24);
+}
+
+// Tile width over the tokens: the least padded work, a narrow tile's column
+// costing more (its workgroup reads the same 256 rows of the other operand).
+int token_tile(int64_t n) {
+    if (n <= 64) return 1;
+    if (n <= 128) return 2;
+    const int64_t c4 = (n + 255) / 256 * 100, c2 = (n + 127) / 128 * 58;
+    return c2 < c4 ? 2 : 4;
+}
+
+MoHeadPlan head_plan(const MoHeadArgs& a, bool backward, bool need_dh, bool need_dw) {
+    MoHeadPlan p = {};
+    p.planes = a.dtype == MO_BF16 ? 1 : 3;
+    p.nb = token_tile(a.tokens);
+    p.n_pad = (a.tokens + 64 * p.nb - 1) / (64 * p.nb) * (64 * p.nb);
+    p.kd = k_extent(a.dim);
+    p.pack_h = p.planes != 1 || !in_place(a.H, a.ldh, a.dim);
+    p.pack_w = p.planes != 1 || !in_place(a.W, a.ldw, a.dim);
+    p.v_tiles = (a.vocab + 255) / 256;
+    const int64_t tn = p.n_pad / (64 * p.nb);
+    // pieces of equal size, bounded by the memory of their copies (and by the
+    // grid of one launch); at least one tile
+    int64_t row = p.pack_w ? 2 * p.planes * p.kd : 0;
+    // (the same pieces whichever gradients are asked for, so that the size query holds for each)
+    if (backward) row += 4 * p.planes * p.n_pad + 2 * p.planes * a.dim;
+    int64_t most = std::min<int64_t>((int64_t(1) << 22) / std::max<int64_t>(tn, (a.dim + 63) / 64), 1 << 13);
+    if (row) most = std::min(most, kHeadPieceBytes / row / 256);
+    most = std::max<int64_t>(most, 1);
+    const int64_t pieces = (p.v_tiles + most - 1) / most;
+    p.piece = (p.v_tiles + pieces - 1) / pieces * 256;
+    Carve take;
+    if (p.pack_h) p.off_hp = take(uint64_t(2) * p.planes * a.tokens * p.kd);
+    if (p.pack_w) p.off_wp = take(uint64_t(2) * p.planes * p.piece * p.kd);
+    if (!backward) {
+        p.off_part = take(uint64_t(8) * p.v_tiles * p.n_pad);
+    } else {
+        p.off_coef = take(uint64_t(4) * p.n_pad);
+        p.off_nl2 = take(uint64_t(4) * p.n_pad);
+        p.off_tval = take(uint64_t(4) * a.tokens * a.k);
+        p.off_d = take(uint64_t(2) * p.planes * p.n_pad * p.piece);
+        p.off_dt = take(uint64_t(2) * p.planes * p.n_pad * p.piece);
+        if (need_dw) {
+            p.nb_dw = a.dim <= 64 ? 1 : a.dim <= 128 ? 2 : 4;
+            p.off_ht = take(uint64_t(2) * p.planes * a.dim * p.n_pad);
+        }
+        if (need_dh) {
+            p.off_wt = take(uint64_t(2) * p.planes * a.dim * p.piece);
+            p.dh_tm = uint32_t((a.dim + 255) / 256);
+            p.dh_tn = uint32_t(tn);
+            // enough splits of K for two rounds of the 256 CUs, whole tiles of 8 stages
+            const int64_t tiles = int64_t(p.dh_tm) * p.dh_tn, groups = p.piece / 256;
+            const int64_t want = std::max<int64_t>(1, std::min<int64_t>(512 / tiles, groups));
+            p.dh_stages = int((groups + want - 1) / want * 8);
+            p.dh_splits = int((groups * 8 + p.dh_stages - 1) / p.dh_stages);
+            p.off_acc = take(uint64_t(4) * p.dh_splits * tiles * 256 * 64 * p.nb);
+        }
+    }
+    p.bytes = take.at;
+    return p;
+}
+
+struct Targets {
+    const int64_t* ids;
+    int64_t ld_ids;
+    int32_t k;
+    const void* teacher;
+    int64_t ld_teacher;
+    int32_t teacher_dtype;
+    float temperature;
+};
+
+mo_status head_args(const mo_head* h, const Targets* t, MoHeadArgs* a) {
+    int64_t ldh, ldw;
+    MO_TRY(head_shape(h, &ldh, &ldw));
+    *a = {};
+    a->H = h->H;
+    a->W = h->W;
+    a->tokens = h->tokens;
+    a->vocab = h->vocab;
+    a->dim = h->dim;
+    a->ldh = ldh;
+    a->ldw = ldw;
+    a->dtype = h->dtype;
+    a->k = t->k;
+    a->ids = t->ids;
+    a->ld_ids = t->ld_ids;
+    a->teacher = t->teacher;
+    a->ld_teacher = t->ld_teacher;
+    a->teacher_dtype = t->teacher_dtype;
+    a->t = t->temperature;
+    a->inv_t = 1.0f / t->temperature;
+    return MO_OK;
+}
+
+mo_status topk_targets(const mo_topk* t, Targets* out) {
+    if (!t || t->k < 1) return MO_ERR_INVALID_ARG;
+    const float T = t->temperature;
+    if (!(T > 0.f) || !finite(T * T) || !finite(1.0f / T)) return MO_ERR_INVALID_ARG;
+    if (t->k > MO_TOPK_MAX || !dtype_ok(t->dtype)) return MO_ERR_UNSUPPORTED;
+    *out = {t->ids, 0, t->k, t->logits, 0, t->dtype, T};
+    MO_TRY(stride_of(t->ld_ids, t->k, &out->ld_ids));
+    return stride_of(t->ld_logits, t->k, &out->ld_teacher);
+}
+
+// Ranges of what every head call reads.
+void head_inputs(const MoHeadArgs& a, std::vector<Range>* r) {
+    const int64_t es = elem_size(a.dtype);
+    r->push_back(matrix_range(a.H, a.tokens, a.dim, a.ldh, es, 0));
+    r->push_back(matrix_range(a.W, a.vocab, a.dim, a.ldw, es, 0));
+    r->push_back(matrix_range(a.ids, a.tokens, a.k, a.ld_ids, 8, 0));
+    if (a.teacher) r->push_back(matrix_range(a.teacher, a.tokens, a.k, a.ld_teacher, elem_size(a.teacher_dtype), 0));
+}
+
+mo_status head_forward(MoHeadArgs& a, void* workspace, size_t workspace_bytes, void* stream, bool distill) {
+    if (a.tokens == 0) return MO_OK;
+    if (!a.H || !a.W || !a.ids || !a.loss || !a.lse || (distill && (!a.teacher || !a.z))) return MO_ERR_INVALID_ARG;
+    MoHeadPlan p = head_plan(a, false, false, false);
+    Carve more{p.bytes};
+    const uint64_t off_z = distill ? 0 : more(uint64_t(4) * a.tokens);
+    p.bytes = more.at;
+    std::vector<Range> ranges;
+    head_inputs(a, &ranges);
+    ranges.push_back(vec_range(a.loss, a.tokens, 4, 1));
+    ranges.push_back(vec_range(a.lse, a.tokens, 4, 1));
+    if (distill) ranges.push_back(vec_range(a.z, a.tokens * a.k, 4, 1));
+    uint8_t* ws;
+    if (!take_workspace(workspace, workspace_bytes, p.bytes, &ranges, &ws)) return MO_ERR_WORKSPACE_TOO_SMALL;
+    if (ranges_conflict(ranges)) return MO_ERR_ALIAS;
+    if (!distill) a.z = reinterpret_cast<float*>(ws + off_z);
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    if (p.pack_h) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_pack(a, p, ws, true, 0, a.tokens, s));
+    MO_RUN(MO_PHASE_HD_TARGET, mo_launch_head_targets(a, s));
+    for (int64_t v0 = 0; v0 < a.vocab; v0 += p.piece) {
+        const int64_t rows = std::min(p.piece, a.vocab - v0);
+        if (p.pack_w) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_pack(a, p, ws, false, v0, rows, s));
+        MO_RUN(MO_PHASE_HD_LSE, mo_launch_head_lse(a, p, ws, v0, rows, s));
+    }
+    MO_RUN(MO_PHASE_HD_TARGET, mo_launch_head_loss(a, p, ws, s));
+    return MO_OK;
+}
+
+// Zeros in a rows x cols matrix.
+mo_status zero_rows(void* p, int64_t rows, int64_t cols, int64_t ld, int32_t dtype, int phase, hipStream_t s) {
+    MoEmbArgs e = {};
+    e.G = p;
+    e.vocab = rows;
+    e.dim = cols;
+    e.ldg = ld;
+    e.g_dtype = dtype;
+    MO_RUN(phase, mo_launch_emb_bwd(e, MoEmbPlan{}, nullptr, s));
+    return MO_OK;
+}
+
+mo_status head_backward(MoHeadArgs& a, void* workspace, size_t workspace_bytes, void* stream, bool distill) {
+    MO_TRY(stride_of(a.lddh, a.dim, &a.lddh));
+    MO_TRY(stride_of(a.lddw, a.dim, &a.lddw));
+    if (!a.dH && !a.dW) return MO_OK;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    if (a.tokens == 0) return a.dW ? zero_rows(a.dW, a.vocab, a.dim, a.lddw, a.dtype, MO_PHASE_HD_DW, s) : MO_OK;
+    if (!a.H || !a.W || !a.ids || !a.lse_in || !a.dloss) return MO_ERR_INVALID_ARG;
+    if (distill ? (!a.teacher || !a.z_in) : !a.loss_in) return MO_ERR_INVALID_ARG;
+    const MoHeadPlan p = head_plan(a, true, a.dH != nullptr, a.dW != nullptr);
+    std::vector<Range> ranges;
+    head_inputs(a, &ranges);
+    const int64_t es = elem_size(a.dtype);
+    ranges.push_back(vec_range(a.lse_in, a.tokens, 4, 0));
+    ranges.push_back(vec_range(a.dloss, a.tokens, 4, 0));
+    if (distill) ranges.push_back(vec_range(a.z_in, a.tokens * a.k, 4, 0));
+    else ranges.push_back(vec_range(a.loss_in, a.tokens, 4, 0));
+    if (a.dH) ranges.push_back(matrix_range(a.dH, a.tokens, a.dim, a.lddh, es, 1));
+    if (a.dW) ranges.push_back(matrix_range(a.dW, a.vocab, a.dim, a.lddw, es, 1));
+    uint8_t* ws;
+    if (!take_workspace(workspace, workspace_bytes, p.bytes, &ranges, &ws)) return MO_ERR_WORKSPACE_TOO_SMALL;
+    if (ranges_conflict(ranges)) return MO_ERR_ALIAS;
+    MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_prep(a, p, ws, s));
+    if (p.pack_h) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_pack(a, p, ws, true, 0, a.tokens, s));
+    if (a.dW) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_ht(a, p, ws, s));
+    for (int64_t v0 = 0; v0 < a.vocab; v0 += p.piece) {
+        const int64_t rows = std::min(p.piece, a.vocab - v0);
+        if (p.pack_w) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_pack(a, p, ws, false, v0, rows, s));
+        if (a.dH) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_wt(a, p, ws, v0, rows, s));
+        MO_RUN(MO_PHASE_HD_DELTA, mo_launch_head_delta(a, p, ws, v0, rows, s));
+        MO_RUN(MO_PHASE_HD_TARGET, mo_launch_head_patch(a, p, ws, v0, rows, s));
+        if (a.dW) MO_RUN(MO_PHASE_HD_DW, mo_launch_head_dw(a, p, ws, v0, rows, s));
+        if (a.dH) MO_RUN(MO_PHASE_HD_DH, mo_launch_head_dh(a, p, ws, v0 == 0, rows, s));
+    }
+    if (a.dH) MO_RUN(MO_PHASE_HD_DH, mo_launch_head_dh_out(a, p, ws, s));
+    return MO_OK;
+}
+
+mo_status head_bytes(const MoHeadArgs& a, int32_t backward, bool distill, size_t* bytes) {
+    if (!bytes) return MO_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (a.tokens == 0) return MO_OK;
+    Carve take{head_plan(a, backward != 0, true, true).bytes};
+    if (!backward && !distill) take(uint64_t(4) * a.tokens);
+    *bytes = size_t(take.at) + MO_WS_ALIGN;
+    return MO_OK;
+}
+
+Targets label_targets(const int64_t* labels) { return {labels, 1, 1, nullptr, 1, MO_F32, 1.0f}; }
+
+}  // namespace
+
+extern "C" {
+
+mo_status layer_norm_forward(const void* X, int64_t ld_x, const float* weight, const float* bias, void* Y,
+                             int64_t ld_y, float* mean, float* rstd, int64_t rows, int64_t cols, int32_t dtype,
+                             float eps, void* stream) {
+    MO_TRY(ln_shape(rows, cols, dtype));
+    if (!finite(eps) || eps < 0.f) return MO_ERR_INVALID_ARG;
+    MoLnArgs a = {};
+    MO_TRY(stride_of(ld_x, cols, &a.ldx));
+    MO_TRY(stride_of(ld_y, cols, &a.ldy));
+    if (rows == 0 || cols == 0) return MO_OK;
+    if (!X || !Y) return MO_ERR_INVALID_ARG;
+    a.X = X;
+    a.Y = Y;
+    a.weight = weight;
+    a.bias = bias;
+    a.mean_out = mean;
+    a.rstd_out = rstd;
+    a.rows = rows;
+    a.cols = cols;
+    a.dtype = dtype;
+    a.eps = eps;
+    const int64_t es = elem_size(dtype);
+    std::vector<Range> r = {matrix_range(X, rows, cols, a.ldx, es, 0), matrix_range(Y, rows, cols, a.ldy, es, 1)};
+    if (weight) r.push_back(vec_range(weight, cols, 4, 0));
+    if (bias) r.push_back(vec_range(bias, cols, 4, 0));
+    if (mean) r.push_back(vec_range(mean, rows, 4, 1));
+    if (rstd) r.push_back(vec_range(rstd, rows, 4, 1));
+    if (ranges_conflict(r)) return MO_ERR_ALIAS;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    MO_RUN(MO_PHASE_LN_FWD, mo_launch_ln_fwd(a, s));
+    return MO_OK;
+}
+
+mo_status layer_norm_workspace_bytes(int64_t rows, int64_t cols, size_t* bytes) {
+    if (!bytes) return MO_ERR_INVALID_ARG;
+    MO_TRY(ln_shape(rows, cols, MO_F32));
+    const uint64_t b = rows && cols ? ln_bwd_bytes(rows, cols) : 0;
+    *bytes = b ? size_t(align_up(b, MO_WS_ALIGN)) + MO_WS_ALIGN : 0;
+    return MO_OK;
+}
+
+mo_status layer_norm_backward(const void* dY, int64_t ld_dy, const void* X, int64_t ld_x, const float* weight,
+                              const float* mean, const float* rstd, void* dX, int64_t ld_dx, float* dweight,
+                              float* dbias, int64_t rows, int64_t cols, int32_t dtype, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+    MO_TRY(ln_shape(rows, cols, dtype));
+    MoLnArgs a = {};
+    MO_TRY(stride_of(ld_x, cols, &a.ldx));
+    MO_TRY(stride_of(ld_dy, cols, &a.lddy));
+    MO_TRY(stride_of(ld_dx, cols, &a.lddx));
+    if (cols == 0) return MO_OK;
+    if (!dX && !dweight && !dbias) return MO_OK;
+    a.X = X;
+    a.dY = dY;
+    a.weight = weight;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.dX = dX;
+    a.dweight = dweight;
+    a.dbias = dbias;
+    a.rows = rows;
+    a.cols = cols;
+    a.dtype = dtype;
+    const bool sums = dweight || dbias;
+    const int64_t es = elem_size(dtype);
+    std::vector<Range> r;
+    if (rows) {
+        if (!X || !dY || !mean || !rstd) return MO_ERR_INVALID_ARG;
+        r.push_back(matrix_range(X, rows, cols, a.ldx, es, 0));
+        r.push_back(matrix_range(dY, rows, cols, a.lddy, es, 0));
+        r.push_back(vec_range(mean, rows, 4, 0));
+        r.push_back(vec_range(rstd, rows, 4, 0));
+        if (dX) r.push_back(matrix_range(dX, rows, cols, a.lddx, es, 1));
+    }
+    if (weight) r.push_back(vec_range(weight, cols, 4, 0));
+    if (dweight) r.push_back(vec_range(dweight, cols, 4, 1));
+    if (dbias) r.push_back(vec_range(dbias, cols, 4, 1));
+    uint8_t* ws = nullptr;
+    if (!take_workspace(workspace, workspace_bytes, sums ? align_up(ln_bwd_bytes(rows, cols), MO_WS_ALIGN) : 0, &r, &ws))
+        return MO_ERR_WORKSPACE_TOO_SMALL;
+    if (ranges_conflict(r)) return MO_ERR_ALIAS;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    float* part = reinterpret_cast<float*>(ws);
+    if (rows) MO_RUN(MO_PHASE_LN_BWD, mo_launch_ln_bwd(a, part, s));
+    if (sums) MO_RUN(MO_PHASE_LN_BWD, mo_launch_ln_reduce(a, part, s));
+    return MO_OK;
+}
+
+mo_status embedding_forward(const int64_t* tokens, int64_t n, const void* W, int64_t ld_w, int64_t vocab,
+                            int64_t dim, int32_t dtype, float scale, void* Y, int64_t ld_y, void* stream) {
+    MO_TRY(emb_shape(n, vocab, dim));
+    if (!dtype_ok(dtype)) return MO_ERR_UNSUPPORTED;
+    if (!finite(scale)) return MO_ERR_INVALID_ARG;
+    MoEmbArgs a = {};
+    MO_TRY(stride_of(ld_w, dim, &a.ldw));
+    MO_TRY(stride_of(ld_y, dim, &a.ldy));
+    if (n == 0 || dim == 0) return MO_OK;
+    if (!tokens || !Y || (vocab && !W)) return MO_ERR_INVALID_ARG;
+    a.tokens = tokens;
+    a.W = W;
+    a.Y = Y;
+    a.n = n;
+    a.vocab = vocab;
+    a.dim = dim;
+    a.w_dtype = dtype;
+    a.scale = scale;
+    const int64_t es = elem_size(dtype);
+    std::vector<Range> r = {vec_range(tokens, n, 8, 0), matrix_range(Y, n, dim, a.ldy, es, 1)};
+    if (vocab) r.push_back(matrix_range(W, vocab, dim, a.ldw, es, 0));
+    if (ranges_conflict(r)) return MO_ERR_ALIAS;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    MO_RUN(MO_PHASE_EMB_FWD, mo_launch_emb_fwd(a, s));
+    return MO_OK;
+}
+
+mo_status embedding_workspace_bytes(int64_t n, int64_t vocab, int64_t dim, size_t* bytes) {
+    if (!bytes) return MO_ERR_INVALID_ARG;
+    MO_TRY(emb_shape(n, vocab, dim));
+    const uint64_t b = emb_plan(n, vocab, dim).bytes;
+    *bytes = b ? size_t(b) + MO_WS_ALIGN : 0;
+    return MO_OK;
+}
+
+mo_status embedding_backward(const int64_t* tokens, int64_t n, const void* dY, int64_t ld_dy, int32_t dy_dtype,
+                             void* G, int64_t ld_g, int32_t g_dtype, int64_t vocab, int64_t dim, float scale,
+                             int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream) {
+    MO_TRY(emb_shape(n, vocab, dim));
+    if (!dtype_ok(dy_dtype) || !dtype_ok(g_dtype)) return MO_ERR_UNSUPPORTED;
+    if (!finite(scale)) return MO_ERR_INVALID_ARG;
+    MoEmbArgs a = {};
+    MO_TRY(stride_of(ld_dy, dim, &a.lddy));
+    MO_TRY(stride_of(ld_g, dim, &a.ldg));
+    if (vocab == 0 || dim == 0 || (n == 0 && accumulate)) return MO_OK;
+    if (!G || (n && (!tokens || !dY))) return MO_ERR_INVALID_ARG;
+    a.tokens = tokens;
+    a.dY = dY;
+    a.G = G;
+    a.n = n;
+    a.vocab = vocab;
+    a.dim = dim;
+    a.dy_dtype = dy_dtype;
+    a.g_dtype = g_dtype;
+    a.accumulate = accumulate != 0;
+    a.scale = scale;
+    const MoEmbPlan p = emb_plan(n, vocab, dim);
+    std::vector<Range> r = {matrix_range(G, vocab, dim, a.ldg, elem_size(g_dtype), 1)};
+    if (n) {
+        r.push_back(vec_range(tokens, n, 8, 0));
+        r.push_back(matrix_range(dY, n, dim, a.lddy, elem_size(dy_dtype), 0));
+    }
+    uint8_t* ws;
+    if (!take_workspace(workspace, workspace_bytes, p.bytes, &r, &ws)) return MO_ERR_WORKSPACE_TOO_SMALL;
+    if (ranges_conflict(r)) return MO_ERR_ALIAS;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    if (n) MO_RUN(MO_PHASE_EMB_SORT, mo_launch_emb_sort(a, p, ws, s));
+    MO_RUN(MO_PHASE_EMB_BWD, mo_launch_emb_bwd(a, p, ws, s));
+    return MO_OK;
+}
+
+mo_status softmax_xent_workspace_bytes(const mo_head* head, int32_t backward, size_t* bytes) {
+    MoHeadArgs a;
+    const Targets t = label_targets(nullptr);
+    MO_TRY(head_args(head, &t, &a));
+    return head_bytes(a, backward, false, bytes);
+}
+
+mo_status softmax_xent_forward(const mo_head* head, const int64_t* labels, float* loss, float* lse, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+    MoHeadArgs a;
+    const Targets t = label_targets(labels);
+    MO_TRY(head_args(head, &t, &a));
+    a.loss = loss;
+    a.lse = lse;
+    return head_forward(a, workspace, workspace_bytes, stream, false);
+}
+
+mo_status softmax_xent_backward(const mo_head* head, const int64_t* labels, const float* loss, const float* lse,
+                                const float* dloss, void* dH, int64_t ld_dh, void* dW, int64_t ld_dw,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+    MoHeadArgs a;
+    const Targets t = label_targets(labels);
+    MO_TRY(head_args(head, &t, &a));
+    a.loss_in = loss;
+    a.lse_in = lse;
+    a.dloss = dloss;
+    a.dH = dH;
+    a.dW = dW;
+    a.lddh = ld_dh;
+    a.lddw = ld_dw;
+    return head_backward(a, workspace, workspace_bytes, stream, false);
+}
+
+mo_status topk_distill_workspace_bytes(const mo_head* head, const mo_topk* top, int32_t backward, size_t* bytes) {
+    MoHeadArgs a;
+    Targets t;
+    MO_TRY(topk_targets(top, &t));
+    MO_TRY(head_args(head, &t, &a));
+    return head_bytes(a, backward, true, bytes);
+}
+
+mo_status topk_distill_forward(const mo_head* head, const mo_topk* top, float* loss, float* lse, float* z,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+    MoHeadArgs a;
+    Targets t;
+    MO_TRY(topk_targets(top, &t));
+    MO_TRY(head_args(head, &t, &a));
+    a.loss = loss;
+    a.lse = lse;
+    a.z = z;
+    return head_forward(a, workspace, workspace_bytes, stream, true);
+}
+
+mo_status topk_distill_backward(const mo_head* head, const mo_topk* top, const float* lse, const float* z,
+                                const float* dloss, void* dH, int64_t ld_dh, void* dW, int64_t ld_dw,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+    MoHeadArgs a;
+    Targets t;
+    MO_TRY(topk_targets(top, &t));
+    MO_TRY(head_args(head, &t, &a));
+    a.lse_in = lse;
+    a.z_in = z;
+    a.dloss = dloss;
+    a.dH = dH;
+    a.dW = dW;
+    a.lddh = ld_dh;
+    a.lddw = ld_dw;
+    return head_backward(a, workspace, workspace_bytes, stream, true);
+}
+
+}  // extern "C"

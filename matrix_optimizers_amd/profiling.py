@@ -37,6 +37,9 @@ FAMILY_SOURCES = {
                 "csrc/mo_worklist.h", "csrc/gemm_core.h", "csrc/tile_dispatch.h"],
     "soap": ["csrc/soap_kernels.hip", "csrc/so_worklist.h", "csrc/soap.cpp", "csrc/device_common.h",
              "csrc/mo_worklist.h"],
+    "operators": ["csrc/embedding.hip", "csrc/layer_norm.hip", "csrc/head_loss.hip", "csrc/head_gemm.h",
+                  "csrc/op_common.h", "csrc/operators.h", "csrc/operators.cpp", "csrc/device_common.h",
+                  "csrc/gemm_core.h"],
 }
 
 

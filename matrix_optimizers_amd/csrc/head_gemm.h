@@ -10,7 +10,7 @@
 //   - fp32 operands come as three bf16 planes whose sum is the value exactly
 //     (split_f32 below).  The product then runs over six of the nine plane
 //     pairs as one long K loop into the same fp32 accumulators; the three left
-//     out are below 2^-23 of the term.  Six bf16 MFMAs cost 6/16 of the fp32
+//     out come to at most 2^-23 of a term.  Six bf16 MFMAs cost 6/16 of the fp32
 //     MFMAs they replace.
 #pragma once
 
@@ -22,18 +22,17 @@ using namespace mo_gemm;
 
 constexpr int H_THREADS = 512;
 
-// x = hi + mid + lo, each the leading eight significand bits of what is left
-// (truncated, so no part overflows); the differences are exact.  Infinities and
-// NaN keep mid and lo at zero.
+// x = hi + mid + lo exactly: each the nearest bf16 to what is left (24 bits of
+// significand = 3 x 8), so |mid| <= 2^-8 |x| and |lo| <= 2^-16 |x|.  A finite x that
+// would round to infinity is truncated; infinities and NaN keep mid and lo at 0.
 MO_DEV void split_f32(float x, bf16_t& hi, bf16_t& mid, bf16_t& lo) {
-    const float h = __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
-    float r = x - h;
-    if (!(__builtin_fabsf(x) < __builtin_inff())) r = 0.f;
-    const float m = __uint_as_float(__float_as_uint(r) & 0xFFFF0000u);
-    // a NaN whose payload sits in the low half would truncate to infinity
-    hi = (bf16_t)(x != x ? x : h);
-    mid = (bf16_t)m;
-    lo = (bf16_t)(r - m);
+    const bool finite = __builtin_fabsf(x) < __builtin_inff();
+    hi = (bf16_t)x;
+    if (finite && !(__builtin_fabsf((float)hi) < __builtin_inff()))
+        hi = (bf16_t)__uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
+    const float r = finite ? x - (float)hi : 0.f;
+    mid = (bf16_t)r;
+    lo = (bf16_t)(r - (float)mid);
 }
 
 // Wave layout of a 256 x TN tile (TN = 64 NB) on 8 wavefronts.

@@ -7,7 +7,9 @@
 // Every element is read once and written once: a row lives in the registers of
 // its threads between the reductions and the result.  Statistics and sums are
 // fp32; the variance is the mean of squared differences from the finished mean
-// (no cancellation for rows with a large mean or a single large entry).
+// (no cancellation for rows with a large mean or a single large entry).  The
+// means are quotients, not products with a rounded 1 / cols, so that a constant
+// row whose sum is exact has variance 0.
 #include "op_common.h"
 #include "operators.h"
 
@@ -66,7 +68,7 @@ __global__ __launch_bounds__(W > 64 ? LN_MAX_THREADS : 256) void ln_fwd_kernel(
 #pragma unroll
             for (int e = 0; e < 8; ++e) b[i].v[e] = 0.f;
     }
-    const float inv = 1.0f / float(cols);
+    const float n_cols = float(cols);
     for (int64_t base = int64_t(blockIdx.x) * teams; base < rows; base += int64_t(gridDim.x) * teams) {
         const int64_t row = base + sub;
         const bool live = row < rows;
@@ -80,7 +82,7 @@ __global__ __launch_bounds__(W > 64 ? LN_MAX_THREADS : 256) void ln_fwd_kernel(
             for (int e = 0; e < 8; ++e) s[0] += x[i].v[e];
         }
         team_sum<W>(s, red, turn);
-        const float mu = s[0] * inv;
+        const float mu = s[0] / n_cols;
         float q[1] = {0.f};
 #pragma unroll
         for (int i = 0; i < R; ++i) {
@@ -92,7 +94,7 @@ __global__ __launch_bounds__(W > 64 ? LN_MAX_THREADS : 256) void ln_fwd_kernel(
             }
         }
         team_sum<W>(q, red, turn);
-        const float r = 1.0f / sqrtf(q[0] * inv + eps);
+        const float r = 1.0f / sqrtf(q[0] / n_cols + eps);
         if (live) {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
@@ -117,7 +119,7 @@ __global__ __launch_bounds__(LN_MAX_THREADS) void ln_fwd_long_kernel(
     float* rstd, int64_t rows, int cols, float eps) {
     __shared__ float red[32];
     int turn = 0;
-    const float inv = 1.0f / float(cols);
+    const float n_cols = float(cols);
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
         const T* x = X + row * ldx;
         float s[1] = {0.f};
@@ -127,7 +129,7 @@ __global__ __launch_bounds__(LN_MAX_THREADS) void ln_fwd_long_kernel(
             for (int e = 0; e < 8; ++e) s[0] += v.v[e];
         }
         team_sum<LN_MAX_THREADS>(s, red, turn);
-        const float mu = s[0] * inv;
+        const float mu = s[0] / n_cols;
         float q[1] = {0.f};
         for (int c = threadIdx.x * 8; c < cols; c += LN_MAX_THREADS * 8) {
             const f32x8 v = widen(ld8n(x + c, cols - c));
@@ -136,7 +138,7 @@ __global__ __launch_bounds__(LN_MAX_THREADS) void ln_fwd_long_kernel(
                 if (c + e < cols) q[0] += (v.v[e] - mu) * (v.v[e] - mu);
         }
         team_sum<LN_MAX_THREADS>(q, red, turn);
-        const float r = 1.0f / sqrtf(q[0] * inv + eps);
+        const float r = 1.0f / sqrtf(q[0] / n_cols + eps);
         for (int c = threadIdx.x * 8; c < cols; c += LN_MAX_THREADS * 8) {
             f32x8 v = widen(ld8n(x + c, cols - c));
 #pragma unroll
@@ -173,7 +175,7 @@ __global__ __launch_bounds__(W > 64 ? LN_MAX_THREADS : 256) void ln_bwd_kernel(
         for (int e = 0; e < 8; ++e) { dw[i].v[e] = 0.f; db[i].v[e] = 0.f; w[i].v[e] = 1.f; }
         if (weight) w[i] = widen(ld8n(weight + c, cols - c));
     }
-    const float inv = 1.0f / float(cols);
+    const float n_cols = float(cols);
     for (int64_t base = int64_t(blockIdx.x) * teams; base < rows; base += int64_t(gridDim.x) * teams) {
         const int64_t row = base + sub;
         const bool live = row < rows;
@@ -200,7 +202,7 @@ __global__ __launch_bounds__(W > 64 ? LN_MAX_THREADS : 256) void ln_bwd_kernel(
         }
         if (dX) {
             team_sum<W>(s, red, turn);
-            const float m1 = s[0] * inv, m2 = s[1] * inv;
+            const float m1 = s[0] / n_cols, m2 = s[1] / n_cols;
             if (live) {
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
@@ -249,7 +251,7 @@ __global__ __launch_bounds__(LN_MAX_THREADS) void ln_bwd_long_kernel(
     const float* rstd, T* dX, int64_t lddx, int64_t rows, int cols) {
     __shared__ float red[64];
     int turn = 0;
-    const float inv = 1.0f / float(cols);
+    const float n_cols = float(cols);
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
         const float mu = mean[row], r = rstd[row];
         const T *x = X + row * ldx, *dy = dY + row * lddy;
@@ -265,7 +267,7 @@ __global__ __launch_bounds__(LN_MAX_THREADS) void ln_bwd_long_kernel(
                 }
         }
         team_sum<LN_MAX_THREADS>(s, red, turn);
-        const float m1 = s[0] * inv, m2 = s[1] * inv;
+        const float m1 = s[0] / n_cols, m2 = s[1] / n_cols;
         for (int c = threadIdx.x * 8; c < cols; c += LN_MAX_THREADS * 8) {
             const f32x8 xv = widen(ld8n(x + c, cols - c)), gv = widen(ld8n(dy + c, cols - c));
             f32x8 o;

@@ -210,8 +210,8 @@ const char* mo_status_string(mo_status status);
 #define MO_PHASE_SO_PRODUCTS 20 /* SOAP: the six eigenbasis products, V', N and W written */
 #define MO_PHASE_SO_WARM    21  /* SOAP: a warm start's four products per eigendecomposition */
 #define MO_PHASE_EMB_FWD    22  /* embedding: lookup */
-#define MO_PHASE_EMB_SORT   23  /* embedding gradient: positions sorted by token */
-#define MO_PHASE_EMB_BWD    24  /* embedding gradient: sums of the runs, zeros elsewhere */
+#define MO_PHASE_EMB_SORT   23  /* embedding gradient: positions sorted by token, zeros in G */
+#define MO_PHASE_EMB_BWD    24  /* embedding gradient: sums of the runs of equal tokens */
 #define MO_PHASE_LN_FWD     25  /* layer norm: forward */
 #define MO_PHASE_LN_BWD     26  /* layer norm: dx, partial and final weight gradients */
 #define MO_PHASE_HD_PREP    27  /* output head: coefficients, operand copies and transposes */

@@ -1,7 +1,5 @@
-// The output head's tiled NT GEMM on bf16 MFMA, C[i][j] = sum_k P[i][k] Q[j][k]:
-// the K pipeline of gemm_core8.h (512 threads, two wavefronts per SIMD, a ring
-// of five LDS stages filled by direct-to-LDS loads) for operands that are the
-// caller's own tensors:
+// The output head's tiled NT GEMM on bf16 MFMA, C[i][j] = sum_k P[i][k] Q[j][k],
+// for operands that are the caller's own tensors:
 //   - P and Q have their own row strides, and rows past the end are read as the
 //     last row (the epilogue drops their results), so a ragged matrix needs no
 //     padded copy;
@@ -12,6 +10,21 @@
 //     pairs as one long K loop into the same fp32 accumulators; the three left
 //     out come to at most 2^-23 of a term.  Six bf16 MFMAs cost 6/16 of the fp32
 //     MFMAs they replace.
+//
+// Design, with the rate of a 16384 x 8192 x 4096 and a 16384 x 4096 x 8192 product
+// (bf16 results written, normal random data) at each step; a library product
+// of the same shapes runs at 1550 and 1590 TFLOP/s on the same card:
+//   1370, 1390  the loop of gemm_core8.h: 32 x 32 x 16 MFMAs, stages of 64 bytes in a
+//               ring of five, a barrier per stage
+//   1430, 1460  16 x 16 x 32 MFMAs: half the accumulator traffic per flop
+//   1420, 1450  stages of 128 bytes (whole lines) in two slots, one barrier per
+//               64 of K instead of two
+//   1440, 1460  loads through buffer descriptors: a scalar offset advances along K, no
+//               address arithmetic on the vector unit
+//   1453, 1490  five eighths of a stage's loads right behind the barrier
+// Tried and not kept: the two wavefronts of a SIMD taking turns at MFMAs and
+// loads with a barrier between (1220, 1235); four wavefronts of 128 x 128 each (1430,
+// 1475); fragment reads sent out faster than one per two MFMAs (1300 to 1430).
 #pragma once
 
 #include "gemm_core.h"
@@ -21,6 +34,9 @@ namespace mo_head_gemm {
 using namespace mo_gemm;
 
 constexpr int H_THREADS = 512;
+constexpr int HKB = 128;                              // bytes of K per stage and row: one line
+constexpr int HP_BYTES = 256 * HKB;                   // 32 KB of P per stage
+constexpr int head_lds(int NB) { return 2 * (HP_BYTES + 64 * NB * HKB); }
 
 // x = hi + mid + lo exactly: each the nearest bf16 to what is left (24 bits of
 // significand = 3 x 8), so |mid| <= 2^-8 |x| and |lo| <= 2^-16 |x|.  A finite x that
@@ -35,13 +51,14 @@ MO_DEV void split_f32(float x, bf16_t& hi, bf16_t& mid, bf16_t& lo) {
     lo = (bf16_t)(r - (float)mid);
 }
 
-// Wave layout of a 256 x TN tile (TN = 64 NB) on 8 wavefronts.
+// Wave layout of a 256 x TN tile (TN = 64 NB) on 8 wavefronts: WM x WN of them,
+// each MB x NBW blocks of 16 x 16.
 template <int NB> struct Layout;
-template <> struct Layout<4> { static constexpr int WM = 2, WN = 4, MB = 4, NBW = 2; };
-template <> struct Layout<2> { static constexpr int WM = 4, WN = 2, MB = 2, NBW = 2; };
-template <> struct Layout<1> { static constexpr int WM = 8, WN = 1, MB = 1, NBW = 2; };
+template <> struct Layout<4> { static constexpr int WM = 2, WN = 4, MB = 8, NBW = 4; };
+template <> struct Layout<2> { static constexpr int WM = 4, WN = 2, MB = 4, NBW = 4; };
+template <> struct Layout<1> { static constexpr int WM = 8, WN = 1, MB = 2, NBW = 4; };
 
-// One operand: bf16 rows at `base`, `ld` bytes apart (256 ld < 2^32), `rows` of
+// One operand: bf16 rows at `base`, `ld` bytes apart (256 ld < 2^31), `rows` of
 // them readable; plane p of an fp32 operand starts p * plane bytes further.
 struct Operand {
     const uint8_t* base;
@@ -53,185 +70,173 @@ struct Operand {
 template <int PL> MO_DEV int seg_p(int s) { return PL == 1 ? 0 : s == 0 ? 2 : (s == 2 || s == 3) ? 1 : 0; }
 template <int PL> MO_DEV int seg_q(int s) { return PL == 1 ? 0 : s == 1 ? 2 : (s == 2 || s == 4) ? 1 : 0; }
 
-constexpr int head_lds(int NB) { return NSTAGE * (OPND_BYTES + 64 * NB * KB); }
+// 128-byte rows of eight 16-byte chunks; chunk c of row r sits at c ^ (r / 2 mod 8).
+// A fragment read takes 16 rows at four consecutive chunks; any 16 lanes that
+// the LDS serves together (consecutive ones, or four groups of four from two
+// chunks) then fall on 16 distinct 16-byte bank groups.
+MO_DEV int hswz(int row) { return (row >> 1) & 7; }
 
 // Accumulates rows p0 .. p0 + 255 of P and q0 .. q0 + TN - 1 of Q over `nk1` K
-// stages of 64 bytes from stage k0 on (nk1 even; 2, 4 or at least 8 with PL = 1,
-// any even count with PL = 3).  Acc is f32x16[MB][NBW]; acc[a][b] of wave (wm, wn) holds rows
-// wm MB 32 + 32 a and columns wn NBW 32 + 32 b in the MFMA layout of gemm_core.h.
-// Ends with a workgroup barrier: the LDS is the epilogue's.
+// stages of 128 bytes (64 elements) from stage k0 on.  Acc is f32x4[MB][NBW];
+// acc[a][b] of wave (wm, wn) holds, in lane l, rows wm 16 MB + 16 a + 4 (l / 16) ..
+// + 3 and column wn 16 NBW + 16 b + l % 16.  Ends with a workgroup barrier: the
+// LDS is the epilogue's.
+//
+// Stage s sits in slot s mod 2.  A stage is four quarters of MFMAs (first and
+// second half of the row blocks, for each half of K).  While one runs, the
+// next one's fragments are read, so all reads of a stage are done when its
+// third quarter ends: there each wave waits for its reads and its loads of
+// stage s + 1, and the barrier publishes s + 1 and frees the slot of s.  The loads of
+// stage s + 2 into that slot go out during the fourth quarter (LH of them) and
+// the first quarter of stage s + 1, and have the two quarters after that to land.
 template <int NB, int PL, class Acc>
 __device__ __forceinline__ void head_tile(uint8_t* smem, const Operand& P, const Operand& Q, int64_t p0,
                                           int64_t q0, int k0, int nk1, Acc& acc) {
 #ifdef __HIP_DEVICE_COMPILE__   // the host pass cannot check the device builtins
     using L = Layout<NB>;
-    constexpr int WN = L::WN, MB = L::MB, NBW = L::NBW;
-    constexpr int TN = 64 * NB;
-    constexpr int SBYTES = OPND_BYTES + TN * KB;
-    constexpr int QI = NB == 4 ? 2 : 1;          // Q load instructions per stage and wave
-    constexpr int LS = 2 + QI;
-    constexpr int LP = 2 * LS;                   // loads per pair of stages
-    constexpr int MF = MB * NBW;
-    constexpr int NR = MB + NBW;
+    constexpr int WN = L::WN, MB = L::MB, NBW = L::NBW, HA = MB / 2, MF = HA * NBW;
+    constexpr int TN = 64 * NB, SBYTES = HP_BYTES + TN * HKB;
+    constexpr int LS = 4 + NB;                   // load instructions per stage and wave
     constexpr int NSEG = PL == 1 ? 1 : 6;
     static_assert(PL == 1 || PL == 3, "planes");
-    const int nk = nk1 * NSEG;
+    const int n = nk1 * NSEG;
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
-    const int r32 = lane & 31, kg = lane >> 5;
+    const int r16 = lane & 15, kg = lane >> 4;
 
-    // Wave w fills P rows [32 w, 32 w + 32) and Q rows [16 QI w, ..), 16 rows
-    // (1 KB) per instruction; lane l -> row + l / 4, physical chunk l % 4.  With
-    // 64 Q rows four waves would do: waves 4 .. 7 repeat the loads of 0 .. 3 (same
-    // bytes to the same place), so every wave counts the same loads.
-    const int lrow = lane >> 2, pch = lane & 3;
-    const uint32_t lch = uint32_t((pch ^ ((lrow >> 2) & 3)) << 4);
-    const int qw = NB == 1 ? (wave & 3) : wave;
-    const uint8_t* Pb = P.base + p0 * P.ld + int64_t(k0) * KB;
-    const uint8_t* Qb = Q.base + q0 * Q.ld + int64_t(k0) * KB;
+    // Loads, straight to LDS: 8 rows of 128 bytes (1 KB) per instruction; wave w fills P rows
+    // [32 w, 32 w + 32) and Q rows [8 NB w, ..); lane l -> row + l / 8, physical
+    // chunk l % 8, which holds chunk (l % 8) ^ swizzle of the row.
+    const uint8_t* Pb = P.base + p0 * P.ld + int64_t(k0) * HKB;
+    const uint8_t* Qb = Q.base + q0 * Q.ld + int64_t(k0) * HKB;
     const int plim = int(P.rows - p0 < 256 ? P.rows - p0 : 256) - 1;
     const int qlim = int(Q.rows - q0 < TN ? Q.rows - q0 : TN) - 1;
     uint32_t vo[LS];
 #pragma unroll
     for (int i = 0; i < LS; ++i) {
-        const int r = (i < 2 ? wave * 32 + i * 16 : qw * 16 * QI + (i - 2) * 16) + lrow;
-        const int lim = i < 2 ? plim : qlim;
-        vo[i] = uint32_t(r < lim ? r : lim) * uint32_t(i < 2 ? P.ld : Q.ld) + lch;
+        const int r = (i < 4 ? wave * 32 + i * 8 : wave * 8 * NB + (i - 4) * 8) + (lane >> 3);
+        const int lim = i < 4 ? plim : qlim;
+        vo[i] = uint32_t(r < lim ? r : lim) * uint32_t(i < 4 ? P.ld : Q.ld) + uint32_t(((lane & 7) ^ hswz(r)) << 4);
     }
-    // cursor of the pair of stages being loaded
-    const uint8_t *cP = Pb + (PL == 1 ? 0 : seg_p<PL>(0) * P.plane);
-    const uint8_t *cQ = Qb + (PL == 1 ? 0 : seg_q<PL>(0) * Q.plane);
-    int ck = 0, cseg = 0;
-    auto next_pair = [&]() __attribute__((always_inline)) {
-        cP += 2 * KB;
-        cQ += 2 * KB;
+    // cursor of the stage being loaded; slot of stage s: s mod 2
+    auto rsrc = [&](const uint8_t* p) __attribute__((always_inline)) {
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, -1, 0x00027000);
+    };
+    auto rP = rsrc(Pb + (PL == 1 ? 0 : seg_p<PL>(0) * P.plane)), rQ = rsrc(Qb + (PL == 1 ? 0 : seg_q<PL>(0) * Q.plane));
+    int ck = 0, cseg = 0, koff = 0;
+    auto next_stage = [&]() __attribute__((always_inline)) {
+        koff += HKB;
         if constexpr (PL != 1) {
-            ck += 2;
-            if (ck == nk1) {
+            if (++ck == nk1) {
                 ck = 0;
                 ++cseg;
-                cP = Pb + seg_p<PL>(cseg) * P.plane;
-                cQ = Qb + seg_q<PL>(cseg) * Q.plane;
+                koff = 0;
+                rP = rsrc(Pb + seg_p<PL>(cseg) * P.plane);
+                rQ = rsrc(Qb + seg_q<PL>(cseg) * Q.plane);
             }
         }
     };
-    // instruction i of stage ks, the (ks & 1)-th of the cursor's pair
-    auto issue1 = [&](int ks, int i) __attribute__((always_inline)) {
-        uint8_t* sp = smem + (ks % NSTAGE) * SBYTES;
-        if (i < 2) sp += (wave * 32 + i * 16) * KB;
-        else sp += OPND_BYTES + (qw * 16 * QI + (i - 2) * 16) * KB;
-        const uint8_t* g = (i < 2 ? cP : cQ) + (ks & 1) * KB;
-        __builtin_amdgcn_global_load_lds(g + vo[i], (lds_void_t*)sp, 16, 0, 0);
+    auto issue1 = [&](int slot, int i) __attribute__((always_inline)) {
+        uint8_t* sp = smem + slot * SBYTES + (i < 4 ? (wave * 32 + i * 8) * HKB : HP_BYTES + (wave * 8 * NB + (i - 4) * 8) * HKB);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(i < 4 ? rP : rQ, (lds_void_t*)sp, 16, vo[i], koff, 0, 0);
     };
 
 #pragma unroll
     for (int a = 0; a < MB; ++a)
 #pragma unroll
-        for (int b = 0; b < NBW; ++b)
-#pragma unroll
-            for (int v = 0; v < 16; ++v) acc[a][b][v] = 0.f;
+        for (int b = 0; b < NBW; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    auto rd1 = [&](int ks, int sub, int i, u32x4 (&fa)[MB], u32x4 (&fb)[NBW]) __attribute__((always_inline)) {
-        const uint8_t* sp = smem + (ks % NSTAGE) * SBYTES;
-        const int chunk = 2 * sub + kg;
-        if (i < MB) fa[i] = *reinterpret_cast<const u32x4*>(sp + swz(wm * (MB * 32) + i * 32 + r32, chunk));
-        else fb[i - MB] = *reinterpret_cast<const u32x4*>(sp + OPND_BYTES + swz(wn * (NBW * 32) + (i - MB) * 32 + r32, chunk));
+    // fragments: 16 rows x 32 K, lane -> row lane % 16, K chunk 4 sub + lane / 16
+    const int x0 = ((kg ^ hswz(r16)) << 4), x1 = x0 ^ 64;
+    const int pbase = (wm * (MB * 16) + r16) * HKB, qbase = HP_BYTES + (wn * (NBW * 16) + r16) * HKB;
+    auto rdp = [&](int slot, int sub, int i) __attribute__((always_inline)) {
+        return *reinterpret_cast<const u32x4*>(smem + slot * SBYTES + pbase + (sub ? x1 : x0) + i * 16 * HKB);
     };
-    auto wait_loads = [&](int after) {
-        if (after == 9) asm volatile("s_waitcnt vmcnt(9)" ::: "memory");
-        else if (after == 8) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
-        else if (after == 7) asm volatile("s_waitcnt vmcnt(7)" ::: "memory");
-        else if (after == 6) asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
-        else if (after == 5) asm volatile("s_waitcnt vmcnt(5)" ::: "memory");
-        else if (after == 4) asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
-        else if (after == 1) asm volatile("s_waitcnt vmcnt(1)" ::: "memory");
-        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    auto rdq = [&](int slot, int sub, int i) __attribute__((always_inline)) {
+        return *reinterpret_cast<const u32x4*>(smem + slot * SBYTES + qbase + (sub ? x1 : x0) + i * 16 * HKB);
     };
-    auto barrier = [&]() {
-        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-    };
-    // MF MFMAs on (fa, fb), the reads of the next substep and quarter q of the
-    // loads of the pair (ia, ia + 1) spread between them (gemm_core8's substep).
-    auto substep = [&](const u32x4 (&fa)[MB], const u32x4 (&fb)[NBW], bool do_read, int rks, int rsub,
-                       u32x4 (&na)[MB], u32x4 (&nb)[NBW], int ia, int q) __attribute__((always_inline)) {
-        const int l0 = q * LP / 4, nl = (q + 1) * LP / 4 - l0;
+    u32x4 a0[HA], a1[HA], b0[NBW], b1[NBW];
+    // Quarter h of a stage: MF MFMAs (row blocks (h & 1) HA .., K half h / 2) with the
+    // next quarter's reads and the loads l0 .. l1 - 1 of another stage between them.
+    auto quarter = [&](int h, int slot, bool reads, int lslot, int l0, int l1) __attribute__((always_inline)) {
+        const int nr = !reads ? 0 : (h & 1) ? HA + NBW : HA;
 #pragma unroll
         for (int i = 0; i < MF; ++i) {
-            Mfma<bf16_t>::run(fa[i / NBW], fb[i % NBW], acc[i / NBW][i % NBW]);
+            const int a = i / NBW, b = i % NBW;
+            const u32x4 fa = (h & 1) ? a1[a] : a0[a], fb = h < 2 ? b0[b] : b1[b];
+            f32x4& c = acc[(h & 1) * HA + a][b];
+            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fa), __builtin_bit_cast(bf16x8, fb), c, 0, 0, 0);
             __builtin_amdgcn_sched_barrier(0);
-            if (do_read) {
-                if (i < NR) rd1(rks, rsub, i, na, nb);
-                if (i == MF - 1)
 #pragma unroll
-                    for (int r = MF; r < NR; ++r) rd1(rks, rsub, r, na, nb);
-            }
-            if (ia >= 0)
-#pragma unroll
-                for (int j = 0; j < nl; ++j)
-                    if ((j + 1) * MF / nl - 1 == i) {
-                        const int l = l0 + j;
-                        issue1(ia + (l & 1), l >> 1);
+            for (int r = 0; r < HA + NBW; ++r)
+                if (r < nr && (2 * r == i || (i == MF - 1 && 2 * r > i))) {
+                    // after 0: a1 (sub 0); 1: b1, a0 (sub 1); 2: a1 (sub 1); 3: b0, a0 of the next stage
+                    if (!(h & 1)) a1[r] = rdp(slot, h / 2, HA + r);
+                    else {
+                        const int sl = h == 1 ? slot : slot ^ 1, sub = h == 1;
+                        if (r < NBW) (h == 1 ? b1 : b0)[r] = rdq(sl, sub, r);
+                        else a0[r - NBW] = rdp(sl, sub, r - NBW);
                     }
+                }
+#pragma unroll
+            for (int l = 0; l < LS; ++l)
+                if (l >= l0 && l < l1) {
+                    const int at = (l - l0) * MF / (l1 - l0) + 1;
+                    if ((at < MF ? at : MF - 1) == i) issue1(lslot, l);
+                }
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-
-    u32x4 f0a[MB], f0b[NBW], f1a[MB], f1b[NBW];
-    if (nk >= 8) {
-        // the schedule of gemm_core8: stage s in ring slot s % 5, pairs of
-        // stages loaded four stages ahead in quarters over four substeps
-        constexpr int W_EVEN = LP, W_ODD = 1 + LP / 2, W_FIRST = 1 + LP;
-#pragma unroll
-        for (int p = 0; p < 4; p += 2) {
-#pragma unroll
-            for (int l = 0; l < LP; ++l) issue1(p + (l & 1), l >> 1);
-            next_pair();
-        }
-        wait_loads(W_FIRST);
-        barrier();
-#pragma unroll
-        for (int i = 0; i < NR; ++i) rd1(0, 0, i, f0a, f0b);
-        __builtin_amdgcn_sched_barrier(0);
-        auto step = [&](int ks, int after, int pa, int qa, int pb, int qb) __attribute__((always_inline)) {
-            substep(f0a, f0b, true, ks, 1, f1a, f1b, pa, qa);
-            if (pa >= 0 && qa == 3) next_pair();
-            wait_loads(after);
-            barrier();     // stage ks + 1 visible everywhere; every read of stage ks done
+    constexpr int LH = (LS * 5 + 7) / 8;
+    // The stage in `slot`: in quarter 0 (ld0) the rest of the next stage's loads, in
+    // quarter 3 (ld3) the first loads of the one after it.
+    auto stage = [&](int slot, bool ld0, bool next, bool ld3) __attribute__((always_inline)) {
+        quarter(0, slot, true, slot ^ 1, ld0 ? LH : 0, ld0 ? LS : 0);
+        if (ld0) next_stage();
+        quarter(1, slot, true, 0, 0, 0);
+        quarter(2, slot, true, 0, 0, 0);
+        if (next) {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
             __builtin_amdgcn_sched_barrier(0);
-            substep(f1a, f1b, true, ks + 1, 0, f0a, f0b, pb, qb);
-        };
-        step(0, W_EVEN, -1, 0, 4, 0);
-        step(1, W_ODD, 4, 1, 4, 2);
-        int ks = 2;
-        for (; ks + 6 <= nk; ks += 2) {
-            step(ks, W_EVEN, ks + 2, 3, ks + 4, 0);
-            step(ks + 1, W_ODD, ks + 4, 1, ks + 4, 2);
         }
-        step(ks, W_EVEN, ks + 2, 3, -1, 0);
-        step(ks + 1, 1, -1, 0, -1, 0);
-        step(ks + 2, 0, -1, 0, -1, 0);
-        substep(f0a, f0b, true, nk - 1, 1, f1a, f1b, -1, 0);
-        substep(f1a, f1b, false, 0, 0, f0a, f0b, -1, 0);
-    } else {
-        // two or four stages: all of them at once
-        for (int p = 0; p < nk; p += 2) {
+        quarter(3, slot, next, slot, 0, ld3 ? LH : 0);
+    };
+
 #pragma unroll
-            for (int l = 0; l < LP; ++l) issue1(p + (l & 1), l >> 1);
-            next_pair();
-        }
-        wait_loads(0);
-        barrier();
-        for (int ks = 0; ks < nk; ++ks) {
+    for (int l = 0; l < LS; ++l) issue1(0, l);
+    next_stage();
+    if (n > 1) {
 #pragma unroll
-            for (int i = 0; i < NR; ++i) rd1(ks, 0, i, f0a, f0b);
-            substep(f0a, f0b, true, ks, 1, f1a, f1b, -1, 0);
-            substep(f1a, f1b, false, 0, 0, f0a, f0b, -1, 0);
-        }
+        for (int l = 0; l < LS; ++l) issue1(1, l);
+        next_stage();
     }
+    if (n == 1) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    else if constexpr (LS == 8) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+    else if constexpr (LS == 6) asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
+    else asm volatile("s_waitcnt vmcnt(5)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < NBW; ++i) b0[i] = rdq(0, 0, i);
+#pragma unroll
+    for (int i = 0; i < HA; ++i) a0[i] = rdp(0, 0, i);
+    __builtin_amdgcn_sched_barrier(0);
+    int s = 0;
+    if (n > 2) {
+        stage(0, false, true, true);
+        for (s = 1; s < n - 2; ++s) stage(s & 1, true, true, true);
+        stage(s & 1, true, true, false);
+        ++s;
+    } else if (n == 2) {
+        stage(0, false, true, false);
+        s = 1;
+    }
+    stage(s & 1, false, false, false);
     __syncthreads();
 #endif
 }

@@ -96,21 +96,21 @@ __global__ __launch_bounds__(256) void head_transpose_kernel(const T* src, int64
 // ---- forward ----------------------------------------------------------------------
 
 // Tile (ti, tj): vocabulary rows 256 ti .. of the piece, tokens TN tj ...  Each
-// lane holds 16 MB vocabulary values of one token per column block, so the
+// lane holds 4 MB vocabulary values of one token per column block, so the
 // maximum and the sum are mostly in registers.
 template <int NB, int PL>
-__global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2, 2))) void head_lse_kernel(
+__global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) void head_lse_kernel(
     Operand W, Operand H, int nk, uint32_t tm, uint32_t tn, float zscale, float2* part, int64_t n_pad) {
     using L = Layout<NB>;
     __shared__ __align__(16) uint8_t smem[head_lds(NB)];
     uint32_t ti, tj;
     if (!head_tile_of(blockIdx.x, tm, tn, ti, tj)) return;
     const int64_t v0 = int64_t(ti) * 256, n0 = int64_t(tj) * 64 * NB;
-    f32x16 acc[L::MB][L::NBW];
+    f32x4 acc[L::MB][L::NBW];
     head_tile<NB, PL>(smem, W, H, v0, n0, 0, nk, acc);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int wm = wave / L::WN, wn = wave % L::WN, r32 = lane & 31, kg = lane >> 5;
-    const int left = int(W.rows - v0 < 256 ? W.rows - v0 : 256) - wm * (L::MB * 32) - kg * 4;
+    const int wm = wave / L::WN, wn = wave % L::WN, r16 = lane & 15, kg = lane >> 4;
+    const int left = int(W.rows - v0 < 256 ? W.rows - v0 : 256) - wm * (L::MB * 16) - kg * 4;
     float2* st = reinterpret_cast<float2*>(smem);   // [WM][TN]
     const float k2 = zscale * LOG2E;
 #pragma unroll
@@ -119,20 +119,21 @@ __global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)
 #pragma unroll
         for (int a = 0; a < L::MB; ++a)
 #pragma unroll
-            for (int v = 0; v < 16; ++v) {
-                const int row = a * 32 + (v >> 2) * 8 + (v & 3);
-                const float z = row < left ? acc[a][b][v] * k2 : -__builtin_inff();
+            for (int v = 0; v < 4; ++v) {
+                const float z = a * 16 + v < left ? acc[a][b][v] * k2 : -__builtin_inff();
                 acc[a][b][v] = z;
                 m = fmaxf(m, z);
             }
+        m = fmaxf(m, __shfl_xor(m, 16, 64));
         m = fmaxf(m, __shfl_xor(m, 32, 64));
         const float mm = m == -__builtin_inff() ? 0.f : m;   // nothing but -inf: the sum is 0
 #pragma unroll
         for (int a = 0; a < L::MB; ++a)
 #pragma unroll
-            for (int v = 0; v < 16; ++v) s += exp2_hw(acc[a][b][v] - mm);
+            for (int v = 0; v < 4; ++v) s += exp2_hw(acc[a][b][v] - mm);
+        s += __shfl_xor(s, 16, 64);
         s += __shfl_xor(s, 32, 64);
-        if (kg == 0) st[wm * 64 * NB + wn * 64 + b * 32 + r32] = float2{m, s};
+        if (kg == 0) st[wm * 64 * NB + wn * 64 + b * 16 + r16] = float2{m, s};
     }
     __syncthreads();
     for (int t = threadIdx.x; t < 64 * NB; t += H_THREADS) {
@@ -316,7 +317,7 @@ __global__ __launch_bounds__(256) void head_distill_prep_kernel(const int64_t* i
 
 // D[plane][token][piece] and DT[plane][vocabulary row][n_pad].
 template <int NB, int PL>
-__global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2, 2))) void head_delta_kernel(
+__global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) void head_delta_kernel(
     Operand W, Operand H, int nk, uint32_t tm, uint32_t tn, float zscale, const float* coef, const float* nl2,
     bf16_t* D, int64_t ldd, int64_t plane_d, bf16_t* DT, int64_t ldt, int64_t plane_t) {
     using L = Layout<NB>;
@@ -324,36 +325,37 @@ __global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)
     uint32_t ti, tj;
     if (!head_tile_of(blockIdx.x, tm, tn, ti, tj)) return;
     const int64_t v0 = int64_t(ti) * 256, n0 = int64_t(tj) * 64 * NB;
-    f32x16 acc[L::MB][L::NBW];
+    f32x4 acc[L::MB][L::NBW];
     head_tile<NB, PL>(smem, W, H, v0, n0, 0, nk, acc);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int wm = wave / L::WN, wn = wave % L::WN, r32 = lane & 31, kg = lane >> 5;
-    const int left = int(W.rows - v0 < 256 ? W.rows - v0 : 256) - wm * (L::MB * 32) - kg * 4;
+    const int wm = wave / L::WN, wn = wave % L::WN, r16 = lane & 15, kg = lane >> 4;
+    const int left = int(W.rows - v0 < 256 ? W.rows - v0 : 256) - wm * (L::MB * 16) - kg * 4;
     uint8_t* st = smem + wave * (32 * 64 * 4);
-    float c[2], l[2];
+    float c[4], l[4];
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-        c[b] = coef[n0 + wn * 64 + b * 32 + r32];
-        l[b] = nl2[n0 + wn * 64 + b * 32 + r32];
+    for (int b = 0; b < 4; ++b) {
+        c[b] = coef[n0 + wn * 64 + b * 16 + r16];
+        l[b] = nl2[n0 + wn * 64 + b * 16 + r16];
     }
     const float k2 = zscale * LOG2E;
+    // 32 rows of the wave's sub-tile at a time through its staging slice
 #pragma unroll
-    for (int a = 0; a < L::MB; ++a) {
+    for (int a = 0; a < L::MB; a += 2) {
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < 4; ++b)
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
+            for (int g = 0; g < 2; ++g) {
                 f32x4 v4;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float d = c[b] * exp2_hw(__builtin_fmaf(acc[a][b][4 * g + e], k2, l[b]));
+                    const float d = c[b] * exp2_hw(__builtin_fmaf(acc[a + g][b][e], k2, l[b]));
                     // rows behind the vocabulary and tokens that take no part
-                    v4[e] = a * 32 + g * 8 + e < left && c[b] != 0.f ? d : 0.f;
+                    v4[e] = (a + g) * 16 + e < left && c[b] != 0.f ? d : 0.f;
                 }
-                *reinterpret_cast<f32x4*>(st + st_off(b * 32 + r32, g * 8 + kg * 4)) = v4;
+                *reinterpret_cast<f32x4*>(st + st_off(b * 16 + r16, g * 16 + kg * 4)) = v4;
             }
         __builtin_amdgcn_wave_barrier();
-        const int64_t vrow = v0 + wm * (L::MB * 32) + a * 32, tok = n0 + wn * 64;
+        const int64_t vrow = v0 + wm * (L::MB * 16) + a * 16, tok = n0 + wn * 64;
         // token j of the block, 8 vocabulary rows
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -404,26 +406,25 @@ __global__ __launch_bounds__(256) void head_patch_kernel(const int64_t* ids, int
 
 // dW rows of the piece = DT HT^T (K over the tokens), rounded to T.
 template <typename T, int NB, int PL>
-__global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2, 2))) void head_dw_kernel(
+__global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) void head_dw_kernel(
     Operand DT, Operand HT, int nk, uint32_t tm, uint32_t tn, T* dW, int64_t ldw, int dim) {
     using L = Layout<NB>;
     __shared__ __align__(16) uint8_t smem[head_lds(NB)];
     uint32_t ti, tj;
     if (!head_tile_of(blockIdx.x, tm, tn, ti, tj)) return;
     const int64_t v0 = int64_t(ti) * 256, c0 = int64_t(tj) * 64 * NB;
-    f32x16 acc[L::MB][L::NBW];
+    f32x4 acc[L::MB][L::NBW];
     head_tile<NB, PL>(smem, DT, HT, v0, c0, 0, nk, acc);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int wm = wave / L::WN, wn = wave % L::WN, r32 = lane & 31, kg = lane >> 5;
+    const int wm = wave / L::WN, wn = wave % L::WN, r16 = lane & 15, kg = lane >> 4;
     uint8_t* st = smem + wave * (32 * 64 * 4);
 #pragma unroll
-    for (int a = 0; a < L::MB; ++a) {
+    for (int a = 0; a < L::MB; a += 2) {
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < 4; ++b)
 #pragma unroll
-            for (int g = 0; g < 4; ++g)
-                *reinterpret_cast<f32x4*>(st + st_off(b * 32 + r32, g * 8 + kg * 4)) =
-                    f32x4{acc[a][b][4 * g], acc[a][b][4 * g + 1], acc[a][b][4 * g + 2], acc[a][b][4 * g + 3]};
+            for (int g = 0; g < 2; ++g)
+                *reinterpret_cast<f32x4*>(st + st_off(b * 16 + r16, g * 16 + kg * 4)) = acc[a + g][b];
         __builtin_amdgcn_wave_barrier();
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -431,7 +432,7 @@ __global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)
             f32x8 v;
 #pragma unroll
             for (int e = 0; e < 8; ++e) v.v[e] = *reinterpret_cast<const float*>(st + st_off(cc * 8 + e, row));
-            const int64_t vr = v0 + wm * (L::MB * 32) + a * 32 + row;
+            const int64_t vr = v0 + wm * (L::MB * 16) + a * 16 + row;
             const int c = int(c0) + wn * 64 + cc * 8;
             if (vr < DT.rows) st8n(dW + vr * ldw + c, v, dim - c);
         }
@@ -442,7 +443,7 @@ __global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)
 // One split of dH^T += WT D^T over the piece's vocabulary rows: the fp32 tile in
 // accumulator order (lane by lane, 16 bytes each), read and written whole.
 template <int NB, int PL>
-__global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2, 2))) void head_dh_kernel(
+__global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) void head_dh_kernel(
     Operand WT, Operand D, int nk, int stages, uint32_t tm, uint32_t tn, uint32_t splits, int first,
     f32x4* out) {
     using L = Layout<NB>;
@@ -454,65 +455,66 @@ __global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)
     ti -= sp * tm;
     const int k0 = int(sp) * stages, n = nk - k0 < stages ? nk - k0 : stages;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    f32x4* o = out + (((int64_t(sp) * tm + ti) * tn + tj) * 8 + wave) * (L::MB * L::NBW * 4 * 64) + lane;
+    f32x4* o = out + (((int64_t(sp) * tm + ti) * tn + tj) * 8 + wave) * (L::MB * L::NBW * 64) + lane;
     if (n <= 0) {
         // a short last piece may leave a split without stages
         if (first)
 #pragma unroll
-            for (int i = 0; i < L::MB * L::NBW * 4; ++i) o[i * 64] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int i = 0; i < L::MB * L::NBW; ++i) o[i * 64] = f32x4{0.f, 0.f, 0.f, 0.f};
         return;
     }
-    f32x16 acc[L::MB][L::NBW];
+    f32x4 acc[L::MB][L::NBW];
     head_tile<NB, PL>(smem, WT, D, int64_t(ti) * 256, int64_t(tj) * 64 * NB, k0, n, acc);
 #pragma unroll
     for (int a = 0; a < L::MB; ++a)
 #pragma unroll
-        for (int b = 0; b < L::NBW; ++b)
+        for (int b = 0; b < L::NBW; ++b) {
+            f32x4* q = o + (a * L::NBW + b) * 64;
+            f32x4 v = acc[a][b];
+            if (!first) {
+                const f32x4 old = *q;
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                f32x4 v = {acc[a][b][4 * g], acc[a][b][4 * g + 1], acc[a][b][4 * g + 2], acc[a][b][4 * g + 3]};
-                f32x4* q = o + ((a * L::NBW + b) * 4 + g) * 64;
-                if (!first) {
-                    const f32x4 old = *q;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] += old[e];
-                }
-                *q = v;
+                for (int e = 0; e < 4; ++e) v[e] += old[e];
             }
+            *q = v;
+        }
 }
 
-// dH <- the sum of the splits in order, one workgroup per wave block of a tile
-// (32 MB columns of dH x 64 tokens), turned through LDS.  Tokens that take no
-// part get zeros.
+// dH <- the sum of the splits in order: one workgroup per 16 columns of dH and
+// the 64 tokens of a wave's block, turned through LDS.  Tokens that take no part
+// get zeros.
 template <typename T, int NB>
 __global__ __launch_bounds__(256) void head_dh_out_kernel(const f32x4* acc, uint32_t tm, uint32_t tn,
                                                           uint32_t splits, const float* coef, T* dH,
                                                           int64_t ld, int64_t tokens, int dim) {
     using L = Layout<NB>;
-    constexpr int BLK = L::MB * L::NBW * 4, COLS = 32 * L::MB;
-    __shared__ float tile[64][COLS + 4];
-    const uint32_t wave = blockIdx.x & 7, tile_id = blockIdx.x >> 3, ti = tile_id / tn, tj = tile_id - ti * tn;
-    for (int i = threadIdx.x; i < BLK * 64; i += 256) {
-        f32x4 v = {0.f, 0.f, 0.f, 0.f};
-        for (uint32_t s = 0; s < splits; ++s) {
-            const f32x4 x = acc[((int64_t(s) * tm * tn + tile_id) * 8 + wave) * (BLK * 64) + i];
+    __shared__ float tile[64][20];
+    // blockIdx.x: tile, then wave, then row block of the wave
+    const uint32_t a = blockIdx.x % L::MB, wave = blockIdx.x / L::MB % 8, tile_id = blockIdx.x / (L::MB * 8);
+    const uint32_t ti = tile_id / tn, tj = tile_id - ti * tn;
+    const int lane = threadIdx.x & 63, b = threadIdx.x >> 6;
+    const f32x4* src = acc + (int64_t(tile_id) * 8 + wave) * (L::MB * L::NBW * 64) + (a * L::NBW + b) * 64 + lane;
+    const int64_t stride = int64_t(tm) * tn * 8 * (L::MB * L::NBW * 64);
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (uint32_t s = 0; s < splits; ++s) {
+        const f32x4 x = src[s * stride];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += x[e];
-        }
-        const int lane = i & 63, q = i >> 6, g = q & 3, b = (q >> 2) % L::NBW, a = (q >> 2) / L::NBW;
-        *reinterpret_cast<f32x4*>(&tile[b * 32 + (lane & 31)][a * 32 + g * 8 + (lane >> 5) * 4]) = v;
+        for (int e = 0; e < 4; ++e) v[e] += x[e];
     }
+    *reinterpret_cast<f32x4*>(&tile[b * 16 + (lane & 15)][(lane >> 4) * 4]) = v;
     __syncthreads();
     const int64_t n0 = int64_t(tj) * 64 * NB + (wave % L::WN) * 64;
-    const int c0 = int(ti) * 256 + int(wave / L::WN) * COLS;
-    for (int i = threadIdx.x; i < 64 * (COLS / 8); i += 256) {
-        const int j = i / (COLS / 8), c = (i % (COLS / 8)) * 8;
-        if (n0 + j >= tokens || c0 + c >= dim) continue;
-        const bool on = coef[n0 + j] != 0.f;
-        f32x8 v;
+    const int c0 = int(ti) * 256 + int(wave / L::WN) * (16 * L::MB) + int(a) * 16;
+    if (threadIdx.x < 128) {
+        const int j = threadIdx.x >> 1, c = (threadIdx.x & 1) * 8;
+        if (n0 + j < tokens && c0 + c < dim) {
+            const bool on = coef[n0 + j] != 0.f;
+            f32x8 o;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v.v[e] = on ? tile[j][c + e] : 0.f;
-        st8n(dH + (n0 + j) * ld + c0 + c, v, dim - c0 - c);
+            for (int e = 0; e < 8; ++e) o.v[e] = on ? tile[j][c + e] : 0.f;
+            st8n(dH + (n0 + j) * ld + c0 + c, o, dim - c0 - c);
+        }
     }
 }
 
@@ -572,7 +574,7 @@ hipError_t mo_launch_head_lse(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t*
     float2* part = reinterpret_cast<float2*>(ws + p.off_part) + v0 / 256 * p.n_pad;
     const dim3 grid(head_grid(uint64_t(tm) * tn)), block(H_THREADS);
 #define MO_CALL(NB, PL) \
-    return go(head_lse_kernel<NB, PL>, grid, block, s, W, H, int(p.kd / 32), tm, tn, a.inv_t, part, p.n_pad)
+    return go(head_lse_kernel<NB, PL>, grid, block, s, W, H, int(p.kd / 64), tm, tn, a.inv_t, part, p.n_pad)
     MO_HEAD_PICK(p.nb, p.planes, MO_CALL);
 #undef MO_CALL
 }
@@ -614,9 +616,9 @@ hipError_t mo_launch_head_ht(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* 
     const dim3 grid(unsigned(p.n_pad / 64), unsigned((a.dim + 63) / 64)), block(256);
     if (p.planes == 1)
         return go(head_transpose_kernel<bf16_t, 1>, grid, block, s, static_cast<const bf16_t*>(a.H), a.ldh, a.tokens,
-                  int(a.dim), coef, dst, p.n_pad, a.dim * p.n_pad);
+                  int(a.dim), coef, dst, p.ld_t, a.dim * p.ld_t);
     return go(head_transpose_kernel<float, 3>, grid, block, s, static_cast<const float*>(a.H), a.ldh, a.tokens,
-              int(a.dim), coef, dst, p.n_pad, a.dim * p.n_pad);
+              int(a.dim), coef, dst, p.ld_t, a.dim * p.ld_t);
 }
 
 hipError_t mo_launch_head_wt(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int64_t v0, int64_t rows,
@@ -625,9 +627,9 @@ hipError_t mo_launch_head_wt(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* 
     const dim3 grid(unsigned((rows + 255) / 256 * 4), unsigned((a.dim + 63) / 64)), block(256);
     if (p.planes == 1)
         return go(head_transpose_kernel<bf16_t, 1>, grid, block, s, static_cast<const bf16_t*>(a.W) + v0 * a.ldw, a.ldw,
-                  rows, int(a.dim), static_cast<const float*>(nullptr), dst, p.piece, a.dim * p.piece);
+                  rows, int(a.dim), static_cast<const float*>(nullptr), dst, p.ld_p, a.dim * p.ld_p);
     return go(head_transpose_kernel<float, 3>, grid, block, s, static_cast<const float*>(a.W) + v0 * a.ldw, a.ldw, rows,
-              int(a.dim), static_cast<const float*>(nullptr), dst, p.piece, a.dim * p.piece);
+              int(a.dim), static_cast<const float*>(nullptr), dst, p.ld_p, a.dim * p.ld_p);
 }
 
 hipError_t mo_launch_head_delta(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int64_t v0, int64_t rows,
@@ -639,8 +641,8 @@ hipError_t mo_launch_head_delta(const MoHeadArgs& a, const MoHeadPlan& p, uint8_
                 *nl2 = reinterpret_cast<const float*>(ws + p.off_nl2);
     bf16_t *D = reinterpret_cast<bf16_t*>(ws + p.off_d), *DT = reinterpret_cast<bf16_t*>(ws + p.off_dt);
 #define MO_CALL(NB, PL)                                                                                      \
-    return go(head_delta_kernel<NB, PL>, grid, block, s, W, H, int(p.kd / 32), tm, tn, a.inv_t, coef, nl2, D, \
-              p.piece, p.n_pad * p.piece, DT, p.n_pad, p.n_pad * p.piece)
+    return go(head_delta_kernel<NB, PL>, grid, block, s, W, H, int(p.kd / 64), tm, tn, a.inv_t, coef, nl2, D, \
+              p.ld_p, p.n_pad * p.ld_p, DT, p.ld_t, p.piece * p.ld_t)
     MO_HEAD_PICK(p.nb, p.planes, MO_CALL);
 #undef MO_CALL
 }
@@ -653,19 +655,19 @@ hipError_t mo_launch_head_patch(const MoHeadArgs& a, const MoHeadPlan& p, uint8_
     bf16_t *D = reinterpret_cast<bf16_t*>(ws + p.off_d), *DT = reinterpret_cast<bf16_t*>(ws + p.off_dt);
     const dim3 grid(cap_grid((pairs + 255) / 256, 1 << 16)), block(256);
     if (p.planes == 1)
-        return go(head_patch_kernel<1>, grid, block, s, a.ids, a.ld_ids, a.k, pairs, tval, coef, v0, rows, D, p.piece,
-                  p.n_pad * p.piece, DT, p.n_pad, p.n_pad * p.piece);
-    return go(head_patch_kernel<3>, grid, block, s, a.ids, a.ld_ids, a.k, pairs, tval, coef, v0, rows, D, p.piece,
-              p.n_pad * p.piece, DT, p.n_pad, p.n_pad * p.piece);
+        return go(head_patch_kernel<1>, grid, block, s, a.ids, a.ld_ids, a.k, pairs, tval, coef, v0, rows, D, p.ld_p,
+                  p.n_pad * p.ld_p, DT, p.ld_t, p.piece * p.ld_t);
+    return go(head_patch_kernel<3>, grid, block, s, a.ids, a.ld_ids, a.k, pairs, tval, coef, v0, rows, D, p.ld_p,
+              p.n_pad * p.ld_p, DT, p.ld_t, p.piece * p.ld_t);
 }
 
 hipError_t mo_launch_head_dw(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int64_t v0, int64_t rows,
                              hipStream_t s) {
-    const Operand DT = rows_of(ws + p.off_dt, p.n_pad, rows, p.n_pad * p.piece);
-    const Operand HT = rows_of(ws + p.off_ht, p.n_pad, a.dim, a.dim * p.n_pad);
+    const Operand DT = rows_of(ws + p.off_dt, p.ld_t, rows, p.piece * p.ld_t);
+    const Operand HT = rows_of(ws + p.off_ht, p.ld_t, a.dim, a.dim * p.ld_t);
     const uint32_t tm = uint32_t((rows + 255) / 256), tn = uint32_t((a.dim + 64 * p.nb_dw - 1) / (64 * p.nb_dw));
     const dim3 grid(head_grid(uint64_t(tm) * tn)), block(H_THREADS);
-    const int nk = int(p.n_pad / 32);
+    const int nk = int(p.n_pad / 64);
     if (p.planes == 1) {
         bf16_t* dW = static_cast<bf16_t*>(a.dW) + v0 * a.lddw;
         if (p.nb_dw == 4) return go(head_dw_kernel<bf16_t, 4, 1>, grid, block, s, DT, HT, nk, tm, tn, dW, a.lddw, int(a.dim));
@@ -680,9 +682,9 @@ hipError_t mo_launch_head_dw(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* 
 
 hipError_t mo_launch_head_dh(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, bool first, int64_t rows,
                              hipStream_t s) {
-    const Operand WT = rows_of(ws + p.off_wt, p.piece, a.dim, a.dim * p.piece);
-    const Operand D = rows_of(ws + p.off_d, p.piece, p.n_pad, p.n_pad * p.piece);
-    const int nk = int((rows + 255) / 256 * 8);   // the piece's rows, rounded up to whole tiles
+    const Operand WT = rows_of(ws + p.off_wt, p.ld_p, a.dim, a.dim * p.ld_p);
+    const Operand D = rows_of(ws + p.off_d, p.ld_p, p.n_pad, p.n_pad * p.ld_p);
+    const int nk = int((rows + 255) / 256 * 4);   // the piece's rows, rounded up to whole tiles
     const dim3 grid(head_grid(uint64_t(p.dh_tm) * p.dh_tn * p.dh_splits)), block(H_THREADS);
     f32x4* acc = reinterpret_cast<f32x4*>(ws + p.off_acc);
 #define MO_CALL(NB, PL)                                                                                        \
@@ -695,7 +697,8 @@ hipError_t mo_launch_head_dh(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* 
 hipError_t mo_launch_head_dh_out(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, hipStream_t s) {
     const f32x4* acc = reinterpret_cast<const f32x4*>(ws + p.off_acc);
     const float* coef = reinterpret_cast<const float*>(ws + p.off_coef);
-    const dim3 grid(p.dh_tm * p.dh_tn * 8), block(256);
+    // 8 waves x MB row blocks, MB = 2 NB
+    const dim3 grid(p.dh_tm * p.dh_tn * 16 * p.nb), block(256);
 #define MO_OUT(T, NB)                                                                                    \
     return go(head_dh_out_kernel<T, NB>, grid, block, s, acc, p.dh_tm, p.dh_tn, uint32_t(p.dh_splits), coef, \
               static_cast<T*>(a.dH), a.lddh, a.tokens, int(a.dim))

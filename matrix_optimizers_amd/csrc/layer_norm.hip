@@ -45,8 +45,9 @@ MO_DEV void team_sum(float (&x)[N], float* red, int& turn) {
 
 // One row per team: W <= 64 threads (256 / W rows per workgroup) or, W = 1024,
 // the whole workgroup of blockDim.x threads.  Thread t of a team holds the
-// 8-element chunks t, t + team, .. (R of them).
-template <typename T, int W, int R>
+// 8-element chunks t, t + team, .. (R of them); the next row is requested before
+// this one's reductions.
+template <typename T, int W, int R, bool FULL>
 __global__ __launch_bounds__(W > 64 ? LN_MAX_THREADS : 256) void ln_fwd_kernel(
     const T* X, int64_t ldx, const float* weight, const float* bias, T* Y, int64_t ldy, float* mean,
     float* rstd, int64_t rows, int cols, float eps) {
@@ -54,33 +55,41 @@ __global__ __launch_bounds__(W > 64 ? LN_MAX_THREADS : 256) void ln_fwd_kernel(
     const int team = W > 64 ? blockDim.x : W, teams = W > 64 ? 1 : 256 / W;
     const int t = W > 64 ? threadIdx.x : threadIdx.x % W;
     const int sub = W > 64 ? 0 : threadIdx.x / W;
+    const int64_t step = int64_t(gridDim.x) * teams;
     int turn = 0;
+    raw8<T> next[R];
+    auto request = [&](int64_t row) __attribute__((always_inline)) {
+        const T* x = X + (row < rows ? row : rows - 1) * ldx;
+#pragma unroll
+        for (int i = 0; i < R; ++i) next[i] = row8<FULL>(x, (t + team * i) * 8, cols);
+    };
+    request(int64_t(blockIdx.x) * teams + sub);
     f32x8 w[R], b[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const int c = (t + team * i) * 8;
-        if (weight) w[i] = widen(ld8n(weight + c, cols - c));
+        if (weight) w[i] = widen(row8<FULL>(weight, c, cols));
         else
 #pragma unroll
             for (int e = 0; e < 8; ++e) w[i].v[e] = 1.f;
-        if (bias) b[i] = widen(ld8n(bias + c, cols - c));
+        if (bias) b[i] = widen(row8<FULL>(bias, c, cols));
         else
 #pragma unroll
             for (int e = 0; e < 8; ++e) b[i].v[e] = 0.f;
     }
     const float n_cols = float(cols);
-    for (int64_t base = int64_t(blockIdx.x) * teams; base < rows; base += int64_t(gridDim.x) * teams) {
+    for (int64_t base = int64_t(blockIdx.x) * teams; base < rows; base += step) {
         const int64_t row = base + sub;
         const bool live = row < rows;
         f32x8 x[R];
         float s[1] = {0.f};
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const int c = (t + team * i) * 8;
-            x[i] = widen(ld8n(X + row * ldx + c, live ? cols - c : 0));
+            x[i] = widen(next[i]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) s[0] += x[i].v[e];
         }
+        if (base + step < rows) request(row + step);
         team_sum<W>(s, red, turn);
         const float mu = s[0] / n_cols;
         float q[1] = {0.f};
@@ -90,7 +99,7 @@ __global__ __launch_bounds__(W > 64 ? LN_MAX_THREADS : 256) void ln_fwd_kernel(
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 x[i].v[e] -= mu;
-                if (c + e < cols) q[0] += x[i].v[e] * x[i].v[e];
+                if (c + (FULL ? 0 : e) < cols) q[0] += x[i].v[e] * x[i].v[e];
             }
         }
         team_sum<W>(q, red, turn);
@@ -98,11 +107,10 @@ __global__ __launch_bounds__(W > 64 ? LN_MAX_THREADS : 256) void ln_fwd_kernel(
         if (live) {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                const int c = (t + team * i) * 8;
                 f32x8 y;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) y.v[e] = x[i].v[e] * r * w[i].v[e] + b[i].v[e];
-                st8n(Y + row * ldy + c, y, cols - c);
+                row8_out<FULL>(Y + row * ldy, (t + team * i) * 8, cols, y);
             }
             if (t == 0) {
                 if (mean) mean[row] = mu;
@@ -157,7 +165,7 @@ __global__ __launch_bounds__(LN_MAX_THREADS) void ln_fwd_long_kernel(
 // dx, and this workgroup's share of dw and db: a thread's columns stay the
 // same over the rows it walks, so the two sums live in its registers and leave
 // one fp32 partial row per workgroup (part[wg][0] = dw, part[wg][1] = db).
-template <typename T, int W, int R>
+template <typename T, int W, int R, bool FULL>
 __global__ __launch_bounds__(W > 64 ? LN_MAX_THREADS : 256) void ln_bwd_kernel(
     const T* dY, int64_t lddy, const T* X, int64_t ldx, const float* weight, const float* mean,
     const float* rstd, T* dX, int64_t lddx, float* part, int64_t rows, int cols) {
@@ -166,38 +174,40 @@ __global__ __launch_bounds__(W > 64 ? LN_MAX_THREADS : 256) void ln_bwd_kernel(
     const int team = W > 64 ? blockDim.x : W, teams = W > 64 ? 1 : 256 / W;
     const int t = W > 64 ? threadIdx.x : threadIdx.x % W;
     const int sub = W > 64 ? 0 : threadIdx.x / W;
+    const int64_t step = int64_t(gridDim.x) * teams;
     int turn = 0;
     f32x8 dw[R], db[R], w[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        const int c = (t + team * i) * 8;
 #pragma unroll
         for (int e = 0; e < 8; ++e) { dw[i].v[e] = 0.f; db[i].v[e] = 0.f; w[i].v[e] = 1.f; }
-        if (weight) w[i] = widen(ld8n(weight + c, cols - c));
+        if (weight) w[i] = widen(row8<FULL>(weight, (t + team * i) * 8, cols));
     }
     const float n_cols = float(cols);
-    for (int64_t base = int64_t(blockIdx.x) * teams; base < rows; base += int64_t(gridDim.x) * teams) {
+    for (int64_t base = int64_t(blockIdx.x) * teams; base < rows; base += step) {
         const int64_t row = base + sub;
         const bool live = row < rows;
-        const float mu = live ? mean[row] : 0.f, r = live ? rstd[row] : 0.f;
+        const int64_t at = live ? row : rows - 1;
+        const float mu = mean[at], r = rstd[at];
         raw8<T> x[R], dy[R];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const int c = (t + team * i) * 8, n = live ? cols - c : 0;
-            x[i] = ld8n(X + row * ldx + c, n);
-            dy[i] = ld8n(dY + row * lddy + c, n);
+            x[i] = row8<FULL>(X + at * ldx, (t + team * i) * 8, cols);
+            dy[i] = row8<FULL>(dY + at * lddy, (t + team * i) * 8, cols);
         }
         float s[2] = {0.f, 0.f};
+        if (live) {
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const f32x8 xv = widen(x[i]), gv = widen(dy[i]);
+            for (int i = 0; i < R; ++i) {
+                const f32x8 xv = widen(x[i]), gv = widen(dy[i]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float xh = (xv.v[e] - mu) * r, g = gv.v[e] * w[i].v[e];
-                s[0] += g;
-                s[1] += g * xh;
-                dw[i].v[e] += gv.v[e] * xh;
-                db[i].v[e] += gv.v[e];
+                for (int e = 0; e < 8; ++e) {
+                    const float xh = (xv.v[e] - mu) * r, g = gv.v[e] * w[i].v[e];
+                    s[0] += g;
+                    s[1] += g * xh;
+                    dw[i].v[e] += gv.v[e] * xh;
+                    db[i].v[e] += gv.v[e];
+                }
             }
         }
         if (dX) {
@@ -206,7 +216,6 @@ __global__ __launch_bounds__(W > 64 ? LN_MAX_THREADS : 256) void ln_bwd_kernel(
             if (live) {
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
-                    const int c = (t + team * i) * 8;
                     const f32x8 xv = widen(x[i]), gv = widen(dy[i]);
                     f32x8 o;
 #pragma unroll
@@ -214,7 +223,7 @@ __global__ __launch_bounds__(W > 64 ? LN_MAX_THREADS : 256) void ln_bwd_kernel(
                         const float xh = (xv.v[e] - mu) * r, g = gv.v[e] * w[i].v[e];
                         o.v[e] = r * (g - m1 - xh * m2);
                     }
-                    st8n(dX + row * lddx + c, o, cols - c);
+                    row8_out<FULL>(dX + row * lddx, (t + team * i) * 8, cols, o);
                 }
             }
         }
@@ -326,24 +335,28 @@ __global__ __launch_bounds__(1024) void ln_reduce_kernel(const float* part, int 
     }
 }
 
-// Columns up to which the register kernels run (chunks of 8 in 1024 threads).
-constexpr int FWD_MAX_COLS = 4 * 8 * LN_MAX_THREADS, BWD_MAX_COLS = 2 * 8 * LN_MAX_THREADS;
+// Columns up to which a row stays in registers (two chunks of 8 per thread).
+constexpr int MAX_COLS = 2 * 8 * LN_MAX_THREADS;
 
 struct Shape { int W, R, threads; };   // team, chunks per thread, workgroup
 
 // Rows of at most 512 columns share a workgroup (8 to 64 threads each); longer
-// ones take a workgroup of their own.
-Shape shape_of(int64_t cols) {
+// ones take a workgroup of their own, with one chunk per thread up to `one`
+// chunks and two above.  Measured at 16384 x 8192 bf16 forward: two chunks 95 us,
+// one 113, four 101; at 16384 x 4096: 47, 50, 49.  Backward at 16381 x 4096 one
+// chunk 87 us, two 87, four 97; at 8192 x 8192 two 90, one 96.
+Shape shape_of(int64_t cols, int one) {
     const int chunks = int((cols + 7) / 8);
     if (chunks <= 64) {
         int W = 8;
         while (W < chunks) W *= 2;
         return {W, 1, 256};
     }
-    const int R = chunks <= LN_MAX_THREADS ? 1 : chunks <= 2 * LN_MAX_THREADS ? 2 : 4;
-    const int threads = ((chunks + R - 1) / R + 63) / 64 * 64;
-    return {LN_MAX_THREADS, R, threads};
+    const int R = chunks <= one ? 1 : 2;
+    return {LN_MAX_THREADS, R, ((chunks + R - 1) / R + 63) / 64 * 64};
 }
+Shape fwd_shape(int64_t cols) { return shape_of(cols, 64); }
+Shape bwd_shape(int64_t cols) { return shape_of(cols, 512); }
 
 unsigned wgs_for(int64_t rows, const Shape& s, int per_cu) {
     const int64_t per = s.W > 64 ? 1 : 256 / s.W;
@@ -351,40 +364,38 @@ unsigned wgs_for(int64_t rows, const Shape& s, int per_cu) {
     return unsigned(want < cap ? want : cap);
 }
 
-template <typename T>
+template <typename T, bool FULL>
 hipError_t fwd(const MoLnArgs& a, hipStream_t s) {
     const T* X = static_cast<const T*>(a.X);
     T* Y = static_cast<T*>(a.Y);
     const int cols = int(a.cols);
-    if (cols > FWD_MAX_COLS) {
+    if (cols > MAX_COLS) {
         hipLaunchKernelGGL(ln_fwd_long_kernel<T>, dim3(unsigned(a.rows < 512 ? a.rows : 512)),
                            dim3(LN_MAX_THREADS), 0, s, X, a.ldx, a.weight, a.bias, Y, a.ldy, a.mean_out,
                            a.rstd_out, a.rows, cols, a.eps);
         return hipGetLastError();
     }
-    const Shape sh = shape_of(cols);
-    const dim3 grid(wgs_for(a.rows, sh, sh.W > 64 ? 4096 / sh.threads : 16)), block(sh.threads);
-#define MO_LN_FWD(W, R)                                                                              \
-    hipLaunchKernelGGL((ln_fwd_kernel<T, W, R>), grid, block, 0, s, X, a.ldx, a.weight, a.bias, Y,   \
+    const Shape sh = fwd_shape(cols);
+    const dim3 grid(wgs_for(a.rows, sh, sh.W > 64 ? 2048 / sh.threads : 16)), block(sh.threads);
+#define MO_LN_FWD(W, R)                                                                               \
+    hipLaunchKernelGGL((ln_fwd_kernel<T, W, R, FULL>), grid, block, 0, s, X, a.ldx, a.weight, a.bias, Y,   \
                        a.ldy, a.mean_out, a.rstd_out, a.rows, cols, a.eps)
     if (sh.W == 8) MO_LN_FWD(8, 1);
     else if (sh.W == 16) MO_LN_FWD(16, 1);
     else if (sh.W == 32) MO_LN_FWD(32, 1);
     else if (sh.W == 64) MO_LN_FWD(64, 1);
-    else if (sh.R == 1) MO_LN_FWD(LN_MAX_THREADS, 1);
-    else if (sh.R == 2) MO_LN_FWD(LN_MAX_THREADS, 2);
-    else MO_LN_FWD(LN_MAX_THREADS, 4);
+    else MO_LN_FWD(LN_MAX_THREADS, 2);
 #undef MO_LN_FWD
     return hipGetLastError();
 }
 
-template <typename T>
+template <typename T, bool FULL>
 hipError_t bwd(const MoLnArgs& a, float* part, int n_part, hipStream_t s) {
     const T *X = static_cast<const T*>(a.X), *dY = static_cast<const T*>(a.dY);
     T* dX = static_cast<T*>(a.dX);
     const int cols = int(a.cols);
     float* pp = a.dweight || a.dbias ? part : nullptr;
-    if (cols > BWD_MAX_COLS) {
+    if (cols > MAX_COLS) {
         if (dX)
             hipLaunchKernelGGL(ln_bwd_long_kernel<T>, dim3(unsigned(a.rows < 512 ? a.rows : 512)),
                                dim3(LN_MAX_THREADS), 0, s, dY, a.lddy, X, a.ldx, a.weight, a.mean, a.rstd, dX,
@@ -394,10 +405,10 @@ hipError_t bwd(const MoLnArgs& a, float* part, int n_part, hipStream_t s) {
                                dim3(256), 0, s, dY, a.lddy, X, a.ldx, a.mean, a.rstd, pp, a.rows, cols);
         return hipGetLastError();
     }
-    const Shape sh = shape_of(cols);
+    const Shape sh = bwd_shape(cols);
     const dim3 grid{unsigned(n_part)}, block(sh.threads);
 #define MO_LN_BWD(W, R)                                                                               \
-    hipLaunchKernelGGL((ln_bwd_kernel<T, W, R>), grid, block, 0, s, dY, a.lddy, X, a.ldx, a.weight,   \
+    hipLaunchKernelGGL((ln_bwd_kernel<T, W, R, FULL>), grid, block, 0, s, dY, a.lddy, X, a.ldx, a.weight,   \
                        a.mean, a.rstd, dX, a.lddx, pp, a.rows, cols)
     if (sh.W == 8) MO_LN_BWD(8, 1);
     else if (sh.W == 16) MO_LN_BWD(16, 1);
@@ -413,17 +424,22 @@ hipError_t bwd(const MoLnArgs& a, float* part, int n_part, hipStream_t s) {
 
 int mo_ln_bwd_parts(int64_t rows, int64_t cols) {
     if (rows == 0) return 0;
-    if (cols > BWD_MAX_COLS) return int(rows < 64 ? rows : 64);
-    const Shape sh = shape_of(cols);
-    return int(wgs_for(rows, sh, sh.W > 64 ? (sh.threads > 512 ? 1 : 1024 / sh.threads) : 4));
+    if (cols > MAX_COLS) return int(rows < 64 ? rows : 64);
+    // two workgroups per CU (one of more than 512 threads): each leaves a partial
+    // row of 8 bytes per column; at 16381 x 4096, four per CU measured 106 us
+    // against 87, one 124
+    const Shape sh = bwd_shape(cols);
+    return int(wgs_for(rows, sh, sh.W > 64 ? (sh.threads > 512 ? 1 : 2) : 4));
 }
 
 hipError_t mo_launch_ln_fwd(const MoLnArgs& a, hipStream_t s) {
-    return a.dtype == MO_BF16 ? fwd<bf16_t>(a, s) : fwd<float>(a, s);
+    if (a.cols % 8 == 0) return a.dtype == MO_BF16 ? fwd<bf16_t, true>(a, s) : fwd<float, true>(a, s);
+    return a.dtype == MO_BF16 ? fwd<bf16_t, false>(a, s) : fwd<float, false>(a, s);
 }
 hipError_t mo_launch_ln_bwd(const MoLnArgs& a, float* part, hipStream_t s) {
     const int n = mo_ln_bwd_parts(a.rows, a.cols);
-    return a.dtype == MO_BF16 ? bwd<bf16_t>(a, part, n, s) : bwd<float>(a, part, n, s);
+    if (a.cols % 8 == 0) return a.dtype == MO_BF16 ? bwd<bf16_t, true>(a, part, n, s) : bwd<float, true>(a, part, n, s);
+    return a.dtype == MO_BF16 ? bwd<bf16_t, false>(a, part, n, s) : bwd<float, false>(a, part, n, s);
 }
 hipError_t mo_launch_ln_reduce(const MoLnArgs& a, const float* part, hipStream_t s) {
     hipLaunchKernelGGL(ln_reduce_kernel, dim3(unsigned((a.cols + 31) / 32), 2), dim3(1024), 0, s, part,

@@ -68,3 +68,31 @@ template <typename T> MO_DEV void st8n(T* p, const f32x8& v, int n) {
             if (e < n) p[e] = from_f32<T>(v.v[e]);
     }
 }
+
+// Chunk c .. c + 7 of a row of `cols` elements, zeros behind its end.  FULL (cols
+// a multiple of 8): a chunk is whole or outside, and is loaded without a branch
+// (from the row's start when it is outside), so that loads of several chunks and
+// rows go out back to back.
+template <bool FULL, typename T> MO_DEV raw8<T> row8(const T* row, int c, int cols) {
+    if constexpr (FULL) {
+        const bool in = c < cols;
+        raw8<T> r = ld8(row + (in ? c : 0));
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) r.q[e] = in ? r.q[e] : 0u;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) { r.lo[e] = in ? r.lo[e] : 0.f; r.hi[e] = in ? r.hi[e] : 0.f; }
+        }
+        return r;
+    } else {
+        return ld8n(row + c, cols - c);
+    }
+}
+template <bool FULL, typename T> MO_DEV void row8_out(T* row, int c, int cols, const f32x8& v) {
+    if constexpr (FULL) {
+        if (c < cols) st8(row + c, v);
+    } else {
+        st8n(row + c, v, cols - c);
+    }
+}

@@ -95,14 +95,22 @@ MoEmbPlan emb_plan(int64_t n, int64_t vocab, int64_t dim) {
     p.passes = (bits + 8) / 9;
     p.bits = (bits + p.passes - 1) / p.passes;
     p.tiles = uint32_t((n + MO_EMB_SORT_TILE - 1) / MO_EMB_SORT_TILE);
-    p.C = int(std::max<int64_t>(4, (n + 2047) / 2048));
+    p.C = int(std::max<int64_t>(4, (n + 511) / 512));
     p.chunks = uint32_t((n + p.C - 1) / p.C);
     Carve take;
     for (int b = 0; b < 2; ++b) {
         p.off_keys[b] = take(uint64_t(n) * 4);
         p.off_idx[b] = take(uint64_t(n) * 4);
     }
-    p.off_hist = take((uint64_t(p.tiles) << p.bits) * 4);
+    // One workgroup sorts up to 2^15 positions (its LDS and registers) where the
+    // key and the position share a 32-bit word, in one launch; otherwise three
+    // launches per pass.
+    int idx_bits = 1;
+    while ((int64_t(1) << idx_bits) < n) ++idx_bits;
+    p.idx_bits = n <= (1 << 15) && bits + idx_bits <= 32 ? idx_bits : 0;
+    if (!p.idx_bits) p.off_hist = take((uint64_t(p.tiles) << p.bits) * 4);
+    p.off_spans = take(uint64_t(p.chunks) * 12);
+    p.off_count = take(4);
     p.off_head = take(uint64_t(p.chunks) * dim * 4);
     p.off_tail = take(uint64_t(p.chunks) * dim * 4);
     p.bytes = take.at;
@@ -124,45 +132,81 @@ mo_status head_shape(const mo_head* h, int64_t* ldh, int64_t* ldw) {
     return stride_of(h->ld_w, h->dim, ldw);
 }
 
-// A K extent the GEMM's stages cover: 64, 128 or a multiple of 64 from 256 on.
-int64_t k_extent(int64_t k) { return k <= 64 ? 64 : k <= 128 ? 128 : std::max<int64_t>(256, (k + 63) / 64 * 64); }
+// A K extent of whole GEMM stages.
+int64_t k_extent(int64_t k) { return (k + 63) / 64 * 64; }
+
+// The row stride of a copy: not a multiple of 4 KB, which would put the 256 rows
+// of a tile's stage on few memory channels.
+int64_t copy_stride(int64_t k) { return k * 2 % 4096 == 0 ? k + 64 : k; }
 
 // Whether bf16 rows can be loaded in place: 16-byte aligned rows of whole
-// stages, less than 2^24 bytes apart (the GEMM's 32-bit row offsets).
+// stages, less than 2^23 bytes apart (the GEMM's row offsets within a tile).
 bool in_place(const void* p, int64_t ld, int64_t dim) {
     return k_extent(dim) == dim && ((reinterpret_cast<uintptr_t>(p) | uintptr_t(ld * 2)) & 15) == 0 &&
-           ld * 2 < (int64_t(1) << 24);
+           ld * 2 < (int64_t(1) << 23);
 }
 
-// Tile width over the tokens: the least padded work, a narrow tile's column
-// costing more (its workgroup reads the same 256 rows of the other operand).
-int token_tile(int64_t n) {
-    if (n <= 64) return 1;
-    if (n <= 128) return 2;
-    const int64_t c4 = (n + 255) / 256 * 100, c2 = (n + 127) / 128 * 58;
-    return c2 < c4 ? 2 : 4;
+// Rounds of the 256 CUs that `tiles` tiles take.
+int64_t rounds(int64_t tiles) { return (tiles + 255) / 256; }
+
+// Relative time of a 256 x 64 nb tile: a narrow one reads the same 256 rows of P.
+int64_t tile_cost(int nb) { return nb == 4 ? 100 : nb == 2 ? 56 : 34; }
+
+// Tile width over the tokens: the least rounds times cost over the vocabulary's tiles.
+int token_tile(int64_t n, int64_t v_tiles) {
+    int best = 4;
+    int64_t least = 0;
+    for (int nb = 4; nb >= 1; nb /= 2) {
+        const int64_t c = rounds((n + 64 * nb - 1) / (64 * nb) * v_tiles) * tile_cost(nb);
+        if (nb == 4 || c < least) {
+            least = c;
+            best = nb;
+        }
+    }
+    return best;
 }
 
 MoHeadPlan head_plan(const MoHeadArgs& a, bool backward, bool need_dh, bool need_dw) {
     MoHeadPlan p = {};
     p.planes = a.dtype == MO_BF16 ? 1 : 3;
-    p.nb = token_tile(a.tokens);
+    p.v_tiles = (a.vocab + 255) / 256;
+    p.nb = token_tile(a.tokens, p.v_tiles);
     p.n_pad = (a.tokens + 64 * p.nb - 1) / (64 * p.nb) * (64 * p.nb);
     p.kd = k_extent(a.dim);
     p.pack_h = p.planes != 1 || !in_place(a.H, a.ldh, a.dim);
     p.pack_w = p.planes != 1 || !in_place(a.W, a.ldw, a.dim);
-    p.v_tiles = (a.vocab + 255) / 256;
+    p.nb_dw = a.dim <= 64 ? 1 : a.dim <= 128 ? 2 : 4;
     const int64_t tn = p.n_pad / (64 * p.nb);
-    // pieces of equal size, bounded by the memory of their copies (and by the
-    // grid of one launch); at least one tile
+    // pieces bounded by the memory of their copies (and by the grid of one launch);
+    // at least one tile
     int64_t row = p.pack_w ? 2 * p.planes * p.kd : 0;
     // (the same pieces whichever gradients are asked for, so that the size query holds for each)
     if (backward) row += 4 * p.planes * p.n_pad + 2 * p.planes * a.dim;
     int64_t most = std::min<int64_t>((int64_t(1) << 22) / std::max<int64_t>(tn, (a.dim + 63) / 64), 1 << 13);
     if (row) most = std::min(most, kHeadPieceBytes / row / 256);
     most = std::max<int64_t>(most, 1);
-    const int64_t pieces = (p.v_tiles + most - 1) / most;
-    p.piece = (p.v_tiles + pieces - 1) / pieces * 256;
+    // Of the piece sizes from `most` down to half of it (64 tried at most), the one
+    // whose products take the least rounds, each round as long as its K: at 8192
+    // tokens x 128256 x 4096, 64 tiles fill the CUs evenly where 72 leave dW half a round.
+    const int64_t tn_dw = (a.dim + 64 * p.nb_dw - 1) / (64 * p.nb_dw);
+    const int64_t top = std::min(most, p.v_tiles);
+    int64_t best = 0, least = 0;
+    for (int64_t m = top; m >= 1 && 2 * m >= top && top - m < 64; --m) {
+        auto cost = [&](int64_t tiles) {
+            int64_t c = p.kd * tile_cost(p.nb) * rounds(tiles * tn) + 40000;   // 40000: a piece's launches
+            if (backward) c += p.n_pad * tile_cost(p.nb_dw) * rounds(tiles * tn_dw);
+            return c;
+        };
+        const int64_t full = p.v_tiles / m, rest = p.v_tiles - full * m;
+        const int64_t c = full * cost(m) + (rest ? cost(rest) : 0);
+        if (best == 0 || c < least) {
+            least = c;
+            best = m;
+        }
+    }
+    p.piece = best * 256;
+    p.ld_t = copy_stride(p.n_pad);
+    p.ld_p = copy_stride(p.piece);
     Carve take;
     if (p.pack_h) p.off_hp = take(uint64_t(2) * p.planes * a.tokens * p.kd);
     if (p.pack_w) p.off_wp = take(uint64_t(2) * p.planes * p.piece * p.kd);
@@ -172,21 +216,20 @@ MoHeadPlan head_plan(const MoHeadArgs& a, bool backward, bool need_dh, bool need
         p.off_coef = take(uint64_t(4) * p.n_pad);
         p.off_nl2 = take(uint64_t(4) * p.n_pad);
         p.off_tval = take(uint64_t(4) * a.tokens * a.k);
-        p.off_d = take(uint64_t(2) * p.planes * p.n_pad * p.piece);
-        p.off_dt = take(uint64_t(2) * p.planes * p.n_pad * p.piece);
+        p.off_d = take(uint64_t(2) * p.planes * p.n_pad * p.ld_p);
+        p.off_dt = take(uint64_t(2) * p.planes * p.piece * p.ld_t);
         if (need_dw) {
-            p.nb_dw = a.dim <= 64 ? 1 : a.dim <= 128 ? 2 : 4;
-            p.off_ht = take(uint64_t(2) * p.planes * a.dim * p.n_pad);
+            p.off_ht = take(uint64_t(2) * p.planes * a.dim * p.ld_t);
         }
         if (need_dh) {
-            p.off_wt = take(uint64_t(2) * p.planes * a.dim * p.piece);
+            p.off_wt = take(uint64_t(2) * p.planes * a.dim * p.ld_p);
             p.dh_tm = uint32_t((a.dim + 255) / 256);
             p.dh_tn = uint32_t(tn);
-            // enough splits of K for two rounds of the 256 CUs, whole tiles of 8 stages
+            // splits of K that fill the 256 CUs once, in whole tiles of 256 rows (4 stages)
             const int64_t tiles = int64_t(p.dh_tm) * p.dh_tn, groups = p.piece / 256;
-            const int64_t want = std::max<int64_t>(1, std::min<int64_t>(512 / tiles, groups));
-            p.dh_stages = int((groups + want - 1) / want * 8);
-            p.dh_splits = int((groups * 8 + p.dh_stages - 1) / p.dh_stages);
+            const int64_t want = std::max<int64_t>(1, std::min<int64_t>(256 / tiles, groups));
+            p.dh_stages = int((groups + want - 1) / want * 4);
+            p.dh_splits = int((groups * 4 + p.dh_stages - 1) / p.dh_stages);
             p.off_acc = take(uint64_t(4) * p.dh_splits * tiles * 256 * 64 * p.nb);
         }
     }
@@ -282,7 +325,7 @@ mo_status zero_rows(void* p, int64_t rows, int64_t cols, int64_t ld, int32_t dty
     e.dim = cols;
     e.ldg = ld;
     e.g_dtype = dtype;
-    MO_RUN(phase, mo_launch_emb_bwd(e, MoEmbPlan{}, nullptr, s));
+    MO_RUN(phase, mo_launch_emb_fill(e, s));
     return MO_OK;
 }
 
@@ -492,7 +535,11 @@ mo_status embedding_backward(const int64_t* tokens, int64_t n, const void* dY, i
     if (!take_workspace(workspace, workspace_bytes, p.bytes, &r, &ws)) return MO_ERR_WORKSPACE_TOO_SMALL;
     if (ranges_conflict(r)) return MO_ERR_ALIAS;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    if (n) MO_RUN(MO_PHASE_EMB_SORT, mo_launch_emb_sort(a, p, ws, s));
+    if (n == 0) {
+        MO_RUN(MO_PHASE_EMB_BWD, mo_launch_emb_fill(a, s));
+        return MO_OK;
+    }
+    MO_RUN(MO_PHASE_EMB_SORT, mo_launch_emb_sort(a, p, ws, s));
     MO_RUN(MO_PHASE_EMB_BWD, mo_launch_emb_bwd(a, p, ws, s));
     return MO_OK;
 }

@@ -35,20 +35,22 @@ struct MoEmbArgs {
     int32_t w_dtype, dy_dtype, g_dtype, accumulate;
     float scale;
 };
-// The sort (passes of `bits` bits over `tiles` tiles) and the run sums (`chunks`
-// chunks of C sorted positions), with their workspace offsets.
+// The sort (passes of `bits` bits; idx_bits > 0: in one workgroup, otherwise over
+// `tiles` tiles) and the run sums (`chunks` chunks of C sorted positions), with
+// their workspace offsets.
 struct MoEmbPlan {
-    int passes, bits, C;
+    int passes, bits, idx_bits, C;
     uint32_t tiles, chunks;
-    uint64_t off_keys[2], off_idx[2], off_hist, off_head, off_tail, bytes;
+    uint64_t off_keys[2], off_idx[2], off_hist, off_spans, off_count, off_head, off_tail, bytes;
 };
+hipError_t mo_launch_emb_fill(const MoEmbArgs& a, hipStream_t s);
 hipError_t mo_launch_emb_fwd(const MoEmbArgs& a, hipStream_t s);
 hipError_t mo_launch_emb_sort(const MoEmbArgs& a, const MoEmbPlan& p, uint8_t* ws, hipStream_t s);
 hipError_t mo_launch_emb_bwd(const MoEmbArgs& a, const MoEmbPlan& p, uint8_t* ws, hipStream_t s);
 
 // ---- output head: softmax cross entropy and distillation ---------------------------
 // H (tokens x dim) and W (vocab x dim) as bf16 planes (one for bf16 tensors, three
-// for fp32 ones).  Every matrix below is read along K in 64-byte stages.
+// for fp32 ones).  Every matrix below is read along K in stages of 64 elements.
 struct MoHeadArgs {
     const void *H, *W;
     int64_t tokens, vocab, dim, ldh, ldw;
@@ -74,6 +76,7 @@ struct MoHeadPlan {
     int64_t kd;             // dim as a K extent (rounded up, zeros behind)
     bool pack_h, pack_w;    // operand copied (padded, split) before use
     int64_t piece;          // vocabulary rows per piece (a multiple of 256)
+    int64_t ld_t, ld_p;     // row strides of the copies along the tokens and along the piece
     int64_t v_tiles;        // 256-row tiles of the vocabulary
     // dH: K stages per split, number of splits, tiles of 256 (dim) x 64 nb
     int dh_stages, dh_splits;

@@ -1,44 +1,110 @@
-"""CPU models of the output head's GEMM (head_gemm.h): its K pipeline (the
-schedule of the eight-wavefront core, checked by the same model at this core's
-load counts), the cursor that walks the plane pairs of a split fp32 product, the
-assignment of tiles to workgroups, and the rows its loads touch."""
+"""CPU models of the output head's GEMM (head_gemm.h): the order in which a
+wavefront issues its loads, reads fragments, waits and passes barriers; the
+cursor that walks the plane pairs of a split fp32 product; the assignment of
+tiles to workgroups; the rows and bytes its loads touch; its LDS swizzle."""
 import os
 import re
 
 import pytest
 
-from test_gemm_pipeline import CSRC, check, wait_cases
-
-HEADER = open(os.path.join(CSRC, "head_gemm.h")).read()
-
-
-@pytest.mark.parametrize("LP", [8, 6])   # 2 (2 + QI): widths 256; 128 and 64
-def test_pipeline_waits_are_exact_and_slots_safe(LP):
-    cases, used = wait_cases("head_gemm.h"), set()
-    for nk in range(8, 601, 2):
-        used |= check(LP, nk)
-    assert used <= cases
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = open(os.path.join(ROOT, "matrix_optimizers_amd", "csrc", "head_gemm.h")).read()
+CPP = open(os.path.join(ROOT, "matrix_optimizers_amd", "csrc", "operators.cpp")).read()
 
 
-def test_short_products_fit_the_ring():
-    """Two or four stages are loaded at once into the five slots; six never occur."""
-    def k_extent(k):
-        return 64 if k <= 64 else 128 if k <= 128 else max(256, (k + 63) // 64 * 64)
-    for k in range(1, 5000):
-        nk = k_extent(k) // 32
-        assert nk % 2 == 0 and (nk in (2, 4) or nk >= 8), k
-        assert k_extent(k) >= k
-    # tokens padded to the tile width give a K extent too
-    for n in range(1, 3000):
-        nb = 1 if n <= 64 else 2 if n <= 128 else (2 if (n + 127) // 128 * 58 < (n + 255) // 256 * 100 else 4)
-        n_pad = -(-n // (64 * nb)) * 64 * nb
-        assert n_pad // 32 in (2, 4) or n_pad // 32 >= 8, n
+def events(n, LS):
+    """One wavefront's ('load', stage), ('read', stage), ('wait', left outstanding),
+    ('barrier',) in program order, for n stages of LS loads each."""
+    num, den = map(int, re.search(r"LH = \(LS \* (\d) \+ 7\) / (\d)", HEADER).groups())
+    LH = (LS * num + 7) // den
+    ev = [("load", 0)] * LS
+    if n > 1:
+        ev += [("load", 1)] * LS
+    ev += [("wait", LS if n > 1 else 0), ("barrier",), ("read", 0)]     # first quarter's fragments
+
+    def stage(s, ld0, nxt, ld3):
+        # a quarter's reads and loads go out between its MFMAs: in any order
+        out = [("read", s)]
+        if ld0:
+            out += [("load", s + 1)] * (LS - LH)
+        out += [("read", s), ("read", s)]
+        if nxt:
+            out += [("wait", 0), ("barrier",), ("read", s + 1)]
+        if ld3:
+            out += [("load", s + 2)] * LH
+        return out
+
+    if n > 2:
+        ev += stage(0, False, True, True)
+        for s in range(1, n - 2):
+            ev += stage(s, True, True, True)
+        ev += stage(n - 2, True, True, False)
+    elif n == 2:
+        ev += stage(0, False, True, False)
+    ev += stage(n - 1, False, False, False)
+    return ev
+
+
+def check(n, LS):
+    ev = events(n, LS)
+    loads = [e[1] for e in ev if e[0] == "load"]
+    assert sorted(loads) == sorted(s for s in range(n) for _ in range(LS))
+    issued, landed, published = [], 0, set()
+    last_read = {}          # slot -> stage read since the last barrier
+    free = {0: True, 1: True}   # slots no read is pending on
+    for e in ev:
+        if e[0] == "load":
+            assert free[e[1] % 2], ("slot still being read", n, e)
+            issued.append(e[1])
+        elif e[0] == "wait":
+            landed = max(landed, len(issued) - e[1])
+        elif e[0] == "barrier":
+            done = issued[:landed]
+            published = {s for s in range(n) if done.count(s) == LS}
+            free = {0: True, 1: True}
+        else:
+            assert e[1] in published, ("read before it is published", n, e)
+            free[e[1] % 2] = False
+    # the barrier that frees a slot comes after the last read of its stage
+    for s in range(n - 2):
+        first_load = max(i for i, e in enumerate(ev) if e == ("read", s))
+        barrier = next(i for i, e in enumerate(ev) if i > first_load and e == ("barrier",))
+        refill = next(i for i, e in enumerate(ev) if e == ("load", s + 2))
+        assert barrier < refill, (n, s)
+
+
+@pytest.mark.parametrize("LS", [8, 6, 5])   # 4 + NB load instructions per stage
+def test_pipeline(LS):
+    for n in list(range(1, 40)) + [64, 129]:
+        check(n, LS)
+
+
+def test_model_catches_an_early_refill(monkeypatch):
+    orig = events
+
+    def bad(n, LS):
+        ev = orig(n, LS)
+        i = next(i for i, e in enumerate(ev) if e == ("load", 2))
+        return ev[:5] + [ev[i]] + ev[5:i] + ev[i + 1:]
+    import sys
+    monkeypatch.setattr(sys.modules[__name__], "events", bad)
+    with pytest.raises(AssertionError):
+        check(8, 8)
+
+
+def test_waits_cover_the_load_counts():
+    """The prologue leaves exactly the second stage's LS = 4 + NB loads outstanding."""
+    assert re.search(r"LS = 4 \+ NB;", HEADER)
+    for ls in (8, 6):
+        assert f"if constexpr (LS == {ls}) asm volatile(\"s_waitcnt vmcnt({ls})\"" in HEADER
+    assert "else asm volatile(\"s_waitcnt vmcnt(5)\"" in HEADER
 
 
 def seg_tables():
     """The plane of P and Q in each of the six segments, read from the source."""
     body_p = re.search(r"int seg_p\(int s\) \{ return (.*?); \}", HEADER).group(1)
     body_q = re.search(r"int seg_q\(int s\) \{ return (.*?); \}", HEADER).group(1)
+
     def ev(expr, s):
         expr = expr.replace("PL == 1 ? 0 : ", "")
         m = re.match(r"s == (\d) \? 2 : \(s == (\d) \|\| s == (\d)\) \? 1 : 0", expr)
@@ -54,15 +120,15 @@ def test_plane_pairs_are_the_six_largest_smallest_first():
     assert weight == sorted(weight, reverse=True)
 
 
-@pytest.mark.parametrize("nk1", [2, 4, 6, 8, 32])
+@pytest.mark.parametrize("nk1", [1, 2, 3, 8, 33])
 def test_cursor_visits_every_stage_of_every_pair_in_order(nk1):
-    """next_pair() after each pair of stages: stage s of the long loop is stage
-    s mod nk1 of segment s / nk1."""
+    """next_stage() after each stage: stage s of the long loop is stage s mod nk1 of
+    segment s / nk1."""
     ck, seg, off, seen = 0, 0, 0, []
-    for _ in range(nk1 * 6 // 2):
-        seen += [(seg, off), (seg, off + 1)]
-        off += 2
-        ck += 2
+    for _ in range(nk1 * 6):
+        seen.append((seg, off))
+        off += 1
+        ck += 1
         if ck == nk1:
             ck, off, seg = 0, 0, seg + 1
     assert seen == [(s, k) for s in range(6) for k in range(nk1)]
@@ -87,19 +153,53 @@ def test_every_tile_runs_once(tm, tn):
     assert sorted(tiles) == [(i, j) for i in range(tm) for j in range(tn)]
 
 
+def swz(row):
+    return (row >> 1) & 7
+
+
 @pytest.mark.parametrize("nb", [4, 2, 1])
 def test_loads_fill_the_stage_and_stay_in_the_rows(nb):
-    """The rows the eight waves' load instructions place in a stage, and the
-    (clamped) rows they read for a matrix that ends inside the tile."""
-    qi = 2 if nb == 4 else 1
-    p_rows, q_rows = set(), set()
+    """The bytes the eight waves' load instructions place in a stage, which chunk of
+    which row each is, and the (clamped) rows they read for a matrix that ends
+    inside the tile."""
+    filled = {}
     for wave in range(8):
-        qw = wave & 3 if nb == 1 else wave
-        for lane in range(64):
-            lrow = lane >> 2
-            p_rows |= {wave * 32 + i * 16 + lrow for i in range(2)}
-            q_rows |= {qw * 16 * qi + i * 16 + lrow for i in range(qi)}
-    assert p_rows == set(range(256)) and q_rows == set(range(64 * nb))
+        for i in range(4 + nb):
+            first = wave * 32 + i * 8 if i < 4 else wave * 8 * nb + (i - 4) * 8
+            base = first * 128 + (0 if i < 4 else 256 * 128)
+            for lane in range(64):
+                r = first + (lane >> 3)
+                at = base + lane * 16
+                assert at not in filled
+                filled[at] = (i >= 4, r, (lane & 7) ^ swz(r))
+    assert sorted(filled) == list(range(0, (256 + 64 * nb) * 128, 16))
+    # where the fragment reads look for chunk c of row r
+    for q, rows in ((False, 256), (True, 64 * nb)):
+        for r in range(rows):
+            for c in range(8):
+                assert filled[(256 * 128 if q else 0) + r * 128 + ((c ^ swz(r)) << 4)] == (q, r, c)
     for have in (1, 17, 255, 256, 300):
         lim = min(have, 256) - 1
-        assert max(min(r, lim) for r in p_rows) <= have - 1
+        assert max(min(r, lim) for r in range(256)) <= have - 1
+
+
+def test_fragment_reads_hit_distinct_banks():
+    """64 lanes read 16 rows x chunks c .. c + 3 (c = 0 or 4): the sixteen lanes served
+    together, consecutive or four groups of four, lie in distinct 16-byte groups
+    of the 256-byte bank line."""
+    for c0 in (0, 4):
+        addr = [(l & 15) * 128 + (((c0 + (l >> 4)) ^ swz(l & 15)) << 4) for l in range(64)]
+        groups = [range(16 * g, 16 * g + 16) for g in range(4)]
+        for h in (0, 32):
+            groups.append([h + x for x in list(range(0, 4)) + list(range(12, 16)) + list(range(20, 28))])
+            groups.append([h + x for x in list(range(4, 12)) + list(range(16, 20)) + list(range(28, 32))])
+        for g in groups:
+            assert len({addr[l] // 16 % 16 for l in g}) == 16, (c0, list(g))
+
+
+def test_copy_strides_cover_their_extents():
+    """copy_stride(k) holds k elements and is never a multiple of 4 KB."""
+    assert "k * 2 % 4096 == 0 ? k + 64 : k" in CPP
+    for k in range(64, 70000, 64):
+        ld = k + 64 if k * 2 % 4096 == 0 else k
+        assert ld >= k and ld * 2 % 4096 != 0 and ld * 2 % 128 == 0

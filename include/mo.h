@@ -217,9 +217,9 @@ const char* mo_status_string(mo_status status);
 #define MO_PHASE_HD_PREP    27  /* output head: coefficients, operand copies and transposes */
 #define MO_PHASE_HD_TARGET  28  /* output head: target logits, losses, delta at the targets */
 #define MO_PHASE_HD_LSE     29  /* output head: logits product with its log-sum-exp */
-#define MO_PHASE_HD_DELTA   30  /* output head: logits product with delta */
-#define MO_PHASE_HD_DW      31  /* output head: dW = delta^T H */
-#define MO_PHASE_HD_DH      32  /* output head: dH = delta W */
+#define MO_PHASE_HD_DELTA   30  /* output head: delta of the first piece of the vocabulary */
+#define MO_PHASE_HD_STEP    31  /* output head: dH and dW of a piece, delta of the next */
+#define MO_PHASE_HD_DH      32  /* output head: dH from its fp32 sums */
 #define MO_PHASE_COUNT      33
 
 /* Enable (1) or disable (0) per-launch timing on the calling thread.  While

@@ -31,7 +31,7 @@ PHASES = ["momentum", "norm", "gram", "poly", "update", "apply", "adamw", "copy"
           "sh_layout", "sh_stats", "sh_rootprep", "sh_root", "sh_left", "sh_right",
           "so_prep", "so_stats", "so_solve", "so_apply", "so_sort", "so_products", "so_warm",
           "emb_fwd", "emb_sort", "emb_bwd", "ln_fwd", "ln_bwd",
-          "hd_prep", "hd_target", "hd_lse", "hd_delta", "hd_dw", "hd_dh"]
+          "hd_prep", "hd_target", "hd_lse", "hd_delta", "hd_step", "hd_dh"]
 
 
 class MoError(RuntimeError):

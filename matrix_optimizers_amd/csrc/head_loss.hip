@@ -14,7 +14,7 @@
 // logits are gathered dot products.  Backward: pieces of the vocabulary, each
 // computed again from H and W into delta (bf16, or the three planes of fp32),
 // in both orientations, from which dW's rows are finished and dH accumulated
-// in fp32.  8 N V d flops in all, against 6 N V d when the logits are kept.
+// in fp32; one launch does that for a piece and computes the next one's delta.  8 N V d flops in all, against 6 N V d when the logits are kept.
 //
 // Rounding: the logits are never rounded (fp32 accumulators); delta takes the
 // tensors' own precision (bf16: half a unit in 2^8, the size of the rounding
@@ -315,29 +315,36 @@ __global__ __launch_bounds__(256) void head_distill_prep_kernel(const int64_t* i
 
 // ---- backward: delta of one piece ----------------------------------------------------
 
-// D[plane][token][piece] and DT[plane][vocabulary row][n_pad].
+// One piece's delta: D[plane][token][piece] and DT[plane][vocabulary row][token],
+// both zero for tokens that take no part and rows behind the vocabulary.
+struct DeltaJob {
+    Operand W, H;
+    int nk;
+    uint32_t tm, tn, blocks;
+    float zscale;
+    const float *coef, *nl2;
+    bf16_t *D, *DT;
+    int64_t ldd, plane_d, ldt, plane_t;
+};
 template <int NB, int PL>
-__global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) void head_delta_kernel(
-    Operand W, Operand H, int nk, uint32_t tm, uint32_t tn, float zscale, const float* coef, const float* nl2,
-    bf16_t* D, int64_t ldd, int64_t plane_d, bf16_t* DT, int64_t ldt, int64_t plane_t) {
+__device__ __forceinline__ void delta_tile(uint8_t* smem, const DeltaJob& j, uint32_t block) {
     using L = Layout<NB>;
-    __shared__ __align__(16) uint8_t smem[head_lds(NB)];
     uint32_t ti, tj;
-    if (!head_tile_of(blockIdx.x, tm, tn, ti, tj)) return;
+    if (!head_tile_of(block, j.tm, j.tn, ti, tj)) return;
     const int64_t v0 = int64_t(ti) * 256, n0 = int64_t(tj) * 64 * NB;
     f32x4 acc[L::MB][L::NBW];
-    head_tile<NB, PL>(smem, W, H, v0, n0, 0, nk, acc);
+    head_tile<NB, PL>(smem, j.W, j.H, v0, n0, 0, j.nk, acc);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int wm = wave / L::WN, wn = wave % L::WN, r16 = lane & 15, kg = lane >> 4;
-    const int left = int(W.rows - v0 < 256 ? W.rows - v0 : 256) - wm * (L::MB * 16) - kg * 4;
+    const int left = int(j.W.rows - v0 < 256 ? j.W.rows - v0 : 256) - wm * (L::MB * 16) - kg * 4;
     uint8_t* st = smem + wave * (32 * 64 * 4);
     float c[4], l[4];
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-        c[b] = coef[n0 + wn * 64 + b * 16 + r16];
-        l[b] = nl2[n0 + wn * 64 + b * 16 + r16];
+        c[b] = j.coef[n0 + wn * 64 + b * 16 + r16];
+        l[b] = j.nl2[n0 + wn * 64 + b * 16 + r16];
     }
-    const float k2 = zscale * LOG2E;
+    const float k2 = j.zscale * LOG2E;
     // 32 rows of the wave's sub-tile at a time through its staging slice
 #pragma unroll
     for (int a = 0; a < L::MB; a += 2) {
@@ -356,16 +363,16 @@ __global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) 
             }
         __builtin_amdgcn_wave_barrier();
         const int64_t vrow = v0 + wm * (L::MB * 16) + a * 16, tok = n0 + wn * 64;
-        // token j of the block, 8 vocabulary rows
+        // a token of the block, 8 vocabulary rows
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            const int j = (lane >> 2) + 16 * t, ic = lane & 3;
-            const f32x4 lo = *reinterpret_cast<const f32x4*>(st + st_off(j, ic * 8));
-            const f32x4 hi = *reinterpret_cast<const f32x4*>(st + st_off(j, ic * 8 + 4));
+            const int col = (lane >> 2) + 16 * t, ic = lane & 3;
+            const f32x4 lo = *reinterpret_cast<const f32x4*>(st + st_off(col, ic * 8));
+            const f32x4 hi = *reinterpret_cast<const f32x4*>(st + st_off(col, ic * 8 + 4));
             f32x8 v;
 #pragma unroll
             for (int e = 0; e < 4; ++e) { v.v[e] = lo[e]; v.v[4 + e] = hi[e]; }
-            put_planes<PL>(D + (tok + j) * ldd + vrow + ic * 8, plane_d, v);
+            put_planes<PL>(j.D + (tok + col) * j.ldd + vrow + ic * 8, j.plane_d, v);
         }
         // vocabulary row, 8 tokens
 #pragma unroll
@@ -374,7 +381,7 @@ __global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) 
             f32x8 v;
 #pragma unroll
             for (int e = 0; e < 8; ++e) v.v[e] = *reinterpret_cast<const float*>(st + st_off(cc * 8 + e, row));
-            put_planes<PL>(DT + (vrow + row) * ldt + tok + cc * 8, plane_t, v);
+            put_planes<PL>(j.DT + (vrow + row) * j.ldt + tok + cc * 8, j.plane_t, v);
         }
         __builtin_amdgcn_wave_barrier();
     }
@@ -405,16 +412,23 @@ __global__ __launch_bounds__(256) void head_patch_kernel(const int64_t* ids, int
 // ---- backward: the two products of a piece --------------------------------------------
 
 // dW rows of the piece = DT HT^T (K over the tokens), rounded to T.
+struct DwJob {
+    Operand DT, HT;
+    int nk;
+    uint32_t tm, tn, blocks;
+    void* dW;
+    int64_t ldw;
+    int dim;
+};
 template <typename T, int NB, int PL>
-__global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) void head_dw_kernel(
-    Operand DT, Operand HT, int nk, uint32_t tm, uint32_t tn, T* dW, int64_t ldw, int dim) {
+__device__ __forceinline__ void dw_tile(uint8_t* smem, const DwJob& j, uint32_t block) {
     using L = Layout<NB>;
-    __shared__ __align__(16) uint8_t smem[head_lds(NB)];
     uint32_t ti, tj;
-    if (!head_tile_of(blockIdx.x, tm, tn, ti, tj)) return;
+    if (!head_tile_of(block, j.tm, j.tn, ti, tj)) return;
     const int64_t v0 = int64_t(ti) * 256, c0 = int64_t(tj) * 64 * NB;
     f32x4 acc[L::MB][L::NBW];
-    head_tile<NB, PL>(smem, DT, HT, v0, c0, 0, nk, acc);
+    head_tile<NB, PL>(smem, j.DT, j.HT, v0, c0, 0, j.nk, acc);
+    T* dW = static_cast<T*>(j.dW);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int wm = wave / L::WN, wn = wave % L::WN, r16 = lane & 15, kg = lane >> 4;
     uint8_t* st = smem + wave * (32 * 64 * 4);
@@ -434,7 +448,7 @@ __global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) 
             for (int e = 0; e < 8; ++e) v.v[e] = *reinterpret_cast<const float*>(st + st_off(cc * 8 + e, row));
             const int64_t vr = v0 + wm * (L::MB * 16) + a * 16 + row;
             const int c = int(c0) + wn * 64 + cc * 8;
-            if (vr < DT.rows) st8n(dW + vr * ldw + c, v, dim - c);
+            if (vr < j.DT.rows) st8n(dW + vr * j.ldw + c, v, j.dim - c);
         }
         __builtin_amdgcn_wave_barrier();
     }
@@ -442,42 +456,69 @@ __global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) 
 
 // One split of dH^T += WT D^T over the piece's vocabulary rows: the fp32 tile in
 // accumulator order (lane by lane, 16 bytes each), read and written whole.
+struct DhJob {
+    Operand WT, D;
+    int nk, stages;
+    uint32_t tm, tn, splits, blocks;
+    int first;
+    f32x4* out;
+};
 template <int NB, int PL>
-__global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) void head_dh_kernel(
-    Operand WT, Operand D, int nk, int stages, uint32_t tm, uint32_t tn, uint32_t splits, int first,
-    f32x4* out) {
+__device__ __forceinline__ void dh_tile(uint8_t* smem, const DhJob& j, uint32_t block) {
     using L = Layout<NB>;
-    __shared__ __align__(16) uint8_t smem[head_lds(NB)];
     uint32_t ti, tj;
     // the splits of a tile are rows of tiles: tile row ti of split s is s tm + ti
-    if (!head_tile_of(blockIdx.x, tm * splits, tn, ti, tj)) return;
-    const uint32_t sp = ti / tm;
-    ti -= sp * tm;
-    const int k0 = int(sp) * stages, n = nk - k0 < stages ? nk - k0 : stages;
+    if (!head_tile_of(block, j.tm * j.splits, j.tn, ti, tj)) return;
+    const uint32_t sp = ti / j.tm;
+    ti -= sp * j.tm;
+    const int k0 = int(sp) * j.stages, n = j.nk - k0 < j.stages ? j.nk - k0 : j.stages;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    f32x4* o = out + (((int64_t(sp) * tm + ti) * tn + tj) * 8 + wave) * (L::MB * L::NBW * 64) + lane;
+    f32x4* o = j.out + (((int64_t(sp) * j.tm + ti) * j.tn + tj) * 8 + wave) * (L::MB * L::NBW * 64) + lane;
     if (n <= 0) {
         // a short last piece may leave a split without stages
-        if (first)
+        if (j.first)
 #pragma unroll
             for (int i = 0; i < L::MB * L::NBW; ++i) o[i * 64] = f32x4{0.f, 0.f, 0.f, 0.f};
         return;
     }
     f32x4 acc[L::MB][L::NBW];
-    head_tile<NB, PL>(smem, WT, D, int64_t(ti) * 256, int64_t(tj) * 64 * NB, k0, n, acc);
+    head_tile<NB, PL>(smem, j.WT, j.D, int64_t(ti) * 256, int64_t(tj) * 64 * NB, k0, n, acc);
 #pragma unroll
     for (int a = 0; a < L::MB; ++a)
 #pragma unroll
         for (int b = 0; b < L::NBW; ++b) {
             f32x4* q = o + (a * L::NBW + b) * 64;
             f32x4 v = acc[a][b];
-            if (!first) {
+            if (!j.first) {
                 const f32x4 old = *q;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] += old[e];
             }
             *q = v;
         }
+}
+
+// One launch: dW and dH of a piece and delta of the next one.  The three do not
+// depend on each other (two sets of D, DT and WT), and together they leave one
+// partly filled last round per piece instead of three.  At 8192 tokens x 128256 x
+// 4096: 19.4 ms for the 26 TFLOP of the three, 18.9 in this order with pieces of
+// 84 tiles, 20.1 in three launches of their own; without any store it would be
+// 17.5 (delta's 4 bytes per logit 0.7, the fp32 sums of dH 0.7, dW 0.3).
+template <typename T, int NB, int NBW, int PL>
+__global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) void head_step_kernel(
+    DhJob dh, DwJob dw, DeltaJob dl) {
+    __shared__ __align__(16) uint8_t smem[head_lds(NB > NBW ? NB : NBW)];
+    uint32_t b = blockIdx.x;
+    if (b < dw.blocks) {
+        dw_tile<T, NBW, PL>(smem, dw, b);
+        return;
+    }
+    b -= dw.blocks;
+    if (b < dh.blocks) {
+        dh_tile<NB, PL>(smem, dh, b);
+        return;
+    }
+    delta_tile<NB, PL>(smem, dl, b - dh.blocks);
 }
 
 // dH <- the sum of the splits in order: one workgroup per 16 columns of dH and
@@ -621,9 +662,9 @@ hipError_t mo_launch_head_ht(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* 
               int(a.dim), coef, dst, p.ld_t, a.dim * p.ld_t);
 }
 
-hipError_t mo_launch_head_wt(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int64_t v0, int64_t rows,
+hipError_t mo_launch_head_wt(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int k, int64_t v0, int64_t rows,
                              hipStream_t s) {
-    bf16_t* dst = reinterpret_cast<bf16_t*>(ws + p.off_wt);
+    bf16_t* dst = reinterpret_cast<bf16_t*>(ws + p.off_wt[k & 1]);
     const dim3 grid(unsigned((rows + 255) / 256 * 4), unsigned((a.dim + 63) / 64)), block(256);
     if (p.planes == 1)
         return go(head_transpose_kernel<bf16_t, 1>, grid, block, s, static_cast<const bf16_t*>(a.W) + v0 * a.ldw, a.ldw,
@@ -632,27 +673,12 @@ hipError_t mo_launch_head_wt(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* 
               int(a.dim), static_cast<const float*>(nullptr), dst, p.ld_p, a.dim * p.ld_p);
 }
 
-hipError_t mo_launch_head_delta(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int64_t v0, int64_t rows,
-                                hipStream_t s) {
-    const Operand H = h_operand(a, p, ws), W = w_operand(a, p, ws, v0, rows);
-    const uint32_t tm = uint32_t((rows + 255) / 256), tn = uint32_t(p.n_pad / (64 * p.nb));
-    const dim3 grid(head_grid(uint64_t(tm) * tn)), block(H_THREADS);
-    const float *coef = reinterpret_cast<const float*>(ws + p.off_coef),
-                *nl2 = reinterpret_cast<const float*>(ws + p.off_nl2);
-    bf16_t *D = reinterpret_cast<bf16_t*>(ws + p.off_d), *DT = reinterpret_cast<bf16_t*>(ws + p.off_dt);
-#define MO_CALL(NB, PL)                                                                                      \
-    return go(head_delta_kernel<NB, PL>, grid, block, s, W, H, int(p.kd / 64), tm, tn, a.inv_t, coef, nl2, D, \
-              p.ld_p, p.n_pad * p.ld_p, DT, p.ld_t, p.piece * p.ld_t)
-    MO_HEAD_PICK(p.nb, p.planes, MO_CALL);
-#undef MO_CALL
-}
-
-hipError_t mo_launch_head_patch(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int64_t v0, int64_t rows,
+hipError_t mo_launch_head_patch(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int k, int64_t v0, int64_t rows,
                                 hipStream_t s) {
     const int64_t pairs = a.tokens * a.k;
     const float *coef = reinterpret_cast<const float*>(ws + p.off_coef),
                 *tval = reinterpret_cast<const float*>(ws + p.off_tval);
-    bf16_t *D = reinterpret_cast<bf16_t*>(ws + p.off_d), *DT = reinterpret_cast<bf16_t*>(ws + p.off_dt);
+    bf16_t *D = reinterpret_cast<bf16_t*>(ws + p.off_d[k & 1]), *DT = reinterpret_cast<bf16_t*>(ws + p.off_dt[k & 1]);
     const dim3 grid(cap_grid((pairs + 255) / 256, 1 << 16)), block(256);
     if (p.planes == 1)
         return go(head_patch_kernel<1>, grid, block, s, a.ids, a.ld_ids, a.k, pairs, tval, coef, v0, rows, D, p.ld_p,
@@ -661,37 +687,68 @@ hipError_t mo_launch_head_patch(const MoHeadArgs& a, const MoHeadPlan& p, uint8_
               p.n_pad * p.ld_p, DT, p.ld_t, p.piece * p.ld_t);
 }
 
-hipError_t mo_launch_head_dw(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int64_t v0, int64_t rows,
-                             hipStream_t s) {
-    const Operand DT = rows_of(ws + p.off_dt, p.ld_t, rows, p.piece * p.ld_t);
-    const Operand HT = rows_of(ws + p.off_ht, p.ld_t, a.dim, a.dim * p.ld_t);
-    const uint32_t tm = uint32_t((rows + 255) / 256), tn = uint32_t((a.dim + 64 * p.nb_dw - 1) / (64 * p.nb_dw));
-    const dim3 grid(head_grid(uint64_t(tm) * tn)), block(H_THREADS);
-    const int nk = int(p.n_pad / 64);
-    if (p.planes == 1) {
-        bf16_t* dW = static_cast<bf16_t*>(a.dW) + v0 * a.lddw;
-        if (p.nb_dw == 4) return go(head_dw_kernel<bf16_t, 4, 1>, grid, block, s, DT, HT, nk, tm, tn, dW, a.lddw, int(a.dim));
-        if (p.nb_dw == 2) return go(head_dw_kernel<bf16_t, 2, 1>, grid, block, s, DT, HT, nk, tm, tn, dW, a.lddw, int(a.dim));
-        return go(head_dw_kernel<bf16_t, 1, 1>, grid, block, s, DT, HT, nk, tm, tn, dW, a.lddw, int(a.dim));
+// Piece k (rows from v0 on; rows 0: none) of dH and dW, and delta of piece k + 1
+// (next_rows 0: none).
+hipError_t mo_launch_head_step(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int k, int64_t v0, int64_t rows,
+                               int64_t next_v0, int64_t next_rows, hipStream_t s) {
+    DhJob dh = {};
+    DwJob dw = {};
+    DeltaJob dl = {};
+    const uint32_t tn = uint32_t(p.n_pad / (64 * p.nb)), tm = uint32_t((rows + 255) / 256);
+    if (rows && a.dH) {
+        dh.WT = rows_of(ws + p.off_wt[k & 1], p.ld_p, a.dim, a.dim * p.ld_p);
+        dh.D = rows_of(ws + p.off_d[k & 1], p.ld_p, p.n_pad, p.n_pad * p.ld_p);
+        dh.nk = int(tm * 4);   // the piece's rows, rounded up to whole tiles
+        dh.stages = p.dh_stages;
+        dh.tm = p.dh_tm;
+        dh.tn = p.dh_tn;
+        dh.splits = uint32_t(p.dh_splits);
+        dh.first = k == 0;
+        dh.out = reinterpret_cast<f32x4*>(ws + p.off_acc);
+        dh.blocks = head_grid(uint64_t(dh.tm) * dh.tn * dh.splits);
     }
-    float* dW = static_cast<float*>(a.dW) + v0 * a.lddw;
-    if (p.nb_dw == 4) return go(head_dw_kernel<float, 4, 3>, grid, block, s, DT, HT, nk, tm, tn, dW, a.lddw, int(a.dim));
-    if (p.nb_dw == 2) return go(head_dw_kernel<float, 2, 3>, grid, block, s, DT, HT, nk, tm, tn, dW, a.lddw, int(a.dim));
-    return go(head_dw_kernel<float, 1, 3>, grid, block, s, DT, HT, nk, tm, tn, dW, a.lddw, int(a.dim));
-}
-
-hipError_t mo_launch_head_dh(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, bool first, int64_t rows,
-                             hipStream_t s) {
-    const Operand WT = rows_of(ws + p.off_wt, p.ld_p, a.dim, a.dim * p.ld_p);
-    const Operand D = rows_of(ws + p.off_d, p.ld_p, p.n_pad, p.n_pad * p.ld_p);
-    const int nk = int((rows + 255) / 256 * 4);   // the piece's rows, rounded up to whole tiles
-    const dim3 grid(head_grid(uint64_t(p.dh_tm) * p.dh_tn * p.dh_splits)), block(H_THREADS);
-    f32x4* acc = reinterpret_cast<f32x4*>(ws + p.off_acc);
-#define MO_CALL(NB, PL)                                                                                        \
-    return go(head_dh_kernel<NB, PL>, grid, block, s, WT, D, nk, p.dh_stages, p.dh_tm, p.dh_tn,                \
-              uint32_t(p.dh_splits), first ? 1 : 0, acc)
-    MO_HEAD_PICK(p.nb, p.planes, MO_CALL);
-#undef MO_CALL
+    if (rows && a.dW) {
+        dw.DT = rows_of(ws + p.off_dt[k & 1], p.ld_t, rows, p.piece * p.ld_t);
+        dw.HT = rows_of(ws + p.off_ht, p.ld_t, a.dim, a.dim * p.ld_t);
+        dw.nk = int(p.n_pad / 64);
+        dw.tm = tm;
+        dw.tn = uint32_t((a.dim + 64 * p.nb_dw - 1) / (64 * p.nb_dw));
+        dw.dW = static_cast<uint8_t*>(a.dW) + v0 * a.lddw * (p.planes == 1 ? 2 : 4);
+        dw.ldw = a.lddw;
+        dw.dim = int(a.dim);
+        dw.blocks = head_grid(uint64_t(dw.tm) * dw.tn);
+    }
+    if (next_rows) {
+        const int n = (k + 1) & 1;
+        dl.W = w_operand(a, p, ws, next_v0, next_rows);
+        dl.H = h_operand(a, p, ws);
+        dl.nk = int(p.kd / 64);
+        dl.tm = uint32_t((next_rows + 255) / 256);
+        dl.tn = tn;
+        dl.zscale = a.inv_t;
+        dl.coef = reinterpret_cast<const float*>(ws + p.off_coef);
+        dl.nl2 = reinterpret_cast<const float*>(ws + p.off_nl2);
+        dl.D = reinterpret_cast<bf16_t*>(ws + p.off_d[n]);
+        dl.DT = reinterpret_cast<bf16_t*>(ws + p.off_dt[n]);
+        dl.ldd = p.ld_p;
+        dl.plane_d = p.n_pad * p.ld_p;
+        dl.ldt = p.ld_t;
+        dl.plane_t = p.piece * p.ld_t;
+        dl.blocks = head_grid(uint64_t(dl.tm) * dl.tn);
+    }
+    const dim3 grid(dh.blocks + dw.blocks + dl.blocks), block(H_THREADS);
+#define MO_STEP(T, NB, PL)                                                                             \
+    return p.nb_dw == 4 ? go(head_step_kernel<T, NB, 4, PL>, grid, block, s, dh, dw, dl)               \
+                        : go(head_step_kernel<T, NB, 1, PL>, grid, block, s, dh, dw, dl)
+    if (p.planes == 1) {
+        if (p.nb == 4) MO_STEP(bf16_t, 4, 1);
+        if (p.nb == 2) MO_STEP(bf16_t, 2, 1);
+        MO_STEP(bf16_t, 1, 1);
+    }
+    if (p.nb == 4) MO_STEP(float, 4, 3);
+    if (p.nb == 2) MO_STEP(float, 2, 3);
+    MO_STEP(float, 1, 3);
+#undef MO_STEP
 }
 
 hipError_t mo_launch_head_dh_out(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, hipStream_t s) {

@@ -121,7 +121,10 @@ MoEmbPlan emb_plan(int64_t n, int64_t vocab, int64_t dim) {
 
 constexpr int64_t kHeadMaxTokens = int64_t(1) << 20, kHeadMaxVocab = int64_t(1) << 26,
                   kHeadMaxDim = int64_t(1) << 16;
-constexpr int64_t kHeadPieceBytes = int64_t(768) << 20;
+// Bytes of a piece's copies backward, two sets (a quarter of it forward): more and smaller pieces add
+// launches and passes over dH's sums (0.9 GB 2 % slower at 8192 x 128256 x 4096,
+// 0.5 GB 4 %), larger ones gained nothing.
+constexpr int64_t kHeadPieceBytes = int64_t(1600) << 20;
 
 mo_status head_shape(const mo_head* h, int64_t* ldh, int64_t* ldw) {
     if (!h) return MO_ERR_INVALID_ARG;
@@ -175,36 +178,18 @@ MoHeadPlan head_plan(const MoHeadArgs& a, bool backward, bool need_dh, bool need
     p.kd = k_extent(a.dim);
     p.pack_h = p.planes != 1 || !in_place(a.H, a.ldh, a.dim);
     p.pack_w = p.planes != 1 || !in_place(a.W, a.ldw, a.dim);
-    p.nb_dw = a.dim <= 64 ? 1 : a.dim <= 128 ? 2 : 4;
+    p.nb_dw = a.dim <= 128 ? 1 : 4;
     const int64_t tn = p.n_pad / (64 * p.nb);
-    // pieces bounded by the memory of their copies (and by the grid of one launch);
+    // equal pieces bounded by the memory of their copies (and by the grid of one launch);
     // at least one tile
     int64_t row = p.pack_w ? 2 * p.planes * p.kd : 0;
     // (the same pieces whichever gradients are asked for, so that the size query holds for each)
-    if (backward) row += 4 * p.planes * p.n_pad + 2 * p.planes * a.dim;
+    if (backward) row += 2 * (4 * p.planes * p.n_pad + 2 * p.planes * a.dim);
     int64_t most = std::min<int64_t>((int64_t(1) << 22) / std::max<int64_t>(tn, (a.dim + 63) / 64), 1 << 13);
-    if (row) most = std::min(most, kHeadPieceBytes / row / 256);
+    if (row) most = std::min(most, (backward ? kHeadPieceBytes : kHeadPieceBytes / 4) / row / 256);
     most = std::max<int64_t>(most, 1);
-    // Of the piece sizes from `most` down to half of it (64 tried at most), the one
-    // whose products take the least rounds, each round as long as its K: at 8192
-    // tokens x 128256 x 4096, 64 tiles fill the CUs evenly where 72 leave dW half a round.
-    const int64_t tn_dw = (a.dim + 64 * p.nb_dw - 1) / (64 * p.nb_dw);
-    const int64_t top = std::min(most, p.v_tiles);
-    int64_t best = 0, least = 0;
-    for (int64_t m = top; m >= 1 && 2 * m >= top && top - m < 64; --m) {
-        auto cost = [&](int64_t tiles) {
-            int64_t c = p.kd * tile_cost(p.nb) * rounds(tiles * tn) + 40000;   // 40000: a piece's launches
-            if (backward) c += p.n_pad * tile_cost(p.nb_dw) * rounds(tiles * tn_dw);
-            return c;
-        };
-        const int64_t full = p.v_tiles / m, rest = p.v_tiles - full * m;
-        const int64_t c = full * cost(m) + (rest ? cost(rest) : 0);
-        if (best == 0 || c < least) {
-            least = c;
-            best = m;
-        }
-    }
-    p.piece = best * 256;
+    const int64_t pieces = (p.v_tiles + most - 1) / most;
+    p.piece = (p.v_tiles + pieces - 1) / pieces * 256;
     p.ld_t = copy_stride(p.n_pad);
     p.ld_p = copy_stride(p.piece);
     Carve take;
@@ -216,13 +201,16 @@ MoHeadPlan head_plan(const MoHeadArgs& a, bool backward, bool need_dh, bool need
         p.off_coef = take(uint64_t(4) * p.n_pad);
         p.off_nl2 = take(uint64_t(4) * p.n_pad);
         p.off_tval = take(uint64_t(4) * a.tokens * a.k);
-        p.off_d = take(uint64_t(2) * p.planes * p.n_pad * p.ld_p);
-        p.off_dt = take(uint64_t(2) * p.planes * p.piece * p.ld_t);
+        const int sets = pieces > 1 ? 2 : 1;
+        for (int i = 0; i < sets; ++i) {
+            p.off_d[i] = take(uint64_t(2) * p.planes * p.n_pad * p.ld_p);
+            p.off_dt[i] = take(uint64_t(2) * p.planes * p.piece * p.ld_t);
+            if (need_dh) p.off_wt[i] = take(uint64_t(2) * p.planes * a.dim * p.ld_p);
+        }
         if (need_dw) {
             p.off_ht = take(uint64_t(2) * p.planes * a.dim * p.ld_t);
         }
         if (need_dh) {
-            p.off_wt = take(uint64_t(2) * p.planes * a.dim * p.ld_p);
             p.dh_tm = uint32_t((a.dim + 255) / 256);
             p.dh_tn = uint32_t(tn);
             // splits of K that fill the 256 CUs once, in whole tiles of 256 rows (4 stages)
@@ -334,7 +322,7 @@ mo_status head_backward(MoHeadArgs& a, void* workspace, size_t workspace_bytes, 
     MO_TRY(stride_of(a.lddw, a.dim, &a.lddw));
     if (!a.dH && !a.dW) return MO_OK;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    if (a.tokens == 0) return a.dW ? zero_rows(a.dW, a.vocab, a.dim, a.lddw, a.dtype, MO_PHASE_HD_DW, s) : MO_OK;
+    if (a.tokens == 0) return a.dW ? zero_rows(a.dW, a.vocab, a.dim, a.lddw, a.dtype, MO_PHASE_HD_STEP, s) : MO_OK;
     if (!a.H || !a.W || !a.ids || !a.lse_in || !a.dloss) return MO_ERR_INVALID_ARG;
     if (distill ? (!a.teacher || !a.z_in) : !a.loss_in) return MO_ERR_INVALID_ARG;
     const MoHeadPlan p = head_plan(a, true, a.dH != nullptr, a.dW != nullptr);
@@ -353,14 +341,18 @@ mo_status head_backward(MoHeadArgs& a, void* workspace, size_t workspace_bytes, 
     MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_prep(a, p, ws, s));
     if (p.pack_h) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_pack(a, p, ws, true, 0, a.tokens, s));
     if (a.dW) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_ht(a, p, ws, s));
-    for (int64_t v0 = 0; v0 < a.vocab; v0 += p.piece) {
-        const int64_t rows = std::min(p.piece, a.vocab - v0);
-        if (p.pack_w) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_pack(a, p, ws, false, v0, rows, s));
-        if (a.dH) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_wt(a, p, ws, v0, rows, s));
-        MO_RUN(MO_PHASE_HD_DELTA, mo_launch_head_delta(a, p, ws, v0, rows, s));
-        MO_RUN(MO_PHASE_HD_TARGET, mo_launch_head_patch(a, p, ws, v0, rows, s));
-        if (a.dW) MO_RUN(MO_PHASE_HD_DW, mo_launch_head_dw(a, p, ws, v0, rows, s));
-        if (a.dH) MO_RUN(MO_PHASE_HD_DH, mo_launch_head_dh(a, p, ws, v0 == 0, rows, s));
+    // turn k: delta of piece k beside dH and dW of piece k - 1
+    const int pieces = int((a.vocab + p.piece - 1) / p.piece);
+    for (int k = 0; k <= pieces; ++k) {
+        const int64_t v0 = k * p.piece, rows = k < pieces ? std::min(p.piece, a.vocab - v0) : 0;
+        if (rows) {
+            if (p.pack_w) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_pack(a, p, ws, false, v0, rows, s));
+            if (a.dH) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_wt(a, p, ws, k, v0, rows, s));
+        }
+        MO_RUN(k == 0 ? MO_PHASE_HD_DELTA : MO_PHASE_HD_STEP,
+               mo_launch_head_step(a, p, ws, k - 1, v0 - p.piece, k ? std::min(p.piece, a.vocab - (v0 - p.piece)) : 0,
+                                   v0, rows, s));
+        if (rows) MO_RUN(MO_PHASE_HD_TARGET, mo_launch_head_patch(a, p, ws, k, v0, rows, s));
     }
     if (a.dH) MO_RUN(MO_PHASE_HD_DH, mo_launch_head_dh_out(a, p, ws, s));
     return MO_OK;

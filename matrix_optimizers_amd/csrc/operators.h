@@ -81,7 +81,7 @@ struct MoHeadPlan {
     // dH: K stages per split, number of splits, tiles of 256 (dim) x 64 nb
     int dh_stages, dh_splits;
     uint32_t dh_tm, dh_tn;
-    uint64_t off_part, off_hp, off_wp, off_coef, off_nl2, off_tval, off_ht, off_wt, off_d, off_dt, off_acc;
+    uint64_t off_part, off_hp, off_wp, off_coef, off_nl2, off_tval, off_ht, off_wt[2], off_d[2], off_dt[2], off_acc;
     uint64_t bytes;
 };
 hipError_t mo_launch_head_pack(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, bool h, int64_t v0,
@@ -92,14 +92,11 @@ hipError_t mo_launch_head_targets(const MoHeadArgs& a, hipStream_t s);
 hipError_t mo_launch_head_loss(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, hipStream_t s);
 hipError_t mo_launch_head_prep(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, hipStream_t s);
 hipError_t mo_launch_head_ht(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, hipStream_t s);
-hipError_t mo_launch_head_wt(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int64_t v0, int64_t rows,
+// k: the piece's number (two sets of piece buffers, used in turn)
+hipError_t mo_launch_head_wt(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int k, int64_t v0, int64_t rows,
                              hipStream_t s);
-hipError_t mo_launch_head_delta(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int64_t v0, int64_t rows,
+hipError_t mo_launch_head_patch(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int k, int64_t v0, int64_t rows,
                                 hipStream_t s);
-hipError_t mo_launch_head_patch(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int64_t v0, int64_t rows,
-                                hipStream_t s);
-hipError_t mo_launch_head_dw(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int64_t v0, int64_t rows,
-                             hipStream_t s);
-hipError_t mo_launch_head_dh(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, bool first, int64_t rows,
-                             hipStream_t s);
+hipError_t mo_launch_head_step(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int k, int64_t v0, int64_t rows,
+                               int64_t next_v0, int64_t next_rows, hipStream_t s);
 hipError_t mo_launch_head_dh_out(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, hipStream_t s);

@@ -88,34 +88,48 @@ class _On:
     allocates with the launch stream current (so that the caching allocator
     hands a freed block out again only in that stream's order)."""
 
+    __slots__ = ("dev", "stream", "guards", "handle")
+
     def __init__(self, dev, stream):
-        self.dev, self.stream = dev, stream
-        self.guards = []
+        self.dev, self.stream, self.guards = dev, stream, ()
 
     def __enter__(self):
         dev, stream = self.dev, self.stream
         if torch.cuda.current_device() != dev.index:
-            self.guards.append(torch.cuda.device(dev))
-            self.guards[-1].__enter__()
+            self._guard(torch.cuda.device(dev))
         if stream is None:
-            self.handle = torch.cuda.current_stream(dev).cuda_stream
-        else:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(B._stream_handle(stream), device=dev)
-            elif stream.device != dev:
-                self.__exit__()
-                raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-            self.handle = stream.cuda_stream
-            self.guards.append(torch.cuda.stream(stream))
-            self.guards[-1].__enter__()
+            # the handle alone: building a Stream object costs as much as the rest of a small call
+            self.handle = torch._C._cuda_getCurrentRawStream(dev.index)
+            return self
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(B._stream_handle(stream), device=dev)
+        elif stream.device != dev:
+            self.__exit__()
+            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+        self.handle = stream.cuda_stream
+        self._guard(torch.cuda.stream(stream))
         return self
+
+    def _guard(self, g):
+        self.guards += (g,)
+        g.__enter__()
 
     def __exit__(self, *exc):
         while self.guards:
-            self.guards.pop().__exit__(None, None, None)
+            g, self.guards = self.guards[-1], self.guards[:-1]
+            g.__exit__(None, None, None)
 
-    def empty(self, shape, dtype):
-        return torch.empty(shape, dtype=dtype, device=self.dev)
+    def matrix(self, t, what, rows, cols, dtype):
+        """(t, row stride): the caller's matrix, checked, or a new one."""
+        if t is None:
+            return torch.empty((rows, cols), dtype=dtype, device=self.dev), 0
+        return t, _matrix(t, what, rows, cols, dtype)
+
+    def vector(self, t, what, n):
+        if t is None:
+            return torch.empty(n, dtype=torch.float32, device=self.dev)
+        _vector(t, what, n)
+        return t
 
     def workspace(self, workspace, need: int):
         """(address, bytes, the tensor to keep until the launch)."""
@@ -144,9 +158,7 @@ def embedding_forward(tokens, W, *, scale: float = 1.0, out=None, stream=None):
     vocab, dim = W.shape
     code = _code(W, "W")
     with _On(dev, stream) as on:
-        if out is None:
-            out = on.empty((n, dim), W.dtype)
-        ldy = _matrix(out, "out", n, dim, W.dtype)
+        out, ldy = on.matrix(out, "out", n, dim, W.dtype)
         _check(lib.embedding_forward(_ptr(tokens), n, _ptr(W), ldw, vocab, dim, code, scale, _ptr(out), ldy,
                                      on.handle), "embedding_forward")
     return out
@@ -198,15 +210,8 @@ def layer_norm_forward(X, weight=None, bias=None, *, eps: float = 1e-5, out=None
     if bias is not None:
         _vector(bias, "bias", cols)
     with _On(dev, stream) as on:
-        if out is None:
-            out = on.empty((rows, cols), X.dtype)
-        if mean is None:
-            mean = on.empty(rows, torch.float32)
-        if rstd is None:
-            rstd = on.empty(rows, torch.float32)
-        ldy = _matrix(out, "out", rows, cols, X.dtype)
-        _vector(mean, "mean", rows)
-        _vector(rstd, "rstd", rows)
+        out, ldy = on.matrix(out, "out", rows, cols, X.dtype)
+        mean, rstd = on.vector(mean, "mean", rows), on.vector(rstd, "rstd", rows)
         _check(lib.layer_norm_forward(_ptr(X), ldx, _ptr(weight), _ptr(bias), _ptr(out), ldy, _ptr(mean),
                                       _ptr(rstd), rows, cols, code, eps, on.handle), "layer_norm_forward")
     return out, mean, rstd
@@ -236,19 +241,10 @@ def layer_norm_backward(dY, X, mean, rstd, weight=None, *, dX=None, dweight=None
         _vector(weight, "weight", cols)
     need = layer_norm_workspace_bytes(rows, cols) if need_dweight or need_dbias else 0
     with _On(dev, stream) as on:
-        if dX is None and need_dX:
-            dX = on.empty((rows, cols), X.dtype)
-        if dweight is None and need_dweight:
-            dweight = on.empty(cols, torch.float32)
-        if dbias is None and need_dbias:
-            dbias = on.empty(cols, torch.float32)
-        lddx = _matrix(dX, "dX", rows, cols, X.dtype) if need_dX else 0
-        if need_dweight:
-            _vector(dweight, "dweight", cols)
-        if need_dbias:
-            _vector(dbias, "dbias", cols)
+        dX, lddx = on.matrix(dX, "dX", rows, cols, X.dtype) if need_dX else (None, 0)
+        out = (dX, on.vector(dweight, "dweight", cols) if need_dweight else None,
+               on.vector(dbias, "dbias", cols) if need_dbias else None)
         ws, have, keep = on.workspace(workspace, need)
-        out = (dX if need_dX else None, dweight if need_dweight else None, dbias if need_dbias else None)
         _check(lib.layer_norm_backward(_ptr(dY), ldy, _ptr(X), ldx, _ptr(weight), _ptr(mean), _ptr(rstd),
                                        _ptr(out[0]), lddx, _ptr(out[1]), _ptr(out[2]), rows, cols, code, ws, have,
                                        on.handle), "layer_norm_backward")
@@ -302,10 +298,7 @@ def softmax_xent_forward(H, W, labels, *, loss=None, lse=None, workspace=None, s
     n = H.shape[0]
     _vector(labels, "labels", n, torch.int64)
     with _On(dev, stream) as on:
-        loss = on.empty(n, torch.float32) if loss is None else loss
-        lse = on.empty(n, torch.float32) if lse is None else lse
-        _vector(loss, "loss", n)
-        _vector(lse, "lse", n)
+        loss, lse = on.vector(loss, "loss", n), on.vector(lse, "lse", n)
         need = softmax_xent_workspace_bytes(H, W) if workspace is None else 0
         ws, have, keep = on.workspace(workspace, need)
         _check(lib.softmax_xent_forward(ctypes.byref(head), _ptr(labels), _ptr(loss), _ptr(lse), ws, have,
@@ -315,13 +308,8 @@ def softmax_xent_forward(H, W, labels, *, loss=None, lse=None, workspace=None, s
 
 
 def _grads(on, H, W, dH, dW, need_dH, need_dW):
-    if dH is None and need_dH:
-        dH = on.empty(tuple(H.shape), H.dtype)
-    if dW is None and need_dW:
-        dW = on.empty(tuple(W.shape), W.dtype)
-    dH, dW = dH if need_dH else None, dW if need_dW else None
-    ldh = _matrix(dH, "dH", H.shape[0], H.shape[1], H.dtype) if need_dH else 0
-    ldw = _matrix(dW, "dW", W.shape[0], W.shape[1], W.dtype) if need_dW else 0
+    dH, ldh = on.matrix(dH, "dH", H.shape[0], H.shape[1], H.dtype) if need_dH else (None, 0)
+    dW, ldw = on.matrix(dW, "dW", W.shape[0], W.shape[1], W.dtype) if need_dW else (None, 0)
     return dH, ldh, dW, ldw
 
 
@@ -360,12 +348,9 @@ def topk_distill_forward(H, W, ids, logits, *, temperature: float = 1.0, loss=No
     head, top = _head(H, W), _topk(H, ids, logits, temperature)
     n, k = ids.shape
     with _On(dev, stream) as on:
-        loss = on.empty(n, torch.float32) if loss is None else loss
-        lse = on.empty(n, torch.float32) if lse is None else lse
-        z = on.empty((n, k), torch.float32) if z is None else z
-        _vector(loss, "loss", n)
-        _vector(lse, "lse", n)
-        _contiguous(z, n, k)
+        loss, lse = on.vector(loss, "loss", n), on.vector(lse, "lse", n)
+        z, _ = on.matrix(z, "z", n, k, torch.float32)
+        _contiguous(z)
         need = topk_distill_workspace_bytes(H, W, ids, logits, temperature=temperature) if workspace is None else 0
         ws, have, keep = on.workspace(workspace, need)
         _check(lib.topk_distill_forward(ctypes.byref(head), ctypes.byref(top), _ptr(loss), _ptr(lse), _ptr(z), ws,
@@ -374,8 +359,7 @@ def topk_distill_forward(H, W, ids, logits, *, temperature: float = 1.0, loss=No
     return loss, lse, z
 
 
-def _contiguous(z, n: int, k: int) -> None:
-    _matrix(z, "z", n, k, torch.float32)
+def _contiguous(z) -> None:
     if not z.is_contiguous():
         raise ValueError("z must be contiguous")
 
@@ -389,7 +373,8 @@ def topk_distill_backward(H, W, ids, logits, lse, z, dloss, *, temperature: floa
     n, k = ids.shape
     _vector(lse, "lse", n)
     _vector(dloss, "dloss", n)
-    _contiguous(z, n, k)
+    _matrix(z, "z", n, k, torch.float32)
+    _contiguous(z)
     with _On(dev, stream) as on:
         dH, ldh, dW, ldw = _grads(on, H, W, dH, dW, need_dH, need_dW)
         need = topk_distill_workspace_bytes(H, W, ids, logits, temperature=temperature, backward=True) \

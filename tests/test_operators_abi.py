@@ -212,12 +212,14 @@ def bytes_of(back, **kw):
 
 def test_the_logits_are_never_kept():
     """Workspaces at 8192 tokens x 128256 x 4096: far below one bf16 copy of the
-    logits (2.1 GB) forward, and bounded backward."""
+    logits (2.1 GB) forward, and bounded backward (a vocabulary four times as
+    long takes no more)."""
     big = dict(tokens=8192, vocab=128256, dim=4096)
     assert bytes_of(0, **big) < 40 << 20
-    assert bytes_of(1, **big) < 1200 << 20
+    assert bytes_of(1, **big) < 1900 << 20
+    assert bytes_of(1, tokens=8192, vocab=4 * 128256, dim=4096) < 1900 << 20
     # a misaligned or strided head is copied in pieces, not whole
-    assert bytes_of(0, W=A[1] + 2, **big) < 900 << 20
+    assert bytes_of(0, W=A[1] + 2, **big) < 500 << 20
 
 
 # ---- the binding's checks --------------------------------------------------------------

@@ -199,5 +199,5 @@ def test_phases_are_timed(gpu):
     finally:
         mo.profile_enable(False)
     for name in ("emb_fwd", "emb_sort", "emb_bwd", "ln_fwd", "ln_bwd", "hd_prep", "hd_target", "hd_lse", "hd_delta",
-                 "hd_dw", "hd_dh"):
+                 "hd_step", "hd_dh"):
         assert got[name][1] > 0 and got[name][0] > 0, name

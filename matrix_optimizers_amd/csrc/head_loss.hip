@@ -6,15 +6,23 @@
 //   cross entropy (T = 1)  loss_n = lse_n - z_ny
 //   distillation           p = softmax(t / T) over the stored entries,
 //                          loss_n = T^2 sum_k p_k (log p_k - (z_k / T - lse_n))
-//   delta_nv = c_n (exp(z_nv / T - lse_n) - p_nv),  c_n = T dloss_n
-//   dH = delta W,  dW = delta^T H
+//   delta_nv = c_n (exp(z_nv / T - lse_n) - p_nv),  c_n = T dloss_n / r
+//   dH = r delta W,  dW = r delta^T H
+//
+// r is the significand, in [1, 2), of one row's T |dloss| (ref_scale below): with
+// the usual mean over rows every c_n is a power of two, and the label's delta,
+// -(1 - p), the largest of its row, is rounded like that number.  Rounded as
+// -(1 - p) / count it would carry nearly the same mantissa, and the same error of up
+// to half a unit, in every row: at 8192 tokens x 128256 x 4096 bf16 the error of dH
+// was 3.0e-3 of its norm; it is 2.0e-3, against 1.7e-3 for the result's rounding alone.
 //
 // Forward: one product whose epilogue keeps, per tile and token, the maximum
 // and the sum of exponentials over the tile's 256 vocabulary rows; the target
 // logits are gathered dot products.  Backward: pieces of the vocabulary, each
 // computed again from H and W into delta (bf16, or the three planes of fp32),
 // in both orientations, from which dW's rows are finished and dH accumulated
-// in fp32; one launch does that for a piece and computes the next one's delta.  8 N V d flops in all, against 6 N V d when the logits are kept.
+// in fp32; one launch does that for a piece and computes the next one's delta.
+// 8 N V d flops in all, against 6 N V d when the logits are kept.
 //
 // Rounding: the logits are never rounded (fp32 accumulators); delta takes the
 // tensors' own precision (bf16: half a unit in 2^8, the size of the rounding
@@ -63,33 +71,47 @@ __global__ __launch_bounds__(256) void head_pack_kernel(const T* src, int64_t ld
     }
 }
 
-// dst[plane][c][ldt] <- src[r][c] for the 64 x 64 tile (blockIdx.x over rows,
-// blockIdx.y over columns); rows from `rows` to 64 * gridDim.x are zero, and so
-// are the rows whose coefficient is 0 (they may hold anything).
+// dst[plane][c][ldt] <- src[r][c] in 64 x 64 tiles; rows from `rows` up to 64 tr are
+// zero, and so are the rows whose coefficient is 0 (they may hold anything).  With
+// `packed` the rows as read go there too (head_pack_kernel's layout), so that a
+// piece of fp32 W is read once for both.  The tiles are taken in blocks of 8 x 8:
+// workgroups that run together then read whole 1 KB pieces of rows and write
+// whole 1 KB pieces of columns (131 MB of bf16 with its transpose: 45 us tile row by
+// tile row).
 template <typename T, int PL>
 __global__ __launch_bounds__(256) void head_transpose_kernel(const T* src, int64_t ld, int64_t rows, int dim,
                                                              const float* coef, bf16_t* dst, int64_t ldt,
-                                                             int64_t plane) {
+                                                             int64_t plane, uint32_t tr, uint32_t tc,
+                                                             bf16_t* packed, int kd, int64_t packed_plane) {
     __shared__ float tile[64][65];
-    const int64_t r0 = int64_t(blockIdx.x) * 64;
-    const int c0 = blockIdx.y * 64;
+    const uint32_t blocks_r = (tr + 7) / 8, blk = blockIdx.x >> 6;
+    const uint32_t ti = blk % blocks_r * 8 + (blockIdx.x & 7), tj = blk / blocks_r * 8 + (blockIdx.x >> 3 & 7);
+    if (ti >= tr || tj >= tc) return;
+    const int64_t r0 = int64_t(ti) * 64;
+    const int c0 = int(tj) * 64;
+    f32x8 v[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int q = threadIdx.x + 256 * i, r = q >> 3, c = (q & 7) * 8;
         const bool on = r0 + r < rows && (!coef || coef[r0 + r] != 0.f);
-        const f32x8 v = widen(ld8n(src + (r0 + r) * ld + c0 + c, on ? dim - c0 - c : 0));
+        v[i] = widen(ld8n(src + (r0 + r) * ld + c0 + c, on ? dim - c0 - c : 0));
+    }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) tile[r][c + e] = v.v[e];
+    for (int i = 0; i < 2; ++i) {
+        const int q = threadIdx.x + 256 * i, r = q >> 3, c = (q & 7) * 8;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) tile[r][c + e] = v[i].v[e];
+        if (packed && r0 + r < rows) put_planes<PL>(packed + (r0 + r) * kd + c0 + c, packed_plane, v[i]);
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int q = threadIdx.x + 256 * i, c = q >> 3, r = (q & 7) * 8;
         if (c0 + c >= dim) continue;
-        f32x8 v;
+        f32x8 o;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v.v[e] = tile[r + e][c];
-        put_planes<PL>(dst + int64_t(c0 + c) * ldt + r0 + r, plane, v);
+        for (int e = 0; e < 8; ++e) o.v[e] = tile[r + e][c];
+        put_planes<PL>(dst + int64_t(c0 + c) * ldt + r0 + r, plane, o);
     }
 }
 
@@ -148,38 +170,59 @@ __global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) 
 }
 
 // z[n][j] = H_n . W_id (not yet divided by T), 0 where the id is outside the
-// vocabulary: one wavefront per pair.
-template <typename T>
+// vocabulary: one wavefront per token and G of its ids, whose rows it requests
+// together (G = 8 at 4096 tokens x 64 ids x 2048: 165 us with one id per wavefront).
+template <typename T, int G>
 __global__ __launch_bounds__(256) void head_target_kernel(const T* H, int64_t ldh, const T* W, int64_t ldw,
                                                           const int64_t* ids, int64_t ld_ids, int k,
-                                                          int64_t pairs, int64_t vocab, int dim, float* z) {
-    const int lane = threadIdx.x & 63;
-    for (int64_t i = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6); i < pairs; i += int64_t(gridDim.x) * 4) {
-        const int64_t n = i / k, id = ids[n * ld_ids + (i - n * k)];
-        float s = 0.f;
-        if (uint64_t(id) < uint64_t(vocab)) {
-            const T *h = H + n * ldh, *w = W + id * ldw;
-            for (int c = lane * 8; c < dim; c += 512) {
-                const f32x8 a = widen(ld8n(h + c, dim - c)), b = widen(ld8n(w + c, dim - c));
+                                                          int64_t tokens, int64_t vocab, int dim, float* z) {
+    const int lane = threadIdx.x & 63, groups = (k + G - 1) / G;
+    const int64_t items = tokens * groups;
+    for (int64_t it = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6); it < items; it += int64_t(gridDim.x) * 4) {
+        const int64_t n = it / groups;
+        const int j0 = int(it - n * groups) * G;
+        const T* w[G];
+        bool in[G], any = false;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) s = __builtin_fmaf(a.v[e], b.v[e], s);
-            }
-            s = wave_sum(s);
+        for (int g = 0; g < G; ++g) {
+            const int64_t id = j0 + g < k ? ids[n * ld_ids + j0 + g] : -1;
+            in[g] = uint64_t(id) < uint64_t(vocab);
+            any |= in[g];
+            w[g] = W + (in[g] ? id : 0) * ldw;   // row 0 stands in for an absent one, not used
         }
-        if (lane == 0) z[i] = s;
+        float s[G];
+#pragma unroll
+        for (int g = 0; g < G; ++g) s[g] = 0.f;
+        if (any)
+            for (int c = lane * 8; c < dim; c += 512) {
+                const f32x8 a = widen(ld8n(H + n * ldh + c, dim - c));
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const f32x8 b = widen(ld8n(w[g] + c, dim - c));
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) s[g] = __builtin_fmaf(a.v[e], b.v[e], s[g]);
+                }
+            }
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const float t = wave_sum(s[g]);
+            if (lane == 0 && j0 + g < k) z[n * k + j0 + g] = in[g] ? t : 0.f;
+        }
     }
 }
 
 // log2-domain partial sums of 32 tokens -> lse (natural log), 32 strided shares
-// of the vocabulary tiles per token, combined in order.  Cross entropy's loss
-// comes with it; z holds the label's logit.
+// of the vocabulary tiles per token, combined in order.  Cross entropy (labels):
+// the label's logit, a dot product per token (two per wavefront), and the loss.
+template <typename T>
 __global__ __launch_bounds__(1024) void head_combine_kernel(const float2* part, int64_t n_pad, int64_t v_tiles,
                                                             int64_t tokens, const int64_t* labels,
-                                                            int64_t vocab, const float* z, float* loss,
-                                                            float* lse) {
+                                                            int64_t vocab, const T* H, int64_t ldh, const T* W,
+                                                            int64_t ldw, int dim, float* loss, float* lse) {
     __shared__ float2 sh[32][33];
+    __shared__ float zl[32];
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const int64_t n = int64_t(blockIdx.x) * 32 + tx;
+    const int64_t n0 = int64_t(blockIdx.x) * 32, n = n0 + tx;
     float m = -__builtin_inff(), s = 0.f;
     if (n < tokens)
         for (int64_t t = ty; t < v_tiles; t += 32) {
@@ -189,6 +232,23 @@ __global__ __launch_bounds__(1024) void head_combine_kernel(const float2* part, 
             m = mn;
         }
     sh[ty][tx] = float2{m, s};
+    if (labels) {
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int j = int(threadIdx.x >> 6) * 2 + i;
+            const int64_t y = n0 + j < tokens ? labels[n0 + j] : -1;
+            float z = 0.f;
+            if (uint64_t(y) < uint64_t(vocab))
+                for (int c = lane * 8; c < dim; c += 512) {
+                    const f32x8 a = widen(ld8n(H + (n0 + j) * ldh + c, dim - c)), b = widen(ld8n(W + y * ldw + c, dim - c));
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) z = __builtin_fmaf(a.v[e], b.v[e], z);
+                }
+            z = wave_sum(z);
+            if (lane == 0) zl[j] = z;
+        }
+    }
     __syncthreads();
     if (ty == 0 && n < tokens) {
         for (int t = 1; t < 32; ++t) m = fmaxf(m, sh[t][tx].x);
@@ -198,7 +258,7 @@ __global__ __launch_bounds__(1024) void head_combine_kernel(const float2* part, 
         float l = m * LN2 + logf(s);
         if (labels) {
             const bool in = uint64_t(labels[n]) < uint64_t(vocab);
-            loss[n] = in ? l - z[n] : 0.f;
+            loss[n] = in ? l - zl[tx] : 0.f;
             l = in ? l : 0.f;
         }
         lse[n] = l;
@@ -256,17 +316,38 @@ __global__ __launch_bounds__(256) void head_distill_loss_kernel(const int64_t* i
 
 // ---- backward: per-token coefficients ------------------------------------------------
 
-// coef[n] = T dloss_n (0: the row takes no part), nl2[n] = -lse_n log2 e, and
-// delta at the label, c (exp(z_y - lse) - 1) = c expm1(-loss).
+// The scale r: the significand of T times the largest finite |dloss| in the first 64
+// rows that hold one other than 0 (1 if none does).  Only the significand: c_n keeps
+// the range of dloss.  Every wavefront computes the same.
+MO_DEV float ref_scale(const float* dloss, int64_t tokens, float t) {
+    for (int64_t n0 = 0; n0 < tokens; n0 += 64) {
+        const int64_t n = n0 + (threadIdx.x & 63);
+        float m = n < tokens ? __builtin_fabsf(dloss[n]) * t : 0.f;
+        if (!(m < __builtin_inff())) m = 0.f;
+#pragma unroll
+        for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+        if (m > 0.f) {
+            int e;
+            return 2.f * frexpf(m, &e);
+        }
+    }
+    return 1.f;
+}
+
+// coef[n] = T dloss_n / r (0: the row takes no part), nl2[n] = -lse_n log2 e, delta at
+// the label, c (exp(z_y - lse) - 1) = c expm1(-loss), and r itself.
 __global__ __launch_bounds__(256) void head_xent_prep_kernel(const int64_t* labels, const float* loss,
                                                              const float* lse, const float* dloss,
                                                              int64_t tokens, int64_t n_pad, int64_t vocab,
-                                                             float* coef, float* nl2, float* tval) {
+                                                             float* coef, float* nl2, float* tval,
+                                                             float* ref) {
+    const float r = ref_scale(dloss, tokens, 1.f);
     const int64_t n = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    if (n == 0) *ref = r;
     if (n >= n_pad) return;
     float c = 0.f, l = 0.f;
     if (n < tokens && uint64_t(labels[n]) < uint64_t(vocab)) {
-        c = dloss[n];
+        c = dloss[n] / r;
         l = -lse[n] * LOG2E;
     }
     coef[n] = c;
@@ -282,9 +363,11 @@ __global__ __launch_bounds__(256) void head_distill_prep_kernel(const int64_t* i
                                                                 int64_t vocab, float inv_t, float t,
                                                                 const float* z, const float* lse,
                                                                 const float* dloss, float* coef, float* nl2,
-                                                                float* tval) {
+                                                                float* tval, float* ref) {
+    const float r = ref_scale(dloss, tokens, t);
     const int lane = threadIdx.x & 63;
     const int64_t n = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
+    if (n == 0 && lane == 0) *ref = r;
     if (n >= n_pad) return;
     float c = 0.f, l = 0.f;
     if (n < tokens) {
@@ -292,7 +375,7 @@ __global__ __launch_bounds__(256) void head_distill_prep_kernel(const int64_t* i
         const uint8_t* te = static_cast<const uint8_t*>(teacher) + n * ld_t * (t_bf16 ? 2 : 4);
         float mt, st;
         if (teacher_row(id, te, t_bf16, k, vocab, inv_t, mt, st)) {
-            c = t * dloss[n];
+            c = t * dloss[n] / r;
             l = lse[n];
         }
         for (int j = lane; j < k; j += 64) {
@@ -411,7 +494,7 @@ __global__ __launch_bounds__(256) void head_patch_kernel(const int64_t* ids, int
 
 // ---- backward: the two products of a piece --------------------------------------------
 
-// dW rows of the piece = DT HT^T (K over the tokens), rounded to T.
+// dW rows of the piece = r DT HT^T (K over the tokens), rounded to T.
 struct DwJob {
     Operand DT, HT;
     int nk;
@@ -419,6 +502,7 @@ struct DwJob {
     void* dW;
     int64_t ldw;
     int dim;
+    const float* ref;
 };
 template <typename T, int NB, int PL>
 __device__ __forceinline__ void dw_tile(uint8_t* smem, const DwJob& j, uint32_t block) {
@@ -429,6 +513,7 @@ __device__ __forceinline__ void dw_tile(uint8_t* smem, const DwJob& j, uint32_t 
     f32x4 acc[L::MB][L::NBW];
     head_tile<NB, PL>(smem, j.DT, j.HT, v0, c0, 0, j.nk, acc);
     T* dW = static_cast<T*>(j.dW);
+    const float r = *j.ref;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int wm = wave / L::WN, wn = wave % L::WN, r16 = lane & 15, kg = lane >> 4;
     uint8_t* st = smem + wave * (32 * 64 * 4);
@@ -445,7 +530,7 @@ __device__ __forceinline__ void dw_tile(uint8_t* smem, const DwJob& j, uint32_t 
             const int cc = lane & 7, row = (lane >> 3) + 8 * t;
             f32x8 v;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v.v[e] = *reinterpret_cast<const float*>(st + st_off(cc * 8 + e, row));
+            for (int e = 0; e < 8; ++e) v.v[e] = r * *reinterpret_cast<const float*>(st + st_off(cc * 8 + e, row));
             const int64_t vr = v0 + wm * (L::MB * 16) + a * 16 + row;
             const int c = int(c0) + wn * 64 + cc * 8;
             if (vr < j.DT.rows) st8n(dW + vr * j.ldw + c, v, j.dim - c);
@@ -521,12 +606,12 @@ __global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) 
     delta_tile<NB, PL>(smem, dl, b - dh.blocks);
 }
 
-// dH <- the sum of the splits in order: one workgroup per 16 columns of dH and
+// dH <- r times the sum of the splits in order: one workgroup per 16 columns of dH and
 // the 64 tokens of a wave's block, turned through LDS.  Tokens that take no part
 // get zeros.
 template <typename T, int NB>
 __global__ __launch_bounds__(256) void head_dh_out_kernel(const f32x4* acc, uint32_t tm, uint32_t tn,
-                                                          uint32_t splits, const float* coef, T* dH,
+                                                          uint32_t splits, const float* coef, const float* ref, T* dH,
                                                           int64_t ld, int64_t tokens, int dim) {
     using L = Layout<NB>;
     __shared__ float tile[64][20];
@@ -551,9 +636,10 @@ __global__ __launch_bounds__(256) void head_dh_out_kernel(const f32x4* acc, uint
         const int j = threadIdx.x >> 1, c = (threadIdx.x & 1) * 8;
         if (n0 + j < tokens && c0 + c < dim) {
             const bool on = coef[n0 + j] != 0.f;
+            const float r = *ref;
             f32x8 o;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o.v[e] = on ? tile[j][c + e] : 0.f;
+            for (int e = 0; e < 8; ++e) o.v[e] = on ? r * tile[j][c + e] : 0.f;
             st8n(dH + (n0 + j) * ld + c0 + c, o, dim - c0 - c);
         }
     }
@@ -621,19 +707,28 @@ hipError_t mo_launch_head_lse(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t*
 }
 
 hipError_t mo_launch_head_targets(const MoHeadArgs& a, hipStream_t s) {
-    const int64_t pairs = a.tokens * a.k;
-    const dim3 grid(cap_grid((pairs + 3) / 4, 1 << 20)), block(256);
-    if (a.dtype == MO_BF16)
-        return go(head_target_kernel<bf16_t>, grid, block, s, static_cast<const bf16_t*>(a.H), a.ldh,
-                  static_cast<const bf16_t*>(a.W), a.ldw, a.ids, a.ld_ids, a.k, pairs, a.vocab, int(a.dim), a.z);
-    return go(head_target_kernel<float>, grid, block, s, static_cast<const float*>(a.H), a.ldh,
-              static_cast<const float*>(a.W), a.ldw, a.ids, a.ld_ids, a.k, pairs, a.vocab, int(a.dim), a.z);
+    const int G = a.k >= 4 ? 8 : 1;
+    const dim3 grid(cap_grid((a.tokens * ((a.k + G - 1) / G) + 3) / 4, 1 << 20)), block(256);
+    if (a.dtype == MO_BF16) {
+        const bf16_t *H = static_cast<const bf16_t*>(a.H), *W = static_cast<const bf16_t*>(a.W);
+        return go(G == 8 ? head_target_kernel<bf16_t, 8> : head_target_kernel<bf16_t, 1>, grid, block, s, H, a.ldh, W,
+                  a.ldw, a.ids, a.ld_ids, a.k, a.tokens, a.vocab, int(a.dim), a.z);
+    }
+    const float *H = static_cast<const float*>(a.H), *W = static_cast<const float*>(a.W);
+    return go(G == 8 ? head_target_kernel<float, 8> : head_target_kernel<float, 1>, grid, block, s, H, a.ldh, W, a.ldw,
+              a.ids, a.ld_ids, a.k, a.tokens, a.vocab, int(a.dim), a.z);
 }
 
 hipError_t mo_launch_head_loss(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, hipStream_t s) {
     const float2* part = reinterpret_cast<const float2*>(ws + p.off_part);
-    hipError_t e = go(head_combine_kernel, dim3(unsigned((a.tokens + 31) / 32)), dim3(1024), s, part, p.n_pad,
-                      p.v_tiles, a.tokens, a.teacher ? nullptr : a.ids, a.vocab, a.z, a.loss, a.lse);
+    const int64_t* labels = a.teacher ? nullptr : a.ids;
+    const dim3 grid(unsigned((a.tokens + 31) / 32)), block(1024);
+    const hipError_t e =
+        a.dtype == MO_BF16
+            ? go(head_combine_kernel<bf16_t>, grid, block, s, part, p.n_pad, p.v_tiles, a.tokens, labels, a.vocab,
+                 static_cast<const bf16_t*>(a.H), a.ldh, static_cast<const bf16_t*>(a.W), a.ldw, int(a.dim), a.loss, a.lse)
+            : go(head_combine_kernel<float>, grid, block, s, part, p.n_pad, p.v_tiles, a.tokens, labels, a.vocab,
+                 static_cast<const float*>(a.H), a.ldh, static_cast<const float*>(a.W), a.ldw, int(a.dim), a.loss, a.lse);
     if (e != hipSuccess || !a.teacher) return e;
     return go(head_distill_loss_kernel, dim3(cap_grid((a.tokens + 3) / 4, 1 << 20)), dim3(256), s, a.ids, a.ld_ids,
               a.teacher, a.ld_teacher, a.teacher_dtype == MO_BF16, a.k, a.tokens, a.vocab, a.inv_t, a.t,
@@ -642,35 +737,40 @@ hipError_t mo_launch_head_loss(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t
 
 hipError_t mo_launch_head_prep(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, hipStream_t s) {
     float *coef = reinterpret_cast<float*>(ws + p.off_coef), *nl2 = reinterpret_cast<float*>(ws + p.off_nl2);
-    float* tval = reinterpret_cast<float*>(ws + p.off_tval);
+    float *tval = reinterpret_cast<float*>(ws + p.off_tval), *ref = reinterpret_cast<float*>(ws + p.off_ref);
     if (!a.teacher)
         return go(head_xent_prep_kernel, dim3(unsigned((p.n_pad + 255) / 256)), dim3(256), s, a.ids, a.loss_in,
-                  a.lse_in, a.dloss, a.tokens, p.n_pad, a.vocab, coef, nl2, tval);
+                  a.lse_in, a.dloss, a.tokens, p.n_pad, a.vocab, coef, nl2, tval, ref);
     return go(head_distill_prep_kernel, dim3(unsigned((p.n_pad + 3) / 4)), dim3(256), s, a.ids, a.ld_ids, a.teacher,
               a.ld_teacher, a.teacher_dtype == MO_BF16, a.k, a.tokens, p.n_pad, a.vocab, a.inv_t, a.t, a.z_in,
-              a.lse_in, a.dloss, coef, nl2, tval);
+              a.lse_in, a.dloss, coef, nl2, tval, ref);
+}
+
+// Transposes `rows` rows (and pads them to tr tiles of 64); with `packed` copies them too.
+static hipError_t transpose(const MoHeadArgs& a, const MoHeadPlan& p, const void* src, int64_t ld, int64_t rows,
+                            uint32_t tr, const float* coef, uint8_t* dst, int64_t ldt, uint8_t* packed,
+                            int64_t packed_rows, hipStream_t s) {
+    // whole stages of the copy: the columns behind dim are its zeros
+    const uint32_t tc = uint32_t(((packed ? p.kd : a.dim) + 63) / 64);
+    const dim3 grid((tr + 7) / 8 * ((tc + 7) / 8) * 64), block(256);
+    bf16_t *d = reinterpret_cast<bf16_t*>(dst), *k = reinterpret_cast<bf16_t*>(packed);
+    if (p.planes == 1)
+        return go(head_transpose_kernel<bf16_t, 1>, grid, block, s, static_cast<const bf16_t*>(src), ld, rows,
+                  int(a.dim), coef, d, ldt, a.dim * ldt, tr, tc, k, int(p.kd), packed_rows * p.kd);
+    return go(head_transpose_kernel<float, 3>, grid, block, s, static_cast<const float*>(src), ld, rows, int(a.dim),
+              coef, d, ldt, a.dim * ldt, tr, tc, k, int(p.kd), packed_rows * p.kd);
 }
 
 hipError_t mo_launch_head_ht(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, hipStream_t s) {
-    const float* coef = reinterpret_cast<const float*>(ws + p.off_coef);
-    bf16_t* dst = reinterpret_cast<bf16_t*>(ws + p.off_ht);
-    const dim3 grid(unsigned(p.n_pad / 64), unsigned((a.dim + 63) / 64)), block(256);
-    if (p.planes == 1)
-        return go(head_transpose_kernel<bf16_t, 1>, grid, block, s, static_cast<const bf16_t*>(a.H), a.ldh, a.tokens,
-                  int(a.dim), coef, dst, p.ld_t, a.dim * p.ld_t);
-    return go(head_transpose_kernel<float, 3>, grid, block, s, static_cast<const float*>(a.H), a.ldh, a.tokens,
-              int(a.dim), coef, dst, p.ld_t, a.dim * p.ld_t);
+    return transpose(a, p, a.H, a.ldh, a.tokens, uint32_t(p.n_pad / 64),
+                     reinterpret_cast<const float*>(ws + p.off_coef), ws + p.off_ht, p.ld_t, nullptr, 0, s);
 }
 
 hipError_t mo_launch_head_wt(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int k, int64_t v0, int64_t rows,
                              hipStream_t s) {
-    bf16_t* dst = reinterpret_cast<bf16_t*>(ws + p.off_wt[k & 1]);
-    const dim3 grid(unsigned((rows + 255) / 256 * 4), unsigned((a.dim + 63) / 64)), block(256);
-    if (p.planes == 1)
-        return go(head_transpose_kernel<bf16_t, 1>, grid, block, s, static_cast<const bf16_t*>(a.W) + v0 * a.ldw, a.ldw,
-                  rows, int(a.dim), static_cast<const float*>(nullptr), dst, p.ld_p, a.dim * p.ld_p);
-    return go(head_transpose_kernel<float, 3>, grid, block, s, static_cast<const float*>(a.W) + v0 * a.ldw, a.ldw, rows,
-              int(a.dim), static_cast<const float*>(nullptr), dst, p.ld_p, a.dim * p.ld_p);
+    const uint8_t* w = static_cast<const uint8_t*>(a.W) + v0 * a.ldw * (p.planes == 1 ? 2 : 4);
+    return transpose(a, p, w, a.ldw, rows, uint32_t((rows + 255) / 256 * 4), nullptr, ws + p.off_wt[k & 1], p.ld_p,
+                     p.pack_w ? ws + p.off_wp : nullptr, p.piece, s);
 }
 
 hipError_t mo_launch_head_patch(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int k, int64_t v0, int64_t rows,
@@ -716,6 +816,7 @@ hipError_t mo_launch_head_step(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t
         dw.dW = static_cast<uint8_t*>(a.dW) + v0 * a.lddw * (p.planes == 1 ? 2 : 4);
         dw.ldw = a.lddw;
         dw.dim = int(a.dim);
+        dw.ref = reinterpret_cast<const float*>(ws + p.off_ref);
         dw.blocks = head_grid(uint64_t(dw.tm) * dw.tn);
     }
     if (next_rows) {
@@ -753,11 +854,12 @@ hipError_t mo_launch_head_step(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t
 
 hipError_t mo_launch_head_dh_out(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, hipStream_t s) {
     const f32x4* acc = reinterpret_cast<const f32x4*>(ws + p.off_acc);
-    const float* coef = reinterpret_cast<const float*>(ws + p.off_coef);
+    const float *coef = reinterpret_cast<const float*>(ws + p.off_coef),
+                *ref = reinterpret_cast<const float*>(ws + p.off_ref);
     // 8 waves x MB row blocks, MB = 2 NB
     const dim3 grid(p.dh_tm * p.dh_tn * 16 * p.nb), block(256);
 #define MO_OUT(T, NB)                                                                                    \
-    return go(head_dh_out_kernel<T, NB>, grid, block, s, acc, p.dh_tm, p.dh_tn, uint32_t(p.dh_splits), coef, \
+    return go(head_dh_out_kernel<T, NB>, grid, block, s, acc, p.dh_tm, p.dh_tn, uint32_t(p.dh_splits), coef, ref, \
               static_cast<T*>(a.dH), a.lddh, a.tokens, int(a.dim))
     if (p.planes == 1) {
         if (p.nb == 4) MO_OUT(bf16_t, 4);

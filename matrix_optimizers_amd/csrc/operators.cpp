@@ -201,6 +201,7 @@ MoHeadPlan head_plan(const MoHeadArgs& a, bool backward, bool need_dh, bool need
         p.off_coef = take(uint64_t(4) * p.n_pad);
         p.off_nl2 = take(uint64_t(4) * p.n_pad);
         p.off_tval = take(uint64_t(4) * a.tokens * a.k);
+        p.off_ref = take(4);
         const int sets = pieces > 1 ? 2 : 1;
         for (int i = 0; i < sets; ++i) {
             p.off_d[i] = take(uint64_t(2) * p.planes * p.n_pad * p.ld_p);
@@ -280,10 +281,7 @@ void head_inputs(const MoHeadArgs& a, std::vector<Range>* r) {
 mo_status head_forward(MoHeadArgs& a, void* workspace, size_t workspace_bytes, void* stream, bool distill) {
     if (a.tokens == 0) return MO_OK;
     if (!a.H || !a.W || !a.ids || !a.loss || !a.lse || (distill && (!a.teacher || !a.z))) return MO_ERR_INVALID_ARG;
-    MoHeadPlan p = head_plan(a, false, false, false);
-    Carve more{p.bytes};
-    const uint64_t off_z = distill ? 0 : more(uint64_t(4) * a.tokens);
-    p.bytes = more.at;
+    const MoHeadPlan p = head_plan(a, false, false, false);
     std::vector<Range> ranges;
     head_inputs(a, &ranges);
     ranges.push_back(vec_range(a.loss, a.tokens, 4, 1));
@@ -292,10 +290,9 @@ mo_status head_forward(MoHeadArgs& a, void* workspace, size_t workspace_bytes, v
     uint8_t* ws;
     if (!take_workspace(workspace, workspace_bytes, p.bytes, &ranges, &ws)) return MO_ERR_WORKSPACE_TOO_SMALL;
     if (ranges_conflict(ranges)) return MO_ERR_ALIAS;
-    if (!distill) a.z = reinterpret_cast<float*>(ws + off_z);
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     if (p.pack_h) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_pack(a, p, ws, true, 0, a.tokens, s));
-    MO_RUN(MO_PHASE_HD_TARGET, mo_launch_head_targets(a, s));
+    if (distill) MO_RUN(MO_PHASE_HD_TARGET, mo_launch_head_targets(a, s));
     for (int64_t v0 = 0; v0 < a.vocab; v0 += p.piece) {
         const int64_t rows = std::min(p.piece, a.vocab - v0);
         if (p.pack_w) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_pack(a, p, ws, false, v0, rows, s));
@@ -346,8 +343,9 @@ mo_status head_backward(MoHeadArgs& a, void* workspace, size_t workspace_bytes, 
     for (int k = 0; k <= pieces; ++k) {
         const int64_t v0 = k * p.piece, rows = k < pieces ? std::min(p.piece, a.vocab - v0) : 0;
         if (rows) {
-            if (p.pack_w) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_pack(a, p, ws, false, v0, rows, s));
+            // the transpose for dH makes the copy as well
             if (a.dH) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_wt(a, p, ws, k, v0, rows, s));
+            else if (p.pack_w) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_pack(a, p, ws, false, v0, rows, s));
         }
         MO_RUN(k == 0 ? MO_PHASE_HD_DELTA : MO_PHASE_HD_STEP,
                mo_launch_head_step(a, p, ws, k - 1, v0 - p.piece, k ? std::min(p.piece, a.vocab - (v0 - p.piece)) : 0,
@@ -358,13 +356,11 @@ mo_status head_backward(MoHeadArgs& a, void* workspace, size_t workspace_bytes, 
     return MO_OK;
 }
 
-mo_status head_bytes(const MoHeadArgs& a, int32_t backward, bool distill, size_t* bytes) {
+mo_status head_bytes(const MoHeadArgs& a, int32_t backward, size_t* bytes) {
     if (!bytes) return MO_ERR_INVALID_ARG;
     *bytes = 0;
     if (a.tokens == 0) return MO_OK;
-    Carve take{head_plan(a, backward != 0, true, true).bytes};
-    if (!backward && !distill) take(uint64_t(4) * a.tokens);
-    *bytes = size_t(take.at) + MO_WS_ALIGN;
+    *bytes = size_t(head_plan(a, backward != 0, true, true).bytes) + MO_WS_ALIGN;
     return MO_OK;
 }
 
@@ -540,7 +536,7 @@ mo_status softmax_xent_workspace_bytes(const mo_head* head, int32_t backward, si
     MoHeadArgs a;
     const Targets t = label_targets(nullptr);
     MO_TRY(head_args(head, &t, &a));
-    return head_bytes(a, backward, false, bytes);
+    return head_bytes(a, backward, bytes);
 }
 
 mo_status softmax_xent_forward(const mo_head* head, const int64_t* labels, float* loss, float* lse, void* workspace,
@@ -574,7 +570,7 @@ mo_status topk_distill_workspace_bytes(const mo_head* head, const mo_topk* top, 
     Targets t;
     MO_TRY(topk_targets(top, &t));
     MO_TRY(head_args(head, &t, &a));
-    return head_bytes(a, backward, true, bytes);
+    return head_bytes(a, backward, bytes);
 }
 
 mo_status topk_distill_forward(const mo_head* head, const mo_topk* top, float* loss, float* lse, float* z,

@@ -81,7 +81,7 @@ struct MoHeadPlan {
     // dH: K stages per split, number of splits, tiles of 256 (dim) x 64 nb
     int dh_stages, dh_splits;
     uint32_t dh_tm, dh_tn;
-    uint64_t off_part, off_hp, off_wp, off_coef, off_nl2, off_tval, off_ht, off_wt[2], off_d[2], off_dt[2], off_acc;
+    uint64_t off_part, off_hp, off_wp, off_coef, off_nl2, off_tval, off_ref, off_ht, off_wt[2], off_d[2], off_dt[2], off_acc;
     uint64_t bytes;
 };
 hipError_t mo_launch_head_pack(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, bool h, int64_t v0,

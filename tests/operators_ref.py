@@ -175,8 +175,10 @@ def head(H, W, dloss=None, labels=None, ids=None, teacher=None, T=1.0):
         bd.scatter_add_(1, at, extra * (p > 0))
     six = 6 if f32 else 1
     drop = 2.0 ** -22 if f32 else 0.0
+    # the sums times the common scale of dloss: one product more (delta's division by
+    # it is within the 2^-21 above)
     out["dH"] = delta @ w
-    out["b_dH"] = (bd + (2 * U * six * V + drop) * delta.abs()) @ w.abs() + ut(H.dtype) * out["dH"].abs()
+    out["b_dH"] = (bd + (2 * U * six * V + drop) * delta.abs()) @ w.abs() + (ut(H.dtype) + U) * out["dH"].abs()
     out["dW"] = delta.t() @ h
-    out["b_dW"] = (bd + (2 * U * six * N + drop) * delta.abs()).t() @ h.abs() + ut(H.dtype) * out["dW"].abs()
+    out["b_dW"] = (bd + (2 * U * six * N + drop) * delta.abs()).t() @ h.abs() + (ut(H.dtype) + U) * out["dW"].abs()
     return out

@@ -224,3 +224,49 @@ def test_gradient_by_differences(gpu, kind):
         p[k], m[k] = p[k] + 1e-5 * v, m[k] - 1e-5 * v
         num = (f(*p) - f(*m)) / 2e-5
         assert abs(float((grad.double() * v).sum()) - num) <= 1e-5 * float((grad.double() * v).abs().sum()) + 1e-9
+
+
+@pytest.mark.parametrize("kind", ["mean", "far apart", "infinite first", "none", "tiny first"])
+def test_weights_of_the_rows(gpu, kind):
+    """dloss of one value (a mean), over many orders of magnitude, with zeros and a
+    non-finite weight in the first rows, and of zeros only."""
+    g, H, W, _ = inputs(200, 500, 96, BF, 51)
+    y = torch.randint(0, 500, (200,), generator=g, device="cuda")
+    if kind == "mean":
+        dloss = torch.full((200,), 1 / 200, device="cuda")
+    elif kind == "far apart":
+        dloss = 10.0 ** torch.linspace(-12, 6, 200, device="cuda")
+    elif kind == "infinite first":
+        dloss = torch.full((200,), -0.3, device="cuda")
+        dloss[:70] = 0
+        y[1] = -1
+        dloss[1] = float("inf")          # a masked row's weight does not count either
+    elif kind == "tiny first":
+        dloss = torch.full((200,), 0.7, device="cuda")
+        dloss[:128] = 0
+        dloss[5] = 1e-30
+    else:
+        dloss = torch.zeros(200, device="cuda")
+    got, dH, dW = run_xent(H, W, y, dloss)
+    compare(got, R.head(H, W, torch.where(y < 0, torch.zeros_like(dloss), dloss), labels=y), dH, dW)
+
+
+def test_a_mean_loses_no_precision(gpu):
+    """With equal weights the gradients' error stays near the rounding of the results
+    (uniform mantissas: 2^-8 / sqrt(12) of a value on average, 1.7e-3 with the
+    spread of mantissas): delta's own rounding, independent of it and of at most
+    the same size, adds at most a factor sqrt(2)."""
+    g = gen(61)
+    n, vocab, dim = 700, 5000, 512
+    W = rand(g, (vocab, dim), BF, 0.02)
+    y = torch.randint(0, vocab, (n,), generator=g, device="cuda")
+    H = (torch.randn((n, dim), generator=g, device="cuda") + 30 * W[y].float()).to(BF)
+    for count in (n, 641, 911, 1021):
+        dloss = torch.full((n,), 1 / count, device="cuda")
+        _, dH, dW = run_xent(H, W, y, dloss)
+        want = R.head(H, W, dloss, labels=y)
+        for got, name in ((dH, "dH"), (dW, "dW")):
+            exact = want[name]
+            own = float((exact.to(BF).double() - exact).norm() / exact.norm())
+            err = float((got.double() - exact).norm() / exact.norm())
+            assert err <= 1.45 * own, (count, name, err, own)

@@ -115,6 +115,91 @@ __global__ __launch_bounds__(256) void head_transpose_kernel(const T* src, int64
     }
 }
 
+// A product with K in splits, one tile of one split per workgroup: the fp32 tile in
+// accumulator order (lane by lane, 16 bytes each) is written, or added to what an
+// earlier launch wrote there.  out[split][tile row][tile column][wave][block][lane].
+struct SplitJob {
+    Operand P, Q;
+    int nk, stages;
+    uint32_t tm, tn, splits, blocks;
+    int first;
+    f32x4* out;
+};
+template <int NB, int PL>
+__device__ __forceinline__ void split_tile(uint8_t* smem, const SplitJob& j, uint32_t block) {
+    using L = Layout<NB>;
+    uint32_t ti, tj;
+    // the splits of a tile are rows of tiles: tile row ti of split s is s tm + ti
+    if (!head_tile_of(block, j.tm * j.splits, j.tn, ti, tj)) return;
+    const uint32_t sp = ti / j.tm;
+    ti -= sp * j.tm;
+    const int k0 = int(sp) * j.stages, n = j.nk - k0 < j.stages ? j.nk - k0 : j.stages;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    f32x4* o = j.out + (((int64_t(sp) * j.tm + ti) * j.tn + tj) * 8 + wave) * (L::MB * L::NBW * 64) + lane;
+    if (n <= 0) {
+        // a short last piece may leave a split without stages
+        if (j.first)
+#pragma unroll
+            for (int i = 0; i < L::MB * L::NBW; ++i) o[i * 64] = f32x4{0.f, 0.f, 0.f, 0.f};
+        return;
+    }
+    f32x4 acc[L::MB][L::NBW];
+    head_tile<NB, PL>(smem, j.P, j.Q, int64_t(ti) * 256, int64_t(tj) * 64 * NB, k0, n, acc);
+#pragma unroll
+    for (int a = 0; a < L::MB; ++a)
+#pragma unroll
+        for (int b = 0; b < L::NBW; ++b) {
+            f32x4* q = o + (a * L::NBW + b) * 64;
+            f32x4 v = acc[a][b];
+            if (!j.first) {
+                const f32x4 old = *q;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] += old[e];
+            }
+            *q = v;
+        }
+}
+
+// The logits of a piece with fewer than 128 tiles, which would leave more than half
+// of the CUs idle: K is split over the others, and the forward's and the
+// backward's epilogues add the splits up in order.  4405 rows x 34 tokens x 4672
+// (18 tiles): the forward takes 36 us in bf16, 67 without splits.
+template <int NB, int PL>
+__global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) void head_split_kernel(SplitJob j) {
+    __shared__ __align__(16) uint8_t smem[head_lds(NB)];
+    split_tile<NB, PL>(smem, j, blockIdx.x);
+}
+// One wavefront's unit of those sums: 32 rows x 64 tokens of tile (ti, tj).
+struct LogitSums {
+    const f32x4* z;
+    uint32_t tm, tn, splits;
+};
+template <int NB> struct Unit {
+    uint32_t ti, tj;
+    int row, col;   // of the unit inside its tile
+    f32x4 acc[2][4];
+    MO_DEV Unit(const LogitSums& s, uint32_t block) {
+        using L = Layout<NB>;
+        const uint32_t pair = block % NB, wave = block / NB % 8, tile = block / (8 * NB);
+        ti = tile / s.tn;
+        tj = tile - ti * s.tn;
+        row = int(wave / L::WN * (L::MB * 16) + pair * 32);
+        col = int(wave % L::WN * 64);
+        const f32x4* q = s.z + (int64_t(tile) * 8 + wave) * (L::MB * L::NBW * 64) + pair * (8 * 64) + (threadIdx.x & 63);
+        const int64_t stride = int64_t(s.tm) * s.tn * 8 * (L::MB * L::NBW * 64);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i / 4][i % 4] = q[i * 64];
+#pragma unroll 4
+        for (uint32_t t = 1; t < s.splits; ++t)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const f32x4 x = q[t * stride + i * 64];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i / 4][i % 4][e] += x[e];
+            }
+    }
+};
+
 // ---- forward ----------------------------------------------------------------------
 
 // Tile (ti, tj): vocabulary rows 256 ti .. of the piece, tokens TN tj ...  Each
@@ -169,6 +254,34 @@ __global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) 
     }
 }
 
+// The same from the sums of the splits, one partial per 32 vocabulary rows.
+template <int NB>
+__global__ __launch_bounds__(64) void head_lse_sum_kernel(LogitSums sums, int64_t rows, float zscale, float2* part,
+                                                          int64_t n_pad) {
+    const Unit<NB> u(sums, blockIdx.x);
+    const int lane = threadIdx.x, r16 = lane & 15, kg = lane >> 4;
+    const int64_t v0 = int64_t(u.ti) * 256 + u.row;
+    const int left = int(rows - v0 < 32 ? rows - v0 : 32) - kg * 4;
+    const float k2 = zscale * LOG2E;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        float z[8], m = -__builtin_inff(), s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            z[i] = i / 4 * 16 + i % 4 < left ? u.acc[i / 4][b][i % 4] * k2 : -__builtin_inff();
+            m = fmaxf(m, z[i]);
+        }
+        m = fmaxf(m, __shfl_xor(m, 16, 64));
+        m = fmaxf(m, __shfl_xor(m, 32, 64));
+        const float mm = m == -__builtin_inff() ? 0.f : m;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += exp2_hw(z[i] - mm);
+        s += __shfl_xor(s, 16, 64);
+        s += __shfl_xor(s, 32, 64);
+        if (kg == 0) part[v0 / 32 * n_pad + int64_t(u.tj) * (64 * NB) + u.col + b * 16 + r16] = float2{m, s};
+    }
+}
+
 // z[n][j] = H_n . W_id (not yet divided by T), 0 where the id is outside the
 // vocabulary: one wavefront per token and G of its ids, whose rows it requests
 // together (G = 8 at 4096 tokens x 64 ids x 2048: 165 us with one id per wavefront).
@@ -212,10 +325,10 @@ __global__ __launch_bounds__(256) void head_target_kernel(const T* H, int64_t ld
 }
 
 // log2-domain partial sums of 32 tokens -> lse (natural log), 32 strided shares
-// of the vocabulary tiles per token, combined in order.  Cross entropy (labels):
+// of the vocabulary's partials per token, combined in order.  Cross entropy (labels):
 // the label's logit, a dot product per token (two per wavefront), and the loss.
 template <typename T>
-__global__ __launch_bounds__(1024) void head_combine_kernel(const float2* part, int64_t n_pad, int64_t v_tiles,
+__global__ __launch_bounds__(1024) void head_combine_kernel(const float2* part, int64_t n_pad, int64_t partials,
                                                             int64_t tokens, const int64_t* labels,
                                                             int64_t vocab, const T* H, int64_t ldh, const T* W,
                                                             int64_t ldw, int dim, float* loss, float* lse) {
@@ -225,7 +338,7 @@ __global__ __launch_bounds__(1024) void head_combine_kernel(const float2* part, 
     const int64_t n0 = int64_t(blockIdx.x) * 32, n = n0 + tx;
     float m = -__builtin_inff(), s = 0.f;
     if (n < tokens)
-        for (int64_t t = ty; t < v_tiles; t += 32) {
+        for (int64_t t = ty; t < partials; t += 32) {
             const float2 q = part[t * n_pad + n];
             const float mn = fmaxf(m, q.x), mm = mn == -__builtin_inff() ? 0.f : mn;
             s = s * exp2_hw(m - mm) + q.y * exp2_hw(q.x - mm);
@@ -409,6 +522,58 @@ struct DeltaJob {
     bf16_t *D, *DT;
     int64_t ldd, plane_d, ldt, plane_t;
 };
+// c and -lse log2 e of the four columns that a lane holds of 64 tokens.
+MO_DEV void delta_tokens(const DeltaJob& j, int64_t tok, float (&c)[4], float (&l)[4]) {
+    const int r16 = threadIdx.x & 15;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        c[b] = j.coef[tok + b * 16 + r16];
+        l[b] = j.nl2[tok + b * 16 + r16];
+    }
+}
+// 32 vocabulary rows x 64 tokens of a wavefront, through its 8 KB of LDS into D
+// and DT; `left`: the lane's rows inside the vocabulary.
+template <int PL>
+__device__ __forceinline__ void delta_rows(uint8_t* st, const DeltaJob& j, const f32x4 (*acc)[4], const float (&c)[4],
+                                           const float (&l)[4], int left, int64_t vrow, int64_t tok) {
+    const int lane = threadIdx.x & 63, r16 = lane & 15, kg = lane >> 4;
+    const float k2 = j.zscale * LOG2E;
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            f32x4 v4;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float d = c[b] * exp2_hw(__builtin_fmaf(acc[g][b][e], k2, l[b]));
+                // rows behind the vocabulary and tokens that take no part
+                v4[e] = g * 16 + e < left && c[b] != 0.f ? d : 0.f;
+            }
+            *reinterpret_cast<f32x4*>(st + st_off(b * 16 + r16, g * 16 + kg * 4)) = v4;
+        }
+    __builtin_amdgcn_wave_barrier();
+    // a token of the block, 8 vocabulary rows
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const int col = (lane >> 2) + 16 * t, ic = lane & 3;
+        const f32x4 lo = *reinterpret_cast<const f32x4*>(st + st_off(col, ic * 8));
+        const f32x4 hi = *reinterpret_cast<const f32x4*>(st + st_off(col, ic * 8 + 4));
+        f32x8 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) { v.v[e] = lo[e]; v.v[4 + e] = hi[e]; }
+        put_planes<PL>(j.D + (tok + col) * j.ldd + vrow + ic * 8, j.plane_d, v);
+    }
+    // vocabulary row, 8 tokens
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const int cc = lane & 7, row = (lane >> 3) + 8 * t;
+        f32x8 v;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v.v[e] = *reinterpret_cast<const float*>(st + st_off(cc * 8 + e, row));
+        put_planes<PL>(j.DT + (vrow + row) * j.ldt + tok + cc * 8, j.plane_t, v);
+    }
+    __builtin_amdgcn_wave_barrier();
+}
 template <int NB, int PL>
 __device__ __forceinline__ void delta_tile(uint8_t* smem, const DeltaJob& j, uint32_t block) {
     using L = Layout<NB>;
@@ -422,52 +587,22 @@ __device__ __forceinline__ void delta_tile(uint8_t* smem, const DeltaJob& j, uin
     const int left = int(j.W.rows - v0 < 256 ? j.W.rows - v0 : 256) - wm * (L::MB * 16) - kg * 4;
     uint8_t* st = smem + wave * (32 * 64 * 4);
     float c[4], l[4];
+    delta_tokens(j, n0 + wn * 64, c, l);
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        c[b] = j.coef[n0 + wn * 64 + b * 16 + r16];
-        l[b] = j.nl2[n0 + wn * 64 + b * 16 + r16];
-    }
-    const float k2 = j.zscale * LOG2E;
-    // 32 rows of the wave's sub-tile at a time through its staging slice
-#pragma unroll
-    for (int a = 0; a < L::MB; a += 2) {
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                f32x4 v4;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float d = c[b] * exp2_hw(__builtin_fmaf(acc[a + g][b][e], k2, l[b]));
-                    // rows behind the vocabulary and tokens that take no part
-                    v4[e] = (a + g) * 16 + e < left && c[b] != 0.f ? d : 0.f;
-                }
-                *reinterpret_cast<f32x4*>(st + st_off(b * 16 + r16, g * 16 + kg * 4)) = v4;
-            }
-        __builtin_amdgcn_wave_barrier();
-        const int64_t vrow = v0 + wm * (L::MB * 16) + a * 16, tok = n0 + wn * 64;
-        // a token of the block, 8 vocabulary rows
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const int col = (lane >> 2) + 16 * t, ic = lane & 3;
-            const f32x4 lo = *reinterpret_cast<const f32x4*>(st + st_off(col, ic * 8));
-            const f32x4 hi = *reinterpret_cast<const f32x4*>(st + st_off(col, ic * 8 + 4));
-            f32x8 v;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) { v.v[e] = lo[e]; v.v[4 + e] = hi[e]; }
-            put_planes<PL>(j.D + (tok + col) * j.ldd + vrow + ic * 8, j.plane_d, v);
-        }
-        // vocabulary row, 8 tokens
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const int cc = lane & 7, row = (lane >> 3) + 8 * t;
-            f32x8 v;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v.v[e] = *reinterpret_cast<const float*>(st + st_off(cc * 8 + e, row));
-            put_planes<PL>(j.DT + (vrow + row) * j.ldt + tok + cc * 8, j.plane_t, v);
-        }
-        __builtin_amdgcn_wave_barrier();
-    }
+    for (int a = 0; a < L::MB; a += 2)
+        delta_rows<PL>(st, j, &acc[a], c, l, left - a * 16, v0 + wm * (L::MB * 16) + a * 16, n0 + wn * 64);
+}
+
+// The same from the sums of the splits.
+template <int NB, int PL>
+__global__ __launch_bounds__(64) void head_delta_sum_kernel(LogitSums sums, DeltaJob j) {
+    __shared__ __align__(16) uint8_t st[32 * 64 * 4];
+    const Unit<NB> u(sums, blockIdx.x);
+    const int64_t v0 = int64_t(u.ti) * 256 + u.row, tok = int64_t(u.tj) * (64 * NB) + u.col;
+    const int left = int(j.W.rows - v0 < 32 ? j.W.rows - v0 : 32) - (threadIdx.x >> 4) * 4;
+    float c[4], l[4];
+    delta_tokens(j, tok, c, l);
+    delta_rows<PL>(st, j, u.acc, c, l, left, v0, tok);
 }
 
 // delta at the targets that fall into the piece, in both orientations.
@@ -539,50 +674,6 @@ __device__ __forceinline__ void dw_tile(uint8_t* smem, const DwJob& j, uint32_t 
     }
 }
 
-// One split of dH^T += WT D^T over the piece's vocabulary rows: the fp32 tile in
-// accumulator order (lane by lane, 16 bytes each), read and written whole.
-struct DhJob {
-    Operand WT, D;
-    int nk, stages;
-    uint32_t tm, tn, splits, blocks;
-    int first;
-    f32x4* out;
-};
-template <int NB, int PL>
-__device__ __forceinline__ void dh_tile(uint8_t* smem, const DhJob& j, uint32_t block) {
-    using L = Layout<NB>;
-    uint32_t ti, tj;
-    // the splits of a tile are rows of tiles: tile row ti of split s is s tm + ti
-    if (!head_tile_of(block, j.tm * j.splits, j.tn, ti, tj)) return;
-    const uint32_t sp = ti / j.tm;
-    ti -= sp * j.tm;
-    const int k0 = int(sp) * j.stages, n = j.nk - k0 < j.stages ? j.nk - k0 : j.stages;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    f32x4* o = j.out + (((int64_t(sp) * j.tm + ti) * j.tn + tj) * 8 + wave) * (L::MB * L::NBW * 64) + lane;
-    if (n <= 0) {
-        // a short last piece may leave a split without stages
-        if (j.first)
-#pragma unroll
-            for (int i = 0; i < L::MB * L::NBW; ++i) o[i * 64] = f32x4{0.f, 0.f, 0.f, 0.f};
-        return;
-    }
-    f32x4 acc[L::MB][L::NBW];
-    head_tile<NB, PL>(smem, j.WT, j.D, int64_t(ti) * 256, int64_t(tj) * 64 * NB, k0, n, acc);
-#pragma unroll
-    for (int a = 0; a < L::MB; ++a)
-#pragma unroll
-        for (int b = 0; b < L::NBW; ++b) {
-            f32x4* q = o + (a * L::NBW + b) * 64;
-            f32x4 v = acc[a][b];
-            if (!j.first) {
-                const f32x4 old = *q;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] += old[e];
-            }
-            *q = v;
-        }
-}
-
 // One launch: dW and dH of a piece and delta of the next one.  The three do not
 // depend on each other (two sets of D, DT and WT), and together they leave one
 // partly filled last round per piece instead of three.  At 8192 tokens x 128256 x
@@ -591,7 +682,7 @@ __device__ __forceinline__ void dh_tile(uint8_t* smem, const DhJob& j, uint32_t 
 // 17.5 (delta's 4 bytes per logit 0.7, the fp32 sums of dH 0.7, dW 0.3).
 template <typename T, int NB, int NBW, int PL>
 __global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) void head_step_kernel(
-    DhJob dh, DwJob dw, DeltaJob dl) {
+    SplitJob dh, DwJob dw, DeltaJob dl) {
     __shared__ __align__(16) uint8_t smem[head_lds(NB > NBW ? NB : NBW)];
     uint32_t b = blockIdx.x;
     if (b < dw.blocks) {
@@ -600,7 +691,7 @@ __global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) 
     }
     b -= dw.blocks;
     if (b < dh.blocks) {
-        dh_tile<NB, PL>(smem, dh, b);
+        split_tile<NB, PL>(smem, dh, b);
         return;
     }
     delta_tile<NB, PL>(smem, dl, b - dh.blocks);
@@ -694,11 +785,40 @@ hipError_t mo_launch_head_pack(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t
               int(a.dim), dst, int(p.kd), plane);
 }
 
+// The splits of a piece's logits, and where their sums are read.
+static hipError_t split_logits(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, const Operand& W, LogitSums* sums,
+                               hipStream_t s) {
+    SplitJob j = {};
+    j.P = W;
+    j.Q = h_operand(a, p, ws);
+    j.nk = int(p.kd / 64);
+    j.stages = p.z_stages;
+    j.tm = uint32_t((W.rows + 255) / 256);
+    j.tn = uint32_t(p.n_pad / (64 * p.nb));
+    j.splits = uint32_t(p.z_splits);
+    j.first = 1;
+    j.out = reinterpret_cast<f32x4*>(ws + p.off_z);
+    *sums = {j.out, j.tm, j.tn, j.splits};
+    const dim3 grid(head_grid(uint64_t(j.tm) * j.tn * j.splits)), block(H_THREADS);
+#define MO_CALL(NB, PL) return go(head_split_kernel<NB, PL>, grid, block, s, j)
+    MO_HEAD_PICK(p.nb, p.planes, MO_CALL);
+#undef MO_CALL
+}
+
 hipError_t mo_launch_head_lse(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int64_t v0, int64_t rows,
                               hipStream_t s) {
     const Operand H = h_operand(a, p, ws), W = w_operand(a, p, ws, v0, rows);
     const uint32_t tm = uint32_t((rows + 255) / 256), tn = uint32_t(p.n_pad / (64 * p.nb));
-    float2* part = reinterpret_cast<float2*>(ws + p.off_part) + v0 / 256 * p.n_pad;
+    float2* part = reinterpret_cast<float2*>(ws + p.off_part) + v0 / 256 * p.n_pad * (p.z_splits > 1 ? 8 : 1);
+    if (p.z_splits > 1) {
+        LogitSums sums;
+        const hipError_t e = split_logits(a, p, ws, W, &sums, s);
+        if (e != hipSuccess) return e;
+        const dim3 units(tm * tn * 8 * uint32_t(p.nb)), wave(64);
+        if (p.nb == 4) return go(head_lse_sum_kernel<4>, units, wave, s, sums, rows, a.inv_t, part, p.n_pad);
+        if (p.nb == 2) return go(head_lse_sum_kernel<2>, units, wave, s, sums, rows, a.inv_t, part, p.n_pad);
+        return go(head_lse_sum_kernel<1>, units, wave, s, sums, rows, a.inv_t, part, p.n_pad);
+    }
     const dim3 grid(head_grid(uint64_t(tm) * tn)), block(H_THREADS);
 #define MO_CALL(NB, PL) \
     return go(head_lse_kernel<NB, PL>, grid, block, s, W, H, int(p.kd / 64), tm, tn, a.inv_t, part, p.n_pad)
@@ -722,12 +842,13 @@ hipError_t mo_launch_head_targets(const MoHeadArgs& a, hipStream_t s) {
 hipError_t mo_launch_head_loss(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, hipStream_t s) {
     const float2* part = reinterpret_cast<const float2*>(ws + p.off_part);
     const int64_t* labels = a.teacher ? nullptr : a.ids;
+    const int64_t partials = p.v_tiles * (p.z_splits > 1 ? 8 : 1);
     const dim3 grid(unsigned((a.tokens + 31) / 32)), block(1024);
     const hipError_t e =
         a.dtype == MO_BF16
-            ? go(head_combine_kernel<bf16_t>, grid, block, s, part, p.n_pad, p.v_tiles, a.tokens, labels, a.vocab,
+            ? go(head_combine_kernel<bf16_t>, grid, block, s, part, p.n_pad, partials, a.tokens, labels, a.vocab,
                  static_cast<const bf16_t*>(a.H), a.ldh, static_cast<const bf16_t*>(a.W), a.ldw, int(a.dim), a.loss, a.lse)
-            : go(head_combine_kernel<float>, grid, block, s, part, p.n_pad, p.v_tiles, a.tokens, labels, a.vocab,
+            : go(head_combine_kernel<float>, grid, block, s, part, p.n_pad, partials, a.tokens, labels, a.vocab,
                  static_cast<const float*>(a.H), a.ldh, static_cast<const float*>(a.W), a.ldw, int(a.dim), a.loss, a.lse);
     if (e != hipSuccess || !a.teacher) return e;
     return go(head_distill_loss_kernel, dim3(cap_grid((a.tokens + 3) / 4, 1 << 20)), dim3(256), s, a.ids, a.ld_ids,
@@ -787,17 +908,50 @@ hipError_t mo_launch_head_patch(const MoHeadArgs& a, const MoHeadPlan& p, uint8_
               p.n_pad * p.ld_p, DT, p.ld_t, p.piece * p.ld_t);
 }
 
+static DeltaJob delta_job(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int k, int64_t v0, int64_t rows) {
+    DeltaJob dl = {};
+    dl.W = w_operand(a, p, ws, v0, rows);
+    dl.H = h_operand(a, p, ws);
+    dl.nk = int(p.kd / 64);
+    dl.tm = uint32_t((rows + 255) / 256);
+    dl.tn = uint32_t(p.n_pad / (64 * p.nb));
+    dl.zscale = a.inv_t;
+    dl.coef = reinterpret_cast<const float*>(ws + p.off_coef);
+    dl.nl2 = reinterpret_cast<const float*>(ws + p.off_nl2);
+    dl.D = reinterpret_cast<bf16_t*>(ws + p.off_d[k & 1]);
+    dl.DT = reinterpret_cast<bf16_t*>(ws + p.off_dt[k & 1]);
+    dl.ldd = p.ld_p;
+    dl.plane_d = p.n_pad * p.ld_p;
+    dl.ldt = p.ld_t;
+    dl.plane_t = p.piece * p.ld_t;
+    dl.blocks = head_grid(uint64_t(dl.tm) * dl.tn);
+    return dl;
+}
+
+// delta of piece k from the splits of its logits.
+hipError_t mo_launch_head_delta_split(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int k, int64_t v0,
+                                      int64_t rows, hipStream_t s) {
+    const DeltaJob dl = delta_job(a, p, ws, k, v0, rows);
+    LogitSums sums;
+    const hipError_t e = split_logits(a, p, ws, dl.W, &sums, s);
+    if (e != hipSuccess) return e;
+    const dim3 units(dl.tm * dl.tn * 8 * uint32_t(p.nb)), wave(64);
+#define MO_CALL(NB, PL) return go(head_delta_sum_kernel<NB, PL>, units, wave, s, sums, dl)
+    MO_HEAD_PICK(p.nb, p.planes, MO_CALL);
+#undef MO_CALL
+}
+
 // Piece k (rows from v0 on; rows 0: none) of dH and dW, and delta of piece k + 1
 // (next_rows 0: none).
 hipError_t mo_launch_head_step(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int k, int64_t v0, int64_t rows,
                                int64_t next_v0, int64_t next_rows, hipStream_t s) {
-    DhJob dh = {};
+    SplitJob dh = {};
     DwJob dw = {};
     DeltaJob dl = {};
     const uint32_t tn = uint32_t(p.n_pad / (64 * p.nb)), tm = uint32_t((rows + 255) / 256);
     if (rows && a.dH) {
-        dh.WT = rows_of(ws + p.off_wt[k & 1], p.ld_p, a.dim, a.dim * p.ld_p);
-        dh.D = rows_of(ws + p.off_d[k & 1], p.ld_p, p.n_pad, p.n_pad * p.ld_p);
+        dh.P = rows_of(ws + p.off_wt[k & 1], p.ld_p, a.dim, a.dim * p.ld_p);
+        dh.Q = rows_of(ws + p.off_d[k & 1], p.ld_p, p.n_pad, p.n_pad * p.ld_p);
         dh.nk = int(tm * 4);   // the piece's rows, rounded up to whole tiles
         dh.stages = p.dh_stages;
         dh.tm = p.dh_tm;
@@ -819,24 +973,7 @@ hipError_t mo_launch_head_step(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t
         dw.ref = reinterpret_cast<const float*>(ws + p.off_ref);
         dw.blocks = head_grid(uint64_t(dw.tm) * dw.tn);
     }
-    if (next_rows) {
-        const int n = (k + 1) & 1;
-        dl.W = w_operand(a, p, ws, next_v0, next_rows);
-        dl.H = h_operand(a, p, ws);
-        dl.nk = int(p.kd / 64);
-        dl.tm = uint32_t((next_rows + 255) / 256);
-        dl.tn = tn;
-        dl.zscale = a.inv_t;
-        dl.coef = reinterpret_cast<const float*>(ws + p.off_coef);
-        dl.nl2 = reinterpret_cast<const float*>(ws + p.off_nl2);
-        dl.D = reinterpret_cast<bf16_t*>(ws + p.off_d[n]);
-        dl.DT = reinterpret_cast<bf16_t*>(ws + p.off_dt[n]);
-        dl.ldd = p.ld_p;
-        dl.plane_d = p.n_pad * p.ld_p;
-        dl.ldt = p.ld_t;
-        dl.plane_t = p.piece * p.ld_t;
-        dl.blocks = head_grid(uint64_t(dl.tm) * dl.tn);
-    }
+    if (next_rows) dl = delta_job(a, p, ws, k + 1, next_v0, next_rows);
     const dim3 grid(dh.blocks + dw.blocks + dl.blocks), block(H_THREADS);
 #define MO_STEP(T, NB, PL)                                                                             \
     return p.nb_dw == 4 ? go(head_step_kernel<T, NB, 4, PL>, grid, block, s, dh, dw, dl)               \

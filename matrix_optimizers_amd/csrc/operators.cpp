@@ -149,20 +149,36 @@ bool in_place(const void* p, int64_t ld, int64_t dim) {
            ld * 2 < (int64_t(1) << 23);
 }
 
-// Rounds of the 256 CUs that `tiles` tiles take.
-int64_t rounds(int64_t tiles) { return (tiles + 255) / 256; }
+// Estimated us of the logits' product in `tiles` tiles of 256 x 64 nb with `stages`
+// stages of 64 K, and the splits of K that it takes.  A stage takes 1.43, 0.8 and
+// 0.6 us in a tile of 256, 128 and 64 tokens (256 CUs at 1.5 PFLOP/s; the narrow ones
+// wait for their loads), six times that with three planes; splits write and read
+// fp32 tiles at 5 TB/s, are added up one after the other, and are one launch more.
+// In all, a step of 4405 rows x 34 tokens x 4672 went from 177 to 107 us in bf16
+// with splits, 5168 x 40 x 256 (4 stages) stays without at 49 us.
+double logits_us(int64_t tiles, int64_t stages, int nb, int planes, int64_t* splits) {
+    const double stage = (nb == 4 ? 1.43 : nb == 2 ? 0.8 : 0.6) * (planes == 1 ? 1 : 6);
+    double least = double((tiles + 255) / 256 * stages) * stage;
+    *splits = 1;
+    for (int64_t k = 2; k <= std::min(256 / tiles, stages); ++k) {
+        const double t = double((stages + k - 1) / k) * stage + double(tiles * k * nb) * 0.026 + double(k) * 0.1 + 4;
+        if (t < least) {
+            least = t;
+            *splits = k;
+        }
+    }
+    return least;
+}
 
-// Relative time of a 256 x 64 nb tile: a narrow one reads the same 256 rows of P.
-int64_t tile_cost(int nb) { return nb == 4 ? 100 : nb == 2 ? 56 : 34; }
-
-// Tile width over the tokens: the least rounds times cost over the vocabulary's tiles.
-int token_tile(int64_t n, int64_t v_tiles) {
+// Tile width over the tokens: the one with the least time.
+int token_tile(int64_t n, int64_t v_tiles, int64_t stages, int planes) {
     int best = 4;
-    int64_t least = 0;
+    double least = 0;
     for (int nb = 4; nb >= 1; nb /= 2) {
-        const int64_t c = rounds((n + 64 * nb - 1) / (64 * nb) * v_tiles) * tile_cost(nb);
-        if (nb == 4 || c < least) {
-            least = c;
+        int64_t splits;
+        const double t = logits_us((n + 64 * nb - 1) / (64 * nb) * v_tiles, stages, nb, planes, &splits);
+        if (nb == 4 || t < least) {
+            least = t;
             best = nb;
         }
     }
@@ -173,9 +189,9 @@ MoHeadPlan head_plan(const MoHeadArgs& a, bool backward, bool need_dh, bool need
     MoHeadPlan p = {};
     p.planes = a.dtype == MO_BF16 ? 1 : 3;
     p.v_tiles = (a.vocab + 255) / 256;
-    p.nb = token_tile(a.tokens, p.v_tiles);
-    p.n_pad = (a.tokens + 64 * p.nb - 1) / (64 * p.nb) * (64 * p.nb);
     p.kd = k_extent(a.dim);
+    p.nb = token_tile(a.tokens, p.v_tiles, p.kd / 64, p.planes);
+    p.n_pad = (a.tokens + 64 * p.nb - 1) / (64 * p.nb) * (64 * p.nb);
     p.pack_h = p.planes != 1 || !in_place(a.H, a.ldh, a.dim);
     p.pack_w = p.planes != 1 || !in_place(a.W, a.ldw, a.dim);
     p.nb_dw = a.dim <= 128 ? 1 : 4;
@@ -192,11 +208,17 @@ MoHeadPlan head_plan(const MoHeadArgs& a, bool backward, bool need_dh, bool need
     p.piece = (p.v_tiles + pieces - 1) / pieces * 256;
     p.ld_t = copy_stride(p.n_pad);
     p.ld_p = copy_stride(p.piece);
+    const int64_t z_tiles = p.piece / 256 * tn, nk = p.kd / 64;
+    int64_t z_want;
+    logits_us(z_tiles, nk, p.nb, p.planes, &z_want);
+    p.z_stages = int((nk + z_want - 1) / z_want);
+    p.z_splits = int((nk + p.z_stages - 1) / p.z_stages);
     Carve take;
+    if (p.z_splits > 1) p.off_z = take(uint64_t(4) * p.z_splits * z_tiles * 256 * 64 * p.nb);
     if (p.pack_h) p.off_hp = take(uint64_t(2) * p.planes * a.tokens * p.kd);
     if (p.pack_w) p.off_wp = take(uint64_t(2) * p.planes * p.piece * p.kd);
     if (!backward) {
-        p.off_part = take(uint64_t(8) * p.v_tiles * p.n_pad);
+        p.off_part = take(uint64_t(8) * p.v_tiles * (p.z_splits > 1 ? 8 : 1) * p.n_pad);
     } else {
         p.off_coef = take(uint64_t(4) * p.n_pad);
         p.off_nl2 = take(uint64_t(4) * p.n_pad);
@@ -338,7 +360,7 @@ mo_status head_backward(MoHeadArgs& a, void* workspace, size_t workspace_bytes, 
     MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_prep(a, p, ws, s));
     if (p.pack_h) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_pack(a, p, ws, true, 0, a.tokens, s));
     if (a.dW) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_ht(a, p, ws, s));
-    // turn k: delta of piece k beside dH and dW of piece k - 1
+    // turn k: delta of piece k beside dH and dW of piece k - 1 (behind them if its logits are split)
     const int pieces = int((a.vocab + p.piece - 1) / p.piece);
     for (int k = 0; k <= pieces; ++k) {
         const int64_t v0 = k * p.piece, rows = k < pieces ? std::min(p.piece, a.vocab - v0) : 0;
@@ -347,9 +369,11 @@ mo_status head_backward(MoHeadArgs& a, void* workspace, size_t workspace_bytes, 
             if (a.dH) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_wt(a, p, ws, k, v0, rows, s));
             else if (p.pack_w) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_pack(a, p, ws, false, v0, rows, s));
         }
-        MO_RUN(k == 0 ? MO_PHASE_HD_DELTA : MO_PHASE_HD_STEP,
-               mo_launch_head_step(a, p, ws, k - 1, v0 - p.piece, k ? std::min(p.piece, a.vocab - (v0 - p.piece)) : 0,
-                                   v0, rows, s));
+        const int64_t last = k ? std::min(p.piece, a.vocab - (v0 - p.piece)) : 0, beside = p.z_splits > 1 ? 0 : rows;
+        if (last || beside)
+            MO_RUN(last ? MO_PHASE_HD_STEP : MO_PHASE_HD_DELTA,
+                   mo_launch_head_step(a, p, ws, k - 1, v0 - p.piece, last, v0, beside, s));
+        if (rows > beside) MO_RUN(MO_PHASE_HD_DELTA, mo_launch_head_delta_split(a, p, ws, k, v0, rows, s));
         if (rows) MO_RUN(MO_PHASE_HD_TARGET, mo_launch_head_patch(a, p, ws, k, v0, rows, s));
     }
     if (a.dH) MO_RUN(MO_PHASE_HD_DH, mo_launch_head_dh_out(a, p, ws, s));

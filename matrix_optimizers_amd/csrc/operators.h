@@ -81,7 +81,8 @@ struct MoHeadPlan {
     // dH: K stages per split, number of splits, tiles of 256 (dim) x 64 nb
     int dh_stages, dh_splits;
     uint32_t dh_tm, dh_tn;
-    uint64_t off_part, off_hp, off_wp, off_coef, off_nl2, off_tval, off_ref, off_ht, off_wt[2], off_d[2], off_dt[2], off_acc;
+    int z_stages, z_splits; // logits: K stages per split, splits (1: none)
+    uint64_t off_part, off_hp, off_wp, off_coef, off_nl2, off_tval, off_ref, off_ht, off_wt[2], off_d[2], off_dt[2], off_acc, off_z;
     uint64_t bytes;
 };
 hipError_t mo_launch_head_pack(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, bool h, int64_t v0,
@@ -97,6 +98,8 @@ hipError_t mo_launch_head_wt(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* 
                              hipStream_t s);
 hipError_t mo_launch_head_patch(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int k, int64_t v0, int64_t rows,
                                 hipStream_t s);
+hipError_t mo_launch_head_delta_split(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int k, int64_t v0,
+                                      int64_t rows, hipStream_t s);
 hipError_t mo_launch_head_step(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int k, int64_t v0, int64_t rows,
                                int64_t next_v0, int64_t next_rows, hipStream_t s);
 hipError_t mo_launch_head_dh_out(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, hipStream_t s);

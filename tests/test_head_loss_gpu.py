@@ -270,3 +270,22 @@ def test_a_mean_loses_no_precision(gpu):
             own = float((exact.to(BF).double() - exact).norm() / exact.norm())
             err = float((got.double() - exact).norm() / exact.norm())
             assert err <= 1.45 * own, (count, name, err, own)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,vocab,dim", [(1, 1, 2000), (34, 700, 2000), (65, 1111, 777), (300, 520, 3000),
+                                         (129, 257, 64), (20, 20000, 1024)])
+def test_long_products_of_few_tiles(gpu, n, vocab, dim, dtype):
+    """Few tiles with a long product: K is split over the workgroups."""
+    g, H, W, dloss = inputs(n, vocab, dim, dtype, n + dim)
+    y = labels_of(g, n, vocab)
+    got, dH, dW = run_xent(H, W, y, dloss)
+    compare(got, R.head(H, W, dloss, labels=y), dH, dW)
+
+
+def test_split_products_in_two_pieces(gpu):
+    """The longest rows there are: two pieces of the vocabulary, each split along K."""
+    g, H, W, dloss = inputs(5, 2000, 65536, F32, 71)
+    y = labels_of(g, 5, 2000)
+    got, dH, dW = run_xent(H, W, y, dloss)
+    compare(got, R.head(H, W, dloss, labels=y), dH, dW)

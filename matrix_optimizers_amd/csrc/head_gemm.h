@@ -39,7 +39,8 @@ constexpr int HP_BYTES = 256 * HKB;                   // 32 KB of P per stage
 constexpr int head_lds(int NB) { return 2 * (HP_BYTES + 64 * NB * HKB); }
 
 // x = hi + mid + lo exactly: each the nearest bf16 to what is left (24 bits of
-// significand = 3 x 8), so |mid| <= 2^-8 |x| and |lo| <= 2^-16 |x|.  A finite x that
+// significand = 3 x 8), so |mid| <= 2^-8 |x| and |lo| <= 2^-16 |x| (below 2^-109, where
+// lo runs out of exponent, to 2^-134).  A finite x that
 // would round to infinity is truncated; infinities and NaN keep mid and lo at 0.
 MO_DEV void split_f32(float x, bf16_t& hi, bf16_t& mid, bf16_t& lo) {
     const bool finite = __builtin_fabsf(x) < __builtin_inff();
@@ -237,6 +238,236 @@ __device__ __forceinline__ void head_tile(uint8_t* smem, const Operand& P, const
         s = 1;
     }
     stage(s & 1, false, false, false);
+    __syncthreads();
+#endif
+}
+
+// ---- P in fp32, as it lies in memory ---------------------------------------------------
+//
+// For few tokens the product is a read of the other operand, and splitting that
+// one into planes first moves it five times more (4 bytes to read, 6 to write, and 12
+// to read back for the six plane pairs).  Here P stays fp32 up to the registers,
+// where each fragment is split; Q (tokens) still comes as planes.  Tiles of 64
+// tokens only: there one wave needs a fragment of P, so it is split once.
+//
+// Stages of 32 K: 256 x 32 fp32 of P (32 KB) and three planes of 64 rows of 64 bytes
+// of Q (12 KB), in a ring of three.  While a stage's 48 MFMAs run, the next one's
+// fragments are read and split.  One product at 64 tokens x 32001 rows x 4096 (524 MB):
+// 117 to 141 us; its loads alone take 99 to 110 and its MFMAs and splitting alone 95 to
+// 105, of which six bf16 products at the rate of a large one are 70.  Without the
+// pipeline over stages it was 129 to 155; tiles of 128 tokens, which do not have the
+// registers for it, took 390 at 256 tokens against 413 with these.
+// P is either
+//   rows along K (NN false): as above, 128-byte rows, chunk c of row r at c ^ pswz(r);
+//   K along the rows (NN true): 32 rows of 256 columns (1 KB); chunk c of row r at
+//     c ^ 4 (r / 8 mod 4), so that the four K groups of a fragment's column fall on
+//     four different quarters of the 64 banks.
+// Q: chunk c of row r at c ^ qswz(r).
+// The 16 lanes that the LDS serves together in a 16-byte read are consecutive ones,
+// or rows 0-3 and 12-15 of one K group with rows 4-11 of the next, or the other way
+// round.  A fragment of P takes chunks 2 kg and 2 kg + 1, so bit 1 of the chunk has
+// to change as bit 0 of r / 2 does; with 64-byte rows the groups of four rows get
+// 0, 2, 3, 1, which stay apart under an exchange of neighbours and ^ 1.
+MO_DEV int pswz(int row) { const int x = row >> 1; return ((x << 1) & 6) | ((x >> 2) & 1); }
+MO_DEV int qswz(int row) { const int g = (row >> 2) & 3; return ((g << 1) & 2) ^ ((g >> 1) * 3); }
+constexpr int S32_SLOTS = 3, S32_BYTES = HP_BYTES + 3 * 64 * 64;
+constexpr int head_lds32() { return S32_SLOTS * S32_BYTES; }
+
+// Eight values as three planes, each the nearest bf16 (ties away from zero) to what is
+// left; eight bits are left for the last one, which is exact.  In integer adds and
+// masks (2 % faster here than conversions and shifts).  The high part stays finite;
+// infinities and NaN leave NaN in the others (a product with the exact planes of
+// split_f32 also ends in NaN: infinity times a zero low part).
+MO_DEV void split_frag(const float (&x)[8], bf16x8 (&p)[3]) {
+    constexpr float M = 3.3895313892515355e38f;   // the largest bf16
+    uint32_t h[8], m[8], l[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        h[e] = (__float_as_uint(__builtin_amdgcn_fmed3f(x[e], -M, M)) + 0x8000u) & 0xFFFF0000u;
+        const float r = x[e] - __uint_as_float(h[e]);
+        m[e] = (__float_as_uint(r) + 0x8000u) & 0xFFFF0000u;
+        l[e] = __float_as_uint(r - __uint_as_float(m[e]));
+    }
+    u32x4 o[3];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {   // the upper halves of two
+        o[0][e] = __builtin_amdgcn_perm(h[2 * e + 1], h[2 * e], 0x07060302u);
+        o[1][e] = __builtin_amdgcn_perm(m[2 * e + 1], m[2 * e], 0x07060302u);
+        o[2][e] = __builtin_amdgcn_perm(l[2 * e + 1], l[2 * e], 0x07060302u);
+    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) p[i] = __builtin_bit_cast(bf16x8, o[i]);
+}
+
+// As head_tile, with P in fp32: `cols` of its columns are there (a multiple of 4).
+// NN false: rows p0 .. of P, K along its columns; NN true: columns p0 .. of P,
+// K along its rows.  K behind the end counts as zeros.  k0 and nk1 in stages of 64 K.
+template <bool NN, class Acc>
+__device__ __forceinline__ void head_tile32(uint8_t* smem, const Operand& P, int cols, const Operand& Q, int64_t p0,
+                                            int64_t q0, int k0, int nk1, Acc& acc) {
+#ifdef __HIP_DEVICE_COMPILE__
+    using L = Layout<1>;
+    constexpr int MB = L::MB, NBW = L::NBW, S = S32_SLOTS;
+    static_assert(L::WN == 1 && MB == 2 && NBW == 4, "8 waves of 32 x 64");
+    // Q: 12 instructions of 16 rows x 64 bytes over the 8 waves (the last one by five of them)
+    constexpr int QI = 2;   // with the four of P: 6 loads per stage and wave
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r16 = lane & 15, kg = lane >> 4;
+    const int n = nk1 * 2, s0 = k0 * 2;   // stages of 32 K, an even number
+    auto rsrc = [&](const uint8_t* p) __attribute__((always_inline)) {
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, -1, 0x00027000);
+    };
+
+    uint32_t prow[4], pch[4], vq[QI];
+    const int plim = int(P.rows - p0 < 256 ? P.rows - p0 : 256) - 1;    // NN false
+    const int qlim = int(Q.rows - q0 < 64 ? Q.rows - q0 : 64) - 1;
+    auto qinst = [&](int i) __attribute__((always_inline)) { return wave + 8 * i < 12 ? wave + 8 * i : 11; };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (NN) {
+            const int r = wave * 4 + i, c = lane ^ (((r >> 3) & 3) << 2), last = int(cols - p0) / 4 - 1;
+            prow[i] = 0;
+            pch[i] = uint32_t(c < last ? c : last) * 16;
+        } else {
+            const int r = wave * 32 + i * 8 + (lane >> 3);
+            prow[i] = uint32_t(r < plim ? r : plim) * uint32_t(P.ld);
+            pch[i] = uint32_t((lane & 7) ^ pswz(r)) * 16;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < QI; ++i) {
+        const int r = qinst(i) % 4 * 16 + (lane >> 2);
+        vq[i] = uint32_t(r < qlim ? r : qlim) * uint32_t(Q.ld) + uint32_t(((lane & 3) ^ qswz(r)) << 4);
+    }
+    const uint8_t* Pb = NN ? P.base + p0 * 4 : P.base + p0 * P.ld;
+    const uint8_t* Qb = Q.base + q0 * Q.ld;
+    const auto rP = rsrc(Pb);
+    auto issue = [&](int s, int slot) __attribute__((always_inline)) {
+        uint8_t* sp = smem + slot * S32_BYTES;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            lds_void_t* to = (lds_void_t*)(sp + (wave * 4 + i) * 1024);
+            if constexpr (NN) {
+                const int64_t k = int64_t(s0 + s) * 32 + wave * 4 + i;
+                const auto row = rsrc(Pb + (k < P.rows ? k : P.rows - 1) * P.ld);
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(row, to, 16, pch[i], 0, 0, 0);
+            } else {
+                const uint32_t at = uint32_t(s0 + s) * 128 + pch[i], last = uint32_t(cols) * 4 - 16;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rP, to, 16, prow[i] + (at < last ? at : last), 0, 0, 0);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < QI; ++i) {
+            const int t = qinst(i);
+            const auto q = rsrc(Qb + t / 4 * Q.plane);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(q, (lds_void_t*)(sp + HP_BYTES + t * 1024), 16, vq[i],
+                                                     (s0 + s) * 64, 0, 0);
+        }
+    };
+
+#pragma unroll
+    for (int a = 0; a < MB; ++a)
+#pragma unroll
+        for (int b = 0; b < NBW; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    const int64_t klim = NN ? P.rows : int64_t(cols);
+    int pat[2];   // NN: K element 0 of column block a; else the two chunks of row block 0
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+        if constexpr (NN) {
+            const int c = wave * 32 + a * 16 + r16;
+            pat[a] = kg * 8 * 1024 + (((c >> 2) ^ (kg << 2)) << 4) + (c & 3) * 4;
+        } else {
+            pat[a] = (wave * 32 + r16) * HKB + (((2 * kg + a) ^ pswz(r16)) << 4);
+        }
+    }
+    const int qat = HP_BYTES + r16 * 64 + ((kg ^ qswz(r16)) << 4);
+
+    struct Frag {
+        bf16x8 p[MB][3];
+        u32x4 q[3][NBW];
+    } f0, f1;
+    float x[MB][8];
+    // the fragments of a stage: from LDS, and P's split
+    auto read = [&](Frag& f, int slot) __attribute__((always_inline)) {
+        const uint8_t* sp = smem + slot * S32_BYTES;
+#pragma unroll
+        for (int a = 0; a < MB; ++a) {
+            if constexpr (NN) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[a][e] = *reinterpret_cast<const float*>(sp + pat[a] + e * 1024);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const f32x4 v = *reinterpret_cast<const f32x4*>(sp + pat[c] + a * (16 * HKB));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[a][c * 4 + e] = v[e];
+                }
+            }
+        }
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+#pragma unroll
+            for (int b = 0; b < NBW; ++b)
+                f.q[p][b] = *reinterpret_cast<const u32x4*>(sp + qat + p * (64 * 64) + b * (16 * 64));
+    };
+    auto split = [&](Frag& f, int s) __attribute__((always_inline)) {
+        const int64_t left = klim - int64_t(s0 + s) * 32;
+        if (left < 32)
+#pragma unroll
+            for (int a = 0; a < MB; ++a)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[a][e] = kg * 8 + e < left ? x[a][e] : 0.f;
+#pragma unroll
+        for (int a = 0; a < MB; ++a) split_frag(x[a], f.p[a]);
+    };
+    // the plane pairs, largest last
+    auto mfma = [&](const Frag& f, int a) __attribute__((always_inline)) {
+#pragma unroll
+        for (int t = 0; t < 6; ++t)
+#pragma unroll
+            for (int b = 0; b < NBW; ++b)
+                acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    f.p[a][seg_p<3>(t)], __builtin_bit_cast(bf16x8, f.q[seg_q<3>(t)][b]), acc[a][b], 0, 0, 0);
+    };
+    // Stage s, its fragments in `f`.
+    int slot = 0;   // of stage s
+    auto stage = [&](int s, Frag& f, Frag& next) __attribute__((always_inline)) {
+        // the loads of stage s + 1 have landed, and every wave has read the slot of stage s
+        if (s + 2 < n) asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
+        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if (s + S < n) issue(s + S, slot);
+        slot = slot == S - 1 ? 0 : slot + 1;
+        // (behind the last stage: what the slot holds, read and not used)
+        read(next, slot);
+        mfma(f, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        split(next, s + 1);
+        mfma(f, 1);
+#pragma unroll
+        for (int t = 0; t < 24; ++t) {
+            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);   // an MFMA
+            __builtin_amdgcn_sched_group_barrier(0x2, 6, 0);   // six of the splitting
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+        if (i < n) issue(i, i);
+    // stage 0 has landed
+    if (n > 2) asm volatile("s_waitcnt vmcnt(12)" ::: "memory");
+    else asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    read(f0, 0);
+    split(f0, 0);
+    for (int s = 0; s < n; s += 2) {
+        stage(s, f0, f1);
+        stage(s + 1, f1, f0);
+    }
     __syncthreads();
 #endif
 }

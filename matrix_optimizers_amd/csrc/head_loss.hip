@@ -37,6 +37,18 @@ using namespace mo_head_gemm;
 
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
+// How a product's operands come (PL): 1: bf16; 3: fp32 as three planes each; F32W: W in
+// fp32 as it lies in memory, the tokens' side as planes.
+constexpr int F32W = 32;
+constexpr int lds_of(int NB, int PL) { return PL == F32W ? head_lds32() : head_lds(NB); }
+// One tile of a product with W: NN: columns of W, K along its rows.
+template <int NB, int PL, bool NN, class Acc>
+__device__ __forceinline__ void w_tile(uint8_t* smem, const Operand& P, int dim, const Operand& Q, int64_t p0,
+                                       int64_t q0, int k0, int n, Acc& acc) {
+    if constexpr (PL == F32W) head_tile32<NN>(smem, P, dim, Q, p0, q0, k0, n, acc);
+    else head_tile<NB, PL>(smem, P, Q, p0, q0, k0, n, acc);
+}
+
 MO_DEV float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // ---- operand copies ---------------------------------------------------------------
@@ -120,12 +132,13 @@ __global__ __launch_bounds__(256) void head_transpose_kernel(const T* src, int64
 // earlier launch wrote there.  out[split][tile row][tile column][wave][block][lane].
 struct SplitJob {
     Operand P, Q;
+    int dim;
     int nk, stages;
     uint32_t tm, tn, splits, blocks;
     int first;
     f32x4* out;
 };
-template <int NB, int PL>
+template <int NB, int PL, bool NN>
 __device__ __forceinline__ void split_tile(uint8_t* smem, const SplitJob& j, uint32_t block) {
     using L = Layout<NB>;
     uint32_t ti, tj;
@@ -144,7 +157,7 @@ __device__ __forceinline__ void split_tile(uint8_t* smem, const SplitJob& j, uin
         return;
     }
     f32x4 acc[L::MB][L::NBW];
-    head_tile<NB, PL>(smem, j.P, j.Q, int64_t(ti) * 256, int64_t(tj) * 64 * NB, k0, n, acc);
+    w_tile<NB, PL, NN>(smem, j.P, j.dim, j.Q, int64_t(ti) * 256, int64_t(tj) * 64 * NB, k0, n, acc);
 #pragma unroll
     for (int a = 0; a < L::MB; ++a)
 #pragma unroll
@@ -166,8 +179,8 @@ __device__ __forceinline__ void split_tile(uint8_t* smem, const SplitJob& j, uin
 // (18 tiles): the forward takes 36 us in bf16, 67 without splits.
 template <int NB, int PL>
 __global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) void head_split_kernel(SplitJob j) {
-    __shared__ __align__(16) uint8_t smem[head_lds(NB)];
-    split_tile<NB, PL>(smem, j, blockIdx.x);
+    __shared__ __align__(16) uint8_t smem[lds_of(NB, PL)];
+    split_tile<NB, PL, false>(smem, j, blockIdx.x);
 }
 // One wavefront's unit of those sums: 32 rows x 64 tokens of tile (ti, tj).
 struct LogitSums {
@@ -207,14 +220,14 @@ template <int NB> struct Unit {
 // maximum and the sum are mostly in registers.
 template <int NB, int PL>
 __global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) void head_lse_kernel(
-    Operand W, Operand H, int nk, uint32_t tm, uint32_t tn, float zscale, float2* part, int64_t n_pad) {
+    Operand W, int dim, Operand H, int nk, uint32_t tm, uint32_t tn, float zscale, float2* part, int64_t n_pad) {
     using L = Layout<NB>;
-    __shared__ __align__(16) uint8_t smem[head_lds(NB)];
+    __shared__ __align__(16) uint8_t smem[lds_of(NB, PL)];
     uint32_t ti, tj;
     if (!head_tile_of(blockIdx.x, tm, tn, ti, tj)) return;
     const int64_t v0 = int64_t(ti) * 256, n0 = int64_t(tj) * 64 * NB;
     f32x4 acc[L::MB][L::NBW];
-    head_tile<NB, PL>(smem, W, H, v0, n0, 0, nk, acc);
+    w_tile<NB, PL, false>(smem, W, dim, H, v0, n0, 0, nk, acc);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int wm = wave / L::WN, wn = wave % L::WN, r16 = lane & 15, kg = lane >> 4;
     const int left = int(W.rows - v0 < 256 ? W.rows - v0 : 256) - wm * (L::MB * 16) - kg * 4;
@@ -324,57 +337,50 @@ __global__ __launch_bounds__(256) void head_target_kernel(const T* H, int64_t ld
     }
 }
 
-// log2-domain partial sums of 32 tokens -> lse (natural log), 32 strided shares
-// of the vocabulary's partials per token, combined in order.  Cross entropy (labels):
-// the label's logit, a dot product per token (two per wavefront), and the loss.
+// log2-domain partial sums of 8 tokens -> lse (natural log), 64 strided shares of
+// the vocabulary's partials per token, combined in order.  Cross entropy (labels):
+// the label's logit, a dot product per token and wavefront, and the loss.
 template <typename T>
-__global__ __launch_bounds__(1024) void head_combine_kernel(const float2* part, int64_t n_pad, int64_t partials,
-                                                            int64_t tokens, const int64_t* labels,
-                                                            int64_t vocab, const T* H, int64_t ldh, const T* W,
-                                                            int64_t ldw, int dim, float* loss, float* lse) {
-    __shared__ float2 sh[32][33];
-    __shared__ float zl[32];
-    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const int64_t n0 = int64_t(blockIdx.x) * 32, n = n0 + tx;
+__global__ __launch_bounds__(512) void head_combine_kernel(const float2* part, int64_t n_pad, int64_t partials,
+                                                           int64_t tokens, const int64_t* labels,
+                                                           int64_t vocab, const T* H, int64_t ldh, const T* W,
+                                                           int64_t ldw, int dim, float* loss, float* lse) {
+    __shared__ float2 sh[8][65];
+    const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t n0 = int64_t(blockIdx.x) * 8;
     float m = -__builtin_inff(), s = 0.f;
-    if (n < tokens)
-        for (int64_t t = ty; t < partials; t += 32) {
-            const float2 q = part[t * n_pad + n];
+    if (n0 + tx < tokens)
+#pragma unroll 4
+        for (int64_t t = ty; t < partials; t += 64) {
+            const float2 q = part[t * n_pad + n0 + tx];
             const float mn = fmaxf(m, q.x), mm = mn == -__builtin_inff() ? 0.f : mn;
             s = s * exp2_hw(m - mm) + q.y * exp2_hw(q.x - mm);
             m = mn;
         }
-    sh[ty][tx] = float2{m, s};
-    if (labels) {
-        const int lane = threadIdx.x & 63;
+    sh[tx][ty] = float2{m, s};
+    const int64_t n = n0 + wave, y = labels && n < tokens ? labels[n] : -1;
+    const bool in = uint64_t(y) < uint64_t(vocab);
+    float z = 0.f;
+    if (in)
+#pragma unroll 4
+        for (int c = lane * 8; c < dim; c += 512) {
+            const f32x8 a = widen(ld8n(H + n * ldh + c, dim - c)), b = widen(ld8n(W + y * ldw + c, dim - c));
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int j = int(threadIdx.x >> 6) * 2 + i;
-            const int64_t y = n0 + j < tokens ? labels[n0 + j] : -1;
-            float z = 0.f;
-            if (uint64_t(y) < uint64_t(vocab))
-                for (int c = lane * 8; c < dim; c += 512) {
-                    const f32x8 a = widen(ld8n(H + (n0 + j) * ldh + c, dim - c)), b = widen(ld8n(W + y * ldw + c, dim - c));
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) z = __builtin_fmaf(a.v[e], b.v[e], z);
-                }
-            z = wave_sum(z);
-            if (lane == 0) zl[j] = z;
+            for (int e = 0; e < 8; ++e) z = __builtin_fmaf(a.v[e], b.v[e], z);
         }
-    }
+    z = wave_sum(z);
     __syncthreads();
-    if (ty == 0 && n < tokens) {
-        for (int t = 1; t < 32; ++t) m = fmaxf(m, sh[t][tx].x);
-        const float mm = m == -__builtin_inff() ? 0.f : m;
-        s = 0.f;
-        for (int t = 0; t < 32; ++t) s += sh[t][tx].y * exp2_hw(sh[t][tx].x - mm);
-        float l = m * LN2 + logf(s);
-        if (labels) {
-            const bool in = uint64_t(labels[n]) < uint64_t(vocab);
-            loss[n] = in ? l - zl[tx] : 0.f;
-            l = in ? l : 0.f;
-        }
-        lse[n] = l;
+    if (n >= tokens) return;
+    const float2 q = sh[wave][lane];
+    m = q.x;
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+    const float mm = m == -__builtin_inff() ? 0.f : m;
+    s = wave_sum(q.y * exp2_hw(q.x - mm));
+    if (lane == 0) {
+        const float l = m * LN2 + logf(s);
+        if (labels) loss[n] = in ? l - z : 0.f;
+        lse[n] = !labels || in ? l : 0.f;
     }
 }
 
@@ -498,7 +504,8 @@ __global__ __launch_bounds__(256) void head_distill_prep_kernel(const int64_t* i
                 float p = 0.f;
                 for (int u = 0; u < k; ++u)
                     if (id[u] == v) p += expf(load_elem(te, u, t_bf16) * inv_t - mt) / st;
-                o = c * (expf(z[n * k + j] * inv_t - l) - p);
+                const float q = expf(z[n * k + j] * inv_t - l);   // at most 1, as in delta_rows
+                o = c * ((q > 1.f ? 1.f : q) - p);
             }
             tval[n * k + j] = o;
         }
@@ -515,7 +522,7 @@ __global__ __launch_bounds__(256) void head_distill_prep_kernel(const int64_t* i
 // both zero for tokens that take no part and rows behind the vocabulary.
 struct DeltaJob {
     Operand W, H;
-    int nk;
+    int dim, nk;
     uint32_t tm, tn, blocks;
     float zscale;
     const float *coef, *nl2;
@@ -545,7 +552,8 @@ __device__ __forceinline__ void delta_rows(uint8_t* st, const DeltaJob& j, const
             f32x4 v4;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float d = c[b] * exp2_hw(__builtin_fmaf(acc[g][b][e], k2, l[b]));
+                // at most 1: lse is rounded, by more than a unit where logits pass 2^24
+                const float q = exp2_hw(__builtin_fmaf(acc[g][b][e], k2, l[b])), d = c[b] * (q > 1.f ? 1.f : q);
                 // rows behind the vocabulary and tokens that take no part
                 v4[e] = g * 16 + e < left && c[b] != 0.f ? d : 0.f;
             }
@@ -581,9 +589,9 @@ __device__ __forceinline__ void delta_tile(uint8_t* smem, const DeltaJob& j, uin
     if (!head_tile_of(block, j.tm, j.tn, ti, tj)) return;
     const int64_t v0 = int64_t(ti) * 256, n0 = int64_t(tj) * 64 * NB;
     f32x4 acc[L::MB][L::NBW];
-    head_tile<NB, PL>(smem, j.W, j.H, v0, n0, 0, j.nk, acc);
+    w_tile<NB, PL, false>(smem, j.W, j.dim, j.H, v0, n0, 0, j.nk, acc);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int wm = wave / L::WN, wn = wave % L::WN, r16 = lane & 15, kg = lane >> 4;
+    const int wm = wave / L::WN, wn = wave % L::WN, kg = lane >> 4;
     const int left = int(j.W.rows - v0 < 256 ? j.W.rows - v0 : 256) - wm * (L::MB * 16) - kg * 4;
     uint8_t* st = smem + wave * (32 * 64 * 4);
     float c[4], l[4];
@@ -646,7 +654,7 @@ __device__ __forceinline__ void dw_tile(uint8_t* smem, const DwJob& j, uint32_t 
     if (!head_tile_of(block, j.tm, j.tn, ti, tj)) return;
     const int64_t v0 = int64_t(ti) * 256, c0 = int64_t(tj) * 64 * NB;
     f32x4 acc[L::MB][L::NBW];
-    head_tile<NB, PL>(smem, j.DT, j.HT, v0, c0, 0, j.nk, acc);
+    head_tile<NB, PL == 1 ? 1 : 3>(smem, j.DT, j.HT, v0, c0, 0, j.nk, acc);
     T* dW = static_cast<T*>(j.dW);
     const float r = *j.ref;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -683,7 +691,7 @@ __device__ __forceinline__ void dw_tile(uint8_t* smem, const DwJob& j, uint32_t 
 template <typename T, int NB, int NBW, int PL>
 __global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) void head_step_kernel(
     SplitJob dh, DwJob dw, DeltaJob dl) {
-    __shared__ __align__(16) uint8_t smem[head_lds(NB > NBW ? NB : NBW)];
+    __shared__ __align__(16) uint8_t smem[lds_of(NB, PL) > head_lds(NBW) ? lds_of(NB, PL) : head_lds(NBW)];
     uint32_t b = blockIdx.x;
     if (b < dw.blocks) {
         dw_tile<T, NBW, PL>(smem, dw, b);
@@ -691,7 +699,7 @@ __global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) 
     }
     b -= dw.blocks;
     if (b < dh.blocks) {
-        split_tile<NB, PL>(smem, dh, b);
+        split_tile<NB, PL, true>(smem, dh, b);
         return;
     }
     delta_tile<NB, PL>(smem, dl, b - dh.blocks);
@@ -745,6 +753,7 @@ Operand h_operand(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws) {
     return p.pack_h ? rows_of(ws + p.off_hp, p.kd, a.tokens, a.tokens * p.kd) : rows_of(a.H, a.ldh, a.tokens, 0);
 }
 Operand w_operand(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int64_t v0, int64_t rows) {
+    if (p.f32w) return {static_cast<const uint8_t*>(a.W) + v0 * a.ldw * 4, a.ldw * 4, rows, 0};
     return p.pack_w ? rows_of(ws + p.off_wp, p.kd, rows, p.piece * p.kd)
                     : rows_of(static_cast<const bf16_t*>(a.W) + v0 * a.ldw, a.ldw, rows, 0);
 }
@@ -791,6 +800,7 @@ static hipError_t split_logits(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t
     SplitJob j = {};
     j.P = W;
     j.Q = h_operand(a, p, ws);
+    j.dim = int(a.dim);
     j.nk = int(p.kd / 64);
     j.stages = p.z_stages;
     j.tm = uint32_t((W.rows + 255) / 256);
@@ -800,6 +810,7 @@ static hipError_t split_logits(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t
     j.out = reinterpret_cast<f32x4*>(ws + p.off_z);
     *sums = {j.out, j.tm, j.tn, j.splits};
     const dim3 grid(head_grid(uint64_t(j.tm) * j.tn * j.splits)), block(H_THREADS);
+    if (p.f32w) return go(head_split_kernel<1, F32W>, grid, block, s, j);
 #define MO_CALL(NB, PL) return go(head_split_kernel<NB, PL>, grid, block, s, j)
     MO_HEAD_PICK(p.nb, p.planes, MO_CALL);
 #undef MO_CALL
@@ -820,8 +831,11 @@ hipError_t mo_launch_head_lse(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t*
         return go(head_lse_sum_kernel<1>, units, wave, s, sums, rows, a.inv_t, part, p.n_pad);
     }
     const dim3 grid(head_grid(uint64_t(tm) * tn)), block(H_THREADS);
+    if (p.f32w)
+        return go(head_lse_kernel<1, F32W>, grid, block, s, W, int(a.dim), H, int(p.kd / 64), tm, tn, a.inv_t, part,
+                  p.n_pad);
 #define MO_CALL(NB, PL) \
-    return go(head_lse_kernel<NB, PL>, grid, block, s, W, H, int(p.kd / 64), tm, tn, a.inv_t, part, p.n_pad)
+    return go(head_lse_kernel<NB, PL>, grid, block, s, W, int(a.dim), H, int(p.kd / 64), tm, tn, a.inv_t, part, p.n_pad)
     MO_HEAD_PICK(p.nb, p.planes, MO_CALL);
 #undef MO_CALL
 }
@@ -843,7 +857,7 @@ hipError_t mo_launch_head_loss(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t
     const float2* part = reinterpret_cast<const float2*>(ws + p.off_part);
     const int64_t* labels = a.teacher ? nullptr : a.ids;
     const int64_t partials = p.v_tiles * (p.z_splits > 1 ? 8 : 1);
-    const dim3 grid(unsigned((a.tokens + 31) / 32)), block(1024);
+    const dim3 grid(unsigned((a.tokens + 7) / 8)), block(512);
     const hipError_t e =
         a.dtype == MO_BF16
             ? go(head_combine_kernel<bf16_t>, grid, block, s, part, p.n_pad, partials, a.tokens, labels, a.vocab,
@@ -912,6 +926,7 @@ static DeltaJob delta_job(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws,
     DeltaJob dl = {};
     dl.W = w_operand(a, p, ws, v0, rows);
     dl.H = h_operand(a, p, ws);
+    dl.dim = int(a.dim);
     dl.nk = int(p.kd / 64);
     dl.tm = uint32_t((rows + 255) / 256);
     dl.tn = uint32_t(p.n_pad / (64 * p.nb));
@@ -950,7 +965,8 @@ hipError_t mo_launch_head_step(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t
     DeltaJob dl = {};
     const uint32_t tn = uint32_t(p.n_pad / (64 * p.nb)), tm = uint32_t((rows + 255) / 256);
     if (rows && a.dH) {
-        dh.P = rows_of(ws + p.off_wt[k & 1], p.ld_p, a.dim, a.dim * p.ld_p);
+        dh.P = p.f32w ? w_operand(a, p, ws, v0, rows) : rows_of(ws + p.off_wt[k & 1], p.ld_p, a.dim, a.dim * p.ld_p);
+        dh.dim = int(a.dim);
         dh.Q = rows_of(ws + p.off_d[k & 1], p.ld_p, p.n_pad, p.n_pad * p.ld_p);
         dh.nk = int(tm * 4);   // the piece's rows, rounded up to whole tiles
         dh.stages = p.dh_stages;
@@ -983,6 +999,7 @@ hipError_t mo_launch_head_step(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t
         if (p.nb == 2) MO_STEP(bf16_t, 2, 1);
         MO_STEP(bf16_t, 1, 1);
     }
+    if (p.f32w) MO_STEP(float, 1, F32W);
     if (p.nb == 4) MO_STEP(float, 4, 3);
     if (p.nb == 2) MO_STEP(float, 2, 3);
     MO_STEP(float, 1, 3);

@@ -149,6 +149,16 @@ bool in_place(const void* p, int64_t ld, int64_t dim) {
            ld * 2 < (int64_t(1) << 23);
 }
 
+// Up to 512 tokens an fp32 W is read in place, in tiles of 64 tokens; more tokens pay for
+// splitting it into planes once.  A step at 32001 rows x 4096 (us, in place and
+// planes): 64 tokens 598 and 1790, 256 1654 and 2277, 512 3106 and 3342; at
+// 32001 x 1000: 512 833 and 855, 1021 1611 and 1467.
+constexpr int64_t kF32InPlaceTokens = 512;
+bool f32_in_place(const void* p, int64_t ld, int64_t dim) {
+    return dim % 4 == 0 && ((reinterpret_cast<uintptr_t>(p) | uintptr_t(ld * 4)) & 15) == 0 &&
+           ld * 4 < (int64_t(1) << 23);
+}
+
 // Estimated us of the logits' product in `tiles` tiles of 256 x 64 nb with `stages`
 // stages of 64 K, and the splits of K that it takes.  A stage takes 1.43, 0.8 and
 // 0.6 us in a tile of 256, 128 and 64 tokens (256 CUs at 1.5 PFLOP/s; the narrow ones
@@ -171,13 +181,13 @@ double logits_us(int64_t tiles, int64_t stages, int nb, int planes, int64_t* spl
 }
 
 // Tile width over the tokens: the one with the least time.
-int token_tile(int64_t n, int64_t v_tiles, int64_t stages, int planes) {
-    int best = 4;
+int token_tile(int64_t n, int64_t v_tiles, int64_t stages, int planes, int widest) {
+    int best = widest;
     double least = 0;
-    for (int nb = 4; nb >= 1; nb /= 2) {
+    for (int nb = widest; nb >= 1; nb /= 2) {
         int64_t splits;
         const double t = logits_us((n + 64 * nb - 1) / (64 * nb) * v_tiles, stages, nb, planes, &splits);
-        if (nb == 4 || t < least) {
+        if (nb == widest || t < least) {
             least = t;
             best = nb;
         }
@@ -190,17 +200,18 @@ MoHeadPlan head_plan(const MoHeadArgs& a, bool backward, bool need_dh, bool need
     p.planes = a.dtype == MO_BF16 ? 1 : 3;
     p.v_tiles = (a.vocab + 255) / 256;
     p.kd = k_extent(a.dim);
-    p.nb = token_tile(a.tokens, p.v_tiles, p.kd / 64, p.planes);
+    p.f32w = p.planes == 3 && a.tokens <= kF32InPlaceTokens && f32_in_place(a.W, a.ldw, a.dim);
+    p.nb = token_tile(a.tokens, p.v_tiles, p.kd / 64, p.planes, p.f32w ? 1 : 4);
     p.n_pad = (a.tokens + 64 * p.nb - 1) / (64 * p.nb) * (64 * p.nb);
     p.pack_h = p.planes != 1 || !in_place(a.H, a.ldh, a.dim);
-    p.pack_w = p.planes != 1 || !in_place(a.W, a.ldw, a.dim);
+    p.pack_w = !p.f32w && (p.planes != 1 || !in_place(a.W, a.ldw, a.dim));
     p.nb_dw = a.dim <= 128 ? 1 : 4;
     const int64_t tn = p.n_pad / (64 * p.nb);
     // equal pieces bounded by the memory of their copies (and by the grid of one launch);
     // at least one tile
     int64_t row = p.pack_w ? 2 * p.planes * p.kd : 0;
     // (the same pieces whichever gradients are asked for, so that the size query holds for each)
-    if (backward) row += 2 * (4 * p.planes * p.n_pad + 2 * p.planes * a.dim);
+    if (backward) row += 2 * (4 * p.planes * p.n_pad + (p.f32w ? 0 : 2 * p.planes * a.dim));
     int64_t most = std::min<int64_t>((int64_t(1) << 22) / std::max<int64_t>(tn, (a.dim + 63) / 64), 1 << 13);
     if (row) most = std::min(most, (backward ? kHeadPieceBytes : kHeadPieceBytes / 4) / row / 256);
     most = std::max<int64_t>(most, 1);
@@ -228,7 +239,7 @@ MoHeadPlan head_plan(const MoHeadArgs& a, bool backward, bool need_dh, bool need
         for (int i = 0; i < sets; ++i) {
             p.off_d[i] = take(uint64_t(2) * p.planes * p.n_pad * p.ld_p);
             p.off_dt[i] = take(uint64_t(2) * p.planes * p.piece * p.ld_t);
-            if (need_dh) p.off_wt[i] = take(uint64_t(2) * p.planes * a.dim * p.ld_p);
+            if (need_dh && !p.f32w) p.off_wt[i] = take(uint64_t(2) * p.planes * a.dim * p.ld_p);
         }
         if (need_dw) {
             p.off_ht = take(uint64_t(2) * p.planes * a.dim * p.ld_t);
@@ -366,7 +377,7 @@ mo_status head_backward(MoHeadArgs& a, void* workspace, size_t workspace_bytes, 
         const int64_t v0 = k * p.piece, rows = k < pieces ? std::min(p.piece, a.vocab - v0) : 0;
         if (rows) {
             // the transpose for dH makes the copy as well
-            if (a.dH) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_wt(a, p, ws, k, v0, rows, s));
+            if (a.dH && !p.f32w) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_wt(a, p, ws, k, v0, rows, s));
             else if (p.pack_w) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_pack(a, p, ws, false, v0, rows, s));
         }
         const int64_t last = k ? std::min(p.piece, a.vocab - (v0 - p.piece)) : 0, beside = p.z_splits > 1 ? 0 : rows;

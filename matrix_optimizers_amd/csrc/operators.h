@@ -74,6 +74,7 @@ struct MoHeadPlan {
     int nb, nb_dw;          // tile width (64 nb): tokens side; dim side of dW
     int64_t n_pad;          // tokens rounded up to the tile width
     int64_t kd;             // dim as a K extent (rounded up, zeros behind)
+    bool f32w;              // fp32 W read in place (few tokens)
     bool pack_h, pack_w;    // operand copied (padded, split) before use
     int64_t piece;          // vocabulary rows per piece (a multiple of 256)
     int64_t ld_t, ld_p;     // row strides of the copies along the tokens and along the piece

@@ -1,10 +1,12 @@
 """CPU models of the output head's GEMM (head_gemm.h): the order in which a
 wavefront issues its loads, reads fragments, waits and passes barriers; the
 cursor that walks the plane pairs of a split fp32 product; the assignment of
-tiles to workgroups; the rows and bytes its loads touch; its LDS swizzle."""
+tiles to workgroups; the rows and bytes its loads touch; its LDS swizzles; the
+splitting of fp32 fragments."""
 import os
 import re
 
+import numpy as np
 import pytest
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -203,3 +205,60 @@ def test_copy_strides_cover_their_extents():
     for k in range(64, 70000, 64):
         ld = k + 64 if k * 2 % 4096 == 0 else k
         assert ld >= k and ld * 2 % 4096 != 0 and ld * 2 % 128 == 0
+
+
+def test_fp32_fragments_split_exactly():
+    """The integer form of the three planes: nearest with ties away from zero, finite
+    high parts, and nothing left over."""
+    rng = np.random.default_rng(5)
+    x = np.concatenate([rng.standard_normal(20000) * 10.0 ** rng.integers(-30, 30, 20000),
+                        [0.0, -0.0, 1.0, 3.4028235e38, -3.4028235e38, 3.3895314e38, 1 + 2.0 ** -8, 1 + 2.0 ** -9]])
+    x = x.astype(np.float32)
+    top = np.float32(3.3895313892515355e38)
+
+    def near(v):
+        return ((v.view(np.uint32) + np.uint32(0x8000)) & np.uint32(0xFFFF0000)).view(np.float32)
+
+    h = near(np.clip(x, -top, top))
+    r = x - h
+    m = near(r)
+    low = r - m
+    assert np.isfinite(h).all()
+    # the last of 24 bits is 2^-23 of the first, and bf16 ends at 2^-133
+    assert ((low.view(np.uint32) & 0xFFFF) == 0)[np.abs(x) >= 2.0 ** -109].all()
+    assert (h.astype(np.float64) + m + low == x).all()
+    assert (np.abs(m) <= 2.0 ** -7 * np.abs(x)).all() and (np.abs(low) <= 2.0 ** -15 * np.abs(x)).all()
+
+
+def test_in_place_fragments_reach_every_bank_once():
+    """The swizzles of the fp32 tiles: each set of 16 lanes served together falls on
+    16 different 16-byte bank groups, for every chunk it reads."""
+    def pswz(r):
+        x = r >> 1
+        return ((x << 1) & 6) | ((x >> 2) & 1)
+
+    def qswz(r):
+        g = (r >> 2) & 3
+        return ((g << 1) & 2) ^ ((g >> 1) * 3)
+
+    assert sorted(pswz(2 * i) for i in range(8)) == list(range(8))
+    assert sorted(qswz(4 * i) for i in range(4)) == list(range(4))
+    sets = [[(r, kg) for r in range(16)] for kg in range(4)]
+    for kg in (0, 2):
+        for a, b in ((kg, kg + 1), (kg + 1, kg)):
+            sets.append([(r, a if r < 4 or r >= 12 else b) for r in range(16)])
+    for lanes in sets:
+        for half in (0, 1):
+            assert len({(r * 128 + (((2 * kg + half) ^ pswz(r)) << 4)) % 256 // 16 for r, kg in lanes}) == 16
+        assert len({(r * 64 + ((kg ^ qswz(r)) << 4)) % 256 // 16 for r, kg in lanes}) == 16
+    # K along the rows: 64 lanes on 64 banks
+    for wave in range(8):
+        for a in (0, 1):
+            for e in range(8):
+                at = [(kg * 8 + e) * 1024 + ((((wave * 32 + a * 16 + r) >> 2) ^ (kg << 2)) << 4) + (r & 3) * 4
+                      for kg in range(4) for r in range(16)]
+                assert len({x % 256 // 4 for x in at}) == 64
+                # and each holds its own element: chunk c of row k at c ^ 4 (k / 8 mod 4)
+                for i, x in enumerate(at):
+                    k, chunk = x // 1024, x % 1024 // 16
+                    assert ((chunk ^ (((k >> 3) & 3) << 2)) * 4 + x % 16 // 4) == wave * 32 + a * 16 + i % 16

@@ -289,3 +289,51 @@ def test_split_products_in_two_pieces(gpu):
     y = labels_of(g, 5, 2000)
     got, dH, dW = run_xent(H, W, y, dloss)
     compare(got, R.head(H, W, dloss, labels=y), dH, dW)
+
+
+@pytest.mark.parametrize("pad", [0, 8])
+@pytest.mark.parametrize("n,vocab,dim", [(1, 1, 4), (5, 300, 20), (64, 513, 36), (130, 256, 100), (63, 1000, 1028),
+                                         (3, 20000, 8), (512, 700, 260), (513, 300, 128)])
+def test_fp32_head_read_in_place(gpu, n, vocab, dim, pad):
+    """Rows of whole 16 bytes: up to 512 tokens W is read as it lies, with ends of dim
+    and of the vocabulary inside a tile and a stage; 513 tokens take the copies."""
+    g, H, W, dloss = inputs(n, vocab, dim, F32, n + vocab + dim, pad)
+    y = labels_of(g, n, vocab)
+    got, dH, dW = run_xent(H, W, y, dloss, pad)
+    compare(got, R.head(H, W, dloss, labels=y), dH, dW)
+
+
+def test_fp32_values_of_the_whole_range(gpu):
+    """Values that would round to infinity in bf16, and ones with few significant bits."""
+    g, H, W, dloss = inputs(40, 300, 64, F32, 83)
+    y = labels_of(g, 40, 300)
+    W[7] = torch.finfo(F32).max                      # finite, beyond the largest bf16
+    H *= 1e-30
+    W[8] = 2.0 ** torch.arange(64, device="cuda")
+    got, dH, dW = run_xent(H, W, y, dloss)
+    assert torch.isfinite(dH).all() and torch.isfinite(dW).all()
+    want = R.head(H, W, dloss, labels=y)
+    for k, v in (("loss", got[0]), ("lse", got[1])):
+        assert ((v.double() - want[k]).abs() <= want["b_" + k]).all()
+
+
+@pytest.mark.parametrize("n", [40, 600])
+def test_fp32_infinities_stay_visible(gpu, n):
+    """An infinity or NaN in a row of W reaches every token's loss as a value that is
+    not finite; one in a masked token's H reaches nothing."""
+    g, H, W, dloss = inputs(n, 300, 64, F32, 89)
+    y = torch.randint(0, 300, (n,), generator=g, device="cuda")
+    y[5] = -1
+    H[5] = float("inf")
+    got, dH, dW = run_xent(H, W, y, dloss)
+    clean = H.clone()
+    clean[5] = 0
+    base, bH, bW = run_xent(clean, W, y, dloss)
+    assert all(torch.equal(a, b) for a, b in zip((*got, dH, dW), (*base, bH, bW)))
+    for bad in (float("inf"), float("nan")):
+        V = W.clone()
+        V[9, 3] = bad
+        loss, lse = mo.softmax_xent_forward(clean, V, y)
+        live = y >= 0
+        # 0 x infinity or a positive infinity; a logit of minus infinity is a finite loss
+        assert (~torch.isfinite(lse[live])).any() and loss[5] == 0 and lse[5] == 0

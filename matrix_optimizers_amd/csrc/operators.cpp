@@ -7,7 +7,6 @@
 
 #include <algorithm>
 #include <cmath>
-#include <vector>
 
 #include "../../include/mo.h"
 #include "host_common.h"
@@ -42,15 +41,30 @@ bool dtype_ok(int32_t d) { return d == MO_F32 || d == MO_BF16; }
 
 Range vec_range(const void* p, int64_t n, int64_t es, int writable) { return matrix_range(p, 1, n, n, es, writable); }
 
+// The ranges of one call, at most ten: no allocation, so no exception can reach the
+// C entry points.
+struct Ranges {
+    Range r[12];
+    int n = 0;
+    void add(const Range& x) { r[n++] = x; }
+    // Any overlap between a writable range and any other?
+    bool conflict() const {
+        for (int i = 0; i < n; ++i)
+            for (int j = 0; j < i; ++j)
+                if ((r[i].writable || r[j].writable) && r[i].lo < r[j].hi && r[j].lo < r[i].hi) return true;
+        return false;
+    }
+};
+
 // The workspace as a range and its aligned base; false when it is too small.
-bool take_workspace(void* workspace, size_t have, uint64_t need, std::vector<Range>* ranges, uint8_t** base) {
+bool take_workspace(void* workspace, size_t have, uint64_t need, Ranges* ranges, uint8_t** base) {
     if (need == 0) {
         *base = nullptr;
         return true;
     }
     if (!workspace || have < need + MO_WS_ALIGN) return false;
     const uintptr_t w = reinterpret_cast<uintptr_t>(workspace);
-    ranges->push_back(Range{w, w + have, 1});
+    ranges->add(Range{w, w + have, 1});
     *base = reinterpret_cast<uint8_t*>(align_up(w, MO_WS_ALIGN));
     return true;
 }
@@ -303,26 +317,26 @@ mo_status topk_targets(const mo_topk* t, Targets* out) {
 }
 
 // Ranges of what every head call reads.
-void head_inputs(const MoHeadArgs& a, std::vector<Range>* r) {
+void head_inputs(const MoHeadArgs& a, Ranges* r) {
     const int64_t es = elem_size(a.dtype);
-    r->push_back(matrix_range(a.H, a.tokens, a.dim, a.ldh, es, 0));
-    r->push_back(matrix_range(a.W, a.vocab, a.dim, a.ldw, es, 0));
-    r->push_back(matrix_range(a.ids, a.tokens, a.k, a.ld_ids, 8, 0));
-    if (a.teacher) r->push_back(matrix_range(a.teacher, a.tokens, a.k, a.ld_teacher, elem_size(a.teacher_dtype), 0));
+    r->add(matrix_range(a.H, a.tokens, a.dim, a.ldh, es, 0));
+    r->add(matrix_range(a.W, a.vocab, a.dim, a.ldw, es, 0));
+    r->add(matrix_range(a.ids, a.tokens, a.k, a.ld_ids, 8, 0));
+    if (a.teacher) r->add(matrix_range(a.teacher, a.tokens, a.k, a.ld_teacher, elem_size(a.teacher_dtype), 0));
 }
 
 mo_status head_forward(MoHeadArgs& a, void* workspace, size_t workspace_bytes, void* stream, bool distill) {
     if (a.tokens == 0) return MO_OK;
     if (!a.H || !a.W || !a.ids || !a.loss || !a.lse || (distill && (!a.teacher || !a.z))) return MO_ERR_INVALID_ARG;
     const MoHeadPlan p = head_plan(a, false, false, false);
-    std::vector<Range> ranges;
+    Ranges ranges;
     head_inputs(a, &ranges);
-    ranges.push_back(vec_range(a.loss, a.tokens, 4, 1));
-    ranges.push_back(vec_range(a.lse, a.tokens, 4, 1));
-    if (distill) ranges.push_back(vec_range(a.z, a.tokens * a.k, 4, 1));
+    ranges.add(vec_range(a.loss, a.tokens, 4, 1));
+    ranges.add(vec_range(a.lse, a.tokens, 4, 1));
+    if (distill) ranges.add(vec_range(a.z, a.tokens * a.k, 4, 1));
     uint8_t* ws;
     if (!take_workspace(workspace, workspace_bytes, p.bytes, &ranges, &ws)) return MO_ERR_WORKSPACE_TOO_SMALL;
-    if (ranges_conflict(ranges)) return MO_ERR_ALIAS;
+    if (ranges.conflict()) return MO_ERR_ALIAS;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     if (p.pack_h) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_pack(a, p, ws, true, 0, a.tokens, s));
     if (distill) MO_RUN(MO_PHASE_HD_TARGET, mo_launch_head_targets(a, s));
@@ -356,18 +370,18 @@ mo_status head_backward(MoHeadArgs& a, void* workspace, size_t workspace_bytes, 
     if (!a.H || !a.W || !a.ids || !a.lse_in || !a.dloss) return MO_ERR_INVALID_ARG;
     if (distill ? (!a.teacher || !a.z_in) : !a.loss_in) return MO_ERR_INVALID_ARG;
     const MoHeadPlan p = head_plan(a, true, a.dH != nullptr, a.dW != nullptr);
-    std::vector<Range> ranges;
+    Ranges ranges;
     head_inputs(a, &ranges);
     const int64_t es = elem_size(a.dtype);
-    ranges.push_back(vec_range(a.lse_in, a.tokens, 4, 0));
-    ranges.push_back(vec_range(a.dloss, a.tokens, 4, 0));
-    if (distill) ranges.push_back(vec_range(a.z_in, a.tokens * a.k, 4, 0));
-    else ranges.push_back(vec_range(a.loss_in, a.tokens, 4, 0));
-    if (a.dH) ranges.push_back(matrix_range(a.dH, a.tokens, a.dim, a.lddh, es, 1));
-    if (a.dW) ranges.push_back(matrix_range(a.dW, a.vocab, a.dim, a.lddw, es, 1));
+    ranges.add(vec_range(a.lse_in, a.tokens, 4, 0));
+    ranges.add(vec_range(a.dloss, a.tokens, 4, 0));
+    if (distill) ranges.add(vec_range(a.z_in, a.tokens * a.k, 4, 0));
+    else ranges.add(vec_range(a.loss_in, a.tokens, 4, 0));
+    if (a.dH) ranges.add(matrix_range(a.dH, a.tokens, a.dim, a.lddh, es, 1));
+    if (a.dW) ranges.add(matrix_range(a.dW, a.vocab, a.dim, a.lddw, es, 1));
     uint8_t* ws;
     if (!take_workspace(workspace, workspace_bytes, p.bytes, &ranges, &ws)) return MO_ERR_WORKSPACE_TOO_SMALL;
-    if (ranges_conflict(ranges)) return MO_ERR_ALIAS;
+    if (ranges.conflict()) return MO_ERR_ALIAS;
     MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_prep(a, p, ws, s));
     if (p.pack_h) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_pack(a, p, ws, true, 0, a.tokens, s));
     if (a.dW) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_ht(a, p, ws, s));
@@ -426,12 +440,14 @@ mo_status layer_norm_forward(const void* X, int64_t ld_x, const float* weight, c
     a.dtype = dtype;
     a.eps = eps;
     const int64_t es = elem_size(dtype);
-    std::vector<Range> r = {matrix_range(X, rows, cols, a.ldx, es, 0), matrix_range(Y, rows, cols, a.ldy, es, 1)};
-    if (weight) r.push_back(vec_range(weight, cols, 4, 0));
-    if (bias) r.push_back(vec_range(bias, cols, 4, 0));
-    if (mean) r.push_back(vec_range(mean, rows, 4, 1));
-    if (rstd) r.push_back(vec_range(rstd, rows, 4, 1));
-    if (ranges_conflict(r)) return MO_ERR_ALIAS;
+    Ranges r;
+    r.add(matrix_range(X, rows, cols, a.ldx, es, 0));
+    r.add(matrix_range(Y, rows, cols, a.ldy, es, 1));
+    if (weight) r.add(vec_range(weight, cols, 4, 0));
+    if (bias) r.add(vec_range(bias, cols, 4, 0));
+    if (mean) r.add(vec_range(mean, rows, 4, 1));
+    if (rstd) r.add(vec_range(rstd, rows, 4, 1));
+    if (r.conflict()) return MO_ERR_ALIAS;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     MO_RUN(MO_PHASE_LN_FWD, mo_launch_ln_fwd(a, s));
     return MO_OK;
@@ -469,22 +485,22 @@ mo_status layer_norm_backward(const void* dY, int64_t ld_dy, const void* X, int6
     a.dtype = dtype;
     const bool sums = dweight || dbias;
     const int64_t es = elem_size(dtype);
-    std::vector<Range> r;
+    Ranges r;
     if (rows) {
         if (!X || !dY || !mean || !rstd) return MO_ERR_INVALID_ARG;
-        r.push_back(matrix_range(X, rows, cols, a.ldx, es, 0));
-        r.push_back(matrix_range(dY, rows, cols, a.lddy, es, 0));
-        r.push_back(vec_range(mean, rows, 4, 0));
-        r.push_back(vec_range(rstd, rows, 4, 0));
-        if (dX) r.push_back(matrix_range(dX, rows, cols, a.lddx, es, 1));
+        r.add(matrix_range(X, rows, cols, a.ldx, es, 0));
+        r.add(matrix_range(dY, rows, cols, a.lddy, es, 0));
+        r.add(vec_range(mean, rows, 4, 0));
+        r.add(vec_range(rstd, rows, 4, 0));
+        if (dX) r.add(matrix_range(dX, rows, cols, a.lddx, es, 1));
     }
-    if (weight) r.push_back(vec_range(weight, cols, 4, 0));
-    if (dweight) r.push_back(vec_range(dweight, cols, 4, 1));
-    if (dbias) r.push_back(vec_range(dbias, cols, 4, 1));
+    if (weight) r.add(vec_range(weight, cols, 4, 0));
+    if (dweight) r.add(vec_range(dweight, cols, 4, 1));
+    if (dbias) r.add(vec_range(dbias, cols, 4, 1));
     uint8_t* ws = nullptr;
     if (!take_workspace(workspace, workspace_bytes, sums ? align_up(ln_bwd_bytes(rows, cols), MO_WS_ALIGN) : 0, &r, &ws))
         return MO_ERR_WORKSPACE_TOO_SMALL;
-    if (ranges_conflict(r)) return MO_ERR_ALIAS;
+    if (r.conflict()) return MO_ERR_ALIAS;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     float* part = reinterpret_cast<float*>(ws);
     if (rows) MO_RUN(MO_PHASE_LN_BWD, mo_launch_ln_bwd(a, part, s));
@@ -511,9 +527,11 @@ mo_status embedding_forward(const int64_t* tokens, int64_t n, const void* W, int
     a.w_dtype = dtype;
     a.scale = scale;
     const int64_t es = elem_size(dtype);
-    std::vector<Range> r = {vec_range(tokens, n, 8, 0), matrix_range(Y, n, dim, a.ldy, es, 1)};
-    if (vocab) r.push_back(matrix_range(W, vocab, dim, a.ldw, es, 0));
-    if (ranges_conflict(r)) return MO_ERR_ALIAS;
+    Ranges r;
+    r.add(vec_range(tokens, n, 8, 0));
+    r.add(matrix_range(Y, n, dim, a.ldy, es, 1));
+    if (vocab) r.add(matrix_range(W, vocab, dim, a.ldw, es, 0));
+    if (r.conflict()) return MO_ERR_ALIAS;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     MO_RUN(MO_PHASE_EMB_FWD, mo_launch_emb_fwd(a, s));
     return MO_OK;
@@ -549,14 +567,15 @@ mo_status embedding_backward(const int64_t* tokens, int64_t n, const void* dY, i
     a.accumulate = accumulate != 0;
     a.scale = scale;
     const MoEmbPlan p = emb_plan(n, vocab, dim);
-    std::vector<Range> r = {matrix_range(G, vocab, dim, a.ldg, elem_size(g_dtype), 1)};
+    Ranges r;
+    r.add(matrix_range(G, vocab, dim, a.ldg, elem_size(g_dtype), 1));
     if (n) {
-        r.push_back(vec_range(tokens, n, 8, 0));
-        r.push_back(matrix_range(dY, n, dim, a.lddy, elem_size(dy_dtype), 0));
+        r.add(vec_range(tokens, n, 8, 0));
+        r.add(matrix_range(dY, n, dim, a.lddy, elem_size(dy_dtype), 0));
     }
     uint8_t* ws;
     if (!take_workspace(workspace, workspace_bytes, p.bytes, &r, &ws)) return MO_ERR_WORKSPACE_TOO_SMALL;
-    if (ranges_conflict(r)) return MO_ERR_ALIAS;
+    if (r.conflict()) return MO_ERR_ALIAS;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     if (n == 0) {
         MO_RUN(MO_PHASE_EMB_BWD, mo_launch_emb_fill(a, s));

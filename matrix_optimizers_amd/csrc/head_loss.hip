@@ -88,8 +88,7 @@ __global__ __launch_bounds__(256) void head_pack_kernel(const T* src, int64_t ld
 // `packed` the rows as read go there too (head_pack_kernel's layout), so that a
 // piece of fp32 W is read once for both.  The tiles are taken in blocks of 8 x 8:
 // workgroups that run together then read whole 1 KB pieces of rows and write
-// whole 1 KB pieces of columns (131 MB of bf16 with its transpose: 45 us tile row by
-// tile row).
+// whole 1 KB pieces of columns (302 MB read and written in 63 us, 4.8 TB/s).
 template <typename T, int PL>
 __global__ __launch_bounds__(256) void head_transpose_kernel(const T* src, int64_t ld, int64_t rows, int dim,
                                                              const float* coef, bf16_t* dst, int64_t ldt,
@@ -297,7 +296,7 @@ __global__ __launch_bounds__(64) void head_lse_sum_kernel(LogitSums sums, int64_
 
 // z[n][j] = H_n . W_id (not yet divided by T), 0 where the id is outside the
 // vocabulary: one wavefront per token and G of its ids, whose rows it requests
-// together (G = 8 at 4096 tokens x 64 ids x 2048: 165 us with one id per wavefront).
+// together (4096 tokens x 64 ids x 2048: 135 us, 165 with one id per wavefront).
 template <typename T, int G>
 __global__ __launch_bounds__(256) void head_target_kernel(const T* H, int64_t ldh, const T* W, int64_t ldw,
                                                           const int64_t* ids, int64_t ld_ids, int k,
@@ -685,8 +684,8 @@ __device__ __forceinline__ void dw_tile(uint8_t* smem, const DwJob& j, uint32_t 
 // One launch: dW and dH of a piece and delta of the next one.  The three do not
 // depend on each other (two sets of D, DT and WT), and together they leave one
 // partly filled last round per piece instead of three.  At 8192 tokens x 128256 x
-// 4096: 19.4 ms for the 26 TFLOP of the three, 18.9 in this order with pieces of
-// 84 tiles, 20.1 in three launches of their own; without any store it would be
+// 4096 (seven pieces) the launches take 18.9 to 19.6 ms for 26 TFLOP, 0.5 more with dH
+// before dW and 1.2 more as three launches per piece; without any store it would be
 // 17.5 (delta's 4 bytes per logit 0.7, the fp32 sums of dH 0.7, dW 0.3).
 template <typename T, int NB, int NBW, int PL>
 __global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) void head_step_kernel(
@@ -795,8 +794,8 @@ hipError_t mo_launch_head_pack(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t
 }
 
 // The splits of a piece's logits, and where their sums are read.
-static hipError_t split_logits(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, const Operand& W, LogitSums* sums,
-                               hipStream_t s) {
+static hipError_t split_logits(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, const Operand& W,
+                               LogitSums* sums, hipStream_t s) {
     SplitJob j = {};
     j.P = W;
     j.Q = h_operand(a, p, ws);

@@ -83,6 +83,23 @@ __global__ __launch_bounds__(256) void head_pack_kernel(const T* src, int64_t ld
     }
 }
 
+// dst[r][c] <- src[r][c], c < k4: fp32 rows of whole 16 bytes, zeros behind dim.
+__global__ __launch_bounds__(256) void head_copy_kernel(const float* src, int64_t ld, int64_t rows, int dim, float* dst,
+                                                        int k4) {
+    const int64_t chunks = int64_t(k4 / 4) * rows;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < chunks; i += int64_t(gridDim.x) * 256) {
+        const int64_t r = i / (k4 / 4);
+        const int c = int(i - r * (k4 / 4)) * 4;
+        const float* p = src + r * ld + c;
+        f32x4 v;
+        if (c + 4 <= dim) v = *reinterpret_cast<const f32x4_e4*>(p);
+        else
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = c + e < dim ? p[e] : 0.f;
+        *reinterpret_cast<f32x4*>(dst + r * k4 + c) = v;
+    }
+}
+
 // dst[plane][c][ldt] <- src[r][c] in 64 x 64 tiles; rows from `rows` up to 64 tr are
 // zero, and so are the rows whose coefficient is 0 (they may hold anything).  With
 // `packed` the rows as read go there too (head_pack_kernel's layout), so that a
@@ -751,7 +768,9 @@ Operand rows_of(const void* p, int64_t ld_elems, int64_t rows, int64_t plane_ele
 Operand h_operand(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws) {
     return p.pack_h ? rows_of(ws + p.off_hp, p.kd, a.tokens, a.tokens * p.kd) : rows_of(a.H, a.ldh, a.tokens, 0);
 }
-Operand w_operand(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int64_t v0, int64_t rows) {
+// W's rows of piece k.
+Operand w_operand(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int k, int64_t v0, int64_t rows) {
+    if (p.f32w && p.pack_w) return {ws + p.off_wt[k & 1], p.k4 * 4, rows, 0};
     if (p.f32w) return {static_cast<const uint8_t*>(a.W) + v0 * a.ldw * 4, a.ldw * 4, rows, 0};
     return p.pack_w ? rows_of(ws + p.off_wp, p.kd, rows, p.piece * p.kd)
                     : rows_of(static_cast<const bf16_t*>(a.W) + v0 * a.ldw, a.ldw, rows, 0);
@@ -793,13 +812,21 @@ hipError_t mo_launch_head_pack(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t
               int(a.dim), dst, int(p.kd), plane);
 }
 
+// Piece k of an fp32 W whose rows are not whole 16 bytes.
+hipError_t mo_launch_head_copy(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int k, int64_t v0, int64_t rows,
+                               hipStream_t s) {
+    const dim3 grid(cap_grid((rows * (p.k4 / 4) + 255) / 256, 1 << 16)), block(256);
+    return go(head_copy_kernel, grid, block, s, static_cast<const float*>(a.W) + v0 * a.ldw, a.ldw, rows, int(a.dim),
+              reinterpret_cast<float*>(ws + p.off_wt[k & 1]), int(p.k4));
+}
+
 // The splits of a piece's logits, and where their sums are read.
 static hipError_t split_logits(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, const Operand& W,
                                LogitSums* sums, hipStream_t s) {
     SplitJob j = {};
     j.P = W;
     j.Q = h_operand(a, p, ws);
-    j.dim = int(a.dim);
+    j.dim = int(p.k4);
     j.nk = int(p.kd / 64);
     j.stages = p.z_stages;
     j.tm = uint32_t((W.rows + 255) / 256);
@@ -817,7 +844,7 @@ static hipError_t split_logits(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t
 
 hipError_t mo_launch_head_lse(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int64_t v0, int64_t rows,
                               hipStream_t s) {
-    const Operand H = h_operand(a, p, ws), W = w_operand(a, p, ws, v0, rows);
+    const Operand H = h_operand(a, p, ws), W = w_operand(a, p, ws, 0, v0, rows);
     const uint32_t tm = uint32_t((rows + 255) / 256), tn = uint32_t(p.n_pad / (64 * p.nb));
     float2* part = reinterpret_cast<float2*>(ws + p.off_part) + v0 / 256 * p.n_pad * (p.z_splits > 1 ? 8 : 1);
     if (p.z_splits > 1) {
@@ -831,7 +858,7 @@ hipError_t mo_launch_head_lse(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t*
     }
     const dim3 grid(head_grid(uint64_t(tm) * tn)), block(H_THREADS);
     if (p.f32w)
-        return go(head_lse_kernel<1, F32W>, grid, block, s, W, int(a.dim), H, int(p.kd / 64), tm, tn, a.inv_t, part,
+        return go(head_lse_kernel<1, F32W>, grid, block, s, W, int(p.k4), H, int(p.kd / 64), tm, tn, a.inv_t, part,
                   p.n_pad);
 #define MO_CALL(NB, PL) \
     return go(head_lse_kernel<NB, PL>, grid, block, s, W, int(a.dim), H, int(p.kd / 64), tm, tn, a.inv_t, part, p.n_pad)
@@ -923,9 +950,9 @@ hipError_t mo_launch_head_patch(const MoHeadArgs& a, const MoHeadPlan& p, uint8_
 
 static DeltaJob delta_job(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int k, int64_t v0, int64_t rows) {
     DeltaJob dl = {};
-    dl.W = w_operand(a, p, ws, v0, rows);
+    dl.W = w_operand(a, p, ws, k, v0, rows);
     dl.H = h_operand(a, p, ws);
-    dl.dim = int(a.dim);
+    dl.dim = int(p.k4);
     dl.nk = int(p.kd / 64);
     dl.tm = uint32_t((rows + 255) / 256);
     dl.tn = uint32_t(p.n_pad / (64 * p.nb));
@@ -964,8 +991,8 @@ hipError_t mo_launch_head_step(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t
     DeltaJob dl = {};
     const uint32_t tn = uint32_t(p.n_pad / (64 * p.nb)), tm = uint32_t((rows + 255) / 256);
     if (rows && a.dH) {
-        dh.P = p.f32w ? w_operand(a, p, ws, v0, rows) : rows_of(ws + p.off_wt[k & 1], p.ld_p, a.dim, a.dim * p.ld_p);
-        dh.dim = int(a.dim);
+        dh.P = p.f32w ? w_operand(a, p, ws, k, v0, rows) : rows_of(ws + p.off_wt[k & 1], p.ld_p, a.dim, a.dim * p.ld_p);
+        dh.dim = int(p.k4);
         dh.Q = rows_of(ws + p.off_d[k & 1], p.ld_p, p.n_pad, p.n_pad * p.ld_p);
         dh.nk = int(tm * 4);   // the piece's rows, rounded up to whole tiles
         dh.stages = p.dh_stages;
@@ -979,7 +1006,7 @@ hipError_t mo_launch_head_step(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t
     if (rows && a.dW) {
         dw.DT = rows_of(ws + p.off_dt[k & 1], p.ld_t, rows, p.piece * p.ld_t);
         dw.HT = rows_of(ws + p.off_ht, p.ld_t, a.dim, a.dim * p.ld_t);
-        dw.nk = int(p.n_pad / 64);
+        dw.nk = int((a.tokens + 63) / 64);
         dw.tm = tm;
         dw.tn = uint32_t((a.dim + 64 * p.nb_dw - 1) / (64 * p.nb_dw));
         dw.dW = static_cast<uint8_t*>(a.dW) + v0 * a.lddw * (p.planes == 1 ? 2 : 4);

@@ -163,11 +163,12 @@ bool in_place(const void* p, int64_t ld, int64_t dim) {
            ld * 2 < (int64_t(1) << 23);
 }
 
-// Up to 512 tokens an fp32 W is read in place, in tiles of 64 tokens; more tokens pay for
+// Up to 512 tokens an fp32 W is read as fp32, in tiles of 64 tokens, in place or, where
+// its rows are not whole 16 bytes, from a padded copy; more tokens pay for
 // splitting it into planes once.  A step at 32001 rows x 4096 (us, in place and
 // planes): 64 tokens 598 and 1790, 256 1654 and 2277, 512 3106 and 3342; at
 // 32001 x 1000: 512 833 and 855, 1021 1611 and 1467.
-constexpr int64_t kF32InPlaceTokens = 512;
+constexpr int64_t kF32Tokens = 512;
 bool f32_in_place(const void* p, int64_t ld, int64_t dim) {
     return dim % 4 == 0 && ((reinterpret_cast<uintptr_t>(p) | uintptr_t(ld * 4)) & 15) == 0 &&
            ld * 4 < (int64_t(1) << 23);
@@ -214,18 +215,20 @@ MoHeadPlan head_plan(const MoHeadArgs& a, bool backward, bool need_dh, bool need
     p.planes = a.dtype == MO_BF16 ? 1 : 3;
     p.v_tiles = (a.vocab + 255) / 256;
     p.kd = k_extent(a.dim);
-    p.f32w = p.planes == 3 && a.tokens <= kF32InPlaceTokens && f32_in_place(a.W, a.ldw, a.dim);
+    p.f32w = p.planes == 3 && a.tokens <= kF32Tokens;
+    p.k4 = (a.dim + 3) / 4 * 4;
     p.nb = token_tile(a.tokens, p.v_tiles, p.kd / 64, p.planes, p.f32w ? 1 : 4);
     p.n_pad = (a.tokens + 64 * p.nb - 1) / (64 * p.nb) * (64 * p.nb);
     p.pack_h = p.planes != 1 || !in_place(a.H, a.ldh, a.dim);
-    p.pack_w = !p.f32w && (p.planes != 1 || !in_place(a.W, a.ldw, a.dim));
+    p.pack_w = p.f32w ? !f32_in_place(a.W, a.ldw, a.dim) : p.planes != 1 || !in_place(a.W, a.ldw, a.dim);
     p.nb_dw = a.dim <= 128 ? 1 : 4;
     const int64_t tn = p.n_pad / (64 * p.nb);
     // equal pieces bounded by the memory of their copies (and by the grid of one launch);
     // at least one tile
-    int64_t row = p.pack_w ? 2 * p.planes * p.kd : 0;
+    const int64_t copy = !p.pack_w ? 0 : p.f32w ? 4 * p.k4 : 2 * p.planes * p.kd;   // bytes of a row
+    int64_t row = copy;
     // (the same pieces whichever gradients are asked for, so that the size query holds for each)
-    if (backward) row += 2 * (4 * p.planes * p.n_pad + (p.f32w ? 0 : 2 * p.planes * a.dim));
+    if (backward) row += 2 * 4 * p.planes * p.n_pad + (p.f32w ? copy : 4 * p.planes * a.dim);
     int64_t most = std::min<int64_t>((int64_t(1) << 22) / std::max<int64_t>(tn, (a.dim + 63) / 64), 1 << 13);
     if (row) most = std::min(most, (backward ? kHeadPieceBytes : kHeadPieceBytes / 4) / row / 256);
     most = std::max<int64_t>(most, 1);
@@ -241,7 +244,9 @@ MoHeadPlan head_plan(const MoHeadArgs& a, bool backward, bool need_dh, bool need
     Carve take;
     if (p.z_splits > 1) p.off_z = take(uint64_t(4) * p.z_splits * z_tiles * 256 * 64 * p.nb);
     if (p.pack_h) p.off_hp = take(uint64_t(2) * p.planes * a.tokens * p.kd);
-    if (p.pack_w) p.off_wp = take(uint64_t(2) * p.planes * p.piece * p.kd);
+    if (p.pack_w && !p.f32w) p.off_wp = take(uint64_t(copy) * p.piece);
+    if (p.pack_w && p.f32w)
+        for (int i = 0; i < (backward && pieces > 1 ? 2 : 1); ++i) p.off_wt[i] = take(uint64_t(copy) * p.piece);
     if (!backward) {
         p.off_part = take(uint64_t(8) * p.v_tiles * (p.z_splits > 1 ? 8 : 1) * p.n_pad);
     } else {
@@ -342,7 +347,8 @@ mo_status head_forward(MoHeadArgs& a, void* workspace, size_t workspace_bytes, v
     if (distill) MO_RUN(MO_PHASE_HD_TARGET, mo_launch_head_targets(a, s));
     for (int64_t v0 = 0; v0 < a.vocab; v0 += p.piece) {
         const int64_t rows = std::min(p.piece, a.vocab - v0);
-        if (p.pack_w) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_pack(a, p, ws, false, v0, rows, s));
+        if (p.pack_w && p.f32w) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_copy(a, p, ws, 0, v0, rows, s));
+        else if (p.pack_w) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_pack(a, p, ws, false, v0, rows, s));
         MO_RUN(MO_PHASE_HD_LSE, mo_launch_head_lse(a, p, ws, v0, rows, s));
     }
     MO_RUN(MO_PHASE_HD_TARGET, mo_launch_head_loss(a, p, ws, s));
@@ -391,7 +397,8 @@ mo_status head_backward(MoHeadArgs& a, void* workspace, size_t workspace_bytes, 
         const int64_t v0 = k * p.piece, rows = k < pieces ? std::min(p.piece, a.vocab - v0) : 0;
         if (rows) {
             // the transpose for dH makes the copy as well
-            if (a.dH && !p.f32w) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_wt(a, p, ws, k, v0, rows, s));
+            if (p.pack_w && p.f32w) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_copy(a, p, ws, k, v0, rows, s));
+            else if (a.dH && !p.f32w) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_wt(a, p, ws, k, v0, rows, s));
             else if (p.pack_w) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_pack(a, p, ws, false, v0, rows, s));
         }
         const int64_t last = k ? std::min(p.piece, a.vocab - (v0 - p.piece)) : 0, beside = p.z_splits > 1 ? 0 : rows;

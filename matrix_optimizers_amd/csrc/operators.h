@@ -74,7 +74,8 @@ struct MoHeadPlan {
     int nb, nb_dw;          // tile width (64 nb): tokens side; dim side of dW
     int64_t n_pad;          // tokens rounded up to the tile width
     int64_t kd;             // dim as a K extent (rounded up, zeros behind)
-    bool f32w;              // fp32 W read in place (few tokens)
+    bool f32w;              // fp32 W read as fp32 (few tokens)
+    int64_t k4;             // dim rounded up to 16 bytes of fp32
     bool pack_h, pack_w;    // operand copied (padded, split) before use
     int64_t piece;          // vocabulary rows per piece (a multiple of 256)
     int64_t ld_t, ld_p;     // row strides of the copies along the tokens and along the piece
@@ -88,6 +89,8 @@ struct MoHeadPlan {
 };
 hipError_t mo_launch_head_pack(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, bool h, int64_t v0,
                                int64_t rows, hipStream_t s);
+hipError_t mo_launch_head_copy(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int k, int64_t v0, int64_t rows,
+                               hipStream_t s);
 hipError_t mo_launch_head_lse(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int64_t v0, int64_t rows,
                               hipStream_t s);
 hipError_t mo_launch_head_targets(const MoHeadArgs& a, hipStream_t s);

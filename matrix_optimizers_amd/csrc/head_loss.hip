@@ -13,8 +13,10 @@
 // the usual mean over rows every c_n is a power of two, and the label's delta,
 // -(1 - p), the largest of its row, is rounded like that number.  Rounded as
 // -(1 - p) / count it would carry nearly the same mantissa, and the same error of up
-// to half a unit, in every row: at 8192 tokens x 128256 x 4096 bf16 the error of dH
-// was 3.0e-3 of its norm; it is 2.0e-3, against 1.7e-3 for the result's rounding alone.
+// to half a unit, in every row.  What rounding takes from delta at a row's targets is
+// added to its dH (head_residual_kernel).  The error of dH at 8192 tokens x 128256 x
+// 4096 bf16 was 3.0e-3 of its norm without the two, 2.0e-3 with the first; it is at
+// most 1.8e-3, 1.7e-3 of which is the result's rounding.
 //
 // Forward: one product whose epilogue keeps, per tile and token, the maximum
 // and the sum of exponentials over the tile's 256 vocabulary rows; the target
@@ -469,13 +471,14 @@ MO_DEV float ref_scale(const float* dloss, int64_t tokens, float t) {
     return 1.f;
 }
 
+// res (bf16): what rounding leaves of delta at a target, for head_residual_kernel.
 // coef[n] = T dloss_n / r (0: the row takes no part), nl2[n] = -lse_n log2 e, delta at
 // the label, c (exp(z_y - lse) - 1) = c expm1(-loss), and r itself.
 __global__ __launch_bounds__(256) void head_xent_prep_kernel(const int64_t* labels, const float* loss,
                                                              const float* lse, const float* dloss,
                                                              int64_t tokens, int64_t n_pad, int64_t vocab,
                                                              float* coef, float* nl2, float* tval,
-                                                             float* ref) {
+                                                             float* res, float* ref) {
     const float r = ref_scale(dloss, tokens, 1.f);
     const int64_t n = int64_t(blockIdx.x) * 256 + threadIdx.x;
     if (n == 0) *ref = r;
@@ -487,7 +490,10 @@ __global__ __launch_bounds__(256) void head_xent_prep_kernel(const int64_t* labe
     }
     coef[n] = c;
     nl2[n] = l;
-    if (n < tokens) tval[n] = c != 0.f ? c * expm1f(-loss[n]) : 0.f;
+    if (n >= tokens) return;
+    const float t = c != 0.f ? c * expm1f(-loss[n]) : 0.f;
+    tval[n] = t;
+    if (res) res[n] = t - (float)(bf16_t)t;
 }
 
 // The same for distillation, one wavefront per row; the entries of an id that a
@@ -498,7 +504,7 @@ __global__ __launch_bounds__(256) void head_distill_prep_kernel(const int64_t* i
                                                                 int64_t vocab, float inv_t, float t,
                                                                 const float* z, const float* lse,
                                                                 const float* dloss, float* coef, float* nl2,
-                                                                float* tval, float* ref) {
+                                                                float* tval, float* res, float* ref) {
     const float r = ref_scale(dloss, tokens, t);
     const int lane = threadIdx.x & 63;
     const int64_t n = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
@@ -516,14 +522,19 @@ __global__ __launch_bounds__(256) void head_distill_prep_kernel(const int64_t* i
         for (int j = lane; j < k; j += 64) {
             const int64_t v = id[j];
             float o = 0.f;
+            bool again = false;   // the id has come before
             if (c != 0.f && uint64_t(v) < uint64_t(vocab)) {
                 float p = 0.f;
                 for (int u = 0; u < k; ++u)
-                    if (id[u] == v) p += expf(load_elem(te, u, t_bf16) * inv_t - mt) / st;
+                    if (id[u] == v) {
+                        p += expf(load_elem(te, u, t_bf16) * inv_t - mt) / st;
+                        again |= u < j;
+                    }
                 const float q = expf(z[n * k + j] * inv_t - l);   // at most 1, as in delta_rows
                 o = c * ((q > 1.f ? 1.f : q) - p);
             }
             tval[n * k + j] = o;
+            if (res) res[n * k + j] = again ? 0.f : o - (float)(bf16_t)o;
         }
     }
     if (lane == 0) {
@@ -651,6 +662,46 @@ __global__ __launch_bounds__(256) void head_patch_kernel(const int64_t* ids, int
     }
 }
 
+// bf16: what delta's rounding at a row's targets takes from its dH, corr[n] =
+// sum_j res_nj W[id_nj] (rounded to bf16, a 2^-16th of dH), added before dH is rounded.
+// The targets' deltas are the largest of a row, in a batch of few tokens the only
+// ones that count.  One wavefront per token and 512 columns, eight rows of W
+// requested together: 46 us at 8192
+// tokens x 4096, 156 at 4096 x 2048 with 64 targets each (1.07 GB of W's rows, 6.9 TB/s
+// with what the caches serve).
+__global__ __launch_bounds__(256) void head_residual_kernel(const bf16_t* W, int64_t ldw, const int64_t* ids,
+                                                            int64_t ld_ids, int k, const float* res,
+                                                            int64_t tokens, int64_t vocab, int dim, bf16_t* corr) {
+    const int lane = threadIdx.x & 63, slabs = (dim + 511) / 512;
+    const int64_t items = tokens * slabs;
+    for (int64_t it = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6); it < items; it += int64_t(gridDim.x) * 4) {
+        const int64_t n = it / slabs;
+        const int c = (int(it - n * slabs) * 64 + lane) * 8;
+        f32x8 sum;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum.v[e] = 0.f;
+        for (int j0 = 0; j0 < k; j0 += 8) {
+            float r[8];
+            raw8<bf16_t> x[8];
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+                const int64_t v = j0 + g < k ? ids[n * ld_ids + j0 + g] : -1;
+                const bool in = uint64_t(v) < uint64_t(vocab);
+                r[g] = in ? res[n * k + j0 + g] : 0.f;
+                x[g] = ld8n(W + (in ? v : 0) * ldw + c, in ? dim - c : 0);
+            }
+#pragma unroll
+            for (int g = 0; g < 8; ++g)
+                if (r[g] != 0.f) {
+                    const f32x8 w = widen(x[g]);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) sum.v[e] = __builtin_fmaf(r[g], w.v[e], sum.v[e]);
+                }
+        }
+        st8n(corr + n * dim + c, sum, dim - c);
+    }
+}
+
 // ---- backward: the two products of a piece --------------------------------------------
 
 // dW rows of the piece = r DT HT^T (K over the tokens), rounded to T.
@@ -721,12 +772,13 @@ __global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) 
     delta_tile<NB, PL>(smem, dl, b - dh.blocks);
 }
 
-// dH <- r times the sum of the splits in order: one workgroup per 16 columns of dH and
+// dH <- r times the sum of the splits in order (and corr, in bf16): one workgroup per 16 columns of dH and
 // the 64 tokens of a wave's block, turned through LDS.  Tokens that take no part
 // get zeros.
 template <typename T, int NB>
 __global__ __launch_bounds__(256) void head_dh_out_kernel(const f32x4* acc, uint32_t tm, uint32_t tn,
-                                                          uint32_t splits, const float* coef, const float* ref, T* dH,
+                                                          uint32_t splits, const float* coef, const float* ref,
+                                                          const T* corr, T* dH,
                                                           int64_t ld, int64_t tokens, int dim) {
     using L = Layout<NB>;
     __shared__ float tile[64][20];
@@ -754,7 +806,14 @@ __global__ __launch_bounds__(256) void head_dh_out_kernel(const f32x4* acc, uint
             const float r = *ref;
             f32x8 o;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o.v[e] = on ? r * tile[j][c + e] : 0.f;
+            for (int e = 0; e < 8; ++e) o.v[e] = tile[j][c + e];
+            if constexpr (sizeof(T) == 2) {
+                const f32x8 x = widen(ld8n(corr + (n0 + j) * dim + c0 + c, dim - c0 - c));
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o.v[e] += x.v[e];
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o.v[e] = on ? r * o.v[e] : 0.f;
             st8n(dH + (n0 + j) * ld + c0 + c, o, dim - c0 - c);
         }
     }
@@ -899,12 +958,13 @@ hipError_t mo_launch_head_loss(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t
 hipError_t mo_launch_head_prep(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, hipStream_t s) {
     float *coef = reinterpret_cast<float*>(ws + p.off_coef), *nl2 = reinterpret_cast<float*>(ws + p.off_nl2);
     float *tval = reinterpret_cast<float*>(ws + p.off_tval), *ref = reinterpret_cast<float*>(ws + p.off_ref);
+    float* res = p.planes == 1 && a.dH ? reinterpret_cast<float*>(ws + p.off_res) : nullptr;
     if (!a.teacher)
         return go(head_xent_prep_kernel, dim3(unsigned((p.n_pad + 255) / 256)), dim3(256), s, a.ids, a.loss_in,
-                  a.lse_in, a.dloss, a.tokens, p.n_pad, a.vocab, coef, nl2, tval, ref);
+                  a.lse_in, a.dloss, a.tokens, p.n_pad, a.vocab, coef, nl2, tval, res, ref);
     return go(head_distill_prep_kernel, dim3(unsigned((p.n_pad + 3) / 4)), dim3(256), s, a.ids, a.ld_ids, a.teacher,
               a.ld_teacher, a.teacher_dtype == MO_BF16, a.k, a.tokens, p.n_pad, a.vocab, a.inv_t, a.t, a.z_in,
-              a.lse_in, a.dloss, coef, nl2, tval, ref);
+              a.lse_in, a.dloss, coef, nl2, tval, res, ref);
 }
 
 // Transposes `rows` rows (and pads them to tr tiles of 64); with `packed` copies them too.
@@ -1038,9 +1098,17 @@ hipError_t mo_launch_head_dh_out(const MoHeadArgs& a, const MoHeadPlan& p, uint8
                 *ref = reinterpret_cast<const float*>(ws + p.off_ref);
     // 8 waves x MB row blocks, MB = 2 NB
     const dim3 grid(p.dh_tm * p.dh_tn * 16 * p.nb), block(256);
+    void* corr = ws + p.off_corr;
+    if (p.planes == 1) {
+        const dim3 items(cap_grid((a.tokens * ((a.dim + 511) / 512) + 3) / 4, 1 << 20));
+        const hipError_t e = go(head_residual_kernel, items, block, s, static_cast<const bf16_t*>(a.W), a.ldw, a.ids,
+                                a.ld_ids, a.k, reinterpret_cast<const float*>(ws + p.off_res), a.tokens, a.vocab,
+                                int(a.dim), static_cast<bf16_t*>(corr));
+        if (e != hipSuccess) return e;
+    }
 #define MO_OUT(T, NB)                                                                                    \
     return go(head_dh_out_kernel<T, NB>, grid, block, s, acc, p.dh_tm, p.dh_tn, uint32_t(p.dh_splits), coef, ref, \
-              static_cast<T*>(a.dH), a.lddh, a.tokens, int(a.dim))
+              static_cast<const T*>(corr), static_cast<T*>(a.dH), a.lddh, a.tokens, int(a.dim))
     if (p.planes == 1) {
         if (p.nb == 4) MO_OUT(bf16_t, 4);
         if (p.nb == 2) MO_OUT(bf16_t, 2);

@@ -254,6 +254,10 @@ MoHeadPlan head_plan(const MoHeadArgs& a, bool backward, bool need_dh, bool need
         p.off_nl2 = take(uint64_t(4) * p.n_pad);
         p.off_tval = take(uint64_t(4) * a.tokens * a.k);
         p.off_ref = take(4);
+        if (p.planes == 1 && need_dh) {
+            p.off_res = take(uint64_t(4) * a.tokens * a.k);
+            p.off_corr = take(uint64_t(2) * a.tokens * a.dim);
+        }
         const int sets = pieces > 1 ? 2 : 1;
         for (int i = 0; i < sets; ++i) {
             p.off_d[i] = take(uint64_t(2) * p.planes * p.n_pad * p.ld_p);

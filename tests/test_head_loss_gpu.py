@@ -337,3 +337,32 @@ def test_fp32_infinities_stay_visible(gpu, n):
         live = y >= 0
         # 0 x infinity or a positive infinity; a logit of minus infinity is a finite loss
         assert (~torch.isfinite(lse[live])).any() and loss[5] == 0 and lse[5] == 0
+
+
+@pytest.mark.parametrize("n,vocab,dim,k", [(3, 5000, 64, 0), (70, 3000, 513, 0), (2, 4000, 72, 5), (70, 3000, 96, 9),
+                                           (600, 2000, 260, 17)])
+def test_targets_lose_no_precision_in_dH(gpu, n, vocab, dim, k):
+    """Logits near zero: delta is about 1 / vocab away from the targets, so what its
+    rounding there adds to dH is at most 2^-8 / sqrt(vocab / targets) of it, and the
+    targets' own rounding is made up for: dH is as near as its rounding to bf16
+    (2 % more for the rest: 2^-8 / sqrt(2000 / 17) against 1.7e-3, in squares)."""
+    g = gen(97 + n)
+    W = rand(g, (vocab, dim), BF, 1.0)
+    H = rand(g, (n, dim), BF, 1e-3)
+    dloss = torch.rand(n, generator=g, device="cuda") + 0.1
+    if k:
+        ids = torch.randint(0, vocab, (n, k), generator=g, device="cuda")
+        ids[:, -1] = ids[:, 0]                       # one id twice
+        ids[0, 1] = -1
+        t = torch.randn((n, k), generator=g, device="cuda")
+        _, lse, z = mo.topk_distill_forward(H, W, ids, t)
+        dH, _ = mo.topk_distill_backward(H, W, ids, t, lse, z, dloss)
+        want = R.head(H, W, dloss, ids=ids, teacher=t)["dH"]
+    else:
+        y = torch.randint(0, vocab, (n,), generator=g, device="cuda")
+        loss, lse = mo.softmax_xent_forward(H, W, y)
+        dH, _ = mo.softmax_xent_backward(H, W, y, loss, lse, dloss)
+        want = R.head(H, W, dloss, labels=y)["dH"]
+    own = float((want.to(BF).double() - want).norm())
+    err = float((dH.double() - want).norm())
+    assert err <= 1.02 * own, err / own

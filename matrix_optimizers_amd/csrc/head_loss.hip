@@ -201,7 +201,7 @@ __global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) 
     split_tile<NB, PL, false>(smem, j, blockIdx.x);
 }
 // One wavefront's unit of those sums: 32 rows x 64 tokens of tile (ti, tj).
-struct LogitSums {
+struct SplitSums {
     const f32x4* z;
     uint32_t tm, tn, splits;
 };
@@ -209,7 +209,7 @@ template <int NB> struct Unit {
     uint32_t ti, tj;
     int row, col;   // of the unit inside its tile
     f32x4 acc[2][4];
-    MO_DEV Unit(const LogitSums& s, uint32_t block) {
+    MO_DEV Unit(const SplitSums& s, uint32_t block) {
         using L = Layout<NB>;
         const uint32_t pair = block % NB, wave = block / NB % 8, tile = block / (8 * NB);
         ti = tile / s.tn;
@@ -287,7 +287,7 @@ __global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) 
 
 // The same from the sums of the splits, one partial per 32 vocabulary rows.
 template <int NB>
-__global__ __launch_bounds__(64) void head_lse_sum_kernel(LogitSums sums, int64_t rows, float zscale, float2* part,
+__global__ __launch_bounds__(64) void head_lse_sum_kernel(SplitSums sums, int64_t rows, float zscale, float2* part,
                                                           int64_t n_pad) {
     const Unit<NB> u(sums, blockIdx.x);
     const int lane = threadIdx.x, r16 = lane & 15, kg = lane >> 4;
@@ -630,7 +630,7 @@ __device__ __forceinline__ void delta_tile(uint8_t* smem, const DeltaJob& j, uin
 
 // The same from the sums of the splits.
 template <int NB, int PL>
-__global__ __launch_bounds__(64) void head_delta_sum_kernel(LogitSums sums, DeltaJob j) {
+__global__ __launch_bounds__(64) void head_delta_sum_kernel(SplitSums sums, DeltaJob j) {
     __shared__ __align__(16) uint8_t st[32 * 64 * 4];
     const Unit<NB> u(sums, blockIdx.x);
     const int64_t v0 = int64_t(u.ti) * 256 + u.row, tok = int64_t(u.tj) * (64 * NB) + u.col;
@@ -704,49 +704,76 @@ __global__ __launch_bounds__(256) void head_residual_kernel(const bf16_t* W, int
 
 // ---- backward: the two products of a piece --------------------------------------------
 
-// dW rows of the piece = r DT HT^T (K over the tokens), rounded to T.
+// dW rows of the piece = r DT HT^T (K over the tokens), rounded to T; or, where that
+// has few tiles (a small vocabulary and many tokens), the fp32 sums of `splits`
+// splits of K in `out` (null: none), for head_dw_sum_kernel.  A step of 8000
+// tokens x 1000 rows x 256 (4 tiles of 125 stages) takes 88 us in bf16, 181 in
+// fp32; 196 and 854 without.
 struct DwJob {
     Operand DT, HT;
-    int nk;
-    uint32_t tm, tn, blocks;
+    int nk, stages;
+    uint32_t tm, tn, splits, blocks;
+    f32x4* out;
     void* dW;
     int64_t ldw;
     int dim;
     const float* ref;
 };
+// 32 rows x 64 columns of a wavefront, through its 8 KB of LDS.
+template <typename T>
+__device__ __forceinline__ void dw_rows(uint8_t* st, const DwJob& j, const f32x4 (*acc)[4], float r, int64_t vrow,
+                                        int64_t col) {
+    const int lane = threadIdx.x & 63, r16 = lane & 15, kg = lane >> 4;
+    T* dW = static_cast<T*>(j.dW);
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+            *reinterpret_cast<f32x4*>(st + st_off(b * 16 + r16, g * 16 + kg * 4)) = acc[g][b];
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const int cc = lane & 7, row = (lane >> 3) + 8 * t;
+        f32x8 v;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v.v[e] = r * *reinterpret_cast<const float*>(st + st_off(cc * 8 + e, row));
+        const int64_t vr = vrow + row;
+        const int c = int(col) + cc * 8;
+        if (vr < j.DT.rows) st8n(dW + vr * j.ldw + c, v, j.dim - c);
+    }
+    __builtin_amdgcn_wave_barrier();
+}
 template <typename T, int NB, int PL>
 __device__ __forceinline__ void dw_tile(uint8_t* smem, const DwJob& j, uint32_t block) {
     using L = Layout<NB>;
     uint32_t ti, tj;
-    if (!head_tile_of(block, j.tm, j.tn, ti, tj)) return;
+    if (!head_tile_of(block, j.tm * j.splits, j.tn, ti, tj)) return;
+    const uint32_t sp = ti / j.tm;
+    ti -= sp * j.tm;
+    const int k0 = int(sp) * j.stages, n = j.nk - k0 < j.stages ? j.nk - k0 : j.stages;
     const int64_t v0 = int64_t(ti) * 256, c0 = int64_t(tj) * 64 * NB;
     f32x4 acc[L::MB][L::NBW];
-    head_tile<NB, PL == 1 ? 1 : 3>(smem, j.DT, j.HT, v0, c0, 0, j.nk, acc);
-    T* dW = static_cast<T*>(j.dW);
-    const float r = *j.ref;
+    head_tile<NB, PL == 1 ? 1 : 3>(smem, j.DT, j.HT, v0, c0, k0, n, acc);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int wm = wave / L::WN, wn = wave % L::WN, r16 = lane & 15, kg = lane >> 4;
-    uint8_t* st = smem + wave * (32 * 64 * 4);
+    const int wm = wave / L::WN, wn = wave % L::WN;
+    if (j.out) {
+        f32x4* o = j.out + (((int64_t(sp) * j.tm + ti) * j.tn + tj) * 8 + wave) * (L::MB * L::NBW * 64) + lane;
 #pragma unroll
-    for (int a = 0; a < L::MB; a += 2) {
+        for (int a = 0; a < L::MB; ++a)
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
-#pragma unroll
-            for (int g = 0; g < 2; ++g)
-                *reinterpret_cast<f32x4*>(st + st_off(b * 16 + r16, g * 16 + kg * 4)) = acc[a + g][b];
-        __builtin_amdgcn_wave_barrier();
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const int cc = lane & 7, row = (lane >> 3) + 8 * t;
-            f32x8 v;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v.v[e] = r * *reinterpret_cast<const float*>(st + st_off(cc * 8 + e, row));
-            const int64_t vr = v0 + wm * (L::MB * 16) + a * 16 + row;
-            const int c = int(c0) + wn * 64 + cc * 8;
-            if (vr < j.DT.rows) st8n(dW + vr * j.ldw + c, v, j.dim - c);
-        }
-        __builtin_amdgcn_wave_barrier();
+            for (int b = 0; b < L::NBW; ++b) o[(a * L::NBW + b) * 64] = acc[a][b];
+        return;
     }
+    const float r = *j.ref;
+#pragma unroll
+    for (int a = 0; a < L::MB; a += 2)
+        dw_rows<T>(smem + wave * (32 * 64 * 4), j, &acc[a], r, v0 + wm * (L::MB * 16) + a * 16, c0 + wn * 64);
+}
+template <typename T, int NB>
+__global__ __launch_bounds__(64) void head_dw_sum_kernel(SplitSums sums, DwJob j) {
+    __shared__ __align__(16) uint8_t st[32 * 64 * 4];
+    const Unit<NB> u(sums, blockIdx.x);
+    dw_rows<T>(st, j, u.acc, *j.ref, int64_t(u.ti) * 256 + u.row, int64_t(u.tj) * (64 * NB) + u.col);
 }
 
 // One launch: dW and dH of a piece and delta of the next one.  The three do not
@@ -881,7 +908,7 @@ hipError_t mo_launch_head_copy(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t
 
 // The splits of a piece's logits, and where their sums are read.
 static hipError_t split_logits(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, const Operand& W,
-                               LogitSums* sums, hipStream_t s) {
+                               SplitSums* sums, hipStream_t s) {
     SplitJob j = {};
     j.P = W;
     j.Q = h_operand(a, p, ws);
@@ -907,7 +934,7 @@ hipError_t mo_launch_head_lse(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t*
     const uint32_t tm = uint32_t((rows + 255) / 256), tn = uint32_t(p.n_pad / (64 * p.nb));
     float2* part = reinterpret_cast<float2*>(ws + p.off_part) + v0 / 256 * p.n_pad * (p.z_splits > 1 ? 8 : 1);
     if (p.z_splits > 1) {
-        LogitSums sums;
+        SplitSums sums;
         const hipError_t e = split_logits(a, p, ws, W, &sums, s);
         if (e != hipSuccess) return e;
         const dim3 units(tm * tn * 8 * uint32_t(p.nb)), wave(64);
@@ -1033,7 +1060,7 @@ static DeltaJob delta_job(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws,
 hipError_t mo_launch_head_delta_split(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int k, int64_t v0,
                                       int64_t rows, hipStream_t s) {
     const DeltaJob dl = delta_job(a, p, ws, k, v0, rows);
-    LogitSums sums;
+    SplitSums sums;
     const hipError_t e = split_logits(a, p, ws, dl.W, &sums, s);
     if (e != hipSuccess) return e;
     const dim3 units(dl.tm * dl.tn * 8 * uint32_t(p.nb)), wave(64);
@@ -1067,29 +1094,40 @@ hipError_t mo_launch_head_step(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t
         dw.DT = rows_of(ws + p.off_dt[k & 1], p.ld_t, rows, p.piece * p.ld_t);
         dw.HT = rows_of(ws + p.off_ht, p.ld_t, a.dim, a.dim * p.ld_t);
         dw.nk = int((a.tokens + 63) / 64);
+        dw.stages = p.dw_stages;
+        dw.splits = uint32_t(p.dw_splits);
+        dw.out = p.dw_splits > 1 ? reinterpret_cast<f32x4*>(ws + p.off_dw) : nullptr;
         dw.tm = tm;
         dw.tn = uint32_t((a.dim + 64 * p.nb_dw - 1) / (64 * p.nb_dw));
         dw.dW = static_cast<uint8_t*>(a.dW) + v0 * a.lddw * (p.planes == 1 ? 2 : 4);
         dw.ldw = a.lddw;
         dw.dim = int(a.dim);
         dw.ref = reinterpret_cast<const float*>(ws + p.off_ref);
-        dw.blocks = head_grid(uint64_t(dw.tm) * dw.tn);
+        dw.blocks = head_grid(uint64_t(dw.tm) * dw.tn * dw.splits);
     }
     if (next_rows) dl = delta_job(a, p, ws, k + 1, next_v0, next_rows);
     const dim3 grid(dh.blocks + dw.blocks + dl.blocks), block(H_THREADS);
+    hipError_t e;
 #define MO_STEP(T, NB, PL)                                                                             \
-    return p.nb_dw == 4 ? go(head_step_kernel<T, NB, 4, PL>, grid, block, s, dh, dw, dl)               \
-                        : go(head_step_kernel<T, NB, 1, PL>, grid, block, s, dh, dw, dl)
+    e = p.nb_dw == 4 ? go(head_step_kernel<T, NB, 4, PL>, grid, block, s, dh, dw, dl)               \
+                     : go(head_step_kernel<T, NB, 1, PL>, grid, block, s, dh, dw, dl)
     if (p.planes == 1) {
         if (p.nb == 4) MO_STEP(bf16_t, 4, 1);
-        if (p.nb == 2) MO_STEP(bf16_t, 2, 1);
-        MO_STEP(bf16_t, 1, 1);
-    }
-    if (p.f32w) MO_STEP(float, 1, F32W);
-    if (p.nb == 4) MO_STEP(float, 4, 3);
-    if (p.nb == 2) MO_STEP(float, 2, 3);
-    MO_STEP(float, 1, 3);
+        else if (p.nb == 2) MO_STEP(bf16_t, 2, 1);
+        else MO_STEP(bf16_t, 1, 1);
+    } else if (p.f32w) MO_STEP(float, 1, F32W);
+    else if (p.nb == 4) MO_STEP(float, 4, 3);
+    else if (p.nb == 2) MO_STEP(float, 2, 3);
+    else MO_STEP(float, 1, 3);
 #undef MO_STEP
+    if (e != hipSuccess || !dw.out) return e;
+    const SplitSums sums = {dw.out, dw.tm, dw.tn, dw.splits};
+    const dim3 units(dw.tm * dw.tn * 8 * uint32_t(p.nb_dw)), wave(64);
+    if (p.planes == 1)
+        return p.nb_dw == 4 ? go(head_dw_sum_kernel<bf16_t, 4>, units, wave, s, sums, dw)
+                            : go(head_dw_sum_kernel<bf16_t, 1>, units, wave, s, sums, dw);
+    return p.nb_dw == 4 ? go(head_dw_sum_kernel<float, 4>, units, wave, s, sums, dw)
+                        : go(head_dw_sum_kernel<float, 1>, units, wave, s, sums, dw);
 }
 
 hipError_t mo_launch_head_dh_out(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, hipStream_t s) {

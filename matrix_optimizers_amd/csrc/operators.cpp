@@ -174,14 +174,14 @@ bool f32_in_place(const void* p, int64_t ld, int64_t dim) {
            ld * 4 < (int64_t(1) << 23);
 }
 
-// Estimated us of the logits' product in `tiles` tiles of 256 x 64 nb with `stages`
+// Estimated us of a product in `tiles` tiles of 256 x 64 nb with `stages`
 // stages of 64 K, and the splits of K that it takes.  A stage takes 1.43, 0.8 and
 // 0.6 us in a tile of 256, 128 and 64 tokens (256 CUs at 1.5 PFLOP/s; the narrow ones
 // wait for their loads), six times that with three planes; splits write and read
 // fp32 tiles at 5 TB/s, are added up one after the other, and are one launch more.
 // In all, a step of 4405 rows x 34 tokens x 4672 went from 177 to 107 us in bf16
 // with splits, 5168 x 40 x 256 (4 stages) stays without at 49 us.
-double logits_us(int64_t tiles, int64_t stages, int nb, int planes, int64_t* splits) {
+double product_us(int64_t tiles, int64_t stages, int nb, int planes, int64_t* splits) {
     const double stage = (nb == 4 ? 1.43 : nb == 2 ? 0.8 : 0.6) * (planes == 1 ? 1 : 6);
     double least = double((tiles + 255) / 256 * stages) * stage;
     *splits = 1;
@@ -201,7 +201,7 @@ int token_tile(int64_t n, int64_t v_tiles, int64_t stages, int planes, int wides
     double least = 0;
     for (int nb = widest; nb >= 1; nb /= 2) {
         int64_t splits;
-        const double t = logits_us((n + 64 * nb - 1) / (64 * nb) * v_tiles, stages, nb, planes, &splits);
+        const double t = product_us((n + 64 * nb - 1) / (64 * nb) * v_tiles, stages, nb, planes, &splits);
         if (nb == widest || t < least) {
             least = t;
             best = nb;
@@ -238,7 +238,7 @@ MoHeadPlan head_plan(const MoHeadArgs& a, bool backward, bool need_dh, bool need
     p.ld_p = copy_stride(p.piece);
     const int64_t z_tiles = p.piece / 256 * tn, nk = p.kd / 64;
     int64_t z_want;
-    logits_us(z_tiles, nk, p.nb, p.planes, &z_want);
+    product_us(z_tiles, nk, p.nb, p.planes, &z_want);
     p.z_stages = int((nk + z_want - 1) / z_want);
     p.z_splits = int((nk + p.z_stages - 1) / p.z_stages);
     Carve take;
@@ -266,6 +266,12 @@ MoHeadPlan head_plan(const MoHeadArgs& a, bool backward, bool need_dh, bool need
         }
         if (need_dw) {
             p.off_ht = take(uint64_t(2) * p.planes * a.dim * p.ld_t);
+            const int64_t tiles = p.piece / 256 * ((a.dim + 64 * p.nb_dw - 1) / (64 * p.nb_dw)), nk_dw = (a.tokens + 63) / 64;
+            int64_t want;
+            product_us(tiles, nk_dw, p.nb_dw, p.planes, &want);
+            p.dw_stages = int((nk_dw + want - 1) / want);
+            p.dw_splits = int((nk_dw + p.dw_stages - 1) / p.dw_stages);
+            if (p.dw_splits > 1) p.off_dw = take(uint64_t(4) * p.dw_splits * tiles * 256 * 64 * p.nb_dw);
         }
         if (need_dh) {
             p.dh_tm = uint32_t((a.dim + 255) / 256);

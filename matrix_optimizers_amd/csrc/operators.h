@@ -84,8 +84,9 @@ struct MoHeadPlan {
     int dh_stages, dh_splits;
     uint32_t dh_tm, dh_tn;
     int z_stages, z_splits; // logits: K stages per split, splits (1: none)
+    int dw_stages, dw_splits; // dW: the same
     uint64_t off_part, off_hp, off_wp, off_coef, off_nl2, off_tval, off_res, off_corr, off_ref, off_ht, off_wt[2],
-        off_d[2], off_dt[2], off_acc, off_z;
+        off_d[2], off_dt[2], off_acc, off_z, off_dw;
     uint64_t bytes;
 };
 hipError_t mo_launch_head_pack(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, bool h, int64_t v0,

@@ -283,6 +283,18 @@ def test_long_products_of_few_tiles(gpu, n, vocab, dim, dtype):
     compare(got, R.head(H, W, dloss, labels=y), dH, dW)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,vocab,dim", [(2000, 300, 100), (1787, 1000, 404), (5000, 40, 64), (900, 513, 130)])
+def test_many_tokens_of_a_small_vocabulary(gpu, n, vocab, dim, dtype):
+    """dW of few tiles with many tokens: its sums over the tokens are split as well."""
+    g, H, W, dloss = inputs(n, vocab, dim, dtype, n + vocab)
+    y = labels_of(g, n, vocab)
+    got, dH, dW = run_xent(H, W, y, dloss, 3)
+    compare(got, R.head(H, W, dloss, labels=y), dH, dW)
+    again = mo.softmax_xent_backward(H, W, y, *got, dloss)
+    assert torch.equal(again[0], dH) and torch.equal(again[1], dW)
+
+
 def test_split_products_in_two_pieces(gpu):
     """The longest rows there are: two pieces of the vocabulary, each split along K."""
     g, H, W, dloss = inputs(5, 2000, 65536, F32, 71)

@@ -191,7 +191,7 @@ __device__ __forceinline__ void split_tile(uint8_t* smem, const SplitJob& j, uin
         }
 }
 
-// The logits of a piece with fewer than 128 tiles, which would leave more than half
+// The logits (and dW) of a piece with fewer than 128 tiles, which would leave more than half
 // of the CUs idle: K is split over the others, and the forward's and the
 // backward's epilogues add the splits up in order.  4405 rows x 34 tokens x 4672
 // (18 tiles): the forward takes 36 us in bf16, 67 without splits.
@@ -704,16 +704,15 @@ __global__ __launch_bounds__(256) void head_residual_kernel(const bf16_t* W, int
 
 // ---- backward: the two products of a piece --------------------------------------------
 
-// dW rows of the piece = r DT HT^T (K over the tokens), rounded to T; or, where that
-// has few tiles (a small vocabulary and many tokens), the fp32 sums of `splits`
-// splits of K in `out` (null: none), for head_dw_sum_kernel.  A step of 8000
+// dW rows of the piece = r DT HT^T (K over the tokens), rounded to T.  Where that has
+// few tiles (a small vocabulary and many tokens) K is split, in a launch of its own
+// (head_split_kernel), and head_dw_sum_kernel adds the splits up.  A step of 8000
 // tokens x 1000 rows x 256 (4 tiles of 125 stages) takes 88 us in bf16, 181 in
 // fp32; 196 and 854 without.
 struct DwJob {
     Operand DT, HT;
-    int nk, stages;
-    uint32_t tm, tn, splits, blocks;
-    f32x4* out;
+    int nk;
+    uint32_t tm, tn, blocks;
     void* dW;
     int64_t ldw;
     int dim;
@@ -747,23 +746,11 @@ template <typename T, int NB, int PL>
 __device__ __forceinline__ void dw_tile(uint8_t* smem, const DwJob& j, uint32_t block) {
     using L = Layout<NB>;
     uint32_t ti, tj;
-    if (!head_tile_of(block, j.tm * j.splits, j.tn, ti, tj)) return;
-    const uint32_t sp = ti / j.tm;
-    ti -= sp * j.tm;
-    const int k0 = int(sp) * j.stages, n = j.nk - k0 < j.stages ? j.nk - k0 : j.stages;
+    if (!head_tile_of(block, j.tm, j.tn, ti, tj)) return;
     const int64_t v0 = int64_t(ti) * 256, c0 = int64_t(tj) * 64 * NB;
     f32x4 acc[L::MB][L::NBW];
-    head_tile<NB, PL == 1 ? 1 : 3>(smem, j.DT, j.HT, v0, c0, k0, n, acc);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int wm = wave / L::WN, wn = wave % L::WN;
-    if (j.out) {
-        f32x4* o = j.out + (((int64_t(sp) * j.tm + ti) * j.tn + tj) * 8 + wave) * (L::MB * L::NBW * 64) + lane;
-#pragma unroll
-        for (int a = 0; a < L::MB; ++a)
-#pragma unroll
-            for (int b = 0; b < L::NBW; ++b) o[(a * L::NBW + b) * 64] = acc[a][b];
-        return;
-    }
+    head_tile<NB, PL == 1 ? 1 : 3>(smem, j.DT, j.HT, v0, c0, 0, j.nk, acc);
+    const int wave = threadIdx.x >> 6, wm = wave / L::WN, wn = wave % L::WN;
     const float r = *j.ref;
 #pragma unroll
     for (int a = 0; a < L::MB; a += 2)
@@ -1094,24 +1081,23 @@ hipError_t mo_launch_head_step(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t
         dw.DT = rows_of(ws + p.off_dt[k & 1], p.ld_t, rows, p.piece * p.ld_t);
         dw.HT = rows_of(ws + p.off_ht, p.ld_t, a.dim, a.dim * p.ld_t);
         dw.nk = int((a.tokens + 63) / 64);
-        dw.stages = p.dw_stages;
-        dw.splits = uint32_t(p.dw_splits);
-        dw.out = p.dw_splits > 1 ? reinterpret_cast<f32x4*>(ws + p.off_dw) : nullptr;
         dw.tm = tm;
         dw.tn = uint32_t((a.dim + 64 * p.nb_dw - 1) / (64 * p.nb_dw));
         dw.dW = static_cast<uint8_t*>(a.dW) + v0 * a.lddw * (p.planes == 1 ? 2 : 4);
         dw.ldw = a.lddw;
         dw.dim = int(a.dim);
         dw.ref = reinterpret_cast<const float*>(ws + p.off_ref);
-        dw.blocks = head_grid(uint64_t(dw.tm) * dw.tn * dw.splits);
+        dw.blocks = p.dw_splits > 1 ? 0 : head_grid(uint64_t(dw.tm) * dw.tn);
     }
     if (next_rows) dl = delta_job(a, p, ws, k + 1, next_v0, next_rows);
     const dim3 grid(dh.blocks + dw.blocks + dl.blocks), block(H_THREADS);
-    hipError_t e;
+    hipError_t e = hipSuccess;
 #define MO_STEP(T, NB, PL)                                                                             \
     e = p.nb_dw == 4 ? go(head_step_kernel<T, NB, 4, PL>, grid, block, s, dh, dw, dl)               \
                      : go(head_step_kernel<T, NB, 1, PL>, grid, block, s, dh, dw, dl)
-    if (p.planes == 1) {
+    if (grid.x == 0) {
+        // dW alone, in splits
+    } else if (p.planes == 1) {
         if (p.nb == 4) MO_STEP(bf16_t, 4, 1);
         else if (p.nb == 2) MO_STEP(bf16_t, 2, 1);
         else MO_STEP(bf16_t, 1, 1);
@@ -1120,14 +1106,28 @@ hipError_t mo_launch_head_step(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t
     else if (p.nb == 2) MO_STEP(float, 2, 3);
     else MO_STEP(float, 1, 3);
 #undef MO_STEP
-    if (e != hipSuccess || !dw.out) return e;
-    const SplitSums sums = {dw.out, dw.tm, dw.tn, dw.splits};
-    const dim3 units(dw.tm * dw.tn * 8 * uint32_t(p.nb_dw)), wave(64);
-    if (p.planes == 1)
-        return p.nb_dw == 4 ? go(head_dw_sum_kernel<bf16_t, 4>, units, wave, s, sums, dw)
-                            : go(head_dw_sum_kernel<bf16_t, 1>, units, wave, s, sums, dw);
-    return p.nb_dw == 4 ? go(head_dw_sum_kernel<float, 4>, units, wave, s, sums, dw)
-                        : go(head_dw_sum_kernel<float, 1>, units, wave, s, sums, dw);
+    if (e != hipSuccess || !dw.tm || p.dw_splits == 1) return e;
+    SplitJob j = {};
+    j.P = dw.DT;
+    j.Q = dw.HT;
+    j.nk = dw.nk;
+    j.stages = p.dw_stages;
+    j.tm = dw.tm;
+    j.tn = dw.tn;
+    j.splits = uint32_t(p.dw_splits);
+    j.first = 1;
+    j.out = reinterpret_cast<f32x4*>(ws + p.off_dw);
+    const SplitSums sums = {j.out, j.tm, j.tn, j.splits};
+    const dim3 sgrid(head_grid(uint64_t(j.tm) * j.tn * j.splits)), units(j.tm * j.tn * 8 * uint32_t(p.nb_dw)), wave(64);
+    const bool wide = p.nb_dw == 4;
+    if (p.planes == 1) {
+        e = go(wide ? head_split_kernel<4, 1> : head_split_kernel<1, 1>, sgrid, block, s, j);
+        if (e != hipSuccess) return e;
+        return go(wide ? head_dw_sum_kernel<bf16_t, 4> : head_dw_sum_kernel<bf16_t, 1>, units, wave, s, sums, dw);
+    }
+    e = go(wide ? head_split_kernel<4, 3> : head_split_kernel<1, 3>, sgrid, block, s, j);
+    if (e != hipSuccess) return e;
+    return go(wide ? head_dw_sum_kernel<float, 4> : head_dw_sum_kernel<float, 1>, units, wave, s, sums, dw);
 }
 
 hipError_t mo_launch_head_dh_out(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, hipStream_t s) {

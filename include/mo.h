@@ -497,11 +497,12 @@ typedef struct mo_head {
 mo_status softmax_xent_workspace_bytes(const mo_head* head, int32_t backward, size_t* bytes);
 
 /* Softmax cross entropy: lse_n = log(sum_v exp(z_nv)), loss_n = lse_n - z_n,label,
- * both fp32 per token.  A label outside 0 .. vocab - 1 marks a position without
- * a target (padding): its loss and lse are 0 and its H row, which may hold
- * anything, takes no part in any gradient.  bf16 tensors go through bf16 MFMA
- * with fp32 accumulation; fp32 ones as three bf16 parts each, to fp32
- * accuracy (an infinity in a row that counts gives NaN).
+ * both fp32 per token, from one sum of products, so that no loss is negative and
+ * one near 0 holds nothing of the logits' rounding.  A label outside 0 .. vocab
+ * - 1 marks a position without a target (padding): its loss and lse are 0 and
+ * its H row, which may hold anything, takes no part in any gradient.  bf16
+ * tensors go through bf16 MFMA with fp32 accumulation; fp32 ones as three bf16
+ * parts each, to fp32 accuracy (an infinity in a row that counts gives NaN).
  * Errors: MO_ERR_INVALID_ARG (null pointer with tokens > 0, tokens < 0, vocab or
  * dim < 1, bad stride), MO_ERR_UNSUPPORTED (dtype, tokens > 2^20, vocab > 2^26,
  * dim > 2^16), MO_ERR_WORKSPACE_TOO_SMALL, MO_ERR_ALIAS, MO_ERR_HIP. */

@@ -18,9 +18,14 @@
 // 4096 bf16 was 3.0e-3 of its norm without the two, 2.0e-3 with the first; it is at
 // most 1.8e-3, 1.7e-3 of which is the result's rounding.
 //
-// Forward: one product whose epilogue keeps, per tile and token, the maximum
-// and the sum of exponentials over the tile's 256 vocabulary rows; the target
-// logits are gathered dot products.  Backward: pieces of the vocabulary, each
+// Forward: one product whose epilogue keeps, per tile and token, the maximum m of
+// the logits and the sum s of exp((z - m) / T) over the tile's 256 vocabulary rows.
+// A loss takes log q = (z_y - m) / T - log s, so z_y has to be the very number whose
+// maximum m is: of a token the model is sure of, nothing but rounding would be left
+// of a logit summed in another order (losses of +-1.5e-5 at logits of 60, and deltas
+// like them).  The label's logit is taken from the product's accumulators, a
+// teacher's k ids' from products of the same instructions in the same order.  With
+// equal bits m - z_y >= 0 and s >= 1, so no cross entropy is negative.  Backward: pieces of the vocabulary, each
 // computed again from H and W into delta (bf16, or the three planes of fp32),
 // in both orientations, from which dW's rows are finished and dH accumulated
 // in fp32; one launch does that for a piece and computes the next one's delta.
@@ -29,6 +34,8 @@
 // Rounding: the logits are never rounded (fp32 accumulators); delta takes the
 // tensors' own precision (bf16: half a unit in 2^8, the size of the rounding
 // of the results themselves; fp32: exact); sums are fp32.
+#include <type_traits>
+
 #include "head_gemm.h"
 #include "op_common.h"
 #include "operators.h"
@@ -55,21 +62,24 @@ MO_DEV float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // ---- operand copies ---------------------------------------------------------------
 
+// The three planes of 8 elements.
+MO_DEV void split_planes(const f32x8& v, bf16x8 (&p)[3]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        bf16_t a, b, c;
+        split_f32(v.v[e], a, b, c);
+        p[0][e] = a; p[1][e] = b; p[2][e] = c;
+    }
+}
 // One 8-element chunk of a value's planes (16 bytes each).
 template <int PL> MO_DEV void put_planes(bf16_t* dst, int64_t plane, const f32x8& v) {
     if constexpr (PL == 1) {
         st8(dst, v);
     } else {
-        bf16x8 h, m, l;
+        bf16x8 p[3];
+        split_planes(v, p);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            bf16_t a, b, c;
-            split_f32(v.v[e], a, b, c);
-            h[e] = a; m[e] = b; l[e] = c;
-        }
-        *reinterpret_cast<u32x4*>(dst) = __builtin_bit_cast(u32x4, h);
-        *reinterpret_cast<u32x4*>(dst + plane) = __builtin_bit_cast(u32x4, m);
-        *reinterpret_cast<u32x4*>(dst + 2 * plane) = __builtin_bit_cast(u32x4, l);
+        for (int i = 0; i < 3; ++i) *reinterpret_cast<u32x4*>(dst + i * plane) = __builtin_bit_cast(u32x4, p[i]);
     }
 }
 
@@ -233,12 +243,26 @@ template <int NB> struct Unit {
 
 // ---- forward ----------------------------------------------------------------------
 
+// The labels of a cross entropy (null: none) and where their logits go; v0: vocabulary
+// row of the piece's first.
+struct Labels {
+    const int64_t* ids;
+    int64_t tokens, vocab, v0;
+    float* z;
+    // Row of token n's label below row `first` of the piece, or -1.
+    MO_DEV int64_t row(int64_t n, int64_t first) const {
+        const int64_t y = ids && n < tokens ? ids[n] : -1;
+        return uint64_t(y) < uint64_t(vocab) ? y - v0 - first : -1;
+    }
+};
+
 // Tile (ti, tj): vocabulary rows 256 ti .. of the piece, tokens TN tj ...  Each
 // lane holds 4 MB vocabulary values of one token per column block, so the
 // maximum and the sum are mostly in registers.
 template <int NB, int PL>
 __global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) void head_lse_kernel(
-    Operand W, int dim, Operand H, int nk, uint32_t tm, uint32_t tn, float zscale, float2* part, int64_t n_pad) {
+    Operand W, int dim, Operand H, int nk, uint32_t tm, uint32_t tn, float zscale, float2* part, int64_t n_pad,
+    Labels labels) {
     using L = Layout<NB>;
     __shared__ __align__(16) uint8_t smem[lds_of(NB, PL)];
     uint32_t ti, tj;
@@ -253,12 +277,13 @@ __global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) 
     const float k2 = zscale * LOG2E;
 #pragma unroll
     for (int b = 0; b < L::NBW; ++b) {
+        const int64_t n = n0 + wn * 64 + b * 16 + r16, y = labels.row(n, v0 + wm * (L::MB * 16) + kg * 4);
         float m = -__builtin_inff(), s = 0.f;
 #pragma unroll
         for (int a = 0; a < L::MB; ++a)
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-                const float z = a * 16 + v < left ? acc[a][b][v] * k2 : -__builtin_inff();
+                const float z = a * 16 + v < left ? acc[a][b][v] : -__builtin_inff();
                 acc[a][b][v] = z;
                 m = fmaxf(m, z);
             }
@@ -268,10 +293,16 @@ __global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) 
 #pragma unroll
         for (int a = 0; a < L::MB; ++a)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) s += exp2_hw(acc[a][b][v] - mm);
+            for (int v = 0; v < 4; ++v) s += exp2_hw((acc[a][b][v] - mm) * k2);
         s += __shfl_xor(s, 16, 64);
         s += __shfl_xor(s, 32, 64);
         if (kg == 0) st[wm * 64 * NB + wn * 64 + b * 16 + r16] = float2{m, s};
+        if (uint64_t(y) < uint64_t(L::MB * 16) && (y & 15) < 4)
+#pragma unroll
+            for (int a = 0; a < L::MB; ++a)
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    if (a * 16 + v == int(y)) labels.z[n] = acc[a][b][v];
     }
     __syncthreads();
     for (int t = threadIdx.x; t < 64 * NB; t += H_THREADS) {
@@ -280,7 +311,7 @@ __global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) 
         for (int w = 0; w < L::WM; ++w) m = fmaxf(m, st[w * 64 * NB + t].x);
         const float mm = m == -__builtin_inff() ? 0.f : m;
 #pragma unroll
-        for (int w = 0; w < L::WM; ++w) s += st[w * 64 * NB + t].y * exp2_hw(st[w * 64 * NB + t].x - mm);
+        for (int w = 0; w < L::WM; ++w) s += st[w * 64 * NB + t].y * exp2_hw((st[w * 64 * NB + t].x - mm) * k2);
         part[int64_t(ti) * n_pad + n0 + t] = float2{m, s};
     }
 }
@@ -288,7 +319,7 @@ __global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) 
 // The same from the sums of the splits, one partial per 32 vocabulary rows.
 template <int NB>
 __global__ __launch_bounds__(64) void head_lse_sum_kernel(SplitSums sums, int64_t rows, float zscale, float2* part,
-                                                          int64_t n_pad) {
+                                                          int64_t n_pad, Labels labels) {
     const Unit<NB> u(sums, blockIdx.x);
     const int lane = threadIdx.x, r16 = lane & 15, kg = lane >> 4;
     const int64_t v0 = int64_t(u.ti) * 256 + u.row;
@@ -296,152 +327,194 @@ __global__ __launch_bounds__(64) void head_lse_sum_kernel(SplitSums sums, int64_
     const float k2 = zscale * LOG2E;
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
+        const int64_t n = int64_t(u.tj) * (64 * NB) + u.col + b * 16 + r16, y = labels.row(n, v0 + kg * 4);
         float z[8], m = -__builtin_inff(), s = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            z[i] = i / 4 * 16 + i % 4 < left ? u.acc[i / 4][b][i % 4] * k2 : -__builtin_inff();
+            z[i] = i / 4 * 16 + i % 4 < left ? u.acc[i / 4][b][i % 4] : -__builtin_inff();
             m = fmaxf(m, z[i]);
         }
         m = fmaxf(m, __shfl_xor(m, 16, 64));
         m = fmaxf(m, __shfl_xor(m, 32, 64));
         const float mm = m == -__builtin_inff() ? 0.f : m;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += exp2_hw(z[i] - mm);
+        for (int i = 0; i < 8; ++i) s += exp2_hw((z[i] - mm) * k2);
         s += __shfl_xor(s, 16, 64);
         s += __shfl_xor(s, 32, 64);
-        if (kg == 0) part[v0 / 32 * n_pad + int64_t(u.tj) * (64 * NB) + u.col + b * 16 + r16] = float2{m, s};
+        if (kg == 0) part[v0 / 32 * n_pad + n] = float2{m, s};
+        if (uint64_t(y) < 32 && (y & 15) < 4)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i / 4 * 16 + i % 4 == int(y)) labels.z[n] = z[i];
     }
 }
 
 // z[n][j] = H_n . W_id (not yet divided by T), 0 where the id is outside the
-// vocabulary: one wavefront per token and G of its ids, whose rows it requests
-// together (4096 tokens x 64 ids x 2048: 135 us, 165 with one id per wavefront).
-template <typename T, int G>
-__global__ __launch_bounds__(256) void head_target_kernel(const T* H, int64_t ldh, const T* W, int64_t ldw,
-                                                          const int64_t* ids, int64_t ld_ids, int k,
-                                                          int64_t tokens, int64_t vocab, int dim, float* z) {
-    const int lane = threadIdx.x & 63, groups = (k + G - 1) / G;
-    const int64_t items = tokens * groups;
+// vocabulary: the bits that the logits' product has for it.  A wavefront takes 16
+// pairs (n, j) as the rows and columns of one 16 x 16 tile and reads its diagonal: the
+// same instructions over the same 32 elements of K, plane pairs and splits in the
+// same order, where each output is a sum over its own row and column alone.  One in
+// 16 products counts; the loads take longer.  W and H come as the product reads
+// them: bf16 as it lies in memory or, PL = 3, the planes of the piece, whose ids alone
+// are done then; F32W: W in fp32.  4096 tokens x 64 ids x 2048: 165 us (1.07 GB of W's
+// rows; 135 as plain dot products, whose bits the product does not have).
+struct TargetJob {
+    const void *W, *H;
+    int64_t ldw, plane_w, ldh, plane_h;   // elements
+    const int64_t* ids;
+    int64_t ld_ids, pairs, vocab;
+    int64_t v0, rows;   // vocabulary rows behind W
+    int k, dim, nk, stages;
+    float* z;
+};
+// Chunk at element e of a row where `on`, else zeros.  FULL: whole chunks, loaded
+// without a branch (from the row's start when off).
+template <bool FULL, typename T> MO_DEV raw8<T> chunk_if(const T* row, int e, int dim, bool on) {
+    if constexpr (FULL) return row8<true>(row, on ? e : 0, on ? dim : 0);
+    else return ld8n(row + e, on ? dim - e : 0);
+}
+template <int PL, bool FULL>
+__global__ __launch_bounds__(256) void head_target_kernel(TargetJob j) {
+#ifdef __HIP_DEVICE_COMPILE__
+    using TW = typename std::conditional<PL == F32W, float, bf16_t>::type;
+    constexpr int DEPTH = PL == F32W ? 4 : 8, NSEG = PL == 3 ? 6 : 1, HP = PL == F32W ? 3 : 1;
+    const int lane = threadIdx.x & 63, r16 = lane & 15, kg = lane >> 4;
+    const int64_t items = (j.pairs + 15) / 16;
     for (int64_t it = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6); it < items; it += int64_t(gridDim.x) * 4) {
-        const int64_t n = it / groups;
-        const int j0 = int(it - n * groups) * G;
-        const T* w[G];
-        bool in[G], any = false;
+        const int64_t i = it * 16 + r16, at = i < j.pairs ? i : j.pairs - 1, n = at / j.k;
+        const int64_t id = i < j.pairs ? j.ids[n * j.ld_ids + (at - n * j.k)] : -1;
+        const bool here = uint64_t(id) < uint64_t(j.vocab) && uint64_t(id - j.v0) < uint64_t(j.rows);
+        const TW* w = static_cast<const TW*>(j.W) + (here ? id - j.v0 : 0) * j.ldw;
+        const bf16_t* h = static_cast<const bf16_t*>(j.H) + n * j.ldh;
+        float sum = 0.f;
+        if (__ballot(here))
+            for (int s0 = 0; s0 < j.nk; s0 += j.stages) {
+                // steps of 32 elements of this split; those behind its end add zeros
+                const int first = s0 * 2, end = (s0 + j.stages < j.nk ? s0 + j.stages : j.nk) * 2;
+                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-            const int64_t id = j0 + g < k ? ids[n * ld_ids + j0 + g] : -1;
-            in[g] = uint64_t(id) < uint64_t(vocab);
-            any |= in[g];
-            w[g] = W + (in[g] ? id : 0) * ldw;   // row 0 stands in for an absent one, not used
-        }
-        float s[G];
+                for (int seg = 0; seg < NSEG; ++seg) {
+                    const TW* ws = PL == 3 ? w + seg_p<3>(seg) * j.plane_w : w;
+                    const bf16_t* hs = PL == 3 ? h + seg_q<3>(seg) * j.plane_h : h;
+                    for (int c = first; c < end; c += DEPTH) {
+                        raw8<TW> wr[DEPTH];
+                        raw8<bf16_t> hr[DEPTH][HP];
 #pragma unroll
-        for (int g = 0; g < G; ++g) s[g] = 0.f;
-        if (any)
-            for (int c = lane * 8; c < dim; c += 512) {
-                const f32x8 a = widen(ld8n(H + n * ldh + c, dim - c));
+                        for (int d = 0; d < DEPTH; ++d) {
+                            const int e = (c + d) * 32 + kg * 8;
+                            const bool on = here && c + d < end;
+                            wr[d] = chunk_if<FULL>(ws, e, j.dim, on);
 #pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    const f32x8 b = widen(ld8n(w[g] + c, dim - c));
+                            for (int q = 0; q < HP; ++q) hr[d][q] = chunk_if<(FULL || PL == F32W)>(hs + q * j.plane_h, e, PL == F32W ? j.nk * 64 : j.dim, on);
+                        }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) s[g] = __builtin_fmaf(a.v[e], b.v[e], s[g]);
+                        for (int d = 0; d < DEPTH; ++d) {
+                            if constexpr (PL == F32W) {
+                                bf16x8 wp[3];
+                                split_frag(widen(wr[d]).v, wp);
+#pragma unroll
+                                for (int t = 0; t < 6; ++t)
+                                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wp[seg_p<3>(t)], __builtin_bit_cast(bf16x8, hr[d][seg_q<3>(t)].q), acc, 0, 0, 0);
+                            } else {
+                                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, wr[d].q),
+                                                                              __builtin_bit_cast(bf16x8, hr[d][0].q), acc, 0, 0, 0);
+                            }
+                        }
+                    }
                 }
-            }
+                // lane l: rows 4 (l / 16) .. + 3, column l mod 16
+                float own = acc[0];
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-            const float t = wave_sum(s[g]);
-            if (lane == 0 && j0 + g < k) z[n * k + j0 + g] = in[g] ? t : 0.f;
-        }
+                for (int v = 1; v < 4; ++v) own = (r16 & 3) == v ? acc[v] : own;
+                sum = s0 == 0 ? own : sum + own;
+            }
+        // ids outside the vocabulary: with the first piece
+        if (kg == r16 >> 2 && i < j.pairs && (here || (j.v0 == 0 && uint64_t(id) >= uint64_t(j.vocab)))) j.z[i] = here ? sum : 0.f;
     }
+#endif
 }
 
-// log2-domain partial sums of 8 tokens -> lse (natural log), 64 strided shares of
-// the vocabulary's partials per token, combined in order.  Cross entropy (labels):
-// the label's logit, a dot product per token and wavefront, and the loss.
-template <typename T>
-__global__ __launch_bounds__(512) void head_combine_kernel(const float2* part, int64_t n_pad, int64_t partials,
-                                                           int64_t tokens, const int64_t* labels,
-                                                           int64_t vocab, const T* H, int64_t ldh, const T* W,
-                                                           int64_t ldw, int dim, float* loss, float* lse) {
+// Partial sums of 8 tokens -> lse, 64 strided shares of the vocabulary's partials per
+// token, combined in order.  Cross entropy (labels): the loss, in place of the label's
+// logit that the product left in it; otherwise (m, log s) over the token's first
+// partial, for the distillation's loss.
+__global__ __launch_bounds__(512) void head_combine_kernel(float2* part, int64_t n_pad, int64_t partials,
+                                                           int64_t tokens, const int64_t* labels, int64_t vocab,
+                                                           float zscale, float* loss, float* lse) {
     __shared__ float2 sh[8][65];
     const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t n0 = int64_t(blockIdx.x) * 8;
+    const float k2 = zscale * LOG2E;
     float m = -__builtin_inff(), s = 0.f;
     if (n0 + tx < tokens)
 #pragma unroll 4
         for (int64_t t = ty; t < partials; t += 64) {
             const float2 q = part[t * n_pad + n0 + tx];
             const float mn = fmaxf(m, q.x), mm = mn == -__builtin_inff() ? 0.f : mn;
-            s = s * exp2_hw(m - mm) + q.y * exp2_hw(q.x - mm);
+            s = s * exp2_hw((m - mm) * k2) + q.y * exp2_hw((q.x - mm) * k2);
             m = mn;
         }
     sh[tx][ty] = float2{m, s};
-    const int64_t n = n0 + wave, y = labels && n < tokens ? labels[n] : -1;
-    const bool in = uint64_t(y) < uint64_t(vocab);
-    float z = 0.f;
-    if (in)
-#pragma unroll 4
-        for (int c = lane * 8; c < dim; c += 512) {
-            const f32x8 a = widen(ld8n(H + n * ldh + c, dim - c)), b = widen(ld8n(W + y * ldw + c, dim - c));
-#pragma unroll
-            for (int e = 0; e < 8; ++e) z = __builtin_fmaf(a.v[e], b.v[e], z);
-        }
-    z = wave_sum(z);
     __syncthreads();
+    const int64_t n = n0 + wave;
     if (n >= tokens) return;
     const float2 q = sh[wave][lane];
     m = q.x;
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
     const float mm = m == -__builtin_inff() ? 0.f : m;
-    s = wave_sum(q.y * exp2_hw(q.x - mm));
+    s = wave_sum(q.y * exp2_hw((q.x - mm) * k2));
     if (lane == 0) {
-        const float l = m * LN2 + logf(s);
-        if (labels) loss[n] = in ? l - z : 0.f;
-        lse[n] = !labels || in ? l : 0.f;
+        const float ls = logf(s);
+        const bool in = !labels || uint64_t(labels[n]) < uint64_t(vocab);
+        if (labels) loss[n] = in ? ls + (m - loss[n]) * zscale : 0.f;
+        else part[n] = float2{m, ls};
+        lse[n] = in ? __builtin_fmaf(m, zscale, ls) : 0.f;
     }
 }
 
-// One row of the teacher, by one wavefront: the maximum of t / T over the entries
-// whose id is inside the vocabulary, and the sum of exp(t / T - maximum).  False
-// for a row with no such entry, or only entries of -infinity.
+// One row of the teacher, by one wavefront: the maximum of t over the entries whose id
+// is inside the vocabulary, and the sum of exp((t - maximum) / T).  False for a row
+// with no such entry, or only entries of -infinity.
 MO_DEV bool teacher_row(const int64_t* ids, const void* teacher, bool bf16, int k, int64_t vocab, float inv_t,
                         float& maxt, float& sum) {
     const int lane = threadIdx.x & 63;
     float m = -__builtin_inff();
     for (int j = lane; j < k; j += 64)
-        if (uint64_t(ids[j]) < uint64_t(vocab)) m = fmaxf(m, load_elem(teacher, j, bf16) * inv_t);
+        if (uint64_t(ids[j]) < uint64_t(vocab)) m = fmaxf(m, load_elem(teacher, j, bf16));
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
     float s = 0.f;
     const float mm = m == -__builtin_inff() ? 0.f : m;
     for (int j = lane; j < k; j += 64)
-        if (uint64_t(ids[j]) < uint64_t(vocab)) s += expf(load_elem(teacher, j, bf16) * inv_t - mm);
+        if (uint64_t(ids[j]) < uint64_t(vocab)) s += expf((load_elem(teacher, j, bf16) - mm) * inv_t);
     sum = wave_sum(s);
     maxt = mm;
     return sum != 0.f;   // NaN counts as live and propagates
 }
 
-// loss_n = T^2 sum_j p_j (log p_j - (z_j / T - lse)); rows without entries: loss
-// and lse 0.  One wavefront per row.
+// loss_n = T^2 sum_j p_j (log p_j - log q_j), log q_j = (z_j - m) / T - log s from the
+// combining launch's (m, log s); rows without entries: loss and lse 0.  One wavefront
+// per row.
 __global__ __launch_bounds__(256) void head_distill_loss_kernel(const int64_t* ids, int64_t ld_ids,
                                                                 const void* teacher, int64_t ld_t, bool t_bf16,
                                                                 int k, int64_t tokens, int64_t vocab,
                                                                 float inv_t, float t, const float* z,
-                                                                float* loss, float* lse) {
+                                                                const float2* ms, float* loss, float* lse) {
     const int lane = threadIdx.x & 63;
     for (int64_t n = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6); n < tokens; n += int64_t(gridDim.x) * 4) {
         const int64_t* id = ids + n * ld_ids;
         const uint8_t* te = static_cast<const uint8_t*>(teacher) + n * ld_t * (t_bf16 ? 2 : 4);
         float mt, st;
         const bool live = teacher_row(id, te, t_bf16, k, vocab, inv_t, mt, st);
-        const float l = lse[n], lst = logf(st);
+        const float2 row = ms[n];
+        const float lst = logf(st);
         float s = 0.f;
         if (live)
             for (int j = lane; j < k; j += 64) {
                 if (uint64_t(id[j]) >= uint64_t(vocab)) continue;
-                const float logp = load_elem(te, j, t_bf16) * inv_t - mt - lst, p = expf(logp);
-                if (p != 0.f) s += p * (logp - (z[n * k + j] * inv_t - l));
+                const float logp = (load_elem(te, j, t_bf16) - mt) * inv_t - lst, p = expf(logp);
+                if (p != 0.f) s += p * (logp - ((z[n * k + j] - row.x) * inv_t - row.y));
             }
         s = wave_sum(s);
         if (lane == 0) {
@@ -527,10 +600,10 @@ __global__ __launch_bounds__(256) void head_distill_prep_kernel(const int64_t* i
                 float p = 0.f;
                 for (int u = 0; u < k; ++u)
                     if (id[u] == v) {
-                        p += expf(load_elem(te, u, t_bf16) * inv_t - mt) / st;
+                        p += expf((load_elem(te, u, t_bf16) - mt) * inv_t) / st;
                         again |= u < j;
                     }
-                const float q = expf(z[n * k + j] * inv_t - l);   // at most 1, as in delta_rows
+                const float q = expf(__builtin_fmaf(z[n * k + j], inv_t, -l));   // at most 1, as in delta_rows
                 o = c * ((q > 1.f ? 1.f : q) - p);
             }
             tval[n * k + j] = o;
@@ -920,53 +993,65 @@ hipError_t mo_launch_head_lse(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t*
     const Operand H = h_operand(a, p, ws), W = w_operand(a, p, ws, 0, v0, rows);
     const uint32_t tm = uint32_t((rows + 255) / 256), tn = uint32_t(p.n_pad / (64 * p.nb));
     float2* part = reinterpret_cast<float2*>(ws + p.off_part) + v0 / 256 * p.n_pad * (p.z_splits > 1 ? 8 : 1);
+    const Labels labels = {a.teacher ? nullptr : a.ids, a.tokens, a.vocab, v0, a.loss};
     if (p.z_splits > 1) {
         SplitSums sums;
         const hipError_t e = split_logits(a, p, ws, W, &sums, s);
         if (e != hipSuccess) return e;
         const dim3 units(tm * tn * 8 * uint32_t(p.nb)), wave(64);
-        if (p.nb == 4) return go(head_lse_sum_kernel<4>, units, wave, s, sums, rows, a.inv_t, part, p.n_pad);
-        if (p.nb == 2) return go(head_lse_sum_kernel<2>, units, wave, s, sums, rows, a.inv_t, part, p.n_pad);
-        return go(head_lse_sum_kernel<1>, units, wave, s, sums, rows, a.inv_t, part, p.n_pad);
+        if (p.nb == 4) return go(head_lse_sum_kernel<4>, units, wave, s, sums, rows, a.inv_t, part, p.n_pad, labels);
+        if (p.nb == 2) return go(head_lse_sum_kernel<2>, units, wave, s, sums, rows, a.inv_t, part, p.n_pad, labels);
+        return go(head_lse_sum_kernel<1>, units, wave, s, sums, rows, a.inv_t, part, p.n_pad, labels);
     }
     const dim3 grid(head_grid(uint64_t(tm) * tn)), block(H_THREADS);
     if (p.f32w)
         return go(head_lse_kernel<1, F32W>, grid, block, s, W, int(p.k4), H, int(p.kd / 64), tm, tn, a.inv_t, part,
-                  p.n_pad);
-#define MO_CALL(NB, PL) \
-    return go(head_lse_kernel<NB, PL>, grid, block, s, W, int(a.dim), H, int(p.kd / 64), tm, tn, a.inv_t, part, p.n_pad)
+                  p.n_pad, labels);
+#define MO_CALL(NB, PL)                                                                                              \
+    return go(head_lse_kernel<NB, PL>, grid, block, s, W, int(a.dim), H, int(p.kd / 64), tm, tn, a.inv_t, part, p.n_pad, \
+              labels)
     MO_HEAD_PICK(p.nb, p.planes, MO_CALL);
 #undef MO_CALL
 }
 
-hipError_t mo_launch_head_targets(const MoHeadArgs& a, hipStream_t s) {
-    const int G = a.k >= 4 ? 8 : 1;
-    const dim3 grid(cap_grid((a.tokens * ((a.k + G - 1) / G) + 3) / 4, 1 << 20)), block(256);
-    if (a.dtype == MO_BF16) {
-        const bf16_t *H = static_cast<const bf16_t*>(a.H), *W = static_cast<const bf16_t*>(a.W);
-        return go(G == 8 ? head_target_kernel<bf16_t, 8> : head_target_kernel<bf16_t, 1>, grid, block, s, H, a.ldh, W,
-                  a.ldw, a.ids, a.ld_ids, a.k, a.tokens, a.vocab, int(a.dim), a.z);
-    }
-    const float *H = static_cast<const float*>(a.H), *W = static_cast<const float*>(a.W);
-    return go(G == 8 ? head_target_kernel<float, 8> : head_target_kernel<float, 1>, grid, block, s, H, a.ldh, W, a.ldw,
-              a.ids, a.ld_ids, a.k, a.tokens, a.vocab, int(a.dim), a.z);
+// The logits of the ids among `rows` vocabulary rows from v0 on.
+hipError_t mo_launch_head_targets(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, int64_t v0, int64_t rows,
+                                  hipStream_t s) {
+    TargetJob j = {};
+    j.ids = a.ids;
+    j.ld_ids = a.ld_ids;
+    j.pairs = a.tokens * a.k;
+    j.vocab = a.vocab;
+    j.v0 = v0;
+    j.rows = rows;
+    j.k = a.k;
+    j.nk = int(p.kd / 64);
+    j.stages = p.z_stages;
+    j.z = a.z;
+    const bool planes = p.planes == 3 && !p.f32w;
+    j.W = planes ? ws + p.off_wp : static_cast<const uint8_t*>(a.W) + v0 * a.ldw * (p.planes == 1 ? 2 : 4);
+    j.ldw = planes ? p.kd : a.ldw;
+    j.plane_w = p.piece * p.kd;
+    j.H = p.planes == 3 ? ws + p.off_hp : a.H;
+    j.ldh = p.planes == 3 ? p.kd : a.ldh;
+    j.plane_h = a.tokens * p.kd;
+    j.dim = int(planes ? p.kd : a.dim);
+    const dim3 grid(cap_grid((j.pairs + 63) / 64, 1 << 20)), block(256);
+    if (planes) return go(head_target_kernel<3, true>, grid, block, s, j);
+    const bool full = a.dim % 8 == 0;
+    if (p.f32w) return go(full ? head_target_kernel<F32W, true> : head_target_kernel<F32W, false>, grid, block, s, j);
+    return go(full ? head_target_kernel<1, true> : head_target_kernel<1, false>, grid, block, s, j);
 }
 
 hipError_t mo_launch_head_loss(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, hipStream_t s) {
-    const float2* part = reinterpret_cast<const float2*>(ws + p.off_part);
-    const int64_t* labels = a.teacher ? nullptr : a.ids;
+    float2* part = reinterpret_cast<float2*>(ws + p.off_part);
     const int64_t partials = p.v_tiles * (p.z_splits > 1 ? 8 : 1);
-    const dim3 grid(unsigned((a.tokens + 7) / 8)), block(512);
-    const hipError_t e =
-        a.dtype == MO_BF16
-            ? go(head_combine_kernel<bf16_t>, grid, block, s, part, p.n_pad, partials, a.tokens, labels, a.vocab,
-                 static_cast<const bf16_t*>(a.H), a.ldh, static_cast<const bf16_t*>(a.W), a.ldw, int(a.dim), a.loss, a.lse)
-            : go(head_combine_kernel<float>, grid, block, s, part, p.n_pad, partials, a.tokens, labels, a.vocab,
-                 static_cast<const float*>(a.H), a.ldh, static_cast<const float*>(a.W), a.ldw, int(a.dim), a.loss, a.lse);
+    const hipError_t e = go(head_combine_kernel, dim3(unsigned((a.tokens + 7) / 8)), dim3(512), s, part, p.n_pad, partials,
+                            a.tokens, a.teacher ? nullptr : a.ids, a.vocab, a.inv_t, a.loss, a.lse);
     if (e != hipSuccess || !a.teacher) return e;
     return go(head_distill_loss_kernel, dim3(cap_grid((a.tokens + 3) / 4, 1 << 20)), dim3(256), s, a.ids, a.ld_ids,
               a.teacher, a.ld_teacher, a.teacher_dtype == MO_BF16, a.k, a.tokens, a.vocab, a.inv_t, a.t,
-              static_cast<const float*>(a.z), a.loss, a.lse);
+              static_cast<const float*>(a.z), static_cast<const float2*>(part), a.loss, a.lse);
 }
 
 hipError_t mo_launch_head_prep(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t* ws, hipStream_t s) {

@@ -356,11 +356,14 @@ mo_status head_forward(MoHeadArgs& a, void* workspace, size_t workspace_bytes, v
     if (ranges.conflict()) return MO_ERR_ALIAS;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     if (p.pack_h) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_pack(a, p, ws, true, 0, a.tokens, s));
-    if (distill) MO_RUN(MO_PHASE_HD_TARGET, mo_launch_head_targets(a, s));
+    // from the planes of each piece, or from W itself at once
+    const bool by_piece = p.planes == 3 && !p.f32w;
+    if (distill && !by_piece) MO_RUN(MO_PHASE_HD_TARGET, mo_launch_head_targets(a, p, ws, 0, a.vocab, s));
     for (int64_t v0 = 0; v0 < a.vocab; v0 += p.piece) {
         const int64_t rows = std::min(p.piece, a.vocab - v0);
         if (p.pack_w && p.f32w) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_copy(a, p, ws, 0, v0, rows, s));
         else if (p.pack_w) MO_RUN(MO_PHASE_HD_PREP, mo_launch_head_pack(a, p, ws, false, v0, rows, s));
+        if (distill && by_piece) MO_RUN(MO_PHASE_HD_TARGET, mo_launch_head_targets(a, p, ws, v0, rows, s));
         MO_RUN(MO_PHASE_HD_LSE, mo_launch_head_lse(a, p, ws, v0, rows, s));
     }
     MO_RUN(MO_PHASE_HD_TARGET, mo_launch_head_loss(a, p, ws, s));

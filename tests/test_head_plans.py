@@ -1,0 +1,64 @@
+"""The output head's plans on the CPU, from the library's own source compiled for the
+host (host/head_plan.cpp): the cases of head_cases.py take the paths they are named
+for."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+from head_cases import BF16, CASES
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+ROOT = os.path.dirname(HERE)
+
+
+@pytest.fixture(scope="session")
+def planner(tmp_path_factory):
+    cxx = shutil.which("g++") or shutil.which("c++")
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    if cxx is None or not os.path.exists(os.path.join(rocm, "include", "hip", "hip_runtime.h")):
+        pytest.skip("no host C++ compiler or no HIP headers")
+    exe = str(tmp_path_factory.mktemp("plan") / "head_plan")
+    subprocess.run([cxx, "-O1", "-std=c++17", "-D__HIP_PLATFORM_AMD__", "-I", os.path.join(rocm, "include"),
+                    "-I", os.path.join(ROOT, "include"), "-I", os.path.join(ROOT, "matrix_optimizers_amd", "csrc"),
+                    os.path.join(HERE, "host", "head_plan.cpp"), "-o", exe, "-Wl,--unresolved-symbols=ignore-all"],
+                   check=True, capture_output=True, text=True)
+
+    def plans(rows):
+        """One dict per (tokens, vocab, dim, dtype code, backward, k, ld_h, ld_w, h offset, w offset)."""
+        text = "\n".join(" ".join(str(x) for x in r) for r in rows)
+        out = subprocess.run([exe], input=text, capture_output=True, text=True, check=True).stdout.splitlines()
+        assert len(out) == len(rows)
+        got = [{k: int(v) for k, v in (f.split("=") for f in line.split())} for line in out]
+        for p in got:
+            if p["status"] == 0:
+                p["split"], p["many"] = int(p["z_splits"] > 1), int(p["pieces"] > 1)
+        return got
+    return plans
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_cases_take_the_paths_they_name(planner, name):
+    dtype, n, vocab, dim, *want = CASES[name]
+    for back, w in enumerate(want):
+        got = planner([(n, vocab, dim, 1 if dtype == BF16 else 0, back, 1, 0, 0, 0, 0)])[0]
+        assert {k: got[k] for k in w} == w, (name, "backward" if back else "forward", got)
+
+
+def test_every_path_has_a_case(planner):
+    """Tile widths, split K, several pieces, copies: each combination that the sizes of
+    a wide grid reach is that of some case, in the backward plan (fp32 W read in place
+    has tiles of 64 tokens alone)."""
+    key = lambda p: (p["planes"], p["f32w"], p["nb"], p["split"], p["many"])
+    have = set()
+    for dtype, n, vocab, dim, _, _ in CASES.values():
+        have.add(key(planner([(n, vocab, dim, 1 if dtype == BF16 else 0, 1, 1, 0, 0, 0, 0)])[0]))
+    rows = [(n, v, d, t, 1, 1, 0, 0, 0, 0) for n in (1, 40, 129, 257, 513, 700, 1345, 2049, 8192)
+            for v in (300, 1984, 10001, 32001, 60001, 100003, 131072) for d in (64, 100, 233, 1024, 2500, 4096, 7354)
+            for t in (0, 1)]
+    missing = {}
+    for r, p in zip(rows, planner(rows)):
+        if key(p) not in have:
+            missing.setdefault(key(p), r)
+    assert not missing, missing

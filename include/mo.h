@@ -512,9 +512,12 @@ mo_status softmax_xent_forward(const mo_head* head, const int64_t* labels, float
 /* Gradients of sum_n dloss_n loss_n: dH (tokens x dim) and dW (vocab x dim), of
  * the head's dtype, each optional (NULL), every row written.  loss and lse are
  * the forward call's.  delta_nv = dloss_n (exp(z_nv - lse_n) - [v = label]) is
- * computed again from H and W and rounded to dtype (divided by the significand
- * of one row's dloss, which the fp32 sums are multiplied with; dH is made up for
- * what that takes from delta at the label); dH = delta W, dW = delta^T H.  A row with dloss_n == 0 takes no part. */
+ * computed again from H and W and rounded to dtype: divided by the significand
+ * of one row's dloss, which the fp32 sums are multiplied with (so the last bits of
+ * a row's gradients depend on the weights of the call's first rows).  bf16: dH is
+ * made up for what the rounding takes from delta at the label, and dW of up to
+ * 128 tokens takes delta in two parts.  dH = delta W, dW = delta^T H.  A row with
+ * dloss_n == 0 takes no part. */
 mo_status softmax_xent_backward(const mo_head* head, const int64_t* labels, const float* loss,
                                 const float* lse, const float* dloss, void* dH, int64_t ld_dh,
                                 void* dW, int64_t ld_dw, void* workspace, size_t workspace_bytes,

@@ -46,9 +46,12 @@ using namespace mo_head_gemm;
 
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
-// How a product's operands come (PL): 1: bf16; 3: fp32 as three planes each; F32W: W in
-// fp32 as it lies in memory, the tokens' side as planes.
+// How the products' operands come (PL): 1: bf16; 2: the same, with delta in two planes for
+// dW; 3: fp32 as three planes each; F32W: W in fp32 as it lies in memory, the tokens'
+// side as planes.
 constexpr int F32W = 32;
+constexpr int w_planes(int PL) { return PL == 2 ? 1 : PL; }      // of the products with W
+constexpr int dw_planes(int PL) { return PL == F32W ? 3 : PL; }   // of delta in dW's
 constexpr int lds_of(int NB, int PL) { return PL == F32W ? head_lds32() : head_lds(NB); }
 // One tile of a product with W: NN: columns of W, K along its rows.
 template <int NB, int PL, bool NN, class Acc>
@@ -79,7 +82,7 @@ template <int PL> MO_DEV void put_planes(bf16_t* dst, int64_t plane, const f32x8
         bf16x8 p[3];
         split_planes(v, p);
 #pragma unroll
-        for (int i = 0; i < 3; ++i) *reinterpret_cast<u32x4*>(dst + i * plane) = __builtin_bit_cast(u32x4, p[i]);
+        for (int i = 0; i < dw_planes(PL); ++i) *reinterpret_cast<u32x4*>(dst + i * plane) = __builtin_bit_cast(u32x4, p[i]);
     }
 }
 
@@ -618,8 +621,8 @@ __global__ __launch_bounds__(256) void head_distill_prep_kernel(const int64_t* i
 
 // ---- backward: delta of one piece ----------------------------------------------------
 
-// One piece's delta: D[plane][token][piece] and DT[plane][vocabulary row][token],
-// both zero for tokens that take no part and rows behind the vocabulary.
+// One piece's delta: D[plane][token][piece] for dH and DT[plane][vocabulary row][token]
+// for dW, both zero for tokens that take no part and rows behind the vocabulary.
 struct DeltaJob {
     Operand W, H;
     int dim, nk;
@@ -669,7 +672,7 @@ __device__ __forceinline__ void delta_rows(uint8_t* st, const DeltaJob& j, const
         f32x8 v;
 #pragma unroll
         for (int e = 0; e < 4; ++e) { v.v[e] = lo[e]; v.v[4 + e] = hi[e]; }
-        put_planes<PL>(j.D + (tok + col) * j.ldd + vrow + ic * 8, j.plane_d, v);
+        put_planes<w_planes(PL)>(j.D + (tok + col) * j.ldd + vrow + ic * 8, j.plane_d, v);
     }
     // vocabulary row, 8 tokens
 #pragma unroll
@@ -689,7 +692,7 @@ __device__ __forceinline__ void delta_tile(uint8_t* smem, const DeltaJob& j, uin
     if (!head_tile_of(block, j.tm, j.tn, ti, tj)) return;
     const int64_t v0 = int64_t(ti) * 256, n0 = int64_t(tj) * 64 * NB;
     f32x4 acc[L::MB][L::NBW];
-    w_tile<NB, PL, false>(smem, j.W, j.dim, j.H, v0, n0, 0, j.nk, acc);
+    w_tile<NB, w_planes(PL), false>(smem, j.W, j.dim, j.H, v0, n0, 0, j.nk, acc);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int wm = wave / L::WN, wn = wave % L::WN, kg = lane >> 4;
     const int left = int(j.W.rows - v0 < 256 ? j.W.rows - v0 : 256) - wm * (L::MB * 16) - kg * 4;
@@ -729,7 +732,7 @@ __global__ __launch_bounds__(256) void head_patch_kernel(const int64_t* ids, int
         else split_f32(x, p[0], p[1], p[2]);
 #pragma unroll
         for (int q = 0; q < PL; ++q) {
-            D[q * plane_d + n * ldd + v] = p[q];
+            if (q < w_planes(PL)) D[q * plane_d + n * ldd + v] = p[q];
             DT[q * plane_t + v * ldt + n] = p[q];
         }
     }
@@ -777,7 +780,8 @@ __global__ __launch_bounds__(256) void head_residual_kernel(const bf16_t* W, int
 
 // ---- backward: the two products of a piece --------------------------------------------
 
-// dW rows of the piece = r DT HT^T (K over the tokens), rounded to T.  Where that has
+// dW rows of the piece = r DT HT^T (K over the tokens), rounded to T.  bf16 with few
+// tokens: delta in two planes.  Where that has
 // few tiles (a small vocabulary and many tokens) K is split, in a launch of its own
 // (head_split_kernel), and head_dw_sum_kernel adds the splits up.  A step of 8000
 // tokens x 1000 rows x 256 (4 tiles of 125 stages) takes 88 us in bf16, 181 in
@@ -822,7 +826,7 @@ __device__ __forceinline__ void dw_tile(uint8_t* smem, const DwJob& j, uint32_t 
     if (!head_tile_of(block, j.tm, j.tn, ti, tj)) return;
     const int64_t v0 = int64_t(ti) * 256, c0 = int64_t(tj) * 64 * NB;
     f32x4 acc[L::MB][L::NBW];
-    head_tile<NB, PL == 1 ? 1 : 3>(smem, j.DT, j.HT, v0, c0, 0, j.nk, acc);
+    head_tile<NB, dw_planes(PL)>(smem, j.DT, j.HT, v0, c0, 0, j.nk, acc);
     const int wave = threadIdx.x >> 6, wm = wave / L::WN, wn = wave % L::WN;
     const float r = *j.ref;
 #pragma unroll
@@ -853,7 +857,7 @@ __global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) 
     }
     b -= dw.blocks;
     if (b < dh.blocks) {
-        split_tile<NB, PL, true>(smem, dh, b);
+        split_tile<NB, w_planes(PL), true>(smem, dh, b);
         return;
     }
     delta_tile<NB, PL>(smem, dl, b - dh.blocks);
@@ -1101,7 +1105,7 @@ hipError_t mo_launch_head_patch(const MoHeadArgs& a, const MoHeadPlan& p, uint8_
     bf16_t *D = reinterpret_cast<bf16_t*>(ws + p.off_d[k & 1]), *DT = reinterpret_cast<bf16_t*>(ws + p.off_dt[k & 1]);
     const dim3 grid(cap_grid((pairs + 255) / 256, 1 << 16)), block(256);
     if (p.planes == 1)
-        return go(head_patch_kernel<1>, grid, block, s, a.ids, a.ld_ids, a.k, pairs, tval, coef, v0, rows, D, p.ld_p,
+        return go(p.dt_planes == 2 ? head_patch_kernel<2> : head_patch_kernel<1>, grid, block, s, a.ids, a.ld_ids, a.k, pairs, tval, coef, v0, rows, D, p.ld_p,
                   p.n_pad * p.ld_p, DT, p.ld_t, p.piece * p.ld_t);
     return go(head_patch_kernel<3>, grid, block, s, a.ids, a.ld_ids, a.k, pairs, tval, coef, v0, rows, D, p.ld_p,
               p.n_pad * p.ld_p, DT, p.ld_t, p.piece * p.ld_t);
@@ -1137,6 +1141,10 @@ hipError_t mo_launch_head_delta_split(const MoHeadArgs& a, const MoHeadPlan& p, 
     if (e != hipSuccess) return e;
     const dim3 units(dl.tm * dl.tn * 8 * uint32_t(p.nb)), wave(64);
 #define MO_CALL(NB, PL) return go(head_delta_sum_kernel<NB, PL>, units, wave, s, sums, dl)
+    if (p.dt_planes == 2) {   // at most 128 tokens
+        if (p.nb == 2) MO_CALL(2, 2);
+        MO_CALL(1, 2);
+    }
     MO_HEAD_PICK(p.nb, p.planes, MO_CALL);
 #undef MO_CALL
 }
@@ -1182,6 +1190,9 @@ hipError_t mo_launch_head_step(const MoHeadArgs& a, const MoHeadPlan& p, uint8_t
                      : go(head_step_kernel<T, NB, 1, PL>, grid, block, s, dh, dw, dl)
     if (grid.x == 0) {
         // dW alone, in splits
+    } else if (p.dt_planes == 2) {
+        if (p.nb == 2) MO_STEP(bf16_t, 2, 2);
+        else MO_STEP(bf16_t, 1, 2);
     } else if (p.planes == 1) {
         if (p.nb == 4) MO_STEP(bf16_t, 4, 1);
         else if (p.nb == 2) MO_STEP(bf16_t, 2, 1);

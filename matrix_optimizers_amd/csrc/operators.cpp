@@ -176,6 +176,15 @@ bool f32_in_place(const void* p, int64_t ld, int64_t dim) {
            ld * 4 < (int64_t(1) << 23);
 }
 
+// Up to 128 tokens a bf16 head's delta goes into dW's product in two planes: rounded, and
+// what the rounding left.  A row of dW is then a term or two whose rounding nothing
+// averages; with one plane dW's error was up to 1.6 times that of rounding the result
+// (1 token x 32001 x 2048: 3.5e-3 of its norm against 2.3e-3; 8 x 128256 x 4096:
+// 2.5e-3, 1.6e-3), with two it is that.  More tokens keep one plane: 1.2 times that in
+// the middle of 60 batches of 129 to 1000 tokens, 1.46 times at most.  Backward at 32001 x 2048 (us, one plane and two):
+// 64 tokens 195 and 201, 128 213 and 231, 512 318 and 363, 2048 800 and 1030.
+constexpr int64_t kTwoPlaneTokens = 128;
+
 // Estimated us of a product in `tiles` tiles of 256 x 64 nb with `stages`
 // stages of 64 K, and the splits of K that it takes.  A stage takes 1.43, 0.8 and
 // 0.6 us in a tile of 256, 128 and 64 tokens (256 CUs at 1.5 PFLOP/s; the narrow ones
@@ -215,6 +224,7 @@ int token_tile(int64_t n, int64_t v_tiles, int64_t stages, int planes, int wides
 MoHeadPlan head_plan(const MoHeadArgs& a, bool backward, bool need_dh, bool need_dw) {
     MoHeadPlan p = {};
     p.planes = a.dtype == MO_BF16 ? 1 : 3;
+    p.dt_planes = p.planes == 1 && a.tokens <= kTwoPlaneTokens ? 2 : p.planes;
     p.v_tiles = (a.vocab + 255) / 256;
     p.kd = k_extent(a.dim);
     p.f32w = p.planes == 3 && a.tokens <= kF32Tokens;
@@ -230,7 +240,7 @@ MoHeadPlan head_plan(const MoHeadArgs& a, bool backward, bool need_dh, bool need
     const int64_t copy = !p.pack_w ? 0 : p.f32w ? 4 * p.k4 : 2 * p.planes * p.kd;   // bytes of a row
     int64_t row = copy;
     // (the same pieces whichever gradients are asked for, so that the size query holds for each)
-    if (backward) row += 2 * 4 * p.planes * p.n_pad + (p.f32w ? copy : 4 * p.planes * a.dim);
+    if (backward) row += 2 * 2 * (p.planes + p.dt_planes) * p.n_pad + (p.f32w ? copy : 4 * p.planes * a.dim);
     int64_t most = std::min<int64_t>((int64_t(1) << 22) / std::max<int64_t>(tn, (a.dim + 63) / 64), 1 << 13);
     if (row) most = std::min(most, (backward || p.planes == 3 ? kHeadPieceBytes : kHeadPieceBytes / 4) / row / 256);
     most = std::max<int64_t>(most, 1);
@@ -263,14 +273,15 @@ MoHeadPlan head_plan(const MoHeadArgs& a, bool backward, bool need_dh, bool need
         const int sets = pieces > 1 ? 2 : 1;
         for (int i = 0; i < sets; ++i) {
             p.off_d[i] = take(uint64_t(2) * p.planes * p.n_pad * p.ld_p);
-            p.off_dt[i] = take(uint64_t(2) * p.planes * p.piece * p.ld_t);
+            p.off_dt[i] = take(uint64_t(2) * p.dt_planes * p.piece * p.ld_t);
             if (need_dh && !p.f32w) p.off_wt[i] = take(uint64_t(2) * p.planes * a.dim * p.ld_p);
         }
         if (need_dw) {
             p.off_ht = take(uint64_t(2) * p.planes * a.dim * p.ld_t);
             const int64_t tiles = p.piece / 256 * ((a.dim + 64 * p.nb_dw - 1) / (64 * p.nb_dw)), nk_dw = (a.tokens + 63) / 64;
             int64_t want;
-            product_us(tiles, nk_dw, p.nb_dw, p.planes, &want);
+            if (p.dt_planes == 2) want = 1;   // two stages of K at most
+            else product_us(tiles, nk_dw, p.nb_dw, p.planes, &want);
             p.dw_stages = int((nk_dw + want - 1) / want);
             p.dw_splits = int((nk_dw + p.dw_stages - 1) / p.dw_stages);
             if (p.dw_splits > 1) p.off_dw = take(uint64_t(4) * p.dw_splits * tiles * 256 * 64 * p.nb_dw);

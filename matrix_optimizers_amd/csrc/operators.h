@@ -71,6 +71,7 @@ struct MoHeadArgs {
 };
 struct MoHeadPlan {
     int planes;             // bf16 planes per operand: 1 or 3
+    int dt_planes;          // of delta in dW's product: 1, 2 or 3
     int nb, nb_dw;          // tile width (64 nb): tokens side; dim side of dW
     int64_t n_pad;          // tokens rounded up to the tile width
     int64_t kd;             // dim as a K extent (rounded up, zeros behind)

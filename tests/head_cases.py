@@ -14,6 +14,12 @@ CASES = {
     "bf16 64 copied split pieces": (BF16, 40, 60001, 5813, dict(nb=1, many=1, pack_w=1),
                                     dict(nb=1, split=1, many=1, pack_w=1)),
     "bf16 64 pieces": (BF16, 40, 100003, 4096, dict(nb=1, pack_w=0), dict(nb=1, split=0, many=1, pack_w=0)),
+    "bf16 64 one plane": (BF16, 300, 1000, 192, dict(nb=1, split=0), dict(nb=1, dt_planes=1, split=0, many=0)),
+    "bf16 64 one plane split": (BF16, 300, 1000, 1024, dict(nb=1, split=1), dict(nb=1, dt_planes=1, split=1, many=0)),
+    "bf16 128 few": (BF16, 100, 60001, 256, dict(nb=2, split=0), dict(nb=2, dt_planes=2, split=0, many=0)),
+    "bf16 128 few split": (BF16, 65, 10001, 7354, dict(nb=2, split=1), dict(nb=2, dt_planes=2, split=1, many=0)),
+    "bf16 128 few pieces": (BF16, 65, 100003, 4096, dict(nb=2), dict(nb=2, dt_planes=2, split=0, many=1)),
+    "bf16 128 few split pieces": (BF16, 65, 60001, 7354, dict(nb=2), dict(nb=2, dt_planes=2, split=1, many=1)),
     "bf16 128": (BF16, 2049, 1984, 192, dict(nb=2, split=0, pack_w=0), dict(nb=2, split=0, many=0, pack_w=0)),
     "bf16 128 copied": (BF16, 205, 29746, 233, dict(nb=2, split=0, pack_w=1), dict(nb=2, split=0, pack_w=1)),
     "bf16 128 copied pieces": (BF16, 257, 100003, 2500, dict(nb=2, many=1), dict(nb=2, split=0, many=1, pack_w=1)),

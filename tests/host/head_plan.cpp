@@ -31,9 +31,9 @@ int main() {
             continue;
         }
         const MoHeadPlan p = head_plan(a, back != 0, true, true);
-        std::printf("status=0 planes=%d f32w=%d nb=%d nb_dw=%d n_pad=%" PRId64 " kd=%" PRId64 " pack_h=%d pack_w=%d piece=%" PRId64
+        std::printf("status=0 planes=%d dt_planes=%d f32w=%d nb=%d nb_dw=%d n_pad=%" PRId64 " kd=%" PRId64 " pack_h=%d pack_w=%d piece=%" PRId64
                     " pieces=%" PRId64 " z_stages=%d z_splits=%d dw_splits=%d dh_splits=%d dh_tm=%u dh_tn=%u bytes=%" PRIu64 "\n",
-                    p.planes, int(p.f32w), p.nb, p.nb_dw, p.n_pad, p.kd, int(p.pack_h), int(p.pack_w), p.piece,
+                    p.planes, p.dt_planes, int(p.f32w), p.nb, p.nb_dw, p.n_pad, p.kd, int(p.pack_h), int(p.pack_w), p.piece,
                     (a.vocab + p.piece - 1) / p.piece, p.z_stages, p.z_splits, p.dw_splits, p.dh_splits, p.dh_tm, p.dh_tn,
                     p.bytes);
     }

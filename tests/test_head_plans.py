@@ -47,14 +47,13 @@ def test_cases_take_the_paths_they_name(planner, name):
 
 
 def test_every_path_has_a_case(planner):
-    """Tile widths, split K, several pieces, copies: each combination that the sizes of
-    a wide grid reach is that of some case, in the backward plan (fp32 W read in place
-    has tiles of 64 tokens alone)."""
-    key = lambda p: (p["planes"], p["f32w"], p["nb"], p["split"], p["many"])
+    """Tile widths, delta's planes, split K, several pieces: each combination that the sizes
+    of a wide grid reach is that of some case, in the backward plan."""
+    key = lambda p: (p["planes"], p["dt_planes"], p["f32w"], p["nb"], p["split"], p["many"])
     have = set()
     for dtype, n, vocab, dim, _, _ in CASES.values():
         have.add(key(planner([(n, vocab, dim, 1 if dtype == BF16 else 0, 1, 1, 0, 0, 0, 0)])[0]))
-    rows = [(n, v, d, t, 1, 1, 0, 0, 0, 0) for n in (1, 40, 129, 257, 513, 700, 1345, 2049, 8192)
+    rows = [(n, v, d, t, 1, 1, 0, 0, 0, 0) for n in (1, 40, 65, 128, 129, 257, 513, 700, 1345, 2049, 8192)
             for v in (300, 1984, 10001, 32001, 60001, 100003, 131072) for d in (64, 100, 233, 1024, 2500, 4096, 7354)
             for t in (0, 1)]
     missing = {}
@@ -62,3 +61,14 @@ def test_every_path_has_a_case(planner):
         if key(p) not in have:
             missing.setdefault(key(p), r)
     assert not missing, missing
+
+
+def test_two_planes_of_delta_go_with_narrow_tiles_and_whole_sums(planner):
+    """The kernels for delta in two planes are built for tiles of 64 and 128 tokens and a
+    dW whose K is not split."""
+    rows = [(n, v, d, 1, 1, 1, 0, 0, 0, 0) for n in (1, 2, 63, 64, 65, 100, 127, 128, 129)
+            for v in (1, 300, 5000, 32001, 131072, 1 << 20, 1 << 24) for d in (1, 64, 128, 129, 1000, 4096, 65536)]
+    for r, p in zip(rows, planner(rows)):
+        assert p["dt_planes"] == (2 if r[0] <= 128 else 1)
+        if p["dt_planes"] == 2:
+            assert p["nb"] <= 2 and p["dw_splits"] == 1, (r, p)

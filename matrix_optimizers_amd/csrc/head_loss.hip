@@ -127,34 +127,37 @@ __global__ __launch_bounds__(256) void head_transpose_kernel(const T* src, int64
                                                              int64_t plane, uint32_t tr, uint32_t tc,
                                                              bf16_t* packed, int kd, int64_t packed_plane) {
     __shared__ float tile[64][65];
-    const uint32_t blocks_r = (tr + 7) / 8, blk = blockIdx.x >> 6;
-    const uint32_t ti = blk % blocks_r * 8 + (blockIdx.x & 7), tj = blk / blocks_r * 8 + (blockIdx.x >> 3 & 7);
-    if (ti >= tr || tj >= tc) return;
-    const int64_t r0 = int64_t(ti) * 64;
-    const int c0 = int(tj) * 64;
-    f32x8 v[2];
+    const uint32_t blocks_r = (tr + 7) / 8, units = blocks_r * ((tc + 7) / 8) * 64;
+    for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const uint32_t blk = u >> 6, ti = blk % blocks_r * 8 + (u & 7), tj = blk / blocks_r * 8 + (u >> 3 & 7);
+        if (ti >= tr || tj >= tc) continue;
+        const int64_t r0 = int64_t(ti) * 64;
+        const int c0 = int(tj) * 64;
+        f32x8 v[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int q = threadIdx.x + 256 * i, r = q >> 3, c = (q & 7) * 8;
-        const bool on = r0 + r < rows && (!coef || coef[r0 + r] != 0.f);
-        v[i] = widen(ld8n(src + (r0 + r) * ld + c0 + c, on ? dim - c0 - c : 0));
-    }
+        for (int i = 0; i < 2; ++i) {
+            const int q = threadIdx.x + 256 * i, r = q >> 3, c = (q & 7) * 8;
+            const bool on = r0 + r < rows && (!coef || coef[r0 + r] != 0.f);
+            v[i] = widen(ld8n(src + (r0 + r) * ld + c0 + c, on ? dim - c0 - c : 0));
+        }
+        if (u != blockIdx.x) __syncthreads();   // the tile before has been read
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int q = threadIdx.x + 256 * i, r = q >> 3, c = (q & 7) * 8;
+        for (int i = 0; i < 2; ++i) {
+            const int q = threadIdx.x + 256 * i, r = q >> 3, c = (q & 7) * 8;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) tile[r][c + e] = v[i].v[e];
-        if (packed && r0 + r < rows) put_planes<PL>(packed + (r0 + r) * kd + c0 + c, packed_plane, v[i]);
-    }
-    __syncthreads();
+            for (int e = 0; e < 8; ++e) tile[r][c + e] = v[i].v[e];
+            if (packed && r0 + r < rows) put_planes<PL>(packed + (r0 + r) * kd + c0 + c, packed_plane, v[i]);
+        }
+        __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int q = threadIdx.x + 256 * i, c = q >> 3, r = (q & 7) * 8;
-        if (c0 + c >= dim) continue;
-        f32x8 o;
+        for (int i = 0; i < 2; ++i) {
+            const int q = threadIdx.x + 256 * i, c = q >> 3, r = (q & 7) * 8;
+            if (c0 + c >= dim) continue;
+            f32x8 o;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o.v[e] = tile[r + e][c];
-        put_planes<PL>(dst + int64_t(c0 + c) * ldt + r0 + r, plane, o);
+            for (int e = 0; e < 8; ++e) o.v[e] = tile[r + e][c];
+            put_planes<PL>(dst + int64_t(c0 + c) * ldt + r0 + r, plane, o);
+        }
     }
 }
 
@@ -873,39 +876,42 @@ __global__ __launch_bounds__(256) void head_dh_out_kernel(const f32x4* acc, uint
                                                           int64_t ld, int64_t tokens, int dim) {
     using L = Layout<NB>;
     __shared__ float tile[64][20];
-    // blockIdx.x: tile, then wave, then row block of the wave
-    const uint32_t a = blockIdx.x % L::MB, wave = blockIdx.x / L::MB % 8, tile_id = blockIdx.x / (L::MB * 8);
-    const uint32_t ti = tile_id / tn, tj = tile_id - ti * tn;
     const int lane = threadIdx.x & 63, b = threadIdx.x >> 6;
-    const f32x4* src = acc + (int64_t(tile_id) * 8 + wave) * (L::MB * L::NBW * 64) + (a * L::NBW + b) * 64 + lane;
     const int64_t stride = int64_t(tm) * tn * 8 * (L::MB * L::NBW * 64);
-    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    // u: tile, then wave, then row block of the wave
+    for (uint32_t u = blockIdx.x; u < tm * tn * 8 * L::MB; u += gridDim.x) {
+        const uint32_t a = u % L::MB, wave = u / L::MB % 8, tile_id = u / (L::MB * 8);
+        const uint32_t ti = tile_id / tn, tj = tile_id - ti * tn;
+        const f32x4* src = acc + (int64_t(tile_id) * 8 + wave) * (L::MB * L::NBW * 64) + (a * L::NBW + b) * 64 + lane;
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
-    for (uint32_t s = 0; s < splits; ++s) {
-        const f32x4 x = src[s * stride];
+        for (uint32_t s = 0; s < splits; ++s) {
+            const f32x4 x = src[s * stride];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += x[e];
-    }
-    *reinterpret_cast<f32x4*>(&tile[b * 16 + (lane & 15)][(lane >> 4) * 4]) = v;
-    __syncthreads();
-    const int64_t n0 = int64_t(tj) * 64 * NB + (wave % L::WN) * 64;
-    const int c0 = int(ti) * 256 + int(wave / L::WN) * (16 * L::MB) + int(a) * 16;
-    if (threadIdx.x < 128) {
-        const int j = threadIdx.x >> 1, c = (threadIdx.x & 1) * 8;
-        if (n0 + j < tokens && c0 + c < dim) {
-            const bool on = coef[n0 + j] != 0.f;
-            const float r = *ref;
-            f32x8 o;
+            for (int e = 0; e < 4; ++e) v[e] += x[e];
+        }
+        if (u != blockIdx.x) __syncthreads();   // the block before has been read
+        *reinterpret_cast<f32x4*>(&tile[b * 16 + (lane & 15)][(lane >> 4) * 4]) = v;
+        __syncthreads();
+        const int64_t n0 = int64_t(tj) * 64 * NB + (wave % L::WN) * 64;
+        const int c0 = int(ti) * 256 + int(wave / L::WN) * (16 * L::MB) + int(a) * 16;
+        if (threadIdx.x < 128) {
+            const int j = threadIdx.x >> 1, c = (threadIdx.x & 1) * 8;
+            if (n0 + j < tokens && c0 + c < dim) {
+                const bool on = coef[n0 + j] != 0.f;
+                const float r = *ref;
+                f32x8 o;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o.v[e] = tile[j][c + e];
-            if constexpr (sizeof(T) == 2) {
-                const f32x8 x = widen(ld8n(corr + (n0 + j) * dim + c0 + c, dim - c0 - c));
+                for (int e = 0; e < 8; ++e) o.v[e] = tile[j][c + e];
+                if constexpr (sizeof(T) == 2) {
+                    const f32x8 x = widen(ld8n(corr + (n0 + j) * dim + c0 + c, dim - c0 - c));
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o.v[e] += x.v[e];
+                    for (int e = 0; e < 8; ++e) o.v[e] += x.v[e];
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o.v[e] = on ? r * o.v[e] : 0.f;
+                st8n(dH + (n0 + j) * ld + c0 + c, o, dim - c0 - c);
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o.v[e] = on ? r * o.v[e] : 0.f;
-            st8n(dH + (n0 + j) * ld + c0 + c, o, dim - c0 - c);
         }
     }
 }
@@ -1076,7 +1082,7 @@ static hipError_t transpose(const MoHeadArgs& a, const MoHeadPlan& p, const void
                             int64_t packed_rows, hipStream_t s) {
     // whole stages of the copy: the columns behind dim are its zeros
     const uint32_t tc = uint32_t(((packed ? p.kd : a.dim) + 63) / 64);
-    const dim3 grid((tr + 7) / 8 * ((tc + 7) / 8) * 64), block(256);
+    const dim3 grid(cap_grid(int64_t((tr + 7) / 8 * ((tc + 7) / 8)) * 64, 1 << 20)), block(256);
     bf16_t *d = reinterpret_cast<bf16_t*>(dst), *k = reinterpret_cast<bf16_t*>(packed);
     if (p.planes == 1)
         return go(head_transpose_kernel<bf16_t, 1>, grid, block, s, static_cast<const bf16_t*>(src), ld, rows,
@@ -1231,7 +1237,7 @@ hipError_t mo_launch_head_dh_out(const MoHeadArgs& a, const MoHeadPlan& p, uint8
     const float *coef = reinterpret_cast<const float*>(ws + p.off_coef),
                 *ref = reinterpret_cast<const float*>(ws + p.off_ref);
     // 8 waves x MB row blocks, MB = 2 NB
-    const dim3 grid(p.dh_tm * p.dh_tn * 16 * p.nb), block(256);
+    const dim3 grid(cap_grid(int64_t(p.dh_tm) * p.dh_tn * 16 * p.nb, 1 << 20)), block(256);
     void* corr = ws + p.off_corr;
     if (p.planes == 1) {
         const dim3 items(cap_grid((a.tokens * ((a.dim + 511) / 512) + 3) / 4, 1 << 20));

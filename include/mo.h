@@ -458,7 +458,7 @@ mo_status embedding_backward(const int64_t* tokens, int64_t n, const void* dY, i
  * r = (mean((x - mu)^2) + eps)^-1/2, Y = (x - mu) r weight + bias, Y of X's
  * dtype.  weight and bias are fp32 vectors of cols (slices of the packed tail),
  * NULL for ones and zeros.  mean and rstd (fp32, rows) receive mu and r for the
- * backward pass, NULL to drop them.  Errors: MO_ERR_INVALID_ARG (null X or Y,
+ * backward pass, NULL to drop them; with cols == 0 nothing is written.  Errors: MO_ERR_INVALID_ARG (null X or Y,
  * negative size, bad stride, eps negative or not finite), MO_ERR_UNSUPPORTED
  * (dtype, cols > 2^24, rows > 2^32), MO_ERR_ALIAS, MO_ERR_HIP. */
 mo_status layer_norm_forward(const void* X, int64_t ld_x, const float* weight, const float* bias,

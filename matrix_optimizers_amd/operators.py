@@ -199,7 +199,8 @@ def embedding_backward(tokens, dY, G, *, scale: float = 1.0, accumulate: bool = 
 def layer_norm_forward(X, weight=None, bias=None, *, eps: float = 1e-5, out=None, mean=None, rstd=None,
                        stream=None) -> Tuple:
     """(Y, mean, rstd) of the rows of X (rows, cols), float32 or bfloat16; weight and
-    bias are float32 vectors (slices of the packed tail) or None."""
+    bias are float32 vectors (slices of the packed tail) or None.  Rows without
+    elements have no mean: mean and rstd are NaN then."""
     lib = load_library()
     dev = _device(X, weight, bias, out, mean, rstd)
     ldx = _matrix(X, "X")
@@ -214,6 +215,9 @@ def layer_norm_forward(X, weight=None, bias=None, *, eps: float = 1e-5, out=None
         mean, rstd = on.vector(mean, "mean", rows), on.vector(rstd, "rstd", rows)
         _check(lib.layer_norm_forward(_ptr(X), ldx, _ptr(weight), _ptr(bias), _ptr(out), ldy, _ptr(mean),
                                       _ptr(rstd), rows, cols, code, eps, on.handle), "layer_norm_forward")
+        if cols == 0:   # the library writes nothing then
+            mean.fill_(float("nan"))
+            rstd.fill_(float("nan"))
     return out, mean, rstd
 
 

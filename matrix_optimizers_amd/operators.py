@@ -94,6 +94,13 @@ class _On:
         self.dev, self.stream, self.guards = dev, stream, ()
 
     def __enter__(self):
+        try:
+            return self._enter()
+        except BaseException:
+            self.__exit__()   # a with statement would not
+            raise
+
+    def _enter(self):
         dev, stream = self.dev, self.stream
         if torch.cuda.current_device() != dev.index:
             self._guard(torch.cuda.device(dev))
@@ -104,15 +111,14 @@ class _On:
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(B._stream_handle(stream), device=dev)
         elif stream.device != dev:
-            self.__exit__()
             raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
         self.handle = stream.cuda_stream
         self._guard(torch.cuda.stream(stream))
         return self
 
     def _guard(self, g):
-        self.guards += (g,)
         g.__enter__()
+        self.guards += (g,)
 
     def __exit__(self, *exc):
         while self.guards:

@@ -6,7 +6,10 @@ Argument marshalling only, as in ``_binding``: tensors are checked, outputs the
 caller does not pass are allocated (on the launch stream), and the call runs in
 the library's HIP kernels on the tensors' device, on ``stream`` or that device's
 current stream.  Nothing is registered with autograd: a backward pass is the call
-that computes it.  A caller's workspace (a uint8 tensor of at least the
+that computes it, and what a call returns has no grad_fn, also where an input requires
+gradients.  Layers that autograd runs between two calls start from a result marked
+with ``requires_grad_()`` and are driven by ``h.backward(dh)`` with the gradient the
+next call computed; the first one's gradient is then that result's ``.grad``.  A caller's workspace (a uint8 tensor of at least the
 ``*_workspace_bytes`` figure) must not be reused by other work before the call has
 finished on its stream.
 """

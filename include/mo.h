@@ -446,9 +446,13 @@ mo_status embedding_workspace_bytes(int64_t n, int64_t vocab, int64_t dim, size_
  * matrix tied to the output head, whose G then already holds the head's
  * gradient).  Without accumulate every row of G is written, rows no token
  * names with zeros.  dY (n x dim, dy_dtype) and G (vocab x dim, g_dtype) may
- * differ in type; sums are fp32 over the positions in increasing order, rounded
- * once.  dY rows of padded positions are not read.  Errors as
- * embedding_forward, MO_ERR_WORKSPACE_TOO_SMALL. */
+ * differ in type; sums are fp32 and rounded once (with accumulate after one more
+ * addition, of what G held).  The positions, sorted by token, are summed in
+ * increasing order in chunks of max(4, ceil(n / 512)); the parts of a token's sum
+ * that several chunks hold are then added in a fixed order.  So the last bits of
+ * a frequent token's row depend on n, padding included, and equal bits hold for
+ * equal whole inputs.  dY rows of padded positions take no part and may hold
+ * anything.  Errors as embedding_forward, MO_ERR_WORKSPACE_TOO_SMALL. */
 mo_status embedding_backward(const int64_t* tokens, int64_t n, const void* dY, int64_t ld_dy,
                              int32_t dy_dtype, void* G, int64_t ld_g, int32_t g_dtype,
                              int64_t vocab, int64_t dim, float scale, int32_t accumulate,

@@ -3,13 +3,14 @@
 //   Y[i] = s W[t_i],   G[v] = s sum_{i : t_i = v} dY[i]   (or G[v] += ..)
 //
 // A token outside 0 .. vocab - 1 marks a padded position: its Y row is zero and
-// its dY row is not read.
+// its dY row takes no part (it may be loaded ahead and is dropped).
 //
 // The gradient is the transpose of the lookup.  Adding rows with atomics would
 // make the sum's order, hence its last bits, change from call to call; instead
 // the positions are sorted by token (stable, so equal tokens stay in position
-// order), and each run of equal tokens is summed in fp32 in that order and
-// written once.
+// order), and the runs of equal tokens are summed in fp32 in that order, in chunks
+// of sorted positions whose size follows from n; a run inside one chunk is written
+// once, the parts of one that crosses chunks are joined in a fixed strided order.
 #include "op_common.h"
 #include "operators.h"
 

@@ -72,3 +72,32 @@ def test_two_planes_of_delta_go_with_narrow_tiles_and_whole_sums(planner):
         assert p["dt_planes"] == (2 if r[0] <= 128 else 1)
         if p["dt_planes"] == 2:
             assert p["nb"] <= 2 and p["dw_splits"] == 1, (r, p)
+
+
+def test_which_operands_are_read_as_they_lie(planner):
+    """bf16: rows of whole 128 bytes at 16-byte addresses less than 8 MB apart; fp32 with at
+    most 512 tokens: W's rows of whole 16 bytes, likewise.  Everything else is copied."""
+    def packs(dtype, n=40, dim=128, ldh=0, ldw=0, oh=0, ow=0):
+        p = planner([(n, 300, dim, dtype, 0, 1, ldh, ldw, oh, ow)])[0]
+        return p["pack_h"], p["pack_w"]
+    assert packs(1) == (0, 0) and packs(1, ldh=136, ldw=192, oh=8, ow=16) == (0, 0)
+    assert packs(1, ldh=132) == (1, 0) and packs(1, ldw=129) == (0, 1)
+    assert packs(1, oh=4) == (1, 0) and packs(1, ow=1) == (0, 1)
+    assert packs(1, dim=100) == packs(1, dim=192 + 8) == (1, 1)
+    assert packs(1, ldw=(1 << 22) - 8) == (0, 0) and packs(1, ldw=1 << 22) == (0, 1)
+    assert packs(0) == packs(0, dim=100) == packs(0, ldw=132, ow=4) == (1, 0)
+    assert packs(0, dim=99) == packs(0, ldw=130) == packs(0, ow=2) == packs(0, ldw=1 << 21) == (1, 1)
+    assert packs(0, n=512) == (1, 0) and packs(0, n=513) == (1, 1)
+
+
+def test_pieces_and_copies_hold_what_they_are_for(planner):
+    """Pieces are whole tiles that cover the vocabulary; splits of K cover it; copies'
+    rows are whole stages."""
+    rows = [(n, v, d, t, b, 1, 0, 0, 0, 0) for n in (1, 64, 65, 128, 129, 512, 513, 8192, 1 << 20)
+            for v in (1, 256, 257, 32001, 131072, 1 << 22) for d in (1, 63, 64, 65, 1000, 4096, 65536)
+            for t in (0, 1) for b in (0, 1)]
+    for (n, v, d, *_), p in zip(rows, planner(rows)):
+        assert p["piece"] % 256 == 0 and (p["pieces"] - 1) * p["piece"] < v <= p["pieces"] * p["piece"]
+        assert p["n_pad"] % (64 * p["nb"]) == 0 and 0 <= p["n_pad"] - n < 64 * p["nb"]
+        assert p["kd"] % 64 == 0 and 0 <= p["kd"] - d < 64
+        assert p["z_splits"] * p["z_stages"] >= p["kd"] // 64 > (p["z_splits"] - 1) * p["z_stages"]

@@ -95,3 +95,27 @@ def test_gradients_meet_autograd_by_hand(gpu):
     # fp32 sums of at most `vocab` terms on the way
     for got, want in ((G, W64.grad), (A.grad, A64.grad)):
         assert float((got.double() - want).norm() / want.norm()) <= 2 * vocab * R.U
+
+
+@pytest.mark.parametrize("n", [1000, 40000])
+@pytest.mark.parametrize("vocab", [300, 5000, (1 << 18) - 1, 1 << 18, (1 << 20) + 3, 1 << 27])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_every_number_of_sorting_passes(gpu, n, vocab, accumulate):
+    """9 bits of the ids a pass: one pass to four, in one workgroup where key and position
+    share a word, in launches of their own otherwise; the first, the last and absent ids."""
+    g = gen(n + vocab % 1000)
+    tokens = token_sets("padded", n, vocab, g)
+    tokens[:4] = torch.tensor([vocab - 1, 0, vocab, -1], device="cuda")
+    dY = rand(g, (n, 3), BF)
+    G = torch.full((vocab, 3), 0.5, device="cuda", dtype=BF)
+    mo.embedding_backward(tokens, dY, G, accumulate=accumulate)
+    torch.cuda.synchronize()
+    ok = ((tokens >= 0) & (tokens < vocab)).cpu()
+    ids, at = tokens.cpu()[ok].unique(return_inverse=True)
+    want, bound = R.embed_grad(at, dY.cpu()[ok], len(ids), 1.0)
+    if accumulate:
+        want = want + 0.5
+        bound = bound + R.U * want.abs()
+    R.check(G[ids.cuda()].cpu(), want, bound + R.ut(BF) * want.abs(), "G")
+    G[ids.cuda()] = 0.5 if accumulate else 0
+    assert bool((G == (0.5 if accumulate else 0)).all())

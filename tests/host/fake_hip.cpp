@@ -1,5 +1,5 @@
-// Stands in for the HIP runtime's launch path (preloaded before it): launches are
-// not made, their grids are recorded.
+// Stands in for the HIP runtime's launch path (loaded before it, for all to see):
+// launches are not made, their grids are recorded.
 #include <cstddef>
 #include <cstdint>
 

@@ -1,8 +1,8 @@
 """Every launch of the operators stays inside one launch's limits (fewer than 2^32
 threads along an axis, 65535 workgroups along y, 1024 threads in a workgroup, none
 empty) at the largest sizes the entry points accept, alone and together.  The built
-library runs against a stand-in for the runtime (host/fake_hip.cpp) that records
-launches instead of making them; the addresses are never used."""
+library runs against a stand-in for the runtime's launches (host/fake_hip.cpp), loaded
+before it, that records them instead of making them; the addresses are never used."""
 import os
 import shutil
 import subprocess
@@ -16,8 +16,8 @@ LIB = os.path.join(ROOT, "matrix_optimizers_amd", "libmo.so")
 
 CHILD = r'''
 import ctypes, itertools, sys
+fake = ctypes.CDLL(sys.argv[2], mode=ctypes.RTLD_GLOBAL)   # found before the library's own dependencies
 lib = ctypes.CDLL(sys.argv[1])
-fake = ctypes.CDLL(sys.argv[2])
 P, I, N, F, Z = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
 
 class Head(ctypes.Structure):
@@ -70,8 +70,7 @@ def test_largest_sizes_fit_their_launches(tmp_path):
     fake = str(tmp_path / "fake_hip.so")
     subprocess.run([cxx, "-O1", "-std=c++17", "-shared", "-fPIC", os.path.join(HERE, "host", "fake_hip.cpp"), "-o", fake],
                    check=True, capture_output=True, text=True)
-    res = subprocess.run([sys.executable, "-c", CHILD, LIB, fake], capture_output=True, text=True, timeout=300,
-                         env={**os.environ, "LD_PRELOAD": fake})
+    res = subprocess.run([sys.executable, "-c", CHILD, LIB, fake], capture_output=True, text=True, timeout=300)
     assert res.returncode == 0, res.stderr[-2000:]
     rows = [line.split() for line in res.stdout.splitlines()]
     assert len(rows) == 16 * 2 + 16 * 2 + 24 * 4

@@ -191,7 +191,7 @@ constexpr int64_t kTwoPlaneTokens = 128;
 // wait for their loads), six times that with three planes; splits write and read
 // fp32 tiles at 5 TB/s, are added up one after the other, and are one launch more.
 // In all, a step of 4405 rows x 34 tokens x 4672 went from 177 to 107 us in bf16
-// with splits, 5168 x 40 x 256 (4 stages) stays without at 49 us.
+// with splits, 5168 x 40 x 256 (4 stages) stays without, at 50 to 60 us.
 double product_us(int64_t tiles, int64_t stages, int nb, int planes, int64_t* splits) {
     const double stage = (nb == 4 ? 1.43 : nb == 2 ? 0.8 : 0.6) * (planes == 1 ? 1 : 6);
     double least = double((tiles + 255) / 256 * stages) * stage;

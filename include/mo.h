@@ -220,7 +220,13 @@ const char* mo_status_string(mo_status status);
 #define MO_PHASE_HD_DELTA   30  /* output head: delta of the first piece of the vocabulary */
 #define MO_PHASE_HD_STEP    31  /* output head: dH and dW of a piece, delta of the next */
 #define MO_PHASE_HD_DH      32  /* output head: dH from its fp32 sums */
-#define MO_PHASE_COUNT      33
+#define MO_PHASE_RN_FWD     33  /* RMS norm: forward */
+#define MO_PHASE_RN_BWD     34  /* RMS norm: dx, partial and final weight gradients */
+#define MO_PHASE_F8_CAST    35  /* 8 bits: activations and weights to 8 bits, and back */
+#define MO_PHASE_F8_PREP    36  /* 8 bits: operand copies and transposes of a product */
+#define MO_PHASE_F8_GEMM    37  /* 8 bits: product */
+#define MO_PHASE_F8_WGRAD   38  /* 8 bits: weight gradient */
+#define MO_PHASE_COUNT      39
 
 /* Enable (1) or disable (0) per-launch timing on the calling thread.  While
  * enabled, every kernel launch is bracketed by HIP events on its own stream;
@@ -419,10 +425,10 @@ mo_status soap_converged(const mo_soap_matrix* mats, int32_t n_mats, const mo_so
 
 /* ---- gradients the owner steps read ---------------------------------------
  * The steps above take gradients as given.  The entry points below compute the
- * ones at the two ends of a model, straight into the buffers the steps read:
- * the embedding's and the output head's matrices (G of a Muon, Shampoo or SOAP
- * descriptor), and the norm vectors of the packed fp32 tail (g of
- * adamw_tail_step).  Conventions as above (strides in elements, 0 = the row
+ * ones at the two ends of a model, of its norms and of its linear layers in 8 bits,
+ * straight into the buffers the steps read: the embedding's, the output head's and
+ * the layers' matrices (G of a Muon, Shampoo or SOAP descriptor), and the norm vectors
+ * of the packed fp32 tail (g of adamw_tail_step).  Conventions as above (strides in elements, 0 = the row
  * length, at most 2^26; any element alignment; host-side checks first;
  * written tensors disjoint from every other; bit-identical results on equal
  * inputs).  No call allocates or uploads, so each can be captured in a graph;
@@ -483,6 +489,107 @@ mo_status layer_norm_backward(const void* dY, int64_t ld_dy, const void* X, int6
                               int64_t ld_dx, float* dweight, float* dbias, int64_t rows,
                               int64_t cols, int32_t dtype, void* workspace,
                               size_t workspace_bytes, void* stream);
+
+/* Root-mean-square norm of each row of X + residual (rows x cols, dtype; residual
+ * NULL: of X): h = X + residual rounded to dtype, r = (mean(h^2) + eps)^-1/2,
+ * y = h r weight, weight an fp32 vector of cols (NULL: ones).  H receives h (only
+ * with a residual), NULL to drop it.  The result goes to Y (dtype), or in 8 bits, as
+ * fp8_quantize of the fp32 y makes it, to q and scales, or to both; at least one.  rstd
+ * (fp32, rows) receives r for the backward pass, NULL to drop it.  With cols == 0
+ * nothing is written.  Errors as layer_norm_forward; MO_ERR_INVALID_ARG also for q
+ * without scales or the reverse, and H without a residual. */
+mo_status rms_norm_forward(const void* X, int64_t ld_x, const void* residual, int64_t ld_residual,
+                           const float* weight, void* H, int64_t ld_h, void* Y, int64_t ld_y,
+                           uint8_t* q, int64_t ld_q, uint8_t* scales, int64_t ld_scales,
+                           float* rstd, int64_t rows, int64_t cols, int32_t dtype, float eps,
+                           void* stream);
+
+/* Bytes of device workspace rms_norm_backward needs for dweight. */
+mo_status rms_norm_workspace_bytes(int64_t rows, int64_t cols, size_t* bytes);
+
+/* Gradients of rms_norm_forward from dY (dtype), h (H, or X where there was no
+ * residual) and the saved rstd: dX (dtype), of X and of the residual alike, and
+ * dweight (fp32 vector of cols), each optional (NULL).  dH (dtype, NULL for none) is
+ * what reaches h by other ways, the gradient of the H that the forward call wrote; it
+ * is added to dX.  The gradient with respect to an 8-bit y is taken as if y had not been
+ * rounded.  With rows == 0, dweight is zeroed.  Sums are fp32 in a fixed order.
+ * Without dweight no workspace is needed.  Errors as layer_norm_backward. */
+mo_status rms_norm_backward(const void* dY, int64_t ld_dy, const void* H, int64_t ld_h,
+                            const float* weight, const float* rstd, const void* dH, int64_t ld_dh,
+                            void* dX, int64_t ld_dx, float* dweight, int64_t rows, int64_t cols,
+                            int32_t dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- matrices in 8 bits ------------------------------------------------------
+ * A block of MO_FP8_BLOCK neighbours of a row (the last one of a row may be shorter) is held
+ * as e4m3 numbers q (one sign, four exponent and three fraction bits, largest 448) and
+ * a power of two, one e8m0 byte b: x = q 2^(b - 127).  b is the least that leaves no
+ * element of the block over 448, at least 0; q is rounded to nearest, ties to even.
+ * A block of zeros has b = 0.  An infinity or NaN takes no part in b and becomes e4m3's NaN
+ * by itself; a byte of 255 (which only a caller writes) makes its block NaN.
+ * Activations have a byte per row and block, weights one per block of 128 x 128
+ * (block_rows), so that a weight and its transpose hold the same numbers. */
+#define MO_FP8_BLOCK 128
+
+/* X (rows x cols, dtype) in 8 bits: q (rows x cols) and scales (rows x
+ * ceil(cols / 128)), for a product or kept for the backward pass.  Errors:
+ * MO_ERR_INVALID_ARG (null pointer, negative size, bad stride), MO_ERR_UNSUPPORTED
+ * (dtype, rows > 2^32, cols > 2^24), MO_ERR_ALIAS, MO_ERR_HIP. */
+mo_status fp8_quantize(const void* X, int64_t ld_x, int32_t dtype, int64_t rows, int64_t cols,
+                       uint8_t* q, int64_t ld_q, uint8_t* scales, int64_t ld_scales, void* stream);
+
+/* X (rows x cols, dtype) from q and scales.  The values are bf16 numbers as they are, save
+ * those below 2^-133 (rounded) and above bf16's largest (infinite).  Errors as
+ * fp8_quantize. */
+mo_status fp8_dequantize(const uint8_t* q, int64_t ld_q, const uint8_t* scales, int64_t ld_scales,
+                         int64_t rows, int64_t cols, void* X, int64_t ld_x, int32_t dtype,
+                         void* stream);
+
+/* A weight W (rows x cols, dtype) in blocks of 128 x 128: q (rows x cols) and scales
+ * (ceil(rows / 128) x ceil(cols / 128)) for the forward product, and the same transposed, qt
+ * (cols x rows) and scales_t, for the product with an output's gradient; either pair may be
+ * NULL.  Errors as fp8_quantize; rows and cols at most 2^20. */
+mo_status fp8_quantize_weight(const void* W, int64_t ld_w, int32_t dtype, int64_t rows, int64_t cols,
+                              uint8_t* q, int64_t ld_q, uint8_t* scales, int64_t ld_scales,
+                              uint8_t* qt, int64_t ld_qt, uint8_t* scales_t, int64_t ld_scales_t,
+                              void* stream);
+
+/* A matrix in 8 bits; its columns are the call's.  block_rows: rows per scale, 1 or
+ * MO_FP8_BLOCK. */
+typedef struct mo_fp8_matrix {
+    const uint8_t* q;
+    const uint8_t* scales;
+    int64_t        rows, ld_q, ld_scales;
+    int32_t        block_rows;
+} mo_fp8_matrix;
+
+/* Bytes of device workspace fp8_matmul needs.  The pointers' and strides' alignment counts
+ * (dim a multiple of 128 with 16-byte aligned rows, and of 512 with 4-byte aligned
+ * scales, is read in place; the rest is copied first). */
+mo_status fp8_matmul_workspace_bytes(const mo_fp8_matrix* A, const mo_fp8_matrix* B, int64_t dim,
+                                     int32_t dtype, size_t* bytes);
+
+/* Y = A B^T: A (A->rows x dim), B (B->rows x dim), Y (A->rows x B->rows, dtype).  With
+ * dim == 0, Y is zeroed.  A bf16 Y comes from 8-bit MFMA, which sums 128 products at a time
+ * to about 2^-17 of the largest of them and these sums in fp32 (1.5e-5 of the result's
+ * norm for normal data); an fp32 Y from bf16 MFMA on the operands' values, with
+ * exact products and fp32 sums.  Errors: MO_ERR_INVALID_ARG (null pointer, negative size,
+ * bad stride, block_rows), MO_ERR_UNSUPPORTED (dtype, rows or dim > 2^20),
+ * MO_ERR_WORKSPACE_TOO_SMALL, MO_ERR_ALIAS, MO_ERR_HIP. */
+mo_status fp8_matmul(const mo_fp8_matrix* A, const mo_fp8_matrix* B, int64_t dim, void* Y, int64_t ld_y,
+                     int32_t dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+mo_status fp8_weight_grad_workspace_bytes(const mo_fp8_matrix* X, int64_t dim, int64_t rows,
+                                          int32_t dy_dtype, size_t* bytes);
+
+/* The weight's gradient of Y = X W^T from an activation kept in 8 bits: G = dY^T X, dY
+ * (X->rows tokens x rows, dy_dtype), X (tokens x dim, block_rows 1), G (rows x dim,
+ * g_dtype), the G of an owner step.  Products are exact (X's values are bf16 numbers, an fp32 dY
+ * is three of them), sums fp32, rounded once; with accumulate nonzero after one more
+ * addition, of what G held.  With no tokens G is zeroed, or left as it is.  Errors as
+ * fp8_matmul. */
+mo_status fp8_weight_grad(const void* dY, int64_t ld_dy, int32_t dy_dtype, const mo_fp8_matrix* X,
+                          int64_t dim, void* G, int64_t ld_g, int32_t g_dtype, int64_t rows,
+                          int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);
 
 /* An output head: hidden states H (tokens x dim) and the weight W (vocab x dim),
  * both of `dtype`.  The logits z = H W^T are never stored: both losses walk the

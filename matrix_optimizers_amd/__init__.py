@@ -16,6 +16,13 @@ the C ABI in ``include/mo.h`` (``libmo.so``), with this thin ctypes binding.
     Y = embedding_forward(tokens, W);  embedding_backward(tokens, dY, G)
     Y, mean, rstd = layer_norm_forward(X, weight, bias)
     dX, dweight, dbias = layer_norm_backward(dY, X, mean, rstd, weight)
+    Y, h, rstd = rms_norm_forward(X, weight, residual=R)
+    q, scales, h, rstd = rms_norm_quantize(X, weight, residual=R)
+    dX, dweight = rms_norm_backward(dY, h, rstd, weight, dH=dH)
+    wq, ws, wqt, wst = fp8_quantize_weight(W)
+    Y = fp8_matmul(q, scales, wq, ws)
+    dX = fp8_matmul(*fp8_quantize(dY), wqt, wst)
+    fp8_weight_grad(dY, q, scales, G);  X = fp8_dequantize(*fp8_quantize(X))
     loss, lse = softmax_xent_forward(H, W, labels)
     dH, dW = softmax_xent_backward(H, W, labels, loss, lse, dloss)
     loss, lse, z = topk_distill_forward(H, W, ids, logits, temperature=T)
@@ -39,21 +46,27 @@ from ._binding import (  # noqa: F401
 
 _OPERATORS = (
     "TOPK_MAX", "embedding_backward", "embedding_forward", "embedding_workspace_bytes",
-    "layer_norm_backward", "layer_norm_forward", "layer_norm_workspace_bytes", "softmax_xent_backward",
+    "layer_norm_backward", "layer_norm_forward", "layer_norm_workspace_bytes", "rms_norm_backward",
+    "rms_norm_forward", "rms_norm_quantize", "rms_norm_workspace_bytes", "softmax_xent_backward",
     "softmax_xent_forward", "softmax_xent_workspace_bytes", "topk_distill_backward", "topk_distill_forward",
     "topk_distill_workspace_bytes",
+)
+_FP8 = (
+    "fp8_dequantize", "fp8_matmul", "fp8_matmul_workspace_bytes", "fp8_quantize", "fp8_quantize_weight",
+    "fp8_weight_grad", "fp8_weight_grad_workspace_bytes",
 )
 
 
 def __getattr__(name):
     """The operators, imported with torch on first use (the rest of the package
     imports without it)."""
-    if name in _OPERATORS:
-        from . import operators
+    if name in _OPERATORS or name in _FP8:
+        from . import fp8, operators
         globals().update({n: getattr(operators, n) for n in _OPERATORS})
+        globals().update({n: getattr(fp8, n) for n in _FP8})
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def __dir__():
-    return sorted(set(globals()) | set(_OPERATORS))
+    return sorted(set(globals()) | set(_OPERATORS) | set(_FP8))

@@ -31,7 +31,8 @@ PHASES = ["momentum", "norm", "gram", "poly", "update", "apply", "adamw", "copy"
           "sh_layout", "sh_stats", "sh_rootprep", "sh_root", "sh_left", "sh_right",
           "so_prep", "so_stats", "so_solve", "so_apply", "so_sort", "so_products", "so_warm",
           "emb_fwd", "emb_sort", "emb_bwd", "ln_fwd", "ln_bwd",
-          "hd_prep", "hd_target", "hd_lse", "hd_delta", "hd_step", "hd_dh"]
+          "hd_prep", "hd_target", "hd_lse", "hd_delta", "hd_step", "hd_dh",
+          "rn_fwd", "rn_bwd", "f8_cast", "f8_prep", "f8_gemm", "f8_wgrad"]
 
 
 class MoError(RuntimeError):
@@ -100,7 +101,9 @@ EXPORTS = ["muon_workspace_bytes", "muon_build_worklist", "muon_owner_step", "ad
            "embedding_backward", "layer_norm_forward", "layer_norm_workspace_bytes",
            "layer_norm_backward", "softmax_xent_workspace_bytes", "softmax_xent_forward",
            "softmax_xent_backward", "topk_distill_workspace_bytes", "topk_distill_forward",
-           "topk_distill_backward"]
+           "topk_distill_backward", "rms_norm_forward", "rms_norm_workspace_bytes", "rms_norm_backward",
+           "fp8_quantize", "fp8_dequantize", "fp8_quantize_weight", "fp8_matmul_workspace_bytes", "fp8_matmul",
+           "fp8_weight_grad_workspace_bytes", "fp8_weight_grad"]
 
 ROLE_MATRIX, ROLE_TAIL = 0, 1
 PLAN_POLICIES = {"role_greedy": 0, "scope_greedy": 1, "cost_aware": 2}
@@ -110,6 +113,12 @@ class MoRole(ctypes.Structure):
     """mo_role of include/mo.h."""
     _fields_ = [("block", ctypes.c_int32), ("kind", ctypes.c_int32),
                 ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
+
+
+class MoFp8Matrix(ctypes.Structure):
+    """mo_fp8_matrix of include/mo.h."""
+    _fields_ = [("q", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("ld_q", ctypes.c_int64), ("ld_scales", ctypes.c_int64), ("block_rows", ctypes.c_int32)]
 
 
 class MoHead(ctypes.Structure):
@@ -177,7 +186,19 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     ptr, i64, i32, f32, size = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float,
                                 ctypes.c_size_t)
     head, topk, out = P(MoHead), P(MoTopk), P(ctypes.c_size_t)
+    fp8 = P(MoFp8Matrix)
     operators = {
+        "rms_norm_forward": [ptr, i64, ptr, i64, ptr, ptr, i64, ptr, i64, ptr, i64, ptr, i64, ptr, i64, i64, i32, f32,
+                             ptr],
+        "rms_norm_workspace_bytes": [i64, i64, out],
+        "rms_norm_backward": [ptr, i64, ptr, i64, ptr, ptr, ptr, i64, ptr, i64, ptr, i64, i64, i32, ptr, size, ptr],
+        "fp8_quantize": [ptr, i64, i32, i64, i64, ptr, i64, ptr, i64, ptr],
+        "fp8_dequantize": [ptr, i64, ptr, i64, i64, i64, ptr, i64, i32, ptr],
+        "fp8_quantize_weight": [ptr, i64, i32, i64, i64, ptr, i64, ptr, i64, ptr, i64, ptr, i64, ptr],
+        "fp8_matmul_workspace_bytes": [fp8, fp8, i64, i32, out],
+        "fp8_matmul": [fp8, fp8, i64, ptr, i64, i32, ptr, size, ptr],
+        "fp8_weight_grad_workspace_bytes": [fp8, i64, i64, i32, out],
+        "fp8_weight_grad": [ptr, i64, i32, fp8, i64, ptr, i64, i32, i64, i32, ptr, size, ptr],
         "embedding_forward": [ptr, i64, ptr, i64, i64, i64, i32, f32, ptr, i64, ptr],
         "embedding_workspace_bytes": [i64, i64, i64, out],
         "embedding_backward": [ptr, i64, ptr, i64, i32, ptr, i64, i32, i64, i64, f32, i32, ptr, size, ptr],

@@ -21,7 +21,8 @@ ARCH = "gfx950"
 
 SOURCES = ["host.cpp", "host_common.cpp", "planner.cpp", "shampoo.cpp", "soap.cpp", "ns_kernels.hip",
            "shampoo_kernels.hip", "soap_kernels.hip", "tail_kernels.hip", "static_scratch.hip",
-           "operators.cpp", "embedding.hip", "layer_norm.hip", "head_loss.hip"]
+           "operators.cpp", "embedding.hip", "layer_norm.hip", "head_loss.hip", "rms_norm.hip", "fp8.cpp",
+           "fp8_cast.hip", "fp8_gemm.hip"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
           "-I", os.path.join(ROOT, "include"), "-I", CSRC,

@@ -1,0 +1,325 @@
+// Host side of the 8-bit operators: casts, the product of two matrices in 8 bits and the
+// weight's gradient from an activation in 8 bits.  Argument checks, workspace plans and
+// launches; the kernels are in fp8_cast.hip and fp8_gemm.hip.  As in operators.cpp every
+// plan follows from sizes and alignments alone, and nothing is uploaded or allocated.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "../../include/mo.h"
+#include "operator_host.h"
+#include "operators.h"
+
+using namespace mo_host;
+
+namespace {
+
+constexpr int64_t kBlock = 128;
+constexpr int64_t kCastRows = int64_t(1) << 32, kCastCols = int64_t(1) << 24;
+// Rows and K of a product and both sides of a weight: tile and block counts stay in 32 bits.
+constexpr int64_t kMaxSide = int64_t(1) << 20;
+
+int64_t blocks_of(int64_t n) { return (n + kBlock - 1) / kBlock; }
+
+mo_status cast_shape(int64_t rows, int64_t cols, int32_t dtype, int64_t max_rows, int64_t max_cols) {
+    if (rows < 0 || cols < 0) return MO_ERR_INVALID_ARG;
+    if (!dtype_ok(dtype) || rows > max_rows || cols > max_cols) return MO_ERR_UNSUPPORTED;
+    return MO_OK;
+}
+
+// A matrix in 8 bits of `cols` columns; its pointers are checked where it has elements.
+mo_status operand_of(const mo_fp8_matrix* m, int64_t cols, MoF8Operand* o) {
+    if (!m || m->rows < 0) return MO_ERR_INVALID_ARG;
+    if (m->block_rows != 1 && m->block_rows != int32_t(kBlock)) return MO_ERR_INVALID_ARG;
+    if (m->rows > kMaxSide) return MO_ERR_UNSUPPORTED;
+    *o = {};
+    o->q = m->q;
+    o->s = m->scales;
+    o->rows = m->rows;
+    o->shift = m->block_rows == 1 ? 0 : 7;
+    MO_TRY(stride_of(m->ld_q, cols, &o->ld));
+    MO_TRY(stride_of(m->ld_scales, blocks_of(cols), &o->ld_s));
+    return m->rows && cols && (!m->q || !m->scales) ? MO_ERR_INVALID_ARG : MO_OK;
+}
+
+void operand_ranges(const MoF8Operand& o, int64_t cols, Ranges* r) {
+    const int64_t srows = o.shift ? blocks_of(o.rows) : o.rows;
+    r->add(matrix_range(o.q, o.rows, cols, o.ld, 1, 0));
+    r->add(matrix_range(o.s, srows, blocks_of(cols), o.ld_s, 1, 0));
+}
+
+// Estimated us of a product in tiles of 256 x 64 nb with `stages` stages of 128 bytes of
+// K, and the splits of K (multiples of `unit` stages) that it takes: see the head's plan
+// (operators.cpp), whose tiles these are.
+double product_us(int64_t tiles, int64_t stages, int nb, int unit, int64_t* splits) {
+    const double stage = nb == 4 ? 1.43 : nb == 2 ? 0.8 : 0.6;
+    double least = double((tiles + 255) / 256 * stages) * stage;
+    *splits = 1;
+    for (int64_t k = 2; k <= std::min(256 / tiles, (stages + unit - 1) / unit); ++k) {
+        const double t = double((stages + k - 1) / k) * stage + double(tiles * k * nb) * 0.026 + double(k) * 0.1 + 4;
+        if (t < least) {
+            least = t;
+            *splits = k;
+        }
+    }
+    return least;
+}
+
+// Tiles and splits of a product with `p` rows along 256 and `q` along 64 nb.
+void plan_tiles(MoF8Plan* plan, int64_t p, int64_t q, int64_t stages, int unit, Carve* take) {
+    double least = 0;
+    int64_t splits = 1;
+    for (int nb = 4; nb >= 1; nb /= 2) {
+        int64_t k;
+        const double t = product_us((p + 255) / 256 * ((q + 64 * nb - 1) / (64 * nb)), stages, nb, unit, &k);
+        if (nb == 4 || t < least) {
+            least = t;
+            plan->nb = nb;
+            splits = k;
+        }
+    }
+    plan->tm = uint32_t((p + 255) / 256);
+    plan->tn = uint32_t((q + 64 * plan->nb - 1) / (64 * plan->nb));
+    plan->nk = int(stages);
+    plan->stages = int(((stages + splits - 1) / splits + unit - 1) / unit * unit);
+    plan->splits = int((stages + plan->stages - 1) / plan->stages);
+    if (plan->splits > 1) plan->off_part = (*take)(uint64_t(plan->splits) * plan->tm * plan->tn * 256 * 64 * plan->nb * 4);
+}
+
+// Whether the rows can be loaded in place: whole blocks, 16-byte aligned rows less than 2^23
+// bytes apart (the row offsets within a tile are 31 bits).
+bool q_in_place(const MoF8Operand& o, int64_t dim) {
+    return dim % kBlock == 0 && ((reinterpret_cast<uintptr_t>(o.q) | uintptr_t(o.ld)) & 15) == 0 && o.ld < (int64_t(1) << 23);
+}
+// Whether the scales can: four stages' at a time, so whole aligned dwords.
+bool s_in_place(const MoF8Operand& o, int64_t dim) {
+    return blocks_of(dim) % 4 == 0 && ((reinterpret_cast<uintptr_t>(o.s) | uintptr_t(o.ld_s)) & 3) == 0;
+}
+
+MoF8Plan matmul_plan(const MoF8Operand& A, const MoF8Operand& B, int64_t dim, int32_t dtype) {
+    MoF8Plan p = {};
+    Carve take;
+    const MoF8Operand* o[2] = {&A, &B};
+    p.bf16 = dtype == MO_F32;
+    if (p.bf16) {
+        p.kd = (dim + 63) / 64 * 64;
+        for (int i = 0; i < 2; ++i) p.off_q[i] = take(uint64_t(o[i]->rows) * p.kd * 2);
+        plan_tiles(&p, B.rows, A.rows, p.kd / 64, 1, &take);
+    } else {
+        p.kd = blocks_of(dim) * kBlock;
+        p.ks = (blocks_of(dim) + 3) / 4 * 4;
+        for (int i = 0; i < 2; ++i) {
+            p.pack_q[i] = !q_in_place(*o[i], dim);
+            p.pack_s[i] = !s_in_place(*o[i], dim);
+            if (p.pack_q[i]) p.off_q[i] = take(uint64_t(o[i]->rows) * p.kd);
+            if (p.pack_s[i]) p.off_s[i] = take(uint64_t(o[i]->shift ? blocks_of(o[i]->rows) : o[i]->rows) * p.ks);
+        }
+        plan_tiles(&p, B.rows, A.rows, p.kd / kBlock, 4, &take);
+    }
+    p.bytes = take.at;
+    return p;
+}
+
+MoF8Plan wgrad_plan(int64_t tokens, int64_t rows, int64_t dim, int32_t dy_dtype) {
+    MoF8Plan p = {};
+    Carve take;
+    p.bf16 = true;
+    p.kd = (tokens + 63) / 64 * 64;
+    // not a multiple of 4 KB, which would put a tile's rows on few memory channels
+    p.ld_t = p.kd * 2 % 4096 == 0 ? p.kd + 64 : p.kd;
+    const int planes = dy_dtype == MO_BF16 ? 1 : 3;
+    p.off_q[0] = take(uint64_t(planes) * rows * p.ld_t * 2);
+    p.off_q[1] = take(uint64_t(dim) * p.ld_t * 2);
+    plan_tiles(&p, dim, rows, p.kd / 64, 1, &take);
+    p.bytes = take.at;
+    return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+mo_status fp8_quantize(const void* X, int64_t ld_x, int32_t dtype, int64_t rows, int64_t cols, uint8_t* q, int64_t ld_q,
+                       uint8_t* scales, int64_t ld_scales, void* stream) {
+    MO_TRY(cast_shape(rows, cols, dtype, kCastRows, kCastCols));
+    MoF8Cast a = {};
+    MO_TRY(stride_of(ld_x, cols, &a.ldx));
+    MO_TRY(stride_of(ld_q, cols, &a.ldq));
+    MO_TRY(stride_of(ld_scales, blocks_of(cols), &a.lds));
+    if (rows == 0 || cols == 0) return MO_OK;
+    if (!X || !q || !scales) return MO_ERR_INVALID_ARG;
+    a.X = X;
+    a.Q = q;
+    a.S = scales;
+    a.rows = rows;
+    a.cols = cols;
+    a.dtype = dtype;
+    Ranges r;
+    r.add(matrix_range(X, rows, cols, a.ldx, elem_size(dtype), 0));
+    r.add(matrix_range(q, rows, cols, a.ldq, 1, 1));
+    r.add(matrix_range(scales, rows, blocks_of(cols), a.lds, 1, 1));
+    if (r.conflict()) return MO_ERR_ALIAS;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    MO_RUN(MO_PHASE_F8_CAST, mo_launch_f8_quantize(a, s));
+    return MO_OK;
+}
+
+mo_status fp8_dequantize(const uint8_t* q, int64_t ld_q, const uint8_t* scales, int64_t ld_scales, int64_t rows,
+                         int64_t cols, void* X, int64_t ld_x, int32_t dtype, void* stream) {
+    MO_TRY(cast_shape(rows, cols, dtype, kCastRows, kCastCols));
+    MoF8Cast a = {};
+    MO_TRY(stride_of(ld_x, cols, &a.ldx));
+    MO_TRY(stride_of(ld_q, cols, &a.ldq));
+    MO_TRY(stride_of(ld_scales, blocks_of(cols), &a.lds));
+    if (rows == 0 || cols == 0) return MO_OK;
+    if (!X || !q || !scales) return MO_ERR_INVALID_ARG;
+    a.out = X;
+    a.Q = const_cast<uint8_t*>(q);
+    a.S = const_cast<uint8_t*>(scales);
+    a.rows = rows;
+    a.cols = cols;
+    a.dtype = dtype;
+    Ranges r;
+    r.add(matrix_range(X, rows, cols, a.ldx, elem_size(dtype), 1));
+    r.add(matrix_range(q, rows, cols, a.ldq, 1, 0));
+    r.add(matrix_range(scales, rows, blocks_of(cols), a.lds, 1, 0));
+    if (r.conflict()) return MO_ERR_ALIAS;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    MO_RUN(MO_PHASE_F8_CAST, mo_launch_f8_dequantize(a, s));
+    return MO_OK;
+}
+
+mo_status fp8_quantize_weight(const void* W, int64_t ld_w, int32_t dtype, int64_t rows, int64_t cols, uint8_t* q,
+                              int64_t ld_q, uint8_t* scales, int64_t ld_scales, uint8_t* qt, int64_t ld_qt,
+                              uint8_t* scales_t, int64_t ld_scales_t, void* stream) {
+    MO_TRY(cast_shape(rows, cols, dtype, kMaxSide, kMaxSide));
+    MoF8Cast a = {};
+    MO_TRY(stride_of(ld_w, cols, &a.ldx));
+    MO_TRY(stride_of(ld_q, cols, &a.ldq));
+    MO_TRY(stride_of(ld_scales, blocks_of(cols), &a.lds));
+    MO_TRY(stride_of(ld_qt, rows, &a.ldqt));
+    MO_TRY(stride_of(ld_scales_t, blocks_of(rows), &a.ldst));
+    if (!q != !scales || !qt != !scales_t) return MO_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0) return MO_OK;
+    if (!W || (!q && !qt)) return MO_ERR_INVALID_ARG;
+    a.X = W;
+    a.Q = q;
+    a.S = scales;
+    a.Qt = qt;
+    a.St = scales_t;
+    a.rows = rows;
+    a.cols = cols;
+    a.dtype = dtype;
+    Ranges r;
+    r.add(matrix_range(W, rows, cols, a.ldx, elem_size(dtype), 0));
+    if (q) {
+        r.add(matrix_range(q, rows, cols, a.ldq, 1, 1));
+        r.add(matrix_range(scales, blocks_of(rows), blocks_of(cols), a.lds, 1, 1));
+    }
+    if (qt) {
+        r.add(matrix_range(qt, cols, rows, a.ldqt, 1, 1));
+        r.add(matrix_range(scales_t, blocks_of(cols), blocks_of(rows), a.ldst, 1, 1));
+    }
+    if (r.conflict()) return MO_ERR_ALIAS;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    MO_RUN(MO_PHASE_F8_CAST, mo_launch_f8_weight(a, s));
+    return MO_OK;
+}
+
+static mo_status matmul_args(const mo_fp8_matrix* A, const mo_fp8_matrix* B, int64_t dim, int32_t dtype, MoF8Operand* a,
+                             MoF8Operand* b) {
+    if (dim < 0) return MO_ERR_INVALID_ARG;
+    if (!dtype_ok(dtype) || dim > kMaxSide) return MO_ERR_UNSUPPORTED;
+    MO_TRY(operand_of(A, dim, a));
+    return operand_of(B, dim, b);
+}
+
+mo_status fp8_matmul_workspace_bytes(const mo_fp8_matrix* A, const mo_fp8_matrix* B, int64_t dim, int32_t dtype,
+                                     size_t* bytes) {
+    if (!bytes) return MO_ERR_INVALID_ARG;
+    *bytes = 0;
+    MoF8Operand a, b;
+    MO_TRY(matmul_args(A, B, dim, dtype, &a, &b));
+    if (a.rows == 0 || b.rows == 0 || dim == 0) return MO_OK;
+    const uint64_t need = matmul_plan(a, b, dim, dtype).bytes;
+    *bytes = need ? size_t(need) + MO_WS_ALIGN : 0;
+    return MO_OK;
+}
+
+mo_status fp8_matmul(const mo_fp8_matrix* A, const mo_fp8_matrix* B, int64_t dim, void* Y, int64_t ld_y, int32_t dtype,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+    MoF8Operand a, b;
+    MO_TRY(matmul_args(A, B, dim, dtype, &a, &b));
+    int64_t ldy;
+    MO_TRY(stride_of(ld_y, b.rows, &ldy));
+    if (a.rows == 0 || b.rows == 0) return MO_OK;
+    if (!Y) return MO_ERR_INVALID_ARG;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    if (dim == 0) return zero_rows(Y, a.rows, b.rows, ldy, dtype, MO_PHASE_F8_GEMM, s);
+    const MoF8Plan p = matmul_plan(a, b, dim, dtype);
+    Ranges r;
+    operand_ranges(a, dim, &r);
+    operand_ranges(b, dim, &r);
+    r.add(matrix_range(Y, a.rows, b.rows, ldy, elem_size(dtype), 1));
+    uint8_t* ws;
+    if (!take_workspace(workspace, workspace_bytes, p.bytes, &r, &ws)) return MO_ERR_WORKSPACE_TOO_SMALL;
+    if (r.conflict()) return MO_ERR_ALIAS;
+    for (int i = 0; i < 2; ++i)
+        if (p.bf16 || p.pack_q[i] || p.pack_s[i])
+            MO_RUN(MO_PHASE_F8_PREP, mo_launch_f8_pack(i ? b : a, p, i, dim, ws, s));
+    MO_RUN(MO_PHASE_F8_GEMM, mo_launch_f8_matmul(a, b, p, Y, ldy, ws, s));
+    return MO_OK;
+}
+
+static mo_status wgrad_args(const mo_fp8_matrix* X, int64_t dim, int64_t rows, int32_t dy_dtype, MoF8Operand* x) {
+    if (dim < 0 || rows < 0) return MO_ERR_INVALID_ARG;
+    if (!dtype_ok(dy_dtype) || dim > kMaxSide || rows > kMaxSide) return MO_ERR_UNSUPPORTED;
+    MO_TRY(operand_of(X, dim, x));
+    return x->shift ? MO_ERR_INVALID_ARG : MO_OK;
+}
+
+mo_status fp8_weight_grad_workspace_bytes(const mo_fp8_matrix* X, int64_t dim, int64_t rows, int32_t dy_dtype,
+                                          size_t* bytes) {
+    if (!bytes) return MO_ERR_INVALID_ARG;
+    *bytes = 0;
+    MoF8Operand x;
+    MO_TRY(wgrad_args(X, dim, rows, dy_dtype, &x));
+    if (x.rows == 0 || dim == 0 || rows == 0) return MO_OK;
+    *bytes = size_t(wgrad_plan(x.rows, rows, dim, dy_dtype).bytes) + MO_WS_ALIGN;
+    return MO_OK;
+}
+
+mo_status fp8_weight_grad(const void* dY, int64_t ld_dy, int32_t dy_dtype, const mo_fp8_matrix* X, int64_t dim, void* G,
+                          int64_t ld_g, int32_t g_dtype, int64_t rows, int32_t accumulate, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+    MoF8Wgrad a = {};
+    MO_TRY(wgrad_args(X, dim, rows, dy_dtype, &a.X));
+    if (!dtype_ok(g_dtype)) return MO_ERR_UNSUPPORTED;
+    MO_TRY(stride_of(ld_dy, rows, &a.lddy));
+    MO_TRY(stride_of(ld_g, dim, &a.ldg));
+    if (rows == 0 || dim == 0 || (a.X.rows == 0 && accumulate)) return MO_OK;
+    if (!G || (a.X.rows && !dY)) return MO_ERR_INVALID_ARG;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    if (a.X.rows == 0) return zero_rows(G, rows, dim, a.ldg, g_dtype, MO_PHASE_F8_WGRAD, s);
+    a.dY = dY;
+    a.G = G;
+    a.rows = rows;
+    a.dim = dim;
+    a.dy_dtype = dy_dtype;
+    a.g_dtype = g_dtype;
+    a.accumulate = accumulate;
+    const MoF8Plan p = wgrad_plan(a.X.rows, rows, dim, dy_dtype);
+    Ranges r;
+    operand_ranges(a.X, dim, &r);
+    r.add(matrix_range(dY, a.X.rows, rows, a.lddy, elem_size(dy_dtype), 0));
+    r.add(matrix_range(G, rows, dim, a.ldg, elem_size(g_dtype), 1));
+    uint8_t* ws;
+    if (!take_workspace(workspace, workspace_bytes, p.bytes, &r, &ws)) return MO_ERR_WORKSPACE_TOO_SMALL;
+    if (r.conflict()) return MO_ERR_ALIAS;
+    MO_RUN(MO_PHASE_F8_PREP, mo_launch_f8_transpose(a, p, true, ws, s));
+    MO_RUN(MO_PHASE_F8_PREP, mo_launch_f8_transpose(a, p, false, ws, s));
+    MO_RUN(MO_PHASE_F8_WGRAD, mo_launch_f8_wgrad(a, p, ws, s));
+    return MO_OK;
+}
+
+}  // extern "C"

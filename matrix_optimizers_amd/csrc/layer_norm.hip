@@ -12,36 +12,11 @@
 // row whose sum is exact has variance 0.
 #include "op_common.h"
 #include "operators.h"
+#include "row_team.h"
 
 namespace {
 
-constexpr int LN_MAX_THREADS = 1024;
-
-// Sum over the team of threads that hold one row.  Rows in at most 64 threads
-// are summed within a wavefront (width W); wider ones take the waves' sums
-// through LDS in wave order.  `red` has two slots of 16 x N floats, used in
-// turn, so one barrier per reduction is enough.
-template <int W, int N>
-MO_DEV void team_sum(float (&x)[N], float* red, int& turn) {
-#pragma unroll
-    for (int off = (W < 64 ? W : 64) / 2; off >= 1; off >>= 1)
-#pragma unroll
-        for (int n = 0; n < N; ++n) x[n] += __shfl_xor(x[n], off, 64);
-    if constexpr (W > 64) {
-        float* slot = red + turn * 16 * N;
-        turn ^= 1;
-        const int waves = blockDim.x >> 6, wave = threadIdx.x >> 6;
-        if ((threadIdx.x & 63) == 0)
-#pragma unroll
-            for (int n = 0; n < N; ++n) slot[wave * N + n] = x[n];
-        __syncthreads();
-#pragma unroll
-        for (int n = 0; n < N; ++n) x[n] = 0.f;
-        for (int w = 0; w < waves; ++w)
-#pragma unroll
-            for (int n = 0; n < N; ++n) x[n] += slot[w * N + n];
-    }
-}
+constexpr int LN_MAX_THREADS = TEAM_MAX_THREADS;
 
 // One row per team: W <= 64 threads (256 / W rows per workgroup) or, W = 1024,
 // the whole workgroup of blockDim.x threads.  Thread t of a team holds the
@@ -338,8 +313,6 @@ __global__ __launch_bounds__(1024) void ln_reduce_kernel(const float* part, int 
 // Columns up to which a row stays in registers (two chunks of 8 per thread).
 constexpr int MAX_COLS = 2 * 8 * LN_MAX_THREADS;
 
-struct Shape { int W, R, threads; };   // team, chunks per thread, workgroup
-
 // Rows of at most 512 columns share a workgroup (8 to 64 threads each); longer
 // ones take a workgroup of their own, with one chunk per thread up to `one`
 // chunks and two above.  Measured at 16384 x 8192 bf16 forward: two chunks 95 us,
@@ -358,12 +331,6 @@ Shape shape_of(int64_t cols, int one) {
 }
 Shape fwd_shape(int64_t cols) { return shape_of(cols, 64); }
 Shape bwd_shape(int64_t cols) { return shape_of(cols, 512); }
-
-unsigned wgs_for(int64_t rows, const Shape& s, int per_cu) {
-    const int64_t per = s.W > 64 ? 1 : 256 / s.W;
-    const int64_t want = (rows + per - 1) / per, cap = 256 * int64_t(per_cu);
-    return unsigned(want < cap ? want : cap);
-}
 
 template <typename T, bool FULL>
 hipError_t fwd(const MoLnArgs& a, hipStream_t s) {

@@ -1,6 +1,6 @@
 // Host side of the operators that write the gradients the owner steps read: the
-// embedding, the layer norm and the output head's losses.  Argument checks,
-// workspace plans and launches; the kernels are in embedding.hip, layer_norm.hip
+// embedding, the norms and the output head's losses.  Argument checks, workspace
+// plans and launches; the kernels are in embedding.hip, layer_norm.hip, rms_norm.hip
 // and head_loss.hip.  Every plan follows from sizes and alignments alone, no host
 // memory is uploaded, and nothing is allocated, so each call can be captured.
 #include <hip/hip_runtime.h>
@@ -11,73 +11,12 @@
 #include "../../include/mo.h"
 #include "host_common.h"
 #include "mo_worklist.h"
+#include "operator_host.h"
 #include "operators.h"
 
 using namespace mo_host;
 
 namespace {
-
-#define MO_TRY(x)                          \
-    do {                                   \
-        const mo_status st_ = (x);         \
-        if (st_ != MO_OK) return st_;      \
-    } while (0)
-#define MO_RUN(phase, launch)                                                              \
-    do {                                                                                   \
-        if (timed_launch(phase, s, [&] { return launch; }) != hipSuccess) return MO_ERR_HIP; \
-    } while (0)
-
-// Row strides up to 2^26 elements: byte ranges stay far inside 63 bits.
-constexpr int64_t kMaxLd = int64_t(1) << 26;
-
-// The stride in elements (0 means the row length).
-mo_status stride_of(int64_t ld, int64_t cols, int64_t* out) {
-    *out = ld ? ld : cols;
-    if (*out < cols) return MO_ERR_INVALID_ARG;
-    return *out > kMaxLd ? MO_ERR_UNSUPPORTED : MO_OK;
-}
-
-bool dtype_ok(int32_t d) { return d == MO_F32 || d == MO_BF16; }
-
-Range vec_range(const void* p, int64_t n, int64_t es, int writable) { return matrix_range(p, 1, n, n, es, writable); }
-
-// The ranges of one call, at most ten: no allocation, so no exception can reach the
-// C entry points.
-struct Ranges {
-    Range r[12];
-    int n = 0;
-    void add(const Range& x) { r[n++] = x; }
-    // Any overlap between a writable range and any other?
-    bool conflict() const {
-        for (int i = 0; i < n; ++i)
-            for (int j = 0; j < i; ++j)
-                if ((r[i].writable || r[j].writable) && r[i].lo < r[j].hi && r[j].lo < r[i].hi) return true;
-        return false;
-    }
-};
-
-// The workspace as a range and its aligned base; false when it is too small.
-bool take_workspace(void* workspace, size_t have, uint64_t need, Ranges* ranges, uint8_t** base) {
-    if (need == 0) {
-        *base = nullptr;
-        return true;
-    }
-    if (!workspace || have < need + MO_WS_ALIGN) return false;
-    const uintptr_t w = reinterpret_cast<uintptr_t>(workspace);
-    ranges->add(Range{w, w + have, 1});
-    *base = reinterpret_cast<uint8_t*>(align_up(w, MO_WS_ALIGN));
-    return true;
-}
-
-// Consecutive 256-byte aligned regions.
-struct Carve {
-    uint64_t at = 0;
-    uint64_t operator()(uint64_t bytes) {
-        const uint64_t o = at;
-        at = align_up(at + bytes, MO_WS_ALIGN);
-        return o;
-    }
-};
 
 // ---- layer norm ------------------------------------------------------------------
 
@@ -90,6 +29,8 @@ mo_status ln_shape(int64_t rows, int64_t cols, int32_t dtype) {
 }
 
 uint64_t ln_bwd_bytes(int64_t rows, int64_t cols) { return uint64_t(mo_ln_bwd_parts(rows, cols)) * 2 * cols * 4; }
+
+uint64_t rms_bwd_bytes(int64_t rows, int64_t cols) { return uint64_t(mo_rms_bwd_parts(rows, cols)) * cols * 4; }
 
 // ---- embedding -------------------------------------------------------------------
 
@@ -381,18 +322,6 @@ mo_status head_forward(MoHeadArgs& a, void* workspace, size_t workspace_bytes, v
     return MO_OK;
 }
 
-// Zeros in a rows x cols matrix.
-mo_status zero_rows(void* p, int64_t rows, int64_t cols, int64_t ld, int32_t dtype, int phase, hipStream_t s) {
-    MoEmbArgs e = {};
-    e.G = p;
-    e.vocab = rows;
-    e.dim = cols;
-    e.ldg = ld;
-    e.g_dtype = dtype;
-    MO_RUN(phase, mo_launch_emb_fill(e, s));
-    return MO_OK;
-}
-
 mo_status head_backward(MoHeadArgs& a, void* workspace, size_t workspace_bytes, void* stream, bool distill) {
     MO_TRY(stride_of(a.lddh, a.dim, &a.lddh));
     MO_TRY(stride_of(a.lddw, a.dim, &a.lddw));
@@ -538,6 +467,105 @@ mo_status layer_norm_backward(const void* dY, int64_t ld_dy, const void* X, int6
     float* part = reinterpret_cast<float*>(ws);
     if (rows) MO_RUN(MO_PHASE_LN_BWD, mo_launch_ln_bwd(a, part, s));
     if (sums) MO_RUN(MO_PHASE_LN_BWD, mo_launch_ln_reduce(a, part, s));
+    return MO_OK;
+}
+
+mo_status rms_norm_forward(const void* X, int64_t ld_x, const void* residual, int64_t ld_residual, const float* weight,
+                           void* H, int64_t ld_h, void* Y, int64_t ld_y, uint8_t* q, int64_t ld_q, uint8_t* scales,
+                           int64_t ld_scales, float* rstd, int64_t rows, int64_t cols, int32_t dtype, float eps,
+                           void* stream) {
+    MO_TRY(ln_shape(rows, cols, dtype));
+    if (!finite(eps) || eps < 0.f) return MO_ERR_INVALID_ARG;
+    const int64_t blocks = (cols + 127) / 128;
+    MoRmsArgs a = {};
+    MO_TRY(stride_of(ld_x, cols, &a.ldx));
+    MO_TRY(stride_of(ld_residual, cols, &a.ldr));
+    MO_TRY(stride_of(ld_h, cols, &a.ldh_out));
+    MO_TRY(stride_of(ld_y, cols, &a.ldy));
+    MO_TRY(stride_of(ld_q, cols, &a.ldq));
+    MO_TRY(stride_of(ld_scales, blocks, &a.lds));
+    if (!q != !scales || (H && !residual)) return MO_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0) return MO_OK;
+    if (!X || (!Y && !q)) return MO_ERR_INVALID_ARG;
+    a.X = X;
+    a.residual = residual;
+    a.weight = weight;
+    a.H_out = H;
+    a.Y = Y;
+    a.Q = q;
+    a.S = scales;
+    a.rstd_out = rstd;
+    a.rows = rows;
+    a.cols = cols;
+    a.dtype = dtype;
+    a.eps = eps;
+    const int64_t es = elem_size(dtype);
+    Ranges r;
+    r.add(matrix_range(X, rows, cols, a.ldx, es, 0));
+    if (residual) r.add(matrix_range(residual, rows, cols, a.ldr, es, 0));
+    if (weight) r.add(vec_range(weight, cols, 4, 0));
+    if (H) r.add(matrix_range(H, rows, cols, a.ldh_out, es, 1));
+    if (Y) r.add(matrix_range(Y, rows, cols, a.ldy, es, 1));
+    if (q) {
+        r.add(matrix_range(q, rows, cols, a.ldq, 1, 1));
+        r.add(matrix_range(scales, rows, blocks, a.lds, 1, 1));
+    }
+    if (rstd) r.add(vec_range(rstd, rows, 4, 1));
+    if (r.conflict()) return MO_ERR_ALIAS;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    MO_RUN(MO_PHASE_RN_FWD, mo_launch_rms_fwd(a, s));
+    return MO_OK;
+}
+
+mo_status rms_norm_workspace_bytes(int64_t rows, int64_t cols, size_t* bytes) {
+    if (!bytes) return MO_ERR_INVALID_ARG;
+    MO_TRY(ln_shape(rows, cols, MO_F32));
+    const uint64_t b = rows && cols ? rms_bwd_bytes(rows, cols) : 0;
+    *bytes = b ? size_t(align_up(b, MO_WS_ALIGN)) + MO_WS_ALIGN : 0;
+    return MO_OK;
+}
+
+mo_status rms_norm_backward(const void* dY, int64_t ld_dy, const void* H, int64_t ld_h, const float* weight,
+                            const float* rstd, const void* dH, int64_t ld_dh, void* dX, int64_t ld_dx, float* dweight,
+                            int64_t rows, int64_t cols, int32_t dtype, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+    MO_TRY(ln_shape(rows, cols, dtype));
+    MoRmsArgs a = {};
+    MO_TRY(stride_of(ld_h, cols, &a.ldh));
+    MO_TRY(stride_of(ld_dy, cols, &a.lddy));
+    MO_TRY(stride_of(ld_dh, cols, &a.lddh));
+    MO_TRY(stride_of(ld_dx, cols, &a.lddx));
+    if (cols == 0 || (!dX && !dweight)) return MO_OK;
+    a.H = H;
+    a.dY = dY;
+    a.dH = dX ? dH : nullptr;
+    a.weight = weight;
+    a.rstd = rstd;
+    a.dX = dX;
+    a.dweight = dweight;
+    a.rows = rows;
+    a.cols = cols;
+    a.dtype = dtype;
+    const int64_t es = elem_size(dtype);
+    Ranges r;
+    if (rows) {
+        if (!H || !dY || !rstd) return MO_ERR_INVALID_ARG;
+        r.add(matrix_range(H, rows, cols, a.ldh, es, 0));
+        r.add(matrix_range(dY, rows, cols, a.lddy, es, 0));
+        r.add(vec_range(rstd, rows, 4, 0));
+        if (a.dH) r.add(matrix_range(dH, rows, cols, a.lddh, es, 0));
+        if (dX) r.add(matrix_range(dX, rows, cols, a.lddx, es, 1));
+    }
+    if (weight) r.add(vec_range(weight, cols, 4, 0));
+    if (dweight) r.add(vec_range(dweight, cols, 4, 1));
+    uint8_t* ws = nullptr;
+    if (!take_workspace(workspace, workspace_bytes, dweight ? align_up(rms_bwd_bytes(rows, cols), MO_WS_ALIGN) : 0, &r, &ws))
+        return MO_ERR_WORKSPACE_TOO_SMALL;
+    if (r.conflict()) return MO_ERR_ALIAS;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    float* part = reinterpret_cast<float*>(ws);
+    if (rows) MO_RUN(MO_PHASE_RN_BWD, mo_launch_rms_bwd(a, part, s));
+    if (dweight) MO_RUN(MO_PHASE_RN_BWD, mo_launch_rms_reduce(a, part, s));
     return MO_OK;
 }
 

@@ -1,6 +1,7 @@
-// Argument records and launchers of the embedding, layer-norm and output-head
-// operators (embedding.hip, layer_norm.hip, head_loss.hip); the entry points
-// that check the arguments and plan the workspace are in operators.cpp.
+// Argument records and launchers of the norms, the embedding, the output head and the
+// 8-bit operators (layer_norm.hip, rms_norm.hip, embedding.hip, head_loss.hip, fp8_cast.hip,
+// fp8_gemm.hip); the entry points that check the arguments and plan the workspace are in
+// operators.cpp and fp8.cpp.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -24,6 +25,65 @@ int mo_ln_bwd_parts(int64_t rows, int64_t cols);
 hipError_t mo_launch_ln_fwd(const MoLnArgs& a, hipStream_t s);
 hipError_t mo_launch_ln_bwd(const MoLnArgs& a, float* part, hipStream_t s);
 hipError_t mo_launch_ln_reduce(const MoLnArgs& a, const float* part, hipStream_t s);
+
+// ---- RMS norm --------------------------------------------------------------------
+struct MoRmsArgs {
+    const void *X, *residual, *H, *dY, *dH;
+    const float *weight, *rstd;
+    void *H_out, *Y, *dX;
+    uint8_t *Q, *S;
+    float *rstd_out, *dweight;
+    int64_t ldx, ldr, ldh, ldh_out, lddy, lddh, ldy, lddx, ldq, lds, rows, cols;
+    int32_t dtype;
+    float eps;
+};
+// Partial rows (each cols fp32) the backward pass leaves for the reduction.
+int mo_rms_bwd_parts(int64_t rows, int64_t cols);
+hipError_t mo_launch_rms_fwd(const MoRmsArgs& a, hipStream_t s);
+hipError_t mo_launch_rms_bwd(const MoRmsArgs& a, float* part, hipStream_t s);
+hipError_t mo_launch_rms_reduce(const MoRmsArgs& a, const float* part, hipStream_t s);
+
+// ---- 8 bits ----------------------------------------------------------------------
+// To 8 bits (X to Q and S, and Qt and St for a weight) and back (Q and S to out, row stride ldx).
+struct MoF8Cast {
+    const void* X;
+    void* out;
+    uint8_t *Q, *S, *Qt, *St;
+    int64_t ldx, ldq, lds, ldqt, ldst, rows, cols;
+    int32_t dtype;
+};
+hipError_t mo_launch_f8_quantize(const MoF8Cast& a, hipStream_t s);
+hipError_t mo_launch_f8_dequantize(const MoF8Cast& a, hipStream_t s);
+hipError_t mo_launch_f8_weight(const MoF8Cast& a, hipStream_t s);
+
+// A matrix in 8 bits; row r's scales are in row r >> shift of s.
+struct MoF8Operand {
+    const uint8_t *q, *s;
+    int64_t rows, ld, ld_s;
+    int shift;
+};
+// G (rows x dim) = dY^T X, both of X.rows tokens.
+struct MoF8Wgrad {
+    const void* dY;
+    MoF8Operand X;
+    void* G;
+    int64_t rows, dim, lddy, ldg;
+    int32_t dy_dtype, g_dtype, accumulate;
+};
+struct MoF8Plan {
+    bool bf16;                  // through the bf16 GEMM
+    int nb;                     // tile width 64 nb along the operand without 256-row tiles
+    int nk, stages, splits;     // K stages in all, per split, splits
+    uint32_t tm, tn;
+    int64_t kd, ks, ld_t;       // row lengths of the copies: elements, scales; stride along the tokens
+    bool pack_q[2], pack_s[2];  // copies needed of A (0) and B (1)
+    uint64_t off_q[2], off_s[2], off_part, bytes;
+};
+hipError_t mo_launch_f8_pack(const MoF8Operand& a, const MoF8Plan& p, int i, int64_t dim, uint8_t* ws, hipStream_t s);
+hipError_t mo_launch_f8_matmul(const MoF8Operand& A, const MoF8Operand& B, const MoF8Plan& p, void* Y, int64_t ldy,
+                               uint8_t* ws, hipStream_t s);
+hipError_t mo_launch_f8_transpose(const MoF8Wgrad& a, const MoF8Plan& p, bool x, uint8_t* ws, hipStream_t s);
+hipError_t mo_launch_f8_wgrad(const MoF8Wgrad& a, const MoF8Plan& p, uint8_t* ws, hipStream_t s);
 
 // ---- embedding -------------------------------------------------------------------
 constexpr int MO_EMB_SORT_TILE = 4096;   // positions per workgroup of the sort

@@ -1,6 +1,7 @@
 """The operators that write the gradients the owner steps read: the embedding, the
-layer norm, the softmax cross entropy of the output head and distillation from a
-teacher's top logits (the second half of ``include/mo.h``).
+layer norm, the RMS norm, the softmax cross entropy of the output head and distillation
+from a teacher's top logits (the second half of ``include/mo.h``; matrices in 8 bits
+are in ``fp8``).
 
 Argument marshalling only, as in ``_binding``: tensors are checked, outputs the
 caller does not pass are allocated (on the launch stream), and the call runs in
@@ -24,6 +25,8 @@ from . import _binding as B
 from ._binding import MoHead, MoTopk, _check, load_library
 
 TOPK_MAX = 1024   # MO_TOPK_MAX of include/mo.h
+FP8_BLOCK = 128   # MO_FP8_BLOCK
+FP8, FP8_SCALE = torch.float8_e4m3fn, torch.float8_e8m0fnu
 
 _DTYPE = {torch.float32: B.MO_F32, torch.bfloat16: B.MO_BF16}
 
@@ -263,6 +266,88 @@ def layer_norm_backward(dY, X, mean, rstd, weight=None, *, dX=None, dweight=None
                                        on.handle), "layer_norm_backward")
         del keep
     return out
+
+
+# ---------------------------------------------------------------------------
+# RMS norm
+# ---------------------------------------------------------------------------
+
+def _rms_forward(X, weight, residual, eps, out, q, scales, h, rstd, stream, to8: bool):
+    lib = load_library()
+    dev = _device(X, weight, residual, out, q, scales, h, rstd)
+    ldx = _matrix(X, "X")
+    rows, cols = X.shape
+    code = _code(X, "X")
+    if weight is not None:
+        _vector(weight, "weight", cols)
+    if residual is None and h is not None:
+        raise ValueError("h is written where there is a residual; without one it is X")
+    ldr = 0 if residual is None else _matrix(residual, "residual", rows, cols, X.dtype)
+    with _On(dev, stream) as on:
+        ldy = ldq = lds = ldh = 0
+        if to8:
+            q, ldq = on.matrix(q, "q", rows, cols, FP8)
+            scales, lds = on.matrix(scales, "scales", rows, -(-cols // FP8_BLOCK), FP8_SCALE)
+        else:
+            out, ldy = on.matrix(out, "out", rows, cols, X.dtype)
+        if residual is not None:
+            h, ldh = on.matrix(h, "h", rows, cols, X.dtype)
+        rstd = on.vector(rstd, "rstd", rows)
+        _check(lib.rms_norm_forward(_ptr(X), ldx, _ptr(residual), ldr, _ptr(weight), _ptr(h), ldh, _ptr(out), ldy,
+                                    _ptr(q), ldq, _ptr(scales), lds, _ptr(rstd), rows, cols, code, eps, on.handle),
+               "rms_norm_forward")
+        if cols == 0:   # the library writes nothing then
+            rstd.fill_(float("nan"))
+    return ((q, scales) if to8 else (out,)) + (X if residual is None else h, rstd)
+
+
+def rms_norm_forward(X, weight=None, *, residual=None, eps: float = 1e-6, out=None, h=None, rstd=None,
+                     stream=None) -> Tuple:
+    """(Y, h, rstd) of the rows of h = X + residual (rows, cols), float32 or bfloat16,
+    rounded to their type: Y = h * rstd * weight, rstd = (mean(h^2) + eps)^-1/2.  weight is a
+    float32 vector (a slice of the packed tail) or None; without a residual h is X itself.
+    Rows without elements have no rstd: it is NaN then."""
+    return _rms_forward(X, weight, residual, eps, out, None, None, h, rstd, stream, False)
+
+
+def rms_norm_quantize(X, weight=None, *, residual=None, eps: float = 1e-6, q=None, scales=None, h=None, rstd=None,
+                      stream=None) -> Tuple:
+    """(q, scales, h, rstd): as rms_norm_forward, with Y in 8 bits as fp8_quantize makes it,
+    without a rounding to X's type before."""
+    return _rms_forward(X, weight, residual, eps, None, q, scales, h, rstd, stream, True)
+
+
+def rms_norm_workspace_bytes(rows: int, cols: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load_library().rms_norm_workspace_bytes(rows, cols, ctypes.byref(out)), "rms_norm_workspace_bytes")
+    return int(out.value)
+
+
+def rms_norm_backward(dY, h, rstd, weight=None, *, dH=None, dX=None, dweight=None, need_dX: bool = True,
+                      need_dweight: bool = True, workspace=None, stream=None) -> Tuple:
+    """(dX, dweight) from the forward call's h, rstd and weight; dX of h's dtype is the
+    gradient of X and of the residual alike, dweight is float32 (a slice of the tail's
+    gradient).  dH, the gradient that reaches h by other ways (down the residual
+    stream), is added to dX.  The ones not needed are neither computed nor returned (None)."""
+    lib = load_library()
+    dev = _device(dY, h, rstd, weight, dH, dX, dweight)
+    ldh = _matrix(h, "h")
+    rows, cols = h.shape
+    code = _code(h, "h")
+    ldy = _matrix(dY, "dY", rows, cols, h.dtype)
+    lddh = 0 if dH is None else _matrix(dH, "dH", rows, cols, h.dtype)
+    _vector(rstd, "rstd", rows)
+    if weight is not None:
+        _vector(weight, "weight", cols)
+    need = rms_norm_workspace_bytes(rows, cols) if need_dweight else 0
+    with _On(dev, stream) as on:
+        dX, lddx = on.matrix(dX, "dX", rows, cols, h.dtype) if need_dX else (None, 0)
+        dweight = on.vector(dweight, "dweight", cols) if need_dweight else None
+        ws, have, keep = on.workspace(workspace, need)
+        _check(lib.rms_norm_backward(_ptr(dY), ldy, _ptr(h), ldh, _ptr(weight), _ptr(rstd), _ptr(dH), lddh, _ptr(dX),
+                                     lddx, _ptr(dweight), rows, cols, code, ws, have, on.handle), "rms_norm_backward")
+        del keep
+    return dX, dweight
 
 
 # ---------------------------------------------------------------------------

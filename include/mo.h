@@ -554,17 +554,18 @@ mo_status fp8_quantize_weight(const void* W, int64_t ld_w, int32_t dtype, int64_
                               void* stream);
 
 /* A matrix in 8 bits; its columns are the call's.  block_rows: rows per scale, 1 or
- * MO_FP8_BLOCK. */
+ * MO_FP8_BLOCK.  The scales lie by rows, ld_scales apart, with inc_scales 0 or 1, or by
+ * columns (the transpose of others): then ld_scales is 1 and inc_scales the columns' stride. */
 typedef struct mo_fp8_matrix {
     const uint8_t* q;
     const uint8_t* scales;
-    int64_t        rows, ld_q, ld_scales;
+    int64_t        rows, ld_q, ld_scales, inc_scales;
     int32_t        block_rows;
 } mo_fp8_matrix;
 
 /* Bytes of device workspace fp8_matmul needs.  The pointers' and strides' alignment counts
  * (dim a multiple of 128 with 16-byte aligned rows, and of 512 with 4-byte aligned
- * scales, is read in place; the rest is copied first). */
+ * scales by rows, is read in place; the rest is copied first). */
 mo_status fp8_matmul_workspace_bytes(const mo_fp8_matrix* A, const mo_fp8_matrix* B, int64_t dim,
                                      int32_t dtype, size_t* bytes);
 

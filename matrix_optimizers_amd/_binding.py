@@ -118,7 +118,8 @@ class MoRole(ctypes.Structure):
 class MoFp8Matrix(ctypes.Structure):
     """mo_fp8_matrix of include/mo.h."""
     _fields_ = [("q", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
-                ("ld_q", ctypes.c_int64), ("ld_scales", ctypes.c_int64), ("block_rows", ctypes.c_int32)]
+                ("ld_q", ctypes.c_int64), ("ld_scales", ctypes.c_int64), ("inc_scales", ctypes.c_int64),
+                ("block_rows", ctypes.c_int32)]
 
 
 class MoHead(ctypes.Structure):

@@ -27,6 +27,8 @@ mo_status cast_shape(int64_t rows, int64_t cols, int32_t dtype, int64_t max_rows
     return MO_OK;
 }
 
+int64_t scale_rows(const MoF8Operand& o) { return o.shift ? blocks_of(o.rows) : o.rows; }
+
 // A matrix in 8 bits of `cols` columns; its pointers are checked where it has elements.
 mo_status operand_of(const mo_fp8_matrix* m, int64_t cols, MoF8Operand* o) {
     if (!m || m->rows < 0) return MO_ERR_INVALID_ARG;
@@ -38,14 +40,22 @@ mo_status operand_of(const mo_fp8_matrix* m, int64_t cols, MoF8Operand* o) {
     o->rows = m->rows;
     o->shift = m->block_rows == 1 ? 0 : 7;
     MO_TRY(stride_of(m->ld_q, cols, &o->ld));
-    MO_TRY(stride_of(m->ld_scales, blocks_of(cols), &o->ld_s));
+    // the scales by rows, or by columns (the transpose of others)
+    o->inc = m->inc_scales ? m->inc_scales : 1;
+    if (o->inc == 1) {
+        MO_TRY(stride_of(m->ld_scales, blocks_of(cols), &o->ld_s));
+    } else {
+        if (m->ld_scales != 1) return MO_ERR_INVALID_ARG;
+        o->ld_s = 1;
+        MO_TRY(stride_of(m->inc_scales, scale_rows(*o), &o->inc));
+    }
     return m->rows && cols && (!m->q || !m->scales) ? MO_ERR_INVALID_ARG : MO_OK;
 }
 
 void operand_ranges(const MoF8Operand& o, int64_t cols, Ranges* r) {
-    const int64_t srows = o.shift ? blocks_of(o.rows) : o.rows;
+    const int64_t n = scale_rows(o), b = blocks_of(cols);
     r->add(matrix_range(o.q, o.rows, cols, o.ld, 1, 0));
-    r->add(matrix_range(o.s, srows, blocks_of(cols), o.ld_s, 1, 0));
+    r->add(o.inc == 1 ? matrix_range(o.s, n, b, o.ld_s, 1, 0) : matrix_range(o.s, b, n, o.inc, 1, 0));
 }
 
 // Estimated us of a product in tiles of 256 x 64 nb with `stages` stages of 128 bytes of
@@ -93,7 +103,7 @@ bool q_in_place(const MoF8Operand& o, int64_t dim) {
 }
 // Whether the scales can: four stages' at a time, so whole aligned dwords.
 bool s_in_place(const MoF8Operand& o, int64_t dim) {
-    return blocks_of(dim) % 4 == 0 && ((reinterpret_cast<uintptr_t>(o.s) | uintptr_t(o.ld_s)) & 3) == 0;
+    return o.inc == 1 && blocks_of(dim) % 4 == 0 && ((reinterpret_cast<uintptr_t>(o.s) | uintptr_t(o.ld_s)) & 3) == 0;
 }
 
 MoF8Plan matmul_plan(const MoF8Operand& A, const MoF8Operand& B, int64_t dim, int32_t dtype) {
@@ -110,9 +120,9 @@ MoF8Plan matmul_plan(const MoF8Operand& A, const MoF8Operand& B, int64_t dim, in
         p.ks = (blocks_of(dim) + 3) / 4 * 4;
         for (int i = 0; i < 2; ++i) {
             p.pack_q[i] = !q_in_place(*o[i], dim);
-            p.pack_s[i] = !s_in_place(*o[i], dim);
+            p.pack_s[i] = !(i == 1 && B.shift) && !s_in_place(*o[i], dim);   // (B's in blocks are read singly)
             if (p.pack_q[i]) p.off_q[i] = take(uint64_t(o[i]->rows) * p.kd);
-            if (p.pack_s[i]) p.off_s[i] = take(uint64_t(o[i]->shift ? blocks_of(o[i]->rows) : o[i]->rows) * p.ks);
+            if (p.pack_s[i]) p.off_s[i] = take(uint64_t(scale_rows(*o[i])) * p.ks);
         }
         plan_tiles(&p, B.rows, A.rows, p.kd / kBlock, 4, &take);
     }

@@ -47,10 +47,15 @@ template <typename T> MO_DEV void put4(const Out<T>& o, int64_t q, int64_t p, f3
     }
 }
 
-// KIND 0: 8-bit operands; 1: bf16; 4: bf16, Q in three planes.
+// KIND 8: 8-bit operands, P's scales in blocks of 128 rows; 9: by rows; 1: bf16; 4: bf16, Q in
+// three planes.
+constexpr int KSQ = 8, KROW = 9;
 template <int KIND> struct Operands { using type = Operand; };
-template <> struct Operands<0> { using type = Operand8; };
-template <int KIND, int NB> constexpr int lds_of() { return KIND == 0 ? f8_lds(NB) : head_lds(NB); }
+template <> struct Operands<KSQ> { using type = Operand8; };
+template <> struct Operands<KROW> { using type = Operand8; };
+template <int KIND, int NB> constexpr int lds_of() {
+    return KIND == KSQ ? f8_lds<true>(NB) : KIND == KROW ? f8_lds<false>(NB) : head_lds(NB);
+}
 
 template <int KIND> struct Job {
     typename Operands<KIND>::type P, Q;
@@ -74,7 +79,7 @@ __global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) 
     const int k0 = int(split) * j.stages, nk = j.nk - k0 < j.stages ? j.nk - k0 : j.stages;
     const int64_t p0 = int64_t(ti) * 256, q0 = int64_t(tj) * 64 * NB;
     f32x4 acc[L::MB][L::NBW];
-    if constexpr (KIND == 0) f8_tile<NB>(smem, j.P, j.Q, p0, q0, k0, nk, acc);
+    if constexpr (KIND >= KSQ) f8_tile<NB, KIND == KSQ>(smem, j.P, j.Q, p0, q0, k0, nk, acc);
     else head_tile<NB, KIND>(smem, j.P, j.Q, p0, q0, k0, nk, acc);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     if constexpr (SPLIT) {
@@ -130,7 +135,7 @@ __global__ __launch_bounds__(256) void f8_copy_kernel(const uint8_t* q, int64_t 
         *reinterpret_cast<u32x2*>(dst + r * kd + c) = ldq8(q + r * ld + c, dim - c);
     }
 }
-__global__ __launch_bounds__(256) void f8_copy_scales_kernel(const uint8_t* s, int64_t ld, int64_t rows, int kb,
+__global__ __launch_bounds__(256) void f8_copy_scales_kernel(const uint8_t* s, int64_t ld, int64_t inc, int64_t rows, int kb,
                                                              uint32_t* dst, int words) {
     const int64_t n = int64_t(words) * rows;
     for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {
@@ -138,19 +143,19 @@ __global__ __launch_bounds__(256) void f8_copy_scales_kernel(const uint8_t* s, i
         const int c = int(i - r * words) * 4;
         uint32_t w = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w |= uint32_t(c + e < kb ? s[r * ld + c + e] : 127) << (8 * e);
+        for (int e = 0; e < 4; ++e) w |= uint32_t(c + e < kb ? s[r * ld + (c + e) * inc] : 127) << (8 * e);
         dst[i] = w;
     }
 }
 
 // The values of q in bf16, rows of kd elements (a multiple of 64, zeros behind dim).
 __global__ __launch_bounds__(256) void f8_unpack_kernel(const uint8_t* q, int64_t ld, const uint8_t* s, int64_t ld_s,
-                                                        int shift, int64_t rows, int dim, bf16_t* dst, int kd) {
+                                                        int64_t inc, int shift, int64_t rows, int dim, bf16_t* dst, int kd) {
     const int64_t chunks = int64_t(kd / 8) * rows;
     for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < chunks; i += int64_t(gridDim.x) * 256) {
         const int64_t r = i / (kd / 8);
         const int c = int(i - r * (kd / 8)) * 8;
-        const float f = c < dim ? scale_value(s[(r >> shift) * ld_s + c / F8_BLOCK]) : 0.f;
+        const float f = c < dim ? scale_value(s[(r >> shift) * ld_s + c / F8_BLOCK * inc]) : 0.f;
         store8(dst + r * kd + c, from_e4m3(ldq8(q + r * ld + c, dim - c), f));
     }
 }
@@ -165,9 +170,9 @@ template <> struct Source<uint8_t> {
     const uint8_t* p;
     int64_t ld;
     const uint8_t* s;
-    int64_t ld_s;
+    int64_t ld_s, inc;
     MO_DEV f32x8 at(int64_t r, int64_t c, int n) const {
-        return from_e4m3(ldq8(p + r * ld + c, n), n > 0 ? scale_value(s[r * ld_s + c / F8_BLOCK]) : 0.f);
+        return from_e4m3(ldq8(p + r * ld + c, n), n > 0 ? scale_value(s[r * ld_s + c / F8_BLOCK * inc]) : 0.f);
     }
 };
 
@@ -262,7 +267,7 @@ template <int KIND> Job<KIND> job_of(const MoF8Plan& p, uint8_t* ws) {
 hipError_t mo_launch_f8_pack(const MoF8Operand& a, const MoF8Plan& p, int i, int64_t dim, uint8_t* ws, hipStream_t s) {
     if (p.bf16) {
         hipLaunchKernelGGL(f8_unpack_kernel, dim3(grid_for(a.rows * (p.kd / 8))), dim3(256), 0, s, a.q, a.ld, a.s, a.ld_s,
-                           a.shift, a.rows, int(dim), reinterpret_cast<bf16_t*>(ws + p.off_q[i]), int(p.kd));
+                           a.inc, a.shift, a.rows, int(dim), reinterpret_cast<bf16_t*>(ws + p.off_q[i]), int(p.kd));
         return hipGetLastError();
     }
     if (p.pack_q[i])
@@ -270,12 +275,26 @@ hipError_t mo_launch_f8_pack(const MoF8Operand& a, const MoF8Plan& p, int i, int
                            ws + p.off_q[i], int(p.kd));
     if (p.pack_s[i]) {
         const int64_t r = (a.rows + (int64_t(1) << a.shift) - 1) >> a.shift;
-        hipLaunchKernelGGL(f8_copy_scales_kernel, dim3(grid_for(r * (p.ks / 4))), dim3(256), 0, s, a.s, a.ld_s, r,
+        hipLaunchKernelGGL(f8_copy_scales_kernel, dim3(grid_for(r * (p.ks / 4))), dim3(256), 0, s, a.s, a.ld_s, a.inc, r,
                            int((dim + F8_BLOCK - 1) / F8_BLOCK), reinterpret_cast<uint32_t*>(ws + p.off_s[i]), int(p.ks / 4));
     }
     return hipGetLastError();
 }
 
+template <int KIND>
+static hipError_t matmul8(const MoF8Operand& A, const MoF8Operand& B, const MoF8Plan& p, void* Y, int64_t ldy,
+                          uint8_t* ws, hipStream_t s) {
+    Job<KIND> j = job_of<KIND>(p, ws);
+    auto operand = [&](const MoF8Operand& a, int i) {
+        Operand8 o = {a.q, a.s, a.ld, a.rows, a.ld_s, a.inc, a.shift};
+        if (p.pack_q[i]) o.q = ws + p.off_q[i], o.ld = p.kd;
+        if (p.pack_s[i]) o.s = ws + p.off_s[i], o.ld_s = p.ks, o.inc = 1;
+        return o;
+    };
+    j.Q = operand(A, 0);
+    j.P = operand(B, 1);
+    return product_nb<KIND, bf16_t>(j, p.nb, {static_cast<bf16_t*>(Y), ldy, B.rows, A.rows, false}, s);
+}
 hipError_t mo_launch_f8_matmul(const MoF8Operand& A, const MoF8Operand& B, const MoF8Plan& p, void* Y, int64_t ldy,
                                uint8_t* ws, hipStream_t s) {
     if (p.bf16) {
@@ -284,16 +303,7 @@ hipError_t mo_launch_f8_matmul(const MoF8Operand& A, const MoF8Operand& B, const
         j.P = {ws + p.off_q[1], p.kd * 2, B.rows, 0};
         return product_nb<1, float>(j, p.nb, {static_cast<float*>(Y), ldy, B.rows, A.rows, false}, s);
     }
-    Job<0> j = job_of<0>(p, ws);
-    auto operand = [&](const MoF8Operand& a, int i) {
-        Operand8 o = {a.q, a.s, a.ld, a.rows, a.ld_s, a.shift};
-        if (p.pack_q[i]) o.q = ws + p.off_q[i], o.ld = p.kd;
-        if (p.pack_s[i]) o.s = ws + p.off_s[i], o.ld_s = p.ks;
-        return o;
-    };
-    j.Q = operand(A, 0);
-    j.P = operand(B, 1);
-    return product_nb<0, bf16_t>(j, p.nb, {static_cast<bf16_t*>(Y), ldy, B.rows, A.rows, false}, s);
+    return B.shift ? matmul8<KSQ>(A, B, p, Y, ldy, ws, s) : matmul8<KROW>(A, B, p, Y, ldy, ws, s);
 }
 
 hipError_t mo_launch_f8_transpose(const MoF8Wgrad& a, const MoF8Plan& p, bool x, uint8_t* ws, hipStream_t s) {
@@ -305,7 +315,7 @@ hipError_t mo_launch_f8_transpose(const MoF8Wgrad& a, const MoF8Plan& p, bool x,
     const int64_t plane = cols * p.ld_t;
     if (x)
         hipLaunchKernelGGL((f8_transpose_kernel<uint8_t, 1>), grid, dim3(256), 0, s,
-                           Source<uint8_t>{a.X.q, a.X.ld, a.X.s, a.X.ld_s}, a.X.rows, cols, dst, p.ld_t, plane, tr, tc);
+                           Source<uint8_t>{a.X.q, a.X.ld, a.X.s, a.X.ld_s, a.X.inc}, a.X.rows, cols, dst, p.ld_t, plane, tr, tc);
     else if (a.dy_dtype == MO_BF16)
         hipLaunchKernelGGL((f8_transpose_kernel<bf16_t, 1>), grid, dim3(256), 0, s,
                            Source<bf16_t>{static_cast<const bf16_t*>(a.dY), a.lddy}, a.X.rows, cols, dst, p.ld_t, plane,

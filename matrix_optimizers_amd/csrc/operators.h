@@ -56,10 +56,10 @@ hipError_t mo_launch_f8_quantize(const MoF8Cast& a, hipStream_t s);
 hipError_t mo_launch_f8_dequantize(const MoF8Cast& a, hipStream_t s);
 hipError_t mo_launch_f8_weight(const MoF8Cast& a, hipStream_t s);
 
-// A matrix in 8 bits; row r's scales are in row r >> shift of s.
+// A matrix in 8 bits; row r's scales are in row r >> shift of s, inc apart.
 struct MoF8Operand {
     const uint8_t *q, *s;
-    int64_t rows, ld, ld_s;
+    int64_t rows, ld, ld_s, inc;
     int shift;
 };
 // G (rows x dim) = dY^T X, both of X.rows tokens.

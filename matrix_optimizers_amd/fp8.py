@@ -28,8 +28,13 @@ def _operand(q, scales, what: str, square=None) -> MoFp8Matrix:
     rows, cols = q.shape
     if square is None:
         square = scales.dim() == 2 and scales.shape[0] != rows
-    lds = _matrix(scales, f"{what}'s scales", _blocks(rows) if square else rows, _blocks(cols), FP8_SCALE)
-    return MoFp8Matrix(q=_ptr(q), scales=_ptr(scales), rows=rows, ld_q=ldq, ld_scales=lds,
+    srows, scols = _blocks(rows) if square else rows, _blocks(cols)
+    lds, inc = 1, 0
+    if scales.dim() == 2 and scales.shape[1] > 1 and scales.stride(1) != 1:   # by columns: others' transpose
+        inc = _matrix(scales.t(), f"{what}'s scales, transposed,", scols, srows, FP8_SCALE)
+    else:
+        lds = _matrix(scales, f"{what}'s scales", srows, scols, FP8_SCALE)
+    return MoFp8Matrix(q=_ptr(q), scales=_ptr(scales), rows=rows, ld_q=ldq, ld_scales=lds, inc_scales=inc,
                        block_rows=FP8_BLOCK if square else 1)
 
 
@@ -55,11 +60,12 @@ def fp8_dequantize(q, scales, *, dtype=torch.bfloat16, out=None, stream=None):
     it is given): exact in both, save under 2^-133 and over bfloat16's largest."""
     lib = load_library()
     dev = _device(q, scales, out)
-    a = _operand(q, scales, "q", square=False)
+    ldq = _matrix(q, "q", dtype=FP8)
     rows, cols = q.shape
+    lds = _matrix(scales, "scales", rows, _blocks(cols), FP8_SCALE)
     with _On(dev, stream) as on:
         out, ldx = _out(on, out, "out", rows, cols, dtype)
-        _check(lib.fp8_dequantize(a.q, a.ld_q, a.scales, a.ld_scales, rows, cols, _ptr(out), ldx, _code(out, "out"),
+        _check(lib.fp8_dequantize(_ptr(q), ldq, _ptr(scales), lds, rows, cols, _ptr(out), ldx, _code(out, "out"),
                                   on.handle), "fp8_dequantize")
     return out
 

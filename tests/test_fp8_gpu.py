@@ -207,6 +207,22 @@ def test_matmul_strides(k):
         assert bool((big == 7).all())
 
 
+@pytest.mark.parametrize("m,n,k", [(70, 300, 512), (300, 1000, 1280), (33, 129, 300)])
+def test_matmul_scales_by_columns(m, n, k):
+    """Scales that are a transposed view: the same result, bit by bit."""
+    A, sa = mo.fp8_quantize(matrix(m, k, F32, 30, spread=3.0))
+    B, sb, Bt, sbt = mo.fp8_quantize_weight(matrix(n, k, F32, 31, spread=0.3))
+    for dtype in (BF16, F32):
+        want = mo.fp8_matmul(A, sa, B, sb, dtype=dtype)
+        assert torch.equal(mo.fp8_matmul(A, sa, B, sbt.t(), dtype=dtype), want)
+        cols = F.codes(sa).t().contiguous().view(F.SCALE).t()
+        assert torch.equal(mo.fp8_matmul(A, cols, B, sbt.t(), dtype=dtype), want)
+        assert torch.equal(mo.fp8_matmul(B, sbt.t(), A, cols, dtype=dtype), mo.fp8_matmul(B, sb, A, sa, dtype=dtype))
+    dY = matrix(m, 200, BF16, 32)
+    G = torch.empty((200, k), device="cuda")
+    assert torch.equal(mo.fp8_weight_grad(dY, A, cols, G).clone(), mo.fp8_weight_grad(dY, A, sa, G))
+
+
 def test_matmul_bad_values():
     """NaN in an element or a scale reaches its row and column alone."""
     A, sa = mo.fp8_quantize(matrix(70, 512, F32, 12))

@@ -58,42 +58,50 @@ void operand_ranges(const MoF8Operand& o, int64_t cols, Ranges* r) {
     r->add(o.inc == 1 ? matrix_range(o.s, n, b, o.ld_s, 1, 0) : matrix_range(o.s, b, n, o.inc, 1, 0));
 }
 
-// Estimated us of a product in tiles of 256 x 64 nb with `stages` stages of 128 bytes of
-// K, and the splits of K (multiples of `unit` stages) that it takes: see the head's plan
-// (operators.cpp), whose tiles these are.
-double product_us(int64_t tiles, int64_t stages, int nb, int unit, int64_t* splits) {
+// Estimated us of a product in `tiles` tiles of 256 x 64 nb with `stages` stages of 128 bytes of
+// K on 256 CUs.  The rounds that fill them take a tile's K whole; the tiles left over are split into
+// the parts (multiples of `unit` stages) that take the least.  The parts' fp32 sums are
+// written, read and added by a second launch.
+double product_us(int64_t tiles, int64_t stages, int nb, int unit, int64_t* full, int64_t* splits) {
     const double stage = nb == 4 ? 1.43 : nb == 2 ? 0.8 : 0.6;
-    double least = double((tiles + 255) / 256 * stages) * stage;
+    const int64_t rem = tiles % 256;
+    const double whole = double(tiles / 256 * stages) * stage;
+    double least = whole + (rem ? double(stages) * stage : 0);
+    *full = tiles;
     *splits = 1;
-    for (int64_t k = 2; k <= std::min(256 / tiles, (stages + unit - 1) / unit); ++k) {
-        const double t = double((stages + k - 1) / k) * stage + double(tiles * k * nb) * 0.026 + double(k) * 0.1 + 4;
+    for (int64_t k = 2; rem && k <= std::min(256 / rem, (stages + unit - 1) / unit); ++k) {
+        const double t = whole + double((stages + k - 1) / k) * stage + double(rem * k * nb) * 0.026 + double(k) * 0.1 + 4;
         if (t < least) {
             least = t;
+            *full = tiles - rem;
             *splits = k;
         }
     }
     return least;
 }
 
-// Tiles and splits of a product with `p` rows along 256 and `q` along 64 nb.
+// Tiles and parts of a product with `p` rows along 256 and `q` along 64 nb.
 void plan_tiles(MoF8Plan* plan, int64_t p, int64_t q, int64_t stages, int unit, Carve* take) {
     double least = 0;
-    int64_t splits = 1;
+    int64_t splits = 1, full = 0;
     for (int nb = 4; nb >= 1; nb /= 2) {
-        int64_t k;
-        const double t = product_us((p + 255) / 256 * ((q + 64 * nb - 1) / (64 * nb)), stages, nb, unit, &k);
+        int64_t f, k;
+        const double t = product_us((p + 255) / 256 * ((q + 64 * nb - 1) / (64 * nb)), stages, nb, unit, &f, &k);
         if (nb == 4 || t < least) {
             least = t;
             plan->nb = nb;
+            full = f;
             splits = k;
         }
     }
     plan->tm = uint32_t((p + 255) / 256);
     plan->tn = uint32_t((q + 64 * plan->nb - 1) / (64 * plan->nb));
+    plan->full = uint32_t(full);
     plan->nk = int(stages);
     plan->stages = int(((stages + splits - 1) / splits + unit - 1) / unit * unit);
     plan->splits = int((stages + plan->stages - 1) / plan->stages);
-    if (plan->splits > 1) plan->off_part = (*take)(uint64_t(plan->splits) * plan->tm * plan->tn * 256 * 64 * plan->nb * 4);
+    if (uint64_t rem = uint64_t(plan->tm) * plan->tn - full)
+        plan->off_part = (*take)(rem * plan->splits * 256 * 64 * plan->nb * 4);
 }
 
 // Whether the rows can be loaded in place: whole blocks, 16-byte aligned rows less than 2^23

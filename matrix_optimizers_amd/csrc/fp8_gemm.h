@@ -1,23 +1,23 @@
-// The tiled NT GEMM on 8-bit operands with a power-of-two scale for each block of 128
-// along K: C[i][j] = sum over blocks kb of 2^(sp[i][kb] + sq[j][kb] - 254) sum_k P[i][k] Q[j][k].
+// The tiled GEMM of the 8-bit operators, C[p][q] = sum_k P[p][k] Q[q][k], on MFMA with
+// fp32 accumulators, for operands with K along their rows:
+//   - both in 8 bits with a power-of-two scale for each block of 128 along K;
+//   - both in bf16; or P in bf16 and Q as three bf16 planes whose sum is an fp32 value.
 //
-// One instruction, 16 x 16 x 128 of e4m3 with e8m0 scales, takes a whole block, so the
-// scales cost no arithmetic.  It holds its products to about 2^-17 of the largest of those
+// 8 bits.  One instruction, 16 x 16 x 128 of e4m3 with e8m0 scales, takes a whole block, so
+// the scales cost no arithmetic.  It holds its products to about 2^-17 of the largest of those
 // it adds together before they go into the fp32 accumulator: measured against 64 bits,
 // 1.5e-5 of the result's norm for normal data at any K, a hundredth of a bf16 rounding.
-// A product whose result is fp32 is therefore not taken here.
+// A product whose result is fp32 is therefore not taken in 8 bits.
 //
-// The tiles, the LDS rows of 128 bytes and their swizzle are those of the bf16 GEMM
-// (head_gemm.h): a stage of 128 bytes per row is 128 elements of K here, one
-// block, and the same bytes keep the matrix cores as long as 64 bf16 ones.  A lane's 32
-// bytes of a fragment are chunks kg and kg + 4 of its row, in P and in Q alike: which
-// element of a block meets which lane does not matter as both sides agree.
+// Tiles, LDS rows of 128 bytes and their swizzle are those of the head's GEMM (head_gemm.h): a
+// stage of 128 bytes per row is 64 elements of K in bf16, 128 in 8 bits, one block.  A lane's 32
+// bytes of a row's stage are its chunks kg and kg + 4, in P and in Q alike: which element of K
+// meets which lane does not matter as both sides agree.
 //
-// Scales of rows: a workgroup's rows load four stages' bytes at once, one dword per row,
-// straight to LDS; a wavefront keeps its 16-row blocks' dwords in registers and
-// shifts them by a byte per stage.  Scales of P in blocks of 128 rows (a weight) are the
-// same for all of a wavefront's rows: the workgroup's two blocks have theirs for all
-// of K in LDS from the start.
+// One workgroup per CU walks over its tiles and loads on across their ends: while a tile's last
+// two stages are multiplied, the next one's first two are on their way, and its results are
+// stored under the next tile's products.  16384 x 14336 x 4096 in 8 bits, one tile per
+// workgroup: 845 us, of which 125 were the stores that nothing hid.
 #pragma once
 
 #include "fp8.h"
@@ -29,89 +29,185 @@ using namespace mo_head_gemm;
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-// One operand: `rows` rows of bytes at q, ld apart (ld < 2^23; 16-byte aligned, K a multiple of
-// 128 bytes of them), and scales at s: row r's at s + (r >> shift) ld_s, inc apart.  Scales
-// of rows are whole aligned dwords of four stages, inc 1.
+// Kinds of operands: 8 bits with P's scales in blocks of 128 rows, or by rows; bf16; bf16 with Q
+// in three planes.
+enum Kind { SQUARE8, ROWS8, BF16, BF16_3 };
+constexpr bool is8(int kind) { return kind == SQUARE8 || kind == ROWS8; }
+
+// One operand: `rows` rows of bytes at q, ld apart (16-byte aligned, K in whole stages, 256 ld
+// < 2^31); plane p of three starts p * plane bytes further.  Scales at s: row r's at s +
+// (r >> shift) ld_s, inc apart; those of rows are whole aligned dwords of four stages, inc 1.
 struct Operand8 {
     const uint8_t *q, *s;
-    int64_t ld, rows, ld_s, inc;
+    int64_t ld, rows, plane, ld_s, inc;
     int shift;
 };
 
-// Two slots of a stage, two of four stages' scales by rows, and P's in blocks (SQ).
-constexpr int F8_MAX_STAGES = 8192;   // K up to 2^20
-template <bool SQ> constexpr int f8_scale_rows(int NB) { return (SQ ? 0 : 256) + 64 * NB; }
-template <bool SQ> constexpr int f8_lds(int NB) {
-    return head_lds(NB) + 2 * f8_scale_rows<SQ>(NB) * 4 + (SQ ? 2 * F8_MAX_STAGES : 0);
+// A product's tiles (tm x tn, 256 x 64 nb): the first `full` of them over all of K, the `rem` others
+// in `splits` parts of `per` stages each, whose sums go to `part`: [tile - full][split][wave][MB x NBW][lane].
+struct Tiles {
+    uint32_t tm, tn, full, rem, splits;
+    int nk, per;
+    f32x4* part;
+};
+
+// Tile i in order: bands of four tile rows, column by column, so that the 32 tiles an XCD runs at
+// once share 4 panels of P and 8 of Q in its L2.
+MO_DEV void tile_at(const Tiles& t, uint32_t i, uint32_t* ti, uint32_t* tj) {
+    const uint32_t band = i / (4 * t.tn), r = i - band * 4 * t.tn;
+    const uint32_t h = t.tm - band * 4 < 4 ? t.tm - band * 4 : 4;
+    *ti = band * 4 + r % h;
+    *tj = r / h;
 }
 
-// As head_tile: rows p0 .. of P and q0 .. of Q over nk stages from k0 on (a multiple of 4, as
-// are the scales' row lengths), Layout and accumulators as there.
+// What a workgroup multiplies at a time.
+struct Item {
+    uint32_t ti, tj, slot;
+    int k0, nk;
+    bool split;
+};
+
+// Item n of this workgroup: its share of the full tiles (each XCD a contiguous share, its
+// workgroups side by side), then of the parts.  False behind the last.
+MO_DEV bool item_of(const Tiles& t, uint32_t n, Item* it) {
+    const uint32_t grid = gridDim.x, rounds = (t.full + grid - 1) / grid;
+    uint32_t tile;
+    if (n < rounds) {
+        const uint32_t b = blockIdx.x + n * grid, x = b & 7, j = b >> 3, share = t.full >> 3, rem = t.full & 7;
+        if (j >= share + (x < rem ? 1u : 0u)) return false;   // (the last round, and then there are no parts)
+        tile = x * share + (x < rem ? x : rem) + j;
+        it->k0 = 0;
+        it->nk = t.nk;
+        it->split = false;
+    } else {
+        const uint32_t parts = t.rem * t.splits, b = blockIdx.x + (n - rounds) * grid;
+        const uint32_t x = b & 7, j = b >> 3, share = parts >> 3, rem = parts & 7;
+        if (j >= share + (x < rem ? 1u : 0u)) return false;
+        const uint32_t i = x * share + (x < rem ? x : rem) + j, s = i / t.rem;
+        tile = i - s * t.rem;
+        it->slot = tile * t.splits + s;
+        tile += t.full;
+        it->k0 = int(s) * t.per;
+        it->nk = t.nk - it->k0 < t.per ? t.nk - it->k0 : t.per;
+        it->split = true;
+    }
+    tile_at(t, tile, &it->ti, &it->tj);
+    return true;
+}
+
+template <int KIND> constexpr int scale_rows(int NB) { return is8(KIND) ? (KIND == SQUARE8 ? 0 : 256) + 64 * NB : 0; }
+// Two slots of a stage, and four of four stages' scales by rows.
+template <int KIND> constexpr int gemm_lds(int NB) { return head_lds(NB) + 4 * scale_rows<KIND>(NB) * 4; }
+
+// Stores behind which a barrier's loads may be waited for without them.
+template <int NB> constexpr int STORES = Layout<NB>::MB * Layout<NB>::NBW / 2;
+
+// Runs over the workgroup's items and hands each one's accumulators to store(item, wave, lane,
+// acc), acc f32x4[MB][NBW] as in head_tile; store returns whether it has issued STORES<NB> stores
+// at least.  All operand checks are the host's.
 //
-// A stage is MB row blocks of NBW MFMAs.  Up to the last two blocks, the fragments of the row
-// blocks ahead are read; then every read of the stage is done, each wave waits for its loads
-// of the next one and the barrier publishes it.  Beside the last two row blocks go the
-// reads of the next stage's first fragments, each into registers that were just used, and
-// the first loads of the stage after it.
-template <int NB, bool SQ, class Acc>
-__device__ __forceinline__ void f8_tile(uint8_t* smem, const Operand8& P, const Operand8& Q, int64_t p0, int64_t q0,
-                                        int k0, int nk, Acc& acc) {
+// A stage is MB row blocks of NBW blocks of MFMAs.  Up to the last two row blocks, the fragments
+// of the row blocks ahead are read; then every read of the stage is done, each wave waits for
+// its loads of the next one and the barrier publishes it.  Beside the last two row blocks go
+// the reads of the next stage's first fragments, each into registers that were just used, and the
+// loads of the stage after it.  One loop body for all stages: with peeled ends the compiler moved
+// the accumulators between them through memory.
+template <int NB, int KIND, class Store>
+__device__ __forceinline__ void run_tiles(uint8_t* smem, const Operand8& P, const Operand8& Q, const Tiles& t,
+                                          const Store& store) {
 #ifdef __HIP_DEVICE_COMPILE__
     using L = Layout<NB>;
     constexpr int WN = L::WN, MB = L::MB, NBW = L::NBW;
-    constexpr int TN = 64 * NB, SBYTES = HP_BYTES + TN * HKB, SROWS = f8_scale_rows<SQ>(NB);
+    constexpr int TN = 64 * NB, SBYTES = HP_BYTES + TN * HKB, SROWS = scale_rows<KIND>(NB);
     constexpr int LS = 4 + NB;                   // load instructions per stage and wave
-    constexpr int RING = MB < 4 ? MB : 4, AHEAD = 2;        // fragments of P held
-    static_assert(NBW == 4 && MB % RING == 0, "layout");
+    constexpr int RING = MB < 4 ? MB : 4;        // fragments of P held
+    static_assert(MB % RING == 0, "layout");
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
     const int r16 = lane & 15, kg = lane >> 4;
 
-    const int plim = int(P.rows - p0 < 256 ? P.rows - p0 : 256) - 1;
-    const int qlim = int(Q.rows - q0 < TN ? Q.rows - q0 : TN) - 1;
+    auto rsrc = [&](const uint8_t* p) __attribute__((always_inline)) {
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, -1, 0x00027000);
+    };
+
+    // ---- the loads' own walk over the items: always two stages ahead of the products ----
+    Item li;
+    uint32_t ln = 0;
+    bool more = item_of(t, 0, &li);
+    if (!more) return;
+    int ls = 0, lseg = 0, koff = 0, lgroup = 0;   // stage of the item, plane, byte offset, group of scales
     uint32_t vo[LS];
+    auto rP = rsrc(P.q), rQ = rsrc(Q.q);
+    constexpr int SI = (SROWS / 64 + 7) / 8 > 0 ? (SROWS / 64 + 7) / 8 : 1;
+    const uint8_t* sg[SI];
+    // The lane, out of the compiler's sight: what is computed from it once per item is not kept in
+    // registers over the stages.
+    auto lane_here = [&]() __attribute__((always_inline)) {
+        int l = lane;
+        asm volatile("" : "+v"(l));
+        return l;
+    };
+    // Sets the addresses to the start of item li.  Rows past an operand's end are its last row.
+    auto enter = [&]() __attribute__((always_inline)) {
+        const int lane = lane_here();
+        const int64_t p0 = int64_t(li.ti) * 256, q0 = int64_t(li.tj) * TN;
+        const int plim = int(P.rows - p0 < 256 ? P.rows - p0 : 256) - 1;
+        const int qlim = int(Q.rows - q0 < TN ? Q.rows - q0 : TN) - 1;
 #pragma unroll
-    for (int i = 0; i < LS; ++i) {
-        const int r = (i < 4 ? wave * 32 + i * 8 : wave * 8 * NB + (i - 4) * 8) + (lane >> 3);
-        const int lim = i < 4 ? plim : qlim;
-        vo[i] = uint32_t(r < lim ? r : lim) * uint32_t(i < 4 ? P.ld : Q.ld) + uint32_t(((lane & 7) ^ hswz(r)) << 4);
-    }
-    const auto rP = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t*>(P.q + p0 * P.ld + int64_t(k0) * HKB), 0, -1, 0x00027000);
-    const auto rQ = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t*>(Q.q + q0 * Q.ld + int64_t(k0) * HKB), 0, -1, 0x00027000);
-    int koff = 0;   // of the stage being loaded
+        for (int i = 0; i < LS; ++i) {
+            const int r = (i < 4 ? wave * 32 + i * 8 : wave * 8 * NB + (i - 4) * 8) + (lane >> 3);
+            const int lim = i < 4 ? plim : qlim;
+            vo[i] = uint32_t(r < lim ? r : lim) * uint32_t(i < 4 ? P.ld : Q.ld) + uint32_t(((lane & 7) ^ hswz(r)) << 4);
+        }
+        rP = rsrc(P.q + p0 * P.ld + int64_t(li.k0) * HKB);
+        rQ = rsrc(Q.q + q0 * Q.ld + int64_t(li.k0) * HKB + (KIND == BF16_3 ? 2 * Q.plane : 0));
+        ls = lseg = koff = 0;
+        if constexpr (SROWS > 0)
+#pragma unroll
+            for (int i = 0; i < SI; ++i) {
+                const int r = (wave + 8 * i) * 64 + lane - (KIND == SQUARE8 ? 0 : 256);
+                if (r < 0) {
+                    sg[i] = P.s + (p0 + (r + 256 < plim ? r + 256 : plim)) * P.ld_s + li.k0;
+                } else {
+                    const int64_t x = q0 + (r < qlim ? r : qlim);
+                    sg[i] = Q.s + (x >> Q.shift) * Q.ld_s + li.k0;
+                }
+            }
+    };
+    enter();
     auto issue1 = [&](int slot, int i) __attribute__((always_inline)) {
         uint8_t* sp = smem + slot * SBYTES + (i < 4 ? (wave * 32 + i * 8) * HKB : HP_BYTES + (wave * 8 * NB + (i - 4) * 8) * HKB);
         __builtin_amdgcn_raw_ptr_buffer_load_lds(i < 4 ? rP : rQ, (lds_void_t*)sp, 16, vo[i], koff, 0, 0);
     };
-    // Row 64 wave + lane of the 256 of P (not SQ) and TN of Q (the waves behind them load none): its
-    // scales of four stages.
-    const uint8_t* sg;
-    {
-        const int r = wave * 64 + lane - (SQ ? 0 : 256);
-        if (r < 0) {
-            sg = P.s + (p0 + (r + 256 < plim ? r + 256 : plim)) * P.ld_s;
-        } else {
-            const int64_t x = q0 + (r < qlim ? r : qlim);
-            sg = Q.s + (x >> Q.shift) * Q.ld_s;
-        }
-        sg += k0;
-    }
+    // Rows 64 (wave + 8 i) + lane of P's (by rows) and Q's scales: one dword, four stages.
     uint8_t* const sl = smem + 2 * SBYTES;
-    auto issue_scales = [&](int group) __attribute__((always_inline)) {
-        if (wave * 64 < SROWS) {
-            __builtin_amdgcn_global_load_lds(sg, (lds_void_t*)(sl + (group & 1) * (SROWS * 4) + wave * 256), 4, 0, 0);
-            sg += 4;
+    auto issue_scales = [&]() __attribute__((always_inline)) {
+        if constexpr (SROWS > 0) {
+            if (ls % 4 != 0 || !more) return;
+#pragma unroll
+            for (int i = 0; i < SI; ++i)
+                if ((wave + 8 * i) * 64 < SROWS) {
+                    __builtin_amdgcn_global_load_lds(sg[i], (lds_void_t*)(sl + (lgroup & 3) * (SROWS * 4) + (wave + 8 * i) * 256), 4, 0, 0);
+                    sg[i] += 4;
+                }
+            ++lgroup;
         }
     };
-
-#pragma unroll
-    for (int a = 0; a < MB; ++a)
-#pragma unroll
-        for (int b = 0; b < NBW; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // To the next stage.  Behind the last item the loads go on with its last stage, into slots that
+    // nothing reads any more.
+    auto advance = [&]() __attribute__((always_inline)) {
+        if (++ls < li.nk) {
+            koff += HKB;
+        } else if (KIND == BF16_3 && lseg < 2 && more) {
+            ++lseg;
+            ls = koff = 0;
+            rQ = rsrc(Q.q + int64_t(li.tj) * TN * Q.ld + int64_t(li.k0) * HKB + (2 - lseg) * Q.plane);
+        } else if (more && (more = item_of(t, ++ln, &li))) {
+            enter();
+        }
+    };
 
     union Frag {
         i32x8 v;
@@ -130,59 +226,80 @@ __device__ __forceinline__ void f8_tile(uint8_t* smem, const Operand8& P, const 
         fb[b].h[0] = *reinterpret_cast<const u32x4*>(p + x0);
         fb[b].h[1] = *reinterpret_cast<const u32x4*>(p + x1);
     };
-    constexpr int MS = SQ ? 1 : MB;
-    uint32_t sp[MS], sq[NBW];   // the scales of this stage in the low byte, the next stages' above
-    uint8_t* const st = sl + 2 * SROWS * 4;   // SQ: [block][stage]
-    const int stl = (nk + 3) & ~3;
-    auto rds = [&](int group) __attribute__((always_inline)) {
-        const uint32_t* p = reinterpret_cast<const uint32_t*>(sl + (group & 1) * (SROWS * 4));
-        if constexpr (SQ) {
-            sp[0] = *reinterpret_cast<const uint32_t*>(st + (wm * (MB * 16) / F8_BLOCK) * stl + group * 4);
+    // This stage's scales.  P's in blocks of 128 rows are one for all rows of a wavefront: lane l of
+    // pblock holds that of stage l of 64.
+    constexpr int MS = KIND == ROWS8 ? MB : 1;
+    uint32_t sp[MS], sq[NBW], pblock = 0, pnext = 0;
+    auto rds = [&](int group, int k) __attribute__((always_inline)) {
+        const uint8_t* p = sl + (group & 3) * (SROWS * 4) + r16 * 4 + k;
+        if constexpr (KIND == ROWS8)
+#pragma unroll
+            for (int a = 0; a < MB; ++a) sp[a] = p[(wm * (MB * 16) + a * 16) * 4];
+#pragma unroll
+        for (int b = 0; b < NBW; ++b) sq[b] = p[((KIND == SQUARE8 ? 0 : 256) + wn * (NBW * 16) + b * 16) * 4];
+    };
+    auto load_block = [&](const Item& it, int s) __attribute__((always_inline)) {
+        const int64_t row = int64_t(it.ti) * 256 + wm * (MB * 16), k = s + lane_here();
+        const uint8_t* p = P.s + ((row < P.rows ? row : P.rows - 1) >> 7) * P.ld_s;
+        pnext = p[(it.k0 + (k < it.nk ? k : it.nk - 1)) * P.inc];
+    };
+    f32x4 acc[MB][NBW];
+    auto mfma = [&](int a, int b) __attribute__((always_inline)) {
+        f32x4& c = acc[a][b];
+        const Frag &x = fa[a % RING], &y = fb[b];
+        if constexpr (is8(KIND)) {
+            c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x.v, y.v, c, 0, 0, 0, int(sp[KIND == ROWS8 ? a : 0]), 0,
+                                                                 int(sq[b]));
         } else {
 #pragma unroll
-            for (int a = 0; a < MB; ++a) sp[a] = p[wm * (MB * 16) + a * 16 + r16];
+            for (int h = 0; h < 2; ++h)
+                c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x.h[h]),
+                                                            __builtin_bit_cast(bf16x8, y.h[h]), c, 0, 0, 0);
         }
-#pragma unroll
-        for (int b = 0; b < NBW; ++b) sq[b] = p[(SQ ? 0 : 256) + wn * (NBW * 16) + b * 16 + r16];
-    };
-    auto mfma = [&](int a, int b) __attribute__((always_inline)) {
-        acc[a][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fa[a % RING].v, fb[b].v, acc[a][b], 0, 0, 0,
-                                                                     int(sp[SQ ? 0 : a]), 0, int(sq[b]));
         __builtin_amdgcn_sched_barrier(0);
     };
-    constexpr int LH = MB == 2 ? LS : LS / 2;   // loads beside the last two row blocks
-    const int kend = (nk - 1) * HKB;
-    // One stage, in `slot`.  Behind the last stages the loads go on with the last stage's addresses,
-    // into slots that nothing reads any more: one loop body, no ends peeled off it (the
-    // compiler moved the accumulators between them through memory).
-    auto stage = [&](int s, int slot) __attribute__((always_inline)) {
-        if (s % 4 == 0) rds(s / 4);
+
+    int stored = 0;   // 1: STORES stores or more are behind the loads that the next barrier waits for
+    // Everything that branches is done first: the compiler moves MFMAs down across branches, and the
+    // reads of their next operands then go to other registers.
+    auto stage = [&](const Item& it, int s, int slot, int group) __attribute__((always_inline)) {
+        advance();
+        issue_scales();
+        if constexpr (KIND == SQUARE8) {
+            if (s % 64 == 0) {
+                if (s > 0) pblock = pnext;
+                if (s + 64 < it.nk) load_block(it, s + 64);
+            }
+            sp[0] = uint32_t(__builtin_amdgcn_readlane(int(pblock), s & 63));
+        }
+        if constexpr (is8(KIND)) rds(group, s & 3);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int a = 0; a < MB - 2; ++a)
 #pragma unroll
             for (int b = 0; b < NBW; ++b) {
                 mfma(a, b);
-                if (a + AHEAD < MB && b == 0) rdp(slot, a + AHEAD);
-                constexpr int N = (MB - 2) * NBW > 0 ? (MB - 2) * NBW : 1;
-#pragma unroll
-                for (int l = LH; l < LS; ++l)
-                    if ((l - LH) * N / (LS - LH + (LS == LH)) + 1 == a * NBW + b) issue1(slot ^ 1, l);
+                if (b == 0) rdp(slot, a + 2);
                 __builtin_amdgcn_sched_barrier(0);
             }
-        if (MB != 2) koff = koff < kend ? koff + HKB : kend;
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        asm volatile("s_cmp_eq_u32 %0, 0\n"
+                     "s_cbranch_scc1 .Lall%=\n"
+                     "s_waitcnt vmcnt(%1)\n"
+                     "s_branch .Lgo%=\n"
+                     ".Lall%=: s_waitcnt vmcnt(0)\n"
+                     ".Lgo%=:" ::"s"(__builtin_amdgcn_readfirstlane(stored)), "n"(STORES<NB>) : "memory", "scc");
+        stored = 0;
         __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
-        if ((s + 2) % 4 == 0 && s + 2 < nk) issue_scales((s + 2) / 4);
 #pragma unroll
         for (int b = 0; b < NBW; ++b) {
             mfma(MB - 2, b);
             if (RING > 2 && b < 2) rdp(slot ^ 1, b);
 #pragma unroll
-            for (int l = 0; l < LH; ++l)
-                if (l * NBW / LH == b) issue1(slot, l);
+            for (int l = 0; l < LS; ++l)
+                if (l * NBW / LS == b) issue1(slot, l);
             __builtin_amdgcn_sched_barrier(0);
             mfma(MB - 1, b);
             rdq(slot ^ 1, b);
@@ -192,40 +309,20 @@ __device__ __forceinline__ void f8_tile(uint8_t* smem, const Operand8& P, const 
             rdp(slot ^ 1, 0);
             rdp(slot ^ 1, 1);
         }
-        if (MB == 2) koff = koff < kend ? koff + HKB : kend;
-#pragma unroll
-        for (int a = 0; a < MS; ++a) sp[a] >>= 8;
-#pragma unroll
-        for (int b = 0; b < NBW; ++b) sq[b] >>= 8;
     };
 
-    uint32_t s0 = 0;
-    const int sblk = tid >> 8;   // P's block whose scales this thread fetches
-    const bool swhole = p0 + sblk * F8_BLOCK < P.rows;
-    const uint8_t* const sb = P.s + ((p0 >> 7) + (swhole ? sblk : 0)) * P.ld_s + int64_t(k0) * P.inc;
-    if constexpr (SQ) {
-        const int k = tid & 255;
-        s0 = sb[(k < nk ? k : nk - 1) * P.inc];
-    }
-    issue_scales(0);
+    Item it = li;
+    if constexpr (KIND == SQUARE8) load_block(it, 0);
+    for (int s = 0; s < 2; ++s) {
+        if (s) advance();
+        issue_scales();
 #pragma unroll
-    for (int l = 0; l < LS; ++l) issue1(0, l);
-    koff = koff < kend ? koff + HKB : kend;
-#pragma unroll
-    for (int l = 0; l < LH; ++l) issue1(1, l);   // the others in stage 0
-    if (MB == 2) koff = koff < kend ? koff + HKB : kend;
-    if constexpr (SQ) {
-        for (int k = tid & 255; k < nk; k += 256) {
-            st[sblk * stl + k] = uint8_t(s0);
-            if (k + 256 < nk) s0 = sb[(k + 256) * P.inc];
-        }
-        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+        for (int l = 0; l < LS; ++l) issue1(s, l);
     }
-    // stage 0 has landed
-    if constexpr (LH == 4) asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
-    else if constexpr (LH == 3) asm volatile("s_waitcnt vmcnt(3)" ::: "memory");
+    // stage 0 has landed (stage 1's LS loads, and a dword of scales at most, came after it)
+    if constexpr (LS == 8) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+    else if constexpr (LS == 6) asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
     else asm volatile("s_waitcnt vmcnt(5)" ::: "memory");
-    static_assert(LH >= 3 && LH <= 5, "waits");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 #pragma unroll
@@ -233,9 +330,31 @@ __device__ __forceinline__ void f8_tile(uint8_t* smem, const Operand8& P, const 
     rdp(0, 0);
     rdp(0, 1);
     __builtin_amdgcn_sched_barrier(0);
-    for (int s = 0; s < nk; ++s) stage(s, s & 1);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
+    int slot = 0, group = 0;
+    for (uint32_t n = 0;;) {
+#pragma unroll
+        for (int a = 0; a < MB; ++a)
+#pragma unroll
+            for (int b = 0; b < NBW; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if constexpr (KIND == SQUARE8) pblock = pnext;
+        Item next;
+        const bool have = item_of(t, ++n, &next);
+        if constexpr (KIND == SQUARE8)
+            if (have && it.nk <= 64) load_block(next, 0);
+        const int stages = it.nk * (KIND == BF16_3 ? 3 : 1);
+#pragma clang loop unroll(disable)
+        for (int s = 0; s < stages; ++s, slot ^= 1) {
+            stage(it, s, slot, group);
+            if (is8(KIND) && s % 4 == 3) ++group;
+        }
+        if (is8(KIND) && stages % 4) ++group;
+        if constexpr (KIND == SQUARE8)
+            if (have && it.nk > 64) load_block(next, 0);
+        stored = store(it, wave, lane_here(), acc) ? 1 : 0;
+        if (!have) break;
+        it = next;
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // (the loads behind the last stage write LDS)
 #endif
 }
 

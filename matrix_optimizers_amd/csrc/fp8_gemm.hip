@@ -14,108 +14,115 @@ using namespace mo_f8;
 
 constexpr int XT = 64;   // rows and columns of a transposing tile
 
-// ---- the products' tiles -------------------------------------------------------------
+// ---- the products ---------------------------------------------------------------------
 
-// Where a tile's results go: dst[q][p], element strides ld and 1.
+// Where the results go: dst[q][p], element strides ld and 1.
 template <typename T> struct Out {
     T* dst;
     int64_t ld, cols, rows;   // cols: along P, rows: along Q
     bool add;
 };
 
-// Four neighbours of row q from column p on.
-template <typename T> MO_DEV void put4(const Out<T>& o, int64_t q, int64_t p, f32x4 v) {
-    const int n = int(o.cols - p < 4 ? o.cols - p : 4);
-    if (q >= o.rows || n <= 0) return;
-    T* d = o.dst + q * o.ld + p;
-    typedef T vec __attribute__((ext_vector_type(4)));
+// N neighbours of a row at d, n of them there.
+template <int N, typename T> MO_DEV void put(T* d, const float (&v)[N], int n, bool add) {
+    typedef T vec __attribute__((ext_vector_type(N)));
     typedef vec vec_e __attribute__((aligned(sizeof(T))));
-    if (n == 4) {
-        if (o.add) {
+    if (n >= N) {
+        vec w;
+        if (add) {
             const vec old = *reinterpret_cast<const vec_e*>(d);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += to_f32(T(old[e]));
-        }
-        vec w;
+            for (int e = 0; e < N; ++e) w[e] = from_f32<T>(v[e] + to_f32(T(old[e])));
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = from_f32<T>(v[e]);
+            for (int e = 0; e < N; ++e) w[e] = from_f32<T>(v[e]);
+        }
         *reinterpret_cast<vec_e*>(d) = w;
     } else {
 #pragma unroll
-        for (int e = 0; e < 3; ++e)
-            if (e < n) d[e] = from_f32<T>(o.add ? v[e] + to_f32(d[e]) : v[e]);
+        for (int e = 0; e < N - 1; ++e)
+            if (e < n) d[e] = from_f32<T>(add ? v[e] + to_f32(d[e]) : v[e]);
     }
 }
-
-// KIND 8: 8-bit operands, P's scales in blocks of 128 rows; 9: by rows; 1: bf16; 4: bf16, Q in
-// three planes.
-constexpr int KSQ = 8, KROW = 9;
-template <int KIND> struct Operands { using type = Operand; };
-template <> struct Operands<KSQ> { using type = Operand8; };
-template <> struct Operands<KROW> { using type = Operand8; };
-template <int KIND, int NB> constexpr int lds_of() {
-    return KIND == KSQ ? f8_lds<true>(NB) : KIND == KROW ? f8_lds<false>(NB) : head_lds(NB);
+// Four neighbours of row q from column p on.
+template <typename T> MO_DEV void put4(const Out<T>& o, int64_t q, int64_t p, f32x4 v) {
+    const int64_t n = o.cols - p;
+    if (q >= o.rows || n <= 0) return;
+    const float x[4] = {v[0], v[1], v[2], v[3]};
+    put<4>(o.dst + q * o.ld + p, x, int(n < 4 ? n : 4), o.add);
+}
+// A column block's results of two row blocks.  A lane has four neighbours of a row in each; the
+// odd rows of 16 lanes change their first block's against their neighbours' second one, so that
+// each lane stores eight neighbours (16 bytes of bf16, 64 in a line by four lanes).
+MO_DEV void put8(const Out<bf16_t>& o, int64_t q, int64_t p, int kg, f32x4 v0, f32x4 v1) {
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+#ifdef __HIP_DEVICE_COMPILE__
+        const auto w = __builtin_amdgcn_permlane16_swap(__float_as_uint(v0[e]), __float_as_uint(v1[e]), false, false);
+        x[e] = __uint_as_float(w[0]);
+        x[4 + e] = __uint_as_float(w[1]);
+#endif
+    }
+    p += (kg & 1) * 16 + (kg >> 1) * 8;
+    const int64_t n = o.cols - p;
+    if (q >= o.rows || n <= 0) return;
+    put<8>(o.dst + q * o.ld + p, x, int(n < 8 ? n : 8), o.add);
 }
 
-template <int KIND> struct Job {
-    typename Operands<KIND>::type P, Q;
-    int nk, stages;           // K stages in all and per split
-    uint32_t tm, tn, splits;
-    f32x4* part;              // the splits' sums: [split][tile][wave][MB x NBW][lane]
-};
-
-template <int KIND, int NB, bool SPLIT, typename T>
-__global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) void f8_product_kernel(Job<KIND> j,
+template <int KIND, int NB, typename T>
+__global__ __launch_bounds__(H_THREADS) __attribute__((amdgpu_waves_per_eu(2))) void f8_product_kernel(Operand8 P,
+                                                                                                       Operand8 Q, Tiles t,
                                                                                                        Out<T> o) {
     using L = Layout<NB>;
-    __shared__ __align__(16) uint8_t smem[lds_of<KIND, NB>()];
-    uint32_t ti, tj, split = 0, b = blockIdx.x;
-    if constexpr (SPLIT) {
-        const uint32_t per = (j.tm * j.tn + 7) / 8 * 8;
-        split = b / per;
-        b -= split * per;
-    }
-    if (!head_tile_of(b, j.tm, j.tn, ti, tj)) return;
-    const int k0 = int(split) * j.stages, nk = j.nk - k0 < j.stages ? j.nk - k0 : j.stages;
-    const int64_t p0 = int64_t(ti) * 256, q0 = int64_t(tj) * 64 * NB;
-    f32x4 acc[L::MB][L::NBW];
-    if constexpr (KIND >= KSQ) f8_tile<NB, KIND == KSQ>(smem, j.P, j.Q, p0, q0, k0, nk, acc);
-    else head_tile<NB, KIND>(smem, j.P, j.Q, p0, q0, k0, nk, acc);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    if constexpr (SPLIT) {
-        f32x4* z = j.part + ((int64_t(split) * j.tm * j.tn + int64_t(ti) * j.tn + tj) * 8 + wave) * (L::MB * L::NBW * 64) + lane;
+    __shared__ __align__(16) uint8_t smem[gemm_lds<KIND>(NB)];
+    auto store = [&](const Item& it, int wave, int lane, const f32x4 (&acc)[L::MB][L::NBW]) __attribute__((always_inline)) {
+        if (it.split) {
+            f32x4* z = t.part + (int64_t(it.slot) * 8 + wave) * (L::MB * L::NBW * 64) + lane;
 #pragma unroll
-        for (int i = 0; i < L::MB * L::NBW; ++i) z[i * 64] = acc[i / L::NBW][i % L::NBW];
-    } else {
-        const int64_t p = p0 + wave / L::WN * (L::MB * 16) + (lane >> 4) * 4, q = q0 + wave % L::WN * 64 + (lane & 15);
+            for (int i = 0; i < L::MB * L::NBW; ++i) z[i * 64] = acc[i / L::NBW][i % L::NBW];
+            return true;
+        }
+        const int kg = lane >> 4;
+        const int64_t p = int64_t(it.ti) * 256 + wave / L::WN * (L::MB * 16);
+        const int64_t q = int64_t(it.tj) * 64 * NB + wave % L::WN * 64 + (lane & 15);
 #pragma unroll
-        for (int b2 = 0; b2 < L::NBW; ++b2)
+        for (int b = 0; b < L::NBW; ++b)
+            if constexpr (sizeof(T) == 2) {
 #pragma unroll
-            for (int a = 0; a < L::MB; ++a) put4(o, q + b2 * 16, p + a * 16, acc[a][b2]);
-    }
+                for (int a = 0; a < L::MB; a += 2) put8(o, q + b * 16, p + a * 16, kg, acc[a][b], acc[a + 1][b]);
+            } else {
+#pragma unroll
+                for (int a = 0; a < L::MB; ++a) put4(o, q + b * 16, p + a * 16 + kg * 4, acc[a][b]);
+            }
+        // (a wave whose rows or columns are not all there may have skipped some)
+        return int64_t(it.ti) * 256 + 256 <= o.cols && int64_t(it.tj) * 64 * NB + 64 * NB <= o.rows;
+    };
+    run_tiles<NB, KIND>(smem, P, Q, t, store);
 }
 
-// The splits' sums in order: one wavefront per 16 x 64 of a wave's block.
+// The parts' sums in order: one wavefront per 16 x 64 of a wave's block.
 template <int NB, typename T>
-__global__ __launch_bounds__(256) void f8_sum_kernel(const f32x4* part, uint32_t tm, uint32_t tn, uint32_t splits, Out<T> o) {
+__global__ __launch_bounds__(256) void f8_sum_kernel(Tiles t, Out<T> o) {
     using L = Layout<NB>;
     const uint32_t unit = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const uint32_t a = unit % L::MB, wave = unit / L::MB % 8, tile = unit / (L::MB * 8);
-    if (tile >= tm * tn) return;
-    const f32x4* z = part + (int64_t(tile) * 8 + wave) * (L::MB * L::NBW * 64) + a * (L::NBW * 64) + lane;
-    const int64_t stride = int64_t(tm) * tn * 8 * (L::MB * L::NBW * 64);
+    const uint32_t a = unit % L::MB, wave = unit / L::MB % 8, slot = unit / (L::MB * 8);
+    if (slot >= t.rem) return;
+    const int64_t stride = 8 * (L::MB * L::NBW * 64);
+    const f32x4* z = t.part + int64_t(slot) * t.splits * stride + int64_t(wave) * (L::MB * L::NBW * 64) + a * (L::NBW * 64) + lane;
     f32x4 s[L::NBW];
 #pragma unroll
     for (int b = 0; b < L::NBW; ++b) s[b] = z[b * 64];
 #pragma unroll 4
-    for (uint32_t t = 1; t < splits; ++t)
+    for (uint32_t k = 1; k < t.splits; ++k)
 #pragma unroll
         for (int b = 0; b < L::NBW; ++b) {
-            const f32x4 x = z[t * stride + b * 64];
+            const f32x4 x = z[k * stride + b * 64];
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[b][e] += x[e];
         }
-    const uint32_t ti = tile / tn, tj = tile - ti * tn;
+    uint32_t ti, tj;
+    tile_at(t, t.full + slot, &ti, &tj);
     const int64_t p = int64_t(ti) * 256 + wave / L::WN * (L::MB * 16) + a * 16 + (lane >> 4) * 4;
     const int64_t q = int64_t(tj) * 64 * NB + wave % L::WN * 64 + (lane & 15);
 #pragma unroll
@@ -234,31 +241,23 @@ unsigned grid_for(int64_t items) {
     return unsigned(want < 4096 ? want : 4096);
 }
 
+// Workgroups of a product: one per CU at most, a multiple of the XCDs.
+unsigned product_grid(const Tiles& t) {
+    const uint64_t items = t.full ? t.full : uint64_t(t.rem) * t.splits;
+    return items < 256 ? unsigned((items + 7) / 8 * 8) : 256u;
+}
 template <int KIND, int NB, typename T>
-hipError_t product(const Job<KIND>& j, const Out<T>& o, hipStream_t s) {
-    const uint32_t tiles = j.tm * j.tn, grid = head_grid(tiles);
-    if (j.splits == 1) {
-        hipLaunchKernelGGL((f8_product_kernel<KIND, NB, false, T>), dim3(grid), dim3(H_THREADS), 0, s, j, o);
-        return hipGetLastError();
-    }
-    hipLaunchKernelGGL((f8_product_kernel<KIND, NB, true, T>), dim3(grid * j.splits), dim3(H_THREADS), 0, s, j, o);
-    hipLaunchKernelGGL((f8_sum_kernel<NB, T>), dim3(tiles * Layout<NB>::MB * 2), dim3(256), 0, s, j.part, j.tm, j.tn,
-                       j.splits, o);
+hipError_t product(const Operand8& P, const Operand8& Q, const Tiles& t, const Out<T>& o, hipStream_t s) {
+    hipLaunchKernelGGL((f8_product_kernel<KIND, NB, T>), dim3(product_grid(t)), dim3(H_THREADS), 0, s, P, Q, t, o);
+    if (t.rem) hipLaunchKernelGGL((f8_sum_kernel<NB, T>), dim3(t.rem * Layout<NB>::MB * 2), dim3(256), 0, s, t, o);
     return hipGetLastError();
 }
 template <int KIND, typename T>
-hipError_t product_nb(const Job<KIND>& j, int nb, const Out<T>& o, hipStream_t s) {
-    return nb == 4 ? product<KIND, 4>(j, o, s) : nb == 2 ? product<KIND, 2>(j, o, s) : product<KIND, 1>(j, o, s);
-}
-template <int KIND> Job<KIND> job_of(const MoF8Plan& p, uint8_t* ws) {
-    Job<KIND> j = {};
-    j.nk = p.nk;
-    j.stages = p.stages;
-    j.tm = p.tm;
-    j.tn = p.tn;
-    j.splits = uint32_t(p.splits);
-    j.part = reinterpret_cast<f32x4*>(ws + p.off_part);
-    return j;
+hipError_t product_nb(const Operand8& P, const Operand8& Q, const MoF8Plan& p, const Out<T>& o, uint8_t* ws, hipStream_t s) {
+    const Tiles t = {p.tm, p.tn, p.full, p.tm * p.tn - p.full, uint32_t(p.splits), p.nk, p.stages,
+                     reinterpret_cast<f32x4*>(ws + p.off_part)};
+    return p.nb == 4 ? product<KIND, 4>(P, Q, t, o, s) : p.nb == 2 ? product<KIND, 2>(P, Q, t, o, s)
+                                                                   : product<KIND, 1>(P, Q, t, o, s);
 }
 
 }  // namespace
@@ -281,29 +280,21 @@ hipError_t mo_launch_f8_pack(const MoF8Operand& a, const MoF8Plan& p, int i, int
     return hipGetLastError();
 }
 
-template <int KIND>
-static hipError_t matmul8(const MoF8Operand& A, const MoF8Operand& B, const MoF8Plan& p, void* Y, int64_t ldy,
-                          uint8_t* ws, hipStream_t s) {
-    Job<KIND> j = job_of<KIND>(p, ws);
+hipError_t mo_launch_f8_matmul(const MoF8Operand& A, const MoF8Operand& B, const MoF8Plan& p, void* Y, int64_t ldy,
+                               uint8_t* ws, hipStream_t s) {
+    if (p.bf16) {
+        const Operand8 Q = {ws + p.off_q[0], nullptr, p.kd * 2, A.rows}, P = {ws + p.off_q[1], nullptr, p.kd * 2, B.rows};
+        return product_nb<BF16, float>(P, Q, p, {static_cast<float*>(Y), ldy, B.rows, A.rows, false}, ws, s);
+    }
     auto operand = [&](const MoF8Operand& a, int i) {
-        Operand8 o = {a.q, a.s, a.ld, a.rows, a.ld_s, a.inc, a.shift};
+        Operand8 o = {a.q, a.s, a.ld, a.rows, 0, a.ld_s, a.inc, a.shift};
         if (p.pack_q[i]) o.q = ws + p.off_q[i], o.ld = p.kd;
         if (p.pack_s[i]) o.s = ws + p.off_s[i], o.ld_s = p.ks, o.inc = 1;
         return o;
     };
-    j.Q = operand(A, 0);
-    j.P = operand(B, 1);
-    return product_nb<KIND, bf16_t>(j, p.nb, {static_cast<bf16_t*>(Y), ldy, B.rows, A.rows, false}, s);
-}
-hipError_t mo_launch_f8_matmul(const MoF8Operand& A, const MoF8Operand& B, const MoF8Plan& p, void* Y, int64_t ldy,
-                               uint8_t* ws, hipStream_t s) {
-    if (p.bf16) {
-        Job<1> j = job_of<1>(p, ws);
-        j.Q = {ws + p.off_q[0], p.kd * 2, A.rows, 0};
-        j.P = {ws + p.off_q[1], p.kd * 2, B.rows, 0};
-        return product_nb<1, float>(j, p.nb, {static_cast<float*>(Y), ldy, B.rows, A.rows, false}, s);
-    }
-    return B.shift ? matmul8<KSQ>(A, B, p, Y, ldy, ws, s) : matmul8<KROW>(A, B, p, Y, ldy, ws, s);
+    const Operand8 Q = operand(A, 0), P = operand(B, 1);
+    const Out<bf16_t> o = {static_cast<bf16_t*>(Y), ldy, B.rows, A.rows, false};
+    return B.shift ? product_nb<SQUARE8>(P, Q, p, o, ws, s) : product_nb<ROWS8>(P, Q, p, o, ws, s);
 }
 
 hipError_t mo_launch_f8_transpose(const MoF8Wgrad& a, const MoF8Plan& p, bool x, uint8_t* ws, hipStream_t s) {
@@ -328,13 +319,13 @@ hipError_t mo_launch_f8_transpose(const MoF8Wgrad& a, const MoF8Plan& p, bool x,
 }
 
 template <int KIND> static hipError_t wgrad(const MoF8Wgrad& a, const MoF8Plan& p, uint8_t* ws, hipStream_t s) {
-    Job<KIND> j = job_of<KIND>(p, ws);
-    j.P = {ws + p.off_q[1], p.ld_t * 2, a.dim, 0};
-    j.Q = {ws + p.off_q[0], p.ld_t * 2, a.rows, a.rows * p.ld_t * 2};
+    const Operand8 P = {ws + p.off_q[1], nullptr, p.ld_t * 2, a.dim};
+    const Operand8 Q = {ws + p.off_q[0], nullptr, p.ld_t * 2, a.rows, a.rows * p.ld_t * 2};
+    const bool add = a.accumulate != 0;
     if (a.g_dtype == MO_BF16)
-        return product_nb<KIND, bf16_t>(j, p.nb, {static_cast<bf16_t*>(a.G), a.ldg, a.dim, a.rows, a.accumulate != 0}, s);
-    return product_nb<KIND, float>(j, p.nb, {static_cast<float*>(a.G), a.ldg, a.dim, a.rows, a.accumulate != 0}, s);
+        return product_nb<KIND, bf16_t>(P, Q, p, {static_cast<bf16_t*>(a.G), a.ldg, a.dim, a.rows, add}, ws, s);
+    return product_nb<KIND, float>(P, Q, p, {static_cast<float*>(a.G), a.ldg, a.dim, a.rows, add}, ws, s);
 }
 hipError_t mo_launch_f8_wgrad(const MoF8Wgrad& a, const MoF8Plan& p, uint8_t* ws, hipStream_t s) {
-    return a.dy_dtype == MO_BF16 ? wgrad<1>(a, p, ws, s) : wgrad<4>(a, p, ws, s);
+    return a.dy_dtype == MO_BF16 ? wgrad<BF16>(a, p, ws, s) : wgrad<BF16_3>(a, p, ws, s);
 }

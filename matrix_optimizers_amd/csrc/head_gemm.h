@@ -73,9 +73,6 @@ template <int PL> MO_DEV int seg_q(int s) { return PL == 1 ? 0 : s == 1 ? 2 : (s
 // Two planes of P (a value rounded to bf16, and what that left) and one of Q.
 template <> MO_DEV int seg_p<2>(int s) { return s == 0 ? 1 : 0; }
 template <> MO_DEV int seg_q<2>(int) { return 0; }
-// One plane of P and three of Q.
-template <> MO_DEV int seg_p<4>(int) { return 0; }
-template <> MO_DEV int seg_q<4>(int s) { return 2 - s; }
 
 // 128-byte rows of eight 16-byte chunks; chunk c of row r sits at c ^ (r / 2 mod 8).
 // A fragment read takes 16 rows at four consecutive chunks; any 16 lanes that
@@ -104,8 +101,8 @@ __device__ __forceinline__ void head_tile(uint8_t* smem, const Operand& P, const
     constexpr int WN = L::WN, MB = L::MB, NBW = L::NBW, HA = MB / 2, MF = HA * NBW;
     constexpr int TN = 64 * NB, SBYTES = HP_BYTES + TN * HKB;
     constexpr int LS = 4 + NB;                   // load instructions per stage and wave
-    constexpr int NSEG = PL == 3 ? 6 : PL == 4 ? 3 : PL;
-    static_assert(PL >= 1 && PL <= 4, "planes");
+    constexpr int NSEG = PL == 3 ? 6 : PL;
+    static_assert(PL >= 1 && PL <= 3, "planes");
     const int n = nk1 * NSEG;
 
     const int tid = threadIdx.x, lane = tid & 63;

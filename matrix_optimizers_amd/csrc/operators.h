@@ -73,8 +73,8 @@ struct MoF8Wgrad {
 struct MoF8Plan {
     bool bf16;                  // through the bf16 GEMM
     int nb;                     // tile width 64 nb along the operand without 256-row tiles
-    int nk, stages, splits;     // K stages in all, per split, splits
-    uint32_t tm, tn;
+    int nk, stages, splits;     // K stages in all; those of a part and the parts of a tile behind the first `full`
+    uint32_t tm, tn, full;
     int64_t kd, ks, ld_t;       // row lengths of the copies: elements, scales; stride along the tokens
     bool pack_q[2], pack_s[2];  // copies needed of A (0) and B (1)
     uint64_t off_q[2], off_s[2], off_part, bytes;

@@ -187,6 +187,28 @@ def test_matmul_scales():
         R.check(mo.fp8_matmul(A, sa, B, sb, dtype=dtype), want, bound, str(dtype))
 
 
+@pytest.mark.parametrize("m,n,k", [(4200, 4100, 128), (4200, 4100, 256), (4100, 4200, 384), (8192, 4096, 640),
+                                   (4133, 5001, 1100), (300, 700, 8320), (130, 300, 16640), (4352, 4352, 8704)])
+def test_matmul_many_tiles(m, n, k):
+    """More tiles than CUs (one workgroup multiplies several, of one to many stages), K that is split, and
+    more stages than one read of a weight's scales holds; each block's scale its own."""
+    A, sa = mo.fp8_quantize(matrix(m, k, F32, 40))
+    B, sb, _, _ = mo.fp8_quantize_weight(matrix(n, k, F32, 41, spread=0.3))
+    g = gen(42, m, n, k)
+    for s in (sa, sb):
+        F.codes(s).copy_(torch.randint(122, 132, s.shape, generator=g, device="cuda"))
+    for dtype in (BF16, F32):
+        want, bound = F.matmul(A, sa, B, sb, 1, 128, dtype)
+        Y = mo.fp8_matmul(A, sa, B, sb, dtype=dtype)
+        R.check(Y, want, bound, str(dtype))
+        off = float((Y.double() - want).norm() / want.norm())
+        assert off <= (R.ut(dtype) if dtype == BF16 else 2e-6), off
+    B1, sb1 = mo.fp8_quantize(matrix(n, k, F32, 41, spread=0.3))
+    F.codes(sb1).copy_(torch.randint(122, 132, sb1.shape, generator=g, device="cuda"))
+    want, bound = F.matmul(A, sa, B1, sb1, 1, 1, BF16)
+    R.check(mo.fp8_matmul(A, sa, B1, sb1), want, bound, "by rows")
+
+
 @pytest.mark.parametrize("k", [512, 500])
 def test_matmul_strides(k):
     m, n = 70, 300
@@ -268,6 +290,20 @@ def test_weight_grad(t, n, k, ydtype, gdtype):
     G = old.clone()
     want, bound = F.wgrad(dY, q, s, gdtype, old)
     R.check(mo.fp8_weight_grad(dY, q, s, G, accumulate=True), want, bound, "G added")
+
+
+@pytest.mark.parametrize("t,n,k,ydtype", [(64, 4200, 4100, BF16), (200, 4100, 4352, F32), (2048, 4400, 4400, BF16),
+                                          (1030, 5001, 4133, F32)])
+def test_weight_grad_many_tiles(t, n, k, ydtype):
+    q, s = mo.fp8_quantize(matrix(t, k, F32, 43))
+    dY = matrix(t, n, ydtype, 44)
+    G = torch.full((n, k), float("nan"), device="cuda")
+    want, bound = F.wgrad(dY, q, s, F32)
+    R.check(mo.fp8_weight_grad(dY, q, s, G), want, bound, "G")
+    assert float((G.double() - want).norm() / want.norm()) <= 2e-6
+    G = torch.empty((n, k), device="cuda", dtype=BF16)
+    want, bound = F.wgrad(dY, q, s, BF16)
+    R.check(mo.fp8_weight_grad(dY, q, s, G), want, bound, "G in bf16")
 
 
 def test_weight_grad_by_differences():

@@ -579,8 +579,12 @@ mo_status fp8_matmul_workspace_bytes(const mo_fp8_matrix* A, const mo_fp8_matrix
 mo_status fp8_matmul(const mo_fp8_matrix* A, const mo_fp8_matrix* B, int64_t dim, void* Y, int64_t ld_y,
                      int32_t dtype, void* workspace, size_t workspace_bytes, void* stream);
 
-mo_status fp8_weight_grad_workspace_bytes(const mo_fp8_matrix* X, int64_t dim, int64_t rows,
-                                          int32_t dy_dtype, size_t* bytes);
+/* Bytes of device workspace fp8_weight_grad needs.  Alignment counts: a bf16 dY of
+ * rows % 8 == 0 and an X of dim % 16 == 0, with 16-byte aligned rows and scales by rows, are
+ * read in place; others are copied first. */
+mo_status fp8_weight_grad_workspace_bytes(const void* dY, int64_t ld_dy, int32_t dy_dtype,
+                                          const mo_fp8_matrix* X, int64_t dim, int64_t rows,
+                                          size_t* bytes);
 
 /* The weight's gradient of Y = X W^T from an activation kept in 8 bits: G = dY^T X, dY
  * (X->rows tokens x rows, dy_dtype), X (tokens x dim, block_rows 1), G (rows x dim,

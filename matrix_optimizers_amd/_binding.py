@@ -198,7 +198,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "fp8_quantize_weight": [ptr, i64, i32, i64, i64, ptr, i64, ptr, i64, ptr, i64, ptr, i64, ptr],
         "fp8_matmul_workspace_bytes": [fp8, fp8, i64, i32, out],
         "fp8_matmul": [fp8, fp8, i64, ptr, i64, i32, ptr, size, ptr],
-        "fp8_weight_grad_workspace_bytes": [fp8, i64, i64, i32, out],
+        "fp8_weight_grad_workspace_bytes": [ptr, i64, i32, fp8, i64, i64, out],
         "fp8_weight_grad": [ptr, i64, i32, fp8, i64, ptr, i64, i32, i64, i32, ptr, size, ptr],
         "embedding_forward": [ptr, i64, ptr, i64, i64, i64, i32, f32, ptr, i64, ptr],
         "embedding_workspace_bytes": [i64, i64, i64, out],

@@ -138,17 +138,29 @@ MoF8Plan matmul_plan(const MoF8Operand& A, const MoF8Operand& B, int64_t dim, in
     return p;
 }
 
-MoF8Plan wgrad_plan(int64_t tokens, int64_t rows, int64_t dim, int32_t dy_dtype) {
+// Whether a weight gradient reads its operands as they lie: a bf16 dY, rows of both in whole aligned 16
+// bytes, less than 2^25 bytes apart (a stage's offsets have 31 bits), scales by rows.
+bool tokens_in_place(const MoF8Wgrad& a) {
+    return a.dy_dtype == MO_BF16 && a.rows % 8 == 0 && a.dim % 16 == 0 && a.lddy < (int64_t(1) << 24) &&
+           a.X.ld < (int64_t(1) << 25) && a.X.inc == 1 && a.X.ld_s < (int64_t(1) << 25) &&
+           ((reinterpret_cast<uintptr_t>(a.dY) | uintptr_t(a.lddy * 2)) & 15) == 0 &&
+           ((reinterpret_cast<uintptr_t>(a.X.q) | uintptr_t(a.X.ld)) & 15) == 0;
+}
+
+MoF8Plan wgrad_plan(const MoF8Wgrad& a) {
     MoF8Plan p = {};
     Carve take;
     p.bf16 = true;
-    p.kd = (tokens + 63) / 64 * 64;
-    // not a multiple of 4 KB, which would put a tile's rows on few memory channels
-    p.ld_t = p.kd * 2 % 4096 == 0 ? p.kd + 64 : p.kd;
-    const int planes = dy_dtype == MO_BF16 ? 1 : 3;
-    p.off_q[0] = take(uint64_t(planes) * rows * p.ld_t * 2);
-    p.off_q[1] = take(uint64_t(dim) * p.ld_t * 2);
-    plan_tiles(&p, dim, rows, p.kd / 64, 1, &take);
+    p.tokens = tokens_in_place(a);
+    p.kd = (a.X.rows + 63) / 64 * 64;
+    if (!p.tokens) {
+        // not a multiple of 4 KB, which would put a tile's rows on few memory channels
+        p.ld_t = p.kd * 2 % 4096 == 0 ? p.kd + 64 : p.kd;
+        const int planes = a.dy_dtype == MO_BF16 ? 1 : 3;
+        p.off_q[0] = take(uint64_t(planes) * a.rows * p.ld_t * 2);
+        p.off_q[1] = take(uint64_t(a.dim) * p.ld_t * 2);
+    }
+    plan_tiles(&p, a.dim, a.rows, p.kd / 64, 1, &take);
     p.bytes = take.at;
     return p;
 }
@@ -289,44 +301,48 @@ mo_status fp8_matmul(const mo_fp8_matrix* A, const mo_fp8_matrix* B, int64_t dim
     return MO_OK;
 }
 
-static mo_status wgrad_args(const mo_fp8_matrix* X, int64_t dim, int64_t rows, int32_t dy_dtype, MoF8Operand* x) {
+static mo_status wgrad_args(const void* dY, int64_t ld_dy, int32_t dy_dtype, const mo_fp8_matrix* X, int64_t dim,
+                            int64_t rows, MoF8Wgrad* a) {
     if (dim < 0 || rows < 0) return MO_ERR_INVALID_ARG;
     if (!dtype_ok(dy_dtype) || dim > kMaxSide || rows > kMaxSide) return MO_ERR_UNSUPPORTED;
-    MO_TRY(operand_of(X, dim, x));
-    return x->shift ? MO_ERR_INVALID_ARG : MO_OK;
+    *a = {};
+    MO_TRY(operand_of(X, dim, &a->X));
+    MO_TRY(stride_of(ld_dy, rows, &a->lddy));
+    if (a->X.shift) return MO_ERR_INVALID_ARG;
+    a->dY = dY;
+    a->dim = dim;
+    a->rows = rows;
+    a->dy_dtype = dy_dtype;
+    return MO_OK;
 }
 
-mo_status fp8_weight_grad_workspace_bytes(const mo_fp8_matrix* X, int64_t dim, int64_t rows, int32_t dy_dtype,
-                                          size_t* bytes) {
+mo_status fp8_weight_grad_workspace_bytes(const void* dY, int64_t ld_dy, int32_t dy_dtype, const mo_fp8_matrix* X,
+                                          int64_t dim, int64_t rows, size_t* bytes) {
     if (!bytes) return MO_ERR_INVALID_ARG;
     *bytes = 0;
-    MoF8Operand x;
-    MO_TRY(wgrad_args(X, dim, rows, dy_dtype, &x));
-    if (x.rows == 0 || dim == 0 || rows == 0) return MO_OK;
-    *bytes = size_t(wgrad_plan(x.rows, rows, dim, dy_dtype).bytes) + MO_WS_ALIGN;
+    MoF8Wgrad a;
+    MO_TRY(wgrad_args(dY, ld_dy, dy_dtype, X, dim, rows, &a));
+    if (a.X.rows == 0 || dim == 0 || rows == 0) return MO_OK;
+    const uint64_t need = wgrad_plan(a).bytes;
+    *bytes = need ? size_t(need) + MO_WS_ALIGN : 0;
     return MO_OK;
 }
 
 mo_status fp8_weight_grad(const void* dY, int64_t ld_dy, int32_t dy_dtype, const mo_fp8_matrix* X, int64_t dim, void* G,
                           int64_t ld_g, int32_t g_dtype, int64_t rows, int32_t accumulate, void* workspace,
                           size_t workspace_bytes, void* stream) {
-    MoF8Wgrad a = {};
-    MO_TRY(wgrad_args(X, dim, rows, dy_dtype, &a.X));
+    MoF8Wgrad a;
+    MO_TRY(wgrad_args(dY, ld_dy, dy_dtype, X, dim, rows, &a));
     if (!dtype_ok(g_dtype)) return MO_ERR_UNSUPPORTED;
-    MO_TRY(stride_of(ld_dy, rows, &a.lddy));
     MO_TRY(stride_of(ld_g, dim, &a.ldg));
     if (rows == 0 || dim == 0 || (a.X.rows == 0 && accumulate)) return MO_OK;
     if (!G || (a.X.rows && !dY)) return MO_ERR_INVALID_ARG;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     if (a.X.rows == 0) return zero_rows(G, rows, dim, a.ldg, g_dtype, MO_PHASE_F8_WGRAD, s);
-    a.dY = dY;
     a.G = G;
-    a.rows = rows;
-    a.dim = dim;
-    a.dy_dtype = dy_dtype;
     a.g_dtype = g_dtype;
     a.accumulate = accumulate;
-    const MoF8Plan p = wgrad_plan(a.X.rows, rows, dim, dy_dtype);
+    const MoF8Plan p = wgrad_plan(a);
     Ranges r;
     operand_ranges(a.X, dim, &r);
     r.add(matrix_range(dY, a.X.rows, rows, a.lddy, elem_size(dy_dtype), 0));
@@ -334,8 +350,10 @@ mo_status fp8_weight_grad(const void* dY, int64_t ld_dy, int32_t dy_dtype, const
     uint8_t* ws;
     if (!take_workspace(workspace, workspace_bytes, p.bytes, &r, &ws)) return MO_ERR_WORKSPACE_TOO_SMALL;
     if (r.conflict()) return MO_ERR_ALIAS;
-    MO_RUN(MO_PHASE_F8_PREP, mo_launch_f8_transpose(a, p, true, ws, s));
-    MO_RUN(MO_PHASE_F8_PREP, mo_launch_f8_transpose(a, p, false, ws, s));
+    if (!p.tokens) {
+        MO_RUN(MO_PHASE_F8_PREP, mo_launch_f8_transpose(a, p, true, ws, s));
+        MO_RUN(MO_PHASE_F8_PREP, mo_launch_f8_transpose(a, p, false, ws, s));
+    }
     MO_RUN(MO_PHASE_F8_WGRAD, mo_launch_f8_wgrad(a, p, ws, s));
     return MO_OK;
 }

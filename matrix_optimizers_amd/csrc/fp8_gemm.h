@@ -14,6 +14,16 @@
 // bytes of a row's stage are its chunks kg and kg + 4, in P and in Q alike: which element of K
 // meets which lane does not matter as both sides agree.
 //
+// Weight gradients (TOKENS): K along both operands' columns, P in 8 bits, Q in bf16, read where
+// they lie.  A stage is 64 rows (tokens) of 256 columns of P and 64 NB of Q, in bf16.  Both go
+// through registers, two stages ahead: P for one conversion per two elements that applies
+// the token's scale (q 2^e is a bf16 number, so exactly), Q because the compiler lets every
+// transposing read wait for all loads to LDS under way (2258 us instead of 1705 for the case
+// below).  The fragments come out of LDS through transposing reads: 16 lanes take 16 columns of four
+// rows.  The granules of 16 columns (32 bytes) of a row are permuted so that the rows that 32
+// lanes read together fall on different banks.  (With transposed copies made first, 16384
+// tokens x 14336 x 4096 took 1705 us, 254 of them for the copies.)
+//
 // One workgroup per CU walks over its tiles and loads on across their ends: while a tile's last
 // two stages are multiplied, the next one's first two are on their way, and its results are
 // stored under the next tile's products.  16384 x 14336 x 4096 in 8 bits, one tile per
@@ -30,33 +40,37 @@ using namespace mo_head_gemm;
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 // Kinds of operands: 8 bits with P's scales in blocks of 128 rows, or by rows; bf16; bf16 with Q
-// in three planes.
-enum Kind { SQUARE8, ROWS8, BF16, BF16_3 };
+// in three planes; P in 8 bits and Q in bf16, both with K along their columns.
+enum Kind { SQUARE8, ROWS8, BF16, BF16_3, TOKENS };
 constexpr bool is8(int kind) { return kind == SQUARE8 || kind == ROWS8; }
 
 // One operand: `rows` rows of bytes at q, ld apart (16-byte aligned, K in whole stages, 256 ld
 // < 2^31); plane p of three starts p * plane bytes further.  Scales at s: row r's at s +
 // (r >> shift) ld_s, inc apart; those of rows are whole aligned dwords of four stages, inc 1.
+// TOKENS: `rows` columns (of P a multiple of 16, of Q of 8) of `tokens` rows, 64 ld < 2^31.
 struct Operand8 {
     const uint8_t *q, *s;
     int64_t ld, rows, plane, ld_s, inc;
     int shift;
+    int64_t tokens;
 };
 
 // A product's tiles (tm x tn, 256 x 64 nb): the first `full` of them over all of K, the `rem` others
 // in `splits` parts of `per` stages each, whose sums go to `part`: [tile - full][split][wave][MB x NBW][lane].
 struct Tiles {
-    uint32_t tm, tn, full, rem, splits;
+    uint32_t tm, tn, full, rem, splits, band;
     int nk, per;
     f32x4* part;
 };
 
-// Tile i in order: bands of four tile rows, column by column, so that the 32 tiles an XCD runs at
-// once share 4 panels of P and 8 of Q in its L2.
+// Tile i in order: bands of `band` tile rows, column by column, so that the 32 tiles an XCD runs at
+// once share the band's panels of P, and keep them, and few of Q.  Bands of 4, 8, 16 rows: 16384 x 14336 x
+// 4096 in 8 bits 752, 742, 765 us; its weight gradient, where P's panels have half the bytes
+// of Q's, 1605, 1565, 1548.
 MO_DEV void tile_at(const Tiles& t, uint32_t i, uint32_t* ti, uint32_t* tj) {
-    const uint32_t band = i / (4 * t.tn), r = i - band * 4 * t.tn;
-    const uint32_t h = t.tm - band * 4 < 4 ? t.tm - band * 4 : 4;
-    *ti = band * 4 + r % h;
+    const uint32_t band = i / (t.band * t.tn), r = i - band * t.band * t.tn;
+    const uint32_t h = t.tm - band * t.band < t.band ? t.tm - band * t.band : t.band;
+    *ti = band * t.band + r % h;
     *tj = r / h;
 }
 
@@ -106,10 +120,12 @@ template <int NB> constexpr int STORES = Layout<NB>::MB * Layout<NB>::NBW / 2;
 // acc), acc f32x4[MB][NBW] as in head_tile; store returns whether it has issued STORES<NB> stores
 // at least.  All operand checks are the host's.
 //
-// A stage is MB row blocks of NBW blocks of MFMAs.  Up to the last two row blocks, the fragments
-// of the row blocks ahead are read; then every read of the stage is done, each wave waits for
-// its loads of the next one and the barrier publishes it.  Beside the last two row blocks go
-// the reads of the next stage's first fragments, each into registers that were just used, and the
+// A stage is MB row blocks of NBW blocks of MFMAs, two rows at a time, column by column (a column's
+// fragment of Q is then read in good time before its first use in the next stage: row by row,
+// 795 us for the product and 1690 for the weight gradient below, and 752 and 1605 in pairs).  Up to
+// the last pair, the fragments of the next pair are read; then every read of the stage is done, each
+// wave waits for its loads of the next one and the barrier publishes it.  Beside the last pair
+// go the reads of the next stage's first fragments, each into registers that were just used, and the
 // loads of the stage after it.  One loop body for all stages: with peeled ends the compiler moved
 // the accumulators between them through memory.
 template <int NB, int KIND, class Store>
@@ -137,6 +153,11 @@ __device__ __forceinline__ void run_tiles(uint8_t* smem, const Operand8& P, cons
     uint32_t ln = 0;
     bool more = item_of(t, 0, &li);
     if (!more) return;
+    constexpr bool TOK = KIND == TOKENS;
+    constexpr int QROW = TN * 2, QCH = QROW / 16;   // TOKENS: bytes and 16-byte chunks of a row of Q in a stage
+    // TOKENS: how row r's granules of 16 columns are permuted (Q's rows of 64 columns: two rows share the banks)
+    auto pf = [&](int r) __attribute__((always_inline)) { return (r & 3) | ((r >> 1 ^ r >> 2) & 4); };
+    auto qf = [&](int r) __attribute__((always_inline)) { return NB == 1 ? (r >> 1 & 1) | ((r >> 2 ^ r >> 3) & 2) : pf(r); };
     int ls = 0, lseg = 0, koff = 0, lgroup = 0;   // stage of the item, plane, byte offset, group of scales
     uint32_t vo[LS];
     auto rP = rsrc(P.q), rQ = rsrc(Q.q);
@@ -149,10 +170,28 @@ __device__ __forceinline__ void run_tiles(uint8_t* smem, const Operand8& P, cons
         asm volatile("" : "+v"(l));
         return l;
     };
+    // TOKENS: the operands from the first row of stage ls on.  What lies behind the last token reads as
+    // zeros; columns behind the last (or the next row's in their place) are not stored.
+    auto rS = rsrc(P.s);
+    auto enter_rows = [&]() __attribute__((always_inline)) {
+        const int64_t t0 = (int64_t(li.k0) + ls) * 64, left = (P.tokens - t0 < 64 ? P.tokens - t0 : 64) - 1;
+        const int64_t p = int64_t(li.ti) * 256, q = int64_t(li.tj) * QROW;
+        auto upto = [&](const uint8_t* from, int64_t bytes) __attribute__((always_inline)) {
+            return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(from), 0, int(bytes), 0x00027000);
+        };
+        rP = upto(P.q + t0 * P.ld + p, left * P.ld + P.rows - p);
+        rS = upto(P.s + t0 * P.ld_s + (p >> 7), left * P.ld_s + ((P.rows + 127) >> 7) - (p >> 7));
+        rQ = upto(Q.q + t0 * Q.ld + q, left * Q.ld + Q.rows * 2 - q);
+    };
     // Sets the addresses to the start of item li.  Rows past an operand's end are its last row.
     auto enter = [&]() __attribute__((always_inline)) {
         const int lane = lane_here();
         const int64_t p0 = int64_t(li.ti) * 256, q0 = int64_t(li.tj) * TN;
+        ls = lseg = koff = 0;
+        if constexpr (TOK) {
+            enter_rows();
+            return;
+        }
         const int plim = int(P.rows - p0 < 256 ? P.rows - p0 : 256) - 1;
         const int qlim = int(Q.rows - q0 < TN ? Q.rows - q0 : TN) - 1;
 #pragma unroll
@@ -163,7 +202,6 @@ __device__ __forceinline__ void run_tiles(uint8_t* smem, const Operand8& P, cons
         }
         rP = rsrc(P.q + p0 * P.ld + int64_t(li.k0) * HKB);
         rQ = rsrc(Q.q + q0 * Q.ld + int64_t(li.k0) * HKB + (KIND == BF16_3 ? 2 * Q.plane : 0));
-        ls = lseg = koff = 0;
         if constexpr (SROWS > 0)
 #pragma unroll
             for (int i = 0; i < SI; ++i) {
@@ -200,6 +238,7 @@ __device__ __forceinline__ void run_tiles(uint8_t* smem, const Operand8& P, cons
     auto advance = [&]() __attribute__((always_inline)) {
         if (++ls < li.nk) {
             koff += HKB;
+            if constexpr (TOK) enter_rows();
         } else if (KIND == BF16_3 && lseg < 2 && more) {
             ++lseg;
             ls = koff = 0;
@@ -209,19 +248,93 @@ __device__ __forceinline__ void run_tiles(uint8_t* smem, const Operand8& P, cons
         }
     };
 
+    // TOKENS: a thread takes 16 columns of two rows of P and eight of NB rows of Q.
+    constexpr int QR = 512 / QCH;   // rows of Q that the workgroup loads at a time
+    u32x4 xq[2], yq[NB];
+    uint32_t xscale[2] = {0, 0};
+    const uint32_t vP = uint32_t(tid >> 4) * uint32_t(P.ld) + (tid & 15) * 16;
+    const uint32_t vS = uint32_t(tid >> 4) * uint32_t(P.ld_s) + (tid >> 3 & 1);
+    const uint32_t vQ = uint32_t(tid / QCH) * uint32_t(Q.ld) + uint32_t(tid % QCH) * 16;
+    auto load_p = [&](int i) __attribute__((always_inline)) {
+        xq[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rP, vP, i * 32 * uint32_t(P.ld), 0));
+        xscale[i] = __builtin_amdgcn_raw_buffer_load_b8(rS, vS, i * 32 * uint32_t(P.ld_s), 0);
+    };
+    auto load_q = [&](int i) __attribute__((always_inline)) {
+        yq[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rQ, vQ, uint32_t(QR * i) * uint32_t(Q.ld), 0));
+    };
+    auto store_p = [&](int slot, int i) __attribute__((always_inline)) {
+        const int r = (tid >> 4) + 32 * i, g = tid & 15;
+        uint8_t* to = smem + slot * SBYTES + r * 512 + ((g ^ pf(r)) << 5);
+        // (the conversion takes the exponent's field, with 0 and 255 as in e8m0)
+        const float f = __uint_as_float(xscale[i] << 23);
+        u32x4 w[2];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            w[e / 2][e % 2 * 2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(xq[i][e], f, false));
+            w[e / 2][e % 2 * 2 + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(xq[i][e], f, true));
+        }
+        // half the lanes write their second eight columns first: 16 lanes then fall on all banks
+        const bool odd = (g & 8) != 0;
+        u32x4 a, b;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) { a[e] = odd ? w[1][e] : w[0][e]; b[e] = odd ? w[0][e] : w[1][e]; }
+        *reinterpret_cast<u32x4*>(to + (odd ? 16 : 0)) = a;
+        *reinterpret_cast<u32x4*>(to + (odd ? 0 : 16)) = b;
+    };
+    auto store_q = [&](int slot, int i) __attribute__((always_inline)) {
+        const int r = tid / QCH + QR * i, c = tid % QCH;
+        *reinterpret_cast<u32x4*>(smem + slot * SBYTES + HP_BYTES + r * QROW + ((c ^ (qf(r) << 1)) << 4)) = yq[i];
+    };
+    // Piece j of the stage in registers goes to LDS, and the one after it comes into its place.
+    auto piece = [&](int slot, int j) __attribute__((always_inline)) {
+        if (j < 2) {
+            store_p(slot, j);
+            load_p(j);
+        } else {
+            store_q(slot, j - 2);
+            load_q(j - 2);
+        }
+    };
+
     union Frag {
         i32x8 v;
         u32x4 h[2];
     };
     const int x0 = ((kg ^ hswz(r16)) << 4), x1 = x0 ^ 64;
-    const int pbase = (wm * (MB * 16) + r16) * HKB, qbase = HP_BYTES + (wn * (NBW * 16) + r16) * HKB;
+    // TOKENS: row kg 8 + r16 / 4 (+ 4 and + 32), columns 4 (r16 % 4) .. of a granule
+    const int trow = kg * 8 + (r16 >> 2);
+    const int pbase = TOK ? trow * 512 + (((wm * MB) ^ pf(trow)) << 5) + (r16 & 3) * 8 : (wm * (MB * 16) + r16) * HKB;
+    const int qbase = HP_BYTES + (TOK ? trow * QROW + (((wn * NBW) ^ qf(trow)) << 5) + (r16 & 3) * 8
+                                      : (wn * (NBW * 16) + r16) * HKB);
     Frag fa[RING], fb[NBW];
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    // a fragment of 16 columns through four transposing reads
+    auto tr = [&](Frag& f, const uint8_t* p, int row) __attribute__((always_inline)) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                              (lds_s16x4*)(p + (h * 32 + j * 4) * row)));
+                f.h[h][2 * j] = x[0];
+                f.h[h][2 * j + 1] = x[1];
+            }
+    };
     auto rdp = [&](int slot, int a) __attribute__((always_inline)) {
+        if constexpr (TOK) {
+            tr(fa[a % RING], smem + slot * SBYTES + (pbase ^ (a << 5)), 512);
+            return;
+        }
         const uint8_t* p = smem + slot * SBYTES + pbase + a * 16 * HKB;
         fa[a % RING].h[0] = *reinterpret_cast<const u32x4*>(p + x0);
         fa[a % RING].h[1] = *reinterpret_cast<const u32x4*>(p + x1);
     };
     auto rdq = [&](int slot, int b) __attribute__((always_inline)) {
+        if constexpr (TOK) {
+            tr(fb[b], smem + slot * SBYTES + (qbase ^ (b << 5)), QROW);
+            return;
+        }
         const uint8_t* p = smem + slot * SBYTES + qbase + b * 16 * HKB;
         fb[b].h[0] = *reinterpret_cast<const u32x4*>(p + x0);
         fb[b].h[1] = *reinterpret_cast<const u32x4*>(p + x1);
@@ -275,14 +388,24 @@ __device__ __forceinline__ void run_tiles(uint8_t* smem, const Operand8& P, cons
         if constexpr (is8(KIND)) rds(group, s & 3);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int a = 0; a < MB - 2; ++a)
+        for (int a = 0; a < MB - 2; a += 2)
 #pragma unroll
-            for (int b = 0; b < NBW; ++b) {
-                mfma(a, b);
-                if (b == 0) rdp(slot, a + 2);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        asm volatile("s_cmp_eq_u32 %0, 0\n"
+            for (int b = 0; b < NBW; ++b)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    mfma(a + i, b);
+                    if (i == 0 && b < 2) rdp(slot, a + 2 + b);
+                    if constexpr (TOK)
+#pragma unroll
+                        for (int j = 0; j < 2 + NB; ++j)
+                            if (j * (MB - 2) * NBW / (2 + NB) + 1 == a * NBW + 2 * b + i) piece(slot ^ 1, j);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+        if constexpr (TOK && MB == 2)
+#pragma unroll
+            for (int j = 0; j < 2 + NB; ++j) piece(slot ^ 1, j);
+        if constexpr (!TOK)
+            asm volatile("s_cmp_eq_u32 %0, 0\n"
                      "s_cbranch_scc1 .Lall%=\n"
                      "s_waitcnt vmcnt(%1)\n"
                      "s_branch .Lgo%=\n"
@@ -297,9 +420,10 @@ __device__ __forceinline__ void run_tiles(uint8_t* smem, const Operand8& P, cons
         for (int b = 0; b < NBW; ++b) {
             mfma(MB - 2, b);
             if (RING > 2 && b < 2) rdp(slot ^ 1, b);
+            if constexpr (!TOK)
 #pragma unroll
-            for (int l = 0; l < LS; ++l)
-                if (l * NBW / LS == b) issue1(slot, l);
+                for (int l = 0; l < LS; ++l)
+                    if (l * NBW / LS == b) issue1(slot, l);
             __builtin_amdgcn_sched_barrier(0);
             mfma(MB - 1, b);
             rdq(slot ^ 1, b);
@@ -313,14 +437,26 @@ __device__ __forceinline__ void run_tiles(uint8_t* smem, const Operand8& P, cons
 
     Item it = li;
     if constexpr (KIND == SQUARE8) load_block(it, 0);
-    for (int s = 0; s < 2; ++s) {
-        if (s) advance();
-        issue_scales();
+    if constexpr (TOK) {
+        load_p(0);
+        load_p(1);
 #pragma unroll
-        for (int l = 0; l < LS; ++l) issue1(s, l);
+        for (int i = 0; i < NB; ++i) load_q(i);
+        advance();
+#pragma unroll
+        for (int j = 0; j < 2 + NB; ++j) piece(0, j);
+        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+    } else {
+        for (int s = 0; s < 2; ++s) {
+            if (s) advance();
+            issue_scales();
+#pragma unroll
+            for (int l = 0; l < LS; ++l) issue1(s, l);
+        }
     }
     // stage 0 has landed (stage 1's LS loads, and a dword of scales at most, came after it)
-    if constexpr (LS == 8) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+    if constexpr (TOK) {}
+    else if constexpr (LS == 8) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
     else if constexpr (LS == 6) asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
     else asm volatile("s_waitcnt vmcnt(5)" ::: "memory");
     __builtin_amdgcn_s_barrier();

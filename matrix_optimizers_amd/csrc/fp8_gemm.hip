@@ -254,7 +254,8 @@ hipError_t product(const Operand8& P, const Operand8& Q, const Tiles& t, const O
 }
 template <int KIND, typename T>
 hipError_t product_nb(const Operand8& P, const Operand8& Q, const MoF8Plan& p, const Out<T>& o, uint8_t* ws, hipStream_t s) {
-    const Tiles t = {p.tm, p.tn, p.full, p.tm * p.tn - p.full, uint32_t(p.splits), p.nk, p.stages,
+    const Tiles t = {p.tm, p.tn, p.full, p.tm * p.tn - p.full, uint32_t(p.splits),
+                     KIND == TOKENS ? 16u : 8u, p.nk, p.stages,
                      reinterpret_cast<f32x4*>(ws + p.off_part)};
     return p.nb == 4 ? product<KIND, 4>(P, Q, t, o, s) : p.nb == 2 ? product<KIND, 2>(P, Q, t, o, s)
                                                                    : product<KIND, 1>(P, Q, t, o, s);
@@ -318,14 +319,21 @@ hipError_t mo_launch_f8_transpose(const MoF8Wgrad& a, const MoF8Plan& p, bool x,
     return hipGetLastError();
 }
 
-template <int KIND> static hipError_t wgrad(const MoF8Wgrad& a, const MoF8Plan& p, uint8_t* ws, hipStream_t s) {
-    const Operand8 P = {ws + p.off_q[1], nullptr, p.ld_t * 2, a.dim};
-    const Operand8 Q = {ws + p.off_q[0], nullptr, p.ld_t * 2, a.rows, a.rows * p.ld_t * 2};
+template <int KIND>
+static hipError_t wgrad(const Operand8& P, const Operand8& Q, const MoF8Wgrad& a, const MoF8Plan& p, uint8_t* ws,
+                        hipStream_t s) {
     const bool add = a.accumulate != 0;
     if (a.g_dtype == MO_BF16)
         return product_nb<KIND, bf16_t>(P, Q, p, {static_cast<bf16_t*>(a.G), a.ldg, a.dim, a.rows, add}, ws, s);
     return product_nb<KIND, float>(P, Q, p, {static_cast<float*>(a.G), a.ldg, a.dim, a.rows, add}, ws, s);
 }
 hipError_t mo_launch_f8_wgrad(const MoF8Wgrad& a, const MoF8Plan& p, uint8_t* ws, hipStream_t s) {
-    return a.dy_dtype == MO_BF16 ? wgrad<BF16>(a, p, ws, s) : wgrad<BF16_3>(a, p, ws, s);
+    if (p.tokens) {
+        const Operand8 P = {a.X.q, a.X.s, a.X.ld, a.dim, 0, a.X.ld_s, a.X.inc, 0, a.X.rows};
+        const Operand8 Q = {static_cast<const uint8_t*>(a.dY), nullptr, a.lddy * 2, a.rows, 0, 0, 0, 0, a.X.rows};
+        return wgrad<TOKENS>(P, Q, a, p, ws, s);
+    }
+    const Operand8 P = {ws + p.off_q[1], nullptr, p.ld_t * 2, a.dim};
+    const Operand8 Q = {ws + p.off_q[0], nullptr, p.ld_t * 2, a.rows, a.rows * p.ld_t * 2};
+    return a.dy_dtype == MO_BF16 ? wgrad<BF16>(P, Q, a, p, ws, s) : wgrad<BF16_3>(P, Q, a, p, ws, s);
 }

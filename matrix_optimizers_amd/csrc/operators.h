@@ -72,6 +72,7 @@ struct MoF8Wgrad {
 };
 struct MoF8Plan {
     bool bf16;                  // through the bf16 GEMM
+    bool tokens;                // a weight gradient from the operands as they lie
     int nb;                     // tile width 64 nb along the operand without 256-row tiles
     int nk, stages, splits;     // K stages in all; those of a part and the parts of a tile behind the first `full`
     uint32_t tm, tn, full;

@@ -143,17 +143,18 @@ def fp8_matmul(A, a_scales, B, b_scales, *, dtype=torch.bfloat16, out=None, work
     return out
 
 
-def _wgrad_bytes(x, dim, rows, code) -> int:
+def _wgrad_bytes(dY, ldy, ycode, x, dim, rows) -> int:
     out = ctypes.c_size_t(0)
-    _check(load_library().fp8_weight_grad_workspace_bytes(ctypes.byref(x), dim, rows, code, ctypes.byref(out)),
-           "fp8_weight_grad_workspace_bytes")
+    _check(load_library().fp8_weight_grad_workspace_bytes(_ptr(dY), ldy, ycode, ctypes.byref(x), dim, rows,
+                                                          ctypes.byref(out)), "fp8_weight_grad_workspace_bytes")
     return int(out.value)
 
 
 def fp8_weight_grad_workspace_bytes(dY, q, scales) -> int:
     """Workspace of fp8_weight_grad on these tensors."""
     x = _operand(q, scales, "q", square=False)
-    return _wgrad_bytes(x, q.shape[1], dY.shape[1], _code(dY, "dY"))
+    ldy = _matrix(dY, "dY", rows=q.shape[0])
+    return _wgrad_bytes(dY, ldy, _code(dY, "dY"), x, q.shape[1], dY.shape[1])
 
 
 def fp8_weight_grad(dY, q, scales, G, *, accumulate: bool = False, workspace=None, stream=None):
@@ -170,7 +171,7 @@ def fp8_weight_grad(dY, q, scales, G, *, accumulate: bool = False, workspace=Non
     ldg = _matrix(G, "G", rows, dim)
     ycode, gcode = _code(dY, "dY"), _code(G, "G")
     with _On(dev, stream) as on:
-        need = _wgrad_bytes(x, dim, rows, ycode) if workspace is None else 0
+        need = _wgrad_bytes(dY, ldy, ycode, x, dim, rows) if workspace is None else 0
         ws, have, keep = on.workspace(workspace, need)
         _check(lib.fp8_weight_grad(_ptr(dY), ldy, ycode, ctypes.byref(x), dim, _ptr(G), ldg, gcode, rows,
                                    1 if accumulate else 0, ws, have, on.handle), "fp8_weight_grad")

@@ -306,6 +306,37 @@ def test_weight_grad_many_tiles(t, n, k, ydtype):
     R.check(mo.fp8_weight_grad(dY, q, s, G), want, bound, "G in bf16")
 
 
+@pytest.mark.parametrize("t,n,k", [(70, 136, 272), (129, 256, 256), (33, 33, 33)])
+def test_weight_grad_bad_values(t, n, k):
+    """Infinities and NaN reach the sums they are in and no others, from the last token too."""
+    q, s = mo.fp8_quantize(matrix(t, k, F32, 45))
+    dY = matrix(t, n, BF16, 46)
+    dY[t - 1, 3] = float("inf")
+    dY[5, 7] = float("nan")
+    F.codes(q)[t - 1, 9] = 0x7F
+    F.codes(s)[2, 0] = 255
+    F.codes(q)[2, 30:] = 0x38
+    x = F.value(q, s)
+    want = dY.double().t() @ x
+    for dt in (BF16, F32):
+        G = mo.fp8_weight_grad(dY, q, s, torch.empty((n, k), device="cuda", dtype=dt)).double()
+        assert torch.equal(torch.isnan(G), torch.isnan(want))
+        assert torch.equal(G[torch.isinf(want)], want[torch.isinf(want)])
+        assert torch.equal(torch.isinf(G), torch.isinf(want))
+
+
+def test_weight_grad_scales():
+    """Tokens' scales far apart, and those of 0 (2^-127)."""
+    t, n, k = 300, 264, 528
+    q, s = mo.fp8_quantize(matrix(t, k, F32, 47))
+    g = gen(48)
+    F.codes(s).copy_(torch.randint(107, 147, s.shape, generator=g, device="cuda"))
+    F.codes(s)[::7] = 0
+    for dY in (matrix(t, n, BF16, 49), matrix(t, n, F32, 49)):
+        want, bound = F.wgrad(dY, q, s, F32)
+        R.check(mo.fp8_weight_grad(dY, q, s, torch.empty((n, k), device="cuda")), want, bound, "G")
+
+
 def test_weight_grad_by_differences():
     """Against differences of the loss sum(dY * (X W^T)), which is linear in W."""
     t, n, k = 9, 5, 140

@@ -104,35 +104,38 @@ void plan_tiles(MoF8Plan* plan, int64_t p, int64_t q, int64_t stages, int unit, 
         plan->off_part = (*take)(rem * plan->splits * 256 * 64 * plan->nb * 4);
 }
 
-// Whether the rows can be loaded in place: whole blocks, 16-byte aligned rows less than 2^23
-// bytes apart (the row offsets within a tile are 31 bits).
+// Whether the rows can be loaded straight to LDS: whole blocks, 16-byte aligned rows.
 bool q_in_place(const MoF8Operand& o, int64_t dim) {
-    return dim % kBlock == 0 && ((reinterpret_cast<uintptr_t>(o.q) | uintptr_t(o.ld)) & 15) == 0 && o.ld < (int64_t(1) << 23);
+    return dim % kBlock == 0 && ((reinterpret_cast<uintptr_t>(o.q) | uintptr_t(o.ld)) & 15) == 0;
 }
 // Whether the scales can: four stages' at a time, so whole aligned dwords.
 bool s_in_place(const MoF8Operand& o, int64_t dim) {
     return o.inc == 1 && blocks_of(dim) % 4 == 0 && ((reinterpret_cast<uintptr_t>(o.s) | uintptr_t(o.ld_s)) & 3) == 0;
 }
 
+// Few rows of A: the product reads B straight into registers, in one launch without a workspace.  us,
+// that and tiles, at 14336 x 4096 with a bf16 result: 16 tokens 15.5 and 19.4, 32 21.1 and 19.7, 64
+// 33.5 and 20.6; at 4096 x 4096: 7.3 and 15.4, 10.0 and 15.6, 15.8 and 15.9; at 1024 x 4096 6.8 and
+// 11.1, 9.5 and 11.2, 15.1 and 11.5.  With an fp32 result, or where the operands are not loaded in place, tiles
+// convert them first: 14336 x 4096 in fp32, 64 tokens, 33.8 and 65 (as a copy made first).
+bool few_rows(const MoF8Operand& A, const MoF8Operand& B, int64_t dim, int32_t dtype) {
+    return A.rows <= (dtype == MO_F32 || !q_in_place(A, dim) || !q_in_place(B, dim) ? 64 : 32);
+}
+
 MoF8Plan matmul_plan(const MoF8Operand& A, const MoF8Operand& B, int64_t dim, int32_t dtype) {
     MoF8Plan p = {};
     Carve take;
     const MoF8Operand* o[2] = {&A, &B};
-    p.bf16 = dtype == MO_F32;
+    p.bf16 = dtype == MO_F32 || !q_in_place(A, dim) || !q_in_place(B, dim);
     if (p.bf16) {
-        p.kd = (dim + 63) / 64 * 64;
-        for (int i = 0; i < 2; ++i) p.off_q[i] = take(uint64_t(o[i]->rows) * p.kd * 2);
-        plan_tiles(&p, B.rows, A.rows, p.kd / 64, 1, &take);
+        plan_tiles(&p, B.rows, A.rows, (dim + 63) / 64, 1, &take);
     } else {
-        p.kd = blocks_of(dim) * kBlock;
         p.ks = (blocks_of(dim) + 3) / 4 * 4;
         for (int i = 0; i < 2; ++i) {
-            p.pack_q[i] = !q_in_place(*o[i], dim);
             p.pack_s[i] = !(i == 1 && B.shift) && !s_in_place(*o[i], dim);   // (B's in blocks are read singly)
-            if (p.pack_q[i]) p.off_q[i] = take(uint64_t(o[i]->rows) * p.kd);
             if (p.pack_s[i]) p.off_s[i] = take(uint64_t(scale_rows(*o[i])) * p.ks);
         }
-        plan_tiles(&p, B.rows, A.rows, p.kd / kBlock, 4, &take);
+        plan_tiles(&p, B.rows, A.rows, dim / kBlock, 4, &take);
     }
     p.bytes = take.at;
     return p;
@@ -261,7 +264,10 @@ static mo_status matmul_args(const mo_fp8_matrix* A, const mo_fp8_matrix* B, int
     if (dim < 0) return MO_ERR_INVALID_ARG;
     if (!dtype_ok(dtype) || dim > kMaxSide) return MO_ERR_UNSUPPORTED;
     MO_TRY(operand_of(A, dim, a));
-    return operand_of(B, dim, b);
+    MO_TRY(operand_of(B, dim, b));
+    // the row offsets within a tile are 31 bits
+    const int64_t most = int64_t(1) << 23;
+    return std::max({a->ld, a->ld_s, b->ld, b->ld_s}) >= most ? MO_ERR_UNSUPPORTED : MO_OK;
 }
 
 mo_status fp8_matmul_workspace_bytes(const mo_fp8_matrix* A, const mo_fp8_matrix* B, int64_t dim, int32_t dtype,
@@ -270,7 +276,7 @@ mo_status fp8_matmul_workspace_bytes(const mo_fp8_matrix* A, const mo_fp8_matrix
     *bytes = 0;
     MoF8Operand a, b;
     MO_TRY(matmul_args(A, B, dim, dtype, &a, &b));
-    if (a.rows == 0 || b.rows == 0 || dim == 0) return MO_OK;
+    if (a.rows == 0 || b.rows == 0 || dim == 0 || few_rows(a, b, dim, dtype)) return MO_OK;
     const uint64_t need = matmul_plan(a, b, dim, dtype).bytes;
     *bytes = need ? size_t(need) + MO_WS_ALIGN : 0;
     return MO_OK;
@@ -286,18 +292,22 @@ mo_status fp8_matmul(const mo_fp8_matrix* A, const mo_fp8_matrix* B, int64_t dim
     if (!Y) return MO_ERR_INVALID_ARG;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     if (dim == 0) return zero_rows(Y, a.rows, b.rows, ldy, dtype, MO_PHASE_F8_GEMM, s);
-    const MoF8Plan p = matmul_plan(a, b, dim, dtype);
     Ranges r;
     operand_ranges(a, dim, &r);
     operand_ranges(b, dim, &r);
     r.add(matrix_range(Y, a.rows, b.rows, ldy, elem_size(dtype), 1));
+    if (few_rows(a, b, dim, dtype)) {
+        if (r.conflict()) return MO_ERR_ALIAS;
+        MO_RUN(MO_PHASE_F8_GEMM, mo_launch_f8_few(a, b, dim, Y, ldy, dtype, s));
+        return MO_OK;
+    }
+    const MoF8Plan p = matmul_plan(a, b, dim, dtype);
     uint8_t* ws;
     if (!take_workspace(workspace, workspace_bytes, p.bytes, &r, &ws)) return MO_ERR_WORKSPACE_TOO_SMALL;
     if (r.conflict()) return MO_ERR_ALIAS;
     for (int i = 0; i < 2; ++i)
-        if (p.bf16 || p.pack_q[i] || p.pack_s[i])
-            MO_RUN(MO_PHASE_F8_PREP, mo_launch_f8_pack(i ? b : a, p, i, dim, ws, s));
-    MO_RUN(MO_PHASE_F8_GEMM, mo_launch_f8_matmul(a, b, p, Y, ldy, ws, s));
+        if (p.pack_s[i]) MO_RUN(MO_PHASE_F8_PREP, mo_launch_f8_pack(i ? b : a, p, i, dim, ws, s));
+    MO_RUN(MO_PHASE_F8_GEMM, mo_launch_f8_matmul(a, b, p, dim, Y, ldy, dtype, ws, s));
     return MO_OK;
 }
 

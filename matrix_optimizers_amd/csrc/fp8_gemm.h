@@ -1,13 +1,17 @@
 // The tiled GEMM of the 8-bit operators, C[p][q] = sum_k P[p][k] Q[q][k], on MFMA with
 // fp32 accumulators, for operands with K along their rows:
 //   - both in 8 bits with a power-of-two scale for each block of 128 along K;
+//   - both in 8 bits, multiplied as the bf16 numbers they stand for (VALUES8);
 //   - both in bf16; or P in bf16 and Q as three bf16 planes whose sum is an fp32 value.
 //
 // 8 bits.  One instruction, 16 x 16 x 128 of e4m3 with e8m0 scales, takes a whole block, so
 // the scales cost no arithmetic.  It holds its products to about 2^-17 of the largest of those
 // it adds together before they go into the fp32 accumulator: measured against 64 bits,
 // 1.5e-5 of the result's norm for normal data at any K, a hundredth of a bf16 rounding.
-// A product whose result is fp32 is therefore not taken in 8 bits.
+// A product whose result is fp32 is therefore not taken in 8 bits, but with the operands' values,
+// whose products are exact in bf16 MFMA: VALUES8 brings 64 elements of K at a time through
+// registers, where they are converted on their way to LDS.  It asks nothing of alignment, and takes
+// the bf16 results of operands that cannot be loaded straight to LDS as well.
 //
 // Tiles, LDS rows of 128 bytes and their swizzle are those of the head's GEMM (head_gemm.h): a
 // stage of 128 bytes per row is 64 elements of K in bf16, 128 in 8 bits, one block.  A lane's 32
@@ -40,14 +44,15 @@ using namespace mo_head_gemm;
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 // Kinds of operands: 8 bits with P's scales in blocks of 128 rows, or by rows; bf16; bf16 with Q
-// in three planes; P in 8 bits and Q in bf16, both with K along their columns.
-enum Kind { SQUARE8, ROWS8, BF16, BF16_3, TOKENS };
+// in three planes; P in 8 bits and Q in bf16, both with K along their columns; 8 bits as values.
+enum Kind { SQUARE8, ROWS8, BF16, BF16_3, TOKENS, VALUES8 };
 constexpr bool is8(int kind) { return kind == SQUARE8 || kind == ROWS8; }
 
 // One operand: `rows` rows of bytes at q, ld apart (16-byte aligned, K in whole stages, 256 ld
 // < 2^31); plane p of three starts p * plane bytes further.  Scales at s: row r's at s +
 // (r >> shift) ld_s, inc apart; those of rows are whole aligned dwords of four stages, inc 1.
-// TOKENS: `rows` columns (of P a multiple of 16, of Q of 8) of `tokens` rows, 64 ld < 2^31.
+// TOKENS: `rows` columns (of P a multiple of 16, of Q of 8) of `tokens` rows, 64 ld < 2^31.  VALUES8: `tokens`
+// elements in a row, no alignment, 256 ld and 256 ld_s < 2^31.
 struct Operand8 {
     const uint8_t *q, *s;
     int64_t ld, rows, plane, ld_s, inc;
@@ -153,11 +158,11 @@ __device__ __forceinline__ void run_tiles(uint8_t* smem, const Operand8& P, cons
     uint32_t ln = 0;
     bool more = item_of(t, 0, &li);
     if (!more) return;
-    constexpr bool TOK = KIND == TOKENS;
+    constexpr bool TOK = KIND == TOKENS, VAL = KIND == VALUES8;
     constexpr int QROW = TN * 2, QCH = QROW / 16;   // TOKENS: bytes and 16-byte chunks of a row of Q in a stage
     // TOKENS: how row r's granules of 16 columns are permuted (Q's rows of 64 columns: two rows share the banks)
-    auto pf = [&](int r) __attribute__((always_inline)) { return (r & 3) | ((r >> 1 ^ r >> 2) & 4); };
-    auto qf = [&](int r) __attribute__((always_inline)) { return NB == 1 ? (r >> 1 & 1) | ((r >> 2 ^ r >> 3) & 2) : pf(r); };
+    auto pf = [&](int r) __attribute__((always_inline)) { return (r & 3) | (((r >> 1) ^ (r >> 2)) & 4); };
+    auto qf = [&](int r) __attribute__((always_inline)) { return NB == 1 ? ((r >> 1) & 1) | (((r >> 2) ^ (r >> 3)) & 2) : pf(r); };
     int ls = 0, lseg = 0, koff = 0, lgroup = 0;   // stage of the item, plane, byte offset, group of scales
     uint32_t vo[LS];
     auto rP = rsrc(P.q), rQ = rsrc(Q.q);
@@ -183,6 +188,27 @@ __device__ __forceinline__ void run_tiles(uint8_t* smem, const Operand8& P, cons
         rS = upto(P.s + t0 * P.ld_s + (p >> 7), left * P.ld_s + ((P.rows + 127) >> 7) - (p >> 7));
         rQ = upto(Q.q + t0 * Q.ld + q, left * Q.ld + Q.rows * 2 - q);
     };
+    // VALUES8: a thread takes 16 bytes of VP rows of P and VQ of Q, 64 bytes of a row by four threads.
+    constexpr int VP = 2, VQ = NB == 4 ? 2 : 1, VR = NB == 1 ? 64 : 128;
+    uint32_t oP[VP], oQ[VQ], oSP[VP], oSQ[VQ];
+    auto enter_values = [&]() __attribute__((always_inline)) {
+        const int64_t p0 = int64_t(li.ti) * 256, q0 = int64_t(li.tj) * TN;
+        const int plim = int(P.rows - p0 < 256 ? P.rows - p0 : 256) - 1;
+        const int qlim = int(Q.rows - q0 < TN ? Q.rows - q0 : TN) - 1;
+        const int r = (lane_here() + wave * 64) >> 2, c = (lane_here() & 3) * 16;
+#pragma unroll
+        for (int i = 0; i < VP; ++i) {
+            const int x = r + 128 * i < plim ? r + 128 * i : plim;
+            oP[i] = uint32_t(x) * uint32_t(P.ld) + c;
+            oSP[i] = uint32_t(((p0 + x) >> P.shift) - (p0 >> P.shift)) * uint32_t(P.ld_s);
+        }
+#pragma unroll
+        for (int i = 0; i < VQ; ++i) {
+            const int y = (r & (VR - 1)) + 128 * i, x = y < qlim ? y : qlim;
+            oQ[i] = uint32_t(x) * uint32_t(Q.ld) + c;
+            oSQ[i] = uint32_t(((q0 + x) >> Q.shift) - (q0 >> Q.shift)) * uint32_t(Q.ld_s);
+        }
+    };
     // Sets the addresses to the start of item li.  Rows past an operand's end are its last row.
     auto enter = [&]() __attribute__((always_inline)) {
         const int lane = lane_here();
@@ -190,6 +216,10 @@ __device__ __forceinline__ void run_tiles(uint8_t* smem, const Operand8& P, cons
         ls = lseg = koff = 0;
         if constexpr (TOK) {
             enter_rows();
+            return;
+        }
+        if constexpr (VAL) {
+            enter_values();
             return;
         }
         const int plim = int(P.rows - p0 < 256 ? P.rows - p0 : 256) - 1;
@@ -253,7 +283,7 @@ __device__ __forceinline__ void run_tiles(uint8_t* smem, const Operand8& P, cons
     u32x4 xq[2], yq[NB];
     uint32_t xscale[2] = {0, 0};
     const uint32_t vP = uint32_t(tid >> 4) * uint32_t(P.ld) + (tid & 15) * 16;
-    const uint32_t vS = uint32_t(tid >> 4) * uint32_t(P.ld_s) + (tid >> 3 & 1);
+    const uint32_t vS = uint32_t(tid >> 4) * uint32_t(P.ld_s) + ((tid >> 3) & 1);
     const uint32_t vQ = uint32_t(tid / QCH) * uint32_t(Q.ld) + uint32_t(tid % QCH) * 16;
     auto load_p = [&](int i) __attribute__((always_inline)) {
         xq[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rP, vP, i * 32 * uint32_t(P.ld), 0));
@@ -294,6 +324,58 @@ __device__ __forceinline__ void run_tiles(uint8_t* smem, const Operand8& P, cons
             store_q(slot, j - 2);
             load_q(j - 2);
         }
+    };
+
+    // VALUES8: a stage into registers, and from there, as bf16, to its slot.
+    u32x4 vp[VP], vq[VQ];
+    uint32_t vsp[VP], vsq[VQ];
+    auto load_values = [&]() __attribute__((always_inline)) {
+        typedef u32x4 u32x4_e1 __attribute__((aligned(1)));
+        const int st = li.k0 + (ls < li.nk ? ls : li.nk - 1);
+        const int64_t p0 = int64_t(li.ti) * 256, q0 = int64_t(li.tj) * TN, k = int64_t(st) * 64;
+        const uint8_t *p = P.q + p0 * P.ld + k, *q = Q.q + q0 * Q.ld + k;
+        const uint8_t *ps = P.s + (p0 >> P.shift) * P.ld_s + (st >> 1) * P.inc;
+        const uint8_t *qs = Q.s + (q0 >> Q.shift) * Q.ld_s + (st >> 1) * Q.inc;
+        if (k + 64 <= P.tokens) {
+#pragma unroll
+            for (int i = 0; i < VP; ++i) vp[i] = *reinterpret_cast<const u32x4_e1*>(p + oP[i]);
+#pragma unroll
+            for (int i = 0; i < VQ; ++i) vq[i] = *reinterpret_cast<const u32x4_e1*>(q + oQ[i]);
+        } else {
+            const int n = int(P.tokens - k) - (tid & 3) * 16;
+            auto part = [&](const uint8_t* x) __attribute__((always_inline)) {
+                const u32x2 lo = ldq8(x, n), hi = ldq8(x + 8, n - 8);
+                return u32x4{lo[0], lo[1], hi[0], hi[1]};
+            };
+#pragma unroll
+            for (int i = 0; i < VP; ++i) vp[i] = part(p + oP[i]);
+#pragma unroll
+            for (int i = 0; i < VQ; ++i) vq[i] = part(q + oQ[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < VP; ++i) vsp[i] = ps[oSP[i]];
+#pragma unroll
+        for (int i = 0; i < VQ; ++i) vsq[i] = qs[oSQ[i]];
+    };
+    auto store_values = [&](int slot) __attribute__((always_inline)) {
+        auto put = [&](uint8_t* to, int r, u32x4 x, uint32_t scale) __attribute__((always_inline)) {
+            const float f = __uint_as_float(scale << 23);   // (the conversion takes the exponent's field, as in e8m0)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                u32x4 w;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    w[2 * e] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * h + e], f, false));
+                    w[2 * e + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * h + e], f, true));
+                }
+                *reinterpret_cast<u32x4*>(to + r * HKB + (((tid & 3) * 2 + h) ^ hswz(r)) * 16) = w;
+            }
+        };
+        uint8_t* to = smem + slot * SBYTES;
+#pragma unroll
+        for (int i = 0; i < VP; ++i) put(to, (tid >> 2) + 128 * i, vp[i], vsp[i]);
+#pragma unroll
+        for (int i = 0; i < VQ; ++i) put(to + HP_BYTES, ((tid >> 2) & (VR - 1)) + 128 * i, vq[i], vsq[i]);
     };
 
     union Frag {
@@ -378,6 +460,10 @@ __device__ __forceinline__ void run_tiles(uint8_t* smem, const Operand8& P, cons
     auto stage = [&](const Item& it, int s, int slot, int group) __attribute__((always_inline)) {
         advance();
         issue_scales();
+        if constexpr (VAL) {
+            store_values(slot ^ 1);
+            load_values();
+        }
         if constexpr (KIND == SQUARE8) {
             if (s % 64 == 0) {
                 if (s > 0) pblock = pnext;
@@ -404,7 +490,7 @@ __device__ __forceinline__ void run_tiles(uint8_t* smem, const Operand8& P, cons
         if constexpr (TOK && MB == 2)
 #pragma unroll
             for (int j = 0; j < 2 + NB; ++j) piece(slot ^ 1, j);
-        if constexpr (!TOK)
+        if constexpr (!TOK && !VAL)
             asm volatile("s_cmp_eq_u32 %0, 0\n"
                      "s_cbranch_scc1 .Lall%=\n"
                      "s_waitcnt vmcnt(%1)\n"
@@ -420,7 +506,7 @@ __device__ __forceinline__ void run_tiles(uint8_t* smem, const Operand8& P, cons
         for (int b = 0; b < NBW; ++b) {
             mfma(MB - 2, b);
             if (RING > 2 && b < 2) rdp(slot ^ 1, b);
-            if constexpr (!TOK)
+            if constexpr (!TOK && !VAL)
 #pragma unroll
                 for (int l = 0; l < LS; ++l)
                     if (l * NBW / LS == b) issue1(slot, l);
@@ -446,6 +532,12 @@ __device__ __forceinline__ void run_tiles(uint8_t* smem, const Operand8& P, cons
 #pragma unroll
         for (int j = 0; j < 2 + NB; ++j) piece(0, j);
         __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+    } else if constexpr (VAL) {
+        load_values();
+        store_values(0);
+        advance();
+        load_values();
+        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
     } else {
         for (int s = 0; s < 2; ++s) {
             if (s) advance();
@@ -455,7 +547,7 @@ __device__ __forceinline__ void run_tiles(uint8_t* smem, const Operand8& P, cons
         }
     }
     // stage 0 has landed (stage 1's LS loads, and a dword of scales at most, came after it)
-    if constexpr (TOK) {}
+    if constexpr (TOK || VAL) {}
     else if constexpr (LS == 8) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
     else if constexpr (LS == 6) asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
     else asm volatile("s_waitcnt vmcnt(5)" ::: "memory");

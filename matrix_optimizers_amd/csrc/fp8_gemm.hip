@@ -8,6 +8,8 @@
 #include "fp8_gemm.h"
 #include "operators.h"
 
+#include <type_traits>
+
 namespace {
 
 using namespace mo_f8;
@@ -129,19 +131,139 @@ __global__ __launch_bounds__(256) void f8_sum_kernel(Tiles t, Out<T> o) {
     for (int b = 0; b < L::NBW; ++b) put4(o, q + b * 16, p, s[b]);
 }
 
+// ---- few tokens ------------------------------------------------------------------------
+
+// Few rows of Q: the product is a read of P, once, and the rest hides behind it.  A workgroup takes 16 RB
+// rows of P; its eight waves take every eighth block of K, straight into registers (no row of P
+// is wanted twice), D blocks of loads under way at a time, and add their sums up through LDS in order.  Q's
+// 16 TB rows come out of the caches.  Nothing is asked of the operands' alignment; what lies
+// behind a row's end is not read.  T float: the values as bf16 numbers, with exact products.
+template <int TB, int RB, typename T>
+__global__ __launch_bounds__(512) void f8_few_kernel(Operand8 P, Operand8 Q, int dim, Out<T> o) {
+#ifdef __HIP_DEVICE_COMPILE__
+    constexpr int D = 4 / RB;
+    __shared__ f32x4 sums[8][RB * TB][64];
+    const int lane = threadIdx.x & 63, r16 = lane & 15, kg = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t p0 = int64_t(blockIdx.x) * (16 * RB);
+    const int nk = (dim + F8_BLOCK - 1) / F8_BLOCK;
+    union Frag {
+        i32x8 v;
+        u32x4 h[2];
+    };
+    const uint8_t *pq[RB], *ps[RB], *qq[TB], *qs[TB];
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+        const int64_t r = p0 + i * 16 + r16, row = r < P.rows ? r : P.rows - 1;
+        pq[i] = P.q + row * P.ld + kg * 16;
+        ps[i] = P.s + (row >> P.shift) * P.ld_s;
+    }
+#pragma unroll
+    for (int i = 0; i < TB; ++i) {
+        const int64_t r = i * 16 + r16, row = r < Q.rows ? r : Q.rows - 1;
+        qq[i] = Q.q + row * Q.ld + kg * 16;
+        qs[i] = Q.s + (row >> Q.shift) * Q.ld_s;
+    }
+    f32x4 acc[RB][TB];
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+        for (int j = 0; j < TB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    typedef u32x4 u32x4_e1 __attribute__((aligned(1)));
+    // Chunks kg and kg + 4 of block k of a row (zeros behind its end; whole blocks without a branch)
+    auto load = [&](Frag& f, const uint8_t* p, int k, bool whole) __attribute__((always_inline)) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint8_t* a = p + int64_t(k) * F8_BLOCK + h * 64;
+            if (whole) {
+                f.h[h] = *reinterpret_cast<const u32x4_e1*>(a);
+            } else {
+                const int n = dim - k * F8_BLOCK - h * 64 - kg * 16;
+                const u32x2 lo = ldq8(a, n), hi = ldq8(a + 8, n - 8);
+                f.h[h] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+            }
+        }
+    };
+    // eight values of half e of chunk h, as bf16
+    auto wide = [&](const Frag& f, int h, int e, uint32_t scale) __attribute__((always_inline)) {
+        const float s = __uint_as_float(scale << 23);   // (the conversion takes the exponent's field, as in e8m0)
+        u32x4 w;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            w[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f.h[h][2 * e + i], s, false));
+            w[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f.h[h][2 * e + i], s, true));
+        }
+        return __builtin_bit_cast(bf16x8, w);
+    };
+    auto run = [&](int k, auto count, bool whole) __attribute__((always_inline)) {
+        constexpr int N = decltype(count)::value;
+        Frag a[N][RB], b[N][TB];
+        uint32_t sa[N][RB], sb[N][TB];
+#pragma unroll
+        for (int d = 0; d < N; ++d) {
+#pragma unroll
+            for (int i = 0; i < RB; ++i) {
+                load(a[d][i], pq[i], k + 8 * d, whole);
+                sa[d][i] = ps[i][(k + 8 * d) * P.inc];
+            }
+#pragma unroll
+            for (int i = 0; i < TB; ++i) {
+                load(b[d][i], qq[i], k + 8 * d, whole);
+                sb[d][i] = qs[i][(k + 8 * d) * Q.inc];
+            }
+        }
+#pragma unroll
+        for (int d = 0; d < N; ++d) {
+            if constexpr (sizeof(T) == 2) {
+#pragma unroll
+                for (int i = 0; i < RB; ++i)
+#pragma unroll
+                    for (int j = 0; j < TB; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[d][i].v, b[d][j].v, acc[i][j], 0, 0, 0,
+                                                                                     int(sa[d][i]), 0, int(sb[d][j]));
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    bf16x8 y[TB];
+#pragma unroll
+                    for (int j = 0; j < TB; ++j) y[j] = wide(b[d][j], c / 2, c % 2, sb[d][j]);
+#pragma unroll
+                    for (int i = 0; i < RB; ++i) {
+                        const bf16x8 x = wide(a[d][i], c / 2, c % 2, sa[d][i]);
+#pragma unroll
+                        for (int j = 0; j < TB; ++j)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y[j], acc[i][j], 0, 0, 0);
+                    }
+                }
+            }
+        }
+    };
+    const int full = dim / F8_BLOCK;
+    int k = wave;
+    for (; k + 8 * (D - 1) < full; k += 8 * D) run(k, std::integral_constant<int, D>(), true);
+    for (; k < full; k += 8) run(k, std::integral_constant<int, 1>(), true);
+    if (k < nk) run(k, std::integral_constant<int, 1>(), false);
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+        for (int j = 0; j < TB; ++j) sums[wave][i * TB + j][lane] = acc[i][j];
+    __syncthreads();
+    for (int u = wave; u < RB * TB; u += 8) {
+        f32x4 s = sums[0][u][lane];
+#pragma unroll
+        for (int w = 1; w < 8; ++w) {
+            const f32x4 x = sums[w][u][lane];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[e] += x[e];
+        }
+        put4(o, u % TB * 16 + r16, p0 + u / TB * 16 + kg * 4, s);
+    }
+#endif
+}
+
 // ---- operands laid out for them ------------------------------------------------------
 
-// q with rows of kd bytes (a multiple of 128, zeros behind dim), and its scales with rows of
-// ks bytes (a multiple of 4, 127 behind the last block).
-__global__ __launch_bounds__(256) void f8_copy_kernel(const uint8_t* q, int64_t ld, int64_t rows, int dim, uint8_t* dst,
-                                                      int kd) {
-    const int64_t chunks = int64_t(kd / 8) * rows;
-    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < chunks; i += int64_t(gridDim.x) * 256) {
-        const int64_t r = i / (kd / 8);
-        const int c = int(i - r * (kd / 8)) * 8;
-        *reinterpret_cast<u32x2*>(dst + r * kd + c) = ldq8(q + r * ld + c, dim - c);
-    }
-}
+// Scales with rows of ks bytes (a multiple of 4, 127 behind the last block).
 __global__ __launch_bounds__(256) void f8_copy_scales_kernel(const uint8_t* s, int64_t ld, int64_t inc, int64_t rows, int kb,
                                                              uint32_t* dst, int words) {
     const int64_t n = int64_t(words) * rows;
@@ -152,18 +274,6 @@ __global__ __launch_bounds__(256) void f8_copy_scales_kernel(const uint8_t* s, i
 #pragma unroll
         for (int e = 0; e < 4; ++e) w |= uint32_t(c + e < kb ? s[r * ld + (c + e) * inc] : 127) << (8 * e);
         dst[i] = w;
-    }
-}
-
-// The values of q in bf16, rows of kd elements (a multiple of 64, zeros behind dim).
-__global__ __launch_bounds__(256) void f8_unpack_kernel(const uint8_t* q, int64_t ld, const uint8_t* s, int64_t ld_s,
-                                                        int64_t inc, int shift, int64_t rows, int dim, bf16_t* dst, int kd) {
-    const int64_t chunks = int64_t(kd / 8) * rows;
-    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < chunks; i += int64_t(gridDim.x) * 256) {
-        const int64_t r = i / (kd / 8);
-        const int c = int(i - r * (kd / 8)) * 8;
-        const float f = c < dim ? scale_value(s[(r >> shift) * ld_s + c / F8_BLOCK * inc]) : 0.f;
-        store8(dst + r * kd + c, from_e4m3(ldq8(q + r * ld + c, dim - c), f));
     }
 }
 
@@ -263,38 +373,47 @@ hipError_t product_nb(const Operand8& P, const Operand8& Q, const MoF8Plan& p, c
 
 }  // namespace
 
-// Operand i (0: A, 1: B) of the product, copied or unpacked into the workspace.
+// The scales of operand i (0: A, 1: B) of the product, copied into the workspace.
 hipError_t mo_launch_f8_pack(const MoF8Operand& a, const MoF8Plan& p, int i, int64_t dim, uint8_t* ws, hipStream_t s) {
-    if (p.bf16) {
-        hipLaunchKernelGGL(f8_unpack_kernel, dim3(grid_for(a.rows * (p.kd / 8))), dim3(256), 0, s, a.q, a.ld, a.s, a.ld_s,
-                           a.inc, a.shift, a.rows, int(dim), reinterpret_cast<bf16_t*>(ws + p.off_q[i]), int(p.kd));
-        return hipGetLastError();
-    }
-    if (p.pack_q[i])
-        hipLaunchKernelGGL(f8_copy_kernel, dim3(grid_for(a.rows * (p.kd / 8))), dim3(256), 0, s, a.q, a.ld, a.rows, int(dim),
-                           ws + p.off_q[i], int(p.kd));
-    if (p.pack_s[i]) {
-        const int64_t r = (a.rows + (int64_t(1) << a.shift) - 1) >> a.shift;
-        hipLaunchKernelGGL(f8_copy_scales_kernel, dim3(grid_for(r * (p.ks / 4))), dim3(256), 0, s, a.s, a.ld_s, a.inc, r,
-                           int((dim + F8_BLOCK - 1) / F8_BLOCK), reinterpret_cast<uint32_t*>(ws + p.off_s[i]), int(p.ks / 4));
-    }
+    const int64_t r = (a.rows + (int64_t(1) << a.shift) - 1) >> a.shift;
+    hipLaunchKernelGGL(f8_copy_scales_kernel, dim3(grid_for(r * (p.ks / 4))), dim3(256), 0, s, a.s, a.ld_s, a.inc, r,
+                       int((dim + F8_BLOCK - 1) / F8_BLOCK), reinterpret_cast<uint32_t*>(ws + p.off_s[i]), int(p.ks / 4));
     return hipGetLastError();
 }
 
-hipError_t mo_launch_f8_matmul(const MoF8Operand& A, const MoF8Operand& B, const MoF8Plan& p, void* Y, int64_t ldy,
-                               uint8_t* ws, hipStream_t s) {
-    if (p.bf16) {
-        const Operand8 Q = {ws + p.off_q[0], nullptr, p.kd * 2, A.rows}, P = {ws + p.off_q[1], nullptr, p.kd * 2, B.rows};
-        return product_nb<BF16, float>(P, Q, p, {static_cast<float*>(Y), ldy, B.rows, A.rows, false}, ws, s);
-    }
+template <int TB, typename T>
+static hipError_t few(const Operand8& P, const Operand8& Q, int64_t dim, const Out<T>& o, hipStream_t s) {
+    // 16 rb rows per workgroup: more read Q's rows less often, fewer workgroups than CUs leave some idle
+    const int64_t rows = P.rows;
+#define MO_FEW(RB)                                                                                                    hipLaunchKernelGGL((f8_few_kernel<TB, RB, T>), dim3(unsigned((rows + 16 * RB - 1) / (16 * RB))), dim3(512), 0, s, P, Q,                        int(dim), o)
+    if (rows >= 256 * 64) MO_FEW(4);
+    else if (rows >= 256 * 32) MO_FEW(2);
+    else MO_FEW(1);
+#undef MO_FEW
+    return hipGetLastError();
+}
+template <typename T>
+static hipError_t few_tb(const Operand8& P, const Operand8& Q, int64_t dim, const Out<T>& o, hipStream_t s) {
+    return Q.rows <= 16 ? few<1>(P, Q, dim, o, s) : Q.rows <= 32 ? few<2>(P, Q, dim, o, s) : few<4>(P, Q, dim, o, s);
+}
+hipError_t mo_launch_f8_few(const MoF8Operand& A, const MoF8Operand& B, int64_t dim, void* Y, int64_t ldy, int32_t dtype,
+                            hipStream_t s) {
+    const Operand8 Q = {A.q, A.s, A.ld, A.rows, 0, A.ld_s, A.inc, A.shift};
+    const Operand8 P = {B.q, B.s, B.ld, B.rows, 0, B.ld_s, B.inc, B.shift};
+    if (dtype == MO_BF16) return few_tb<bf16_t>(P, Q, dim, {static_cast<bf16_t*>(Y), ldy, B.rows, A.rows, false}, s);
+    return few_tb<float>(P, Q, dim, {static_cast<float*>(Y), ldy, B.rows, A.rows, false}, s);
+}
+hipError_t mo_launch_f8_matmul(const MoF8Operand& A, const MoF8Operand& B, const MoF8Plan& p, int64_t dim, void* Y,
+                               int64_t ldy, int32_t dtype, uint8_t* ws, hipStream_t s) {
     auto operand = [&](const MoF8Operand& a, int i) {
-        Operand8 o = {a.q, a.s, a.ld, a.rows, 0, a.ld_s, a.inc, a.shift};
-        if (p.pack_q[i]) o.q = ws + p.off_q[i], o.ld = p.kd;
+        Operand8 o = {a.q, a.s, a.ld, a.rows, 0, a.ld_s, a.inc, a.shift, dim};
         if (p.pack_s[i]) o.s = ws + p.off_s[i], o.ld_s = p.ks, o.inc = 1;
         return o;
     };
     const Operand8 Q = operand(A, 0), P = operand(B, 1);
+    if (dtype == MO_F32) return product_nb<VALUES8, float>(P, Q, p, {static_cast<float*>(Y), ldy, B.rows, A.rows, false}, ws, s);
     const Out<bf16_t> o = {static_cast<bf16_t*>(Y), ldy, B.rows, A.rows, false};
+    if (p.bf16) return product_nb<VALUES8>(P, Q, p, o, ws, s);
     return B.shift ? product_nb<SQUARE8>(P, Q, p, o, ws, s) : product_nb<ROWS8>(P, Q, p, o, ws, s);
 }
 

@@ -71,18 +71,21 @@ struct MoF8Wgrad {
     int32_t dy_dtype, g_dtype, accumulate;
 };
 struct MoF8Plan {
-    bool bf16;                  // through the bf16 GEMM
+    bool bf16;                  // through bf16 MFMA
     bool tokens;                // a weight gradient from the operands as they lie
     int nb;                     // tile width 64 nb along the operand without 256-row tiles
     int nk, stages, splits;     // K stages in all; those of a part and the parts of a tile behind the first `full`
     uint32_t tm, tn, full;
-    int64_t kd, ks, ld_t;       // row lengths of the copies: elements, scales; stride along the tokens
-    bool pack_q[2], pack_s[2];  // copies needed of A (0) and B (1)
+    int64_t kd, ks, ld_t;       // tokens in whole stages; row length of copied scales; stride along the tokens
+    bool pack_s[2];             // the scales of A (0) and B (1) are copied
     uint64_t off_q[2], off_s[2], off_part, bytes;
 };
 hipError_t mo_launch_f8_pack(const MoF8Operand& a, const MoF8Plan& p, int i, int64_t dim, uint8_t* ws, hipStream_t s);
-hipError_t mo_launch_f8_matmul(const MoF8Operand& A, const MoF8Operand& B, const MoF8Plan& p, void* Y, int64_t ldy,
-                               uint8_t* ws, hipStream_t s);
+// Few rows of A: no plan, no workspace.
+hipError_t mo_launch_f8_few(const MoF8Operand& A, const MoF8Operand& B, int64_t dim, void* Y, int64_t ldy, int32_t dtype,
+                            hipStream_t s);
+hipError_t mo_launch_f8_matmul(const MoF8Operand& A, const MoF8Operand& B, const MoF8Plan& p, int64_t dim, void* Y,
+                               int64_t ldy, int32_t dtype, uint8_t* ws, hipStream_t s);
 hipError_t mo_launch_f8_transpose(const MoF8Wgrad& a, const MoF8Plan& p, bool x, uint8_t* ws, hipStream_t s);
 hipError_t mo_launch_f8_wgrad(const MoF8Wgrad& a, const MoF8Plan& p, uint8_t* ws, hipStream_t s);
 

@@ -24,18 +24,18 @@ def _blocks(n: int) -> int:
 
 def _operand(q, scales, what: str, square=None) -> MoFp8Matrix:
     """square: whether the scales are of blocks of 128 x 128; None: by their rows."""
-    ldq = _matrix(q, what, dtype=FP8)
+    ldq = _matrix(q, what, None, None, FP8)
     rows, cols = q.shape
+    shape = scales.shape
     if square is None:
-        square = scales.dim() == 2 and scales.shape[0] != rows
-    srows, scols = _blocks(rows) if square else rows, _blocks(cols)
+        square = len(shape) == 2 and shape[0] != rows
+    srows, scols = -(-rows // FP8_BLOCK) if square else rows, -(-cols // FP8_BLOCK)
     lds, inc = 1, 0
-    if scales.dim() == 2 and scales.shape[1] > 1 and scales.stride(1) != 1:   # by columns: others' transpose
+    if len(shape) == 2 and shape[1] > 1 and scales.stride(1) != 1:   # by columns: others' transpose
         inc = _matrix(scales.t(), f"{what}'s scales, transposed,", scols, srows, FP8_SCALE)
     else:
-        lds = _matrix(scales, f"{what}'s scales", srows, scols, FP8_SCALE)
-    return MoFp8Matrix(q=_ptr(q), scales=_ptr(scales), rows=rows, ld_q=ldq, ld_scales=lds, inc_scales=inc,
-                       block_rows=FP8_BLOCK if square else 1)
+        lds = _matrix(scales, what + "'s scales", srows, scols, FP8_SCALE)
+    return MoFp8Matrix(_ptr(q), _ptr(scales), rows, ldq, lds, inc, FP8_BLOCK if square else 1)
 
 
 def fp8_quantize(X, *, q=None, scales=None, stream=None) -> Tuple:
@@ -110,7 +110,7 @@ def _matmul_args(A, a_scales, B, b_scales):
 
 def _matmul_bytes(a, b, dim, code) -> int:
     out = ctypes.c_size_t(0)
-    _check(load_library().fp8_matmul_workspace_bytes(ctypes.byref(a), ctypes.byref(b), dim, code, ctypes.byref(out)),
+    _check(load_library().fp8_matmul_workspace_bytes(a, b, dim, code, out),
            "fp8_matmul_workspace_bytes")
     return int(out.value)
 
@@ -133,20 +133,18 @@ def fp8_matmul(A, a_scales, B, b_scales, *, dtype=torch.bfloat16, out=None, work
     a, b = _matmul_args(A, a_scales, B, b_scales)
     dim = A.shape[1]
     with _On(dev, stream) as on:
-        out, ldy = _out(on, out, "out", A.shape[0], B.shape[0], dtype)
+        out, ldy = _out(on, out, "out", a.rows, b.rows, dtype)
         code = _DTYPE[out.dtype]
         need = _matmul_bytes(a, b, dim, code) if workspace is None else 0
         ws, have, keep = on.workspace(workspace, need)
-        _check(lib.fp8_matmul(ctypes.byref(a), ctypes.byref(b), dim, _ptr(out), ldy, code, ws, have, on.handle),
-               "fp8_matmul")
+        _check(lib.fp8_matmul(a, b, dim, _ptr(out), ldy, code, ws, have, on.handle), "fp8_matmul")
         del keep
     return out
 
 
 def _wgrad_bytes(dY, ldy, ycode, x, dim, rows) -> int:
     out = ctypes.c_size_t(0)
-    _check(load_library().fp8_weight_grad_workspace_bytes(_ptr(dY), ldy, ycode, ctypes.byref(x), dim, rows,
-                                                          ctypes.byref(out)), "fp8_weight_grad_workspace_bytes")
+    _check(load_library().fp8_weight_grad_workspace_bytes(_ptr(dY), ldy, ycode, x, dim, rows, out), "fp8_weight_grad_workspace_bytes")
     return int(out.value)
 
 
@@ -173,7 +171,7 @@ def fp8_weight_grad(dY, q, scales, G, *, accumulate: bool = False, workspace=Non
     with _On(dev, stream) as on:
         need = _wgrad_bytes(dY, ldy, ycode, x, dim, rows) if workspace is None else 0
         ws, have, keep = on.workspace(workspace, need)
-        _check(lib.fp8_weight_grad(_ptr(dY), ldy, ycode, ctypes.byref(x), dim, _ptr(G), ldg, gcode, rows,
+        _check(lib.fp8_weight_grad(_ptr(dY), ldy, ycode, x, dim, _ptr(G), ldg, gcode, rows,
                                    1 if accumulate else 0, ws, have, on.handle), "fp8_weight_grad")
         del keep
     return G

@@ -29,6 +29,7 @@ FP8_BLOCK = 128   # MO_FP8_BLOCK
 FP8, FP8_SCALE = torch.float8_e4m3fn, torch.float8_e8m0fnu
 
 _DTYPE = {torch.float32: B.MO_F32, torch.bfloat16: B.MO_BF16}
+_empty = torch.empty
 
 
 # ---------------------------------------------------------------------------
@@ -59,27 +60,38 @@ def _code(t, what: str) -> int:
 
 def _matrix(t, what: str, rows: Optional[int] = None, cols: Optional[int] = None, dtype=None) -> int:
     """Checks a row-major matrix; its row stride in elements."""
+    shape = t.shape
+    if len(shape) == 2:
+        r, c = shape
+        if (rows is None or r == rows) and (cols is None or c == cols) and (dtype is None or t.dtype is dtype):
+            if not r or not c:
+                return 0
+            s0, s1 = t.stride()
+            if s1 == 1 or c == 1:
+                if r == 1:
+                    return 0
+                if s0 >= c:
+                    return s0
+    return _not_a_matrix(t, what, rows, cols, dtype)
+
+
+def _not_a_matrix(t, what, rows, cols, dtype) -> int:
     if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
         want = f"({'rows' if rows is None else rows}, {'cols' if cols is None else cols})"
         raise ValueError(f"{what} must be 2D {want}, not {tuple(t.shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
-    if t.numel() == 0:
-        return 0
     if t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError(f"{what} must be row-major with unit column stride")
-    if t.shape[0] == 1:
-        return 0
     # a row stride of 0 (an expanded row) or less than a row would alias rows
-    if t.stride(0) < t.shape[1]:
-        raise ValueError(f"{what} has overlapping rows (stride {t.stride(0)})")
-    return int(t.stride(0))
+    raise ValueError(f"{what} has overlapping rows (stride {t.stride(0)})")
 
 
 def _vector(t, what: str, n: int, dtype=torch.float32) -> None:
-    if t.dim() != 1 or t.shape[0] != n:
-        raise ValueError(f"{what} must be a vector of {n}, not {tuple(t.shape)}")
-    if t.dtype != dtype:
+    shape = t.shape
+    if len(shape) != 1 or shape[0] != n:
+        raise ValueError(f"{what} must be a vector of {n}, not {tuple(shape)}")
+    if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
     if n > 1 and t.stride(0) != 1:
         raise ValueError(f"{what} must be contiguous")
@@ -134,12 +146,12 @@ class _On:
     def matrix(self, t, what, rows, cols, dtype):
         """(t, row stride): the caller's matrix, checked, or a new one."""
         if t is None:
-            return torch.empty((rows, cols), dtype=dtype, device=self.dev), 0
+            return _empty((rows, cols), dtype=dtype, device=self.dev), 0
         return t, _matrix(t, what, rows, cols, dtype)
 
     def vector(self, t, what, n):
         if t is None:
-            return torch.empty(n, dtype=torch.float32, device=self.dev)
+            return _empty(n, dtype=torch.float32, device=self.dev)
         _vector(t, what, n)
         return t
 

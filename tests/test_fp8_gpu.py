@@ -211,6 +211,8 @@ def test_matmul_many_tiles(m, n, k):
 
 @pytest.mark.parametrize("k", [512, 500])
 def test_matmul_strides(k):
+    """Odd strides and addresses.  Where they change how the operands are read, a bf16 result comes from other
+    MFMAs, so it is held to the formula; an fp32 result comes from the same ones either way."""
     m, n = 70, 300
     A, sa = mo.fp8_quantize(matrix(m, k, F32, 10))
     B, sb, _, _ = mo.fp8_quantize_weight(matrix(n, k, F32, 11))
@@ -224,7 +226,8 @@ def test_matmul_strides(k):
             return v.view(t.dtype)
         big = torch.full((m + 1, n + 7), 7.0, device="cuda", dtype=dtype)
         got = mo.fp8_matmul(odd(A, 5, 3), odd(sa, 3, 1), odd(B, 9, 1), odd(sb, 6, 2), out=big[:m, 3:3 + n])
-        assert torch.equal(got, want)
+        R.check(got, *F.matmul(A, sa, B, sb, 1, 128, dtype), "odd strides")
+        assert dtype == BF16 or torch.equal(got, want)
         big[:m, 3:3 + n] = 7
         assert bool((big == 7).all())
 

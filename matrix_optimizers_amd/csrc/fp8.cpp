@@ -58,12 +58,18 @@ void operand_ranges(const MoF8Operand& o, int64_t cols, Ranges* r) {
     r->add(o.inc == 1 ? matrix_range(o.s, n, b, o.ld_s, 1, 0) : matrix_range(o.s, b, n, o.inc, 1, 0));
 }
 
-// Estimated us of a product in `tiles` tiles of 256 x 64 nb with `stages` stages of 128 bytes of
-// K on 256 CUs.  The rounds that fill them take a tile's K whole; the tiles left over are split into
-// the parts (multiples of `unit` stages) that take the least.  The parts' fp32 sums are
-// written, read and added by a second launch.
-double product_us(int64_t tiles, int64_t stages, int nb, int unit, int64_t* full, int64_t* splits) {
-    const double stage = nb == 4 ? 1.43 : nb == 2 ? 0.8 : 0.6;
+// us of a stage (128 bytes of K) of a tile of 256 x 256, 128 and 64, one tile per CU: in 8 bits, from 8 bits
+// converted, in bf16, and a weight gradient's from the operands as they lie.
+struct StageTimes { double t[3]; };
+constexpr StageTimes kStage8 = {{1.5, 0.9, 0.75}}, kStageValues = {{1.5, 1.0, 0.8}}, kStageBf16 = {{1.35, 0.85, 0.72}},
+                     kStageTokens = {{1.72, 1.15, 0.9}};
+
+// Estimated us of a product in `tiles` tiles with `stages` stages of `stage` us on 256 CUs.  The rounds that
+// fill them take a tile's K whole; the tiles left over are split into the parts (multiples of `unit` stages)
+// that take the least.  The parts' fp32 sums are written, read and added by a second launch.  Of 15
+// products between 64 x 4096 x 4096 and 4096 x 4096 x 4096 with each kind of operands, the choice is
+// within 7 % of the best of all widths and up to 16 parts.
+double product_us(int64_t tiles, int64_t stages, double stage, int nb, int unit, int64_t* full, int64_t* splits) {
     const int64_t rem = tiles % 256;
     const double whole = double(tiles / 256 * stages) * stage;
     double least = whole + (rem ? double(stages) * stage : 0);
@@ -81,13 +87,16 @@ double product_us(int64_t tiles, int64_t stages, int nb, int unit, int64_t* full
 }
 
 // Tiles and parts of a product with `p` rows along 256 and `q` along 64 nb.
-void plan_tiles(MoF8Plan* plan, int64_t p, int64_t q, int64_t stages, int unit, Carve* take) {
+void plan_tiles(MoF8Plan* plan, int64_t p, int64_t q, int64_t stages, const StageTimes& times, double planes, int unit,
+                Carve* take) {
     double least = 0;
     int64_t splits = 1, full = 0;
-    for (int nb = 4; nb >= 1; nb /= 2) {
+    for (int i = 0; i < 3; ++i) {
+        const int nb = 4 >> i;
         int64_t f, k;
-        const double t = product_us((p + 255) / 256 * ((q + 64 * nb - 1) / (64 * nb)), stages, nb, unit, &f, &k);
-        if (nb == 4 || t < least) {
+        const double t = product_us((p + 255) / 256 * ((q + 64 * nb - 1) / (64 * nb)), stages, times.t[i] * planes, nb, unit,
+                                    &f, &k);
+        if (i == 0 || t < least) {
             least = t;
             plan->nb = nb;
             full = f;
@@ -128,14 +137,14 @@ MoF8Plan matmul_plan(const MoF8Operand& A, const MoF8Operand& B, int64_t dim, in
     const MoF8Operand* o[2] = {&A, &B};
     p.bf16 = dtype == MO_F32 || !q_in_place(A, dim) || !q_in_place(B, dim);
     if (p.bf16) {
-        plan_tiles(&p, B.rows, A.rows, (dim + 63) / 64, 1, &take);
+        plan_tiles(&p, B.rows, A.rows, (dim + 63) / 64, kStageValues, 1, 1, &take);
     } else {
         p.ks = (blocks_of(dim) + 3) / 4 * 4;
         for (int i = 0; i < 2; ++i) {
             p.pack_s[i] = !(i == 1 && B.shift) && !s_in_place(*o[i], dim);   // (B's in blocks are read singly)
             if (p.pack_s[i]) p.off_s[i] = take(uint64_t(scale_rows(*o[i])) * p.ks);
         }
-        plan_tiles(&p, B.rows, A.rows, dim / kBlock, 4, &take);
+        plan_tiles(&p, B.rows, A.rows, dim / kBlock, kStage8, 1, 4, &take);
     }
     p.bytes = take.at;
     return p;
@@ -163,7 +172,7 @@ MoF8Plan wgrad_plan(const MoF8Wgrad& a) {
         p.off_q[0] = take(uint64_t(planes) * a.rows * p.ld_t * 2);
         p.off_q[1] = take(uint64_t(a.dim) * p.ld_t * 2);
     }
-    plan_tiles(&p, a.dim, a.rows, p.kd / 64, 1, &take);
+    plan_tiles(&p, a.dim, a.rows, p.kd / 64, p.tokens ? kStageTokens : kStageBf16, a.dy_dtype == MO_BF16 ? 1 : 3, 1, &take);
     p.bytes = take.at;
     return p;
 }
@@ -360,10 +369,7 @@ mo_status fp8_weight_grad(const void* dY, int64_t ld_dy, int32_t dy_dtype, const
     uint8_t* ws;
     if (!take_workspace(workspace, workspace_bytes, p.bytes, &r, &ws)) return MO_ERR_WORKSPACE_TOO_SMALL;
     if (r.conflict()) return MO_ERR_ALIAS;
-    if (!p.tokens) {
-        MO_RUN(MO_PHASE_F8_PREP, mo_launch_f8_transpose(a, p, true, ws, s));
-        MO_RUN(MO_PHASE_F8_PREP, mo_launch_f8_transpose(a, p, false, ws, s));
-    }
+    if (!p.tokens) MO_RUN(MO_PHASE_F8_PREP, mo_launch_f8_transpose(a, p, ws, s));
     MO_RUN(MO_PHASE_F8_WGRAD, mo_launch_f8_wgrad(a, p, ws, s));
     return MO_OK;
 }

@@ -293,57 +293,69 @@ template <> struct Source<uint8_t> {
     }
 };
 
-// dst[plane][c][ldt] <- src[r][c] in 64 x 64 tiles, zeros for rows from `rows` up to 64 tr;
-// the tiles in blocks of 8 x 8 (whole 1 KB pieces of rows and columns by workgroups
-// that run together).
+// dst[plane][c][ldt] <- src[r][c], zeros for rows from `rows` up to 64 tr.
+template <typename T> struct Transpose {
+    Source<T> src;
+    int64_t cols;
+    bf16_t* dst;
+    int64_t plane;
+    uint32_t tc, units;   // tiles of 64 columns; tiles in whole blocks of 8 x 8
+};
+// One 64 x 64 tile of it; the tiles in blocks of 8 x 8 (whole 1 KB pieces of rows and columns by
+// workgroups that run together).
 template <typename T, int PL>
-__global__ __launch_bounds__(256) void f8_transpose_kernel(Source<T> src, int64_t rows, int64_t cols, bf16_t* dst,
-                                                           int64_t ldt, int64_t plane, uint32_t tr, uint32_t tc) {
-    __shared__ float tile[XT][XT + 1];
-    const uint32_t blocks_r = (tr + 7) / 8, units = blocks_r * ((tc + 7) / 8) * 64;
-    for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const uint32_t blk = u >> 6, ti = blk % blocks_r * 8 + (u & 7), tj = blk / blocks_r * 8 + (u >> 3 & 7);
-        if (ti >= tr || tj >= tc) continue;
-        const int64_t r0 = int64_t(ti) * XT, c0 = int64_t(tj) * XT;
-        f32x8 v[2];
+MO_DEV void transpose_tile(float (&tile)[XT][XT + 1], const Transpose<T>& t, uint32_t u, int64_t rows, int64_t ldt, uint32_t tr) {
+    const uint32_t blocks_r = (tr + 7) / 8;
+    const uint32_t blk = u >> 6, ti = blk % blocks_r * 8 + (u & 7), tj = blk / blocks_r * 8 + (u >> 3 & 7);
+    if (ti >= tr || tj >= t.tc) return;
+    const int64_t r0 = int64_t(ti) * XT, c0 = int64_t(tj) * XT;
+    f32x8 v[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int w = threadIdx.x + 256 * i, r = w >> 3, c = (w & 7) * 8;
-            const int64_t left = cols - c0 - c;
-            const bool in = r0 + r < rows;
-            v[i] = src.at(in ? r0 + r : 0, left > 0 ? c0 + c : 0, in ? int(left < 8 ? left : 8) : 0);
-        }
-        __syncthreads();   // the tile before has been read
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int w = threadIdx.x + 256 * i, r = w >> 3, c = (w & 7) * 8;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) tile[r][c + e] = v[i].v[e];
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int w = threadIdx.x + 256 * i, c = w >> 3, r = (w & 7) * 8;
-            if (c0 + c >= cols) continue;
-            bf16x8 p[3];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float x = tile[r + e][c];
-                if constexpr (PL == 1) {
-                    p[0][e] = (bf16_t)x;
-                } else {
-                    bf16_t h, m, l;
-                    split_f32(x, h, m, l);
-                    p[0][e] = h;
-                    p[1][e] = m;
-                    p[2][e] = l;
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < PL; ++k)
-                *reinterpret_cast<u32x4*>(dst + k * plane + (c0 + c) * ldt + r0 + r) = __builtin_bit_cast(u32x4, p[k]);
-        }
+    for (int i = 0; i < 2; ++i) {
+        const int w = threadIdx.x + 256 * i, r = w >> 3, c = (w & 7) * 8;
+        const int64_t left = t.cols - c0 - c;
+        const bool in = r0 + r < rows;
+        v[i] = t.src.at(in ? r0 + r : 0, left > 0 ? c0 + c : 0, in ? int(left < 8 ? left : 8) : 0);
     }
+    __syncthreads();   // the tile before has been read
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int w = threadIdx.x + 256 * i, r = w >> 3, c = (w & 7) * 8;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) tile[r][c + e] = v[i].v[e];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int w = threadIdx.x + 256 * i, c = w >> 3, r = (w & 7) * 8;
+        if (c0 + c >= t.cols) continue;
+        bf16x8 p[3];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float x = tile[r + e][c];
+            if constexpr (PL == 1) {
+                p[0][e] = (bf16_t)x;
+            } else {
+                bf16_t h, m, l;
+                split_f32(x, h, m, l);
+                p[0][e] = h;
+                p[1][e] = m;
+                p[2][e] = l;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < PL; ++k)
+            *reinterpret_cast<u32x4*>(t.dst + k * t.plane + (c0 + c) * ldt + r0 + r) = __builtin_bit_cast(u32x4, p[k]);
+    }
+}
+// Both operands of a weight gradient in one launch.
+template <typename T, int PL>
+__global__ __launch_bounds__(256) void f8_transpose_kernel(Transpose<uint8_t> x, Transpose<T> y, int64_t rows, int64_t ldt,
+                                                           uint32_t tr) {
+    __shared__ float tile[XT][XT + 1];
+    for (uint32_t u = blockIdx.x; u < x.units + y.units; u += gridDim.x)
+        if (u < x.units) transpose_tile<uint8_t, 1>(tile, x, u, rows, ldt, tr);
+        else transpose_tile<T, PL>(tile, y, u - x.units, rows, ldt, tr);
 }
 
 unsigned grid_for(int64_t items) {
@@ -417,25 +429,22 @@ hipError_t mo_launch_f8_matmul(const MoF8Operand& A, const MoF8Operand& B, const
     return B.shift ? product_nb<SQUARE8>(P, Q, p, o, ws, s) : product_nb<ROWS8>(P, Q, p, o, ws, s);
 }
 
-hipError_t mo_launch_f8_transpose(const MoF8Wgrad& a, const MoF8Plan& p, bool x, uint8_t* ws, hipStream_t s) {
-    const int64_t cols = x ? a.dim : a.rows;
-    const uint32_t tr = uint32_t(p.kd / XT), tc = uint32_t((cols + XT - 1) / XT);
-    const uint64_t units = uint64_t((tr + 7) / 8) * ((tc + 7) / 8) * 64;
-    const dim3 grid(unsigned(units < 8192 ? units : 8192));
-    bf16_t* dst = reinterpret_cast<bf16_t*>(ws + p.off_q[x ? 1 : 0]);
-    const int64_t plane = cols * p.ld_t;
-    if (x)
-        hipLaunchKernelGGL((f8_transpose_kernel<uint8_t, 1>), grid, dim3(256), 0, s,
-                           Source<uint8_t>{a.X.q, a.X.ld, a.X.s, a.X.ld_s, a.X.inc}, a.X.rows, cols, dst, p.ld_t, plane, tr, tc);
-    else if (a.dy_dtype == MO_BF16)
-        hipLaunchKernelGGL((f8_transpose_kernel<bf16_t, 1>), grid, dim3(256), 0, s,
-                           Source<bf16_t>{static_cast<const bf16_t*>(a.dY), a.lddy}, a.X.rows, cols, dst, p.ld_t, plane,
-                           tr, tc);
-    else
-        hipLaunchKernelGGL((f8_transpose_kernel<float, 3>), grid, dim3(256), 0, s,
-                           Source<float>{static_cast<const float*>(a.dY), a.lddy}, a.X.rows, cols, dst, p.ld_t, plane, tr,
-                           tc);
+template <typename T, int PL>
+static hipError_t transpose(const MoF8Wgrad& a, const MoF8Plan& p, uint8_t* ws, hipStream_t s) {
+    const uint32_t tr = uint32_t(p.kd / XT), br = (tr + 7) / 8;
+    auto tiles = [](int64_t cols) { return uint32_t((cols + XT - 1) / XT); };
+    const uint32_t tx = tiles(a.dim), ty = tiles(a.rows);
+    const Transpose<uint8_t> x = {{a.X.q, a.X.ld, a.X.s, a.X.ld_s, a.X.inc}, a.dim, reinterpret_cast<bf16_t*>(ws + p.off_q[1]),
+                                  0, tx, br * ((tx + 7) / 8) * 64};
+    const Transpose<T> y = {{static_cast<const T*>(a.dY), a.lddy}, a.rows, reinterpret_cast<bf16_t*>(ws + p.off_q[0]),
+                            a.rows * p.ld_t, ty, br * ((ty + 7) / 8) * 64};
+    const uint32_t units = x.units + y.units;
+    hipLaunchKernelGGL((f8_transpose_kernel<T, PL>), dim3(units < 8192 ? units : 8192), dim3(256), 0, s, x, y, a.X.rows,
+                       p.ld_t, tr);
     return hipGetLastError();
+}
+hipError_t mo_launch_f8_transpose(const MoF8Wgrad& a, const MoF8Plan& p, uint8_t* ws, hipStream_t s) {
+    return a.dy_dtype == MO_BF16 ? transpose<bf16_t, 1>(a, p, ws, s) : transpose<float, 3>(a, p, ws, s);
 }
 
 template <int KIND>

@@ -146,7 +146,7 @@ class _On:
     def matrix(self, t, what, rows, cols, dtype):
         """(t, row stride): the caller's matrix, checked, or a new one."""
         if t is None:
-            return _empty((rows, cols), dtype=dtype, device=self.dev), 0
+            return _empty(rows, cols, dtype=dtype, device=self.dev), 0
         return t, _matrix(t, what, rows, cols, dtype)
 
     def vector(self, t, what, n):

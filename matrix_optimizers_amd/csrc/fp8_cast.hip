@@ -4,58 +4,47 @@
 #include "fp8.h"
 #include "operators.h"
 
+#include <algorithm>
+
 namespace {
 
-// 16 threads per block of 128, 8 elements each.  A workgroup takes CG blocks side by
-// side of 16 / CG rows, U times over: the loads of U rows are under way together.
-constexpr int U = 4;
+// 16 threads per block of 128, 8 elements each.  A workgroup takes CG blocks side by side of 16 / CG
+// rows; one after the other only where the grid ends.  16384 x 14336 bf16 to 8 bits: 124 us (5.7 TB/s); in
+// 8192 workgroups that walk over rows, four rows' loads under way, 136.
 
 template <typename T>
 __global__ __launch_bounds__(256) void f8_quantize_kernel(const T* X, int64_t ldx, int64_t rows, int cols, uint8_t* Q,
                                                           int64_t ldq, uint8_t* S, int64_t lds, int cg) {
     const int g = threadIdx.x >> 4, t = threadIdx.x & 15, rg = 16 / cg;
     const int blk = int(blockIdx.x) * cg + g % cg, c = blk * F8_BLOCK + t * 8, n = cols - c;
-    const int64_t step = int64_t(gridDim.y) * rg;
     if (blk * F8_BLOCK >= cols) return;
-    for (int64_t row = int64_t(blockIdx.y) * rg + g / cg; row < rows; row += step * U) {
-        raw8<T> x[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t r = row + u * step;
-            x[u] = ld8n(X + (r < rows ? r : row) * ldx + c, n);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t r = row + u * step;
-            if (r >= rows) break;
-            const f32x8 v = widen(x[u]);
-            const uint32_t b = scale_byte(max16(amax8(v)));
-            stq8(Q + r * ldq + c, to_e4m3(v, scale_inverse(b)), n);
-            if (t == 0) S[r * lds + blk] = uint8_t(b);
-        }
+    for (int64_t r = int64_t(blockIdx.y) * rg + g / cg; r < rows; r += int64_t(gridDim.y) * rg) {
+        const f32x8 v = widen(ld8n(X + r * ldx + c, n));
+        const uint32_t b = scale_byte(max16(amax8(v)));
+        stq8(Q + r * ldq + c, to_e4m3(v, scale_inverse(b)), n);
+        if (t == 0) S[r * lds + blk] = uint8_t(b);
     }
 }
 
+// Stored past the caches: 16381 x 4096 to bf16 31 us instead of 39; with the reading of the result behind it
+// 73.5 instead of 72.3, at 16384 x 14336 233 instead of 246.
 template <typename T>
 __global__ __launch_bounds__(256) void f8_dequantize_kernel(const uint8_t* Q, int64_t ldq, const uint8_t* S, int64_t lds,
                                                             int64_t rows, int cols, T* X, int64_t ldx, int cg) {
     const int g = threadIdx.x >> 4, t = threadIdx.x & 15, rg = 16 / cg;
     const int blk = int(blockIdx.x) * cg + g % cg, c = blk * F8_BLOCK + t * 8, n = cols - c;
-    const int64_t step = int64_t(gridDim.y) * rg;
     if (c >= cols) return;
-    for (int64_t row = int64_t(blockIdx.y) * rg + g / cg; row < rows; row += step * U) {
-        u32x2 q[U];
-        uint32_t s[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t r = row + u * step < rows ? row + u * step : row;
-            q[u] = ldq8(Q + r * ldq + c, n);
-            s[u] = S[r * lds + blk];
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t r = row + u * step;
-            if (r < rows) st8n(X + r * ldx + c, from_e4m3(q[u], scale_value(s[u])), n);
+    for (int64_t r = int64_t(blockIdx.y) * rg + g / cg; r < rows; r += int64_t(gridDim.y) * rg) {
+        const f32x8 v = from_e4m3(ldq8(Q + r * ldq + c, n), scale_value(S[r * lds + blk]));
+        T* x = X + r * ldx + c;
+        if (n < 8) {
+            st8n(x, v, n);
+        } else if constexpr (sizeof(T) == 2) {
+            __builtin_nontemporal_store(narrow(v, T()).q, reinterpret_cast<u32x4_e2*>(x));
+        } else {
+            const raw8<T> w = narrow(v, T());
+            __builtin_nontemporal_store(w.lo, reinterpret_cast<f32x4_e4*>(x));
+            __builtin_nontemporal_store(w.hi, reinterpret_cast<f32x4_e4*>(x + 4));
         }
     }
 }
@@ -139,9 +128,9 @@ struct CastGrid {
         const int64_t kb = (cols + F8_BLOCK - 1) / F8_BLOCK;
         cg = 1;
         while (cg < 16 && cg < kb) cg *= 2;
-        const int64_t gx = (kb + cg - 1) / cg, rg = 16 / cg, want = (rows + rg * U - 1) / (rg * U);
-        const int64_t cap = gx >= 8192 ? 1 : 8192 / gx;
-        grid = dim3(unsigned(gx), unsigned(want < cap ? want : cap));
+        const int64_t gx = (kb + cg - 1) / cg, rg = 16 / cg, want = (rows + rg - 1) / rg;
+        const int64_t most = int64_t(1) << 22, cap = gx >= most ? 1 : most / gx;
+        grid = dim3(unsigned(gx), unsigned(std::min({want, cap, int64_t(65535)})));
     }
 };
 

@@ -153,20 +153,29 @@ __global__ __launch_bounds__(W > 64 ? TEAM_MAX_THREADS : 256) void rms_bwd_kerne
         if (a.weight) w[i] = widen(row8<FULL>(a.weight, (t + team * i) * 8, cols));
     }
     const float n_cols = float(cols);
-    for (int64_t base = int64_t(blockIdx.x) * teams; base < a.rows; base += step) {
-        const int64_t row = base + sub;
-        const bool live = row < a.rows;
-        const int64_t at = live ? row : a.rows - 1;
-        const float r = a.rstd[at];
-        raw8<T> h[R], dy[R], dh[R];
+    raw8<T> nh[R], ny[R], nd[R];
+    float nr;
+    auto request = [&](int64_t row) __attribute__((always_inline)) {
+        row = row < a.rows ? row : a.rows - 1;
+        nr = a.rstd[row];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            h[i] = row8<FULL>(H + at * a.ldh, (t + team * i) * 8, cols);
-            dy[i] = row8<FULL>(dY + at * a.lddy, (t + team * i) * 8, cols);
+            nh[i] = row8<FULL>(H + row * a.ldh, (t + team * i) * 8, cols);
+            ny[i] = row8<FULL>(dY + row * a.lddy, (t + team * i) * 8, cols);
         }
         if (dX && dH)
 #pragma unroll
-            for (int i = 0; i < R; ++i) dh[i] = row8<FULL>(dH + at * a.lddh, (t + team * i) * 8, cols);
+            for (int i = 0; i < R; ++i) nd[i] = row8<FULL>(dH + row * a.lddh, (t + team * i) * 8, cols);
+    };
+    request(int64_t(blockIdx.x) * teams + sub);
+    for (int64_t base = int64_t(blockIdx.x) * teams; base < a.rows; base += step) {
+        const int64_t row = base + sub;
+        const bool live = row < a.rows;
+        const float r = nr;
+        raw8<T> h[R], dy[R], dh[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) { h[i] = nh[i]; dy[i] = ny[i]; dh[i] = nd[i]; }
+        if (base + step < a.rows) request(row + step);
         float s[1] = {0.f};
         if (live) {
 #pragma unroll
@@ -289,19 +298,31 @@ constexpr int MAX_COLS = 2 * 8 * TEAM_MAX_THREADS;
 
 // Rows of at most 512 columns share a workgroup (16 to 64 threads each: a block of 128 is
 // 16 threads); longer ones take a workgroup of their own, with one chunk per thread up to
-// `one` chunks and two above.
-Shape shape_of(int64_t cols, int one) {
+// 4096 columns and two above.
+Shape shape_of(int64_t cols) {
     const int chunks = int((cols + 7) / 8);
     if (chunks <= 64) {
         int W = 16;
         while (W < chunks) W *= 2;
         return {W, 1, 256};
     }
-    const int R = chunks <= one ? 1 : 2;
+    const int R = chunks <= 512 ? 1 : 2;
     return {TEAM_MAX_THREADS, R, ((chunks + R - 1) / R + 63) / 64 * 64};
 }
-Shape fwd_shape(int64_t cols) { return shape_of(cols, 64); }
-Shape bwd_shape(int64_t cols) { return shape_of(cols, 512); }
+
+// Forward, up to 8192 columns each row has a workgroup of its own (bf16 to 8 bits with a residual,
+// 16384 x 8192 168 us, 5.6 TB/s; with as many workgroups as fit, walking over rows, 178; 16384 x 4096
+// 83 and 92), wider ones walk (9362 x 14336 184 us, 208 with one row each).
+unsigned fwd_wgs(int64_t rows, const Shape& sh) {
+    return wgs_for(rows, sh, sh.W <= 64 ? 16 : sh.threads <= 512 ? 1 << 20 : 2048 / sh.threads);
+}
+// Backward, each workgroup leaves a partial row of 4 bytes per column: as few per CU as keep the loads
+// going.  us at 16384 rows of 1024, 2048, 4096 and 8192 columns: 41.6, 57.8, 105 and 198.5 (4.6 to 5.4 TB/s), with
+// half as many workgroups per CU 43 (three), 64.7, 117, -, with twice as many 69, 73, 120, 210.
+int bwd_per_cu(const Shape& sh) {
+    if (sh.W <= 64) return 2;
+    return sh.threads <= 128 ? 4 : sh.threads <= 256 ? 3 : sh.threads <= 512 && sh.R == 1 ? 2 : 1;
+}
 
 template <typename T, bool FULL, bool RES>
 hipError_t fwd(const MoRmsArgs& a, hipStream_t s) {
@@ -310,12 +331,13 @@ hipError_t fwd(const MoRmsArgs& a, hipStream_t s) {
                            0, s, a);
         return hipGetLastError();
     }
-    const Shape sh = fwd_shape(a.cols);
-    const dim3 grid(wgs_for(a.rows, sh, sh.W > 64 ? 2048 / sh.threads : 16)), block(sh.threads);
+    const Shape sh = shape_of(a.cols);
+    const dim3 grid(fwd_wgs(a.rows, sh)), block(sh.threads);
 #define MO_RMS_FWD(W, R) hipLaunchKernelGGL((rms_fwd_kernel<T, W, R, FULL, RES>), grid, block, 0, s, a)
     if (sh.W == 16) MO_RMS_FWD(16, 1);
     else if (sh.W == 32) MO_RMS_FWD(32, 1);
     else if (sh.W == 64) MO_RMS_FWD(64, 1);
+    else if (sh.R == 1) MO_RMS_FWD(TEAM_MAX_THREADS, 1);
     else MO_RMS_FWD(TEAM_MAX_THREADS, 2);
 #undef MO_RMS_FWD
     return hipGetLastError();
@@ -333,7 +355,7 @@ hipError_t bwd(const MoRmsArgs& a, float* part, int n_part, hipStream_t s) {
                                dim3(256), 0, s, a, pp);
         return hipGetLastError();
     }
-    const Shape sh = bwd_shape(a.cols);
+    const Shape sh = shape_of(a.cols);
     const dim3 grid{unsigned(n_part)}, block(sh.threads);
 #define MO_RMS_BWD(W, R) hipLaunchKernelGGL((rms_bwd_kernel<T, W, R, FULL>), grid, block, 0, s, a, pp)
     if (sh.W == 16) MO_RMS_BWD(16, 1);
@@ -350,8 +372,8 @@ hipError_t bwd(const MoRmsArgs& a, float* part, int n_part, hipStream_t s) {
 int mo_rms_bwd_parts(int64_t rows, int64_t cols) {
     if (rows == 0) return 0;
     if (cols > MAX_COLS) return int(rows < 64 ? rows : 64);
-    const Shape sh = bwd_shape(cols);
-    return int(wgs_for(rows, sh, sh.W > 64 ? (sh.threads > 512 ? 1 : 2) : 4));
+    const Shape sh = shape_of(cols);
+    return int(wgs_for(rows, sh, bwd_per_cu(sh)));
 }
 
 hipError_t mo_launch_rms_fwd(const MoRmsArgs& a, hipStream_t s) {

@@ -61,7 +61,7 @@ void operand_ranges(const MoF8Operand& o, int64_t cols, Ranges* r) {
 // us of a stage (128 bytes of K) of a tile of 256 x 256, 128 and 64, one tile per CU: in 8 bits, from 8 bits
 // converted, in bf16, and a weight gradient's from the operands as they lie.
 struct StageTimes { double t[3]; };
-constexpr StageTimes kStage8 = {{1.5, 0.9, 0.75}}, kStageValues = {{1.5, 1.0, 0.8}}, kStageBf16 = {{1.35, 0.85, 0.72}},
+constexpr StageTimes kStage8 = {{1.5, 0.85, 0.6}}, kStageValues = {{1.5, 1.0, 0.8}}, kStageBf16 = {{1.35, 0.78, 0.55}},
                      kStageTokens = {{1.72, 1.15, 0.9}};
 
 // Estimated us of a product in `tiles` tiles with `stages` stages of `stage` us on 256 CUs.  The rounds that

@@ -115,8 +115,13 @@ MO_DEV bool item_of(const Tiles& t, uint32_t n, Item* it) {
 }
 
 template <int KIND> constexpr int scale_rows(int NB) { return is8(KIND) ? (KIND == SQUARE8 ? 0 : 256) + 64 * NB : 0; }
-// Two slots of a stage, and four of four stages' scales by rows.
-template <int KIND> constexpr int gemm_lds(int NB) { return head_lds(NB) + 4 * scale_rows<KIND>(NB) * 4; }
+// Narrow tiles multiply a stage sooner than memory answers, and leave room for a third slot in LDS (us of 64
+// stages of 512 x 4096, tiles of 64: bf16 46 with two, 35 with three; 112 stages in 8 bits 87 and 65).  Kinds
+// that go through registers wait for other things: a second set of registers changed nothing.
+constexpr bool direct(int kind) { return kind != TOKENS && kind != VALUES8; }   // straight to LDS
+template <int KIND> constexpr int slots(int NB) { return direct(KIND) && NB < 4 ? 3 : 2; }
+// The slots of a stage, and four of four stages' scales by rows.
+template <int KIND> constexpr int gemm_lds(int NB) { return head_lds(NB) / 2 * slots<KIND>(NB) + 4 * scale_rows<KIND>(NB) * 4; }
 
 // Stores behind which a barrier's loads may be waited for without them.
 template <int NB> constexpr int STORES = Layout<NB>::MB * Layout<NB>::NBW / 2;
@@ -141,6 +146,7 @@ __device__ __forceinline__ void run_tiles(uint8_t* smem, const Operand8& P, cons
     constexpr int WN = L::WN, MB = L::MB, NBW = L::NBW;
     constexpr int TN = 64 * NB, SBYTES = HP_BYTES + TN * HKB, SROWS = scale_rows<KIND>(NB);
     constexpr int LS = 4 + NB;                   // load instructions per stage and wave
+    constexpr int SLOTS = slots<KIND>(NB);
     constexpr int RING = MB < 4 ? MB : 4;        // fragments of P held
     static_assert(MB % RING == 0, "layout");
 
@@ -153,7 +159,7 @@ __device__ __forceinline__ void run_tiles(uint8_t* smem, const Operand8& P, cons
         return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, -1, 0x00027000);
     };
 
-    // ---- the loads' own walk over the items: always two stages ahead of the products ----
+    // ---- the loads' own walk over the items: always as many stages ahead as there are slots ----
     Item li;
     uint32_t ln = 0;
     bool more = item_of(t, 0, &li);
@@ -250,7 +256,7 @@ __device__ __forceinline__ void run_tiles(uint8_t* smem, const Operand8& P, cons
         __builtin_amdgcn_raw_ptr_buffer_load_lds(i < 4 ? rP : rQ, (lds_void_t*)sp, 16, vo[i], koff, 0, 0);
     };
     // Rows 64 (wave + 8 i) + lane of P's (by rows) and Q's scales: one dword, four stages.
-    uint8_t* const sl = smem + 2 * SBYTES;
+    uint8_t* const sl = smem + SLOTS * SBYTES;
     auto issue_scales = [&]() __attribute__((always_inline)) {
         if constexpr (SROWS > 0) {
             if (ls % 4 != 0 || !more) return;
@@ -457,11 +463,11 @@ __device__ __forceinline__ void run_tiles(uint8_t* smem, const Operand8& P, cons
     int stored = 0;   // 1: STORES stores or more are behind the loads that the next barrier waits for
     // Everything that branches is done first: the compiler moves MFMAs down across branches, and the
     // reads of their next operands then go to other registers.
-    auto stage = [&](const Item& it, int s, int slot, int group) __attribute__((always_inline)) {
+    auto stage = [&](const Item& it, int s, int slot, int next, int group) __attribute__((always_inline)) {
         advance();
         issue_scales();
         if constexpr (VAL) {
-            store_values(slot ^ 1);
+            store_values(next);
             load_values();
         }
         if constexpr (KIND == SQUARE8) {
@@ -484,19 +490,20 @@ __device__ __forceinline__ void run_tiles(uint8_t* smem, const Operand8& P, cons
                     if constexpr (TOK)
 #pragma unroll
                         for (int j = 0; j < 2 + NB; ++j)
-                            if (j * (MB - 2) * NBW / (2 + NB) + 1 == a * NBW + 2 * b + i) piece(slot ^ 1, j);
+                            if (j * (MB - 2) * NBW / (2 + NB) + 1 == a * NBW + 2 * b + i) piece(next, j);
                     __builtin_amdgcn_sched_barrier(0);
                 }
         if constexpr (TOK && MB == 2)
 #pragma unroll
-            for (int j = 0; j < 2 + NB; ++j) piece(slot ^ 1, j);
-        if constexpr (!TOK && !VAL)
+            for (int j = 0; j < 2 + NB; ++j) piece(next, j);
+        if constexpr (direct(KIND))
             asm volatile("s_cmp_eq_u32 %0, 0\n"
                      "s_cbranch_scc1 .Lall%=\n"
                      "s_waitcnt vmcnt(%1)\n"
                      "s_branch .Lgo%=\n"
-                     ".Lall%=: s_waitcnt vmcnt(0)\n"
-                     ".Lgo%=:" ::"s"(__builtin_amdgcn_readfirstlane(stored)), "n"(STORES<NB>) : "memory", "scc");
+                     ".Lall%=: s_waitcnt vmcnt(%2)\n"
+                     ".Lgo%=:" ::"s"(__builtin_amdgcn_readfirstlane(stored)), "n"((SLOTS - 2) * LS + STORES<NB>),
+                     "n"((SLOTS - 2) * LS) : "memory", "scc");
         stored = 0;
         __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
         __builtin_amdgcn_s_barrier();
@@ -505,19 +512,19 @@ __device__ __forceinline__ void run_tiles(uint8_t* smem, const Operand8& P, cons
 #pragma unroll
         for (int b = 0; b < NBW; ++b) {
             mfma(MB - 2, b);
-            if (RING > 2 && b < 2) rdp(slot ^ 1, b);
-            if constexpr (!TOK && !VAL)
+            if (RING > 2 && b < 2) rdp(next, b);
+            if constexpr (direct(KIND))
 #pragma unroll
                 for (int l = 0; l < LS; ++l)
                     if (l * NBW / LS == b) issue1(slot, l);
             __builtin_amdgcn_sched_barrier(0);
             mfma(MB - 1, b);
-            rdq(slot ^ 1, b);
+            rdq(next, b);
             __builtin_amdgcn_sched_barrier(0);
         }
         if (RING == 2) {
-            rdp(slot ^ 1, 0);
-            rdp(slot ^ 1, 1);
+            rdp(next, 0);
+            rdp(next, 1);
         }
     };
 
@@ -539,18 +546,15 @@ __device__ __forceinline__ void run_tiles(uint8_t* smem, const Operand8& P, cons
         load_values();
         __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
     } else {
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < SLOTS; ++s) {
             if (s) advance();
             issue_scales();
 #pragma unroll
             for (int l = 0; l < LS; ++l) issue1(s, l);
         }
     }
-    // stage 0 has landed (stage 1's LS loads, and a dword of scales at most, came after it)
-    if constexpr (TOK || VAL) {}
-    else if constexpr (LS == 8) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
-    else if constexpr (LS == 6) asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
-    else asm volatile("s_waitcnt vmcnt(5)" ::: "memory");
+    // stage 0 has landed (the others' LS loads each, and dwords of scales, came after it)
+    if constexpr (direct(KIND)) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((SLOTS - 1) * LS) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 #pragma unroll
@@ -571,8 +575,10 @@ __device__ __forceinline__ void run_tiles(uint8_t* smem, const Operand8& P, cons
             if (have && it.nk <= 64) load_block(next, 0);
         const int stages = it.nk * (KIND == BF16_3 ? 3 : 1);
 #pragma clang loop unroll(disable)
-        for (int s = 0; s < stages; ++s, slot ^= 1) {
-            stage(it, s, slot, group);
+        for (int s = 0; s < stages; ++s) {
+            const int next = SLOTS == 2 ? slot ^ 1 : slot + 1 == SLOTS ? 0 : slot + 1;
+            stage(it, s, slot, next, group);
+            slot = next;
             if (is8(KIND) && s % 4 == 3) ++group;
         }
         if (is8(KIND) && stages % 4) ++group;

@@ -314,7 +314,7 @@ Shape shape_of(int64_t cols) {
 // 16384 x 8192 168 us, 5.6 TB/s; with as many workgroups as fit, walking over rows, 178; 16384 x 4096
 // 83 and 92), wider ones walk (9362 x 14336 184 us, 208 with one row each).
 unsigned fwd_wgs(int64_t rows, const Shape& sh) {
-    return wgs_for(rows, sh, sh.W <= 64 ? 16 : sh.threads <= 512 ? 1 << 20 : 2048 / sh.threads);
+    return wgs_for(rows, sh, sh.W <= 64 ? 16 : sh.threads <= 512 ? 1 << 12 : 2048 / sh.threads);
 }
 // Backward, each workgroup leaves a partial row of 4 bytes per column: as few per CU as keep the loads
 // going.  us at 16384 rows of 1024, 2048, 4096 and 8192 columns: 41.6, 57.8, 105 and 198.5 (4.6 to 5.4 TB/s), with

@@ -538,7 +538,7 @@ mo_status fp8_quantize(const void* X, int64_t ld_x, int32_t dtype, int64_t rows,
                        uint8_t* q, int64_t ld_q, uint8_t* scales, int64_t ld_scales, void* stream);
 
 /* X (rows x cols, dtype) from q and scales.  The values are bf16 numbers as they are, save
- * those below 2^-133 (rounded) and above bf16's largest (infinite).  Errors as
+ * those below 2^-130 (rounded to multiples of 2^-133) and above bf16's largest (infinite).  Errors as
  * fp8_quantize. */
 mo_status fp8_dequantize(const uint8_t* q, int64_t ld_q, const uint8_t* scales, int64_t ld_scales,
                          int64_t rows, int64_t cols, void* X, int64_t ld_x, int32_t dtype,
@@ -572,8 +572,8 @@ mo_status fp8_matmul_workspace_bytes(const mo_fp8_matrix* A, const mo_fp8_matrix
  * dim == 0, Y is zeroed.  A bf16 Y comes from 8-bit MFMA, which sums 128 products at a time
  * to about 2^-17 of the largest of them and these sums in fp32 (1.5e-5 of the result's
  * norm for normal data); an fp32 Y, and a bf16 one of operands whose dim is not a multiple of
- * 128 or whose rows are not 16-byte aligned, from bf16 MFMA on the operands' values, with
- * exact products and fp32 sums, at half the rate.  Errors: MO_ERR_INVALID_ARG (null pointer,
+ * 128 or whose rows are not 16-byte aligned, from bf16 MFMA on the operands' values as
+ * fp8_dequantize makes them, with exact products and fp32 sums, at half the rate.  Errors: MO_ERR_INVALID_ARG (null pointer,
  * negative size, bad stride, block_rows), MO_ERR_UNSUPPORTED (dtype, rows or dim > 2^20, a
  * row stride of 2^23 or more), MO_ERR_WORKSPACE_TOO_SMALL, MO_ERR_ALIAS, MO_ERR_HIP. */
 mo_status fp8_matmul(const mo_fp8_matrix* A, const mo_fp8_matrix* B, int64_t dim, void* Y, int64_t ld_y,
@@ -588,8 +588,8 @@ mo_status fp8_weight_grad_workspace_bytes(const void* dY, int64_t ld_dy, int32_t
 
 /* The weight's gradient of Y = X W^T from an activation kept in 8 bits: G = dY^T X, dY
  * (X->rows tokens x rows, dy_dtype), X (tokens x dim, block_rows 1), G (rows x dim,
- * g_dtype), the G of an owner step.  Products are exact (X's values are bf16 numbers, an fp32 dY
- * is three of them), sums fp32, rounded once; with accumulate nonzero after one more
+ * g_dtype), the G of an owner step.  Products are exact (X's values are fp8_dequantize's bf16 numbers, an fp32
+ * dY is three of them), sums fp32, rounded once; with accumulate nonzero after one more
  * addition, of what G held.  With no tokens G is zeroed, or left as it is.  Errors as
  * fp8_matmul. */
 mo_status fp8_weight_grad(const void* dY, int64_t ld_dy, int32_t dy_dtype, const mo_fp8_matrix* X,

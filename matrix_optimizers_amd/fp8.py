@@ -57,7 +57,8 @@ def fp8_quantize(X, *, q=None, scales=None, stream=None) -> Tuple:
 
 def fp8_dequantize(q, scales, *, dtype=torch.bfloat16, out=None, stream=None):
     """The values of fp8_quantize's q and scales in float32 or bfloat16 (``out``'s dtype where
-    it is given): exact in both, save under 2^-133 and over bfloat16's largest."""
+    it is given): exact in float32; in bfloat16 those under 2^-130 are rounded to multiples
+    of 2^-133, and those over its largest are infinite."""
     lib = load_library()
     dev = _device(q, scales, out)
     ldq = _matrix(q, "q", dtype=FP8)

@@ -277,3 +277,28 @@ def test_a_result_beyond_2_32_elements(gpu):
     mo.fp8_weight_grad(dY, q, s, G)
     want, bound = F.wgrad(dY[:, -last:], q, s, BF)
     R.check(G[-last:], want, bound, "G")
+
+
+@pytest.mark.parametrize("m,n,k", [(5, 300, 512), (70, 300, 640), (70, 300, 600), (300, 256, 1024)])
+def test_scales_at_both_ends(gpu, m, n, k):
+    """The least scales (down to bf16's subnormal numbers) against the largest: products as of any
+    others.  Where values are taken as bf16 numbers, one below 2^-130 is rounded to a multiple of 2^-133
+    (bf16's last step; a value has four bits), so it is off by 2^-134 at most."""
+    A, sa = mo.fp8_quantize(rand(gen(11), (m, k), F32))
+    B, sb = mo.fp8_quantize(rand(gen(12), (n, k), F32))
+    a = F.codes(A)
+    a[(a & 0x7F) < 8] = 0
+    g = gen(13)
+    F.codes(sa).copy_(torch.randint(0, 3, sa.shape, generator=g, device="cuda"))
+    F.codes(sb).copy_(torch.randint(225, 240, sb.shape, generator=g, device="cuda"))
+    off = 2.0 ** -134 * F.value(B, sb).abs().sum(1)
+    for dt in (BF, F32):
+        Y, bound = F.matmul(A, sa, B, sb, 1, 1, dt)
+        bound = bound + off * (1 + R.ut(dt))
+        R.check(mo.fp8_matmul(A, sa, B, sb, dtype=dt), Y, bound, str(dt))
+        R.check(mo.fp8_matmul(B, sb, A, sa, dtype=dt), Y.t(), bound.t(), str(dt))
+    dY = rand(gen(14), (m, 200), BF) * 2.0 ** 110
+    off = 2.0 ** -134 * dY.double().abs().sum(0)[:, None]
+    for y in (dY, dY.float()):
+        G, bound = F.wgrad(y, A, sa, F32)
+        R.check(mo.fp8_weight_grad(y, A, sa, torch.empty((200, k), device="cuda")), G, bound + off, "G")

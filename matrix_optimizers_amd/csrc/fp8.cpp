@@ -86,8 +86,8 @@ double product_us(int64_t tiles, int64_t stages, double stage, int nb, int unit,
     return least;
 }
 
-// Tiles and parts of a product with `p` rows along 256 and `q` along 64 nb.
-void plan_tiles(MoF8Plan* plan, int64_t p, int64_t q, int64_t stages, const StageTimes& times, double planes, int unit,
+// Tiles and parts of a product with `p` rows along 256 and `q` along 64 nb; its estimated us.
+double plan_tiles(MoF8Plan* plan, int64_t p, int64_t q, int64_t stages, const StageTimes& times, double planes, int unit,
                 Carve* take) {
     double least = 0;
     int64_t splits = 1, full = 0;
@@ -111,6 +111,7 @@ void plan_tiles(MoF8Plan* plan, int64_t p, int64_t q, int64_t stages, const Stag
     plan->splits = int((stages + plan->stages - 1) / plan->stages);
     if (uint64_t rem = uint64_t(plan->tm) * plan->tn - full)
         plan->off_part = (*take)(rem * plan->splits * 256 * 64 * plan->nb * 4);
+    return least;
 }
 
 // Whether the rows can be loaded straight to LDS: whole blocks, 16-byte aligned rows.
@@ -122,31 +123,67 @@ bool s_in_place(const MoF8Operand& o, int64_t dim) {
     return o.inc == 1 && blocks_of(dim) % 4 == 0 && ((reinterpret_cast<uintptr_t>(o.s) | uintptr_t(o.ld_s)) & 3) == 0;
 }
 
-// Few rows of A: the product reads B straight into registers, in one launch without a workspace.  us,
-// that and tiles, at 14336 x 4096 with a bf16 result: 16 tokens 15.5 and 19.4, 32 21.1 and 19.7, 64
-// 33.5 and 20.6; at 4096 x 4096: 7.3 and 15.4, 10.0 and 15.6, 15.8 and 15.9; at 1024 x 4096 6.8 and
-// 11.1, 9.5 and 11.2, 15.1 and 11.5.  With an fp32 result, or where the operands are not loaded in place, tiles
-// convert them first: 14336 x 4096 in fp32, 64 tokens, 33.8 and 65 (as a copy made first).
-bool few_rows(const MoF8Operand& A, const MoF8Operand& B, int64_t dim, int32_t dtype) {
-    return A.rows <= (dtype == MO_F32 || !q_in_place(A, dim) || !q_in_place(B, dim) ? 64 : 32);
+// Estimated us of a product in small blocks, 16 rb rows of P (K along both) by 16 tb of Q per workgroup, `slots` of
+// them on the card at a time: `start`, then a workgroup's own time for a share of K (every eighth block, so
+// `turns` of them) or that of all workgroups, whichever is more.  At 4.4 a CU holds one, and rounds are whole.
+struct SmallBlocks {
+    int tb, rb, slots;
+    double start, own0, own, all0, all;
+    double us(int64_t p, int64_t q, double turns) const {
+        const int64_t n = ((p + 16 * rb - 1) / (16 * rb)) * ((q + 16 * tb - 1) / (16 * tb));
+        if (n >= int64_t(1) << 20) return 1e30;
+        const double rounds = slots == 256 ? double((n + 255) / 256) : double(n) / slots;
+        return start + std::max(own0 + own * turns, rounds * (all0 + all * turns));
+    }
+};
+constexpr SmallBlocks kSmall[] = {{1, 1, 512, 3.1, 0, 0.36, 1.07, 0.53},
+                                  {1, 2, 512, 3.1, 0, 0.48, 1.1, 0.95},
+                                  {2, 2, 512, 3.1, 0, 0.69, 1.35, 1.25},
+                                  {4, 4, 256, 1.5, 0, 0, 2.7, 1.85}};
+
+// A product in small blocks, without a workspace and in one launch, where that takes less than in tiles.
+// The estimates come from these and others like them, us in tiles and in the small blocks of the first
+// to last kind above, bf16 results: 16 tokens x 4096 x 4096 13.5, 4.6 5.3 6.3 10.5; 64 x 4096 x 4096 13.9, 9.0 7.5
+// 6.6 10.5; 64 x 14336 x 4096 18.9, 26.8 20.8 17.4 16.1; 18 x 1792 x 12672 22.6, 7.6 9.3 11.8 21.9; 512 x
+// 2048 x 2048 14.6, 20.2 13.3 10.1 7.9; 512 x 4096 x 4096 22.7, 51.9 39.5 28.5 21.1; 2048 x 2048 x 256 7.7,
+// 42.5 26.4 17.2 14.2.  fp32 results take 1.15 of the time in either, and rows that are not 16-byte
+// aligned 1.4 in small blocks (1021 x 2001 x 1000 21.6, 17.7; x 1024 19.1, 12.7).
+bool plan_small(MoF8Plan* plan, const MoF8Operand& A, const MoF8Operand& B, int64_t dim, int32_t dtype, double tiles_us) {
+    const bool aligned = ((reinterpret_cast<uintptr_t>(A.q) | uintptr_t(A.ld) | reinterpret_cast<uintptr_t>(B.q) | uintptr_t(B.ld)) & 15) == 0;
+    const double turns = double(blocks_of(dim)) / 8, slower = (dtype == MO_F32 ? 1.15 : 1.0) * (aligned ? 1.0 : 1.4);
+    const double read = double(A.rows + B.rows) * double(dim) / 5.2e6;
+    double least = tiles_us;
+    plan->tb = 0;
+    for (const SmallBlocks& b : kSmall) {
+        const double t = std::max(b.us(B.rows, A.rows, turns) * slower, read);
+        if (t < least) {
+            least = t;
+            plan->tb = b.tb;
+            plan->rb = b.rb;
+        }
+    }
+    return plan->tb != 0;
 }
 
 MoF8Plan matmul_plan(const MoF8Operand& A, const MoF8Operand& B, int64_t dim, int32_t dtype) {
     MoF8Plan p = {};
     Carve take;
     const MoF8Operand* o[2] = {&A, &B};
+    double us;
     p.bf16 = dtype == MO_F32 || !q_in_place(A, dim) || !q_in_place(B, dim);
     if (p.bf16) {
-        plan_tiles(&p, B.rows, A.rows, (dim + 63) / 64, kStageValues, 1, 1, &take);
+        us = plan_tiles(&p, B.rows, A.rows, (dim + 63) / 64, kStageValues, 1, 1, &take);
     } else {
         p.ks = (blocks_of(dim) + 3) / 4 * 4;
         for (int i = 0; i < 2; ++i) {
             p.pack_s[i] = !(i == 1 && B.shift) && !s_in_place(*o[i], dim);   // (B's in blocks are read singly)
             if (p.pack_s[i]) p.off_s[i] = take(uint64_t(scale_rows(*o[i])) * p.ks);
         }
-        plan_tiles(&p, B.rows, A.rows, dim / kBlock, kStage8, 1, 4, &take);
+        us = plan_tiles(&p, B.rows, A.rows, dim / kBlock, kStage8, 1, 4, &take);
     }
-    p.bytes = take.at;
+    // a launch and a tile's ends; the results, which nothing hides in the last tile
+    us += 4.3 + (p.splits == 1 ? double(A.rows) * double(B.rows) * double(elem_size(dtype)) / 5e6 : 0);
+    p.bytes = plan_small(&p, A, B, dim, dtype, us) ? 0 : take.at;
     return p;
 }
 
@@ -285,7 +322,7 @@ mo_status fp8_matmul_workspace_bytes(const mo_fp8_matrix* A, const mo_fp8_matrix
     *bytes = 0;
     MoF8Operand a, b;
     MO_TRY(matmul_args(A, B, dim, dtype, &a, &b));
-    if (a.rows == 0 || b.rows == 0 || dim == 0 || few_rows(a, b, dim, dtype)) return MO_OK;
+    if (a.rows == 0 || b.rows == 0 || dim == 0) return MO_OK;
     const uint64_t need = matmul_plan(a, b, dim, dtype).bytes;
     *bytes = need ? size_t(need) + MO_WS_ALIGN : 0;
     return MO_OK;
@@ -305,15 +342,14 @@ mo_status fp8_matmul(const mo_fp8_matrix* A, const mo_fp8_matrix* B, int64_t dim
     operand_ranges(a, dim, &r);
     operand_ranges(b, dim, &r);
     r.add(matrix_range(Y, a.rows, b.rows, ldy, elem_size(dtype), 1));
-    if (few_rows(a, b, dim, dtype)) {
-        if (r.conflict()) return MO_ERR_ALIAS;
-        MO_RUN(MO_PHASE_F8_GEMM, mo_launch_f8_few(a, b, dim, Y, ldy, dtype, s));
-        return MO_OK;
-    }
     const MoF8Plan p = matmul_plan(a, b, dim, dtype);
     uint8_t* ws;
     if (!take_workspace(workspace, workspace_bytes, p.bytes, &r, &ws)) return MO_ERR_WORKSPACE_TOO_SMALL;
     if (r.conflict()) return MO_ERR_ALIAS;
+    if (p.tb) {
+        MO_RUN(MO_PHASE_F8_GEMM, mo_launch_f8_small(a, b, p, dim, Y, ldy, dtype, s));
+        return MO_OK;
+    }
     for (int i = 0; i < 2; ++i)
         if (p.pack_s[i]) MO_RUN(MO_PHASE_F8_PREP, mo_launch_f8_pack(i ? b : a, p, i, dim, ws, s));
     MO_RUN(MO_PHASE_F8_GEMM, mo_launch_f8_matmul(a, b, p, dim, Y, ldy, dtype, ws, s));

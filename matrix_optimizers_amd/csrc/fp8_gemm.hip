@@ -131,37 +131,58 @@ __global__ __launch_bounds__(256) void f8_sum_kernel(Tiles t, Out<T> o) {
     for (int b = 0; b < L::NBW; ++b) put4(o, q + b * 16, p, s[b]);
 }
 
-// ---- few tokens ------------------------------------------------------------------------
+// ---- small products --------------------------------------------------------------------
 
-// Few rows of Q: the product is a read of P, once, and the rest hides behind it.  A workgroup takes 16 RB
-// rows of P; its eight waves take every eighth block of K, straight into registers (no row of P
-// is wanted twice), D blocks of loads under way at a time, and add their sums up through LDS in order.  Q's
-// 16 TB rows come out of the caches.  Nothing is asked of the operands' alignment; what lies
-// behind a row's end is not read.  T float: the values as bf16 numbers, with exact products.
+// Few rows of Q, or little of everything: the product is a read of its operands, and the rest hides behind it.  A
+// workgroup takes 16 RB rows of P and 16 TB of Q; its eight waves take every eighth block of K, D of them
+// at a time, straight into registers, and add their sums up through LDS in order.  Workgroups start at
+// different blocks, so that rows a power of two apart do not all ask the same memory channel at a time.
+// Nothing is asked of the operands' alignment; what lies behind a row's end is not read.  T float: the
+// values as bf16 numbers, with exact products.
+//
+// Four neighbouring lanes load 64 bytes of a row, 16 rows at once; the MFMA wants a row's four pieces in lanes
+// 16 apart, so they change places through the wave's own part of LDS (which it uses in order:
+// no barrier).  Loaded as the MFMA wants them, neighbouring lanes would read 16 different rows, and their lines
+// are looked up one by one: 64 x 4096 x 4096 took 12.3 us and 8 x 14336 x 4096 12.6.
 template <int TB, int RB, typename T>
-__global__ __launch_bounds__(512) void f8_few_kernel(Operand8 P, Operand8 Q, int dim, Out<T> o) {
+__global__ __launch_bounds__(512) void f8_small_kernel(Operand8 P, Operand8 Q, int dim, uint32_t bp, uint32_t bq, Out<T> o) {
 #ifdef __HIP_DEVICE_COMPILE__
     constexpr int D = 4 / RB;
-    __shared__ f32x4 sums[8][RB * TB][64];
+    __shared__ f32x4 sums[8][RB * TB < 4 ? 4 : RB * TB][64];
     const int lane = threadIdx.x & 63, r16 = lane & 15, kg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t p0 = int64_t(blockIdx.x) * (16 * RB);
-    const int nk = (dim + F8_BLOCK - 1) / F8_BLOCK;
+    // each XCD a contiguous share of the bp x bq blocks, the shorter side's side by side
+    const uint32_t share = gridDim.x >> 3, rem = gridDim.x & 7, x = blockIdx.x & 7;
+    const uint32_t block = x * share + (x < rem ? x : rem) + (blockIdx.x >> 3);
+    const int64_t p0 = int64_t(bq < bp ? block / bq : block % bp) * (16 * RB);
+    const int64_t q0 = int64_t(bq < bp ? block % bq : block / bp) * (16 * TB);
+    const int full = dim / F8_BLOCK;
     union Frag {
         i32x8 v;
         u32x4 h[2];
     };
+    const int lr = lane >> 2, lc = lane & 3;   // the row and the piece that a lane loads
+    // Piece c of row r is piece 4 r + (c ^ r / 4) of 64: both sides of the turn use all banks.
+    const int there = lr * 4 + (lc ^ (lr >> 2)), here = r16 * 4 + (kg ^ (r16 >> 2));
+    auto turn = [&](u32x4 x, int i) __attribute__((always_inline)) {
+        u32x4* z = reinterpret_cast<u32x4*>(sums[wave][i & 3]);
+        z[there] = x;
+        asm volatile("" ::: "memory");
+        const u32x4 y = z[here];
+        asm volatile("" ::: "memory");
+        return y;
+    };
     const uint8_t *pq[RB], *ps[RB], *qq[TB], *qs[TB];
 #pragma unroll
     for (int i = 0; i < RB; ++i) {
-        const int64_t r = p0 + i * 16 + r16, row = r < P.rows ? r : P.rows - 1;
-        pq[i] = P.q + row * P.ld + kg * 16;
+        const int64_t r = p0 + i * 16 + lr, row = r < P.rows ? r : P.rows - 1;
+        pq[i] = P.q + row * P.ld + lc * 16;
         ps[i] = P.s + (row >> P.shift) * P.ld_s;
     }
 #pragma unroll
     for (int i = 0; i < TB; ++i) {
-        const int64_t r = i * 16 + r16, row = r < Q.rows ? r : Q.rows - 1;
-        qq[i] = Q.q + row * Q.ld + kg * 16;
+        const int64_t r = q0 + i * 16 + lr, row = r < Q.rows ? r : Q.rows - 1;
+        qq[i] = Q.q + row * Q.ld + lc * 16;
         qs[i] = Q.s + (row >> Q.shift) * Q.ld_s;
     }
     f32x4 acc[RB][TB];
@@ -170,7 +191,7 @@ __global__ __launch_bounds__(512) void f8_few_kernel(Operand8 P, Operand8 Q, int
 #pragma unroll
         for (int j = 0; j < TB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     typedef u32x4 u32x4_e1 __attribute__((aligned(1)));
-    // Chunks kg and kg + 4 of block k of a row (zeros behind its end; whole blocks without a branch)
+    // A lane's two pieces of block k of a row (zeros behind its end; whole blocks without a branch)
     auto load = [&](Frag& f, const uint8_t* p, int k, bool whole) __attribute__((always_inline)) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -178,13 +199,18 @@ __global__ __launch_bounds__(512) void f8_few_kernel(Operand8 P, Operand8 Q, int
             if (whole) {
                 f.h[h] = *reinterpret_cast<const u32x4_e1*>(a);
             } else {
-                const int n = dim - k * F8_BLOCK - h * 64 - kg * 16;
+                const int n = dim - k * F8_BLOCK - h * 64 - lc * 16;
                 const u32x2 lo = ldq8(a, n), hi = ldq8(a + 8, n - 8);
                 f.h[h] = u32x4{lo[0], lo[1], hi[0], hi[1]};
             }
         }
     };
-    // eight values of half e of chunk h, as bf16
+    auto turn_all = [&](Frag& f, uint32_t& scale, int i) __attribute__((always_inline)) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) f.h[h] = turn(f.h[h], 2 * i + h);
+        scale = uint32_t(__builtin_amdgcn_ds_bpermute(r16 * 16, int(scale)));
+    };
+    // eight values of half e of piece h, as bf16
     auto wide = [&](const Frag& f, int h, int e, uint32_t scale) __attribute__((always_inline)) {
         const float s = __uint_as_float(scale << 23);   // (the conversion takes the exponent's field, as in e8m0)
         u32x4 w;
@@ -195,25 +221,35 @@ __global__ __launch_bounds__(512) void f8_few_kernel(Operand8 P, Operand8 Q, int
         }
         return __builtin_bit_cast(bf16x8, w);
     };
-    auto run = [&](int k, auto count, bool whole) __attribute__((always_inline)) {
+    const int first = full ? int(block % uint32_t(full)) : 0;
+    auto run = [&](int n, auto count, bool whole) __attribute__((always_inline)) {
         constexpr int N = decltype(count)::value;
         Frag a[N][RB], b[N][TB];
         uint32_t sa[N][RB], sb[N][TB];
 #pragma unroll
         for (int d = 0; d < N; ++d) {
+            int k = n + 8 * d;
+            if (whole) {
+                k += first;
+                k = k < full ? k : k - full;
+            }
 #pragma unroll
             for (int i = 0; i < RB; ++i) {
-                load(a[d][i], pq[i], k + 8 * d, whole);
-                sa[d][i] = ps[i][(k + 8 * d) * P.inc];
+                load(a[d][i], pq[i], k, whole);
+                sa[d][i] = ps[i][k * P.inc];
             }
 #pragma unroll
             for (int i = 0; i < TB; ++i) {
-                load(b[d][i], qq[i], k + 8 * d, whole);
-                sb[d][i] = qs[i][(k + 8 * d) * Q.inc];
+                load(b[d][i], qq[i], k, whole);
+                sb[d][i] = qs[i][k * Q.inc];
             }
         }
 #pragma unroll
         for (int d = 0; d < N; ++d) {
+#pragma unroll
+            for (int i = 0; i < RB; ++i) turn_all(a[d][i], sa[d][i], i);
+#pragma unroll
+            for (int i = 0; i < TB; ++i) turn_all(b[d][i], sb[d][i], RB + i);
             if constexpr (sizeof(T) == 2) {
 #pragma unroll
                 for (int i = 0; i < RB; ++i)
@@ -238,25 +274,25 @@ __global__ __launch_bounds__(512) void f8_few_kernel(Operand8 P, Operand8 Q, int
             }
         }
     };
-    const int full = dim / F8_BLOCK;
-    int k = wave;
-    for (; k + 8 * (D - 1) < full; k += 8 * D) run(k, std::integral_constant<int, D>(), true);
-    for (; k < full; k += 8) run(k, std::integral_constant<int, 1>(), true);
-    if (k < nk) run(k, std::integral_constant<int, 1>(), false);
+    int n = wave;
+    for (; n + 8 * (D - 1) < full; n += 8 * D) run(n, std::integral_constant<int, D>(), true);
+    for (; n < full; n += 8) run(n, std::integral_constant<int, 1>(), true);
+    if (n == full && dim % F8_BLOCK) run(n, std::integral_constant<int, 1>(), false);
 #pragma unroll
     for (int i = 0; i < RB; ++i)
 #pragma unroll
-        for (int j = 0; j < TB; ++j) sums[wave][i * TB + j][lane] = acc[i][j];
+        for (int j = 0; j < TB; ++j) sums[wave][i * TB + j][here] = acc[i][j];
     __syncthreads();
+    // (turned back: four lanes store a row's 16 neighbours)
     for (int u = wave; u < RB * TB; u += 8) {
-        f32x4 s = sums[0][u][lane];
+        f32x4 s = sums[0][u][there];
 #pragma unroll
         for (int w = 1; w < 8; ++w) {
-            const f32x4 x = sums[w][u][lane];
+            const f32x4 x = sums[w][u][there];
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[e] += x[e];
         }
-        put4(o, u % TB * 16 + r16, p0 + u / TB * 16 + kg * 4, s);
+        put4(o, q0 + u % TB * 16 + lr, p0 + u / TB * 16 + lc * 4, s);
     }
 #endif
 }
@@ -393,27 +429,25 @@ hipError_t mo_launch_f8_pack(const MoF8Operand& a, const MoF8Plan& p, int i, int
     return hipGetLastError();
 }
 
-template <int TB, typename T>
-static hipError_t few(const Operand8& P, const Operand8& Q, int64_t dim, const Out<T>& o, hipStream_t s) {
-    // 16 rb rows per workgroup: more read Q's rows less often, fewer workgroups than CUs leave some idle
-    const int64_t rows = P.rows;
-#define MO_FEW(RB)                                                                                                    hipLaunchKernelGGL((f8_few_kernel<TB, RB, T>), dim3(unsigned((rows + 16 * RB - 1) / (16 * RB))), dim3(512), 0, s, P, Q,                        int(dim), o)
-    if (rows >= 256 * 64) MO_FEW(4);
-    else if (rows >= 256 * 32) MO_FEW(2);
-    else MO_FEW(1);
-#undef MO_FEW
-    return hipGetLastError();
+template <int TB, int RB, typename T>
+static void small_tile(const Operand8& P, const Operand8& Q, int64_t dim, const Out<T>& o, hipStream_t s) {
+    const uint32_t bp = uint32_t((P.rows + 16 * RB - 1) / (16 * RB)), bq = uint32_t((Q.rows + 16 * TB - 1) / (16 * TB));
+    hipLaunchKernelGGL((f8_small_kernel<TB, RB, T>), dim3(bp * bq), dim3(512), 0, s, P, Q, int(dim), bp, bq, o);
 }
 template <typename T>
-static hipError_t few_tb(const Operand8& P, const Operand8& Q, int64_t dim, const Out<T>& o, hipStream_t s) {
-    return Q.rows <= 16 ? few<1>(P, Q, dim, o, s) : Q.rows <= 32 ? few<2>(P, Q, dim, o, s) : few<4>(P, Q, dim, o, s);
+static hipError_t small(const Operand8& P, const Operand8& Q, int64_t dim, int tb, int rb, const Out<T>& o, hipStream_t s) {
+    if (tb == 4) small_tile<4, 4>(P, Q, dim, o, s);
+    else if (tb == 2) small_tile<2, 2>(P, Q, dim, o, s);
+    else if (rb == 2) small_tile<1, 2>(P, Q, dim, o, s);
+    else small_tile<1, 1>(P, Q, dim, o, s);
+    return hipGetLastError();
 }
-hipError_t mo_launch_f8_few(const MoF8Operand& A, const MoF8Operand& B, int64_t dim, void* Y, int64_t ldy, int32_t dtype,
-                            hipStream_t s) {
+hipError_t mo_launch_f8_small(const MoF8Operand& A, const MoF8Operand& B, const MoF8Plan& p, int64_t dim, void* Y, int64_t ldy,
+                              int32_t dtype, hipStream_t s) {
     const Operand8 Q = {A.q, A.s, A.ld, A.rows, 0, A.ld_s, A.inc, A.shift};
     const Operand8 P = {B.q, B.s, B.ld, B.rows, 0, B.ld_s, B.inc, B.shift};
-    if (dtype == MO_BF16) return few_tb<bf16_t>(P, Q, dim, {static_cast<bf16_t*>(Y), ldy, B.rows, A.rows, false}, s);
-    return few_tb<float>(P, Q, dim, {static_cast<float*>(Y), ldy, B.rows, A.rows, false}, s);
+    if (dtype == MO_BF16) return small<bf16_t>(P, Q, dim, p.tb, p.rb, {static_cast<bf16_t*>(Y), ldy, B.rows, A.rows, false}, s);
+    return small<float>(P, Q, dim, p.tb, p.rb, {static_cast<float*>(Y), ldy, B.rows, A.rows, false}, s);
 }
 hipError_t mo_launch_f8_matmul(const MoF8Operand& A, const MoF8Operand& B, const MoF8Plan& p, int64_t dim, void* Y,
                                int64_t ldy, int32_t dtype, uint8_t* ws, hipStream_t s) {

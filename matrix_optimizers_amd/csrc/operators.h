@@ -73,6 +73,7 @@ struct MoF8Wgrad {
 struct MoF8Plan {
     bool bf16;                  // through bf16 MFMA
     bool tokens;                // a weight gradient from the operands as they lie
+    int tb, rb;                 // tb > 0: a small product, 16 tb x 16 rb of it per workgroup, and nothing below
     int nb;                     // tile width 64 nb along the operand without 256-row tiles
     int nk, stages, splits;     // K stages in all; those of a part and the parts of a tile behind the first `full`
     uint32_t tm, tn, full;
@@ -81,9 +82,8 @@ struct MoF8Plan {
     uint64_t off_q[2], off_s[2], off_part, bytes;
 };
 hipError_t mo_launch_f8_pack(const MoF8Operand& a, const MoF8Plan& p, int i, int64_t dim, uint8_t* ws, hipStream_t s);
-// Few rows of A: no plan, no workspace.
-hipError_t mo_launch_f8_few(const MoF8Operand& A, const MoF8Operand& B, int64_t dim, void* Y, int64_t ldy, int32_t dtype,
-                            hipStream_t s);
+hipError_t mo_launch_f8_small(const MoF8Operand& A, const MoF8Operand& B, const MoF8Plan& p, int64_t dim, void* Y,
+                              int64_t ldy, int32_t dtype, hipStream_t s);
 hipError_t mo_launch_f8_matmul(const MoF8Operand& A, const MoF8Operand& B, const MoF8Plan& p, int64_t dim, void* Y,
                                int64_t ldy, int32_t dtype, uint8_t* ws, hipStream_t s);
 hipError_t mo_launch_f8_transpose(const MoF8Wgrad& a, const MoF8Plan& p, uint8_t* ws, hipStream_t s);

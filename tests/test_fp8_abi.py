@@ -166,11 +166,12 @@ def mm_bytes(a, b, dim, dtype=1):
 
 
 def test_matmul_workspace():
-    # parts along K of 64 tiles; none for a grid of whole rounds, a few rows or no work
-    need = mm_bytes(act(1000), wei(1000), 4096)
-    assert need > 0 and mm(act(1000), wei(1000), 4096, have=need - 1) == WS_SMALL
-    assert mm(act(1000), wei(1000), 4096, ws=None) == WS_SMALL
-    assert mm(act(1000), wei(1000), 4096, ws=A[4] + 64) == ALIAS
+    # parts along a long K of few tiles; none for a grid of whole rounds, a small product or no work
+    long = act(1500), wei(1000), 16384
+    need = mm_bytes(*long)
+    assert need > 0 and mm(*long, have=need - 1) == WS_SMALL
+    assert mm(*long, ws=None) == WS_SMALL
+    assert mm(*long, ws=A[4] + 64) == ALIAS
     assert mm_bytes(act(4096), wei(4096), 4096) == 0
     for few in (1, 32):
         assert mm_bytes(act(few), wei(4096), 4096) == 0 and mm_bytes(act(few), wei(4096), 500) == 0
@@ -276,7 +277,7 @@ def test_binding_operands():
         M8._matmul_args(q, s, *host8(300, 200))
     with pytest.raises(TypeError):
         mo.fp8_matmul_workspace_bytes(q, s, q, s, dtype=torch.float16)
-    assert mo.fp8_matmul_workspace_bytes(q, s, q, s) == 0 and mo.fp8_matmul_workspace_bytes(*host8(300, 4096), *host8(300, 4096)) > 0
+    assert mo.fp8_matmul_workspace_bytes(q, s, q, s) == 0 and mo.fp8_matmul_workspace_bytes(*host8(1500, 16384), *host8(1000, 16384)) > 0
     assert mo.fp8_weight_grad_workspace_bytes(torch.zeros(300, 7), q, s) > 0
     with pytest.raises(ValueError):
         mo.fp8_weight_grad_workspace_bytes(torch.zeros(299, 7), q, s)

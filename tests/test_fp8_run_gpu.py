@@ -163,12 +163,12 @@ def test_captured_step_replays(gpu, size):
 def test_two_graphs_share_a_workspace(gpu):
     """Two captured products on one caller's workspace, replayed in turn on one stream."""
     g = gen(5)
-    A = [mo.fp8_quantize(rand(g, (700, 4096), BF)) for _ in range(2)]
-    B = [mo.fp8_quantize_weight(rand(g, (640, 4096), BF), need_t=False)[:2] for _ in range(2)]
+    A = [mo.fp8_quantize(rand(g, (1500, 16384), BF)) for _ in range(2)]
+    B = [mo.fp8_quantize_weight(rand(g, (1000, 16384), BF), need_t=False)[:2] for _ in range(2)]
     need = mo.fp8_matmul_workspace_bytes(*A[0], *B[0])
     assert need > 0
     ws = torch.empty(need, dtype=torch.uint8, device="cuda")
-    out = [torch.empty((700, 640), device="cuda", dtype=BF) for _ in range(2)]
+    out = [torch.empty((1500, 1000), device="cuda", dtype=BF) for _ in range(2)]
     want = [mo.fp8_matmul(*a, *b) for a, b in zip(A, B)]
     torch.cuda.synchronize()
     graphs = []

@@ -165,25 +165,45 @@ bool plan_small(MoF8Plan* plan, const MoF8Operand& A, const MoF8Operand& B, int6
     return plan->tb != 0;
 }
 
-MoF8Plan matmul_plan(const MoF8Operand& A, const MoF8Operand& B, int64_t dim, int32_t dtype) {
-    MoF8Plan p = {};
+// A product in tiles, in 8 bits where `bits8`; its estimated us.  In 8 bits rows that are not in place are copied first.
+double plan_product(MoF8Plan* p, const MoF8Operand& A, const MoF8Operand& B, int64_t dim, bool bits8) {
     Carve take;
     const MoF8Operand* o[2] = {&A, &B};
     double us;
-    p.bf16 = dtype == MO_F32 || !q_in_place(A, dim) || !q_in_place(B, dim);
-    if (p.bf16) {
-        us = plan_tiles(&p, B.rows, A.rows, (dim + 63) / 64, kStageValues, 1, 1, &take);
-    } else {
-        p.ks = (blocks_of(dim) + 3) / 4 * 4;
+    *p = {};
+    p->bf16 = !bits8;
+    if (bits8) {
+        double copied = 0;
+        p->ks = (blocks_of(dim) + 3) / 4 * 4;
+        // not a multiple of 4 KB, which would put a tile's rows on few memory channels
+        p->ld_q = blocks_of(dim) * kBlock + (blocks_of(dim) % 32 == 0 ? kBlock : 0);
         for (int i = 0; i < 2; ++i) {
-            p.pack_s[i] = !(i == 1 && B.shift) && !s_in_place(*o[i], dim);   // (B's in blocks are read singly)
-            if (p.pack_s[i]) p.off_s[i] = take(uint64_t(scale_rows(*o[i])) * p.ks);
+            p->pack_q[i] = !q_in_place(*o[i], dim);
+            p->pack_s[i] = !(i == 1 && B.shift) && !s_in_place(*o[i], dim);   // (B's in blocks are read singly)
+            if (p->pack_q[i]) p->off_q[i] = take(uint64_t(o[i]->rows) * p->ld_q);
+            if (p->pack_s[i]) p->off_s[i] = take(uint64_t(scale_rows(*o[i])) * p->ks);
+            if (p->pack_q[i]) copied += double(o[i]->rows) * double(p->ld_q);
         }
-        us = plan_tiles(&p, B.rows, A.rows, dim / kBlock, kStage8, 1, 4, &take);
+        us = plan_tiles(p, B.rows, A.rows, blocks_of(dim), kStage8, 1, 4, &take) + (copied > 0 ? 4 + 2 * copied / 4.5e6 : 0) +
+             (p->pack_s[0] || p->pack_s[1] ? 3 : 0);
+    } else {
+        us = plan_tiles(p, B.rows, A.rows, (dim + 63) / 64, kStageValues, 1, 1, &take);
+    }
+    p->bytes = take.at;
+    return us;
+}
+
+MoF8Plan matmul_plan(const MoF8Operand& A, const MoF8Operand& B, int64_t dim, int32_t dtype) {
+    MoF8Plan p;
+    double us = plan_product(&p, A, B, dim, dtype == MO_BF16);
+    if (p.pack_q[0] || p.pack_q[1]) {
+        MoF8Plan values;
+        const double t = plan_product(&values, A, B, dim, false);
+        if (t < us) us = t, p = values;
     }
     // a launch and a tile's ends; the results, which nothing hides in the last tile
     us += 4.3 + (p.splits == 1 ? double(A.rows) * double(B.rows) * double(elem_size(dtype)) / 5e6 : 0);
-    p.bytes = plan_small(&p, A, B, dim, dtype, us) ? 0 : take.at;
+    if (plan_small(&p, A, B, dim, dtype, us)) p.bytes = 0;
     return p;
 }
 
@@ -350,6 +370,7 @@ mo_status fp8_matmul(const mo_fp8_matrix* A, const mo_fp8_matrix* B, int64_t dim
         MO_RUN(MO_PHASE_F8_GEMM, mo_launch_f8_small(a, b, p, dim, Y, ldy, dtype, s));
         return MO_OK;
     }
+    if (p.pack_q[0] || p.pack_q[1]) MO_RUN(MO_PHASE_F8_PREP, mo_launch_f8_copy(a, b, p, dim, ws, s));
     for (int i = 0; i < 2; ++i)
         if (p.pack_s[i]) MO_RUN(MO_PHASE_F8_PREP, mo_launch_f8_pack(i ? b : a, p, i, dim, ws, s));
     MO_RUN(MO_PHASE_F8_GEMM, mo_launch_f8_matmul(a, b, p, dim, Y, ldy, dtype, ws, s));

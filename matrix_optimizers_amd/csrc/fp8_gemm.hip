@@ -313,6 +313,35 @@ __global__ __launch_bounds__(256) void f8_copy_scales_kernel(const uint8_t* s, i
     }
 }
 
+// Rows to copy, 16-byte aligned and zeros behind their end: of either operand.
+struct CopyRows {
+    const uint8_t* src;
+    int64_t ld, rows;
+    uint8_t* dst;
+};
+__global__ __launch_bounds__(256) void f8_copy_rows_kernel(CopyRows a, CopyRows b, int dim, int64_t ldd) {
+    typedef u32x4 u32x4_e1 __attribute__((aligned(1)));
+    const int lane = threadIdx.x & 63, chunks = int(ldd >> 4);
+    for (int64_t w = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6); w < a.rows + b.rows; w += int64_t(gridDim.x) * 4) {
+        const bool first = w < a.rows;
+        const int64_t r = first ? w : w - a.rows;
+        const uint8_t* src = first ? a.src + r * a.ld : b.src + r * b.ld;
+        uint8_t* dst = (first ? a.dst : b.dst) + r * ldd;
+#pragma unroll 4
+        for (int c = lane; c < chunks; c += 64) {
+            u32x4 x;
+            const int n = dim - c * 16;
+            if (n >= 16) {
+                x = *reinterpret_cast<const u32x4_e1*>(src + c * 16);
+            } else {
+                const u32x2 lo = ldq8(src + c * 16, n), hi = ldq8(src + c * 16 + 8, n - 8);
+                x = u32x4{lo[0], lo[1], hi[0], hi[1]};
+            }
+            *reinterpret_cast<u32x4*>(dst + c * 16) = x;
+        }
+    }
+}
+
 // Eight values of a row to transpose: of a matrix, or of one in 8 bits.
 template <typename T> struct Source {
     const T* p;
@@ -421,6 +450,13 @@ hipError_t product_nb(const Operand8& P, const Operand8& Q, const MoF8Plan& p, c
 
 }  // namespace
 
+// The rows of both operands of the product, or of the one that is not in place.
+hipError_t mo_launch_f8_copy(const MoF8Operand& a, const MoF8Operand& b, const MoF8Plan& p, int64_t dim, uint8_t* ws, hipStream_t s) {
+    const CopyRows x = {a.q, a.ld, p.pack_q[0] ? a.rows : 0, ws + p.off_q[0]};
+    const CopyRows y = {b.q, b.ld, p.pack_q[1] ? b.rows : 0, ws + p.off_q[1]};
+    hipLaunchKernelGGL(f8_copy_rows_kernel, dim3(grid_for((x.rows + y.rows) * 64)), dim3(256), 0, s, x, y, int(dim), p.ld_q);
+    return hipGetLastError();
+}
 // The scales of operand i (0: A, 1: B) of the product, copied into the workspace.
 hipError_t mo_launch_f8_pack(const MoF8Operand& a, const MoF8Plan& p, int i, int64_t dim, uint8_t* ws, hipStream_t s) {
     const int64_t r = (a.rows + (int64_t(1) << a.shift) - 1) >> a.shift;
@@ -453,6 +489,7 @@ hipError_t mo_launch_f8_matmul(const MoF8Operand& A, const MoF8Operand& B, const
                                int64_t ldy, int32_t dtype, uint8_t* ws, hipStream_t s) {
     auto operand = [&](const MoF8Operand& a, int i) {
         Operand8 o = {a.q, a.s, a.ld, a.rows, 0, a.ld_s, a.inc, a.shift, dim};
+        if (p.pack_q[i]) o.q = ws + p.off_q[i], o.ld = p.ld_q;
         if (p.pack_s[i]) o.s = ws + p.off_s[i], o.ld_s = p.ks, o.inc = 1;
         return o;
     };

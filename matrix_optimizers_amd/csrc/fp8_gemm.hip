@@ -313,7 +313,7 @@ __global__ __launch_bounds__(256) void f8_copy_scales_kernel(const uint8_t* s, i
     }
 }
 
-// Rows to copy, 16-byte aligned and zeros behind their end: of either operand.
+// Rows to copy, 16-byte aligned and zeros behind their end: of either operand.  A wavefront per row; bound by memory.
 struct CopyRows {
     const uint8_t* src;
     int64_t ld, rows;

@@ -125,7 +125,8 @@ bool s_in_place(const MoF8Operand& o, int64_t dim) {
 
 // Estimated us of a product in small blocks, 16 rb rows of P (K along both) by 16 tb of Q per workgroup, `slots` of
 // them on the card at a time: `start`, then a workgroup's own time for a share of K (every eighth block, so
-// `turns` of them) or that of all workgroups, whichever is more.  At 4.4 a CU holds one, and rounds are whole.
+// `turns` of them) or that of all workgroups, whichever is more; behind the fourth turn the L2 no longer holds what
+// the workgroups read.  Of 4 x 4 a CU holds one, and rounds are whole.
 struct SmallBlocks {
     int tb, rb, slots;
     double start, own0, own, all0, all;
@@ -133,7 +134,8 @@ struct SmallBlocks {
         const int64_t n = ((p + 16 * rb - 1) / (16 * rb)) * ((q + 16 * tb - 1) / (16 * tb));
         if (n >= int64_t(1) << 20) return 1e30;
         const double rounds = slots == 256 ? double((n + 255) / 256) : double(n) / slots;
-        return start + std::max(own0 + own * turns, rounds * (all0 + all * turns));
+        const double longer = 1 + std::min(0.4, 0.1 * std::max(0.0, turns - 4)) * (slots == 256 ? 0.5 : 1);
+        return start + std::max(own0 + own * turns, rounds * (all0 + all * turns * longer));
     }
 };
 constexpr SmallBlocks kSmall[] = {{1, 1, 512, 3.1, 0, 0.36, 1.07, 0.53},
@@ -146,7 +148,8 @@ constexpr SmallBlocks kSmall[] = {{1, 1, 512, 3.1, 0, 0.36, 1.07, 0.53},
 // to last kind above, bf16 results: 16 tokens x 4096 x 4096 13.5, 4.6 5.3 6.3 10.5; 64 x 4096 x 4096 13.9, 9.0 7.5
 // 6.6 10.5; 64 x 14336 x 4096 18.9, 26.8 20.8 17.4 16.1; 18 x 1792 x 12672 22.6, 7.6 9.3 11.8 21.9; 512 x
 // 2048 x 2048 14.6, 20.2 13.3 10.1 7.9; 512 x 4096 x 4096 22.7, 51.9 39.5 28.5 21.1; 2048 x 2048 x 256 7.7,
-// 42.5 26.4 17.2 14.2.  fp32 results take 1.15 of the time in either, and rows that are not 16-byte
+// 42.5 26.4 17.2 14.2; 700 x 1500 x 8320 25.3, 62 47.7 37.9 34.9.  Of 27 products of 40 x 28672 x 8192 to 2048 x 2048
+// x 8192 in both types the choice is within 18 % of the best of all, of most the best.  fp32 results take 1.15 of the time in either, and rows that are not 16-byte
 // aligned 1.4 in small blocks (1021 x 2001 x 1000 21.6, 17.7; x 1024 19.1, 12.7).
 bool plan_small(MoF8Plan* plan, const MoF8Operand& A, const MoF8Operand& B, int64_t dim, int32_t dtype, double tiles_us) {
     const bool aligned = ((reinterpret_cast<uintptr_t>(A.q) | uintptr_t(A.ld) | reinterpret_cast<uintptr_t>(B.q) | uintptr_t(B.ld)) & 15) == 0;

@@ -30,6 +30,7 @@ PRODUCTS = [
     ((9000, 2600, 2048, 0, 128, 0, 0), dict(nb=4, many=1)), ((9000, 2600, 640, 0, 1, 3, 0), dict(nb=4, many=1, copy_a=1, scales_a=1, scales_b=1)),
     ((4133, 5001, 8320, 0, 128, 0, 0), dict(nb=4, split=1, many=1, scales_a=1)),
     ((4133, 5001, 8320, 0, 1, 3, 0), dict(nb=4, split=1, many=1, copy_a=1, scales_a=1, scales_b=1)),
+    ((9000, 260, 16640, 0, 128, 0, 0), dict(nb=4, split=1, scales_a=1)), ((300, 1500, 16640, 1, 128, 3, 0), dict(values=1, nb=1, split=1)),
     ((70, 2600, 128, 1, 128, 3, 0), dict(values=1, nb=1)), ((70, 5001, 128, 0, 1, 3, 0), dict(values=1, nb=1)),
     ((9000, 260, 128, 1, 128, 0, 0), dict(values=1, nb=2)), ((9000, 260, 128, 0, 128, 3, 1), dict(values=1, nb=2)),
     ((700, 1500, 8320, 1, 128, 3, 1), dict(values=1, nb=2, split=1)), ((9000, 777, 4100, 1, 1, 0, 0), dict(values=1, nb=2, split=1, many=1)),

@@ -8,6 +8,7 @@
 #include "fp8_gemm.h"
 #include "operators.h"
 
+#include <cfloat>
 #include <type_traits>
 
 namespace {
@@ -358,6 +359,145 @@ template <> struct Source<uint8_t> {
     }
 };
 
+// ---- small weight gradients ------------------------------------------------------------
+
+// 64 rows of G (columns of dY) by 64 of its columns (of X) per workgroup, 64 tokens at a time: both operands
+// come as they lie, eight neighbours of a row per thread and load, and go to LDS as bf16 (an fp32 dY as its three
+// parts), from where transposing reads make fragments of them, as in TOKENS (fp8_gemm.h).  Nothing is asked of
+// alignment, nothing is copied first, and several workgroups on a CU hide each other's waits; but every
+// operand is read out of LDS for 64 columns of the other alone, so large gradients go faster in tiles.  The
+// results turn in LDS, so that 16 lanes store 64 neighbours of a row.
+template <typename T, typename TG>
+__global__ __launch_bounds__(256) void f8_small_wgrad_kernel(Source<uint8_t> x, Source<T> y, int64_t tokens, Out<TG> o, uint32_t bx,
+                                                             uint32_t by) {
+#ifdef __HIP_DEVICE_COMPILE__
+    constexpr int PL = sizeof(T) == 4 ? 3 : 1, PLANE = 64 * 128, ROW = 68;   // ROW: floats of a row of results
+    constexpr int BYTES = PLANE * (1 + PL) > 64 * ROW * 4 ? PLANE * (1 + PL) : 64 * ROW * 4;
+    __shared__ __align__(16) uint8_t smem[BYTES];
+    const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, kg = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wp = wave & 1, wq = wave >> 1;
+    // each XCD a contiguous share of the blocks, the shorter side's side by side
+    const uint32_t share = gridDim.x >> 3, rem = gridDim.x & 7, xcd = blockIdx.x & 7;
+    const uint32_t block = xcd * share + (xcd < rem ? xcd : rem) + (blockIdx.x >> 3);
+    const int64_t p0 = int64_t(by < bx ? block / by : block % bx) * 64, q0 = int64_t(by < bx ? block % by : block / bx) * 64;
+    // a thread's eight columns, of tokens row and row + 32 of a chunk
+    const int row = tid >> 3, c = tid & 7;
+    const int np = int(o.cols - p0 - c * 8 < 8 ? o.cols - p0 - c * 8 : 8), nq = int(o.rows - q0 - c * 8 < 8 ? o.rows - q0 - c * 8 : 8);
+    const uint8_t* const xp = x.p + p0 + c * 8;
+    const uint8_t* const xs = x.s + (p0 >> 7) * x.inc;
+    const T* const yp = y.p + q0 + c * 8;
+    u32x2 xq[2];
+    uint32_t scale[2];
+    raw8<T> yv[2];
+    auto load = [&](int64_t t0) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int64_t t = t0 + row + 32 * i;
+            const bool in = t < tokens;
+            xq[i] = ldq8(xp + (in ? t : 0) * x.ld, in ? np : 0);
+            scale[i] = in ? xs[t * x.ld_s] : 0u;
+            yv[i] = ld8n(yp + (in ? t : 0) * y.ld, in ? nq : 0);
+        }
+    };
+    // rows of 64 columns in granules of 16, permuted as TOKENS permutes Q's
+    auto qf = [&](int r) __attribute__((always_inline)) { return ((r >> 1) & 1) | (((r >> 2) ^ (r >> 3)) & 2); };
+    auto put_row = [&](uint8_t* plane, int r, u32x4 v) __attribute__((always_inline)) {
+        *reinterpret_cast<u32x4*>(plane + r * 128 + ((c ^ (qf(r) << 1)) << 4)) = v;
+    };
+    auto store = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = row + 32 * i;
+            const float f = __uint_as_float(scale[i] << 23);   // (the conversion takes the exponent's field, as in e8m0)
+            u32x4 w;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                w[2 * e] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(xq[i][e], f, false));
+                w[2 * e + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(xq[i][e], f, true));
+            }
+            put_row(smem, r, w);
+            if constexpr (PL == 1) {
+                put_row(smem + PLANE, r, __builtin_bit_cast(u32x4, yv[i]));
+            } else {
+                // its upper 8 bits, the next 8 and the rest, cut off and so exact; an infinity is one in the
+                // first part alone, a NaN stays one
+                const f32x8 v = widen(yv[i]);
+                uint32_t z[3][8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float f = __builtin_canonicalizef(v.v[e]), g = __builtin_amdgcn_fmed3f(f, -FLT_MAX, FLT_MAX);
+                    const float r = g - __uint_as_float(__float_as_uint(g) & 0xFFFF0000u);
+                    z[0][e] = __float_as_uint(f);
+                    z[1][e] = __float_as_uint(r);
+                    z[2][e] = __float_as_uint(r - __uint_as_float(__float_as_uint(r) & 0xFFFF0000u));
+                }
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    u32x4 u;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) u[e] = __builtin_amdgcn_perm(z[k][2 * e + 1], z[k][2 * e], 0x07060302);   // the upper halves
+                    put_row(smem + (1 + k) * PLANE, r, u);
+                }
+            }
+        }
+    };
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    const int trow = kg * 8 + (r16 >> 2);
+    // tokens 32 h .. of granule g's 16 columns
+    auto frag = [&](const uint8_t* plane, int g, int h) __attribute__((always_inline)) {
+        const uint8_t* p = plane + trow * 128 + ((g ^ qf(trow)) << 5) + (r16 & 3) * 8 + h * 32 * 128;
+        u32x4 f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + j * 4 * 128)));
+            f[2 * j] = v[0];
+            f[2 * j + 1] = v[1];
+        }
+        return __builtin_bit_cast(bf16x8, f);
+    };
+    f32x4 acc[2][2];
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    load(0);
+    for (int64_t t0 = 0; t0 < tokens; t0 += 64) {
+        store();
+        __syncthreads();
+        if (t0 + 64 < tokens) load(t0 + 64);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            bf16x8 p[2];
+#pragma unroll
+            for (int a = 0; a < 2; ++a) p[a] = frag(smem, wp * 2 + a, h);
+            // the smallest part first
+#pragma unroll
+            for (int k = PL; k >= 1; --k)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const bf16x8 q = frag(smem + k * PLANE, wq * 2 + b, h);
+#pragma unroll
+                    for (int a = 0; a < 2; ++a) acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p[a], q, acc[a][b], 0, 0, 0);
+                }
+        }
+        __syncthreads();
+    }
+    float* const z = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+            *reinterpret_cast<f32x4*>(z + (wq * 32 + b * 16 + r16) * ROW + wp * 32 + a * 16 + kg * 4) = acc[a][b];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 16 + (tid >> 4), k = (tid & 15) * 4;
+        put4(o, q0 + r, p0 + k, *reinterpret_cast<const f32x4*>(z + r * ROW + k));
+    }
+#endif
+}
+
 // dst[plane][c][ldt] <- src[r][c], zeros for rows from `rows` up to 64 tr.
 template <typename T> struct Transpose {
     Source<T> src;
@@ -516,6 +656,20 @@ static hipError_t transpose(const MoF8Wgrad& a, const MoF8Plan& p, uint8_t* ws, 
 }
 hipError_t mo_launch_f8_transpose(const MoF8Wgrad& a, const MoF8Plan& p, uint8_t* ws, hipStream_t s) {
     return a.dy_dtype == MO_BF16 ? transpose<bf16_t, 1>(a, p, ws, s) : transpose<float, 3>(a, p, ws, s);
+}
+
+template <typename T, typename TG>
+static hipError_t small_wgrad(const MoF8Wgrad& a, hipStream_t s) {
+    const uint32_t bx = uint32_t((a.dim + 63) / 64), by = uint32_t((a.rows + 63) / 64);
+    const Source<uint8_t> x = {a.X.q, a.X.ld, a.X.s, a.X.ld_s, a.X.inc};
+    const Source<T> y = {static_cast<const T*>(a.dY), a.lddy};
+    const Out<TG> o = {static_cast<TG*>(a.G), a.ldg, a.dim, a.rows, a.accumulate != 0};
+    hipLaunchKernelGGL((f8_small_wgrad_kernel<T, TG>), dim3(bx * by), dim3(256), 0, s, x, y, a.X.rows, o, bx, by);
+    return hipGetLastError();
+}
+hipError_t mo_launch_f8_small_wgrad(const MoF8Wgrad& a, hipStream_t s) {
+    if (a.dy_dtype == MO_BF16) return a.g_dtype == MO_BF16 ? small_wgrad<bf16_t, bf16_t>(a, s) : small_wgrad<bf16_t, float>(a, s);
+    return a.g_dtype == MO_BF16 ? small_wgrad<float, bf16_t>(a, s) : small_wgrad<float, float>(a, s);
 }
 
 template <int KIND>

@@ -90,6 +90,7 @@ hipError_t mo_launch_f8_small(const MoF8Operand& A, const MoF8Operand& B, const 
 hipError_t mo_launch_f8_matmul(const MoF8Operand& A, const MoF8Operand& B, const MoF8Plan& p, int64_t dim, void* Y,
                                int64_t ldy, int32_t dtype, uint8_t* ws, hipStream_t s);
 hipError_t mo_launch_f8_transpose(const MoF8Wgrad& a, const MoF8Plan& p, uint8_t* ws, hipStream_t s);
+hipError_t mo_launch_f8_small_wgrad(const MoF8Wgrad& a, hipStream_t s);
 hipError_t mo_launch_f8_wgrad(const MoF8Wgrad& a, const MoF8Plan& p, uint8_t* ws, hipStream_t s);
 
 // ---- embedding -------------------------------------------------------------------

@@ -5,8 +5,8 @@ A product: rows of A, rows of B, K, whether the result is fp32, rows per scale o
 A's rows are off alignment, whether A's scales lie by columns; then its path: `small` (16 tb and 16 rb rows per
 workgroup as tb rb) or tiles of 64 nb columns, as `values` or in 8 bits, K in parts (`split`), more than
 one round of tiles (`many`), copies of A, of B and of their scales.
-A weight gradient: tokens, rows, dim, fp32 dY, elements by which dY is off; its path: read in place
-(`tokens`), planes of dY, nb, split, many."""
+A weight gradient: tokens, rows, dim, fp32 dY, elements by which dY is off; its path: planes of dY, and blocks
+of 64 x 64 (`small`) or tiles: read in place (`tokens`), nb, split, many."""
 
 PRODUCTS = [
     ((70, 100, 500, 0, 128, 0, 0), dict(small=11)), ((70, 100, 500, 1, 128, 1, 0), dict(small=11)),
@@ -39,19 +39,41 @@ PRODUCTS = [
 ]
 
 WGRADS = [
-    ((64, 104, 112, 0, 0), dict(tokens=1, planes=1, nb=1)), ((1030, 104, 112, 0, 0), dict(tokens=1, planes=1, nb=1, split=1)),
-    ((64, 2600, 2048, 0, 0), dict(tokens=1, planes=1, nb=2)), ((2100, 5008, 272, 0, 0), dict(tokens=1, planes=1, nb=2, split=1)),
-    ((8000, 5008, 2048, 0, 0), dict(tokens=1, planes=1, nb=2, split=1, many=1)), ((64, 5008, 2048, 0, 0), dict(tokens=1, planes=1, nb=4)),
-    ((64, 5008, 4112, 0, 0), dict(tokens=1, planes=1, nb=4, many=1)), ((8000, 1504, 2048, 0, 0), dict(tokens=1, planes=1, nb=4, split=1)),
-    ((2100, 5008, 4112, 0, 0), dict(tokens=1, planes=1, nb=4, split=1, many=1)),
-    ((64, 104, 112, 0, 1), dict(planes=1, nb=1)), ((1030, 104, 112, 0, 1), dict(planes=1, nb=1, split=1)),
-    ((64, 2600, 2048, 0, 1), dict(planes=1, nb=2)), ((64, 5008, 4112, 0, 1), dict(planes=1, nb=2, many=1)),
-    ((8000, 5008, 112, 0, 1), dict(planes=1, nb=2, split=1)), ((8000, 5008, 2048, 0, 1), dict(planes=1, nb=2, split=1, many=1)),
-    ((64, 5008, 2048, 0, 1), dict(planes=1, nb=4)), ((8000, 1504, 2048, 0, 1), dict(planes=1, nb=4, split=1)),
-    ((8000, 5008, 4112, 0, 1), dict(planes=1, nb=4, split=1, many=1)),
-    ((64, 104, 112, 1, 0), dict(planes=3, nb=1)), ((300, 104, 112, 1, 0), dict(planes=3, nb=1, split=1)),
-    ((64, 2600, 2048, 1, 0), dict(planes=3, nb=2)), ((64, 5008, 4112, 1, 1), dict(planes=3, nb=2, many=1)),
-    ((8000, 2600, 112, 1, 0), dict(planes=3, nb=2, split=1)), ((1030, 5008, 2048, 1, 0), dict(planes=3, nb=2, split=1, many=1)),
-    ((64, 5008, 2048, 1, 0), dict(planes=3, nb=4)), ((8000, 5008, 272, 1, 1), dict(planes=3, nb=4, split=1)),
-    ((2100, 5008, 4112, 1, 0), dict(planes=3, nb=4, split=1, many=1)),
+    ((1, 7, 3, 1, 1), dict(small=4, planes=3)),
+    ((65, 129, 257, 0, 0), dict(small=4, planes=1)),
+    ((300, 70, 1101, 1, 1), dict(small=4, planes=3)),
+    ((700, 264, 272, 0, 1), dict(small=4, planes=1)),
+    ((64, 5008, 2048, 1, 0), dict(small=4, planes=3)),
+    ((1030, 1504, 112, 0, 1), dict(planes=1, nb=1)),
+    ((1030, 64, 112, 0, 1), dict(planes=1, nb=1, split=1)),
+    ((4100, 9000, 272, 0, 1), dict(planes=1, nb=1, split=1, many=1)),
+    ((70, 777, 8016, 0, 0), dict(planes=1, nb=2)),
+    ((1, 5008, 4112, 0, 1), dict(planes=1, nb=2, many=1)),
+    ((8000, 5008, 112, 0, 1), dict(planes=1, nb=2, split=1)),
+    ((2100, 9000, 2048, 0, 1), dict(planes=1, nb=2, split=1, many=1)),
+    ((70, 9000, 1101, 0, 1), dict(planes=1, nb=4)),
+    ((1, 9000, 8016, 0, 1), dict(planes=1, nb=4, many=1)),
+    ((16000, 9000, 112, 0, 1), dict(planes=1, nb=4, split=1)),
+    ((4100, 9000, 2048, 0, 1), dict(planes=1, nb=4, split=1, many=1)),
+    ((300, 777, 4112, 1, 0), dict(planes=3, nb=1)),
+    ((1030, 64, 112, 1, 0), dict(planes=3, nb=1, split=1)),
+    ((300, 2600, 2048, 1, 1), dict(planes=3, nb=2)),
+    ((70, 5008, 4112, 1, 1), dict(planes=3, nb=2, many=1)),
+    ((8000, 2600, 112, 1, 0), dict(planes=3, nb=2, split=1)),
+    ((1030, 5008, 2048, 1, 0), dict(planes=3, nb=2, split=1, many=1)),
+    ((70, 1504, 8016, 1, 1), dict(planes=3, nb=4)),
+    ((70, 9000, 8016, 1, 0), dict(planes=3, nb=4, many=1)),
+    ((16000, 5008, 112, 1, 1), dict(planes=3, nb=4, split=1)),
+    ((1030, 9000, 2048, 1, 0), dict(planes=3, nb=4, split=1, many=1)),
+    ((300, 1504, 2048, 0, 0), dict(tokens=1, planes=1, nb=1)),
+    ((1030, 64, 112, 0, 0), dict(tokens=1, planes=1, nb=1, split=1)),
+    ((70, 2600, 2048, 0, 0), dict(tokens=1, planes=1, nb=2)),
+    ((4100, 5008, 112, 0, 0), dict(tokens=1, planes=1, nb=2, split=1)),
+    ((8000, 5008, 2048, 0, 0), dict(tokens=1, planes=1, nb=2, split=1, many=1)),
+    ((1, 2600, 4112, 0, 0), dict(tokens=1, planes=1, nb=4)),
+    ((1, 9000, 4112, 0, 0), dict(tokens=1, planes=1, nb=4, many=1)),
+    ((8000, 9000, 112, 0, 0), dict(tokens=1, planes=1, nb=4, split=1)),
+    ((1030, 9000, 2048, 0, 0), dict(tokens=1, planes=1, nb=4, split=1, many=1)),
+    ((1, 64, 112, 0, 0), dict(small=4, planes=1)),
+    ((1, 64, 112, 1, 0), dict(small=4, planes=3)),
 ]

@@ -31,7 +31,7 @@ int main() {
             MoF8Wgrad a;
             if (wgrad_args(at(3, oy * elem_size(dt)), 0, dt, &X, k, n, &a) != MO_OK) return 1;
             const MoF8Plan p = wgrad_plan(a);
-            std::printf("tokens=%d planes=%d nb=%d splits=%d rounds=%d bytes=%" PRIu64 "\n", int(p.tokens), dt == MO_BF16 ? 1 : 3, p.nb, p.splits,
+            std::printf("small=%d tokens=%d planes=%d nb=%d splits=%d rounds=%d bytes=%" PRIu64 "\n", p.tb, int(p.tokens), dt == MO_BF16 ? 1 : 3, p.nb, p.splits,
                         int(p.full / 256 + (p.full % 256 || p.splits > 1)), p.bytes);
         }
     }

@@ -207,7 +207,8 @@ def wg(dY=A[0], ldy=0, yt=1, x="default", dim=512, G=A[4], ldg=0, gt=0, rows=600
     (dict(yt=2), UNSUPPORTED), (dict(gt=2), UNSUPPORTED), (dict(dim=(1 << 20) + 1), UNSUPPORTED),
     (dict(rows=(1 << 20) + 1), UNSUPPORTED), (dict(x=wei((1 << 20) + 1, block_rows=1)), UNSUPPORTED),
     (dict(ldy=(1 << 26) + 1), UNSUPPORTED), (dict(G=A[0] + 64), ALIAS), (dict(G=A[2]), ALIAS), (dict(G=A[3] + 1), ALIAS),
-    (dict(yt=0, ws=A[4]), ALIAS), (dict(yt=0, have=4096), WS_SMALL), (dict(yt=0, ws=None), WS_SMALL),
+    (dict(x=wei(16384, block_rows=1), ws=A[4]), ALIAS), (dict(x=wei(16384, block_rows=1), have=4096), WS_SMALL),
+    (dict(x=wei(16384, block_rows=1), ws=None), WS_SMALL),
     (dict(rows=0), OK), (dict(dim=0, G=None), OK), (dict(x=wei(0, block_rows=1), acc=1, G=None), OK)])
 def test_weight_grad_refusals(kw, code):
     assert wg(**kw) == code
@@ -227,7 +228,7 @@ def test_weight_grad_workspace():
     assert st == OK and need >= (3 + 1) * 16384 * 4096 * 2
     assert wg_bytes(dY=A[0] + 2, **big)[1] >= 2 * 16384 * 4096 * 2
     assert wg_bytes(ldy=4097, **big)[1] >= 2 * 16384 * 4096 * 2
-    assert wg_bytes() == (OK, 0)                           # a few stages of K are not worth parts
+    assert wg_bytes() == (OK, 0)                           # a small one takes no workspace
     long = dict(x=wei(16384, block_rows=1))                # many are, of 3 x 2 to 8 tiles
     st, need = wg_bytes(**long)
     assert st == OK and need >= 2 * 600 * 512 * 4 and wg(have=need - 1, **long) == WS_SMALL
@@ -281,7 +282,8 @@ def test_binding_operands():
     with pytest.raises(TypeError):
         mo.fp8_matmul_workspace_bytes(q, s, q, s, dtype=torch.float16)
     assert mo.fp8_matmul_workspace_bytes(q, s, q, s) == 0 and mo.fp8_matmul_workspace_bytes(*host8(1500, 16384), *host8(1000, 16384)) > 0
-    assert mo.fp8_weight_grad_workspace_bytes(torch.zeros(300, 7), q, s) > 0
+    assert mo.fp8_weight_grad_workspace_bytes(torch.zeros(300, 7), q, s) == 0
+    assert mo.fp8_weight_grad_workspace_bytes(torch.zeros(16384, 7), *host8(16384, 300)) > 0
     with pytest.raises(ValueError):
         mo.fp8_weight_grad_workspace_bytes(torch.zeros(299, 7), q, s)
     with pytest.raises(TypeError):

@@ -36,7 +36,7 @@ def plans(tmp_path_factory):
             p["split"], p["many"] = int(p.pop("splits") > 1), int(p.pop("rounds") > 1)
             p["bytes"] = int(p["bytes"] > 0)
             if p.get("small"):
-                p = {"small": p["small"], "bytes": p["bytes"]}
+                p = {k: p[k] for k in ("small", "planes", "bytes") if k in p}
             got.append(p)
         return got
     return run
@@ -58,7 +58,7 @@ def test_cases_take_the_paths_they_name(plans):
         assert {k: v for k, v in p.items() if v} == want, (c, p)
         # a workspace where something is copied, transposed or in parts, and only there
         parts = [want.get(k) for k in ("split", "copy_a", "copy_b", "scales_a", "scales_b")]
-        assert needs == int(any(parts) or ("planes" in want and not want.get("tokens"))), c
+        assert needs == int(any(parts) or ("planes" in want and not want.get("tokens") and not want.get("small"))), c
 
 
 def test_every_path_has_a_case(plans):

@@ -12,8 +12,8 @@ from test_embedding_gpu import gen, rand
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
-# tokens, width, inner width: 8-bit products, converted operands, a few tokens, K in parts
-SIZES = [(200, 256, 512), (70, 200, 330), (5, 384, 256), (1100, 256, 640)]
+# tokens, width, inner width: small products, odd ones, a few tokens, K in parts, copied and transposed operands
+SIZES = [(200, 256, 512), (70, 200, 330), (5, 384, 256), (1100, 256, 640), (4100, 1000, 1500)]
 
 
 class Block:
@@ -216,7 +216,7 @@ def test_a_matrix_with_itself(gpu):
 
 
 def test_phases_are_timed(gpu):
-    m = Block(*SIZES[1])
+    m = Block(*SIZES[4])
     mo.profile_enable(True)
     try:
         mo.profile_read()

@@ -582,7 +582,7 @@ mo_status fp8_matmul(const mo_fp8_matrix* A, const mo_fp8_matrix* B, int64_t dim
 
 /* Bytes of device workspace fp8_weight_grad needs.  Alignment counts: a bf16 dY of
  * rows % 8 == 0 and an X of dim % 16 == 0, with 16-byte aligned rows and scales by rows, are
- * read in place; others are copied first. */
+ * read in place, and all operands of small gradients; others are copied first. */
 mo_status fp8_weight_grad_workspace_bytes(const void* dY, int64_t ld_dy, int32_t dy_dtype,
                                           const mo_fp8_matrix* X, int64_t dim, int64_t rows,
                                           size_t* bytes);

@@ -219,26 +219,40 @@ bool tokens_in_place(const MoF8Wgrad& a) {
            ((reinterpret_cast<uintptr_t>(a.X.q) | uintptr_t(a.X.ld)) & 15) == 0;
 }
 
-// Whether a weight gradient takes less in blocks of 64 x 64, straight from the operands in one launch, than in tiles
-// (`tiles_us` with a launch, the results that nothing hides, and a launch that transposes): a workgroup alone on
-// its CU has its own time for 64 tokens, each further one adds to it.  (G's type is not known to the workspace's
-// query: dY's stands for it.)  us in blocks and in tiles: dY and G in
-// bf16, 98 tokens x 281 x 9600 6.5, 12.2; 1021 x 1024 x 1024 13.2, 19.2; 64 x 4096 x 4096 14.1, 13.9; 512 x 4096 x
-// 4096 40, 27; both in fp32, 206 x 5632 x 256 10.2, 21.1; 257 x 1000 x 2001 14.6, 20.4; 721 x 9344 x 16 19.9,
-// 37.7; 512 x 4096 x 4096 84, 62.
-bool wgrad_small(const MoF8Wgrad& a, const MoF8Plan& p, double tiles_us) {
+// A weight gradient in blocks of 64 x 64 straight from the operands, where that takes less than in tiles (`tiles_us`,
+// with a launch, the results that nothing hides, and a launch that transposes): a workgroup alone on
+// its CU has its own time for 64 tokens, each further one adds to it; few blocks share a long K's tokens among up to
+// 32 workgroups each, whose fp32 sums a second launch adds.  (G's type is not known to the workspace's query: dY's
+// stands for it.)  us in blocks and in tiles: dY and G in bf16, 98 tokens x 281 x 9600 6.5, 12.2; 1021 x 1024 x
+// 1024 13.2, 19.2; 64 x 4096 x 4096 14.1, 13.9; 512 x 4096 x 4096 40, 27; both in fp32, 206 x 5632 x 256 10.2, 21.1;
+// 257 x 1000 x 2001 14.6, 20.4; 721 x 9344 x 16 19.9, 37.7; 512 x 4096 x 4096 84, 62.
+void plan_small_wgrad(const MoF8Wgrad& a, double tiles_us, MoF8Plan* p) {
     const bool wide = a.dy_dtype == MO_F32;
     const double t = double(a.X.rows), n = double(a.rows), k = double(a.dim);
-    const int64_t blocks = ((a.rows + 63) / 64) * ((a.dim + 63) / 64);
-    if (blocks >= int64_t(1) << 20) return false;
-    const double per = double(blocks) / 256, chunks = double((a.X.rows + 63) / 64);
+    const int64_t blocks = ((a.rows + 63) / 64) * ((a.dim + 63) / 64), chunks = (a.X.rows + 63) / 64;
+    if (blocks >= int64_t(1) << 18) return;
     // rows of dY that are not 16-byte aligned touch more lines (bf16, 1627 x 5147 x 384 35, 29; 2766 x 10607 x 411 131, 63)
     const bool aligned = ((reinterpret_cast<uintptr_t>(a.dY) | uintptr_t(a.lddy * elem_size(a.dy_dtype))) & 15) == 0;
-    const double us = 4.2 + per * (wide ? 0.45 : 0.3) + chunks * (aligned ? 1 : wide ? 1.25 : 1.6) *
-                      ((wide ? 1.0 : 0.56) + std::max(0.0, per - 1) * (wide ? 0.56 : 0.26));
-    tiles_us += 4.3 + (p.splits == 1 ? n * k * double(elem_size(a.dy_dtype)) / 5e6 : 0) +
-                (p.tokens ? 0 : 3.5 + (t * n * double(elem_size(a.dy_dtype)) + t * k + 2 * t * ((wide ? 3 : 1) * n + k)) / 4.5e6);
-    return us < tiles_us;
+    const double slower = aligned ? 1 : wide ? 1.25 : 1.6;
+    double least = tiles_us + 4.3 + (p->splits == 1 ? n * k * double(elem_size(a.dy_dtype)) / 5e6 : 0) +
+                   (p->tokens ? 0 : 3.5 + (t * n * double(elem_size(a.dy_dtype)) + t * k + 2 * t * ((wide ? 3 : 1) * n + k)) / 4.5e6);
+    for (int64_t splits = 1; splits <= std::min(chunks, int64_t(32)); ++splits) {
+        const double per = double(blocks * splits) / 256;
+        if (splits > 1 && per > 4) break;
+        const double us = 4.2 + per * (wide ? 0.45 : 0.3) + double((chunks + splits - 1) / splits) * slower *
+                          ((wide ? 1.0 : 0.56) + std::max(0.0, per - 1) * (wide ? 0.56 : 0.26)) +
+                          (splits > 1 ? 3 + 0.08 * double(splits) + double(blocks * splits) * 0.008 : 0);
+        if (us < least) {
+            least = us;
+            p->tb = 4;
+            p->stages = int((chunks + splits - 1) / splits);
+        }
+    }
+    if (!p->tb) return;
+    p->splits = int((chunks + p->stages - 1) / p->stages);
+    Carve take;
+    if (p->splits > 1) p->off_part = take(uint64_t(blocks) * p->splits * 4096 * 4);
+    p->bytes = take.at;
 }
 
 MoF8Plan wgrad_plan(const MoF8Wgrad& a) {
@@ -255,8 +269,8 @@ MoF8Plan wgrad_plan(const MoF8Wgrad& a) {
         p.off_q[1] = take(uint64_t(a.dim) * p.ld_t * 2);
     }
     const double tiles_us = plan_tiles(&p, a.dim, a.rows, p.kd / 64, p.tokens ? kStageTokens : kStageBf16, a.dy_dtype == MO_BF16 ? 1 : 3, 1, &take);
-    if (wgrad_small(a, p, tiles_us)) p.tb = 4;
-    p.bytes = p.tb ? 0 : take.at;
+    p.bytes = take.at;
+    plan_small_wgrad(a, tiles_us, &p);
     return p;
 }
 
@@ -453,7 +467,7 @@ mo_status fp8_weight_grad(const void* dY, int64_t ld_dy, int32_t dy_dtype, const
     if (!take_workspace(workspace, workspace_bytes, p.bytes, &r, &ws)) return MO_ERR_WORKSPACE_TOO_SMALL;
     if (r.conflict()) return MO_ERR_ALIAS;
     if (p.tb) {
-        MO_RUN(MO_PHASE_F8_WGRAD, mo_launch_f8_small_wgrad(a, s));
+        MO_RUN(MO_PHASE_F8_WGRAD, mo_launch_f8_small_wgrad(a, p, ws, s));
         return MO_OK;
     }
     if (!p.tokens) MO_RUN(MO_PHASE_F8_PREP, mo_launch_f8_transpose(a, p, ws, s));

@@ -1,8 +1,9 @@
 // Products with matrices in 8 bits:
-//   Y = A B^T, both in 8 bits (bf16 results: fp8_gemm.h; fp32 results: the operands' values,
-//       which are bf16 numbers, through the bf16 GEMM), and
+//   Y = A B^T, both in 8 bits: in tiles (fp8_gemm.h; an fp32 result from the operands' values, which
+//       are bf16 numbers) or, small ones, in blocks straight from registers; and
 //   G = dY^T X, X an activation kept in 8 bits, dY as it is: X's values are bf16 numbers, an
-//       fp32 dY is three of them.
+//       fp32 dY is three of them.  In tiles, from the operands as they lie or from transposed
+//       copies, or, small ones, in blocks.
 // P, the operand with tiles of 256 rows, is the one along the result's columns: a lane's
 // four accumulators are then four neighbours of a row.
 #include "fp8_gemm.h"
@@ -366,20 +367,25 @@ template <> struct Source<uint8_t> {
 // parts), from where transposing reads make fragments of them, as in TOKENS (fp8_gemm.h).  Nothing is asked of
 // alignment, nothing is copied first, and several workgroups on a CU hide each other's waits; but every
 // operand is read out of LDS for 64 columns of the other alone, so large gradients go faster in tiles.  The
-// results turn in LDS, so that 16 lanes store 64 neighbours of a row.
+// results turn in LDS, so that 16 lanes store 64 neighbours of a row.  A workgroup alone takes 0.56 us for 64 tokens in
+// bf16 and 1.0 in fp32, bound by the wait from load to LDS to MFMA; several on a CU 0.26 and 0.56 each, bound by
+// LDS (and by cutting fp32 in parts).  257 tokens x 1000 x 2001 in fp32: 12.9 us with the call, 19.7 in tiles.  Few
+// blocks share a block's tokens among several workgroups (7803 x 16 x 16 in fp32: 14 us, 29 in tiles).
 template <typename T, typename TG>
 __global__ __launch_bounds__(256) void f8_small_wgrad_kernel(Source<uint8_t> x, Source<T> y, int64_t tokens, Out<TG> o, uint32_t bx,
-                                                             uint32_t by) {
+                                                             uint32_t by, int64_t per, float* part) {
 #ifdef __HIP_DEVICE_COMPILE__
     constexpr int PL = sizeof(T) == 4 ? 3 : 1, PLANE = 64 * 128, ROW = 68;   // ROW: floats of a row of results
     constexpr int BYTES = PLANE * (1 + PL) > 64 * ROW * 4 ? PLANE * (1 + PL) : 64 * ROW * 4;
     __shared__ __align__(16) uint8_t smem[BYTES];
     const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, kg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wp = wave & 1, wq = wave >> 1;
-    // each XCD a contiguous share of the blocks, the shorter side's side by side
+    // each XCD a contiguous share of the blocks, the shorter side's side by side; `per` tokens of a block at most
     const uint32_t share = gridDim.x >> 3, rem = gridDim.x & 7, xcd = blockIdx.x & 7;
-    const uint32_t block = xcd * share + (xcd < rem ? xcd : rem) + (blockIdx.x >> 3);
+    const uint32_t unit = xcd * share + (xcd < rem ? xcd : rem) + (blockIdx.x >> 3), block = unit % (bx * by);
     const int64_t p0 = int64_t(by < bx ? block / by : block % bx) * 64, q0 = int64_t(by < bx ? block % by : block / bx) * 64;
+    const int64_t from = int64_t(unit / (bx * by)) * per;
+    if (tokens > from + per) tokens = from + per;
     // a thread's eight columns, of tokens row and row + 32 of a chunk
     const int row = tid >> 3, c = tid & 7;
     const int np = int(o.cols - p0 - c * 8 < 8 ? o.cols - p0 - c * 8 : 8), nq = int(o.rows - q0 - c * 8 < 8 ? o.rows - q0 - c * 8 : 8);
@@ -461,8 +467,8 @@ __global__ __launch_bounds__(256) void f8_small_wgrad_kernel(Source<uint8_t> x, 
     for (int a = 0; a < 2; ++a)
 #pragma unroll
         for (int b = 0; b < 2; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-    load(0);
-    for (int64_t t0 = 0; t0 < tokens; t0 += 64) {
+    load(from);
+    for (int64_t t0 = from; t0 < tokens; t0 += 64) {
         store();
         __syncthreads();
         if (t0 + 64 < tokens) load(t0 + 64);
@@ -493,9 +499,29 @@ __global__ __launch_bounds__(256) void f8_small_wgrad_kernel(Source<uint8_t> x, 
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = i * 16 + (tid >> 4), k = (tid & 15) * 4;
-        put4(o, q0 + r, p0 + k, *reinterpret_cast<const f32x4*>(z + r * ROW + k));
+        const f32x4 v = *reinterpret_cast<const f32x4*>(z + r * ROW + k);
+        if (part) *reinterpret_cast<f32x4*>(part + int64_t(unit) * 4096 + r * 64 + k) = v;
+        else put4(o, q0 + r, p0 + k, v);
     }
 #endif
+}
+
+// The sums of the parts of each block's tokens, in order.
+template <typename TG>
+__global__ __launch_bounds__(256) void f8_small_sum_kernel(const float* part, uint32_t splits, uint32_t bx, uint32_t by, Out<TG> o) {
+    const uint32_t block = blockIdx.x >> 2;
+    const int at = (blockIdx.x & 3) * 1024 + threadIdx.x * 4;
+    const f32x4* z = reinterpret_cast<const f32x4*>(part + int64_t(block) * 4096 + at);
+    const int64_t stride = int64_t(bx * by) * 1024;
+    f32x4 s = z[0];
+#pragma unroll 8
+    for (uint32_t k = 1; k < splits; ++k) {
+        const f32x4 v = z[k * stride];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] += v[e];
+    }
+    const int64_t p0 = int64_t(by < bx ? block / by : block % bx) * 64, q0 = int64_t(by < bx ? block % by : block / bx) * 64;
+    put4(o, q0 + (at >> 6), p0 + (at & 63), s);
 }
 
 // dst[plane][c][ldt] <- src[r][c], zeros for rows from `rows` up to 64 tr.
@@ -659,17 +685,20 @@ hipError_t mo_launch_f8_transpose(const MoF8Wgrad& a, const MoF8Plan& p, uint8_t
 }
 
 template <typename T, typename TG>
-static hipError_t small_wgrad(const MoF8Wgrad& a, hipStream_t s) {
-    const uint32_t bx = uint32_t((a.dim + 63) / 64), by = uint32_t((a.rows + 63) / 64);
+static hipError_t small_wgrad(const MoF8Wgrad& a, const MoF8Plan& p, uint8_t* ws, hipStream_t s) {
+    const uint32_t bx = uint32_t((a.dim + 63) / 64), by = uint32_t((a.rows + 63) / 64), splits = uint32_t(p.splits);
     const Source<uint8_t> x = {a.X.q, a.X.ld, a.X.s, a.X.ld_s, a.X.inc};
     const Source<T> y = {static_cast<const T*>(a.dY), a.lddy};
     const Out<TG> o = {static_cast<TG*>(a.G), a.ldg, a.dim, a.rows, a.accumulate != 0};
-    hipLaunchKernelGGL((f8_small_wgrad_kernel<T, TG>), dim3(bx * by), dim3(256), 0, s, x, y, a.X.rows, o, bx, by);
+    float* part = splits > 1 ? reinterpret_cast<float*>(ws + p.off_part) : nullptr;
+    hipLaunchKernelGGL((f8_small_wgrad_kernel<T, TG>), dim3(bx * by * splits), dim3(256), 0, s, x, y, a.X.rows, o, bx, by,
+                       int64_t(p.stages) * 64, part);
+    if (part) hipLaunchKernelGGL(f8_small_sum_kernel<TG>, dim3(bx * by * 4), dim3(256), 0, s, part, splits, bx, by, o);
     return hipGetLastError();
 }
-hipError_t mo_launch_f8_small_wgrad(const MoF8Wgrad& a, hipStream_t s) {
-    if (a.dy_dtype == MO_BF16) return a.g_dtype == MO_BF16 ? small_wgrad<bf16_t, bf16_t>(a, s) : small_wgrad<bf16_t, float>(a, s);
-    return a.g_dtype == MO_BF16 ? small_wgrad<float, bf16_t>(a, s) : small_wgrad<float, float>(a, s);
+hipError_t mo_launch_f8_small_wgrad(const MoF8Wgrad& a, const MoF8Plan& p, uint8_t* ws, hipStream_t s) {
+    if (a.dy_dtype == MO_BF16) return a.g_dtype == MO_BF16 ? small_wgrad<bf16_t, bf16_t>(a, p, ws, s) : small_wgrad<bf16_t, float>(a, p, ws, s);
+    return a.g_dtype == MO_BF16 ? small_wgrad<float, bf16_t>(a, p, ws, s) : small_wgrad<float, float>(a, p, ws, s);
 }
 
 template <int KIND>

@@ -73,7 +73,8 @@ struct MoF8Wgrad {
 struct MoF8Plan {
     bool bf16;                  // through bf16 MFMA
     bool tokens;                // a weight gradient from the operands as they lie
-    int tb, rb;                 // tb > 0: a small product, 16 tb x 16 rb of it per workgroup, and nothing below
+    int tb, rb;                 // tb > 0: in small blocks, of a product 16 tb x 16 rb per workgroup and nothing below,
+                                // of a weight gradient 64 x 64, and of what follows `stages` (of 64 tokens), `splits`, off_part
     int nb;                     // tile width 64 nb along the operand without 256-row tiles
     int nk, stages, splits;     // K stages in all; those of a part and the parts of a tile behind the first `full`
     uint32_t tm, tn, full;
@@ -90,7 +91,7 @@ hipError_t mo_launch_f8_small(const MoF8Operand& A, const MoF8Operand& B, const 
 hipError_t mo_launch_f8_matmul(const MoF8Operand& A, const MoF8Operand& B, const MoF8Plan& p, int64_t dim, void* Y,
                                int64_t ldy, int32_t dtype, uint8_t* ws, hipStream_t s);
 hipError_t mo_launch_f8_transpose(const MoF8Wgrad& a, const MoF8Plan& p, uint8_t* ws, hipStream_t s);
-hipError_t mo_launch_f8_small_wgrad(const MoF8Wgrad& a, hipStream_t s);
+hipError_t mo_launch_f8_small_wgrad(const MoF8Wgrad& a, const MoF8Plan& p, uint8_t* ws, hipStream_t s);
 hipError_t mo_launch_f8_wgrad(const MoF8Wgrad& a, const MoF8Plan& p, uint8_t* ws, hipStream_t s);
 
 // ---- embedding -------------------------------------------------------------------

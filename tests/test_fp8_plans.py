@@ -36,7 +36,7 @@ def plans(tmp_path_factory):
             p["split"], p["many"] = int(p.pop("splits") > 1), int(p.pop("rounds") > 1)
             p["bytes"] = int(p["bytes"] > 0)
             if p.get("small"):
-                p = {k: p[k] for k in ("small", "planes", "bytes") if k in p}
+                p = {k: p[k] for k in ("small", "planes", "split", "bytes") if k in p and (k != "split" or "planes" in p)}
             got.append(p)
         return got
     return run

@@ -297,12 +297,13 @@ __device__ __forceinline__ void run_tiles(uint8_t* smem, const Operand8& P, cons
     const uint32_t vP = uint32_t(tid >> 4) * uint32_t(P.ld) + (tid & 15) * 16;
     const uint32_t vS = uint32_t(tid >> 4) * uint32_t(P.ld_s) + ((tid >> 3) & 1);
     const uint32_t vQ = uint32_t(tid / QCH) * uint32_t(Q.ld) + uint32_t(tid % QCH) * 16;
+    // (a row's whole offset is the vector one: the descriptor's range does not hold for a scalar offset)
     auto load_p = [&](int i) __attribute__((always_inline)) {
-        xq[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rP, vP, i * 32 * uint32_t(P.ld), 0));
-        xscale[i] = __builtin_amdgcn_raw_buffer_load_b8(rS, vS, i * 32 * uint32_t(P.ld_s), 0);
+        xq[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rP, vP + uint32_t(32 * i) * uint32_t(P.ld), 0, 0));
+        xscale[i] = __builtin_amdgcn_raw_buffer_load_b8(rS, vS + uint32_t(32 * i) * uint32_t(P.ld_s), 0, 0);
     };
     auto load_q = [&](int i) __attribute__((always_inline)) {
-        yq[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rQ, vQ, uint32_t(QR * i) * uint32_t(Q.ld), 0));
+        yq[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rQ, vQ + uint32_t(QR * i) * uint32_t(Q.ld), 0, 0));
     };
     auto store_p = [&](int slot, int i) __attribute__((always_inline)) {
         const int r = (tid >> 4) + 32 * i, g = tid & 15;

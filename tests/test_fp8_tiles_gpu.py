@@ -1,5 +1,6 @@
-"""The tiled kernels of the 8-bit products and weight gradients (fp8_layouts) on operands in wider buffers
-whose padding, and what lies right behind the last row, is NaN."""
+"""The tiled kernels of the 8-bit products and weight gradients (fp8_layouts) at what they are most
+likely to get wrong: NaN, infinities and NaN scales, the least and the largest scales, and operands in
+wider buffers whose padding, and what lies right behind the last row, is NaN."""
 import pytest
 import torch
 
@@ -78,6 +79,59 @@ def test_product(gpu, c):
     assert off <= (R.ut(dt) if dt == BF else 2e-6), off
 
 
+@pytest.mark.parametrize("c", PRODUCTS, ids=name)
+def test_product_bad_values(gpu, c):
+    """NaN in an element or a scale reaches its rows and columns alone; the others stay what they are."""
+    A, sa = operand(1, c.m, c.k, 1)
+    B, sb = operand(3, c.n, c.k, c.blk)
+    kb, r = sa.shape[1], c.blk
+    rows_a, rows_b = [0, c.m // 2, c.m - 1], [3, c.n - 1]
+    clean = []
+    for q, bad in ((A, rows_a + [5]), (B, rows_b + list(range(r * 1, min(2 * r, c.n)) if r > 1 else [40]))):
+        z = q.clone()
+        F.codes(z)[bad] = 0
+        clean.append((z, bad))
+    F.codes(A)[rows_a[0], c.k - 1] = 0x7F
+    F.codes(A)[rows_a[1], 0] = 0xFF
+    F.codes(A)[rows_a[2], c.k // 2] = 0x7F
+    F.codes(B)[rows_b[0], c.k - 1] = 0xFF
+    F.codes(B)[rows_b[1], 70] = 0x7F
+    F.codes(sa)[5, kb - 1] = 255
+    F.codes(sb)[1 if r > 1 else 40, 0] = 255
+    nan = torch.zeros((c.m, c.n), dtype=torch.bool, device="cuda")
+    nan[clean[0][1]] = True
+    nan[:, clean[1][1]] = True
+    Y = product(c, A, sa, B, sb)
+    assert torch.equal(torch.isnan(Y), nan)
+    F.codes(sa)[5, kb - 1] = 127
+    F.codes(sb)[1 if r > 1 else 40, 0] = 127
+    dt = F32 if c.f32 else BF
+    want, bound = F.matmul(clean[0][0], sa, clean[1][0], sb, 1, r, dt)
+    R.check(torch.where(nan, want, Y.double()), want, bound, "the others")
+
+
+@pytest.mark.parametrize("c", PRODUCTS, ids=name)
+def test_product_scales(gpu, c):
+    """Scales 2^-20 to 2^20 meet the right blocks; then the least of A's against large ones of B, and the
+    other way round.  Where values are taken as bf16 numbers, one below 2^-130 is rounded to a multiple of
+    2^-133 (bf16's last step; a value has four bits), so it is off by 2^-134 at most."""
+    dt = F32 if c.f32 else BF
+    A, sa = operand(1, c.m, c.k, 1)
+    B, sb = operand(3, c.n, c.k, c.blk)
+    g = gen(5)
+    draw = lambda s, lo, hi: F.codes(s).copy_(torch.randint(lo, hi, s.shape, generator=g, device="cuda"))
+    draw(sa, 107, 148), draw(sb, 107, 148)
+    R.check(product(c, A, sa, B, sb), *F.matmul(A, sa, B, sb, 1, c.blk, dt), "far apart")
+    for least, x, other, most, r in ((sa, A, B, sb, c.blk), (sb, B, A, sa, 1)):
+        a = F.codes(x)
+        a[(a & 0x7F) < 8] = 0
+        draw(least, 0, 3), draw(most, 225, 240)
+        Y, bound = F.matmul(A, sa, B, sb, 1, c.blk, dt)
+        off = 2.0 ** -134 * F.value(other, most, r).abs().sum(1)
+        bound = bound + (off if x is A else off[:, None]) * (1 + R.ut(dt))
+        R.check(product(c, A, sa, B, sb), Y, bound, "both ends")
+
+
 # ---- weight gradients -------------------------------------------------------------------
 
 def gradient(c, dY, q, s, dtype=F32, old=None):
@@ -108,3 +162,53 @@ def test_weight_grad(gpu, c):
     R.check(gradient(c, dY, q, s, BF, old), *F.wgrad(dY, q, s, BF, old), "G added")
 
 
+@pytest.mark.parametrize("c", WGRADS, ids=name)
+def test_weight_grad_bad_values(gpu, c):
+    """Infinities, NaN, float32's largest and NaN scales reach the sums they are in and no others, from the
+    first token and from the last."""
+    dY, q, s = gradient_inputs(c)
+    dY0, q0, t = dY.clone(), q.clone(), c.t
+    dY[t - 1, 3], dY[5, 7], dY[t - 1, c.n - 1] = float("inf"), float("nan"), -float("inf")
+    if c.f32:
+        dY[0, 11] = torch.finfo(F32).max
+    F.codes(q)[t - 1, 9] = 0x7F
+    F.codes(q)[0, c.k - 1] = 0xFF
+    F.codes(s)[2, 1] = 255
+    x = F.value(q, s)
+    want = dY.double().t() @ x
+    rows = [3, 7, c.n - 1] + ([11] if c.f32 else [])
+    cols = [9, c.k - 1] + list(range(128, 256))
+    G = gradient(c, dY, q, s)
+    assert torch.equal(torch.isnan(G), torch.isnan(want))
+    inf = torch.isinf(want) & (torch.arange(c.n, device="cuda") != 11)[:, None]
+    assert torch.equal(torch.isinf(G) & (torch.arange(c.n, device="cuda") != 11)[:, None], inf)
+    assert torch.equal(G.double()[inf], want[inf])
+    F.codes(s)[2, 1] = 127
+    good = torch.ones((c.n, c.k), dtype=torch.bool, device="cuda")
+    good[rows] = False
+    good[:, cols] = False
+    want, bound = F.wgrad(dY0, q0, s, F32)
+    R.check(torch.where(good, G.double(), want), want, bound, "the others")
+    if c.f32:   # what its three parts make up, where that does not overflow
+        dY0[0, 11] = torch.finfo(F32).max
+        want, bound = F.wgrad(dY0, q0, s, F32)
+        good[11] = want[11].abs() < torch.finfo(F32).max / 2
+        good[11, cols] = False
+        R.check(torch.where(good, G.double(), want)[11:12], want[11:12], bound[11:12], "float32's largest")
+
+
+@pytest.mark.parametrize("c", WGRADS, ids=name)
+def test_weight_grad_scales(gpu, c):
+    """Tokens' scales far apart, and those of 0 (2^-127); then the least alone, against a large dY."""
+    dY, q, s = gradient_inputs(c)
+    g = gen(11)
+    F.codes(s).copy_(torch.randint(107, 148, s.shape, generator=g, device="cuda"))
+    F.codes(s)[::7] = 0
+    R.check(gradient(c, dY, q, s), *F.wgrad(dY, q, s, F32), "far apart")
+    F.codes(s).copy_(torch.randint(0, 3, s.shape, generator=g, device="cuda"))
+    a = F.codes(q)
+    a[(a & 0x7F) < 8] = 0
+    dY = dY * 2.0 ** 110
+    want, bound = F.wgrad(dY, q, s, F32)
+    off = 2.0 ** -134 * dY.double().abs().sum(0)[:, None]
+    R.check(gradient(c, dY, q, s), want, bound + off, "the least")

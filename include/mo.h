@@ -593,8 +593,10 @@ mo_status fp8_weight_grad_workspace_bytes(const void* dY, int64_t ld_dy, int32_t
  * (X->rows tokens x rows, dy_dtype), X (tokens x dim, block_rows 1), G (rows x dim,
  * g_dtype), the G of an owner step.  Products are exact (X's values are fp8_dequantize's bf16 numbers, an fp32
  * dY is three of them), sums fp32, rounded once; with accumulate nonzero after one more
- * addition, of what G held.  With no tokens G is zeroed, or left as it is.  Errors as
- * fp8_matmul. */
+ * addition, of what G held.  With no tokens G is zeroed, or left as it is.  Errors:
+ * MO_ERR_INVALID_ARG (null pointer, negative size, bad stride, block_rows other than 1),
+ * MO_ERR_UNSUPPORTED (a dtype, tokens, rows or dim > 2^20, a stride over 2^26),
+ * MO_ERR_WORKSPACE_TOO_SMALL, MO_ERR_ALIAS, MO_ERR_HIP. */
 mo_status fp8_weight_grad(const void* dY, int64_t ld_dy, int32_t dy_dtype, const mo_fp8_matrix* X,
                           int64_t dim, void* G, int64_t ld_g, int32_t g_dtype, int64_t rows,
                           int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);

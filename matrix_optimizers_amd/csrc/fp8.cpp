@@ -129,19 +129,19 @@ bool s_in_place(const MoF8Operand& o, int64_t dim) {
 // the workgroups read.  Of 4 x 4 a CU holds one, and rounds are whole.
 struct SmallBlocks {
     int tb, rb, slots;
-    double start, own0, own, all0, all;
+    double start, own, all0, all;
     double us(int64_t p, int64_t q, double turns) const {
         const int64_t n = ((p + 16 * rb - 1) / (16 * rb)) * ((q + 16 * tb - 1) / (16 * tb));
         if (n >= int64_t(1) << 20) return 1e30;
         const double rounds = slots == 256 ? double((n + 255) / 256) : double(n) / slots;
         const double longer = 1 + std::min(0.4, 0.1 * std::max(0.0, turns - 4)) * (slots == 256 ? 0.5 : 1);
-        return start + std::max(own0 + own * turns, rounds * (all0 + all * turns * longer));
+        return start + std::max(own * turns, rounds * (all0 + all * turns * longer));
     }
 };
-constexpr SmallBlocks kSmall[] = {{1, 1, 512, 3.1, 0, 0.36, 1.07, 0.53},
-                                  {1, 2, 512, 3.1, 0, 0.48, 1.1, 0.95},
-                                  {2, 2, 512, 3.1, 0, 0.69, 1.35, 1.25},
-                                  {4, 4, 256, 1.5, 0, 0, 2.7, 1.85}};
+constexpr SmallBlocks kSmall[] = {{1, 1, 512, 3.1, 0.36, 1.07, 0.53},
+                                  {1, 2, 512, 3.1, 0.48, 1.1, 0.95},
+                                  {2, 2, 512, 3.1, 0.69, 1.35, 1.25},
+                                  {4, 4, 256, 1.5, 0, 2.7, 1.85}};
 
 // A product in small blocks, without a workspace and in one launch, where that takes less than in tiles.
 // The estimates come from these and others like them, us in tiles and in the small blocks of the first

@@ -570,9 +570,10 @@ mo_status fp8_matmul_workspace_bytes(const mo_fp8_matrix* A, const mo_fp8_matrix
                                      int32_t dtype, size_t* bytes);
 
 /* Y = A B^T: A (A->rows x dim), B (B->rows x dim), Y (A->rows x B->rows, dtype).  With
- * dim == 0, Y is zeroed.  A bf16 Y comes from 8-bit MFMA, which sums 128 products at a time
- * to about 2^-17 of the largest of them and these sums in fp32 (1.5e-5 of the result's
- * norm for normal data).  An fp32 Y comes from bf16 MFMA on the operands' values as
+ * dim == 0, Y is zeroed.  A bf16 Y comes from 8-bit MFMA, which takes 128 products at a time,
+ * each to about 2^-17 of the largest of them, and sums in fp32: 1.5e-5 of the result's norm for
+ * normal data, but where large products cancel, up to 128 times that of the largest is left
+ * (2^-13 of it, measured, in a block of one cancelling pair and 126 products of 2^-17).  An fp32 Y comes from bf16 MFMA on the operands' values as
  * fp8_dequantize makes them, with exact products and fp32 sums, at half the rate; so does a bf16
  * Y of larger products (small ones are in 8 bits whatever their alignment) whose operands are
  * neither aligned nor worth a copy.  Errors: MO_ERR_INVALID_ARG (null pointer,

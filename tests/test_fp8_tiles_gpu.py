@@ -132,6 +132,20 @@ def test_product_scales(gpu, c):
         R.check(product(c, A, sa, B, sb), Y, bound, "both ends")
 
 
+@pytest.mark.parametrize("m,n,k", [(64, 64, 128), (64, 200, 1024), (1030, 2600, 2048), (9000, 777, 2048)])
+def test_product_of_large_terms_that_cancel(gpu, m, n, k):
+    """Two products in each block that are 2^17 times the others and cancel: each of a block's products is kept to
+    about 2^-17 of its largest for a bf16 result (fp8_ref's bound takes 2^-16), and exactly for an fp32 one."""
+    A, B = (rand(gen(s), (r, k), F32) for s, r in ((21, m), (22, n)))
+    for b in range(0, k, 128):
+        A[:, b + 5], A[:, b + 100], B[:, b + 5], B[:, b + 100] = 448, -448, 448, 448
+    A, B = A.to(F.FP8), B.to(F.FP8)
+    sa, sb = (torch.full((r, k // 128), 127, dtype=torch.uint8, device="cuda").view(F.SCALE) for r in (m, n))
+    for dt in (BF, F32):
+        want, bound = F.matmul(A, sa, B, sb, 1, 1, dt)
+        R.check(mo.fp8_matmul(A, sa, B, sb, dtype=dt), want, bound, str(dt))
+
+
 # ---- weight gradients -------------------------------------------------------------------
 
 def gradient(c, dY, q, s, dtype=F32, old=None):

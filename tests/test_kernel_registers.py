@@ -43,3 +43,10 @@ def test_nothing_is_spilled(assembly, src):
     bad = [k for k in kernels(assembly[src]) if k[1] or k[2]]
     assert not bad, bad
 
+
+def test_stores_past_the_caches_leave_whole_lines(assembly):
+    """Only bf16 results of the way back from 8 bits: a lane has two stores of fp32 and one of bf16, so that fp32's
+    leave every other 16 bytes of a line to the next one."""
+    bodies = re.findall(r"^(\w+):.*?\n(.*?)\n\s*s_endpgm", assembly["fp8_cast.hip"], re.M | re.S)
+    past = {name for name, body in bodies if re.search(r"global_store_\w+ .*\bnt\b", body)}
+    assert len(bodies) >= 6 and len(past) == 1 and all("dequantize" in n and "IDF16b" in n for n in past), past

@@ -30,7 +30,10 @@ mo_status ln_shape(int64_t rows, int64_t cols, int32_t dtype) {
 
 uint64_t ln_bwd_bytes(int64_t rows, int64_t cols) { return uint64_t(mo_ln_bwd_parts(rows, cols)) * 2 * cols * 4; }
 
-uint64_t rms_bwd_bytes(int64_t rows, int64_t cols) { return uint64_t(mo_rms_bwd_parts(rows, cols)) * cols * 4; }
+// (the query does not know the type: the more of both)
+uint64_t rms_bwd_bytes(int64_t rows, int64_t cols) {
+    return uint64_t(std::max(mo_rms_bwd_parts(rows, cols, MO_BF16), mo_rms_bwd_parts(rows, cols, MO_F32))) * cols * 4;
+}
 
 // ---- embedding -------------------------------------------------------------------
 

@@ -38,7 +38,7 @@ struct MoRmsArgs {
     float eps;
 };
 // Partial rows (each cols fp32) the backward pass leaves for the reduction.
-int mo_rms_bwd_parts(int64_t rows, int64_t cols);
+int mo_rms_bwd_parts(int64_t rows, int64_t cols, int32_t dtype);
 hipError_t mo_launch_rms_fwd(const MoRmsArgs& a, hipStream_t s);
 hipError_t mo_launch_rms_bwd(const MoRmsArgs& a, float* part, hipStream_t s);
 hipError_t mo_launch_rms_reduce(const MoRmsArgs& a, const float* part, hipStream_t s);

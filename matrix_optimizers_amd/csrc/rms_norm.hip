@@ -322,11 +322,14 @@ unsigned fwd_wgs(int64_t rows, const Shape& sh) {
     return wgs_for(rows, sh, sh.W <= 64 ? 16 : sh.threads <= 512 ? 1 << 12 : 2048 / sh.threads);
 }
 // Backward, each workgroup leaves a partial row of 4 bytes per column: as few per CU as keep the loads
-// going.  us at 16384 rows of 1024, 2048, 4096 and 8192 columns: 41.6, 57.8, 105 and 198.5 (4.6 to 5.4 TB/s), with
-// half as many workgroups per CU 43 (three), 64.7, 117, -, with twice as many 69, 73, 120, 210.
-int bwd_per_cu(const Shape& sh) {
+// going.  bf16, us at 16384 rows of 1024, 2048, 4096 and 8192 columns with dH: 41.6, 57.8, 105 and 198.5 (4.6 to 5.4
+// TB/s), with half as many workgroups per CU 43 (three), 64.7, 117, -, with twice as many 69, 73, 120, 210.  Rows of two
+// chunks leave a CU with five to seven wavefronts where they are short of 8192 columns: two of them in bf16
+// (4104, 5000 and 7168 columns 111, 131 and 186, one alone 142, 160 and 189), one in fp32, which has twice the bytes
+// under way (209, 257 and 363; 201, 244 and 337).
+int bwd_per_cu(const Shape& sh, bool bf16) {
     if (sh.W <= 64) return 2;
-    return sh.threads <= 128 ? 4 : sh.threads <= 256 ? 3 : sh.threads <= 512 && sh.R == 1 ? 2 : 1;
+    return sh.threads <= 128 ? 4 : sh.threads <= 256 ? 3 : sh.threads <= (sh.R == 1 ? 512 : bf16 ? 448 : 0) ? 2 : 1;
 }
 
 template <typename T, bool FULL, bool RES>
@@ -374,11 +377,11 @@ hipError_t bwd(const MoRmsArgs& a, float* part, int n_part, hipStream_t s) {
 
 }  // namespace
 
-int mo_rms_bwd_parts(int64_t rows, int64_t cols) {
+int mo_rms_bwd_parts(int64_t rows, int64_t cols, int32_t dtype) {
     if (rows == 0) return 0;
     if (cols > MAX_COLS) return int(rows < 64 ? rows : 64);
     const Shape sh = shape_of(cols);
-    return int(wgs_for(rows, sh, bwd_per_cu(sh)));
+    return int(wgs_for(rows, sh, bwd_per_cu(sh, dtype == MO_BF16)));
 }
 
 hipError_t mo_launch_rms_fwd(const MoRmsArgs& a, hipStream_t s) {
@@ -388,12 +391,12 @@ hipError_t mo_launch_rms_fwd(const MoRmsArgs& a, hipStream_t s) {
 #undef MO_RMS_T
 }
 hipError_t mo_launch_rms_bwd(const MoRmsArgs& a, float* part, hipStream_t s) {
-    const int n = mo_rms_bwd_parts(a.rows, a.cols);
+    const int n = mo_rms_bwd_parts(a.rows, a.cols, a.dtype);
     if (a.cols % 8 == 0) return a.dtype == MO_BF16 ? bwd<bf16_t, true>(a, part, n, s) : bwd<float, true>(a, part, n, s);
     return a.dtype == MO_BF16 ? bwd<bf16_t, false>(a, part, n, s) : bwd<float, false>(a, part, n, s);
 }
 hipError_t mo_launch_rms_reduce(const MoRmsArgs& a, const float* part, hipStream_t s) {
     hipLaunchKernelGGL(rms_reduce_kernel, dim3(unsigned((a.cols + 31) / 32)), dim3(1024), 0, s, part,
-                       mo_rms_bwd_parts(a.rows, a.cols), a.dweight, int(a.cols));
+                       mo_rms_bwd_parts(a.rows, a.cols, a.dtype), a.dweight, int(a.cols));
     return hipGetLastError();
 }

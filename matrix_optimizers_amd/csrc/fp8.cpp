@@ -67,8 +67,8 @@ constexpr StageTimes kStage8 = {{1.5, 0.85, 0.6}}, kStageValues = {{1.5, 1.0, 0.
 // Estimated us of a product in `tiles` tiles with `stages` stages of `stage` us on 256 CUs.  The rounds that
 // fill them take a tile's K whole; the tiles left over are split into the parts (multiples of `unit` stages)
 // that take the least.  The parts' fp32 sums are written, read and added by a second launch.  Of 15
-// products between 64 x 4096 x 4096 and 4096 x 4096 x 4096 with each kind of operands, the choice is
-// the best of all widths and up to 16 parts in most, and within 14 % of it in all.
+// products from 40 x 28672 x 8192 to 4096 x 4096 x 4096 in both result types, the choice is within 5 % of the best of
+// all widths and up to 16 parts in most, and within 12 % of it in all.
 double product_us(int64_t tiles, int64_t stages, double stage, int nb, int unit, int64_t* full, int64_t* splits) {
     const int64_t rem = tiles % 256;
     const double whole = double(tiles / 256 * stages) * stage;
@@ -144,15 +144,17 @@ constexpr SmallBlocks kSmall[] = {{1, 1, 512, 3.1, 0.36, 1.07, 0.53},
                                   {4, 4, 256, 1.5, 0, 2.7, 1.85}};
 
 // A product in small blocks, without a workspace and in one launch, where that takes less than in tiles.
-// The estimates come from these and others like them, us in tiles and in the small blocks of the first
-// to last kind above, bf16 results: 16 tokens x 4096 x 4096 13.5, 4.6 5.3 6.3 10.5; 64 x 4096 x 4096 13.9, 9.0 7.5
-// 6.6 10.5; 64 x 14336 x 4096 18.9, 26.8 20.8 17.4 16.1; 18 x 1792 x 12672 22.6, 7.6 9.3 11.8 21.9; 512 x
-// 2048 x 2048 14.6, 20.2 13.3 10.1 7.9; 512 x 4096 x 4096 22.7, 51.9 39.5 28.5 21.1; 2048 x 2048 x 256 7.7,
-// 42.5 26.4 17.2 14.2; 700 x 1500 x 8320 25.3, 62 47.7 37.9 34.9.  Of 27 products of 40 x 28672 x 8192 to 2048 x 2048
-// x 8192 in both types the choice is within 18 % of the best of all, of most the best.  fp32 results take 1.15 of the time in either, and rows that are not 16-byte
-// aligned 1.4 in small blocks (1021 x 2001 x 1000 21.6, 17.7; x 1024 19.1, 12.7).
+// The estimates come from these and others like them, us of the kernels in tiles and in the small blocks of the
+// first to last kind above, bf16 results: 16 tokens x 4096 x 4096 16.0, 5.0 5.7 6.7 11.1; 64 x 4096 x 4096 16.9, 10.6
+// 8.8 7.6 11.7; 64 x 14336 x 4096 20.1, 26.2 21.5 17.7 16.0; 18 x 1792 x 12672 19.9, 8.8 10.2 12.6 22.8; 512 x 2048
+// x 2048 14.5, 20.9 14.5 11.2 8.8; 512 x 4096 x 4096 23.6, 54.3 41.6 31.3 23.4; 2048 x 2048 x 256 10.5, 41.8 26.1 17.6
+// 14.9; 700 x 1500 x 8320 28.8, 61.0 45.8 37.9 36.4.  Of 15 products from 40 x 28672 x 8192 to 4096 x 4096 x 4096 in both
+// types the choice is within 12 % of the best of all, of most the best; of 150 drawn ones it takes 1.03 of the best
+// kind's time in the mean.  fp32 results take 1.15 of the time in either, and rows that are not 16-byte aligned 1.4
+// in small blocks (1021 x 2001 x 1000 in tiles and in blocks of the last kind 21.7, 18.1; x 1024 19.0, 13.6).
 bool plan_small(MoF8Plan* plan, const MoF8Operand& A, const MoF8Operand& B, int64_t dim, int32_t dtype, double tiles_us) {
-    const bool aligned = ((reinterpret_cast<uintptr_t>(A.q) | uintptr_t(A.ld) | reinterpret_cast<uintptr_t>(B.q) | uintptr_t(B.ld)) & 15) == 0;
+    const uintptr_t rows_at = reinterpret_cast<uintptr_t>(A.q) | uintptr_t(A.ld) | reinterpret_cast<uintptr_t>(B.q) | uintptr_t(B.ld);
+    const bool aligned = (rows_at & 15) == 0;
     const double turns = double(blocks_of(dim)) / 8, slower = (dtype == MO_F32 ? 1.15 : 1.0) * (aligned ? 1.0 : 1.4);
     const double read = double(A.rows + B.rows) * double(dim) / 5.2e6;
     double least = tiles_us;
@@ -223,19 +225,21 @@ bool tokens_in_place(const MoF8Wgrad& a) {
 // with a launch, the results that nothing hides, and a launch that transposes): a workgroup alone on
 // its CU has its own time for 64 tokens, each further one adds to it; few blocks share a long K's tokens among up to
 // 32 workgroups each, whose fp32 sums a second launch adds.  (G's type is not known to the workspace's query: dY's
-// stands for it.)  us in blocks and in tiles: dY and G in bf16, 98 tokens x 281 x 9600 6.5, 12.2; 1021 x 1024 x
-// 1024 13.2, 19.2; 64 x 4096 x 4096 14.1, 13.9; 512 x 4096 x 4096 40, 27; both in fp32, 206 x 5632 x 256 10.2, 21.1;
-// 257 x 1000 x 2001 14.6, 20.4; 721 x 9344 x 16 19.9, 37.7; 512 x 4096 x 4096 84, 62.
+// stands for it.)  us of the kernels in blocks and in tiles: dY and G in bf16, 98 tokens x 281 x 9600 7.2, 12.8; 1021 x
+// 1024 x 1024 14.0, 18.9; 64 x 4096 x 4096 14.2, 13.7; 512 x 4096 x 4096 40.8, 27.0; both in fp32, 206 x 5632 x 256
+// 10.3, 21.8; 257 x 1000 x 2001 14.7, 20.5; 721 x 9344 x 16 18.5, 37.2; 512 x 4096 x 4096 78.8, 60.8.
 void plan_small_wgrad(const MoF8Wgrad& a, double tiles_us, MoF8Plan* p) {
     const bool wide = a.dy_dtype == MO_F32;
     const double t = double(a.X.rows), n = double(a.rows), k = double(a.dim);
     const int64_t blocks = ((a.rows + 63) / 64) * ((a.dim + 63) / 64), chunks = (a.X.rows + 63) / 64;
     if (blocks >= int64_t(1) << 18) return;
-    // rows of dY that are not 16-byte aligned touch more lines (bf16, 1627 x 5147 x 384 35, 29; 2766 x 10607 x 411 131, 63)
+    // rows of dY that are not 16-byte aligned touch more lines (bf16, 1627 x 5147 x 384 37.7, 30.7; 2766 x
+    // 10607 x 411 129, 63)
     const bool aligned = ((reinterpret_cast<uintptr_t>(a.dY) | uintptr_t(a.lddy * elem_size(a.dy_dtype))) & 15) == 0;
     const double slower = aligned ? 1 : wide ? 1.25 : 1.6;
     double least = tiles_us + 4.3 + (p->splits == 1 ? n * k * double(elem_size(a.dy_dtype)) / 5e6 : 0) +
-                   (p->tokens ? 0 : 3.5 + (t * n * double(elem_size(a.dy_dtype)) + t * k + 2 * t * ((wide ? 3 : 1) * n + k)) / 4.5e6);
+                   (p->tokens ? 0
+                              : 3.5 + (t * n * double(elem_size(a.dy_dtype)) + t * k + 2 * t * ((wide ? 3 : 1) * n + k)) / 4.5e6);
     for (int64_t splits = 1; splits <= std::min(chunks, int64_t(32)); ++splits) {
         const double per = double(blocks * splits) / 256;
         if (splits > 1 && per > 4) break;
@@ -268,7 +272,8 @@ MoF8Plan wgrad_plan(const MoF8Wgrad& a) {
         p.off_q[0] = take(uint64_t(planes) * a.rows * p.ld_t * 2);
         p.off_q[1] = take(uint64_t(a.dim) * p.ld_t * 2);
     }
-    const double tiles_us = plan_tiles(&p, a.dim, a.rows, p.kd / 64, p.tokens ? kStageTokens : kStageBf16, a.dy_dtype == MO_BF16 ? 1 : 3, 1, &take);
+    const double tiles_us = plan_tiles(&p, a.dim, a.rows, p.kd / 64, p.tokens ? kStageTokens : kStageBf16,
+                                       a.dy_dtype == MO_BF16 ? 1 : 3, 1, &take);
     p.bytes = take.at;
     plan_small_wgrad(a, tiles_us, &p);
     return p;

@@ -11,7 +11,7 @@
 // A product whose result is fp32 is therefore not taken in 8 bits, but with the operands' values,
 // whose products are exact in bf16 MFMA: VALUES8 brings 64 elements of K at a time through
 // registers, where they are converted on their way to LDS.  It asks nothing of alignment, and takes
-// the bf16 results of operands that cannot be loaded straight to LDS as well.
+// the bf16 results of operands that cannot be loaded straight to LDS and are not worth a copy as well.
 //
 // Tiles, LDS rows of 128 bytes and their swizzle are those of the head's GEMM (head_gemm.h): a
 // stage of 128 bytes per row is 64 elements of K in bf16, 128 in 8 bits, one block.  A lane's 32
@@ -33,11 +33,12 @@
 // next tile's products.  16384 x 14336 x 4096 in 8 bits, one tile per workgroup: 845 us, of which 125
 // were the stores that nothing hid.
 //
-// 16384 x 14336 x 4096 takes 735 to 796 us in 8 bits (2420 to 2620 TFLOP/s) and 1530 to 1625 as a weight
-// gradient of 16384 tokens, by card: the power limit holds the clock at 1.76 and 2.0 GHz with MFMAs in
-// 60 and 53 % of the cycles; fp32 results 1530.  What lies beside the stages (1.4 us of 256 x 256 in 8 bits) is 8
-// us a tile, most of it 128 KB of results per CU at HBM's rate.  Workgroups started 2 to 4 us apart, so
-// that they would not store together, took as long.
+// 16384 x 14336 x 4096 takes 735 to 796 us in 8 bits (2420 to 2620 TFLOP/s), where a library product of the same
+// numbers with one scale each takes 630 to 690, and 1514 to 1625 as a weight gradient (the library's bf16 product along
+// the tokens 1850 to 1960), by card: the clock is held at 1.76 and 2.0 GHz with MFMAs in 60 and 53 % of the cycles;
+// fp32 results 1530 to 1564.  What lies beside the stages (1.4 us of 256 x 256 in 8 bits) is 8 us a tile, most of it
+// 128 KB of results per CU at HBM's rate.  Workgroups started 2 to 4 us apart, so that they would not store together,
+// took as long.
 #pragma once
 
 #include "fp8.h"
@@ -174,7 +175,9 @@ __device__ __forceinline__ void run_tiles(uint8_t* smem, const Operand8& P, cons
     constexpr int QROW = TN * 2, QCH = QROW / 16;   // TOKENS: bytes and 16-byte chunks of a row of Q in a stage
     // TOKENS: how row r's granules of 16 columns are permuted (Q's rows of 64 columns: two rows share the banks)
     auto pf = [&](int r) __attribute__((always_inline)) { return (r & 3) | (((r >> 1) ^ (r >> 2)) & 4); };
-    auto qf = [&](int r) __attribute__((always_inline)) { return NB == 1 ? ((r >> 1) & 1) | (((r >> 2) ^ (r >> 3)) & 2) : pf(r); };
+    auto qf = [&](int r) __attribute__((always_inline)) {
+        return NB == 1 ? ((r >> 1) & 1) | (((r >> 2) ^ (r >> 3)) & 2) : pf(r);
+    };
     int ls = 0, lseg = 0, koff = 0, lgroup = 0;   // stage of the item, plane, byte offset, group of scales
     uint32_t vo[LS];
     auto rP = rsrc(P.q), rQ = rsrc(Q.q);
@@ -269,7 +272,8 @@ __device__ __forceinline__ void run_tiles(uint8_t* smem, const Operand8& P, cons
 #pragma unroll
             for (int i = 0; i < SI; ++i)
                 if ((wave + 8 * i) * 64 < SROWS) {
-                    __builtin_amdgcn_global_load_lds(sg[i], (lds_void_t*)(sl + (lgroup & 3) * (SROWS * 4) + (wave + 8 * i) * 256), 4, 0, 0);
+                    __builtin_amdgcn_global_load_lds(sg[i], (lds_void_t*)(sl + (lgroup & 3) * (SROWS * 4) + (wave + 8 * i) * 256),
+                                                     4, 0, 0);
                     sg[i] += 4;
                 }
             ++lgroup;
@@ -299,11 +303,13 @@ __device__ __forceinline__ void run_tiles(uint8_t* smem, const Operand8& P, cons
     const uint32_t vQ = uint32_t(tid / QCH) * uint32_t(Q.ld) + uint32_t(tid % QCH) * 16;
     // (a row's whole offset is the vector one: the descriptor's range does not hold for a scalar offset)
     auto load_p = [&](int i) __attribute__((always_inline)) {
-        xq[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rP, vP + uint32_t(32 * i) * uint32_t(P.ld), 0, 0));
+        xq[i] = __builtin_bit_cast(
+            u32x4, __builtin_amdgcn_raw_buffer_load_b128(rP, vP + uint32_t(32 * i) * uint32_t(P.ld), 0, 0));
         xscale[i] = __builtin_amdgcn_raw_buffer_load_b8(rS, vS + uint32_t(32 * i) * uint32_t(P.ld_s), 0, 0);
     };
     auto load_q = [&](int i) __attribute__((always_inline)) {
-        yq[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rQ, vQ + uint32_t(QR * i) * uint32_t(Q.ld), 0, 0));
+        yq[i] = __builtin_bit_cast(
+            u32x4, __builtin_amdgcn_raw_buffer_load_b128(rQ, vQ + uint32_t(QR * i) * uint32_t(Q.ld), 0, 0));
     };
     auto store_p = [&](int slot, int i) __attribute__((always_inline)) {
         const int r = (tid >> 4) + 32 * i, g = tid & 15;

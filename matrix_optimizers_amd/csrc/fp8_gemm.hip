@@ -113,7 +113,8 @@ __global__ __launch_bounds__(256) void f8_sum_kernel(Tiles t, Out<T> o) {
     const uint32_t a = unit % L::MB, wave = unit / L::MB % 8, slot = unit / (L::MB * 8);
     if (slot >= t.rem) return;
     const int64_t stride = 8 * (L::MB * L::NBW * 64);
-    const f32x4* z = t.part + int64_t(slot) * t.splits * stride + int64_t(wave) * (L::MB * L::NBW * 64) + a * (L::NBW * 64) + lane;
+    const f32x4* z =
+        t.part + int64_t(slot) * t.splits * stride + int64_t(wave) * (L::MB * L::NBW * 64) + a * (L::NBW * 64) + lane;
     f32x4 s[L::NBW];
 #pragma unroll
     for (int b = 0; b < L::NBW; ++b) s[b] = z[b * 64];
@@ -369,11 +370,11 @@ template <> struct Source<uint8_t> {
 // operand is read out of LDS for 64 columns of the other alone, so large gradients go faster in tiles.  The
 // results turn in LDS, so that 16 lanes store 64 neighbours of a row.  A workgroup alone takes 0.56 us for 64 tokens in
 // bf16 and 1.0 in fp32, bound by the wait from load to LDS to MFMA; several on a CU 0.26 and 0.56 each, bound by
-// LDS (and by cutting fp32 in parts).  257 tokens x 1000 x 2001 in fp32: 12.9 us with the call, 19.7 in tiles.  Few
-// blocks share a block's tokens among several workgroups (7803 x 16 x 16 in fp32: 14 us, 29 in tiles).
+// LDS (and by cutting fp32 in parts).  257 tokens x 1000 x 2001 in fp32: 13.1 us with the call, 20 in tiles.  Few
+// blocks share a block's tokens among several workgroups (7803 x 16 x 16 in fp32: 14 us, 30 in tiles).
 template <typename T, typename TG>
-__global__ __launch_bounds__(256) void f8_small_wgrad_kernel(Source<uint8_t> x, Source<T> y, int64_t tokens, Out<TG> o, uint32_t bx,
-                                                             uint32_t by, int64_t per, float* part) {
+__global__ __launch_bounds__(256) void f8_small_wgrad_kernel(Source<uint8_t> x, Source<T> y, int64_t tokens, Out<TG> o,
+                                                             uint32_t bx, uint32_t by, int64_t per, float* part) {
 #ifdef __HIP_DEVICE_COMPILE__
     constexpr int PL = sizeof(T) == 4 ? 3 : 1, PLANE = 64 * 128, ROW = 68;   // ROW: floats of a row of results
     constexpr int BYTES = PLANE * (1 + PL) > 64 * ROW * 4 ? PLANE * (1 + PL) : 64 * ROW * 4;
@@ -388,7 +389,8 @@ __global__ __launch_bounds__(256) void f8_small_wgrad_kernel(Source<uint8_t> x, 
     if (tokens > from + per) tokens = from + per;
     // a thread's eight columns, of tokens row and row + 32 of a chunk
     const int row = tid >> 3, c = tid & 7;
-    const int np = int(o.cols - p0 - c * 8 < 8 ? o.cols - p0 - c * 8 : 8), nq = int(o.rows - q0 - c * 8 < 8 ? o.rows - q0 - c * 8 : 8);
+    const int np = int(o.cols - p0 - c * 8 < 8 ? o.cols - p0 - c * 8 : 8);
+    const int nq = int(o.rows - q0 - c * 8 < 8 ? o.rows - q0 - c * 8 : 8);
     const uint8_t* const xp = x.p + p0 + c * 8;
     const uint8_t* const xs = x.s + (p0 >> 7) * x.inc;
     const T* const yp = y.p + q0 + c * 8;
@@ -441,7 +443,8 @@ __global__ __launch_bounds__(256) void f8_small_wgrad_kernel(Source<uint8_t> x, 
                 for (int k = 0; k < 3; ++k) {
                     u32x4 u;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) u[e] = __builtin_amdgcn_perm(z[k][2 * e + 1], z[k][2 * e], 0x07060302);   // the upper halves
+                    for (int e = 0; e < 4; ++e)   // the upper halves
+                        u[e] = __builtin_amdgcn_perm(z[k][2 * e + 1], z[k][2 * e], 0x07060302);
                     put_row(smem + (1 + k) * PLANE, r, u);
                 }
             }
@@ -508,7 +511,8 @@ __global__ __launch_bounds__(256) void f8_small_wgrad_kernel(Source<uint8_t> x, 
 
 // The sums of the parts of each block's tokens, in order.
 template <typename TG>
-__global__ __launch_bounds__(256) void f8_small_sum_kernel(const float* part, uint32_t splits, uint32_t bx, uint32_t by, Out<TG> o) {
+__global__ __launch_bounds__(256) void f8_small_sum_kernel(const float* part, uint32_t splits, uint32_t bx, uint32_t by,
+                                                           Out<TG> o) {
     const uint32_t block = blockIdx.x >> 2;
     const int at = (blockIdx.x & 3) * 1024 + threadIdx.x * 4;
     const f32x4* z = reinterpret_cast<const f32x4*>(part + int64_t(block) * 4096 + at);
@@ -617,7 +621,8 @@ hipError_t product_nb(const Operand8& P, const Operand8& Q, const MoF8Plan& p, c
 }  // namespace
 
 // The rows of both operands of the product, or of the one that is not in place.
-hipError_t mo_launch_f8_copy(const MoF8Operand& a, const MoF8Operand& b, const MoF8Plan& p, int64_t dim, uint8_t* ws, hipStream_t s) {
+hipError_t mo_launch_f8_copy(const MoF8Operand& a, const MoF8Operand& b, const MoF8Plan& p, int64_t dim, uint8_t* ws,
+                             hipStream_t s) {
     const CopyRows x = {a.q, a.ld, p.pack_q[0] ? a.rows : 0, ws + p.off_q[0]};
     const CopyRows y = {b.q, b.ld, p.pack_q[1] ? b.rows : 0, ws + p.off_q[1]};
     hipLaunchKernelGGL(f8_copy_rows_kernel, dim3(grid_for((x.rows + y.rows) * 64)), dim3(256), 0, s, x, y, int(dim), p.ld_q);
@@ -697,7 +702,8 @@ static hipError_t small_wgrad(const MoF8Wgrad& a, const MoF8Plan& p, uint8_t* ws
     return hipGetLastError();
 }
 hipError_t mo_launch_f8_small_wgrad(const MoF8Wgrad& a, const MoF8Plan& p, uint8_t* ws, hipStream_t s) {
-    if (a.dy_dtype == MO_BF16) return a.g_dtype == MO_BF16 ? small_wgrad<bf16_t, bf16_t>(a, p, ws, s) : small_wgrad<bf16_t, float>(a, p, ws, s);
+    if (a.dy_dtype == MO_BF16)
+        return a.g_dtype == MO_BF16 ? small_wgrad<bf16_t, bf16_t>(a, p, ws, s) : small_wgrad<bf16_t, float>(a, p, ws, s);
     return a.g_dtype == MO_BF16 ? small_wgrad<float, bf16_t>(a, p, ws, s) : small_wgrad<float, float>(a, p, ws, s);
 }
 

@@ -145,7 +145,8 @@ def fp8_matmul(A, a_scales, B, b_scales, *, dtype=torch.bfloat16, out=None, work
 
 def _wgrad_bytes(dY, ldy, ycode, x, dim, rows) -> int:
     out = ctypes.c_size_t(0)
-    _check(load_library().fp8_weight_grad_workspace_bytes(_ptr(dY), ldy, ycode, x, dim, rows, out), "fp8_weight_grad_workspace_bytes")
+    _check(load_library().fp8_weight_grad_workspace_bytes(_ptr(dY), ldy, ycode, x, dim, rows, out),
+           "fp8_weight_grad_workspace_bytes")
     return int(out.value)
 
 

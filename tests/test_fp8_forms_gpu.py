@@ -96,3 +96,25 @@ def test_rms_norm_backward_forms(gpu, rows, cols, dtype):
     for other in (None, dh):
         none, dw2 = mo.rms_norm_backward(dy, x, r, w, dH=other, need_dX=False)
         assert none is None and torch.equal(dw2, dw)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("cols", [100, 1000, 8192, 16400])
+def test_rms_norm_rows_out_of_range(gpu, dtype, cols):
+    """Squares are fp32: a row whose sum of squares overflows has r and y 0; with eps 0 a row of zeros, or of values
+    whose squares underflow, has an infinite r.  The rows beside them are as alone."""
+    x = rand(gen(cols), (5, cols), dtype)
+    good = x.clone()
+    x[1, 3], x[2], x[3] = 1e30, 0, 1e-30
+    for eps in (1e-6, 0.0):
+        y, _, r = mo.rms_norm_forward(x, eps=eps)
+        q, s, _, r8 = mo.rms_norm_quantize(x, eps=eps)
+        assert torch.equal(r, r8)
+        want = mo.rms_norm_forward(good, eps=eps)
+        for i in (0, 4):
+            assert torch.equal(y[i], want[0][i]) and torch.equal(r[i], want[2][i])
+        assert float(r[1]) == 0 and bool((y[1] == 0).all()) and bool((q[1].float() == 0).all())
+        if eps:   # (1000 to a few roundings of 2^-24: 3e-4)
+            assert bool((y[2] == 0).all()) and bool(((r[2:4] - 1e3).abs() <= 1e-3).all())
+        else:
+            assert bool(torch.isinf(r[2:4]).all()) and bool(torch.isnan(y[2]).all()) and bool(torch.isnan(q[2].float()).all())

@@ -145,13 +145,13 @@ constexpr SmallBlocks kSmall[] = {{1, 1, 512, 3.1, 0.36, 1.07, 0.53},
 
 // A product in small blocks, without a workspace and in one launch, where that takes less than in tiles.
 // The estimates come from these and others like them, us of the kernels in tiles and in the small blocks of the
-// first to last kind above, bf16 results: 16 tokens x 4096 x 4096 16.0, 5.0 5.7 6.7 11.1; 64 x 4096 x 4096 16.9, 10.6
-// 8.8 7.6 11.7; 64 x 14336 x 4096 20.1, 26.2 21.5 17.7 16.0; 18 x 1792 x 12672 19.9, 8.8 10.2 12.6 22.8; 512 x 2048
-// x 2048 14.5, 20.9 14.5 11.2 8.8; 512 x 4096 x 4096 23.6, 54.3 41.6 31.3 23.4; 2048 x 2048 x 256 10.5, 41.8 26.1 17.6
-// 14.9; 700 x 1500 x 8320 28.8, 61.0 45.8 37.9 36.4.  Of 15 products from 40 x 28672 x 8192 to 4096 x 4096 x 4096 in both
+// first to last kind above, bf16 results: 16 tokens x 4096 x 4096 16.1, 4.8 5.4 6.4 10.7; 64 x 4096 x 4096 16.1, 9.8
+// 8.1 7.2 11.7; 64 x 14336 x 4096 19.9, 26.3 20.2 17.9 15.7; 18 x 1792 x 12672 19.4, 8.4 9.9 12.3 22.1; 512 x 2048
+// x 2048 13.9, 19.5 13.5 10.4 8.1; 512 x 4096 x 4096 22.7, 54.8 41.5 31.3 23.2; 2048 x 2048 x 256 9.8, 42.0 25.7 17.6
+// 14.1; 700 x 1500 x 8320 29.0, 61.2 46.0 38.0 35.9.  Of 15 products from 40 x 28672 x 8192 to 4096 x 4096 x 4096 in both
 // types the choice is within 12 % of the best of all, of most the best; of 150 drawn ones it takes 1.03 of the best
 // kind's time in the mean.  fp32 results take 1.15 of the time in either, and rows that are not 16-byte aligned 1.4
-// in small blocks (1021 x 2001 x 1000 in tiles and in blocks of the last kind 21.7, 18.1; x 1024 19.0, 13.6).
+// in small blocks (1021 x 2001 x 1000 in tiles and in blocks of the last kind 22.6, 17.5; x 1024 18.7, 13.0).
 bool plan_small(MoF8Plan* plan, const MoF8Operand& A, const MoF8Operand& B, int64_t dim, int32_t dtype, double tiles_us) {
     const uintptr_t rows_at = reinterpret_cast<uintptr_t>(A.q) | uintptr_t(A.ld) | reinterpret_cast<uintptr_t>(B.q) | uintptr_t(B.ld);
     const bool aligned = (rows_at & 15) == 0;
@@ -225,16 +225,16 @@ bool tokens_in_place(const MoF8Wgrad& a) {
 // with a launch, the results that nothing hides, and a launch that transposes): a workgroup alone on
 // its CU has its own time for 64 tokens, each further one adds to it; few blocks share a long K's tokens among up to
 // 32 workgroups each, whose fp32 sums a second launch adds.  (G's type is not known to the workspace's query: dY's
-// stands for it.)  us of the kernels in blocks and in tiles: dY and G in bf16, 98 tokens x 281 x 9600 7.2, 12.8; 1021 x
-// 1024 x 1024 14.0, 18.9; 64 x 4096 x 4096 14.2, 13.7; 512 x 4096 x 4096 40.8, 27.0; both in fp32, 206 x 5632 x 256
-// 10.3, 21.8; 257 x 1000 x 2001 14.7, 20.5; 721 x 9344 x 16 18.5, 37.2; 512 x 4096 x 4096 78.8, 60.8.
+// stands for it.)  us of the kernels in blocks and in tiles: dY and G in bf16, 98 tokens x 281 x 9600 7.0, 13.0; 1021 x
+// 1024 x 1024 13.7, 18.5; 64 x 4096 x 4096 14.2, 13.6; 512 x 4096 x 4096 40.8, 26.5; both in fp32, 206 x 5632 x 256
+// 9.8, 21.8; 257 x 1000 x 2001 13.1, 19.8; 721 x 9344 x 16 18.2, 36.4; 512 x 4096 x 4096 79.7, 59.5.
 void plan_small_wgrad(const MoF8Wgrad& a, double tiles_us, MoF8Plan* p) {
     const bool wide = a.dy_dtype == MO_F32;
     const double t = double(a.X.rows), n = double(a.rows), k = double(a.dim);
     const int64_t blocks = ((a.rows + 63) / 64) * ((a.dim + 63) / 64), chunks = (a.X.rows + 63) / 64;
     if (blocks >= int64_t(1) << 18) return;
-    // rows of dY that are not 16-byte aligned touch more lines (bf16, 1627 x 5147 x 384 37.7, 30.7; 2766 x
-    // 10607 x 411 129, 63)
+    // rows of dY that are not 16-byte aligned touch more lines (bf16, 1627 x 5147 x 384 37.1, 29.9; 2766 x
+    // 10607 x 411 128, 62)
     const bool aligned = ((reinterpret_cast<uintptr_t>(a.dY) | uintptr_t(a.lddy * elem_size(a.dy_dtype))) & 15) == 0;
     const double slower = aligned ? 1 : wide ? 1.25 : 1.6;
     double least = tiles_us + 4.3 + (p->splits == 1 ? n * k * double(elem_size(a.dy_dtype)) / 5e6 : 0) +

@@ -36,7 +36,7 @@
 // 16384 x 14336 x 4096 takes 735 to 796 us in 8 bits (2420 to 2620 TFLOP/s), where a library product of the same
 // numbers with one scale each takes 630 to 690, and 1514 to 1625 as a weight gradient (the library's bf16 product along
 // the tokens 1850 to 1960), by card: the clock is held at 1.76 and 2.0 GHz with MFMAs in 60 and 53 % of the cycles;
-// fp32 results 1530 to 1564.  What lies beside the stages (1.4 us of 256 x 256 in 8 bits) is 8 us a tile, most of it
+// fp32 results 1530 to 1580.  What lies beside the stages (1.4 us of 256 x 256 in 8 bits) is 8 us a tile, most of it
 // 128 KB of results per CU at HBM's rate.  Workgroups started 2 to 4 us apart, so that they would not store together,
 // took as long.
 #pragma once

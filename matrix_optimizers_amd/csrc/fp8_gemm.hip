@@ -371,7 +371,7 @@ template <> struct Source<uint8_t> {
 // results turn in LDS, so that 16 lanes store 64 neighbours of a row.  A workgroup alone takes 0.56 us for 64 tokens in
 // bf16 and 1.0 in fp32, bound by the wait from load to LDS to MFMA; several on a CU 0.26 and 0.56 each, bound by
 // LDS (and by cutting fp32 in parts).  257 tokens x 1000 x 2001 in fp32: 13.1 us with the call, 20 in tiles.  Few
-// blocks share a block's tokens among several workgroups (7803 x 16 x 16 in fp32: 14 us, 30 in tiles).
+// blocks share a block's tokens among several workgroups (7803 x 16 x 16 in fp32: 15 us, 30 in tiles).
 template <typename T, typename TG>
 __global__ __launch_bounds__(256) void f8_small_wgrad_kernel(Source<uint8_t> x, Source<T> y, int64_t tokens, Out<TG> o,
                                                              uint32_t bx, uint32_t by, int64_t per, float* part) {
